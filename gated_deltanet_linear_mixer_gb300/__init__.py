@@ -8,7 +8,9 @@ is missing the calls raise.  Build it with ``gated_deltanet_linear_mixer_gb300._
 (or ``__graft_entry__.build()``).
 
 Entry points (same names as the C ABI, without the ``gdn_`` prefix):
-``conv``, ``prefill``, ``prefill_workspace_size``, ``decode``, ``decode_commit``.
+``conv``, ``prefill``, ``prefill_workspace_size``, ``decode``, ``decode_commit``; for the
+full-attention layers of a hybrid stack and its speculative loop (``paged.py``):
+``kv_append``, ``kv_attention``, ``kv_read``, ``accept_drafts``.
 """
 from __future__ import annotations
 
@@ -33,8 +35,9 @@ ACT_SILU, ACT_SIGMOID = 0, 1
 EXPORTS = ("gdn_conv", "gdn_prefill_workspace_size", "gdn_prefill", "gdn_prefill_noalloc",
            "gdn_prefill_noalloc_scratch_bytes", "gdn_decode", "gdn_verify", "gdn_decode_commit",
            "gdn_layer_prefill_workspace_size", "gdn_layer_prefill",
-           "gdn_timing_enable", "gdn_timing_report", "gdn_device_error", "gdn_sync_status",
-           "gdn_last_error", "gdn_version")
+           "gdn_kv_append", "gdn_kv_read", "gdn_kv_attention_workspace_size", "gdn_kv_attention",
+           "gdn_accept_drafts", "gdn_timing_enable", "gdn_timing_report",
+           "gdn_device_error", "gdn_sync_status", "gdn_last_error", "gdn_version")
 
 
 class GDNError(RuntimeError):
@@ -64,6 +67,30 @@ class _Proj(ctypes.Structure):
                 ("w_b", ctypes.c_void_p), ("w_out", ctypes.c_void_p)]
 
 
+class _KVDims(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("rope_style", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int32)]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -91,6 +118,17 @@ def load(path: str | None = None):
     lib.gdn_layer_prefill_workspace_size.argtypes = [PD, I32, I32, P, ctypes.POINTER(ctypes.c_size_t)]
     lib.gdn_layer_prefill.argtypes = [PD, PP, ctypes.POINTER(_Proj), I32, I32, P, P, P, P, P, P, P,
                                       P, P, ctypes.c_size_t, P]
+    I64, PK, PC = ctypes.c_int64, ctypes.POINTER(_KVDims), ctypes.POINTER(_KVCache)
+    PB, PR = ctypes.POINTER(_KVBatch), ctypes.POINTER(_Rows)
+    lib.gdn_kv_append.argtypes = [PK, PC, PB, P, PR, PR, PR, P, I32, P, P, P]
+    lib.gdn_kv_read.argtypes = [PK, PC, PB, P, I32, P, P, P]
+    lib.gdn_kv_attention_workspace_size.argtypes = [PK, I32, P, I32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.gdn_kv_attention.argtypes = [PK, PC, PB, P, I32, PR, P, P, ctypes.c_size_t, P]
+    lib.gdn_accept_drafts.argtypes = [I32, I32, I32, I32, I32, P, P, I64, P, I64, P, P, P, I64, P,
+                                      P, P]
+    for f in ("gdn_kv_append", "gdn_kv_read", "gdn_kv_attention_workspace_size",
+              "gdn_kv_attention", "gdn_accept_drafts"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("gdn_conv", "gdn_prefill_workspace_size", "gdn_prefill", "gdn_prefill_noalloc",
               "gdn_decode", "gdn_verify", "gdn_decode_commit", "gdn_layer_prefill_workspace_size",
               "gdn_layer_prefill"):
@@ -463,7 +501,11 @@ def decode_commit(d: Dims, accepted, x, inter_states, state, conv_state=None):
     _check("gdn_decode_commit", st)
 
 
-__all__ = ["Dims", "Params", "GDNError", "load", "version", "timing_enable", "timing_report",
+from .paged import (KVCache, KVDims, accept_drafts, kv_append, kv_attention,  # noqa: E402
+                    kv_attention_workspace_size, kv_read)
+
+__all__ = ["KVCache", "KVDims", "accept_drafts", "kv_append", "kv_attention",
+           "kv_attention_workspace_size", "kv_read", "Dims", "Params", "GDNError", "load", "version", "timing_enable", "timing_report",
            "device_error", "sync_status",
            "conv", "prefill",
            "prefill_workspace_size", "decode", "verify", "decode_commit", "Proj",

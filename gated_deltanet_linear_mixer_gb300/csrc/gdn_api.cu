@@ -12,6 +12,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_kv.h"
 
 namespace {
 
@@ -211,6 +212,8 @@ gdn_status set_error(gdn_status st, const char* fn, const char* fmt, ...) {
     return st;
 }
 
+void clear_error() { g_err[0] = '\0'; }
+
 void* timing_start(const char* name, cudaStream_t stream) {
     std::lock_guard<std::mutex> lk(g_timing_mu);
     if (!g_timing_on) return nullptr;
@@ -280,6 +283,11 @@ gdn_status gdn_sync_status(void* stream) {
     int code = 0;
     if ((st = cuda_status(gdn::read_device_error(&code, true), fn, "reading the error word")) != GDN_OK)
         return st;
+    if (code == gdn::kKvErrTable || code == gdn::kKvErrRope)
+        return fail(GDN_ERR_INVALID_ARG, fn,
+                    "a cache operator met device data out of range (code %d: %s) and left it out; the "
+                    "outputs of the cache calls since the last check are incomplete",
+                    code, code == gdn::kKvErrTable ? "a block table entry or a length" : "a rotation position");
     if (code)
         return fail(GDN_ERR_TIMEOUT, fn,
                     "a bounded device wait gave up (wait code %d%s); the "

@@ -37,6 +37,7 @@
 
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
+#include "gdn_kv.h"
 #include "gdn_chunk_ops.cuh"
 #include "gdn_tc.cuh"
 #include "gdn_tma_host.h"
@@ -1505,12 +1506,14 @@ cudaError_t read_device_error(int* code, bool reset) {
         e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
     }
     // the projection GEMM's word (codes 20..23), the recurrent kernel's (30),
-    // the per-channel prep's (13, 14)
-    int gemm = 0, rec = 0, kda = 0;
+    // the per-channel prep's (13, 14), the cache operators' (40, 41)
+    int gemm = 0, rec = 0, kda = 0, kv = 0, attn = 0;
     if (e == cudaSuccess) e = read_gemm_error(&gemm, reset);
     if (e == cudaSuccess) e = read_rec_error(&rec, reset);
     if (e == cudaSuccess) e = read_kda_error(&kda, reset);
-    if (e == cudaSuccess && *code == 0) *code = gemm ? gemm : rec ? rec : kda;
+    if (e == cudaSuccess) e = read_kv_error(&kv, reset);
+    if (e == cudaSuccess) e = read_kv_attn_error(&attn, reset);
+    if (e == cudaSuccess && *code == 0) *code = gemm ? gemm : rec ? rec : kda ? kda : attn ? attn : kv;
     return e;
 }
 

@@ -1,0 +1,57 @@
+// Device helpers of the paged 8-bit cache: codes to values and back.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn_common.cuh"
+#include "gdn_kv.h"
+
+namespace gdn {
+
+// Cache codes.  top: the largest code value; a block's scale is its largest
+// |value| times 1 / top (one fp32 product), a code is value / scale rounded to
+// nearest even.
+struct KvInt8 {
+    __device__ static constexpr float top() { return 127.0f; }
+    __device__ __forceinline__ static float value(uint8_t c) {
+        return static_cast<float>(static_cast<int8_t>(c));
+    }
+    __device__ __forceinline__ static uint8_t code(float y) {  // NaN -> 0
+        y = y == y ? fminf(fmaxf(rintf(y), -127.0f), 127.0f) : 0.0f;
+        return static_cast<uint8_t>(static_cast<int8_t>(static_cast<int>(y)));
+    }
+};
+struct KvE4m3 {
+    __device__ static constexpr float top() { return 448.0f; }
+    __device__ __forceinline__ static float value(uint8_t c) {
+        return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+    }
+    __device__ __forceinline__ static uint8_t code(float y) {
+        return y == y ? __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3) : 0;
+    }
+};
+
+// Sequence and index within it of slot x, where sequence i owns slots
+// cu[i] / B + 2 i onwards: at least as many as the pages of B tokens that its
+// cu[i+1] - cu[i] consecutive positions can touch.
+__device__ __forceinline__ int seq_of_slot(const int32_t* __restrict__ cu, int n, int B, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] / B + 2 * mid <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Instantiates a launcher fn<activation type, code format, head dim>(a, stream)
+// for the names bf16, e4m3 and head_dim in scope.
+#define GDN_KV_PICK_D(fn, T, F)                                    \
+    (head_dim == 64 ? fn<T, F, 64>(a, stream)                      \
+                    : head_dim == 128 ? fn<T, F, 128>(a, stream) : fn<T, F, 256>(a, stream))
+#define GDN_KV_PICK(fn)                                                                        \
+    (bf16 ? (e4m3 ? GDN_KV_PICK_D(fn, __nv_bfloat16, KvE4m3) : GDN_KV_PICK_D(fn, __nv_bfloat16, KvInt8)) \
+          : (e4m3 ? GDN_KV_PICK_D(fn, float, KvE4m3) : GDN_KV_PICK_D(fn, float, KvInt8)))
+
+}  // namespace gdn

@@ -1,0 +1,92 @@
+// Launch interface of the paged 8-bit cache operators and of draft
+// verification (gdn_kv_api.cu validates, these launch).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gdn {
+
+// Device error codes of the cache operators (not waits).
+constexpr int kKvErrTable = 40;  // block table entry or length out of range
+constexpr int kKvErrRope = 41;   // position outside the rotation table
+
+struct KvCache {
+    uint8_t* k;      // codes [n_pages, Hkv, B, D]
+    uint8_t* v;
+    float* k_scale;  // [n_pages, Hkv]
+    float* v_scale;
+    int n_pages;
+};
+
+// Rows [T, heads, D]: channels contiguous, strides in elements.
+struct KvRows {
+    const void* data;
+    long long token_stride, head_stride;
+};
+
+struct KvBatch {
+    int n_seq, pages_per_seq;
+    const int32_t* cu;       // [n_seq+1]
+    const int32_t* kv_lens;  // [n_seq] (gdn_kv_read: the first positions)
+    const int32_t* table;    // [n_seq, pages_per_seq]
+    int n_tokens;            // cu[n_seq]
+    int max_q;               // longest sequence of the call
+    int uniform_q;           // every sequence's tokens where they are all alike, else 0
+};
+
+struct KvAppendArgs {
+    KvCache c;
+    KvBatch b;
+    int n_q_heads, n_kv_heads, page_size, rope_dim, rope_style;
+    KvRows q, k, v;             // q.data may be null
+    const float* rope;          // [rope_len, rope_dim]
+    int rope_len;
+    const int32_t* positions;   // [T] or null
+    void* q_out;
+};
+
+struct KvReadArgs {
+    KvCache c;
+    KvBatch b;
+    int n_kv_heads, page_size;
+    void *k_out, *v_out;
+};
+
+struct KvAttnArgs {
+    KvCache c;
+    KvBatch b;
+    int n_q_heads, n_kv_heads, page_size, window;
+    float scale;
+    KvRows q;
+    void* out;
+    float* partial;   // split partials (workspace), see gdn_kv_attn.cu
+    int max_kv_len;
+};
+
+struct AcceptArgs {
+    int n_seq, T, vocab;
+    const int32_t* drafts;
+    const void* target;
+    const void* draft;  // or null
+    long long target_stride, draft_stride, noise_stride;
+    const float *temperature, *uniforms, *noise;
+    int32_t *accepted, *tokens;
+};
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, int head_dim, bool bf16, bool e4m3,
+                             cudaStream_t stream);
+cudaError_t launch_kv_read(const KvReadArgs& a, int head_dim, bool bf16, bool e4m3,
+                           cudaStream_t stream);
+size_t kv_attention_workspace(int n_seq, const int32_t* cu_host, int n_q_heads, int n_kv_heads,
+                              int head_dim, bool bf16, int max_kv_len);
+cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3,
+                                cudaStream_t stream);
+// form: gdn_dist_form; logits and probabilities in bf16 or f32.
+cudaError_t launch_accept_drafts(const AcceptArgs& a, bool logits, bool bf16, cudaStream_t stream);
+
+cudaError_t read_kv_error(int* code, bool reset);       // append, read
+cudaError_t read_kv_attn_error(int* code, bool reset);  // attention
+
+}  // namespace gdn

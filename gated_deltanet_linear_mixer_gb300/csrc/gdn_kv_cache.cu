@@ -1,0 +1,285 @@
+// Appending to the paged 8-bit cache (with the position rotation of q and k on
+// the way) and reading values back out of it.
+//
+// kv_append: one thread block per (page the call writes to, kv head, K or V)
+// finds the block's largest |new value|, settles the block's scale and writes
+// the codes, so the scale needs no atomics and every result is independent of
+// order; further thread blocks of the same launch rotate q.  A thread holds
+// its (rotated) values in registers between the maximum and the rounding, so
+// the new rows are read once.  Products and sums of the rotation are rounded
+// one by one (no fused multiply-add) and the division is the exact one: the
+// stored codes do not depend on how a compiler contracts an expression.
+#include <algorithm>
+
+#include "gdn_internal.h"
+#include "gdn_kv.cuh"
+
+namespace gdn {
+
+namespace {
+
+__device__ int g_kv_error = 0;
+
+// 16 channels of a row, as two 8-channel vectors at c0 and c1: the two members
+// of 8 rotation pairs, or 16 unrotated channels.
+struct Unit {
+    int c0, c1;
+    bool rotated;
+};
+__device__ __forceinline__ Unit unit_at(int u, int rope_dim, int style) {
+    Unit r;
+    r.rotated = 16 * u < rope_dim;
+    r.c0 = (r.rotated && style == 0) ? 8 * u : 16 * u;
+    r.c1 = (r.rotated && style == 0) ? 8 * u + rope_dim / 2 : 16 * u + 8;
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* x) {
+    constexpr int N = Vec16<T>::N;
+#pragma unroll
+    for (int i = 0; i < 8; i += N) Vec16<T>::load(p + i, x + i);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* x) {
+    constexpr int N = Vec16<T>::N;
+#pragma unroll
+    for (int i = 0; i < 8; i += N) Vec16<T>::store(p + i, x + i);
+}
+
+__device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
+    const float ra = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    const float rb = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    a = ra;
+    b = rb;
+}
+
+// x[0..7], x[8..15]: the unit's two vectors; cs: the row's cosines and sines of
+// pairs 8u .. 8u + 7.
+__device__ __forceinline__ void rotate_unit(float* x, const float* row, int u, int rope_dim, int style) {
+    float c[8], s[8];
+    load8(row + 8 * u, c);
+    load8(row + rope_dim / 2 + 8 * u, s);
+    if (style == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rotate_pair(x[i], x[8 + i], c[i], s[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rotate_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
+    }
+}
+
+// The rotation table's row of a token; stays inside the table.
+__device__ __forceinline__ const float* rope_row(const KvAppendArgs& a, int tok, int pos) {
+    int p = a.positions ? a.positions[tok] : pos;
+    if (p < 0 || p >= a.rope_len) {
+        atomicCAS(&g_kv_error, 0, kKvErrRope);
+        p = p < 0 ? 0 : a.rope_len - 1;
+    }
+    return a.rope + static_cast<size_t>(p) * a.rope_dim;
+}
+
+constexpr int kUnitsPerThread = 4;  // 64 values held in registers
+
+template <typename T, typename F, int D>
+__global__ void __launch_bounds__(512) kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
+    constexpr int U = D / 16;  // units of a row
+    const int tid = threadIdx.x, nt = blockDim.x;
+    const int B = a.page_size;
+
+    if (static_cast<int>(blockIdx.x) >= n_store_blocks) {  // q rows
+        const long long total = static_cast<long long>(a.b.n_tokens) * a.n_q_heads * U;
+        const long long step = static_cast<long long>(gridDim.x - n_store_blocks) * nt;
+        for (long long i = static_cast<long long>(blockIdx.x - n_store_blocks) * nt + tid; i < total; i += step) {
+            const int u = static_cast<int>(i % U);
+            const long long r = i / U;
+            const int h = static_cast<int>(r % a.n_q_heads), tok = static_cast<int>(r / a.n_q_heads);
+            const Unit w = unit_at(u, a.rope_dim, a.rope_style);
+            const T* src = static_cast<const T*>(a.q.data) + tok * a.q.token_stride + h * a.q.head_stride;
+            float x[16];
+            load8(src + w.c0, x);
+            load8(src + w.c1, x + 8);
+            if (w.rotated) {
+                int pos = 0;
+                if (!a.positions) {
+                    const int s = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
+                    pos = a.b.kv_lens[s] - (a.b.cu[s + 1] - tok);
+                }
+                rotate_unit(x, rope_row(a, tok, pos), u, a.rope_dim, a.rope_style);
+            }
+            T* dst = static_cast<T*>(a.q_out) + (static_cast<size_t>(tok) * a.n_q_heads + h) * D;
+            store8(dst + w.c0, x);
+            store8(dst + w.c1, x + 8);
+        }
+        return;
+    }
+
+    const int is_v = blockIdx.x & 1, item = (blockIdx.x >> 1) / a.n_kv_heads;
+    const int h = (blockIdx.x >> 1) - item * a.n_kv_heads;
+    int seq, local;
+    if (a.b.uniform_q) {
+        const int per = (a.b.uniform_q + B - 2) / B + 1;
+        seq = item / per;
+        local = item - seq * per;
+    } else {
+        seq = seq_of_slot(a.b.cu, a.b.n_seq, B, item);
+        local = item - (a.b.cu[seq] / B + 2 * seq);
+    }
+    const int q0 = a.b.cu[seq], len = a.b.kv_lens[seq], start = len - (a.b.cu[seq + 1] - q0);
+    const long long cap = static_cast<long long>(a.b.pages_per_seq) * B;
+    if ((start < 0 || len > cap) && tid == 0) atomicCAS(&g_kv_error, 0, kKvErrTable);
+    const int p0 = max(start, 0), p1 = static_cast<int>(min(static_cast<long long>(len), cap));
+    const int lp = p0 / B + local;
+    if (p0 >= p1 || lp > (p1 - 1) / B) return;
+    const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + lp];
+    if (page < 0 || page >= a.c.n_pages) {
+        if (tid == 0) atomicCAS(&g_kv_error, 0, kKvErrTable);
+        return;
+    }
+    const int r0 = max(p0 - lp * B, 0), r1 = min(p1 - lp * B, B);  // new rows of the page
+    const int kept = start > lp * B ? r0 : 0;                      // earlier rows of this sequence
+
+    const KvRows& rows = is_v ? a.v : a.k;
+    float x[kUnitsPerThread][16];
+    float most = 0.0f;
+    const int n_units = (r1 - r0) * U;
+#pragma unroll
+    for (int it = 0; it < kUnitsPerThread; ++it) {
+        const int i = tid + it * nt;
+        if (i < n_units) {
+            const int u = i % U, pos = lp * B + r0 + i / U, tok = q0 + (pos - start);
+            const Unit w = unit_at(u, is_v ? 0 : a.rope_dim, a.rope_style);
+            const T* src = static_cast<const T*>(rows.data) + tok * rows.token_stride + h * rows.head_stride;
+            load8(src + w.c0, x[it]);
+            load8(src + w.c1, x[it] + 8);
+            if (w.rotated) rotate_unit(x[it], rope_row(a, tok, pos), u, a.rope_dim, a.rope_style);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float m = fabsf(x[it][e]);
+                if (m <= 3.402823466e38f) most = fmaxf(most, m);  // finite values only
+            }
+        }
+    }
+    const size_t block = static_cast<size_t>(page) * a.n_kv_heads + h;
+    float* scale_at = (is_v ? a.c.v_scale : a.c.k_scale) + block;
+    const float old = kept > 0 ? *scale_at : 0.0f;
+    __shared__ float part[16];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+    if ((tid & 31) == 0) part[tid >> 5] = most;
+    __syncthreads();
+    most = part[0];
+    for (int w = 1; w < nt / 32; ++w) most = fmaxf(most, part[w]);
+    const float scale = fmaxf(old, __fmul_rn(most, 1.0f / F::top()));
+    uint8_t* codes = (is_v ? a.c.v : a.c.k) + block * B * D;
+    if (kept > 0 && scale > old) {
+        const float ratio = old / scale;
+        uint4* p = reinterpret_cast<uint4*>(codes);
+        for (int i = tid; i < kept * U; i += nt) {
+            uint4 w = p[i];
+            uint8_t* c = reinterpret_cast<uint8_t*>(&w);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) c[e] = F::code(__fmul_rn(F::value(c[e]), ratio));
+            p[i] = w;
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < kUnitsPerThread; ++it) {
+        const int i = tid + it * nt;
+        if (i < n_units) {
+            const int u = i % U, row = r0 + i / U;
+            const Unit w = unit_at(u, is_v ? 0 : a.rope_dim, a.rope_style);
+            uint8_t c[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) c[e] = scale > 0.0f ? F::code(x[it][e] / scale) : 0;
+            uint2 lo, hi;
+            memcpy(&lo, c, 8);
+            memcpy(&hi, c + 8, 8);
+            *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * D + w.c0) = lo;
+            *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * D + w.c1) = hi;
+        }
+    }
+    if (tid == 0) *scale_at = scale;
+}
+
+constexpr int kReadThreads = 256;
+
+// One thread takes 16 codes of K and of V.
+template <typename T, typename F, int D>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvReadArgs a) {
+    constexpr int U = D / 16;
+    const long long total = static_cast<long long>(a.b.n_tokens) * a.n_kv_heads * U;
+    const long long i = static_cast<long long>(blockIdx.x) * kReadThreads + threadIdx.x;
+    if (i >= total) return;
+    const int u = static_cast<int>(i % U);
+    const long long r = i / U;
+    const int h = static_cast<int>(r % a.n_kv_heads), tok = static_cast<int>(r / a.n_kv_heads);
+    const int seq = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
+    const long long pos = static_cast<long long>(a.b.kv_lens[seq]) + (tok - a.b.cu[seq]);
+    const long long lp = pos < 0 ? -1 : pos / a.page_size;
+    const int page = lp >= 0 && lp < a.b.pages_per_seq
+                         ? a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + lp] : -1;
+    const bool mapped = page >= 0 && page < a.c.n_pages;
+    if (!mapped) atomicCAS(&g_kv_error, 0, kKvErrTable);
+    const size_t block = static_cast<size_t>(mapped ? page : 0) * a.n_kv_heads + h;
+    const size_t at = (block * a.page_size + (mapped ? pos % a.page_size : 0)) * D + 16 * u;
+#pragma unroll
+    for (int is_v = 0; is_v < 2; ++is_v) {
+        float x[16] = {};
+        if (mapped) {
+            const uint4 w = *reinterpret_cast<const uint4*>((is_v ? a.c.v : a.c.k) + at);
+            const float s = (is_v ? a.c.v_scale : a.c.k_scale)[block];
+            const uint8_t* c = reinterpret_cast<const uint8_t*>(&w);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = F::value(c[e]) * s;
+        }
+        T* dst = static_cast<T*>(is_v ? a.v_out : a.k_out) + static_cast<size_t>(r) * D + 16 * u;
+        store8(dst, x);
+        store8(dst + 8, x + 8);
+    }
+}
+
+template <typename T, typename F, int D>
+cudaError_t append_t(const KvAppendArgs& a, cudaStream_t st) {
+    const int B = a.page_size;
+    // enough threads that kUnitsPerThread units each cover a whole page
+    const int nt = std::max(64, B * D / (16 * kUnitsPerThread));
+    const long long slots = a.b.uniform_q ? static_cast<long long>(a.b.n_seq) * ((a.b.uniform_q + B - 2) / B + 1)
+                                          : static_cast<long long>(a.b.n_tokens) / B + 2LL * a.b.n_seq;
+    const long long store = slots * a.n_kv_heads * 2;
+    const long long q_units = a.q.data ? static_cast<long long>(a.b.n_tokens) * a.n_q_heads * (D / 16) : 0;
+    const long long q_blocks = std::min((q_units + nt - 1) / nt, 152LL * 16);
+    if (store + q_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    kv_append_kernel<T, F, D><<<static_cast<unsigned>(store + q_blocks), nt, 0, st>>>(a, static_cast<int>(store));
+    return cudaGetLastError();
+}
+
+template <typename T, typename F, int D>
+cudaError_t read_t(const KvReadArgs& a, cudaStream_t st) {
+    const long long units = static_cast<long long>(a.b.n_tokens) * a.n_kv_heads * (D / 16);
+    const long long blocks = (units + kReadThreads - 1) / kReadThreads;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    kv_read_kernel<T, F, D><<<static_cast<unsigned>(blocks), kReadThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
+    return GDN_KV_PICK(append_t);
+}
+
+cudaError_t launch_kv_read(const KvReadArgs& a, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
+    return GDN_KV_PICK(read_t);
+}
+
+cudaError_t read_kv_error(int* code, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_kv_error, sizeof(int));
+    if (e == cudaSuccess && reset) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_kv_error, &zero, sizeof(int));
+    }
+    return e;
+}
+
+}  // namespace gdn

@@ -41,9 +41,10 @@
  * - Failure injection (testing a caller's failure path, as cortiq-engine
  *   0.8.76 pipeline.rs does with its test-only nll_test_fail_at): the environment variable GDN_FAULT
  *   is a comma-separated list of sites -- conv, prefill, decode, verify,
- *   commit, layer, or all.  A call whose site is listed validates its
- *   arguments, then returns GDN_ERR_INJECTED without enqueuing anything, so
- *   every caller buffer is left as it was.  The site stall_scan is a device
+ *   commit, layer, kv_append, kv_read, kv_attention, accept, or all.  A call
+ *   whose site is listed validates its arguments, then returns
+ *   GDN_ERR_INJECTED without enqueuing anything, so every caller buffer is
+ *   left as it was.  The site stall_scan is a device
  *   test hook: a bf16 prefill that takes the fused tensor-core launch makes
  *   its scan wait (for at most 1 ms) on a chunk flag that nothing sets, so
  *   that the bounded wait runs out; the call returns GDN_OK and the next
@@ -290,6 +291,174 @@ gdn_status gdn_layer_prefill(const gdn_dims* dims, const gdn_params* params,
                              const void* conv_state_in, void* conv_state_out, void* h_out,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Full attention over a paged 8-bit cache, and the verification of drafts:
+ * the operators a hybrid stack needs next to the mixer above (its
+ * interleaved full-attention layers, and the step that decides how many
+ * drafted tokens stand, whose result gdn_decode_commit takes).
+ *
+ * The cache.  Page p holds page_size consecutive tokens of one sequence:
+ *   k, v             [n_pages, n_kv_heads, page_size, head_dim] 8-bit codes
+ *   k_scale, v_scale [n_pages, n_kv_heads] fp32: one scale for each block of
+ *                    page_size tokens and head; a value is code * scale
+ * Token position j of sequence i lives in page block_table[i, j / page_size],
+ * row j % page_size.  kv_lens[i] is sequence i's length INCLUDING the tokens
+ * of the call: its q_i = cu_seqlens[i+1] - cu_seqlens[i] tokens occupy
+ * positions kv_lens[i] - q_i .. kv_lens[i] - 1.  gdn_kv_append and
+ * gdn_kv_attention take the same arrays, append first.
+ *   A block_table entry outside [0, n_pages) is an unmapped page: nothing is
+ * written to it and no query sees its keys.  A call that meets one where it
+ * needs a page, a kv_len above pages_per_seq * page_size, a negative first
+ * position or a position outside the rotation table stays in bounds and
+ * records a code in the device error word: gdn_sync_status then returns
+ * GDN_ERR_INVALID_ARG (40 block table or length, 41 rotation table).
+ */
+
+/* Codes of the cache: int8 (round to nearest even, symmetric, +-127) or
+ * 8-bit floating point e4m3 (+-448). */
+typedef enum gdn_kv_format { GDN_KV_INT8 = 0, GDN_KV_E4M3 = 1 } gdn_kv_format;
+
+/* Pairs of channels that the position rotation turns, of the first rope_dim
+ * channels of a head: (i, i + rope_dim/2) or (2i, 2i + 1). */
+typedef enum gdn_rope_style { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_style;
+
+/* Geometry.  n_q_heads a multiple (at most 64 times) of n_kv_heads; query head
+ * h reads kv head h / (n_q_heads / n_kv_heads).  head_dim 64, 128 or 256;
+ * page_size 16, 32, 64 or 128; rope_dim a multiple of 16, at most head_dim (0:
+ * no rotation); window 0 (all earlier positions) or the number of positions a
+ * query sees, its own among them; scale > 0 multiplies q.k. */
+typedef struct gdn_kv_dims {
+    int32_t n_q_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t dtype;      /* gdn_dtype of q, k, v and out */
+    int32_t format;     /* gdn_kv_format */
+    int32_t rope_dim;
+    int32_t rope_style; /* gdn_rope_style */
+    int32_t window;
+    float scale;
+} gdn_kv_dims;
+
+typedef struct gdn_kv_cache {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int32_t n_pages;
+} gdn_kv_cache;
+
+/* The sequences of a call (cu_seqlens on the device and on the host, as in
+ * gdn_prefill) and their pages, block_table [n_seq, pages_per_seq] int32. */
+typedef struct gdn_kv_batch {
+    int32_t n_seq;
+    int32_t pages_per_seq;
+    const int32_t* cu_seqlens;
+    const int32_t* cu_seqlens_host;
+    const int32_t* block_table;
+} gdn_kv_batch;
+
+/* Rows [T, heads, head_dim] in the activation dtype: channels contiguous,
+ * token and head strides in elements (a slice of a fused projection's output
+ * is such rows); the base and both strides multiples of 16 bytes. */
+typedef struct gdn_rows {
+    const void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} gdn_rows;
+
+/*
+ * gdn_kv_append -- rotate and append.  Per token at position p, with c, s =
+ * rope[p] the cosines and sines of its rope_dim/2 pairs:
+ *   (x1, x2) <- (x1 c - x2 s, x2 c + x1 s)     for k, and for q where given
+ * then k (rotated) and v are stored as codes.  Per page and head the call
+ * touches: a = the largest finite |value| among the new ones, and
+ *   scale <- max(scale, a / 127 or a / 448)    where the page holds earlier
+ *                                              tokens of the sequence,
+ *   scale <- a / 127 or a / 448                where it does not.
+ * New codes are value / scale rounded to nearest even, saturating (NaN becomes
+ * 0, infinities the largest code); if the scale grew, the codes of the page's
+ * earlier tokens are rounded to it, once.  Rows past the sequence's end are
+ * left as they are.  Two sequences of a call may share pages only where the
+ * call does not write.
+ *   rope [rope_len, rope_dim] fp32, row p = (rope_dim/2 cosines | sines);
+ *   NULL iff rope_dim is 0.  positions [T] int32 or NULL: the rows of rope to
+ *   use where they are not the cache positions.
+ *   q NULL or [T, n_q_heads, head_dim] rows, q_out [T, n_q_heads, head_dim]
+ *   contiguous, in the activation dtype; q_out may be q's own memory.
+ */
+gdn_status gdn_kv_append(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
+                         const gdn_kv_batch* batch, const int32_t* kv_lens, const gdn_rows* q,
+                         const gdn_rows* k, const gdn_rows* v, const float* rope,
+                         int32_t rope_len, const int32_t* positions, void* q_out, void* stream);
+
+/*
+ * gdn_kv_read -- cached values back out of the pages: of sequence i the
+ * cu_seqlens[i+1] - cu_seqlens[i] tokens from position starts[i] on, code *
+ * scale, packed.  k_out, v_out [R, n_kv_heads, head_dim] in out_dtype (a
+ * gdn_dtype).  Tokens of unmapped pages read as 0.
+ */
+gdn_status gdn_kv_read(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
+                       const gdn_kv_batch* batch, const int32_t* starts, int32_t out_dtype,
+                       void* k_out, void* v_out, void* stream);
+
+/*
+ * gdn_kv_attention -- causal attention of the call's queries over the cache:
+ *   o_t = sum_j p_tj v_j,  p_t = softmax_j(scale q_t . k_j)
+ * over max(0, P - window + 1) <= j <= P, P the query's position (window 0: all
+ * j <= P).  A query that sees no key (its position is negative, or every page
+ * it would see is unmapped) gives zeros.
+ *   q [T, n_q_heads, head_dim] rows (rotated already), out [T, n_q_heads,
+ *   head_dim] contiguous.  max_kv_len: at least every kv_lens[i]; it sets how
+ *   the keys are split among thread blocks (a longer sequence is still
+ *   attended to in full).
+ *   workspace: at least gdn_kv_attention_workspace_size() bytes, 256-byte
+ *   aligned (NULL when that is 0).
+ * bf16 activations: tensor cores, codes and probabilities as f16 operands,
+ * fp32 accumulation and softmax.  fp32 activations: the same with queries and
+ * probabilities as f16 (hi, lo) pairs.
+ */
+gdn_status gdn_kv_attention_workspace_size(const gdn_kv_dims* dims, int32_t n_seq,
+                                           const int32_t* cu_seqlens_host, int32_t max_kv_len,
+                                           size_t* bytes);
+gdn_status gdn_kv_attention(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
+                            const gdn_kv_batch* batch, const int32_t* kv_lens,
+                            int32_t max_kv_len, const gdn_rows* q, void* out, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* What target and draft rows hold: probabilities (fp32), or logits (fp32 or
+ * bf16) of which the distribution is softmax(logits / temperature). */
+typedef enum gdn_dist_form { GDN_DIST_PROBS = 0, GDN_DIST_LOGITS = 1 } gdn_dist_form;
+
+/*
+ * gdn_accept_drafts -- speculative verification from given random numbers.
+ * Row t of target is the target model's distribution p_t for the token after
+ * the first t drafts, row t of draft the distribution q_t that draft t was
+ * drawn from.  Draft x_t stands iff every earlier one does and
+ *   uniforms[t] * q_t(x_t) < p_t(x_t).
+ * At the first draft that falls, and after the last, one token is drawn:
+ *   r = max(p - q, 0) at a fallen draft (r = p where that is all zero, and
+ *   after the last draft),   token = argmax_j r_j / noise_j,
+ * the lowest j on ties; with noise ~ Exp(1) and uniforms ~ U[0, 1) the tokens
+ * are distributed as the target's own.  With draft NULL a draft was certain
+ * (q one at x_t, zero elsewhere).  A draft outside [0, vocab) (-1) marks the
+ * end of that sequence's drafts: its row is drawn from like the one after the
+ * last.  Temperature 0 takes the largest logit (the lowest index on ties): a
+ * draft stands iff it is that.  A row with no positive r gives token -1.
+ *   drafts, uniforms [n_seq, T]; target [n_seq, T + 1, vocab] and draft
+ *   [n_seq, T, vocab] with row strides in elements (the sequence stride is
+ *   T + 1, or T, rows); noise [n_seq, vocab] fp32 with its row stride;
+ *   temperature [n_seq] fp32 >= 0 (logits; NULL: 1).  0 <= T <= 16.
+ *   accepted [n_seq] int32: how many drafts stand (gdn_decode_commit's
+ *   `accepted`).  tokens [n_seq, T + 1] int32: those drafts, the drawn token,
+ *   then -1.
+ */
+gdn_status gdn_accept_drafts(int32_t n_seq, int32_t T, int32_t vocab, int32_t form, int32_t dtype,
+                             const int32_t* drafts, const void* target, int64_t target_stride,
+                             const void* draft, int64_t draft_stride, const float* temperature,
+                             const float* uniforms, const float* noise, int64_t noise_stride,
+                             int32_t* accepted, int32_t* tokens, void* stream);
+
 /*
  * gdn_timing_enable / gdn_timing_report -- per-kernel device timing (the
  * library's tracing hook; the pages time their GDN phases with scoped timers,
@@ -313,7 +482,8 @@ size_t gdn_timing_report(char* buf, size_t buf_len);
  * waits for its tiles, and for its v tile, products and the next item's tiles;
  * 20..23 the projection GEMM's; 30 the
  * token-recurrent kernel's wait for a state copy) and exit cleanly; their
- * outputs are then invalid.  Waits for the device (cudaMemcpyFromSymbol), writes the code to
+ * outputs are then invalid.  Codes 40 and 41 are not waits: a cache operator
+ * met device data out of range (see the cache above) and stayed in bounds.  Waits for the device (cudaMemcpyFromSymbol), writes the code to
  * *code (0 = no error) and clears it when reset != 0.
  */
 gdn_status gdn_device_error(int32_t* code, int32_t reset);
@@ -322,8 +492,9 @@ gdn_status gdn_device_error(int32_t* code, int32_t reset);
  * gdn_sync_status -- waits for `stream` (cudaStream_t as void*), then reads and
  * clears the device error word: GDN_ERR_TIMEOUT if a bounded device wait gave
  * up since the last check (the outputs and states of the calls since then are
- * invalid and must be recomputed; the CUDA context stays usable), GDN_ERR_CUDA
- * if the stream reports a CUDA error, else GDN_OK.  A serving loop calls it
+ * invalid and must be recomputed; the CUDA context stays usable),
+ * GDN_ERR_INVALID_ARG if a cache operator met device data out of range,
+ * GDN_ERR_CUDA if the stream reports a CUDA error, else GDN_OK.  A serving loop calls it
  * where it would synchronize anyway, and fails the affected requests closed.
  */
 gdn_status gdn_sync_status(void* stream);
