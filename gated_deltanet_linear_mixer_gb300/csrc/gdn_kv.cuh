@@ -1,6 +1,8 @@
 // Device helpers of the paged 8-bit cache: codes to values and back.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -43,6 +45,20 @@ __device__ __forceinline__ int seq_of_slot(const int32_t* __restrict__ cu, int n
         if (cu[mid] / B + 2 * mid <= x) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// Lets `kernel` use `bytes` of dynamic shared memory, once per device (ready:
+// one bit per device; devices past 63 ask every time).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // Instantiates a launcher fn<activation type, code format, head dim>(a, stream)

@@ -79,8 +79,8 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, int head_dim, bool bf16, boo
                              cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadArgs& a, int head_dim, bool bf16, bool e4m3,
                            cudaStream_t stream);
-size_t kv_attention_workspace(int n_seq, const int32_t* cu_host, int n_q_heads, int n_kv_heads,
-                              int head_dim, bool bf16, int max_kv_len);
+size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window,
+                              bool bf16, int max_kv_len);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3,
                                 cudaStream_t stream);
 // form: gdn_dist_form; logits and probabilities in bf16 or f32.

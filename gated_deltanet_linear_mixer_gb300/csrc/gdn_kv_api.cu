@@ -119,6 +119,11 @@ gdn_status check_rows(const gdn_rows* r, const char* name, const gdn_kv_dims* d,
     return GDN_OK;
 }
 
+size_t attention_workspace(const gdn_kv_dims* d, int n_seq, int max_q, int max_kv_len) {
+    return gdn::kv_attention_workspace(n_seq, max_q, d->n_q_heads, d->n_kv_heads, d->head_dim, d->window,
+                                       d->dtype == GDN_DTYPE_BF16, max_kv_len);
+}
+
 gdn::KvCache cache_of(const gdn_kv_cache* c) {
     return gdn::KvCache{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scale, c->v_scale, c->n_pages};
 }
@@ -191,9 +196,12 @@ gdn_status gdn_kv_attention_workspace_size(const gdn_kv_dims* dims, int32_t n_se
     if (!bytes) return set_error(GDN_ERR_INVALID_ARG, fn, "bytes is NULL");
     if ((st = check_cu(n_seq, cu_seqlens_host, fn)) != GDN_OK) return st;
     if (max_kv_len < 0) return set_error(GDN_ERR_INVALID_ARG, fn, "max_kv_len must be >= 0 (got %d)", max_kv_len);
-    *bytes = n_seq == 0 ? 0
-                        : gdn::kv_attention_workspace(n_seq, cu_seqlens_host, dims->n_q_heads, dims->n_kv_heads,
-                                                      dims->head_dim, dims->dtype == GDN_DTYPE_BF16, max_kv_len);
+    int max_q = 0;
+    for (int i = 0; i < n_seq; ++i) {
+        const int q = cu_seqlens_host[i + 1] - cu_seqlens_host[i];
+        max_q = q > max_q ? q : max_q;
+    }
+    *bytes = attention_workspace(dims, n_seq, max_q, max_kv_len);
     gdn::clear_error();
     return GDN_OK;
 }
@@ -212,9 +220,7 @@ gdn_status gdn_kv_attention(const gdn_kv_dims* dims, const gdn_kv_cache* cache, 
     if (a.b.n_tokens == 0) return GDN_OK;
     if ((st = check_rows(q, "q", dims, &a.q, fn)) != GDN_OK) return st;
     if (!out || !aligned16(out)) return set_error(GDN_ERR_INVALID_ARG, fn, "out must be given and 16-byte aligned");
-    const size_t need = gdn::kv_attention_workspace(a.b.n_seq, batch->cu_seqlens_host, dims->n_q_heads,
-                                                    dims->n_kv_heads, dims->head_dim,
-                                                    dims->dtype == GDN_DTYPE_BF16, max_kv_len);
+    const size_t need = attention_workspace(dims, a.b.n_seq, a.b.max_q, max_kv_len);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return set_error(GDN_ERR_WORKSPACE, fn, "workspace of %zu bytes needed, %zu given", need,
                          workspace ? workspace_bytes : (size_t)0);

@@ -1,10 +1,32 @@
-// Causal attention over the paged 8-bit cache.
+// Causal attention over the paged 8-bit cache: few query rows per kv head
+// (single tokens, drafts), and fp32 activations of any length.
 //
-// kv_attn_rows: one thread block per (token, query head); each of its warps
-// walks every fourth key with a running maximum and sum, and the warps'
-// results are joined at the end.
+// Mathematics.  Row r = (token, head of the group) of one sequence and kv head
+// attends to the keys its position and window allow.  Codes are small integers
+// (or e4m3 values), exact in f16 and in bf16, so the tensor cores work on the
+// codes themselves; a block's scales come in outside of the products:
+//   y_rj = (q_r . ck_j) scale s_k[blk(j)] log2 e + log2 s_v[blk(j)]
+//   w_rj = 2^(y_rj - m_r),  o_r = sum_j w_rj cv_j / sum_blk (sum_j w_rj) / s_v[blk]
+// The value scale enters the exponent; the denominator takes it out again, once
+// per 16 keys.  m_r is a reference, not the exact maximum: it moves (and o_r is
+// rescaled) only when a score exceeds it by 2^kLazy.
+// Queries become f16 after division by a power of two per row (bf16 has fewer
+// bits than f16, so that is exact down to 2^-24 of the row's largest).  Weights
+// become two bf16 terms, 16 bits: bf16's range holds the smallest of them (f16
+// would drop weights below 2^-24 of the largest, all that is left in a channel
+// where the heavy keys are zero), and one term's 2^-8 would be as large as the
+// output's own rounding.  With fp32 activations queries are f16 (hi, lo) pairs,
+// 22 bits, and weights three bf16 terms, 24 bits.
+//
+// One thread block takes 16 rows and a range of keys.  Each of its four warps
+// takes every fourth group of 16 keys on its own, with its own running state
+// and its own ring of asynchronous copies (no block-wide barrier until the
+// end): 16 keys lie in one page, so a group is one contiguous run of codes and
+// two scales.  A long axis is split over thread blocks and joined by
+// kv_attn_join.
 #include <algorithm>
-#include <climits>
+#include <atomic>
+#include <cuda_fp16.h>
 
 #include "gdn_internal.h"
 #include "gdn_kv.cuh"
@@ -15,75 +37,602 @@ namespace {
 
 __device__ int g_kv_attn_error = 0;
 
-constexpr int kRowWarps = 4;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kRows = 16;         // query rows of a thread block (the tensor core's M)
+constexpr int kGroup = 16;        // keys of a warp's step
+constexpr int kStepKeys = kGroup * kWarps;
+constexpr int kSpan = 64;         // steps whose pages and scales are looked up at a time
+constexpr float kLazy = 8.0f;     // a reference lags behind the maximum by at most 2^8
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The residual of pack_f16(lo, hi), as f16.
+__device__ __forceinline__ uint32_t pack_f16_rest(uint32_t h, float lo, float hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_f16(lo - f.x, hi - f.y);
+}
+
+// Four codes of a word to f16: codes (0, 1) and (2, 3).
+template <typename F> __device__ __forceinline__ void widen_f16(uint32_t w, uint32_t& a, uint32_t& b);
+template <> __device__ __forceinline__ void widen_f16<KvInt8>(uint32_t w, uint32_t& a, uint32_t& b) {
+    // bytes u = code + 128 under the exponent of 1024 are the f16 1024 + u; less 1152 it is the code
+    w ^= 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    uint32_t x = __byte_perm(w, 0x64646464u, 0x4140), y = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 hx = __hsub2(*reinterpret_cast<__half2*>(&x), off), hy = __hsub2(*reinterpret_cast<__half2*>(&y), off);
+    a = *reinterpret_cast<const uint32_t*>(&hx);
+    b = *reinterpret_cast<const uint32_t*>(&hy);
+}
+template <> __device__ __forceinline__ void widen_f16<KvE4m3>(uint32_t w, uint32_t& a, uint32_t& b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+}
+
+// Two codes of ab, (0, 1) or (2, 3), to bf16.
+template <int S> __device__ __forceinline__ uint32_t widen_int8_bf16(uint32_t ab) {
+    // Under the exponent of 128 the low seven bits of a code are the bf16
+    // 128 + (c & 127); the sign bit alone is 128, or 256 for a negative code; their difference is c
+    const uint32_t x = __byte_perm(ab, 0x43434343u, S == 0 ? 0x4140 : 0x4342);
+    const uint32_t lo = x & 0xFF7FFF7Fu, hi = x & 0xFF80FF80u;
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <int S> __device__ __forceinline__ uint32_t widen_e4m3_bf16(uint32_t ab) {
+    // sign, and exponent and fraction moved to their places: the value times 2^(7 - 127)
+    const uint32_t h = __byte_perm(ab, 0u, S == 0 ? 0x1404 : 0x3424);
+    const uint32_t x = ((h >> 4) & 0x07F007F0u) | (h & 0x80008000u);
+    const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7B80));  // 2^120
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), up);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Four codes of row a and four of row b: out[k] = (a_k, b_k).
+template <typename F> __device__ __forceinline__ void widen_pairs(uint32_t a, uint32_t b, uint32_t* out);
+template <> __device__ __forceinline__ void widen_pairs<KvInt8>(uint32_t a, uint32_t b, uint32_t* out) {
+    const uint32_t x = __byte_perm(a, b, 0x5140), y = __byte_perm(a, b, 0x7362);
+    out[0] = widen_int8_bf16<0>(x);
+    out[1] = widen_int8_bf16<1>(x);
+    out[2] = widen_int8_bf16<0>(y);
+    out[3] = widen_int8_bf16<1>(y);
+}
+template <> __device__ __forceinline__ void widen_pairs<KvE4m3>(uint32_t a, uint32_t b, uint32_t* out) {
+    const uint32_t x = __byte_perm(a, b, 0x5140), y = __byte_perm(a, b, 0x7362);
+    out[0] = widen_e4m3_bf16<0>(x);
+    out[1] = widen_e4m3_bf16<1>(x);
+    out[2] = widen_e4m3_bf16<0>(y);
+    out[3] = widen_e4m3_bf16<1>(y);
+}
+
+// Where 16-byte chunk c of row r lies in a group's tile: chunks are permuted so
+// that the 8 lanes that one shared-memory phase serves (K: two rows of four
+// chunks; V: four rows two apart, two chunks) touch different banks.
+template <int D> __device__ __forceinline__ uint32_t k_at(uint32_t r, uint32_t c) {
+    return r * D + ((D >= 128 ? c ^ ((r & 1) << 2) : c) << 4);
+}
+template <int D> __device__ __forceinline__ uint32_t v_at(uint32_t r, uint32_t c) {
+    if (D >= 128) return r * D + ((c ^ (((r >> 1) & 3) << 1)) << 4);
+    return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+    const int n = take ? 16 : 0;  // 0: the 16 bytes become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+// The keys [first, last] that a thread block's rows may see, from their
+// positions; first is rounded down to a step.
+struct Range {
+    int first, end;  // end: one past the last key
+};
+__device__ __forceinline__ Range key_range(int lo_pos, int hi_pos, int len, int window) {
+    Range r;
+    r.first = window ? max(0, lo_pos - window + 1) / kStepKeys * kStepKeys : 0;
+    r.end = min(hi_pos + 1, len);
+    return r;
+}
+
+// Rows [16 x tile, ...) of sequence seq: shared by the kernel and the join.
+struct Tile {
+    int seq, h, row0, n_rows, q0, len, start;
+    Range keys;
+};
+__device__ __forceinline__ bool tile_of(const KvAttnArgs& a, int tile, int h, int seq, Tile& t) {
+    const int G = a.n_q_heads / a.n_kv_heads;
+    t.seq = seq;
+    t.h = h;
+    t.q0 = a.b.cu[seq];
+    const int qn = a.b.cu[seq + 1] - t.q0;
+    t.row0 = tile * kRows;
+    t.n_rows = min(kRows, qn * G - t.row0);
+    if (t.n_rows <= 0) return false;
+    t.len = a.b.kv_lens[seq];
+    t.start = t.len - qn;
+    const long long cap = static_cast<long long>(a.b.pages_per_seq) * a.page_size;
+    if (t.len > cap) t.len = static_cast<int>(cap);
+    t.keys = key_range(t.start + t.row0 / G, t.start + (t.row0 + t.n_rows - 1) / G, t.len, a.window);
+    return true;
+}
+
+struct Split {
+    int n, chunk;  // ranges of `chunk` keys; the last takes what is left
+};
+
+template <typename T, int D> struct Cfg {
+    static constexpr bool kPair = sizeof(T) == 4;  // fp32 activations: queries as pairs
+    static constexpr int kTerms = kPair ? 3 : 2;      // bf16 terms of a weight
+    static constexpr int kStages = D == 256 ? 3 : 4;
+    static constexpr int kTile = kGroup * D;            // one group's K (or V) codes
+    static constexpr int kQPitch = D + 8;               // f16 elements
+    static constexpr int kRing = kWarps * kStages * 2 * kTile;
+    static constexpr int kJoin = kWarps * kRows * D * 4;  // the warps' results, after the ring's use
+    static constexpr int kData = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kQ = kRows * kQPitch * 2 * (kPair ? 2 : 1);
+    static constexpr int kLook = kWarps * kSpan * 12;
+    static constexpr int kSmem = kData + kQ + kLook + (kRows + 2 * kWarps * kRows) * 4;
+};
 
 template <typename T, typename F, int D>
-__global__ void __launch_bounds__(32 * kRowWarps) kv_attn_rows_kernel(const KvAttnArgs a) {
-    constexpr int E = D / 32;  // channels of a lane: lane + 32 e
-    const int tok = blockIdx.x, hq = blockIdx.y, h = hq / (a.n_q_heads / a.n_kv_heads);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int seq = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
-    const long long cap = static_cast<long long>(a.b.pages_per_seq) * a.page_size;
-    int len = a.b.kv_lens[seq];
-    const int pos = len - (a.b.cu[seq + 1] - tok);
-    if (len > cap) {
-        if (threadIdx.x == 0) atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
-        len = static_cast<int>(cap);
-    }
-    const int last = min(pos, len - 1), first = a.window ? max(0, pos - a.window + 1) : 0;
-    const T* q = static_cast<const T*>(a.q.data) + tok * a.q.token_stride + hq * a.q.head_stride;
-    float qr[E], o[E] = {};
+__global__ void __launch_bounds__(kThreads)
+kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
+    using C = Cfg<T, D>;
+    constexpr int S = C::kStages;
+    constexpr int NT = D / 8;               // 8-column tiles of the output
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int tile = blockIdx.x % n_tiles, split = blockIdx.x / n_tiles;
+    const int G = a.n_q_heads / a.n_kv_heads;
+    Tile t;
+    if (!tile_of(a, tile, blockIdx.y, blockIdx.z, t)) return;
+    if (tid == 0 && t.len < a.b.kv_lens[t.seq]) atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
+    const int begin = t.keys.first + split * sp.chunk;
+    const int end = split == sp.n - 1 ? t.keys.end : min(t.keys.end, begin + sp.chunk);
+    if (split > 0 && begin >= end) return;  // the join does not read this one
+
+    __half* q_hi = reinterpret_cast<__half*>(smem + C::kData);
+    int* look_page = reinterpret_cast<int*>(smem + C::kData + C::kQ) + warp * kSpan;
+    float* look_k = reinterpret_cast<float*>(smem + C::kData + C::kQ) + (kWarps + warp) * kSpan;
+    float* look_v = reinterpret_cast<float*>(smem + C::kData + C::kQ) + (2 * kWarps + warp) * kSpan;
+    float* q_scale = reinterpret_cast<float*>(smem + C::kData + C::kQ + C::kLook);
+    float* part_m = q_scale + kRows;
+    float* part_l = part_m + kWarps * kRows;
+
+    // Queries: 8 lanes a row, rounded to f16 under a power of two of the row.
+    {
+        constexpr int N = Vec16<T>::N, V = D / (8 * N);
+        const int r = tid >> 3, l8 = tid & 7, row = t.row0 + r;
+        float x[V * N];
+        float most = 0.0f;
+        if (r < t.n_rows) {
+            const T* src = static_cast<const T*>(a.q.data) + (t.q0 + row / G) * a.q.token_stride +
+                           (t.h * G + row % G) * a.q.head_stride;
 #pragma unroll
-    for (int e = 0; e < E; ++e) qr[e] = to_f32(q[lane + 32 * e]);
-    float m = -INFINITY, l = 0.0f;
-    for (int j = first + warp; j <= last; j += kRowWarps) {
-        const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + j / a.page_size];
-        if (page < 0 || page >= a.c.n_pages) {
-            if (lane == 0) atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
-            continue;
+            for (int v = 0; v < V; ++v) Vec16<T>::load(src + (v * 8 + l8) * N, x + v * N);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V * N; ++e) x[e] = 0.0f;
         }
-        const size_t block = static_cast<size_t>(page) * a.n_kv_heads + h;
-        const size_t at = (block * a.page_size + j % a.page_size) * D;
-        float s = 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += qr[e] * F::value(a.c.k[at + lane + 32 * e]);
-        s = group_sum<32>(s) * (a.c.k_scale[block] * a.scale);
-        const float mn = fmaxf(m, s), c = expf(m - mn), p = expf(s - mn);
-        const float pv = p * a.c.v_scale[block];
-        l = l * c + p;
+        for (int e = 0; e < V * N; ++e) most = fmaxf(most, fabsf(x[e]));
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * c + pv * F::value(a.c.v[at + lane + 32 * e]);
-        m = mn;
+        for (int off = 4; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+        const int ex = most > 0.0f && most <= 3.402823466e38f ? max(ilogbf(most), -100) : 0;
+        if (l8 == 0) q_scale[r] = scalbnf(a.scale * kLog2e, ex);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+                const int d = (v * 8 + l8) * N + e;
+                const float lo = scalbnf(x[v * N + e], -ex), hi = scalbnf(x[v * N + e + 1], -ex);
+                const uint32_t h = pack_f16(lo, hi);
+                *reinterpret_cast<uint32_t*>(q_hi + r * C::kQPitch + d) = h;
+                if (C::kPair)
+                    *reinterpret_cast<uint32_t*>(q_hi + (kRows + r) * C::kQPitch + d) = pack_f16_rest(h, lo, hi);
+            }
     }
-    __shared__ float sm[kRowWarps], sl[kRowWarps], so[kRowWarps][D];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
     __syncthreads();
-    float mm = -INFINITY, ll = 0.0f;
-    for (int w = 0; w < kRowWarps; ++w) mm = fmaxf(mm, sm[w]);
-    for (int w = 0; w < kRowWarps; ++w) ll += sl[w] == 0.0f ? 0.0f : sl[w] * expf(sm[w] - mm);
-    T* out = static_cast<T*>(a.out) + (static_cast<size_t>(tok) * a.n_q_heads + hq) * D;
-    for (int d = threadIdx.x; d < D; d += 32 * kRowWarps) {
-        float x = 0.0f;
-        for (int w = 0; w < kRowWarps; ++w) x += sl[w] == 0.0f ? 0.0f : so[w][d] * expf(sm[w] - mm);
-        out[d] = from_f32<T>(ll > 0.0f ? x / ll : 0.0f);
+
+    // A operand of 16 channels: channel order within 64 is (t4, step, 4), the order in which a lane
+    // reads 16 codes of a key.
+    const uint32_t q_base = static_cast<uint32_t>(__cvta_generic_to_shared(q_hi));
+    auto load_q = [&](int step, int part, uint32_t* f) {
+        const int d = (step >> 2) * 64 + 16 * t4 + 4 * (step & 3);
+        const uint2 u = lds64(q_base + ((part * kRows + g) * C::kQPitch + d) * 2);
+        const uint2 v = lds64(q_base + ((part * kRows + g + 8) * C::kQPitch + d) * 2);
+        f[0] = u.x; f[1] = v.x; f[2] = u.y; f[3] = v.y;
+    };
+    uint32_t qf[C::kPair ? 1 : D / 16][4];
+    if (!C::kPair)
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) load_q(s, 0, qf[C::kPair ? 0 : s]);
+
+    const float qs[2] = {q_scale[g], q_scale[g + 8]};
+    const int pos[2] = {t.start + (t.row0 + g) / G, t.start + (t.row0 + g + 8) / G};
+    const int min_pos = t.start + t.row0 / G;
+    const int max_lo = a.window ? t.start + (t.row0 + t.n_rows - 1) / G - a.window + 1 : 0;
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vs_low = INFINITY;
+
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * 2 * C::kTile;
+    const int n_steps = begin < end ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
+    for (int span = 0; span < n_steps; span += kSpan) {
+        const int steps = min(kSpan, n_steps - span);
+        const int key0 = begin + span * kStepKeys + warp * kGroup;
+        // pages and scales of this warp's groups
+        __syncwarp();
+        for (int i = lane; i < steps; i += 32) {
+            const int key = key0 + i * kStepKeys;
+            int page = -1;
+            float ks = 0.0f, vs = 0.0f;
+            if (key < end) {
+                page = a.b.table[static_cast<size_t>(t.seq) * a.b.pages_per_seq + key / a.page_size];
+                if (page < 0 || page >= a.c.n_pages) {
+                    // needed unless every row's window has left it behind
+                    if (key + kGroup > t.keys.first && (!a.window || key + kGroup - 1 > min_pos - a.window))
+                        atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
+                    page = -1;
+                } else {
+                    const size_t block = static_cast<size_t>(page) * a.n_kv_heads + t.h;
+                    ks = a.c.k_scale[block];
+                    vs = a.c.v_scale[block];
+                    if (vs > 0.0f) vs_low = fminf(vs_low, vs);
+                }
+            }
+            look_page[i] = page;
+            look_k[i] = ks;
+            look_v[i] = vs;
+        }
+        // Values of a scale of 0 add nothing to the output but count in the sum: such a group is
+        // given the smallest scale in sight, negative as a mark, so that it does not lift m.
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
+        for (int i = lane; i < steps; i += 32)
+            if (look_v[i] == 0.0f) look_v[i] = vs_low < INFINITY ? -vs_low : -1.0f;
+        __syncwarp();
+        auto fetch = [&](int i) {
+            if (i < steps) {
+                const int key = key0 + i * kStepKeys, page = look_page[i];
+                const size_t at = page < 0 ? 0 : ((static_cast<size_t>(page) * a.n_kv_heads + t.h) * a.page_size +
+                                                  key % a.page_size) * D;
+                const uint32_t slot = ring + (i % S) * 2 * C::kTile;
+#pragma unroll
+                for (int c = lane; c < C::kTile / 16; c += 32) {
+                    const uint32_t r = c / (D / 16), cc = c % (D / 16);
+                    const bool take = page >= 0 && key + static_cast<int>(r) < end;
+                    cp_async16(slot + k_at<D>(r, cc), a.c.k + at + (take ? c * 16 : 0), take);
+                    cp_async16(slot + C::kTile + v_at<D>(r, cc), a.c.v + at + (take ? c * 16 : 0), take);
+                }
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) fetch(i);
+        for (int i = 0; i < steps; ++i) {
+            cp_wait<S - 2>();
+            __syncwarp();
+            fetch(i + S - 1);
+            const int key = key0 + i * kStepKeys;
+            if (key >= end || look_page[i] < 0) continue;
+            const uint32_t kt = ring + (i % S) * 2 * C::kTile, vt = kt + C::kTile;
+
+            float s[2][4] = {};
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const uint4 w0 = lds128(kt + k_at<D>(g, 4 * j + t4)), w1 = lds128(kt + k_at<D>(g + 8, 4 * j + t4));
+                const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t b0, b1, c0, c1;
+                    widen_f16<F>(x0[e], b0, b1);
+                    widen_f16<F>(x1[e], c0, c1);
+                    if (C::kPair) {
+                        uint32_t f[4];
+                        load_q(4 * j + e, 1, f);
+                        mma_f16(s[0], f, b0, b1);
+                        mma_f16(s[1], f, c0, c1);
+                        load_q(4 * j + e, 0, f);
+                        mma_f16(s[0], f, b0, b1);
+                        mma_f16(s[1], f, c0, c1);
+                    } else {
+                        mma_f16(s[0], qf[C::kPair ? 0 : 4 * j + e], b0, b1);
+                        mma_f16(s[1], qf[C::kPair ? 0 : 4 * j + e], c0, c1);
+                    }
+                }
+            }
+            const float ks = look_k[i], vs = fabsf(look_v[i]), lv = log2f(vs);
+            const bool whole = key + kGroup - 1 <= min_pos && key >= max_lo && key + kGroup <= end;
+            float y[2][4], top[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float f = qs[r] * ks;
+                top[r] = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int j = key + (n >> 1) * 8 + 2 * t4 + (n & 1);
+                    float v = fmaf(s[n >> 1][2 * r + (n & 1)], f, lv);
+                    if (!whole && (j > pos[r] || j >= end || (a.window && j <= pos[r] - a.window))) v = -INFINITY;
+                    y[r][n] = v;
+                    top[r] = fmaxf(top[r], v);
+                }
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+            }
+            if (__any_sync(0xffffffffu, top[0] > m[0] + kLazy || top[1] > m[1] + kLazy)) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float mn = fmaxf(m[r], top[r]);
+                    const float c = m[r] == -INFINITY ? 0.0f : exp2_ftz(m[r] - mn);
+                    m[r] = mn;
+                    l[r] *= c;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        o[n][2 * r] *= c;
+                        o[n][2 * r + 1] *= c;
+                    }
+                }
+            }
+            uint32_t p[C::kTerms][4];  // weights as bf16 terms
+            const float inv = 1.0f / vs;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float ref = m[r] == -INFINITY ? 0.0f : m[r];
+                float w[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) w[n] = exp2_ftz(y[r][n] - ref);
+                l[r] = fmaf((w[0] + w[1]) + (w[2] + w[3]), inv, l[r]);
+#pragma unroll
+                for (int k = 0; k < C::kTerms; ++k)
+#pragma unroll
+                    for (int n = 0; n < 4; n += 2) {
+                        const uint32_t h = pack_bf16_pair(w[n], w[n + 1]);
+                        p[k][r + n] = h;
+                        w[n] -= bf16_low(h);
+                        w[n + 1] -= bf16_high(h);
+                    }
+            }
+            if (look_v[i] < 0.0f) continue;
+            // output: column n of 8-column tile (jj, e) is channel 128 jj + 16 n + e (D = 64: 8 n + e)
+#pragma unroll
+            for (int jj = 0; jj < (D >= 128 ? D / 128 : 1); ++jj) {
+                constexpr int W = D >= 128 ? 4 : 2;  // words of a lane's run of channels
+                uint32_t x[4][W];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t row = 2 * t4 + (r & 1) + 8 * (r >> 1);
+                    if (D >= 128) {
+                        const uint4 v = lds128(vt + v_at<D>(row, 8 * jj + g));
+                        x[r][0] = v.x; x[r][1] = v.y; x[r][W - 2] = v.z; x[r][W - 1] = v.w;
+                    } else {
+                        const uint2 v = lds64(vt + v_at<D>(row, g >> 1) + (g & 1) * 8);
+                        x[r][0] = v.x; x[r][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    uint32_t b0[4], b1[4];
+                    widen_pairs<F>(x[0][e], x[1][e], b0);
+                    widen_pairs<F>(x[2][e], x[3][e], b1);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float* acc = o[jj * 16 + 4 * e + k];
+#pragma unroll
+                        for (int n = C::kTerms - 1; n >= 0; --n) mma_bf16(acc, p[n], b0[k], b1[k]);
+                    }
+                }
+            }
+        }
+        cp_wait<0>();
     }
+
+    // Join the four warps: rows' references and sums, then the scaled outputs through shared memory.
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (t4 == 0) {
+            part_m[warp * kRows + g + 8 * r] = m[r];
+            part_l[warp * kRows + g + 8 * r] = l[r];
+        }
+    }
+    __syncthreads();
+    float* all = reinterpret_cast<float*>(smem);  // [warp][row][D], float4 slots permuted (bank conflicts)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = g + 8 * r;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * kRows + row]);
+        const float c = m[r] == -INFINITY ? 0.0f : exp2_ftz(m[r] - top);
+        float* dst = all + (warp * kRows + row) * D;
+        constexpr int RUN = D >= 128 ? 16 : 8;  // consecutive channels of one column
+#pragma unroll
+        for (int jj = 0; jj < (D >= 128 ? D / 128 : 1); ++jj)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < RUN; e += 4) {
+                    const int d = 128 * jj + RUN * (2 * t4 + n) + e;
+                    const int slot = (d >> 2) ^ (((row & 1) << 2) | ((d >> 5) & 3));
+                    float4 v;
+                    v.x = o[jj * 16 + e][2 * r + n] * c;
+                    v.y = o[jj * 16 + e + 1][2 * r + n] * c;
+                    v.z = o[jj * 16 + e + 2][2 * r + n] * c;
+                    v.w = o[jj * 16 + e + 3][2 * r + n] * c;
+                    *reinterpret_cast<float4*>(dst + 4 * slot) = v;
+                }
+    }
+    __syncthreads();
+    const size_t unit = ((static_cast<size_t>(t.seq) * a.n_kv_heads + t.h) * n_tiles + tile) * sp.n + split;
+    float* part = a.partial + unit * kRows * (D + 2);
+    for (int i = tid; i < t.n_rows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), d = (i % (D / 4)) * 4;
+        const int slot = (d >> 2) ^ (((row & 1) << 2) | ((d >> 5) & 3));
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(all + (w * kRows + row) * D + 4 * slot);
+            x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
+        }
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * kRows + row]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = part_m[w * kRows + row];
+            sum += mw == -INFINITY ? 0.0f : part_l[w * kRows + row] * exp2_ftz(mw - top);
+        }
+        if (sp.n > 1) {
+            *reinterpret_cast<float4*>(part + row * D + d) = x;
+            if (d == 0) {
+                part[kRows * D + row] = top;
+                part[kRows * D + kRows + row] = sum;
+            }
+        } else {
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            const int rr = t.row0 + row;
+            T* out = static_cast<T*>(a.out) +
+                     (static_cast<size_t>(t.q0 + rr / G) * a.n_q_heads + t.h * G + rr % G) * D + d;
+            if (C::kPair) {
+                *reinterpret_cast<float4*>(out) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+            } else {
+                uint2 w;
+                w.x = pack_bf16_pair(x.x * inv, x.y * inv);
+                w.y = pack_bf16_pair(x.z * inv, x.w * inv);
+                *reinterpret_cast<uint2*>(out) = w;
+            }
+        }
+    }
+}
+
+// Joins the splits of one row: out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m).
+template <typename T, int D>
+__global__ void __launch_bounds__(D / 4) kv_attn_join(const KvAttnArgs a, const Split sp, const int n_tiles) {
+    const int tile = blockIdx.x / kRows, row = blockIdx.x % kRows, G = a.n_q_heads / a.n_kv_heads;
+    Tile t;
+    if (!tile_of(a, tile, blockIdx.y, blockIdx.z, t) || row >= t.n_rows) return;
+    const int span = t.keys.end - t.keys.first;
+    const int n = max(1, min(sp.n, (span + sp.chunk - 1) / sp.chunk));
+    const size_t unit = ((static_cast<size_t>(t.seq) * a.n_kv_heads + t.h) * n_tiles + tile) * sp.n;
+    const float* part = a.partial + unit * kRows * (D + 2);
+    constexpr size_t kNext = kRows * (D + 2);
+    float top = -INFINITY, sum = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < n; ++s) top = fmaxf(top, part[s * kNext + kRows * D + row]);
+    for (int s = 0; s < n; ++s) {
+        const float ms = part[s * kNext + kRows * D + row];
+        if (ms == -INFINITY) continue;
+        const float c = exp2_ftz(ms - top);
+        const float4 v = *reinterpret_cast<const float4*>(part + s * kNext + row * D + 4 * threadIdx.x);
+        sum += part[s * kNext + kRows * D + kRows + row] * c;
+        x.x += v.x * c; x.y += v.y * c; x.z += v.z * c; x.w += v.w * c;
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int rr = t.row0 + row;
+    T* out = static_cast<T*>(a.out) + (static_cast<size_t>(t.q0 + rr / G) * a.n_q_heads + t.h * G + rr % G) * D +
+             4 * threadIdx.x;
+    if (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(out) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    } else {
+        uint2 w;
+        w.x = pack_bf16_pair(x.x * inv, x.y * inv);
+        w.y = pack_bf16_pair(x.z * inv, x.w * inv);
+        *reinterpret_cast<uint2*>(out) = w;
+    }
+}
+
+// How many ranges the keys are split into: enough thread blocks for a few
+// rounds over the 152 SMs, but no range below kMinChunk keys (a range's fixed
+// cost, its queries and its partial result, is about that of 100 keys).
+constexpr int kMinChunk = 256;
+constexpr long long kTargetBlocks = 152 * 8;
+Split split_of(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int window, long long max_kv_len) {
+    const int G = n_q_heads / n_kv_heads;
+    const long long tiles = (static_cast<long long>(max_q) * G + kRows - 1) / kRows;
+    const long long units = std::max(1LL, tiles * n_kv_heads * n_seq);
+    long long span = std::max(1LL, max_kv_len);
+    if (window) span = std::min(span, static_cast<long long>(window) + max_q + kStepKeys);
+    long long n = std::min((kTargetBlocks + units - 1) / units, (span + kMinChunk - 1) / kMinChunk);
+    n = std::max(1LL, std::min(n, 512LL));
+    long long chunk = (span + n - 1) / n;
+    chunk = (chunk + kStepKeys - 1) / kStepKeys * kStepKeys;
+    return Split{static_cast<int>((span + chunk - 1) / chunk), static_cast<int>(chunk)};
 }
 
 template <typename T, typename F, int D>
 cudaError_t attn_t(const KvAttnArgs& a, cudaStream_t st) {
-    kv_attn_rows_kernel<T, F, D>
-        <<<dim3(a.b.n_tokens, a.n_q_heads), 32 * kRowWarps, 0, st>>>(a);
-    return cudaGetLastError();
+    using C = Cfg<T, D>;
+    const int G = a.n_q_heads / a.n_kv_heads;
+    const Split sp = split_of(a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, a.window, a.max_kv_len);
+    const long long tiles = (static_cast<long long>(a.b.max_q) * G + kRows - 1) / kRows;
+    if (tiles * sp.n > 0x7fffffffLL / kRows) return cudaErrorInvalidConfiguration;
+    static std::atomic<unsigned long long> ready{0};
+    cudaError_t e = allow_smem(kv_attn_kernel<T, F, D>, C::kSmem, ready);
+    if (e != cudaSuccess) return e;
+    const int nt = static_cast<int>(tiles);
+    e = timed_launch("kv_attn", st, [&] {
+        kv_attn_kernel<T, F, D><<<dim3(nt * sp.n, a.n_kv_heads, a.b.n_seq), kThreads, C::kSmem, st>>>(a, sp, nt);
+        return cudaGetLastError();
+    });
+    if (e != cudaSuccess || sp.n == 1) return e;
+    return timed_launch("kv_attn_join", st, [&] {
+        kv_attn_join<T, D><<<dim3(nt * kRows, a.n_kv_heads, a.b.n_seq), D / 4, 0, st>>>(a, sp, nt);
+        return cudaGetLastError();
+    });
 }
 
 }  // namespace
 
-size_t kv_attention_workspace(int, const int32_t*, int, int, int, bool, int) { return 0; }
+size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window, bool,
+                              int max_kv_len) {
+    if (max_q == 0) return 0;
+    const Split sp = split_of(n_seq, max_q, n_q_heads, n_kv_heads, window, max_kv_len);
+    if (sp.n == 1) return 0;
+    const size_t tiles = (static_cast<size_t>(max_q) * (n_q_heads / n_kv_heads) + kRows - 1) / kRows;
+    const size_t bytes = tiles * n_kv_heads * n_seq * sp.n * kRows * (head_dim + 2) * sizeof(float);
+    return (bytes + 255) & ~static_cast<size_t>(255);
+}
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
     return GDN_KV_PICK(attn_t);
