@@ -18,7 +18,12 @@
 // output's own rounding.  With fp32 activations queries are f16 (hi, lo) pairs,
 // 22 bits, and weights three bf16 terms, 24 bits.
 //
-// One thread block takes 16 rows and a range of keys.  Each of its four warps
+// One thread block takes 8, 16 or 32 rows and a range of keys.  Keys (and value
+// channels) are the tensor core's M, the rows its N, so that a group of 8 heads
+// fills the tile and a code is widened once for all rows:
+//   S^T [16 keys x rows] = K Q^T,   O^T [16 channels x rows] += V^T P^T
+// The accumulator of S^T holds a key's rows where the second product wants a
+// row's keys: one 8 x 8 transpose per 8 keys and term.  Each of the four warps
 // takes every fourth group of 16 keys on its own, with its own running state
 // and its own ring of asynchronous copies (no block-wide barrier until the
 // end): 16 keys lie in one page, so a group is one contiguous run of codes and
@@ -38,10 +43,9 @@ namespace {
 __device__ int g_kv_attn_error = 0;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kRows = 16;         // query rows of a thread block (the tensor core's M)
 constexpr int kGroup = 16;        // keys of a warp's step
 constexpr int kStepKeys = kGroup * kWarps;
-constexpr int kSpan = 64;         // steps whose pages and scales are looked up at a time
+constexpr int kSpan = 32;         // steps whose pages and scales are looked up at a time
 constexpr float kLazy = 8.0f;     // a reference lags behind the maximum by at most 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -62,6 +66,12 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transposes an 8 x 8 tile of 16-bit values held two a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -172,19 +182,19 @@ __device__ __forceinline__ Range key_range(int lo_pos, int hi_pos, int len, int 
     return r;
 }
 
-// Rows [16 x tile, ...) of sequence seq: shared by the kernel and the join.
+// Rows [rows x tile, ...) of sequence seq: shared by the kernel and the join.
 struct Tile {
     int seq, h, row0, n_rows, q0, len, start;
     Range keys;
 };
-__device__ __forceinline__ bool tile_of(const KvAttnArgs& a, int tile, int h, int seq, Tile& t) {
+__device__ __forceinline__ bool tile_of(const KvAttnArgs& a, int rows, int tile, int h, int seq, Tile& t) {
     const int G = a.n_q_heads / a.n_kv_heads;
     t.seq = seq;
     t.h = h;
     t.q0 = a.b.cu[seq];
     const int qn = a.b.cu[seq + 1] - t.q0;
-    t.row0 = tile * kRows;
-    t.n_rows = min(kRows, qn * G - t.row0);
+    t.row0 = tile * rows;
+    t.n_rows = min(rows, qn * G - t.row0);
     if (t.n_rows <= 0) return false;
     t.len = a.b.kv_lens[seq];
     t.start = t.len - qn;
@@ -198,32 +208,47 @@ struct Split {
     int n, chunk;  // ranges of `chunk` keys; the last takes what is left
 };
 
-template <typename T, int D> struct Cfg {
-    static constexpr bool kPair = sizeof(T) == 4;  // fp32 activations: queries as pairs
+// Four channels of a row of the output.
+template <typename T, int D>
+__device__ __forceinline__ void store_row(const KvAttnArgs& a, const Tile& t, int row, int d, float4 x, float f) {
+    const int G = a.n_q_heads / a.n_kv_heads;
+    T* out = static_cast<T*>(a.out) + (static_cast<size_t>(t.q0 + row / G) * a.n_q_heads + t.h * G + row % G) * D + d;
+    if (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(out) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+    else
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16_pair(x.x * f, x.y * f), pack_bf16_pair(x.z * f, x.w * f));
+}
+
+template <typename T, int D, int NQ> struct Cfg {
+    static constexpr bool kPair = sizeof(T) == 4;     // fp32 activations: queries as pairs
     static constexpr int kTerms = kPair ? 3 : 2;      // bf16 terms of a weight
-    static constexpr int kStages = D == 256 ? 3 : 4;
-    static constexpr int kTile = kGroup * D;            // one group's K (or V) codes
-    static constexpr int kQPitch = D + 8;               // f16 elements
+    static constexpr int kRows = 8 * NQ;
+    static constexpr int kTile = kGroup * D;          // one group's K (or V) codes
+    static constexpr int kStages = D == 256 ? 2 : D == 128 ? 3 : 4;
+    static constexpr int kQPitch = D + 16;            // f16 elements
     static constexpr int kRing = kWarps * kStages * 2 * kTile;
     static constexpr int kJoin = kWarps * kRows * D * 4;  // the warps' results, after the ring's use
     static constexpr int kData = kRing > kJoin ? kRing : kJoin;
     static constexpr int kQ = kRows * kQPitch * 2 * (kPair ? 2 : 1);
     static constexpr int kLook = kWarps * kSpan * 12;
     static constexpr int kSmem = kData + kQ + kLook + (kRows + 2 * kWarps * kRows) * 4;
+    // thread blocks of an SM that the registers are planned for
+    static constexpr int kBlocks = D * NQ <= 128 ? 4 : D * NQ <= 256 ? 3 : 2;
 };
 
-template <typename T, typename F, int D>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, typename F, int D, int NQ>
+__global__ void __launch_bounds__(kThreads, Cfg<T, D, NQ>::kBlocks)
 kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
-    using C = Cfg<T, D>;
-    constexpr int S = C::kStages;
-    constexpr int NT = D / 8;               // 8-column tiles of the output
+    using C = Cfg<T, D, NQ>;
+    constexpr int S = C::kStages, R = C::kRows;
+    constexpr int MT = D / 16;              // 16-channel tiles of the output
+    constexpr int CH = NQ == 1 ? 2 : 1;     // accumulators a score is spread over
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int tile = blockIdx.x % n_tiles, split = blockIdx.x / n_tiles;
     const int G = a.n_q_heads / a.n_kv_heads;
     Tile t;
-    if (!tile_of(a, tile, blockIdx.y, blockIdx.z, t)) return;
+    if (!tile_of(a, R, tile, blockIdx.y, blockIdx.z, t)) return;
     if (tid == 0 && t.len < a.b.kv_lens[t.seq]) atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
     const int begin = t.keys.first + split * sp.chunk;
     const int end = split == sp.n - 1 ? t.keys.end : min(t.keys.end, begin + sp.chunk);
@@ -234,13 +259,13 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     float* look_k = reinterpret_cast<float*>(smem + C::kData + C::kQ) + (kWarps + warp) * kSpan;
     float* look_v = reinterpret_cast<float*>(smem + C::kData + C::kQ) + (2 * kWarps + warp) * kSpan;
     float* q_scale = reinterpret_cast<float*>(smem + C::kData + C::kQ + C::kLook);
-    float* part_m = q_scale + kRows;
-    float* part_l = part_m + kWarps * kRows;
+    float* part_m = q_scale + R;
+    float* part_l = part_m + kWarps * R;
 
     // Queries: 8 lanes a row, rounded to f16 under a power of two of the row.
-    {
+    for (int r = tid >> 3; r < (R + 15) / 16 * 16; r += kThreads / 8) {
         constexpr int N = Vec16<T>::N, V = D / (8 * N);
-        const int r = tid >> 3, l8 = tid & 7, row = t.row0 + r;
+        const int l8 = tid & 7, row = t.row0 + r;
         float x[V * N];
         float most = 0.0f;
         if (r < t.n_rows) {
@@ -256,6 +281,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
         for (int e = 0; e < V * N; ++e) most = fmaxf(most, fabsf(x[e]));
 #pragma unroll
         for (int off = 4; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+        if (r >= R) continue;
         const int ex = most > 0.0f && most <= 3.402823466e38f ? max(ilogbf(most), -100) : 0;
         if (l8 == 0) q_scale[r] = scalbnf(a.scale * kLog2e, ex);
 #pragma unroll
@@ -266,51 +292,58 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                 const float lo = scalbnf(x[v * N + e], -ex), hi = scalbnf(x[v * N + e + 1], -ex);
                 const uint32_t h = pack_f16(lo, hi);
                 *reinterpret_cast<uint32_t*>(q_hi + r * C::kQPitch + d) = h;
-                if (C::kPair)
-                    *reinterpret_cast<uint32_t*>(q_hi + (kRows + r) * C::kQPitch + d) = pack_f16_rest(h, lo, hi);
+                if (C::kPair) *reinterpret_cast<uint32_t*>(q_hi + (R + r) * C::kQPitch + d) = pack_f16_rest(h, lo, hi);
             }
     }
     __syncthreads();
 
-    // A operand of 16 channels: channel order within 64 is (t4, step, 4), the order in which a lane
+    // B operand of 16 channels: channel order within 64 is (t4, step, 4), the order in which a lane
     // reads 16 codes of a key.
     const uint32_t q_base = static_cast<uint32_t>(__cvta_generic_to_shared(q_hi));
-    auto load_q = [&](int step, int part, uint32_t* f) {
+    auto load_q = [&](int step, int part, int nq) {
         const int d = (step >> 2) * 64 + 16 * t4 + 4 * (step & 3);
-        const uint2 u = lds64(q_base + ((part * kRows + g) * C::kQPitch + d) * 2);
-        const uint2 v = lds64(q_base + ((part * kRows + g + 8) * C::kQPitch + d) * 2);
-        f[0] = u.x; f[1] = v.x; f[2] = u.y; f[3] = v.y;
+        return lds64(q_base + ((part * R + nq * 8 + g) * C::kQPitch + d) * 2);
     };
-    uint32_t qf[C::kPair ? 1 : D / 16][4];
+    uint2 qf[C::kPair ? 1 : D / 16][NQ];
     if (!C::kPair)
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) load_q(s, 0, qf[C::kPair ? 0 : s]);
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) qf[C::kPair ? 0 : s][n] = load_q(s, 0, n);
 
-    const float qs[2] = {q_scale[g], q_scale[g + 8]};
-    const int pos[2] = {t.start + (t.row0 + g) / G, t.start + (t.row0 + g + 8) / G};
     const int min_pos = t.start + t.row0 / G;
     const int max_lo = a.window ? t.start + (t.row0 + t.n_rows - 1) / G - a.window + 1 : 0;
-    float o[NT][4];
+    float o[MT][NQ][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vs_low = INFINITY;
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
+    float qs[NQ][2], m[NQ][2], l[NQ][2], vs_low = INFINITY;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            qs[n][c] = q_scale[8 * n + 2 * t4 + c];
+            m[n][c] = -INFINITY;
+            l[n][c] = 0.0f;
+        }
 
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * 2 * C::kTile;
     const int n_steps = begin < end ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
     for (int span = 0; span < n_steps; span += kSpan) {
         const int steps = min(kSpan, n_steps - span);
         const int key0 = begin + span * kStepKeys + warp * kGroup;
-        // pages and scales of this warp's groups
+        // pages and scales of this warp's groups, one a lane
         __syncwarp();
-        for (int i = lane; i < steps; i += 32) {
-            const int key = key0 + i * kStepKeys;
+        {
+            const int key = key0 + lane * kStepKeys;
             int page = -1;
-            float ks = 0.0f, vs = 0.0f;
-            if (key < end) {
+            float ks = 0.0f, vs = 1.0f;
+            if (lane < steps && key < end) {
                 page = a.b.table[static_cast<size_t>(t.seq) * a.b.pages_per_seq + key / a.page_size];
                 if (page < 0 || page >= a.c.n_pages) {
                     // needed unless every row's window has left it behind
-                    if (key + kGroup > t.keys.first && (!a.window || key + kGroup - 1 > min_pos - a.window))
+                    if (!a.window || key + kGroup - 1 > min_pos - a.window)
                         atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
                     page = -1;
                 } else {
@@ -320,16 +353,15 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                     if (vs > 0.0f) vs_low = fminf(vs_low, vs);
                 }
             }
-            look_page[i] = page;
-            look_k[i] = ks;
-            look_v[i] = vs;
-        }
-        // Values of a scale of 0 add nothing to the output but count in the sum: such a group is
-        // given the smallest scale in sight, negative as a mark, so that it does not lift m.
+            // Values of a scale of 0 add nothing to the output but count in the sum: such a group
+            // is given the smallest scale in sight, negative as a mark, so that it does not lift m.
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
-        for (int i = lane; i < steps; i += 32)
-            if (look_v[i] == 0.0f) look_v[i] = vs_low < INFINITY ? -vs_low : -1.0f;
+            for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
+            if (vs == 0.0f) vs = vs_low < INFINITY ? -vs_low : -1.0f;
+            look_page[lane] = page;
+            look_k[lane] = ks;
+            look_v[lane] = vs;
+        }
         __syncwarp();
         auto fetch = [&](int i) {
             if (i < steps) {
@@ -337,12 +369,22 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                 const size_t at = page < 0 ? 0 : ((static_cast<size_t>(page) * a.n_kv_heads + t.h) * a.page_size +
                                                   key % a.page_size) * D;
                 const uint32_t slot = ring + (i % S) * 2 * C::kTile;
+                const uint8_t *ksrc = a.c.k + at + lane * 16, *vsrc = a.c.v + at + lane * 16;
+                if (page >= 0 && key + kGroup <= end) {
 #pragma unroll
-                for (int c = lane; c < C::kTile / 16; c += 32) {
-                    const uint32_t r = c / (D / 16), cc = c % (D / 16);
-                    const bool take = page >= 0 && key + static_cast<int>(r) < end;
-                    cp_async16(slot + k_at<D>(r, cc), a.c.k + at + (take ? c * 16 : 0), take);
-                    cp_async16(slot + C::kTile + v_at<D>(r, cc), a.c.v + at + (take ? c * 16 : 0), take);
+                    for (int c = 0; c < C::kTile / 16; c += 32) {
+                        const uint32_t r = (c + lane) / (D / 16), cc = lane % (D / 16);
+                        cp_async16(slot + k_at<D>(r, cc), ksrc + c * 16, true);
+                        cp_async16(slot + C::kTile + v_at<D>(r, cc), vsrc + c * 16, true);
+                    }
+                } else {  // rows past the end become zeros: what lies there may be no number
+#pragma unroll
+                    for (int c = 0; c < C::kTile / 16; c += 32) {
+                        const uint32_t r = (c + lane) / (D / 16), cc = lane % (D / 16);
+                        const bool take = page >= 0 && key + static_cast<int>(r) < end;
+                        cp_async16(slot + k_at<D>(r, cc), take ? ksrc + c * 16 : a.c.k, take);
+                        cp_async16(slot + C::kTile + v_at<D>(r, cc), take ? vsrc + c * 16 : a.c.v, take);
+                    }
                 }
             }
             cp_commit();
@@ -350,90 +392,115 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
 #pragma unroll
         for (int i = 0; i < S - 1; ++i) fetch(i);
         for (int i = 0; i < steps; ++i) {
-            cp_wait<S - 2>();
-            __syncwarp();
-            fetch(i + S - 1);
+            if (S > 2) {  // the slot fetched into was read in the step before
+                cp_wait<S - 2>();
+                __syncwarp();
+                fetch(i + S - 1);
+            } else {
+                __syncwarp();
+                fetch(i + 1);
+                cp_wait<1>();
+                __syncwarp();
+            }
             const int key = key0 + i * kStepKeys;
             if (key >= end || look_page[i] < 0) continue;
             const uint32_t kt = ring + (i % S) * 2 * C::kTile, vt = kt + C::kTile;
 
-            float s[2][4] = {};
+            float s[CH][NQ][4];
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) s[c][n][0] = s[c][n][1] = s[c][n][2] = s[c][n][3] = 0.0f;
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
                 const uint4 w0 = lds128(kt + k_at<D>(g, 4 * j + t4)), w1 = lds128(kt + k_at<D>(g + 8, 4 * j + t4));
                 const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    uint32_t b0, b1, c0, c1;
-                    widen_f16<F>(x0[e], b0, b1);
-                    widen_f16<F>(x1[e], c0, c1);
-                    if (C::kPair) {
-                        uint32_t f[4];
-                        load_q(4 * j + e, 1, f);
-                        mma_f16(s[0], f, b0, b1);
-                        mma_f16(s[1], f, c0, c1);
-                        load_q(4 * j + e, 0, f);
-                        mma_f16(s[0], f, b0, b1);
-                        mma_f16(s[1], f, c0, c1);
-                    } else {
-                        mma_f16(s[0], qf[C::kPair ? 0 : 4 * j + e], b0, b1);
-                        mma_f16(s[1], qf[C::kPair ? 0 : 4 * j + e], c0, c1);
+                    uint32_t f[4];
+                    widen_f16<F>(x0[e], f[0], f[2]);
+                    widen_f16<F>(x1[e], f[1], f[3]);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        if (C::kPair) {
+                            const uint2 lo = load_q(4 * j + e, 1, n), hi = load_q(4 * j + e, 0, n);
+                            mma_f16(s[e % CH][n], f, lo.x, lo.y);
+                            mma_f16(s[e % CH][n], f, hi.x, hi.y);
+                        } else {
+                            const uint2 b = qf[C::kPair ? 0 : 4 * j + e][n];
+                            mma_f16(s[e % CH][n], f, b.x, b.y);
+                        }
                     }
                 }
             }
             const float ks = look_k[i], vs = fabsf(look_v[i]), lv = log2f(vs);
             const bool whole = key + kGroup - 1 <= min_pos && key >= max_lo && key + kGroup <= end;
-            float y[2][4], top[2];
+            bool lift = false;
+            float top[NQ][2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float f = qs[r] * ks;
-                top[r] = -INFINITY;
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int j = key + (n >> 1) * 8 + 2 * t4 + (n & 1);
-                    float v = fmaf(s[n >> 1][2 * r + (n & 1)], f, lv);
-                    if (!whole && (j > pos[r] || j >= end || (a.window && j <= pos[r] - a.window))) v = -INFINITY;
-                    y[r][n] = v;
-                    top[r] = fmaxf(top[r], v);
-                }
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            }
-            if (__any_sync(0xffffffffu, top[0] > m[0] + kLazy || top[1] > m[1] + kLazy)) {
+                for (int c = 0; c < 2; ++c) {
+                    const float f = qs[n][c] * ks;
+                    float v[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float mn = fmaxf(m[r], top[r]);
-                    const float c = m[r] == -INFINITY ? 0.0f : exp2_ftz(m[r] - mn);
-                    m[r] = mn;
-                    l[r] *= c;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        o[n][2 * r] *= c;
-                        o[n][2 * r + 1] *= c;
+                    for (int k = 0; k < 2; ++k) {
+                        float x = s[0][n][2 * k + c];
+                        if (CH > 1) x += s[CH - 1][n][2 * k + c];
+                        v[k] = fmaf(x, f, lv);
+                        if (!whole) {
+                            const int j = key + g + 8 * k, pos = t.start + (t.row0 + 8 * n + 2 * t4 + c) / G;
+                            if (j > pos || j >= end || (a.window && j <= pos - a.window)) v[k] = -INFINITY;
+                        }
+                        s[0][n][2 * k + c] = v[k];
                     }
+                    top[n][c] = fmaxf(v[0], v[1]);
+                    lift |= top[n][c] > m[n][c] + kLazy;
                 }
+            if (__any_sync(0xffffffffu, lift)) {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mn = top[n][c];
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+                        mn = fmaxf(m[n][c], mn);
+                        const float f = m[n][c] == -INFINITY ? 0.0f : exp2_ftz(m[n][c] - mn);
+                        m[n][c] = mn;
+                        l[n][c] *= f;
+#pragma unroll
+                        for (int i2 = 0; i2 < MT; ++i2) {
+                            o[i2][n][c] *= f;
+                            o[i2][n][2 + c] *= f;
+                        }
+                    }
             }
-            uint32_t p[C::kTerms][4];  // weights as bf16 terms
+            uint2 p[C::kTerms][NQ];  // weights as bf16 terms
             const float inv = 1.0f / vs;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float ref = m[r] == -INFINITY ? 0.0f : m[r];
+            for (int n = 0; n < NQ; ++n) {
                 float w[4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) w[n] = exp2_ftz(y[r][n] - ref);
-                l[r] = fmaf((w[0] + w[1]) + (w[2] + w[3]), inv, l[r]);
+                for (int c = 0; c < 2; ++c) {
+                    const float ref = m[n][c] == -INFINITY ? 0.0f : m[n][c];
+                    w[c] = exp2_ftz(s[0][n][c] - ref);
+                    w[2 + c] = exp2_ftz(s[0][n][2 + c] - ref);
+                    l[n][c] = fmaf(w[c] + w[2 + c], inv, l[n][c]);
+                }
 #pragma unroll
-                for (int k = 0; k < C::kTerms; ++k)
-#pragma unroll
-                    for (int n = 0; n < 4; n += 2) {
-                        const uint32_t h = pack_bf16_pair(w[n], w[n + 1]);
-                        p[k][r + n] = h;
-                        w[n] -= bf16_low(h);
-                        w[n + 1] -= bf16_high(h);
-                    }
+                for (int k = 0; k < C::kTerms; ++k) {
+                    const uint32_t u = pack_bf16_pair(w[0], w[1]), v = pack_bf16_pair(w[2], w[3]);
+                    w[0] -= bf16_low(u);
+                    w[1] -= bf16_high(u);
+                    w[2] -= bf16_low(v);
+                    w[3] -= bf16_high(v);
+                    p[k][n] = make_uint2(transpose8(u), transpose8(v));
+                }
             }
             if (look_v[i] < 0.0f) continue;
-            // output: column n of 8-column tile (jj, e) is channel 128 jj + 16 n + e (D = 64: 8 n + e)
+            // output: a lane's run of 16 channels (D = 64: 8), 128 jj + 16 g + e; 16-channel tile
+            // (jj, e / 2) holds e in its first eight rows and e + 1 in the others
 #pragma unroll
             for (int jj = 0; jj < (D >= 128 ? D / 128 : 1); ++jj) {
                 constexpr int W = D >= 128 ? 4 : 2;  // words of a lane's run of channels
@@ -451,15 +518,17 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                 }
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
-                    uint32_t b0[4], b1[4];
-                    widen_pairs<F>(x[0][e], x[1][e], b0);
-                    widen_pairs<F>(x[2][e], x[3][e], b1);
+                    uint32_t lo[4], hi[4];
+                    widen_pairs<F>(x[0][e], x[1][e], lo);
+                    widen_pairs<F>(x[2][e], x[3][e], hi);
+                    const uint32_t f0[4] = {lo[0], lo[1], hi[0], hi[1]}, f1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float* acc = o[jj * 16 + 4 * e + k];
+                    for (int k = C::kTerms - 1; k >= 0; --k)
 #pragma unroll
-                        for (int n = C::kTerms - 1; n >= 0; --n) mma_bf16(acc, p[n], b0[k], b1[k]);
-                    }
+                        for (int n = 0; n < NQ; ++n) {
+                            mma_bf16(o[jj * 8 + 2 * e][n], f0, p[k][n].x, p[k][n].y);
+                            mma_bf16(o[jj * 8 + 2 * e + 1][n], f1, p[k][n].x, p[k][n].y);
+                        }
                 }
             }
         }
@@ -468,158 +537,178 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
 
     // Join the four warps: rows' references and sums, then the scaled outputs through shared memory.
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (t4 == 0) {
-            part_m[warp * kRows + g + 8 * r] = m[r];
-            part_l[warp * kRows + g + 8 * r] = l[r];
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], off);
+            if (g == 0) {
+                part_m[warp * R + 8 * n + 2 * t4 + c] = m[n][c];
+                part_l[warp * R + 8 * n + 2 * t4 + c] = l[n][c];
+            }
         }
-    }
     __syncthreads();
     float* all = reinterpret_cast<float*>(smem);  // [warp][row][D], float4 slots permuted (bank conflicts)
+    constexpr int RUN = D >= 128 ? 16 : 8;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-        float top = -INFINITY;
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * kRows + row]);
-        const float c = m[r] == -INFINITY ? 0.0f : exp2_ftz(m[r] - top);
-        float* dst = all + (warp * kRows + row) * D;
-        constexpr int RUN = D >= 128 ? 16 : 8;  // consecutive channels of one column
+        for (int c = 0; c < 2; ++c) {
+            const int row = 8 * n + 2 * t4 + c;
+            float top = -INFINITY;
 #pragma unroll
-        for (int jj = 0; jj < (D >= 128 ? D / 128 : 1); ++jj)
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * R + row]);
+            const float f = m[n][c] == -INFINITY ? 0.0f : exp2_ftz(m[n][c] - top);
+            float* dst = all + (warp * R + row) * D;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int jj = 0; jj < (D >= 128 ? D / 128 : 1); ++jj)
 #pragma unroll
                 for (int e = 0; e < RUN; e += 4) {
-                    const int d = 128 * jj + RUN * (2 * t4 + n) + e;
-                    const int slot = (d >> 2) ^ (((row & 1) << 2) | ((d >> 5) & 3));
-                    float4 v;
-                    v.x = o[jj * 16 + e][2 * r + n] * c;
-                    v.y = o[jj * 16 + e + 1][2 * r + n] * c;
-                    v.z = o[jj * 16 + e + 2][2 * r + n] * c;
-                    v.w = o[jj * 16 + e + 3][2 * r + n] * c;
-                    *reinterpret_cast<float4*>(dst + 4 * slot) = v;
+                    const int slot = ((128 * jj + RUN * g + e) >> 2) ^ ((row >> 1) & 3);
+                    const auto& u = o[jj * 8 + e / 2][n];
+                    const auto& v = o[jj * 8 + e / 2 + 1][n];
+                    *reinterpret_cast<float4*>(dst + 4 * slot) =
+                        make_float4(u[c] * f, u[2 + c] * f, v[c] * f, v[2 + c] * f);
                 }
-    }
+        }
     __syncthreads();
     const size_t unit = ((static_cast<size_t>(t.seq) * a.n_kv_heads + t.h) * n_tiles + tile) * sp.n + split;
-    float* part = a.partial + unit * kRows * (D + 2);
+    float* part = a.partial + unit * R * (D + 2);
     for (int i = tid; i < t.n_rows * (D / 4); i += kThreads) {
         const int row = i / (D / 4), d = (i % (D / 4)) * 4;
-        const int slot = (d >> 2) ^ (((row & 1) << 2) | ((d >> 5) & 3));
+        const int slot = (d >> 2) ^ ((row >> 1) & 3);
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float4 v = *reinterpret_cast<const float4*>(all + (w * kRows + row) * D + 4 * slot);
+            const float4 v = *reinterpret_cast<const float4*>(all + (w * R + row) * D + 4 * slot);
             x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
         }
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * kRows + row]);
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * R + row]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float mw = part_m[w * kRows + row];
-            sum += mw == -INFINITY ? 0.0f : part_l[w * kRows + row] * exp2_ftz(mw - top);
+            const float mw = part_m[w * R + row];
+            sum += mw == -INFINITY ? 0.0f : part_l[w * R + row] * exp2_ftz(mw - top);
         }
         if (sp.n > 1) {
             *reinterpret_cast<float4*>(part + row * D + d) = x;
             if (d == 0) {
-                part[kRows * D + row] = top;
-                part[kRows * D + kRows + row] = sum;
+                part[R * D + row] = top;
+                part[R * D + R + row] = sum;
             }
         } else {
-            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-            const int rr = t.row0 + row;
-            T* out = static_cast<T*>(a.out) +
-                     (static_cast<size_t>(t.q0 + rr / G) * a.n_q_heads + t.h * G + rr % G) * D + d;
-            if (C::kPair) {
-                *reinterpret_cast<float4*>(out) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-            } else {
-                uint2 w;
-                w.x = pack_bf16_pair(x.x * inv, x.y * inv);
-                w.y = pack_bf16_pair(x.z * inv, x.w * inv);
-                *reinterpret_cast<uint2*>(out) = w;
-            }
+            store_row<T, D>(a, t, t.row0 + row, d, x, sum > 0.0f ? 1.0f / sum : 0.0f);
         }
     }
 }
 
 // Joins the splits of one row: out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m).
+// A thread block takes 64 channels of a row; its 16 groups of 16 lanes take
+// every 16th split.
+constexpr int kJoinGroups = 16, kJoinCols = 64;
 template <typename T, int D>
-__global__ void __launch_bounds__(D / 4) kv_attn_join(const KvAttnArgs a, const Split sp, const int n_tiles) {
-    const int tile = blockIdx.x / kRows, row = blockIdx.x % kRows, G = a.n_q_heads / a.n_kv_heads;
+__global__ void __launch_bounds__(kJoinGroups * kJoinCols / 4)
+kv_attn_join(const KvAttnArgs a, const Split sp, const int rows, const int n_tiles) {
+    const int part_of_row = blockIdx.x % (D / kJoinCols), r = blockIdx.x / (D / kJoinCols);
+    const int tile = r / rows, row = r % rows;
     Tile t;
-    if (!tile_of(a, tile, blockIdx.y, blockIdx.z, t) || row >= t.n_rows) return;
+    if (!tile_of(a, rows, tile, blockIdx.y, blockIdx.z, t) || row >= t.n_rows) return;
     const int span = t.keys.end - t.keys.first;
     const int n = max(1, min(sp.n, (span + sp.chunk - 1) / sp.chunk));
     const size_t unit = ((static_cast<size_t>(t.seq) * a.n_kv_heads + t.h) * n_tiles + tile) * sp.n;
-    const float* part = a.partial + unit * kRows * (D + 2);
-    constexpr size_t kNext = kRows * (D + 2);
-    float top = -INFINITY, sum = 0.0f;
+    const size_t next = static_cast<size_t>(rows) * (D + 2);
+    const float* part = a.partial + unit * next;
+    const float* at_m = part + rows * D + row;
+    const float* at_l = at_m + rows;
+    const int lane = threadIdx.x % (kJoinCols / 4), grp = threadIdx.x / (kJoinCols / 4);
+    const int d = part_of_row * kJoinCols + 4 * lane;
+    float top = -INFINITY;
+    for (int s = grp; s < n; s += kJoinGroups) top = fmaxf(top, at_m[s * next]);
+    __shared__ float sm[kJoinGroups], sl[kJoinGroups];
+    __shared__ float4 sx[kJoinGroups][kJoinCols / 4];
+    if (lane == 0) sm[grp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinGroups; ++w) top = fmaxf(top, sm[w]);
+    float sum = 0.0f;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < n; ++s) top = fmaxf(top, part[s * kNext + kRows * D + row]);
-    for (int s = 0; s < n; ++s) {
-        const float ms = part[s * kNext + kRows * D + row];
-        if (ms == -INFINITY) continue;
-        const float c = exp2_ftz(ms - top);
-        const float4 v = *reinterpret_cast<const float4*>(part + s * kNext + row * D + 4 * threadIdx.x);
-        sum += part[s * kNext + kRows * D + kRows + row] * c;
+#pragma unroll 4
+    for (int s = grp; s < n; s += kJoinGroups) {
+        const float ms = at_m[s * next], ls = at_l[s * next];
+        const float4 v = *reinterpret_cast<const float4*>(part + s * next + row * D + d);
+        const float c = ms == -INFINITY ? 0.0f : exp2_ftz(ms - top);
+        sum += ls * c;
         x.x += v.x * c; x.y += v.y * c; x.z += v.z * c; x.w += v.w * c;
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const int rr = t.row0 + row;
-    T* out = static_cast<T*>(a.out) + (static_cast<size_t>(t.q0 + rr / G) * a.n_q_heads + t.h * G + rr % G) * D +
-             4 * threadIdx.x;
-    if (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(out) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    } else {
-        uint2 w;
-        w.x = pack_bf16_pair(x.x * inv, x.y * inv);
-        w.y = pack_bf16_pair(x.z * inv, x.w * inv);
-        *reinterpret_cast<uint2*>(out) = w;
+    sx[grp][lane] = x;
+    if (lane == 0) sl[grp] = sum;
+    __syncthreads();
+    if (grp != 0) return;
+    for (int w = 1; w < kJoinGroups; ++w) {
+        const float4 v = sx[w][lane];
+        x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
+        sum += sl[w];
     }
+    store_row<T, D>(a, t, t.row0 + row, d, x, sum > 0.0f ? 1.0f / sum : 0.0f);
 }
 
-// How many ranges the keys are split into: enough thread blocks for a few
-// rounds over the 152 SMs, but no range below kMinChunk keys (a range's fixed
-// cost, its queries and its partial result, is about that of 100 keys).
-constexpr int kMinChunk = 256;
-constexpr long long kTargetBlocks = 152 * 8;
-Split split_of(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int window, long long max_kv_len) {
+// Rows of a thread block: the fewest tiles of 8 that hold a sequence's rows,
+// as far as the output's registers (D / 16 x 4 x NQ a lane, at most 128) allow.
+int tiles_of_8(int head_dim, long long rows) {
+    const int most = head_dim == 256 ? 2 : 4;
+    return rows <= 8 ? 1 : rows <= 16 || most == 2 ? 2 : 4;
+}
+
+// How many ranges the keys are split into: enough thread blocks for several
+// rounds over the SMs (ragged lengths even out), but no range below kMinChunk
+// keys (a range's fixed cost, its queries and its partial result, is about
+// that of 100 keys).
+constexpr int kMinChunk = 128;
+constexpr long long kTargetBlocks = 4096, kMostSplits = 228;
+Split split_of(int rows, int n_seq, int max_q, int n_q_heads, int n_kv_heads, int window, long long max_kv_len) {
     const int G = n_q_heads / n_kv_heads;
-    const long long tiles = (static_cast<long long>(max_q) * G + kRows - 1) / kRows;
+    const long long tiles = (static_cast<long long>(max_q) * G + rows - 1) / rows;
     const long long units = std::max(1LL, tiles * n_kv_heads * n_seq);
     long long span = std::max(1LL, max_kv_len);
     if (window) span = std::min(span, static_cast<long long>(window) + max_q + kStepKeys);
     long long n = std::min((kTargetBlocks + units - 1) / units, (span + kMinChunk - 1) / kMinChunk);
-    n = std::max(1LL, std::min(n, 512LL));
+    n = std::max(1LL, std::min(n, kMostSplits));
     long long chunk = (span + n - 1) / n;
     chunk = (chunk + kStepKeys - 1) / kStepKeys * kStepKeys;
     return Split{static_cast<int>((span + chunk - 1) / chunk), static_cast<int>(chunk)};
 }
 
-template <typename T, typename F, int D>
-cudaError_t attn_t(const KvAttnArgs& a, cudaStream_t st) {
-    using C = Cfg<T, D>;
+template <typename T, typename F, int D, int NQ>
+cudaError_t attn_nq(const KvAttnArgs& a, cudaStream_t st) {
+    using C = Cfg<T, D, NQ>;
     const int G = a.n_q_heads / a.n_kv_heads;
-    const Split sp = split_of(a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, a.window, a.max_kv_len);
-    const long long tiles = (static_cast<long long>(a.b.max_q) * G + kRows - 1) / kRows;
-    if (tiles * sp.n > 0x7fffffffLL / kRows) return cudaErrorInvalidConfiguration;
+    const Split sp = split_of(C::kRows, a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, a.window, a.max_kv_len);
+    const long long tiles = (static_cast<long long>(a.b.max_q) * G + C::kRows - 1) / C::kRows;
+    if (tiles * sp.n > 0x7fffffffLL / (C::kRows * (D / kJoinCols))) return cudaErrorInvalidConfiguration;
     static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = allow_smem(kv_attn_kernel<T, F, D>, C::kSmem, ready);
+    cudaError_t e = allow_smem(kv_attn_kernel<T, F, D, NQ>, C::kSmem, ready);
     if (e != cudaSuccess) return e;
     const int nt = static_cast<int>(tiles);
     e = timed_launch("kv_attn", st, [&] {
-        kv_attn_kernel<T, F, D><<<dim3(nt * sp.n, a.n_kv_heads, a.b.n_seq), kThreads, C::kSmem, st>>>(a, sp, nt);
+        kv_attn_kernel<T, F, D, NQ><<<dim3(nt * sp.n, a.n_kv_heads, a.b.n_seq), kThreads, C::kSmem, st>>>(a, sp, nt);
         return cudaGetLastError();
     });
     if (e != cudaSuccess || sp.n == 1) return e;
     return timed_launch("kv_attn_join", st, [&] {
-        kv_attn_join<T, D><<<dim3(nt * kRows, a.n_kv_heads, a.b.n_seq), D / 4, 0, st>>>(a, sp, nt);
+        kv_attn_join<T, D><<<dim3(nt * C::kRows * (D / kJoinCols), a.n_kv_heads, a.b.n_seq),
+                             kJoinGroups * kJoinCols / 4, 0, st>>>(a, sp, C::kRows, nt);
         return cudaGetLastError();
     });
+}
+
+template <typename T, typename F, int D>
+cudaError_t attn_t(const KvAttnArgs& a, cudaStream_t st) {
+    switch (tiles_of_8(D, static_cast<long long>(a.b.max_q) * (a.n_q_heads / a.n_kv_heads))) {
+        case 1: return attn_nq<T, F, D, 1>(a, st);
+        case 2: return attn_nq<T, F, D, 2>(a, st);
+        default: return attn_nq<T, F, D, D == 256 ? 2 : 4>(a, st);
+    }
 }
 
 }  // namespace
@@ -627,10 +716,12 @@ cudaError_t attn_t(const KvAttnArgs& a, cudaStream_t st) {
 size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window, bool,
                               int max_kv_len) {
     if (max_q == 0) return 0;
-    const Split sp = split_of(n_seq, max_q, n_q_heads, n_kv_heads, window, max_kv_len);
+    const long long all = static_cast<long long>(max_q) * (n_q_heads / n_kv_heads);
+    const int rows = 8 * tiles_of_8(head_dim, all);
+    const Split sp = split_of(rows, n_seq, max_q, n_q_heads, n_kv_heads, window, max_kv_len);
     if (sp.n == 1) return 0;
-    const size_t tiles = (static_cast<size_t>(max_q) * (n_q_heads / n_kv_heads) + kRows - 1) / kRows;
-    const size_t bytes = tiles * n_kv_heads * n_seq * sp.n * kRows * (head_dim + 2) * sizeof(float);
+    const size_t tiles = (all + rows - 1) / rows;
+    const size_t bytes = tiles * n_kv_heads * n_seq * sp.n * rows * (head_dim + 2) * sizeof(float);
     return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
