@@ -12,23 +12,27 @@
 // rescaled) only when a score exceeds it by 2^kLazy.
 // Queries become f16 after division by a power of two per row (bf16 has fewer
 // bits than f16, so that is exact down to 2^-24 of the row's largest).  Weights
-// become two bf16 terms, 16 bits: bf16's range holds the smallest of them (f16
-// would drop weights below 2^-24 of the largest, all that is left in a channel
-// where the heavy keys are zero), and one term's 2^-8 would be as large as the
-// output's own rounding.  With fp32 activations queries are f16 (hi, lo) pairs,
-// 22 bits, and weights three bf16 terms, 24 bits.
+// become f16, 11 bits, in a group of keys whose weights are all normal f16
+// numbers (2^-14 .. 2^15 with kBias, scores within 2^-21 of the reference);
+// else two bf16 terms, 16 bits: f16 would drop weights below 2^-24 of the
+// largest, all that is left in a channel where the heavy keys are zero, and one
+// bf16 term's 2^-8 would be as large as the output's own rounding.  The second
+// form costs a third more of the step's instructions.  With fp32 activations
+// queries are f16 (hi, lo) pairs, 22 bits, and weights three bf16 terms.
 //
 // One thread block takes 8, 16 or 32 rows and a range of keys.  Keys (and value
 // channels) are the tensor core's M, the rows its N, so that a group of 8 heads
 // fills the tile and a code is widened once for all rows:
 //   S^T [16 keys x rows] = K Q^T,   O^T [16 channels x rows] += V^T P^T
 // The accumulator of S^T holds a key's rows where the second product wants a
-// row's keys: one 8 x 8 transpose per 8 keys and term.  Each of the four warps
-// takes every fourth group of 16 keys on its own, with its own running state
-// and its own ring of asynchronous copies (no block-wide barrier until the
-// end): 16 keys lie in one page, so a group is one contiguous run of codes and
-// two scales.  A long axis is split over thread blocks and joined by
-// kv_attn_join.
+// row's keys: one 8 x 8 transpose per 8 keys and term.  V^T's operand comes by
+// the transposing 8-bit matrix load, which gives a lane four consecutive keys
+// of a channel; S^T's rows take the keys in the order that fits (0, 1, 4, 5, ..,
+// then 2, 3, 6, 7, ..).  Each of the four warps takes every fourth group of 16
+// keys on its own, with its own running state and its own ring of asynchronous
+// copies (no block-wide barrier until the end): 16 keys lie in one page, so a
+// group is one contiguous run of codes and two scales.  A long axis is split
+// over thread blocks and joined by kv_attn_join.
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
@@ -47,6 +51,8 @@ constexpr int kGroup = 16;        // keys of a warp's step
 constexpr int kStepKeys = kGroup * kWarps;
 constexpr int kSpan = 32;         // steps whose pages and scales are looked up at a time
 constexpr float kLazy = 8.0f;     // a reference lags behind the maximum by at most 2^8
+constexpr float kBias = 7.0f;     // weights are 2^7 times theirs: at most 2^15
+constexpr float kNormal = 21.0f;  // scores down to 2^-21 of the reference are normal f16 weights
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_ftz(float x) {
@@ -66,6 +72,14 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two 16 x 16 tiles of 8-bit codes, transposed: of tile c, f[2c] and f[2c + 1]
+// are four consecutive rows (4 (lane % 4) ..) of columns lane / 4 and that + 8.
+__device__ __forceinline__ void load_codes_t(uint32_t addr, uint32_t* f) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                 : "r"(addr)
+                 : "memory");
 }
 // Transposes an 8 x 8 tile of 16-bit values held two a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -106,49 +120,41 @@ template <> __device__ __forceinline__ void widen_f16<KvE4m3>(uint32_t w, uint32
         : "r"(w));
 }
 
-// Two codes of ab, (0, 1) or (2, 3), to bf16.
-template <int S> __device__ __forceinline__ uint32_t widen_int8_bf16(uint32_t ab) {
-    // Under the exponent of 128 the low seven bits of a code are the bf16
-    // 128 + (c & 127); the sign bit alone is 128, or 256 for a negative code; their difference is c
-    const uint32_t x = __byte_perm(ab, 0x43434343u, S == 0 ? 0x4140 : 0x4342);
-    const uint32_t lo = x & 0xFF7FFF7Fu, hi = x & 0xFF80FF80u;
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// The same to bf16.
+template <typename F> __device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t& a, uint32_t& b);
+template <> __device__ __forceinline__ void widen_bf16<KvInt8>(uint32_t w, uint32_t& a, uint32_t& b) {
+    // under the exponent of 128 the low seven bits of a code are the bf16 128 + (c & 127); the sign
+    // bit alone is 128, or 256 for a negative code; their difference is c
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = __byte_perm(w, 0x43434343u, i == 0 ? 0x4140 : 0x4342);
+        const uint32_t lo = x & 0xFF7FFF7Fu, hi = x & 0xFF80FF80u;
+        const __nv_bfloat162 r =
+            __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
+        (i == 0 ? a : b) = *reinterpret_cast<const uint32_t*>(&r);
+    }
 }
-template <int S> __device__ __forceinline__ uint32_t widen_e4m3_bf16(uint32_t ab) {
-    // sign, and exponent and fraction moved to their places: the value times 2^(7 - 127)
-    const uint32_t h = __byte_perm(ab, 0u, S == 0 ? 0x1404 : 0x3424);
-    const uint32_t x = ((h >> 4) & 0x07F007F0u) | (h & 0x80008000u);
+template <> __device__ __forceinline__ void widen_bf16<KvE4m3>(uint32_t w, uint32_t& a, uint32_t& b) {
+    // sign, and exponent and fraction moved to their places, are the value times 2^(7 - 127)
     const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7B80));  // 2^120
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), up);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Four codes of row a and four of row b: out[k] = (a_k, b_k).
-template <typename F> __device__ __forceinline__ void widen_pairs(uint32_t a, uint32_t b, uint32_t* out);
-template <> __device__ __forceinline__ void widen_pairs<KvInt8>(uint32_t a, uint32_t b, uint32_t* out) {
-    const uint32_t x = __byte_perm(a, b, 0x5140), y = __byte_perm(a, b, 0x7362);
-    out[0] = widen_int8_bf16<0>(x);
-    out[1] = widen_int8_bf16<1>(x);
-    out[2] = widen_int8_bf16<0>(y);
-    out[3] = widen_int8_bf16<1>(y);
-}
-template <> __device__ __forceinline__ void widen_pairs<KvE4m3>(uint32_t a, uint32_t b, uint32_t* out) {
-    const uint32_t x = __byte_perm(a, b, 0x5140), y = __byte_perm(a, b, 0x7362);
-    out[0] = widen_e4m3_bf16<0>(x);
-    out[1] = widen_e4m3_bf16<1>(x);
-    out[2] = widen_e4m3_bf16<0>(y);
-    out[3] = widen_e4m3_bf16<1>(y);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t h = __byte_perm(w, 0u, i == 0 ? 0x1404 : 0x3424);
+        const uint32_t x = ((h >> 4) & 0x07F007F0u) | (h & 0x80008000u);
+        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), up);
+        (i == 0 ? a : b) = *reinterpret_cast<const uint32_t*>(&r);
+    }
 }
 
 // Where 16-byte chunk c of row r lies in a group's tile: chunks are permuted so
-// that the 8 lanes that one shared-memory phase serves (K: two rows of four
-// chunks; V: four rows two apart, two chunks) touch different banks.
+// that what one shared-memory phase serves (K: two rows of four chunks; V: one
+// chunk of eight rows) lies in different banks.
 template <int D> __device__ __forceinline__ uint32_t k_at(uint32_t r, uint32_t c) {
     return r * D + ((D >= 128 ? c ^ ((r & 1) << 2) : c) << 4);
 }
 template <int D> __device__ __forceinline__ uint32_t v_at(uint32_t r, uint32_t c) {
-    if (D >= 128) return r * D + ((c ^ (((r >> 1) & 3) << 1)) << 4);
-    return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4);
+    if (D >= 128) return r * D + ((c ^ (r & 7)) << 4);
+    return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ ((r >> 1) & 3)) << 4);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
@@ -222,15 +228,16 @@ __device__ __forceinline__ void store_row(const KvAttnArgs& a, const Tile& t, in
 template <typename T, int D, int NQ> struct Cfg {
     static constexpr bool kPair = sizeof(T) == 4;     // fp32 activations: queries as pairs
     static constexpr int kTerms = kPair ? 3 : 2;      // bf16 terms of a weight
+    static constexpr int kJoinPitch = D + 4;          // floats of a row of the warps' results
     static constexpr int kRows = 8 * NQ;
     static constexpr int kTile = kGroup * D;          // one group's K (or V) codes
     static constexpr int kStages = D == 256 ? 2 : D == 128 ? 3 : 4;
     static constexpr int kQPitch = D + 16;            // f16 elements
     static constexpr int kRing = kWarps * kStages * 2 * kTile;
-    static constexpr int kJoin = kWarps * kRows * D * 4;  // the warps' results, after the ring's use
+    static constexpr int kJoin = kWarps * kRows * kJoinPitch * 4;  // the warps' results, after the ring's use
     static constexpr int kData = kRing > kJoin ? kRing : kJoin;
     static constexpr int kQ = kRows * kQPitch * 2 * (kPair ? 2 : 1);
-    static constexpr int kLook = kWarps * kSpan * 12;
+    static constexpr int kLook = kWarps * kSpan * 16;
     static constexpr int kSmem = kData + kQ + kLook + (kRows + 2 * kWarps * kRows) * 4;
     // thread blocks of an SM that the registers are planned for
     static constexpr int kBlocks = D * NQ <= 128 ? 4 : D * NQ <= 256 ? 3 : 2;
@@ -257,7 +264,8 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     __half* q_hi = reinterpret_cast<__half*>(smem + C::kData);
     int* look_page = reinterpret_cast<int*>(smem + C::kData + C::kQ) + warp * kSpan;
     float* look_k = reinterpret_cast<float*>(smem + C::kData + C::kQ) + (kWarps + warp) * kSpan;
-    float* look_v = reinterpret_cast<float*>(smem + C::kData + C::kQ) + (2 * kWarps + warp) * kSpan;
+    float* look_lv = reinterpret_cast<float*>(smem + C::kData + C::kQ) + (2 * kWarps + warp) * kSpan;
+    float* look_inv = reinterpret_cast<float*>(smem + C::kData + C::kQ) + (3 * kWarps + warp) * kSpan;
     float* q_scale = reinterpret_cast<float*>(smem + C::kData + C::kQ + C::kLook);
     float* part_m = q_scale + R;
     float* part_l = part_m + kWarps * R;
@@ -282,14 +290,17 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
 #pragma unroll
         for (int off = 4; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
         if (r >= R) continue;
-        const int ex = most > 0.0f && most <= 3.402823466e38f ? max(ilogbf(most), -100) : 0;
-        if (l8 == 0) q_scale[r] = scalbnf(a.scale * kLog2e, ex);
+        // the largest's exponent, and its powers of two
+        const int ex = most > 0.0f && most <= 3.402823466e38f
+                           ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126) : 0;
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        if (l8 == 0) q_scale[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int e = 0; e < N; e += 2) {
                 const int d = (v * 8 + l8) * N + e;
-                const float lo = scalbnf(x[v * N + e], -ex), hi = scalbnf(x[v * N + e + 1], -ex);
+                const float lo = x[v * N + e] * down, hi = x[v * N + e + 1] * down;
                 const uint32_t h = pack_f16(lo, hi);
                 *reinterpret_cast<uint32_t*>(q_hi + r * C::kQPitch + d) = h;
                 if (C::kPair) *reinterpret_cast<uint32_t*>(q_hi + (R + r) * C::kQPitch + d) = pack_f16_rest(h, lo, hi);
@@ -311,6 +322,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) qf[C::kPair ? 0 : s][n] = load_q(s, 0, n);
 
+    const int kr = 4 * (g >> 1) + (g & 1);  // this lane's keys of a group: kr, and kr + 2
     const int min_pos = t.start + t.row0 / G;
     const int max_lo = a.window ? t.start + (t.row0 + t.n_rows - 1) / G - a.window + 1 : 0;
     float o[MT][NQ][4];
@@ -354,13 +366,15 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                 }
             }
             // Values of a scale of 0 add nothing to the output but count in the sum: such a group
-            // is given the smallest scale in sight, negative as a mark, so that it does not lift m.
+            // is given the smallest scale in sight, so that it does not lift m, and a mark.
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
-            if (vs == 0.0f) vs = vs_low < INFINITY ? -vs_low : -1.0f;
+            const bool zero = vs == 0.0f;
+            if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
             look_page[lane] = page;
             look_k[lane] = ks;
-            look_v[lane] = vs;
+            look_lv[lane] = log2f(vs);
+            look_inv[lane] = (zero ? -1.0f : 1.0f) / vs;
         }
         __syncwarp();
         auto fetch = [&](int i) {
@@ -413,7 +427,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                 for (int n = 0; n < NQ; ++n) s[c][n][0] = s[c][n][1] = s[c][n][2] = s[c][n][3] = 0.0f;
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
-                const uint4 w0 = lds128(kt + k_at<D>(g, 4 * j + t4)), w1 = lds128(kt + k_at<D>(g + 8, 4 * j + t4));
+                const uint4 w0 = lds128(kt + k_at<D>(kr, 4 * j + t4)), w1 = lds128(kt + k_at<D>(kr + 2, 4 * j + t4));
                 const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -433,7 +447,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                     }
                 }
             }
-            const float ks = look_k[i], vs = fabsf(look_v[i]), lv = log2f(vs);
+            const float ks = look_k[i], lv = look_lv[i], mark = look_inv[i], inv = fabsf(mark);
             const bool whole = key + kGroup - 1 <= min_pos && key >= max_lo && key + kGroup <= end;
             bool lift = false;
             float top[NQ][2];
@@ -449,7 +463,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                         if (CH > 1) x += s[CH - 1][n][2 * k + c];
                         v[k] = fmaf(x, f, lv);
                         if (!whole) {
-                            const int j = key + g + 8 * k, pos = t.start + (t.row0 + 8 * n + 2 * t4 + c) / G;
+                            const int j = key + kr + 2 * k, pos = t.start + (t.row0 + 8 * n + 2 * t4 + c) / G;
                             if (j > pos || j >= end || (a.window && j <= pos - a.window)) v[k] = -INFINITY;
                         }
                         s[0][n][2 * k + c] = v[k];
@@ -476,65 +490,71 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                         }
                     }
             }
-            uint2 p[C::kTerms][NQ];  // weights as bf16 terms
-            const float inv = 1.0f / vs;
+            float w[NQ][4];
+            bool small = false;
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                float w[4];
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float ref = m[n][c] == -INFINITY ? 0.0f : m[n][c];
-                    w[c] = exp2_ftz(s[0][n][c] - ref);
-                    w[2 + c] = exp2_ftz(s[0][n][2 + c] - ref);
-                    l[n][c] = fmaf(w[c] + w[2 + c], inv, l[n][c]);
+                    const float ref = m[n][c] == -INFINITY ? 0.0f : m[n][c] - kBias;
+                    small |= fminf(s[0][n][c], s[0][n][2 + c]) < ref + (kBias - kNormal);
+                    w[n][c] = exp2_ftz(s[0][n][c] - ref);
+                    w[n][2 + c] = exp2_ftz(s[0][n][2 + c] - ref);
+                    l[n][c] = fmaf(w[n][c] + w[n][2 + c], inv, l[n][c]);
                 }
+            if (mark < 0.0f) continue;
+            // output: 16-channel tile i holds channel 16 i + g in its first eight rows, + 8 in the others
+            const uint32_t vrow = lane & 15, vchunk = lane >> 4;
+            if (!C::kPair && !__any_sync(0xffffffffu, small)) {
+                uint2 p[NQ];
 #pragma unroll
-                for (int k = 0; k < C::kTerms; ++k) {
-                    const uint32_t u = pack_bf16_pair(w[0], w[1]), v = pack_bf16_pair(w[2], w[3]);
-                    w[0] -= bf16_low(u);
-                    w[1] -= bf16_high(u);
-                    w[2] -= bf16_low(v);
-                    w[3] -= bf16_high(v);
-                    p[k][n] = make_uint2(transpose8(u), transpose8(v));
-                }
-            }
-            if (look_v[i] < 0.0f) continue;
-            // output: a lane's run of 16 channels (D = 64: 8), 128 jj + 16 g + e; 16-channel tile
-            // (jj, e / 2) holds e in its first eight rows and e + 1 in the others
+                for (int n = 0; n < NQ; ++n)
+                    p[n] = make_uint2(transpose8(pack_f16(w[n][0], w[n][1])), transpose8(pack_f16(w[n][2], w[n][3])));
 #pragma unroll
-            for (int jj = 0; jj < (D >= 128 ? D / 128 : 1); ++jj) {
-                constexpr int W = D >= 128 ? 4 : 2;  // words of a lane's run of channels
-                uint32_t x[4][W];
+                for (int i2 = 0; i2 < MT; i2 += 2) {
+                    uint32_t x[4], f[2][4];
+                    load_codes_t(vt + v_at<D>(vrow, i2 + vchunk), x);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t row = 2 * t4 + (r & 1) + 8 * (r >> 1);
-                    if (D >= 128) {
-                        const uint4 v = lds128(vt + v_at<D>(row, 8 * jj + g));
-                        x[r][0] = v.x; x[r][1] = v.y; x[r][W - 2] = v.z; x[r][W - 1] = v.w;
-                    } else {
-                        const uint2 v = lds64(vt + v_at<D>(row, g >> 1) + (g & 1) * 8);
-                        x[r][0] = v.x; x[r][1] = v.y;
+                    for (int k = 0; k < 2; ++k) {
+                        widen_f16<F>(x[2 * k], f[k][0], f[k][2]);
+                        widen_f16<F>(x[2 * k + 1], f[k][1], f[k][3]);
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) mma_f16(o[i2 + k][n], f[k], p[n].x, p[n].y);
                     }
                 }
+            } else {
+                uint2 p[C::kTerms][NQ];
 #pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    uint32_t lo[4], hi[4];
-                    widen_pairs<F>(x[0][e], x[1][e], lo);
-                    widen_pairs<F>(x[2][e], x[3][e], hi);
-                    const uint32_t f0[4] = {lo[0], lo[1], hi[0], hi[1]}, f1[4] = {lo[2], lo[3], hi[2], hi[3]};
+                for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int k = C::kTerms - 1; k >= 0; --k)
+                    for (int k = 0; k < C::kTerms; ++k) {
+                        const uint32_t u = pack_bf16_pair(w[n][0], w[n][1]), v = pack_bf16_pair(w[n][2], w[n][3]);
+                        w[n][0] -= bf16_low(u);
+                        w[n][1] -= bf16_high(u);
+                        w[n][2] -= bf16_low(v);
+                        w[n][3] -= bf16_high(v);
+                        p[k][n] = make_uint2(transpose8(u), transpose8(v));
+                    }
 #pragma unroll
-                        for (int n = 0; n < NQ; ++n) {
-                            mma_bf16(o[jj * 8 + 2 * e][n], f0, p[k][n].x, p[k][n].y);
-                            mma_bf16(o[jj * 8 + 2 * e + 1][n], f1, p[k][n].x, p[k][n].y);
-                        }
+                for (int i2 = 0; i2 < MT; i2 += 2) {
+                    uint32_t x[4], f[2][4];
+                    load_codes_t(vt + v_at<D>(vrow, i2 + vchunk), x);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        widen_bf16<F>(x[2 * k], f[k][0], f[k][2]);
+                        widen_bf16<F>(x[2 * k + 1], f[k][1], f[k][3]);
+#pragma unroll
+                        for (int e = C::kTerms - 1; e >= 0; --e)
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n) mma_bf16(o[i2 + k][n], f[k], p[e][n].x, p[e][n].y);
+                    }
                 }
             }
         }
         cp_wait<0>();
     }
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Join the four warps: rows' references and sums, then the scaled outputs through shared memory.
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -548,8 +568,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             }
         }
     __syncthreads();
-    float* all = reinterpret_cast<float*>(smem);  // [warp][row][D], float4 slots permuted (bank conflicts)
-    constexpr int RUN = D >= 128 ? 16 : 8;
+    float* all = reinterpret_cast<float*>(smem);  // [warp][row][kJoinPitch]
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -559,28 +578,22 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * R + row]);
             const float f = m[n][c] == -INFINITY ? 0.0f : exp2_ftz(m[n][c] - top);
-            float* dst = all + (warp * R + row) * D;
+            float* dst = all + (warp * R + row) * C::kJoinPitch + g;
 #pragma unroll
-            for (int jj = 0; jj < (D >= 128 ? D / 128 : 1); ++jj)
-#pragma unroll
-                for (int e = 0; e < RUN; e += 4) {
-                    const int slot = ((128 * jj + RUN * g + e) >> 2) ^ ((row >> 1) & 3);
-                    const auto& u = o[jj * 8 + e / 2][n];
-                    const auto& v = o[jj * 8 + e / 2 + 1][n];
-                    *reinterpret_cast<float4*>(dst + 4 * slot) =
-                        make_float4(u[c] * f, u[2 + c] * f, v[c] * f, v[2 + c] * f);
-                }
+            for (int i = 0; i < MT; ++i) {
+                dst[16 * i] = o[i][n][c] * f;
+                dst[16 * i + 8] = o[i][n][2 + c] * f;
+            }
         }
     __syncthreads();
     const size_t unit = ((static_cast<size_t>(t.seq) * a.n_kv_heads + t.h) * n_tiles + tile) * sp.n + split;
     float* part = a.partial + unit * R * (D + 2);
     for (int i = tid; i < t.n_rows * (D / 4); i += kThreads) {
         const int row = i / (D / 4), d = (i % (D / 4)) * 4;
-        const int slot = (d >> 2) ^ ((row >> 1) & 3);
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float4 v = *reinterpret_cast<const float4*>(all + (w * R + row) * D + 4 * slot);
+            const float4 v = *reinterpret_cast<const float4*>(all + (w * R + row) * C::kJoinPitch + d);
             x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
         }
         float top = -INFINITY, sum = 0.0f;
@@ -603,17 +616,24 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     }
 }
 
-// Joins the splits of one row: out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m).
-// A thread block takes 64 channels of a row; its 16 groups of 16 lanes take
-// every 16th split.
-constexpr int kJoinGroups = 16, kJoinCols = 64;
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinGroups * kJoinCols / 4)
+// Joins the splits of a row: out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m).
+// 16 lanes take 64 channels of a row; GROUPS such groups of a thread block share
+// one row's splits (few rows, many splits), or take a row each (GROUPS 1).
+// Launched as the main kernel's programmatic dependent: it waits for that
+// kernel's results before it reads any.
+constexpr int kJoinThreads = 256, kJoinLanes = 16, kJoinCols = 4 * kJoinLanes;
+template <typename T, int D, int GROUPS>
+__global__ void __launch_bounds__(kJoinThreads)
 kv_attn_join(const KvAttnArgs a, const Split sp, const int rows, const int n_tiles) {
-    const int part_of_row = blockIdx.x % (D / kJoinCols), r = blockIdx.x / (D / kJoinCols);
-    const int tile = r / rows, row = r % rows;
+    constexpr int kUnits = kJoinThreads / kJoinLanes / GROUPS;  // (row, 64 channels) of a thread block
+    const int lane = threadIdx.x % kJoinLanes, grp = threadIdx.x / kJoinLanes % GROUPS;
+    const int at = blockIdx.x * kUnits + threadIdx.x / (kJoinLanes * GROUPS);
+    const int r = at / (D / kJoinCols), tile = r / rows, row = r % rows;
     Tile t;
-    if (!tile_of(a, rows, tile, blockIdx.y, blockIdx.z, t) || row >= t.n_rows) return;
+    const bool mine = tile < n_tiles && tile_of(a, rows, tile, blockIdx.y, blockIdx.z, t) && row < t.n_rows;
+    if (GROUPS > 1 && !mine) return;  // all of the thread block
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (GROUPS == 1 && !mine) return;
     const int span = t.keys.end - t.keys.first;
     const int n = max(1, min(sp.n, (span + sp.chunk - 1) / sp.chunk));
     const size_t unit = ((static_cast<size_t>(t.seq) * a.n_kv_heads + t.h) * n_tiles + tile) * sp.n;
@@ -621,36 +641,55 @@ kv_attn_join(const KvAttnArgs a, const Split sp, const int rows, const int n_til
     const float* part = a.partial + unit * next;
     const float* at_m = part + rows * D + row;
     const float* at_l = at_m + rows;
-    const int lane = threadIdx.x % (kJoinCols / 4), grp = threadIdx.x / (kJoinCols / 4);
-    const int d = part_of_row * kJoinCols + 4 * lane;
+    const int d = at % (D / kJoinCols) * kJoinCols + 4 * lane;
     float top = -INFINITY;
-    for (int s = grp; s < n; s += kJoinGroups) top = fmaxf(top, at_m[s * next]);
-    __shared__ float sm[kJoinGroups], sl[kJoinGroups];
-    __shared__ float4 sx[kJoinGroups][kJoinCols / 4];
-    if (lane == 0) sm[grp] = top;
-    __syncthreads();
+#pragma unroll 4
+    for (int s = grp; s < n; s += GROUPS) top = fmaxf(top, at_m[s * next]);
+    __shared__ float sm[GROUPS], sl[GROUPS];
+    __shared__ float4 sx[GROUPS][kJoinLanes];
+    if (GROUPS > 1) {
+        if (lane == 0) sm[grp] = top;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kJoinGroups; ++w) top = fmaxf(top, sm[w]);
+        for (int w = 0; w < GROUPS; ++w) top = fmaxf(top, sm[w]);
+    }
     float sum = 0.0f;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int s = grp; s < n; s += kJoinGroups) {
+    for (int s = grp; s < n; s += GROUPS) {
         const float ms = at_m[s * next], ls = at_l[s * next];
         const float4 v = *reinterpret_cast<const float4*>(part + s * next + row * D + d);
         const float c = ms == -INFINITY ? 0.0f : exp2_ftz(ms - top);
         sum += ls * c;
         x.x += v.x * c; x.y += v.y * c; x.z += v.z * c; x.w += v.w * c;
     }
-    sx[grp][lane] = x;
-    if (lane == 0) sl[grp] = sum;
-    __syncthreads();
-    if (grp != 0) return;
-    for (int w = 1; w < kJoinGroups; ++w) {
-        const float4 v = sx[w][lane];
-        x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
-        sum += sl[w];
+    if (GROUPS > 1) {
+        sx[grp][lane] = x;
+        if (lane == 0) sl[grp] = sum;
+        __syncthreads();
+        if (grp != 0) return;
+        for (int w = 1; w < GROUPS; ++w) {
+            const float4 v = sx[w][lane];
+            x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
+            sum += sl[w];
+        }
     }
     store_row<T, D>(a, t, t.row0 + row, d, x, sum > 0.0f ? 1.0f / sum : 0.0f);
+}
+
+template <typename T, int D, int GROUPS>
+cudaError_t join_t(const KvAttnArgs& a, const Split sp, int rows, int n_tiles, cudaStream_t st) {
+    constexpr int kUnits = kJoinThreads / kJoinLanes / GROUPS;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((n_tiles * rows * (D / kJoinCols) + kUnits - 1) / kUnits, a.n_kv_heads, a.b.n_seq);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_attn_join<T, D, GROUPS>, a, sp, rows, n_tiles);
 }
 
 // Rows of a thread block: the fewest tiles of 8 that hold a sequence's rows,
@@ -695,10 +734,9 @@ cudaError_t attn_nq(const KvAttnArgs& a, cudaStream_t st) {
         return cudaGetLastError();
     });
     if (e != cudaSuccess || sp.n == 1) return e;
+    // up to 8 splits are one lane's few loads in flight
     return timed_launch("kv_attn_join", st, [&] {
-        kv_attn_join<T, D><<<dim3(nt * C::kRows * (D / kJoinCols), a.n_kv_heads, a.b.n_seq),
-                             kJoinGroups * kJoinCols / 4, 0, st>>>(a, sp, C::kRows, nt);
-        return cudaGetLastError();
+        return sp.n <= 8 ? join_t<T, D, 1>(a, sp, C::kRows, nt, st) : join_t<T, D, 16>(a, sp, C::kRows, nt, st);
     });
 }
 
