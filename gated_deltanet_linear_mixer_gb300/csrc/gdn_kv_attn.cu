@@ -270,6 +270,80 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     float* part_m = q_scale + R;
     float* part_l = part_m + kWarps * R;
 
+    // This warp's groups of a span: pages (one a lane), then the first copies, then the scales, so
+    // that the codes of the first groups are on their way before anything else is waited for.
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * 2 * C::kTile;
+    const int n_steps = begin < end ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
+    const int min_pos = t.start + t.row0 / G;
+    int steps = 0, key0 = 0;
+    float vs_low = INFINITY;
+    auto fetch = [&](int i) {
+        if (i < steps) {
+            const int key = key0 + i * kStepKeys, page = look_page[i];
+            const size_t at = page < 0 ? 0 : ((static_cast<size_t>(page) * a.n_kv_heads + t.h) * a.page_size +
+                                              key % a.page_size) * D;
+            const uint32_t slot = ring + (i % S) * 2 * C::kTile;
+            const uint8_t *ksrc = a.c.k + at + lane * 16, *vsrc = a.c.v + at + lane * 16;
+            if (page >= 0 && key + kGroup <= end) {
+#pragma unroll
+                for (int c = 0; c < C::kTile / 16; c += 32) {
+                    const uint32_t r = (c + lane) / (D / 16), cc = lane % (D / 16);
+                    cp_async16(slot + k_at<D>(r, cc), ksrc + c * 16, true);
+                    cp_async16(slot + C::kTile + v_at<D>(r, cc), vsrc + c * 16, true);
+                }
+            } else {  // rows past the end become zeros: what lies there may be no number
+#pragma unroll
+                for (int c = 0; c < C::kTile / 16; c += 32) {
+                    const uint32_t r = (c + lane) / (D / 16), cc = lane % (D / 16);
+                    const bool take = page >= 0 && key + static_cast<int>(r) < end;
+                    cp_async16(slot + k_at<D>(r, cc), take ? ksrc + c * 16 : a.c.k, take);
+                    cp_async16(slot + C::kTile + v_at<D>(r, cc), take ? vsrc + c * 16 : a.c.v, take);
+                }
+            }
+        }
+        cp_commit();
+    };
+    auto open_span = [&](int span) {
+        steps = min(kSpan, n_steps - span);
+        key0 = begin + span * kStepKeys + warp * kGroup;
+        const int key = key0 + lane * kStepKeys;
+        int page = -1;
+        if (lane < steps && key < end) {
+            page = a.b.table[static_cast<size_t>(t.seq) * a.b.pages_per_seq + key / a.page_size];
+            if (page < 0 || page >= a.c.n_pages) {
+                // needed unless every row's window has left it behind
+                if (!a.window || key + kGroup - 1 > min_pos - a.window) atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
+                page = -1;
+            }
+        }
+        __syncwarp();
+        look_page[lane] = page;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) fetch(i);
+    };
+    auto look_scales = [&]() {
+        const int page = look_page[lane];
+        float ks = 0.0f, vs = 1.0f;
+        if (page >= 0) {
+            const size_t block = static_cast<size_t>(page) * a.n_kv_heads + t.h;
+            ks = a.c.k_scale[block];
+            vs = a.c.v_scale[block];
+            if (vs > 0.0f) vs_low = fminf(vs_low, vs);
+        }
+        // Values of a scale of 0 add nothing to the output but count in the sum: such a group
+        // is given the smallest scale in sight, so that it does not lift m, and a mark.
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
+        const bool zero = vs == 0.0f;
+        if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
+        look_k[lane] = ks;
+        look_lv[lane] = log2f(vs);
+        look_inv[lane] = (zero ? -1.0f : 1.0f) / vs;
+        __syncwarp();
+    };
+    if (n_steps > 0) open_span(0);
+
     // Queries: 8 lanes a row, rounded to f16 under a power of two of the row.
     for (int r = tid >> 3; r < (R + 15) / 16 * 16; r += kThreads / 8) {
         constexpr int N = Vec16<T>::N, V = D / (8 * N);
@@ -323,14 +397,14 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             for (int n = 0; n < NQ; ++n) qf[C::kPair ? 0 : s][n] = load_q(s, 0, n);
 
     const int kr = 4 * (g >> 1) + (g & 1);  // this lane's keys of a group: kr, and kr + 2
-    const int min_pos = t.start + t.row0 / G;
     const int max_lo = a.window ? t.start + (t.row0 + t.n_rows - 1) / G - a.window + 1 : 0;
     float o[MT][NQ][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int n = 0; n < NQ; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
-    float qs[NQ][2], m[NQ][2], l[NQ][2], vs_low = INFINITY;
+    float qs[NQ][2], m[NQ][2], l[NQ][2];
+    bool fresh = true;  // nothing was added to o and l yet
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -340,71 +414,9 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             l[n][c] = 0.0f;
         }
 
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * 2 * C::kTile;
-    const int n_steps = begin < end ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
     for (int span = 0; span < n_steps; span += kSpan) {
-        const int steps = min(kSpan, n_steps - span);
-        const int key0 = begin + span * kStepKeys + warp * kGroup;
-        // pages and scales of this warp's groups, one a lane
-        __syncwarp();
-        {
-            const int key = key0 + lane * kStepKeys;
-            int page = -1;
-            float ks = 0.0f, vs = 1.0f;
-            if (lane < steps && key < end) {
-                page = a.b.table[static_cast<size_t>(t.seq) * a.b.pages_per_seq + key / a.page_size];
-                if (page < 0 || page >= a.c.n_pages) {
-                    // needed unless every row's window has left it behind
-                    if (!a.window || key + kGroup - 1 > min_pos - a.window)
-                        atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
-                    page = -1;
-                } else {
-                    const size_t block = static_cast<size_t>(page) * a.n_kv_heads + t.h;
-                    ks = a.c.k_scale[block];
-                    vs = a.c.v_scale[block];
-                    if (vs > 0.0f) vs_low = fminf(vs_low, vs);
-                }
-            }
-            // Values of a scale of 0 add nothing to the output but count in the sum: such a group
-            // is given the smallest scale in sight, so that it does not lift m, and a mark.
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
-            const bool zero = vs == 0.0f;
-            if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
-            look_page[lane] = page;
-            look_k[lane] = ks;
-            look_lv[lane] = log2f(vs);
-            look_inv[lane] = (zero ? -1.0f : 1.0f) / vs;
-        }
-        __syncwarp();
-        auto fetch = [&](int i) {
-            if (i < steps) {
-                const int key = key0 + i * kStepKeys, page = look_page[i];
-                const size_t at = page < 0 ? 0 : ((static_cast<size_t>(page) * a.n_kv_heads + t.h) * a.page_size +
-                                                  key % a.page_size) * D;
-                const uint32_t slot = ring + (i % S) * 2 * C::kTile;
-                const uint8_t *ksrc = a.c.k + at + lane * 16, *vsrc = a.c.v + at + lane * 16;
-                if (page >= 0 && key + kGroup <= end) {
-#pragma unroll
-                    for (int c = 0; c < C::kTile / 16; c += 32) {
-                        const uint32_t r = (c + lane) / (D / 16), cc = lane % (D / 16);
-                        cp_async16(slot + k_at<D>(r, cc), ksrc + c * 16, true);
-                        cp_async16(slot + C::kTile + v_at<D>(r, cc), vsrc + c * 16, true);
-                    }
-                } else {  // rows past the end become zeros: what lies there may be no number
-#pragma unroll
-                    for (int c = 0; c < C::kTile / 16; c += 32) {
-                        const uint32_t r = (c + lane) / (D / 16), cc = lane % (D / 16);
-                        const bool take = page >= 0 && key + static_cast<int>(r) < end;
-                        cp_async16(slot + k_at<D>(r, cc), take ? ksrc + c * 16 : a.c.k, take);
-                        cp_async16(slot + C::kTile + v_at<D>(r, cc), take ? vsrc + c * 16 : a.c.v, take);
-                    }
-                }
-            }
-            cp_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) fetch(i);
+        if (span > 0) open_span(span);
+        look_scales();
         for (int i = 0; i < steps; ++i) {
             if (S > 2) {  // the slot fetched into was read in the step before
                 cp_wait<S - 2>();
@@ -482,6 +494,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                         mn = fmaxf(m[n][c], mn);
                         const float f = m[n][c] == -INFINITY ? 0.0f : exp2_ftz(m[n][c] - mn);
                         m[n][c] = mn;
+                        if (fresh) continue;
                         l[n][c] *= f;
 #pragma unroll
                         for (int i2 = 0; i2 < MT; ++i2) {
@@ -489,6 +502,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                             o[i2][n][2 + c] *= f;
                         }
                     }
+                fresh = false;
             }
             float w[NQ][4];
             bool small = false;
@@ -617,72 +631,83 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
 }
 
 // Joins the splits of a row: out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m).
-// 16 lanes take 64 channels of a row; GROUPS such groups of a thread block share
-// one row's splits (few rows, many splits), or take a row each (GROUPS 1).
-// Launched as the main kernel's programmatic dependent: it waits for that
-// kernel's results before it reads any.
-constexpr int kJoinThreads = 256, kJoinLanes = 16, kJoinCols = 4 * kJoinLanes;
+// 16 lanes take 64 channels of a row; GROUPS such groups share one row's splits,
+// at most kJoinEach each, all loaded before any is used.  Launched as the main
+// kernel's programmatic dependent: it waits for that kernel's results before it
+// reads any.
+constexpr int kJoinLanes = 16, kJoinCols = 4 * kJoinLanes, kJoinEach = 8;
+template <int GROUPS> constexpr int kJoinThreads = GROUPS * kJoinLanes < 256 ? 256 : GROUPS * kJoinLanes;
 template <typename T, int D, int GROUPS>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads<GROUPS>)
 kv_attn_join(const KvAttnArgs a, const Split sp, const int rows, const int n_tiles) {
-    constexpr int kUnits = kJoinThreads / kJoinLanes / GROUPS;  // (row, 64 channels) of a thread block
+    constexpr int kUnits = kJoinThreads<GROUPS> / (kJoinLanes * GROUPS);  // (row, 64 channels) of a thread block
     const int lane = threadIdx.x % kJoinLanes, grp = threadIdx.x / kJoinLanes % GROUPS;
-    const int at = blockIdx.x * kUnits + threadIdx.x / (kJoinLanes * GROUPS);
+    const int here = threadIdx.x / (kJoinLanes * GROUPS), at = blockIdx.x * kUnits + here;
     const int r = at / (D / kJoinCols), tile = r / rows, row = r % rows;
     Tile t;
     const bool mine = tile < n_tiles && tile_of(a, rows, tile, blockIdx.y, blockIdx.z, t) && row < t.n_rows;
-    if (GROUPS > 1 && !mine) return;  // all of the thread block
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (GROUPS == 1 && !mine) return;
-    const int span = t.keys.end - t.keys.first;
-    const int n = max(1, min(sp.n, (span + sp.chunk - 1) / sp.chunk));
-    const size_t unit = ((static_cast<size_t>(t.seq) * a.n_kv_heads + t.h) * n_tiles + tile) * sp.n;
+    const int span = mine ? t.keys.end - t.keys.first : 0;
+    const int n = mine ? max(1, min(sp.n, (span + sp.chunk - 1) / sp.chunk)) : 0;
+    const size_t unit = mine ? ((static_cast<size_t>(t.seq) * a.n_kv_heads + t.h) * n_tiles + tile) * sp.n : 0;
     const size_t next = static_cast<size_t>(rows) * (D + 2);
     const float* part = a.partial + unit * next;
-    const float* at_m = part + rows * D + row;
-    const float* at_l = at_m + rows;
     const int d = at % (D / kJoinCols) * kJoinCols + 4 * lane;
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int s = grp; s < n; s += GROUPS) top = fmaxf(top, at_m[s * next]);
-    __shared__ float sm[GROUPS], sl[GROUPS];
-    __shared__ float4 sx[GROUPS][kJoinLanes];
-    if (GROUPS > 1) {
-        if (lane == 0) sm[grp] = top;
-        __syncthreads();
+    float ms[kJoinEach], ls[kJoinEach], top = -INFINITY;
+    float4 vs[kJoinEach];
 #pragma unroll
-        for (int w = 0; w < GROUPS; ++w) top = fmaxf(top, sm[w]);
-    }
-    float sum = 0.0f;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int s = grp; s < n; s += GROUPS) {
-        const float ms = at_m[s * next], ls = at_l[s * next];
-        const float4 v = *reinterpret_cast<const float4*>(part + s * next + row * D + d);
-        const float c = ms == -INFINITY ? 0.0f : exp2_ftz(ms - top);
-        sum += ls * c;
-        x.x += v.x * c; x.y += v.y * c; x.z += v.z * c; x.w += v.w * c;
-    }
-    if (GROUPS > 1) {
-        sx[grp][lane] = x;
-        if (lane == 0) sl[grp] = sum;
-        __syncthreads();
-        if (grp != 0) return;
-        for (int w = 1; w < GROUPS; ++w) {
-            const float4 v = sx[w][lane];
-            x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
-            sum += sl[w];
+    for (int k = 0; k < kJoinEach; ++k) {
+        const int s = grp + GROUPS * k;
+        ms[k] = -INFINITY;
+        ls[k] = 0.0f;
+        vs[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (s < n) {
+            ms[k] = part[s * next + rows * D + row];
+            ls[k] = part[s * next + rows * D + rows + row];
+            vs[k] = *reinterpret_cast<const float4*>(part + s * next + row * D + d);
         }
     }
-    store_row<T, D>(a, t, t.row0 + row, d, x, sum > 0.0f ? 1.0f / sum : 0.0f);
+#pragma unroll
+    for (int k = 0; k < kJoinEach; ++k) top = fmaxf(top, ms[k]);
+    float sum = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kJoinEach; ++k) {
+        const float c = ms[k] == -INFINITY ? 0.0f : exp2_ftz(ms[k] - top);
+        sum += ls[k] * c;
+        x.x += vs[k].x * c; x.y += vs[k].y * c; x.z += vs[k].z * c; x.w += vs[k].w * c;
+    }
+    if (GROUPS > 1) {
+        __shared__ float sm[kUnits][GROUPS], sl[kUnits][GROUPS];
+        __shared__ float4 sx[kUnits][GROUPS][kJoinLanes];
+        sx[here][grp][lane] = x;
+        if (lane == 0) {
+            sm[here][grp] = top;
+            sl[here][grp] = sum;
+        }
+        __syncthreads();
+        if (grp != 0) return;
+#pragma unroll
+        for (int w = 0; w < GROUPS; ++w) top = fmaxf(top, sm[here][w]);
+        sum = 0.0f;
+        x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int w = 0; w < GROUPS; ++w) {
+            const float c = sm[here][w] == -INFINITY ? 0.0f : exp2_ftz(sm[here][w] - top);
+            const float4 v = sx[here][w][lane];
+            sum += sl[here][w] * c;
+            x.x += v.x * c; x.y += v.y * c; x.z += v.z * c; x.w += v.w * c;
+        }
+    }
+    if (mine) store_row<T, D>(a, t, t.row0 + row, d, x, sum > 0.0f ? 1.0f / sum : 0.0f);
 }
 
 template <typename T, int D, int GROUPS>
 cudaError_t join_t(const KvAttnArgs& a, const Split sp, int rows, int n_tiles, cudaStream_t st) {
-    constexpr int kUnits = kJoinThreads / kJoinLanes / GROUPS;
+    constexpr int kUnits = kJoinThreads<GROUPS> / (kJoinLanes * GROUPS);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((n_tiles * rows * (D / kJoinCols) + kUnits - 1) / kUnits, a.n_kv_heads, a.b.n_seq);
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.blockDim = dim3(kJoinThreads<GROUPS>);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -699,12 +724,17 @@ int tiles_of_8(int head_dim, long long rows) {
     return rows <= 8 ? 1 : rows <= 16 || most == 2 ? 2 : 4;
 }
 
-// How many ranges the keys are split into: enough thread blocks for several
-// rounds over the SMs (ragged lengths even out), but no range below kMinChunk
-// keys (a range's fixed cost, its queries and its partial result, is about
-// that of 100 keys).
-constexpr int kMinChunk = 128;
-constexpr long long kTargetBlocks = 4096, kMostSplits = 228;
+// How many ranges the keys are split into.  Several rounds of thread blocks over
+// the SMs' 456 places even out ragged lengths, but a range's fixed cost (its
+// queries, its partial result) counts from about 16 thread blocks an SM on: 256
+// sequences of 127..8191 keys, head_dim 256, take 224 / 196 / 193 / 195 us at
+// 1024 / 2048 / 3072 / 4096 blocks, 64 x 4 drafts of head_dim 128 118 / 107 / 114
+// / 118 us.  One sequence is split down to one step a warp (1000 keys: 7.3 us;
+// 9.3 us at 128 keys a range), 131,000 keys into half a round (31 us; 36 us at 76
+// ranges).
+constexpr int kMinChunk = kStepKeys;
+constexpr long long kTargetBlocks = 152 * 16, kMostSplits = 228;
+static_assert(kMostSplits <= 32 * kJoinEach, "the join holds this many splits");
 Split split_of(int rows, int n_seq, int max_q, int n_q_heads, int n_kv_heads, int window, long long max_kv_len) {
     const int G = n_q_heads / n_kv_heads;
     const long long tiles = (static_cast<long long>(max_q) * G + rows - 1) / rows;
@@ -734,9 +764,10 @@ cudaError_t attn_nq(const KvAttnArgs& a, cudaStream_t st) {
         return cudaGetLastError();
     });
     if (e != cudaSuccess || sp.n == 1) return e;
-    // up to 8 splits are one lane's few loads in flight
     return timed_launch("kv_attn_join", st, [&] {
-        return sp.n <= 8 ? join_t<T, D, 1>(a, sp, C::kRows, nt, st) : join_t<T, D, 16>(a, sp, C::kRows, nt, st);
+        return sp.n <= kJoinEach       ? join_t<T, D, 1>(a, sp, C::kRows, nt, st)
+               : sp.n <= 4 * kJoinEach ? join_t<T, D, 4>(a, sp, C::kRows, nt, st)
+                                       : join_t<T, D, 32>(a, sp, C::kRows, nt, st);
     });
 }
 
