@@ -1506,14 +1506,16 @@ cudaError_t read_device_error(int* code, bool reset) {
         e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
     }
     // the projection GEMM's word (codes 20..23), the recurrent kernel's (30),
-    // the per-channel prep's (13, 14), the cache operators' (40, 41)
-    int gemm = 0, rec = 0, kda = 0, kv = 0, attn = 0;
+    // the per-channel prep's (13, 14), the cache operators' (40, 41, 42..47)
+    int gemm = 0, rec = 0, kda = 0, kv = 0, attn = 0, prompt = 0;
     if (e == cudaSuccess) e = read_gemm_error(&gemm, reset);
     if (e == cudaSuccess) e = read_rec_error(&rec, reset);
     if (e == cudaSuccess) e = read_kda_error(&kda, reset);
     if (e == cudaSuccess) e = read_kv_error(&kv, reset);
     if (e == cudaSuccess) e = read_kv_attn_error(&attn, reset);
-    if (e == cudaSuccess && *code == 0) *code = gemm ? gemm : rec ? rec : kda ? kda : attn ? attn : kv;
+    if (e == cudaSuccess) e = read_kv_prompt_error(&prompt, reset);
+    if (e == cudaSuccess && *code == 0)
+        *code = gemm ? gemm : rec ? rec : kda ? kda : prompt ? prompt : attn ? attn : kv;
     return e;
 }
 

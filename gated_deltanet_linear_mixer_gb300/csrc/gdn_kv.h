@@ -81,12 +81,16 @@ cudaError_t launch_kv_read(const KvReadArgs& a, int head_dim, bool bf16, bool e4
                            cudaStream_t stream);
 size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window,
                               bool bf16, int max_kv_len);
+// The kernel for many rows (gdn_kv_prompt.cu): whether it takes a call, and its launch.
+bool kv_prompt_serves(int n_seq, int max_q, int n_q_heads, int n_kv_heads, bool bf16);
+cudaError_t launch_kv_prompt(const KvAttnArgs& a, int head_dim, bool e4m3, cudaStream_t stream);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3,
                                 cudaStream_t stream);
 // form: gdn_dist_form; logits and probabilities in bf16 or f32.
 cudaError_t launch_accept_drafts(const AcceptArgs& a, bool logits, bool bf16, cudaStream_t stream);
 
 cudaError_t read_kv_error(int* code, bool reset);       // append, read
-cudaError_t read_kv_attn_error(int* code, bool reset);  // attention
+cudaError_t read_kv_attn_error(int* code, bool reset);  // attention, few rows
+cudaError_t read_kv_prompt_error(int* code, bool reset);  // attention, many rows
 
 }  // namespace gdn

@@ -35,7 +35,6 @@
 // over thread blocks and joined by kv_attn_join.
 #include <algorithm>
 #include <atomic>
-#include <cuda_fp16.h>
 
 #include "gdn_internal.h"
 #include "gdn_kv.cuh"
@@ -53,13 +52,6 @@ constexpr int kSpan = 32;         // steps whose pages and scales are looked up 
 constexpr float kLazy = 8.0f;     // a reference lags behind the maximum by at most 2^8
 constexpr float kBias = 7.0f;     // weights are 2^7 times theirs: at most 2^15
 constexpr float kNormal = 21.0f;  // scores down to 2^-21 of the reference are normal f16 weights
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float exp2_ftz(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -90,37 +82,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 // The residual of pack_f16(lo, hi), as f16.
 __device__ __forceinline__ uint32_t pack_f16_rest(uint32_t h, float lo, float hi) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return pack_f16(lo - f.x, hi - f.y);
 }
 
-// Four codes of a word to f16: codes (0, 1) and (2, 3).
-template <typename F> __device__ __forceinline__ void widen_f16(uint32_t w, uint32_t& a, uint32_t& b);
-template <> __device__ __forceinline__ void widen_f16<KvInt8>(uint32_t w, uint32_t& a, uint32_t& b) {
-    // bytes u = code + 128 under the exponent of 1024 are the f16 1024 + u; less 1152 it is the code
-    w ^= 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    uint32_t x = __byte_perm(w, 0x64646464u, 0x4140), y = __byte_perm(w, 0x64646464u, 0x4342);
-    const __half2 hx = __hsub2(*reinterpret_cast<__half2*>(&x), off), hy = __hsub2(*reinterpret_cast<__half2*>(&y), off);
-    a = *reinterpret_cast<const uint32_t*>(&hx);
-    b = *reinterpret_cast<const uint32_t*>(&hy);
-}
-template <> __device__ __forceinline__ void widen_f16<KvE4m3>(uint32_t w, uint32_t& a, uint32_t& b) {
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "mov.b32 {lo, hi}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-        : "=r"(a), "=r"(b)
-        : "r"(w));
-}
-
-// The same to bf16.
+// Four codes of a word to bf16: codes (0, 1) and (2, 3).
 template <typename F> __device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t& a, uint32_t& b);
 template <> __device__ __forceinline__ void widen_bf16<KvInt8>(uint32_t w, uint32_t& a, uint32_t& b) {
     // under the exponent of 128 the low seven bits of a code are the bf16 128 + (c & 127); the sign
@@ -782,9 +750,9 @@ cudaError_t attn_t(const KvAttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window, bool,
+size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window, bool bf16,
                               int max_kv_len) {
-    if (max_q == 0) return 0;
+    if (max_q == 0 || kv_prompt_serves(n_seq, max_q, n_q_heads, n_kv_heads, bf16)) return 0;
     const long long all = static_cast<long long>(max_q) * (n_q_heads / n_kv_heads);
     const int rows = 8 * tiles_of_8(head_dim, all);
     const Split sp = split_of(rows, n_seq, max_q, n_q_heads, n_kv_heads, window, max_kv_len);
@@ -795,6 +763,8 @@ size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_head
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
+    if (kv_prompt_serves(a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, bf16))
+        return launch_kv_prompt(a, head_dim, e4m3, stream);
     return GDN_KV_PICK(attn_t);
 }
 
