@@ -216,16 +216,17 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
             const bool whole = key + kKeys - 1 <= lo_pos && key >= max_lo && key + kKeys <= end;
-            float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j) {
-                s[j] = fmaf(s[j], qs * gc[j / 16].ks, gc[j / 16].lv);
-                if (!whole) {
-                    const int k = key + j;
-                    if (k > pos || k >= end || (a.window && k <= pos - a.window)) s[j] = -INFINITY;
-                }
-                top = fmaxf(top, s[j]);
+            for (int j = 0; j < kKeys; ++j) s[j] = fmaf(s[j], qs * gc[j / 16].ks, gc[j / 16].lv);
+            if (!whole) {
+                const int hi = min(pos, end - 1) - key, lo = a.window ? pos - a.window + 1 - key : 0;
+#pragma unroll
+                for (int j = 0; j < kKeys; ++j) s[j] = j > hi || j < lo ? -INFINITY : s[j];
             }
+            float tops[4] = {s[0], s[1], s[2], s[3]};  // four chains
+#pragma unroll
+            for (int j = 4; j < kKeys; ++j) tops[j & 3] = fmaxf(tops[j & 3], s[j]);
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             const bool lift = __any_sync(0xffffffffu, top > m + kLazy);
             float f = 1.0f;
             if (lift) {
