@@ -19,8 +19,13 @@
 //                      registers) to f16 operand tiles in shared memory, K and
 //                      V in turn, two buffers each; V needs no transpose, its
 //                      operand is MN-major
+//   1 look-up warp     pages' scales to the block constants of the tiles ahead
 //   1 issuing thread   S_i+1 = Q K_i+1^T ahead of O += P_i V_i, so that the
 //                      softmax of one tile runs under the products of others
+// The operand tiles are written by ordinary stores and read by the tensor core:
+// the issuing thread, which has waited for the writers, fences the one against
+// the other.  (A writer's fence would also wait for the loads that it has in
+// flight: 275 us instead of @@ for a prompt of 4096 tokens.)
 // Every wait is bounded (2 s); a wait that gives up records a code (42..48) in
 // this file's device error word and its role stops.
 #include <algorithm>
@@ -46,7 +51,7 @@ constexpr float kBias = 7.0f;        // weights are 2^7 times theirs: at most 2^
 
 template <int D> struct PCfg {
     static constexpr int kConvWarps = D == 256 ? 8 : 4;
-    static constexpr int kThreads = 32 * (4 + kConvWarps + 1);
+    static constexpr int kThreads = 32 * (4 + kConvWarps + 2);
     static constexpr int kPBufs = D == 256 ? 2 : 1;
     static constexpr uint32_t kQ = kM * D * 2, kTile = kKeys * D * 2, kP = kM * kKeys * 2;
     // the operand tiles, then Shared; at head_dim 128 two thread blocks fill an SM's 228 KB to the byte
@@ -82,7 +87,7 @@ struct GroupConst {
 
 struct Shared {
     uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2],
-        c_full[kConst], o_full;
+        c_full[kConst], c_empty[kConst], o_full;
     GroupConst consts[kConst][kGroups];
     float q_scale[kM];
     uint32_t tmem_slot;
@@ -138,14 +143,23 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
             mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.p_empty[i], 1);
         }
-        for (int i = 0; i < kConst; ++i) mbar_init(&sh.c_full[i], 1);
+        for (int i = 0; i < kConst; ++i) {
+            mbar_init(&sh.c_full[i], 1);
+            mbar_init(&sh.c_empty[i], 4);
+        }
         fence_barrier_init();
     }
-    if (warp == 4 + CW) tmem_alloc(&sh.tmem_slot, C::kCols);
+    if (warp == 5 + CW) tmem_alloc(&sh.tmem_slot, C::kCols);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem_slot, t_out = tmem + 2 * kKeys;
+
+    auto page_of = [&](int key) {  // negative: past the end, or not mapped
+        if (key >= end) return -1;
+        const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + key / a.page_size];
+        return page < a.c.n_pages ? page : -1;
+    };
 
     if (warp < 4) {
         // ---- queries: 32 rows a warp, rounded to f16 under a power of two of the row
@@ -188,7 +202,6 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
                 memcpy(__builtin_assume_aligned(dst, E * 2), w, E * 2);
             }
         }
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
 
@@ -201,8 +214,8 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
         bool ok = true;
         for (int i = 0; i < n_tiles; ++i) {
             const int key = first + i * kKeys, sb = i & 1, pb = i % PB;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[sb], (i >> 1) & 1) &&
-                                                   mbar_wait(&sh.c_full[i % kConst], (i / kConst) & 1)))) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_full[sb], (i >> 1) & 1) &&
+                                                   mbar_wait_brief(&sh.c_full[i % kConst], (i / kConst) & 1)))) {
                 if (lane == 0) prompt_fail(42);
                 break;
             }
@@ -214,7 +227,10 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
             for (int g = 0; g < kGroups; ++g) gc[g] = sh.consts[i % kConst][g];
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
+            if (lane == 0) {
+                mbar_arrive(&sh.s_empty[sb]);
+                mbar_arrive(&sh.c_empty[i % kConst]);
+            }
             const bool whole = key + kKeys - 1 <= lo_pos && key >= max_lo && key + kKeys <= end;
 #pragma unroll
             for (int j = 0; j < kKeys; ++j) s[j] = fmaf(s[j], qs * gc[j / 16].ks, gc[j / 16].lv);
@@ -250,7 +266,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
                 l = fmaf(sum, fabsf(gc[g].inv), l);
             }
             // the buffer's earlier weights were used; with one buffer, that is the last tile's product
-            if (i >= PB && !(ok = __all_sync(0xffffffffu, mbar_wait(&sh.p_empty[pb], (i / PB - 1) & 1)))) {
+            if (i >= PB && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.p_empty[pb], (i / PB - 1) & 1)))) {
                 if (lane == 0) prompt_fail(43);
                 break;
             }
@@ -261,7 +277,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
                     make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
             if (lift && i > 0) {  // the output so far, once the products before this tile's are done
                 const int last = i - 1;
-                if (PB > 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sh.p_empty[last % PB], (last / PB) & 1)))) {
+                if (PB > 1 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.p_empty[last % PB], (last / PB) & 1)))) {
                     if (lane == 0) prompt_fail(43);
                     break;
                 }
@@ -276,12 +292,11 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
                 }
                 tc_fence_before_sync();
             }
-            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[pb]);
         }
         // ---- epilogue
-        if (ok && n_tiles > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sh.o_full, 0))) && lane == 0) prompt_fail(44);
+        if (ok && n_tiles > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.o_full, 0))) && lane == 0) prompt_fail(44);
         if (ok) {
             tc_fence_after_sync();
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -311,111 +326,123 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
 #pragma unroll
         for (int i = 0; i < RT; ++i) row[i] = 8 * (cw + CW * i) + (lane & 7);
         const uint8_t* codes[2] = {a.c.k, a.c.v};
-        auto page_of = [&](int key) {
-            if (key >= end) return -1;
-            const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + key / a.page_size];
-            return page < a.c.n_pages ? page : -1;
-        };
-        uint4 raw[2][RT][N];
-        int page[RT], next[RT];
-        auto load = [&](int kv, int i) {  // tile i's codes; rows past the end, and of unmapped pages, are zeros
+        // Two tiles of codes are in flight in registers: a tile's registers take the codes two tiles
+        // on as soon as they are converted; pages are looked up one tile before that.
+        uint4 raw[2][2][RT][N];
+        int page[2][RT];
+        auto load = [&](int b, int kv, int i) {  // rows past the end, and of unmapped pages, are zeros
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const int key = first + i * kKeys + row[t];
-                const bool take = page[t] >= 0;
-                const size_t at = take ? ((static_cast<size_t>(page[t]) * a.n_kv_heads + h) * a.page_size + key % a.page_size) * D
+                const int key = first + i * kKeys + row[t], pg = page[b][t];
+                const bool take = pg >= 0;
+                const size_t at = take ? ((static_cast<size_t>(pg) * a.n_kv_heads + h) * a.page_size + key % a.page_size) * D
                                        : 0;
 #pragma unroll
                 for (int n = 0; n < N; ++n)
-                    raw[kv][t][n] = take ? *reinterpret_cast<const uint4*>(codes[kv] + at + 16 * (c0 + 4 * n))
-                                         : make_uint4(0, 0, 0, 0);
+                    raw[b][kv][t][n] = take ? *reinterpret_cast<const uint4*>(codes[kv] + at + 16 * (c0 + 4 * n))
+                                            : make_uint4(0, 0, 0, 0);
             }
         };
+        bool ok = true;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + b * kKeys + row[t]);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            load(b, 0, b);
+            load(b, 1, b);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + (b + 2) * kKeys + row[t]);
+        for (int i0 = 0; ok && i0 < n_tiles; i0 += 2) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int i = i0 + b;
+                if (i >= n_tiles || !ok) break;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (i >= 2 && ok)
+                        ok = __all_sync(0xffffffffu, mbar_wait_brief(kv ? &sh.v_empty[b] : &sh.k_empty[b], ((i >> 1) - 1) & 1));
+                    if (!ok) break;
+                    uint8_t* tile = (kv ? sv : sk) + b * C::kTile;
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            // 16 codes are two 16-byte chunks of column block n: row of 64 channels, swizzled
+                            const uint4 x = raw[b][kv][t][n];
+                            uint4 lo, hi;
+                            widen_f16<F>(x.x, lo.x, lo.y);
+                            widen_f16<F>(x.y, lo.z, lo.w);
+                            widen_f16<F>(x.z, hi.x, hi.y);
+                            widen_f16<F>(x.w, hi.z, hi.w);
+                            uint8_t* dst = tile + n * (kKeys * 128);
+                            *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0)) = lo;
+                            *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0 + 1)) = hi;
+                        }
+                    load(b, kv, i + 2);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kv ? &sh.v_full[b] : &sh.k_full[b]);
+                }
+#pragma unroll
+                for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + (i + 4) * kKeys + row[t]);
+            }
+        }
+        if (!ok && lane == 0) prompt_fail(45);
+    } else if (warp == 4 + CW) {
+        // ---- block constants, kConst tiles of groups at a time
         float vs_low = INFINITY;
         bool ok = true;
-        if (n_tiles > 0) {
-#pragma unroll
-            for (int t = 0; t < RT; ++t) page[t] = page_of(first + row[t]);
-            load(0, 0);
-            load(1, 0);
-        }
-        for (int i = 0; i < n_tiles; ++i) {
-            const int b = i & 1;
-#pragma unroll
-            for (int t = 0; t < RT; ++t) next[t] = page_of(first + (i + 1) * kKeys + row[t]);
-            if (cw == 0 && lane < kGroups) {  // block constants of the tile's groups
-                const int key = first + i * kKeys + 16 * lane, pg = page_of(key);
-                GroupConst g{0.0f, -INFINITY, 1.0f};
+        for (int i0 = 0; ok && i0 < n_tiles; i0 += kConst) {
+            const int key = first + i0 * kKeys + 16 * lane;
+            GroupConst g{0.0f, -INFINITY, 1.0f};
+            float vs = 1.0f;
+            if (lane < kConst * kGroups) {
+                const int pg = page_of(key);
                 if (pg >= 0) {
                     const size_t block = static_cast<size_t>(pg) * a.n_kv_heads + h;
-                    float vs = a.c.v_scale[block];
                     g.ks = a.c.k_scale[block];
-                    const bool zero = vs == 0.0f;
+                    vs = a.c.v_scale[block];
+                    g.lv = 0.0f;
                     if (vs > 0.0f) vs_low = fminf(vs_low, vs);
-                    if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
-                    g.lv = log2f(vs);
-                    g.inv = (zero ? -1.0f : 1.0f) / vs;
                 } else if (key < end && (!a.window || key + 15 > lo_pos - a.window)) {
                     prompt_fail(kKvErrTable);
                 }
-                sh.consts[i % kConst][lane] = g;
-            }
-            if (cw == 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.c_full[i % kConst]);
             }
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                if (i >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait(kv ? &sh.v_empty[b] : &sh.k_empty[b], ((i >> 1) - 1) & 1)))) {
+            for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
+            const bool zero = vs == 0.0f;  // such a group is given the smallest scale in sight, and a mark
+            if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
+            g.lv += log2f(vs);
+            g.inv = (zero ? -1.0f : 1.0f) / vs;
+            for (int q = 0; q < kConst && i0 + q < n_tiles; ++q) {
+                if (i0 > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.c_empty[q], (i0 / kConst - 1) & 1)))) {
                     if (lane == 0) prompt_fail(45);
                     break;
                 }
-                uint8_t* tile = (kv ? sv : sk) + b * C::kTile;
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        // 16 codes are two 16-byte chunks of column block n: row of 64 channels, swizzled
-                        const uint4 x = raw[kv][t][n];
-                        uint4 lo, hi;
-                        widen_f16<F>(x.x, lo.x, lo.y);
-                        widen_f16<F>(x.y, lo.z, lo.w);
-                        widen_f16<F>(x.z, hi.x, hi.y);
-                        widen_f16<F>(x.w, hi.z, hi.w);
-                        uint8_t* dst = tile + n * (kKeys * 128);
-                        *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0)) = lo;
-                        *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0 + 1)) = hi;
-                    }
-                fence_proxy_async_smem();
+                if (lane / kGroups == q) sh.consts[q][lane % kGroups] = g;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(kv ? &sh.v_full[b] : &sh.k_full[b]);
-                if (kv == 0) {
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) {  // the next tile's K while V is converted
-                        const int keep = page[t];
-                        page[t] = next[t];
-                        next[t] = keep;
-                    }
-                    if (i + 1 < n_tiles) load(0, i + 1);
-                } else if (i + 1 < n_tiles) {
-                    load(1, i + 1);
-                }
+                if (lane == 0) mbar_arrive(&sh.c_full[q]);
             }
-            if (!ok) break;
         }
     } else if (lane == 0) {
         // ---- issue
         constexpr uint32_t id_s = idesc_f16_f32(kM, kKeys, false), id_o = idesc_f16_f32(kM, D, true);
         const uint32_t aq = smem_u32(sq), ak = smem_u32(sk), av = smem_u32(sv), ap = smem_u32(sp);
-        bool ok = n_tiles == 0 || mbar_wait(&sh.q_full, 0);
+        bool ok = n_tiles == 0 || mbar_wait_brief(&sh.q_full, 0);
         uint64_t* last = nullptr;
         uint32_t last_par = 0;
         for (int i = 0; ok && i <= n_tiles; ++i) {
             if (i < n_tiles) {
                 const int b = i & 1;
-                if (!(ok = mbar_wait(&sh.k_full[b], (i >> 1) & 1))) break;
-                if (i >= 2 && !(ok = mbar_wait(&sh.s_empty[b], ((i >> 1) - 1) & 1))) break;
+                if (!(ok = mbar_wait_brief(&sh.k_full[b], (i >> 1) & 1))) break;
+                if (i >= 2 && !(ok = mbar_wait_brief(&sh.s_empty[b], ((i >> 1) - 1) & 1))) break;
                 tc_fence_after_sync();
+                fence_proxy_async_smem();
 #pragma unroll
                 for (int n = 0; n < D / 64; ++n) {
                     const uint64_t da = desc_kmajor_sw128(aq + n * (kM * 128));
@@ -431,9 +458,10 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
             }
             if (i > 0) {
                 const int j = i - 1, b = j & 1, pb = j % PB;
-                if (!(ok = mbar_wait(&sh.v_full[b], (j >> 1) & 1))) break;
-                if (!(ok = mbar_wait(&sh.p_full[pb], (j / PB) & 1))) break;
+                if (!(ok = mbar_wait_brief(&sh.v_full[b], (j >> 1) & 1))) break;
+                if (!(ok = mbar_wait_brief(&sh.p_full[pb], (j / PB) & 1))) break;
                 tc_fence_after_sync();
+                fence_proxy_async_smem();
                 const uint64_t da = desc_kmajor_sw128(ap + pb * C::kP);
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
@@ -452,13 +480,13 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
         }
         if (!ok) prompt_fail(46);
         // nothing of this thread block is in flight when its tensor memory is freed
-        if (last && !mbar_wait(last, last_par)) prompt_fail(47);
+        if (last && !mbar_wait_brief(last, last_par)) prompt_fail(47);
     }
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 4 + CW) tmem_dealloc(tmem, C::kCols);
+    if (warp == 5 + CW) tmem_dealloc(tmem, C::kCols);
 }
 
 template <typename F, int D>

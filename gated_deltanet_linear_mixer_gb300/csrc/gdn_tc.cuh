@@ -80,6 +80,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     return true;
 }
 
+// The same bound by the SM cycle counter alone (2^32 cycles, ~2 s), looked at
+// once in 256 tries: for short waits between warps of a thread block, where
+// reading the timers at every try delays the waiter.
+__device__ __forceinline__ bool mbar_wait_brief(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long c0 = clock64();
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n)
+        if ((n & 255u) == 0 && clock64() - c0 > (1ll << 32)) return false;
+    return true;
+}
+
 // --------------------------------------------------------------------- TMA
 // 2-D tiled bulk tensor load global -> shared, completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
