@@ -1,8 +1,9 @@
-"""Builds libgdn.so (the CUDA kernels + C ABI) in-tree with nvcc for sm_103a.
+"""Builds libgdn.so (the CUDA kernels + C ABI) in-tree with nvcc for sm_103a, and
+_gdn_bind.so (the native argument marshalling of paged.py) with g++.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library next to this file.  Rebuilds only when a source or header is newer than
-the library.
+the libraries.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgdn.so")
+BIND_SRC = os.path.join(CSRC, "gdn_bind.cpp")
+BIND_PATH = os.path.join(PKG, "_gdn_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -37,14 +41,30 @@ def sources():
 
 def _inputs():
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
-        glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(INCLUDE, "gdn.h"), __file__]
+        glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(INCLUDE, "gdn.h"), BIND_SRC, __file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BIND_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BIND_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _bind_flags():
+    """Include and link flags of a CPython module on top of this PyTorch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    compile_flags = ["-O2", "-std=c++17", "-fPIC", "-DUSE_CUDA",
+                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                     "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+                     "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+                     "-I", INCLUDE]
+    link_flags = ["-shared", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                  "-L", PKG, "-lgdn", f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"]
+    return compile_flags, link_flags
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -64,15 +84,25 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return obj
 
+    def run(what, cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+    cxx = os.environ.get("CXX") or "g++"
+    bind_compile, bind_link = _bind_flags()
+    bind_obj = os.path.join(BUILD_DIR, "gdn_bind.cpp.o")
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        bind = ex.submit(run, "g++ on gdn_bind.cpp", [cxx, *bind_compile, "-c", BIND_SRC, "-o", bind_obj])
         objs = list(ex.map(compile_one, srcs))
+        bind.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of libgdn.so failed:\n{r.stdout}\n{r.stderr}")
+    run("link of libgdn.so", [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
     os.replace(tmp, LIB_PATH)
+    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    run("link of _gdn_bind.so", [cxx, bind_obj, "-o", tmp, *bind_link])
+    os.replace(tmp, BIND_PATH)
     return LIB_PATH
 
 
