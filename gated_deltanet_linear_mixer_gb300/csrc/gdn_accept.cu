@@ -1,145 +1,289 @@
 // Verification of drafted tokens from given random numbers
 // (gdn_accept_drafts in include/gdn.h states the rule).
 //
-// One thread block per sequence walks its rows: logits rows first give their
-// maximum (with its lowest index) and sum of exponentials, the draft's two
-// probabilities decide whether it stands, and the row where that ends gives
-// the token by the largest r / noise.  The race r / noise needs no prefix sums
-// over the vocabulary, so the result does not depend on the order in which
-// threads add.
-#include <cfloat>
+// Mathematics.  p_t(x) = e^((l_x - m_t) / tau) / Z_t needs a row's maximum and
+// sum (given probabilities need neither); drafts are then decided one after the
+// other; and the row where that ends gives argmax_j r_j / e_j.  The race r / e
+// needs no prefix sums over the vocabulary, so a result does not depend on the
+// order in which threads add, and a row is read once for its sums and once more
+// (from L2) for its race.
+//
+// A cluster of thread blocks takes a sequence, each block a slice of the
+// vocabulary; sums and winners are exchanged through distributed shared memory,
+// so a sequence needs one launch and no workspace.  What bounds it: HBM for
+// large vocabularies and many sequences, else the chain of memory round trips:
+// lengths, rows, exchange, row again, exchange.  Of logits, the rows of `step`
+// drafts are summed at a time, different warps on different rows: all of them
+// where a block's slice is short, one draft after the other where bytes count
+// and a fallen draft spares the rows behind it.
+#include <algorithm>
+#include <cooperative_groups.h>
 
-#include "gdn_common.cuh"
 #include "gdn_internal.h"
-#include "gdn_kv.h"
+#include "gdn_kv.cuh"
+#include "gdn_tc.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxDrafts = 16, kMaxCluster = 8;
+constexpr int kRowsMost = 2 * kMaxDrafts + 1;
+constexpr int kUnroll = 8;
 
-struct Best {
-    float v;
-    int i;
+// A row's logits over one lane's share: running maximum and sum of exponentials
+// (of base 2, arguments times c = log2 e / tau), or maximum and its lowest index.
+struct Stat {
+    float m, s;
+    int at;
 };
-__device__ __forceinline__ Best better(Best a, Best b) {  // the larger; the lower index on ties
-    return (b.v > a.v || (b.v == a.v && b.i < a.i)) ? b : a;
+__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
+    Stat r;
+    r.m = fmaxf(a.m, b.m);
+    r.s = (a.m == -INFINITY ? 0.0f : a.s * exp2_ftz((a.m - r.m) * c)) +
+          (b.m == -INFINITY ? 0.0f : b.s * exp2_ftz((b.m - r.m) * c));
+    r.at = a.m > b.m || (a.m == b.m && a.at < b.at) ? a.at : b.at;
+    return r;
 }
-__device__ __forceinline__ Best block_best(Best x) {
-    __shared__ Best part[32];
+
+// Elements lo, lo + step, .. below hi; GREEDY: only where the maximum is.
+template <typename T, bool GREEDY>
+__device__ __forceinline__ Stat row_stat(const T* x, int lo, int hi, int step, float c) {
+    Stat r{-INFINITY, 0.0f, 0x7fffffff};
+    for (int j = lo; j < hi; j += kUnroll * step) {
+        float v[kUnroll];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const Best y{__shfl_xor_sync(0xffffffffu, x.v, off), __shfl_xor_sync(0xffffffffu, x.i, off)};
-        x = better(x, y);
+        for (int k = 0; k < kUnroll; ++k) v[k] = j + k * step < hi ? to_f32(x[j + k * step]) : -INFINITY;
+        if (GREEDY) {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (v[k] > r.m) {
+                    r.m = v[k];
+                    r.at = j + k * step;
+                }
+        } else {
+            float top = v[0];
+#pragma unroll
+            for (int k = 1; k < kUnroll; ++k) top = fmaxf(top, v[k]);
+            if (top > r.m) {
+                r.s = r.m == -INFINITY ? 0.0f : r.s * exp2_ftz((r.m - top) * c);
+                r.m = top;
+            }
+            if (r.m > -INFINITY) {
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k) r.s += exp2_ftz((v[k] - r.m) * c);
+            }
+        }
     }
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = part[0];
-    for (int w = 1; w < kThreads / 32; ++w) x = better(x, part[w]);
-    __syncthreads();
-    return x;
-}
-__device__ __forceinline__ float block_sum(float x) {
-    __shared__ float part[32];
-    x = group_sum<32>(x);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0f;
-    for (int w = 0; w < kThreads / 32; ++w) x += part[w];
-    __syncthreads();
-    return x;
+    return r;
 }
 
-// A row's distribution: probability of token j is exp((x_j - top) inv_t) / sum.
+// A row's distribution: p_j = 2^((x_j - top) c) scale.
 struct Row {
-    float top, inv_sum;
-    int at;  // lowest index of the largest logit
+    float top, scale;
+};
+template <typename T, bool LOGITS>
+__device__ __forceinline__ float prob(float x, float c, const Row& r) {
+    return LOGITS ? exp2_ftz((x - r.top) * c) * r.scale : x;
+}
+
+// Positive scores order as their bits do; the lower index wins a tie.
+__device__ __forceinline__ unsigned long long race_key(float score, int j) {
+    return static_cast<unsigned long long>(__float_as_uint(score)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(j));
+}
+
+struct Shared {
+    Stat part[kRowsMost][kWarps];          // of this block's warps
+    Stat all[kRowsMost][kMaxCluster];      // of the cluster's blocks
+    Row rows[kRowsMost];                   // target rows, then draft rows, of the step
+    int top_at[kRowsMost];
+    unsigned long long best[kWarps];
+    unsigned long long winners[2][kMaxCluster];
 };
 
-template <typename T>
-__device__ Row row_stats(const T* x, int vocab, float inv_t) {
-    Best b{-INFINITY, 0x7fffffff};
-    for (int j = threadIdx.x; j < vocab; j += kThreads) b = better(b, Best{to_f32(x[j]), j});
-    b = block_best(b);
-    float s = 0.0f;
-    if (b.v > -INFINITY)
-        for (int j = threadIdx.x; j < vocab; j += kThreads) s += expf((to_f32(x[j]) - b.v) * inv_t);
-    s = block_sum(s);
-    return Row{b.v, s > 0.0f ? 1.0f / s : 0.0f, b.i};
-}
-
 template <typename T, bool LOGITS>
-__device__ __forceinline__ float prob(const T* x, int j, const Row& r, float inv_t) {
-    if (!LOGITS) return to_f32(x[j]);
-    return r.inv_sum > 0.0f ? expf((to_f32(x[j]) - r.top) * inv_t) * r.inv_sum : 0.0f;
-}
-
-template <typename T, bool LOGITS>
-__global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptArgs a) {
-    const int seq = blockIdx.x, V = a.vocab;
-    const T* target = static_cast<const T*>(a.target) + static_cast<long long>(seq) * (a.T + 1) * a.target_stride;
-    const T* draft = static_cast<const T*>(a.draft) + static_cast<long long>(seq) * a.T * a.draft_stride;
+__global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptArgs a, const int step) {
+    __shared__ Shared sh;
+    tc::cluster_arrive();  // a block writes to another only once that has started: waited for below
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int seq = blockIdx.x / C, V = a.vocab, T_ = a.T;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int share = (V + C - 1) / C, lo = min(V, rank * share), hi = min(V, lo + share);
+    const T* target = static_cast<const T*>(a.target) + static_cast<long long>(seq) * (T_ + 1) * a.target_stride;
+    const T* draft = a.draft ? static_cast<const T*>(a.draft) + static_cast<long long>(seq) * T_ * a.draft_stride : nullptr;
     const float temp = LOGITS && a.temperature ? a.temperature[seq] : 1.0f;
     const bool greedy = LOGITS && !(temp > 0.0f);
-    const float inv_t = greedy ? 1.0f : 1.0f / temp;
-    int32_t* tokens = a.tokens + static_cast<long long>(seq) * (a.T + 1);
-    Row p{0, 0, 0}, q{0, 0, 0};
-    int t = 0, fallen = -1;
-    const T *px = nullptr, *qx = nullptr;
-    for (;; ++t) {
-        px = target + t * a.target_stride;
-        if (LOGITS) p = row_stats(px, V, inv_t);
-        fallen = -1;
-        if (t == a.T) break;
-        const int x = a.drafts[static_cast<long long>(seq) * a.T + t];
-        if (x < 0 || x >= V) break;
-        fallen = x;
-        if (greedy) {
-            if (x != p.at) break;
-        } else {
-            float qv = 1.0f;
-            if (a.draft) {
-                qx = draft + t * a.draft_stride;
-                if (LOGITS) q = row_stats(qx, V, inv_t);
-                qv = prob<T, LOGITS>(qx, x, q, inv_t);
-            }
-            const float u = a.uniforms[static_cast<long long>(seq) * a.T + t];
-            if (!(u * qv < prob<T, LOGITS>(px, x, p, inv_t))) break;
-        }
-        if (threadIdx.x == 0) tokens[t] = x;
+    const float c = greedy ? kLog2e : kLog2e / temp;
+    // lane t: draft t, whether there is one, and its random number
+    int x = -1;
+    float u = 0.0f;
+    if (lane < T_) {
+        x = a.drafts[static_cast<long long>(seq) * T_ + lane];
+        u = a.uniforms[static_cast<long long>(seq) * T_ + lane];
     }
-    int token;
-    if (greedy) {
-        token = p.top > -INFINITY ? p.at : -1;
+    if (x < 0 || x >= V) x = -1;
+    const unsigned there = __ballot_sync(0xffffffffu, x >= 0);
+    const int drafts = __ffs(~there) - 1;  // drafts before the first gap: rows 0 .. drafts may be drawn from
+    // given probabilities, and the logits of the drafts: two numbers a draft
+    float px = 0.0f, qx = 1.0f;
+    if (lane < drafts && !greedy) {
+        px = to_f32(target[lane * a.target_stride + x]);
+        if (draft) qx = to_f32(draft[lane * a.draft_stride + x]);
+    }
+
+    tc::cluster_wait();
+    int t = 0, first = 0;  // drafts that stand; first row of the step in shared memory
+    bool fell = false;
+    Row p{0.0f, 1.0f}, q{0.0f, 1.0f};
+    int top_at = -1;
+    if (!LOGITS) {
+        const unsigned ok = __ballot_sync(0xffffffffu, lane < drafts && u * qx < px);
+        t = __ffs(~ok) - 1;
+        fell = t < drafts;
     } else {
-        const float* e = a.noise + static_cast<long long>(seq) * a.noise_stride;
-        Best b{0.0f, 0x7fffffff};
-        for (int pass = fallen >= 0 ? 0 : 1; pass < 2 && !(b.v > 0.0f); ++pass) {
-            Best mine{0.0f, 0x7fffffff};
-            for (int j = threadIdx.x; j < V; j += kThreads) {
-                float r = prob<T, LOGITS>(px, j, p, inv_t);
-                if (pass == 0) r -= a.draft ? prob<T, LOGITS>(qx, j, q, inv_t) : (j == fallen ? 1.0f : 0.0f);
-                if (r > 0.0f) mine = better(mine, Best{r / e[j], j});
+        for (;;) {
+            // rows of drafts first .. first + n - 1, and the row after them where that is the last
+            const int n = min(step, drafts - first), nt = first + n == drafts ? n + 1 : n;
+            const int nd = draft && !greedy ? n : 0, rows = nt + nd;
+            const int per = max(1, kWarps / rows), lanes = 32 * per;
+            for (int r = warp / per; r < rows; r += max(1, kWarps / per)) {
+                const T* row = r < nt ? target + (first + r) * a.target_stride : draft + (first + r - nt) * a.draft_stride;
+                const int at = lo + (warp % per) * 32 + lane;
+                Stat s = greedy ? row_stat<T, true>(row, at, hi, lanes, c) : row_stat<T, false>(row, at, hi, lanes, c);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) {
+                    const Stat o{__shfl_xor_sync(0xffffffffu, s.m, off), __shfl_xor_sync(0xffffffffu, s.s, off),
+                                 __shfl_xor_sync(0xffffffffu, s.at, off)};
+                    s = join(s, o, c);
+                }
+                if (lane == 0) sh.part[r][warp % per] = s;
             }
-            b = block_best(mine);
+            __syncthreads();
+            for (int r = tid; r < rows * C; r += kThreads) {  // this block's result of a row to every block
+                const int row = r / C, to = r % C;
+                Stat s = sh.part[row][0];
+                for (int w = 1; w < per; ++w) s = join(s, sh.part[row][w], c);
+                *cluster.map_shared_rank(&sh.all[row][rank], to) = s;
+            }
+            cluster.sync();
+            if (tid < rows) {
+                Stat s = sh.all[tid][0];
+                for (int b = 1; b < C; ++b) s = join(s, sh.all[tid][b], c);
+                // a row without a finite logit leaves nothing
+                sh.rows[tid] = s.m > -INFINITY && s.s > 0.0f ? Row{s.m, 1.0f / s.s} : Row{0.0f, 0.0f};
+                sh.top_at[tid] = s.m > -INFINITY ? s.at : -1;
+            }
+            __syncthreads();
+            // the step's drafts, a lane each
+            bool stands = false;
+            if (lane >= first && lane < first + n) {
+                const int r = lane - first;
+                if (greedy) {
+                    stands = sh.top_at[r] == x;
+                } else {
+                    const float pv = prob<T, true>(px, c, sh.rows[r]);
+                    const float qv = draft ? prob<T, true>(qx, c, sh.rows[nt + r]) : 1.0f;
+                    stands = u * qv < pv;
+                }
+            }
+            const unsigned ok = __ballot_sync(0xffffffffu, stands) | ((1u << first) - 1);
+            t = __ffs(~ok) - 1;
+            fell = t < first + n;
+            if (fell || first + n == drafts) {
+                p = sh.rows[t - first];
+                top_at = sh.top_at[t - first];
+                if (fell && nd) q = sh.rows[nt + t - first];
+                break;
+            }
+            first += n;
+            cluster.sync();  // every block has read its results before the next ones arrive
         }
-        token = b.v > 0.0f ? b.i : -1;
     }
-    if (threadIdx.x == 0) {
-        a.accepted[seq] = t;
-        tokens[t] = token;
-        for (int k = t + 1; k <= a.T; ++k) tokens[k] = -1;
+
+    int token = -1;
+    if (greedy) {
+        token = top_at;
+    } else {
+        const T* pr = target + t * a.target_stride;
+        const T* qr = fell && draft ? draft + t * a.draft_stride : nullptr;
+        const int certain = fell && !draft ? __shfl_sync(0xffffffffu, x, t) : -1;  // a draft with q = 1
+        const float* e = a.noise + static_cast<long long>(seq) * a.noise_stride;
+        unsigned long long won = 0;
+        for (int pass = fell ? 0 : 1; pass < 2 && won == 0; ++pass) {
+            unsigned long long best = 0;
+            for (int j = lo + tid; j < hi; j += kUnroll * kThreads) {
+                float pv[kUnroll], qv[kUnroll], ev[kUnroll];
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k) {
+                    const int i = j + k * kThreads;
+                    pv[k] = i < hi ? to_f32(pr[i]) : 0.0f;
+                    qv[k] = i < hi && pass == 0 && qr ? to_f32(qr[i]) : 0.0f;
+                    ev[k] = i < hi ? e[i] : 1.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k) {
+                    const int i = j + k * kThreads;
+                    float r = prob<T, LOGITS>(pv[k], c, p);
+                    if (pass == 0) r -= qr ? prob<T, LOGITS>(qv[k], c, q) : (i == certain ? 1.0f : 0.0f);
+                    const float score = r / ev[k];
+                    if (i < hi && r > 0.0f && score > 0.0f) {
+                        const unsigned long long key = race_key(score, i);
+                        best = key > best ? key : best;
+                    }
+                }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, off);
+                best = o > best ? o : best;
+            }
+            if (lane == 0) sh.best[warp] = best;
+            __syncthreads();
+            if (tid < C) {
+                for (int w = 0; w < kWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
+                *cluster.map_shared_rank(&sh.winners[pass][rank], tid) = best;
+            }
+            cluster.sync();
+            for (int b = 0; b < C; ++b) won = sh.winners[pass][b] > won ? sh.winners[pass][b] : won;
+        }
+        if (won) token = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(won));
     }
+    if (rank == 0 && warp == 0) {
+        if (lane == 0) a.accepted[seq] = t;
+        if (lane <= T_) a.tokens[static_cast<long long>(seq) * (T_ + 1) + lane] = lane < t ? x : lane == t ? token : -1;
+    }
+    cluster.sync();  // no block leaves while another may still write to it
+}
+
+template <typename T, bool LOGITS>
+cudaError_t accept_t(const AcceptArgs& a, cudaStream_t st) {
+    // Blocks of a sequence: enough to occupy the SMs (four blocks fit on one), no slice below 1024.
+    int C = kMaxCluster;
+    while (C > 1 && (static_cast<long long>(a.n_seq) * C > 152 * 4 || a.vocab / C < 1024)) C /= 2;
+    // Drafts summed at a time: all of them while a lane's share of a row stays below 64 logits.
+    const int share = a.vocab / C / kThreads;
+    const int step = share * (a.T + 1) <= 128 ? kMaxDrafts : share <= 32 ? 4 : 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.n_seq) * C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = C;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, accept_kernel<T, LOGITS>, a, step);
 }
 
 }  // namespace
 
 cudaError_t launch_accept_drafts(const AcceptArgs& a, bool logits, bool bf16, cudaStream_t stream) {
-    if (!logits) accept_kernel<float, false><<<a.n_seq, kThreads, 0, stream>>>(a);
-    else if (bf16) accept_kernel<__nv_bfloat16, true><<<a.n_seq, kThreads, 0, stream>>>(a);
-    else accept_kernel<float, true><<<a.n_seq, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (!logits) return accept_t<float, false>(a, stream);
+    return bf16 ? accept_t<__nv_bfloat16, true>(a, stream) : accept_t<float, true>(a, stream);
 }
 
 }  // namespace gdn
