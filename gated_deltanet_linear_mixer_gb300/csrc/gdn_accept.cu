@@ -48,34 +48,57 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
     return r;
 }
 
-// Elements lo, lo + step, .. below hi; GREEDY: only where the maximum is.
+template <bool GREEDY, int N>
+__device__ __forceinline__ void take(Stat& r, const float* v, int at, float c) {
+    float top = v[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) top = fmaxf(top, v[k]);
+    if (!(top > r.m || (!GREEDY && r.m > -INFINITY))) return;
+    if (GREEDY) {
+#pragma unroll
+        for (int k = N - 1; k >= 0; --k)
+            if (v[k] == top) r.at = at + k;
+        r.m = top;
+        return;
+    }
+    if (top > r.m) {
+        r.s = r.m == -INFINITY ? 0.0f : r.s * exp2_ftz((r.m - top) * c);
+        r.m = top;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.s += exp2_ftz((v[k] - r.m) * c);
+}
+
+// Lane `idx` of `lanes`' share of elements lo .. hi - 1 of a row, which may start
+// anywhere: single elements up to a 16-byte boundary, then 16-byte vectors, 64
+// bytes (bf16; fp32 128) of them in flight, then single elements.
+// GREEDY: only where the maximum is.
 template <typename T, bool GREEDY>
-__device__ __forceinline__ Stat row_stat(const T* x, int lo, int hi, int step, float c) {
+__device__ __forceinline__ Stat row_stat(const T* x, int lo, int hi, int idx, int lanes, float c) {
+    constexpr int N = Vec16<T>::N, U = 32 / N;
     Stat r{-INFINITY, 0.0f, 0x7fffffff};
-    for (int j = lo; j < hi; j += kUnroll * step) {
-        float v[kUnroll];
+    const int lead = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(x + lo) & 15u)) & 15u) / static_cast<int>(sizeof(T));
+    const int body = min(hi, lo + lead), nv = (hi - body) / N, tail = body + nv * N;
+    if (lo + idx < body) {
+        const float v = to_f32(x[lo + idx]);
+        take<GREEDY, 1>(r, &v, lo + idx, c);
+    }
+    for (int v = idx; v < nv; v += U * lanes) {
+        uint4 raw[U];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) v[k] = j + k * step < hi ? to_f32(x[j + k * step]) : -INFINITY;
-        if (GREEDY) {
+        for (int k = 0; k < U; ++k)
+            if (v + k * lanes < nv) raw[k] = Vec16<T>::load_raw(x + body + (v + k * lanes) * N);
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
-                if (v[k] > r.m) {
-                    r.m = v[k];
-                    r.at = j + k * step;
-                }
-        } else {
-            float top = v[0];
-#pragma unroll
-            for (int k = 1; k < kUnroll; ++k) top = fmaxf(top, v[k]);
-            if (top > r.m) {
-                r.s = r.m == -INFINITY ? 0.0f : r.s * exp2_ftz((r.m - top) * c);
-                r.m = top;
+        for (int k = 0; k < U; ++k)
+            if (v + k * lanes < nv) {
+                float f[N];
+                Vec16<T>::unpack(raw[k], f);
+                take<GREEDY, N>(r, f, body + (v + k * lanes) * N, c);
             }
-            if (r.m > -INFINITY) {
-#pragma unroll
-                for (int k = 0; k < kUnroll; ++k) r.s += exp2_ftz((v[k] - r.m) * c);
-            }
-        }
+    }
+    if (tail + idx < hi) {
+        const float v = to_f32(x[tail + idx]);
+        take<GREEDY, 1>(r, &v, tail + idx, c);
     }
     return r;
 }
@@ -151,8 +174,8 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptArgs a, co
             const int per = max(1, kWarps / rows), lanes = 32 * per;
             for (int r = warp / per; r < rows; r += max(1, kWarps / per)) {
                 const T* row = r < nt ? target + (first + r) * a.target_stride : draft + (first + r - nt) * a.draft_stride;
-                const int at = lo + (warp % per) * 32 + lane;
-                Stat s = greedy ? row_stat<T, true>(row, at, hi, lanes, c) : row_stat<T, false>(row, at, hi, lanes, c);
+                const int idx = (warp % per) * 32 + lane;
+                Stat s = greedy ? row_stat<T, true>(row, lo, hi, idx, lanes, c) : row_stat<T, false>(row, lo, hi, idx, lanes, c);
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) {
                     const Stat o{__shfl_xor_sync(0xffffffffu, s.m, off), __shfl_xor_sync(0xffffffffu, s.s, off),
