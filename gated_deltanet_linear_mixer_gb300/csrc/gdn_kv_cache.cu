@@ -20,18 +20,16 @@ namespace {
 
 __device__ int g_kv_error = 0;
 
-// 16 channels of a row, as two 8-channel vectors at c0 and c1: the two members
-// of 8 rotation pairs, or 16 unrotated channels.
+// 16 channels of a row, as two 8-channel vectors at c0 and c1, such that
+// neighbouring units' vectors are neighbours in memory: the two members of 8
+// rotation pairs (style half), else vectors that hold whole pairs, or none.
 struct Unit {
     int c0, c1;
-    bool rotated;
 };
-__device__ __forceinline__ Unit unit_at(int u, int rope_dim, int style) {
-    Unit r;
-    r.rotated = 16 * u < rope_dim;
-    r.c0 = (r.rotated && style == 0) ? 8 * u : 16 * u;
-    r.c1 = (r.rotated && style == 0) ? 8 * u + rope_dim / 2 : 16 * u + 8;
-    return r;
+template <int D> __device__ __forceinline__ Unit unit_at(int u, int rope_dim, int style) {
+    if (style != 0 || rope_dim == 0) return Unit{8 * u, 8 * u + D / 2};
+    if (16 * u < rope_dim) return Unit{8 * u, 8 * u + rope_dim / 2};
+    return Unit{rope_dim / 2 + 8 * u, rope_dim / 2 + 8 * u + (D - rope_dim) / 2};
 }
 
 template <typename T>
@@ -54,18 +52,25 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s
     b = rb;
 }
 
-// x[0..7], x[8..15]: the unit's two vectors; cs: the row's cosines and sines of
-// pairs 8u .. 8u + 7.
-__device__ __forceinline__ void rotate_unit(float* x, const float* row, int u, int rope_dim, int style) {
+// x[0..7], x[8..15]: the vectors of unit u; row: the cosines and sines of its token.
+__device__ __forceinline__ void rotate_unit(float* x, const float* row, int u, const Unit& w, int rope_dim, int style) {
     float c[8], s[8];
-    load8(row + 8 * u, c);
-    load8(row + rope_dim / 2 + 8 * u, s);
     if (style == 0) {
+        if (16 * u >= rope_dim) return;
+        load8(row + 8 * u, c);
+        load8(row + rope_dim / 2 + 8 * u, s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) rotate_pair(x[i], x[8 + i], c[i], s[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rotate_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
+        for (int v = 0; v < 2; ++v) {  // four pairs a vector
+            const int ch = v ? w.c1 : w.c0;
+            if (ch >= rope_dim) continue;
+            Vec16<float>::load(row + ch / 2, c);
+            Vec16<float>::load(row + rope_dim / 2 + ch / 2, s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rotate_pair(x[8 * v + 2 * i], x[8 * v + 2 * i + 1], c[i], s[i]);
+        }
     }
 }
 
@@ -79,37 +84,56 @@ __device__ __forceinline__ const float* rope_row(const KvAppendArgs& a, int tok,
     return a.rope + static_cast<size_t>(p) * a.rope_dim;
 }
 
-constexpr int kUnitsPerThread = 4;  // 64 values held in registers
+constexpr int kQUnits = 4;  // units of q a lane has in flight
 
-template <typename T, typename F, int D>
-__global__ void __launch_bounds__(512) kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
+// UNITS: units of new rows a thread holds in registers (4: whole pages; 1: a few
+// rows a page, where small thread blocks keep many pages in flight).
+template <typename T, typename F, int D, int UNITS>
+__global__ void __launch_bounds__(UNITS == 1 ? 256 : 512)
+kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
     constexpr int U = D / 16;  // units of a row
     const int tid = threadIdx.x, nt = blockDim.x;
     const int B = a.page_size;
 
-    if (static_cast<int>(blockIdx.x) >= n_store_blocks) {  // q rows
-        const long long total = static_cast<long long>(a.b.n_tokens) * a.n_q_heads * U;
-        const long long step = static_cast<long long>(gridDim.x - n_store_blocks) * nt;
-        for (long long i = static_cast<long long>(blockIdx.x - n_store_blocks) * nt + tid; i < total; i += step) {
-            const int u = static_cast<int>(i % U);
-            const long long r = i / U;
-            const int h = static_cast<int>(r % a.n_q_heads), tok = static_cast<int>(r / a.n_q_heads);
-            const Unit w = unit_at(u, a.rope_dim, a.rope_style);
-            const T* src = static_cast<const T*>(a.q.data) + tok * a.q.token_stride + h * a.q.head_stride;
-            float x[16];
-            load8(src + w.c0, x);
-            load8(src + w.c1, x + 8);
-            if (w.rotated) {
-                int pos = 0;
-                if (!a.positions) {
-                    const int s = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
-                    pos = a.b.kv_lens[s] - (a.b.cu[s + 1] - tok);
-                }
-                rotate_unit(x, rope_row(a, tok, pos), u, a.rope_dim, a.rope_style);
+    if (static_cast<int>(blockIdx.x) >= n_store_blocks) {
+        // q: a warp takes 32 kQUnits units of one token, which has one position and one table row
+        const int units = a.n_q_heads * U, parts = (units + 32 * kQUnits - 1) / (32 * kQUnits);
+        const long long w = static_cast<long long>(blockIdx.x - n_store_blocks) * (nt / 32) + (tid >> 5);
+        const int tok = static_cast<int>(w / parts);
+        if (tok >= a.b.n_tokens) return;
+        const int first = static_cast<int>(w % parts) * 32 * kQUnits + (tid & 31);
+        const T* src = static_cast<const T*>(a.q.data) + tok * a.q.token_stride;
+        T* dst = static_cast<T*>(a.q_out) + static_cast<size_t>(tok) * a.n_q_heads * D;
+        float x[kQUnits][16];
+#pragma unroll
+        for (int k = 0; k < kQUnits; ++k) {
+            const int i = first + 32 * k;
+            if (i < units) {
+                const Unit r = unit_at<D>(i % U, a.rope_dim, a.rope_style);
+                const T* row = src + i / U * a.q.head_stride;
+                load8(row + r.c0, x[k]);
+                load8(row + r.c1, x[k] + 8);
             }
-            T* dst = static_cast<T*>(a.q_out) + (static_cast<size_t>(tok) * a.n_q_heads + h) * D;
-            store8(dst + w.c0, x);
-            store8(dst + w.c1, x + 8);
+        }
+        const float* row = nullptr;
+        if (a.rope_dim > 0) {
+            int pos = 0;
+            if (!a.positions) {
+                const int s = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
+                pos = a.b.kv_lens[s] - (a.b.cu[s + 1] - tok);
+            }
+            row = rope_row(a, tok, pos);
+        }
+#pragma unroll
+        for (int k = 0; k < kQUnits; ++k) {
+            const int i = first + 32 * k;
+            if (i < units) {
+                const int u = i % U;
+                const Unit r = unit_at<D>(u, a.rope_dim, a.rope_style);
+                if (row) rotate_unit(x[k], row, u, r, a.rope_dim, a.rope_style);
+                store8(dst + i / U * D + r.c0, x[k]);
+                store8(dst + i / U * D + r.c1, x[k] + 8);
+            }
         }
         return;
     }
@@ -140,19 +164,19 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const KvAppendArgs a, co
     const int kept = start > lp * B ? r0 : 0;                      // earlier rows of this sequence
 
     const KvRows& rows = is_v ? a.v : a.k;
-    float x[kUnitsPerThread][16];
+    float x[UNITS][16];
     float most = 0.0f;
     const int n_units = (r1 - r0) * U;
 #pragma unroll
-    for (int it = 0; it < kUnitsPerThread; ++it) {
+    for (int it = 0; it < UNITS; ++it) {
         const int i = tid + it * nt;
         if (i < n_units) {
             const int u = i % U, pos = lp * B + r0 + i / U, tok = q0 + (pos - start);
-            const Unit w = unit_at(u, is_v ? 0 : a.rope_dim, a.rope_style);
+            const Unit w = unit_at<D>(u, is_v ? 0 : a.rope_dim, a.rope_style);
             const T* src = static_cast<const T*>(rows.data) + tok * rows.token_stride + h * rows.head_stride;
             load8(src + w.c0, x[it]);
             load8(src + w.c1, x[it] + 8);
-            if (w.rotated) rotate_unit(x[it], rope_row(a, tok, pos), u, a.rope_dim, a.rope_style);
+            if (!is_v && a.rope_dim > 0) rotate_unit(x[it], rope_row(a, tok, pos), u, w, a.rope_dim, a.rope_style);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float m = fabsf(x[it][e]);
@@ -184,11 +208,11 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const KvAppendArgs a, co
         }
     }
 #pragma unroll
-    for (int it = 0; it < kUnitsPerThread; ++it) {
+    for (int it = 0; it < UNITS; ++it) {
         const int i = tid + it * nt;
         if (i < n_units) {
             const int u = i % U, row = r0 + i / U;
-            const Unit w = unit_at(u, is_v ? 0 : a.rope_dim, a.rope_style);
+            const Unit w = unit_at<D>(u, is_v ? 0 : a.rope_dim, a.rope_style);
             uint8_t c[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) c[e] = scale > 0.0f ? F::code(x[it][e] / scale) : 0;
@@ -202,62 +226,90 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const KvAppendArgs a, co
     if (tid == 0) *scale_at = scale;
 }
 
-constexpr int kReadThreads = 256;
+constexpr int kReadThreads = 256, kReadVectors = 4;
 
-// One thread takes 16 codes of K and of V.
+// A warp takes 32 kReadVectors 16-byte vectors of one token's K and V outputs:
+// the token's page is looked up once.
 template <typename T, typename F, int D>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvReadArgs a) {
-    constexpr int U = D / 16;
-    const long long total = static_cast<long long>(a.b.n_tokens) * a.n_kv_heads * U;
-    const long long i = static_cast<long long>(blockIdx.x) * kReadThreads + threadIdx.x;
-    if (i >= total) return;
-    const int u = static_cast<int>(i % U);
-    const long long r = i / U;
-    const int h = static_cast<int>(r % a.n_kv_heads), tok = static_cast<int>(r / a.n_kv_heads);
+    constexpr int N = Vec16<T>::N, P = D / N;  // codes of a vector, vectors of a head
+    const int per_row = a.n_kv_heads * P, parts = (per_row + 32 * kReadVectors - 1) / (32 * kReadVectors);
+    const long long w = static_cast<long long>(blockIdx.x) * (kReadThreads / 32) + (threadIdx.x >> 5);
+    const int tok = static_cast<int>(w / parts);
+    if (tok >= a.b.n_tokens) return;
+    const int first = static_cast<int>(w % parts) * 32 * kReadVectors + (threadIdx.x & 31);
     const int seq = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
     const long long pos = static_cast<long long>(a.b.kv_lens[seq]) + (tok - a.b.cu[seq]);
     const long long lp = pos < 0 ? -1 : pos / a.page_size;
     const int page = lp >= 0 && lp < a.b.pages_per_seq
                          ? a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + lp] : -1;
-    const bool mapped = page >= 0 && page < a.c.n_pages;
-    if (!mapped) atomicCAS(&g_kv_error, 0, kKvErrTable);
-    const size_t block = static_cast<size_t>(mapped ? page : 0) * a.n_kv_heads + h;
-    const size_t at = (block * a.page_size + (mapped ? pos % a.page_size : 0)) * D + 16 * u;
+    const bool mapped = page >= 0 && page < a.c.n_pages;  // else zeros
+    if (!mapped && (threadIdx.x & 31) == 0) atomicCAS(&g_kv_error, 0, kKvErrTable);
+    const size_t block0 = static_cast<size_t>(mapped ? page : 0) * a.n_kv_heads;
+    const int slot = mapped ? static_cast<int>(pos % a.page_size) : 0;
+    uint2 code[kReadVectors][2];
+    float scale[kReadVectors][2];
 #pragma unroll
-    for (int is_v = 0; is_v < 2; ++is_v) {
-        float x[16] = {};
-        if (mapped) {
-            const uint4 w = *reinterpret_cast<const uint4*>((is_v ? a.c.v : a.c.k) + at);
-            const float s = (is_v ? a.c.v_scale : a.c.k_scale)[block];
-            const uint8_t* c = reinterpret_cast<const uint8_t*>(&w);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = F::value(c[e]) * s;
+    for (int k = 0; k < kReadVectors; ++k) {
+        const int i = first + 32 * k;
+        code[k][0] = code[k][1] = make_uint2(0, 0);
+        scale[k][0] = scale[k][1] = 0.0f;
+        if (i >= per_row || !mapped) continue;
+        const size_t block = block0 + i / P;
+        const size_t at = (block * a.page_size + slot) * D + i % P * N;
+        if (N == 8) {
+            code[k][0] = *reinterpret_cast<const uint2*>(a.c.k + at);
+            code[k][1] = *reinterpret_cast<const uint2*>(a.c.v + at);
+        } else {
+            code[k][0].x = *reinterpret_cast<const uint32_t*>(a.c.k + at);
+            code[k][1].x = *reinterpret_cast<const uint32_t*>(a.c.v + at);
         }
-        T* dst = static_cast<T*>(is_v ? a.v_out : a.k_out) + static_cast<size_t>(r) * D + 16 * u;
-        store8(dst, x);
-        store8(dst + 8, x + 8);
+        scale[k][0] = a.c.k_scale[block];
+        scale[k][1] = a.c.v_scale[block];
+    }
+#pragma unroll
+    for (int k = 0; k < kReadVectors; ++k) {
+        const int i = first + 32 * k;
+        if (i >= per_row) continue;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            float x[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const uint32_t word = e < 4 ? code[k][kv].x : code[k][kv].y;
+                x[e] = F::value(static_cast<uint8_t>(word >> (8 * (e & 3)))) * scale[k][kv];
+            }
+            Vec16<T>::store(static_cast<T*>(kv ? a.v_out : a.k_out) + (static_cast<size_t>(tok) * per_row + i) * N, x);
+        }
     }
 }
 
-template <typename T, typename F, int D>
-cudaError_t append_t(const KvAppendArgs& a, cudaStream_t st) {
+template <typename T, typename F, int D, int UNITS>
+cudaError_t append_units(const KvAppendArgs& a, int nt, cudaStream_t st) {
     const int B = a.page_size;
-    // enough threads that kUnitsPerThread units each cover a whole page
-    const int nt = std::max(64, B * D / (16 * kUnitsPerThread));
     const long long slots = a.b.uniform_q ? static_cast<long long>(a.b.n_seq) * ((a.b.uniform_q + B - 2) / B + 1)
                                           : static_cast<long long>(a.b.n_tokens) / B + 2LL * a.b.n_seq;
     const long long store = slots * a.n_kv_heads * 2;
-    const long long q_units = a.q.data ? static_cast<long long>(a.b.n_tokens) * a.n_q_heads * (D / 16) : 0;
-    const long long q_blocks = std::min((q_units + nt - 1) / nt, 152LL * 16);
+    const long long parts = (a.n_q_heads * (D / 16) + 32 * kQUnits - 1) / (32 * kQUnits);
+    const long long q_blocks = a.q.data ? (a.b.n_tokens * parts + nt / 32 - 1) / (nt / 32) : 0;
     if (store + q_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kv_append_kernel<T, F, D><<<static_cast<unsigned>(store + q_blocks), nt, 0, st>>>(a, static_cast<int>(store));
+    kv_append_kernel<T, F, D, UNITS><<<static_cast<unsigned>(store + q_blocks), nt, 0, st>>>(a, static_cast<int>(store));
     return cudaGetLastError();
 }
 
 template <typename T, typename F, int D>
+cudaError_t append_t(const KvAppendArgs& a, cudaStream_t st) {
+    // units of new rows in a page: up to 128 are a small thread block's one each, whole pages four a thread
+    const int units = std::min(a.b.max_q, a.page_size) * (D / 16);
+    return units <= 128 ? append_units<T, F, D, 1>(a, std::max(64, (units + 31) / 32 * 32), st)
+                        : append_units<T, F, D, 4>(a, std::max(64, (units + 127) / 128 * 32), st);
+}
+
+template <typename T, typename F, int D>
 cudaError_t read_t(const KvReadArgs& a, cudaStream_t st) {
-    const long long units = static_cast<long long>(a.b.n_tokens) * a.n_kv_heads * (D / 16);
-    const long long blocks = (units + kReadThreads - 1) / kReadThreads;
+    const int per_row = a.n_kv_heads * (D / Vec16<T>::N);
+    const long long warps = static_cast<long long>(a.b.n_tokens) * ((per_row + 32 * kReadVectors - 1) / (32 * kReadVectors));
+    const long long blocks = (warps + kReadThreads / 32 - 1) / (kReadThreads / 32);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     kv_read_kernel<T, F, D><<<static_cast<unsigned>(blocks), kReadThreads, 0, st>>>(a);
     return cudaGetLastError();
