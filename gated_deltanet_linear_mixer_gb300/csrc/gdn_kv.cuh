@@ -15,15 +15,17 @@ namespace gdn {
 
 // Cache codes.  top: the largest code value; a block's scale is its largest
 // |value| times 1 / top (one fp32 product), a code is value / scale rounded to
-// nearest even.
+// nearest even, saturating, NaN as 0.
 struct KvInt8 {
     __device__ static constexpr float top() { return 127.0f; }
     __device__ __forceinline__ static float value(uint8_t c) {
         return static_cast<float>(static_cast<int8_t>(c));
     }
-    __device__ __forceinline__ static uint8_t code(float y) {  // NaN -> 0
-        y = y == y ? fminf(fmaxf(rintf(y), -127.0f), 127.0f) : 0.0f;
-        return static_cast<uint8_t>(static_cast<int8_t>(static_cast<int>(y)));
+    __device__ __forceinline__ static uint32_t code4(const float* y) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = max(min(__float2int_rn(y[i]), 127), -127);  // NaN converts to 0
+        return __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
     }
 };
 struct KvE4m3 {
@@ -31,8 +33,13 @@ struct KvE4m3 {
     __device__ __forceinline__ static float value(uint8_t c) {
         return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
     }
-    __device__ __forceinline__ static uint8_t code(float y) {
-        return y == y ? __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3) : 0;
+    __device__ __forceinline__ static uint32_t code4(const float* y) {
+        float z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = y[i] == y[i] ? y[i] : 0.0f;
+        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(z[0], z[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(z[2], z[3]), __NV_SATFINITE, __NV_E4M3);
+        return a | b << 16;
     }
 };
 
@@ -69,16 +76,29 @@ template <> __device__ __forceinline__ void widen_f16<KvE4m3>(uint32_t w, uint32
         : "r"(w));
 }
 
-// Sequence and index within it of slot x, where sequence i owns slots
-// cu[i] / B + 2 i onwards: at least as many as the pages of B tokens that its
-// cu[i+1] - cu[i] consecutive positions can touch.
-__device__ __forceinline__ int seq_of_slot(const int32_t* __restrict__ cu, int n, int B, int x) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] / B + 2 * mid <= x) lo = mid; else hi = mid - 1;
+// The largest i in 0 .. n - 1 with key(i) <= x (key does not decrease, key(0) <=
+// x), by the whole warp: one load for up to 32 sequences, two for up to 1024.
+template <typename K> __device__ __forceinline__ int warp_search(int n, int x, K&& key) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, at < n && key(lo + at) <= x);
+        const int k = 31 - __clz(below);
+        lo += k * step;
+        n = min(step, n - k * step);
     }
     return lo;
+}
+// The sequence of packed token t, by a warp.
+__device__ __forceinline__ int warp_seq_of_token(const int32_t* __restrict__ cu, int n, int t) {
+    return warp_search(n, t, [&](int i) { return cu[i]; });
+}
+// The sequence of slot x, where sequence i owns slots cu[i] / B + 2 i onwards: at
+// least as many as the pages of B tokens that its cu[i+1] - cu[i] consecutive
+// positions can touch.
+__device__ __forceinline__ int warp_seq_of_slot(const int32_t* __restrict__ cu, int n, int B, int x) {
+    return warp_search(n, x, [&](int i) { return cu[i] / B + 2 * i; });
 }
 
 // Lets `kernel` use `bytes` of dynamic shared memory, once per device (ready:

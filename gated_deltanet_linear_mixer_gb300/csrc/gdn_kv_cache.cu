@@ -84,7 +84,7 @@ __device__ __forceinline__ const float* rope_row(const KvAppendArgs& a, int tok,
     return a.rope + static_cast<size_t>(p) * a.rope_dim;
 }
 
-constexpr int kQUnits = 4;  // units of q a lane has in flight
+constexpr int kQUnits = 2;  // units of q a lane has in flight
 
 // UNITS: units of new rows a thread holds in registers (4: whole pages; 1: a few
 // rows a page, where small thread blocks keep many pages in flight).
@@ -119,7 +119,7 @@ kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
         if (a.rope_dim > 0) {
             int pos = 0;
             if (!a.positions) {
-                const int s = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
+                const int s = a.b.uniform_q ? tok / a.b.uniform_q : warp_seq_of_token(a.b.cu, a.b.n_seq, tok);
                 pos = a.b.kv_lens[s] - (a.b.cu[s + 1] - tok);
             }
             row = rope_row(a, tok, pos);
@@ -146,7 +146,7 @@ kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
         seq = item / per;
         local = item - seq * per;
     } else {
-        seq = seq_of_slot(a.b.cu, a.b.n_seq, B, item);
+        seq = warp_seq_of_slot(a.b.cu, a.b.n_seq, B, item);
         local = item - (a.b.cu[seq] / B + 2 * seq);
     }
     const int q0 = a.b.cu[seq], len = a.b.kv_lens[seq], start = len - (a.b.cu[seq + 1] - q0);
@@ -200,11 +200,17 @@ kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
         const float ratio = old / scale;
         uint4* p = reinterpret_cast<uint4*>(codes);
         for (int i = tid; i < kept * U; i += nt) {
-            uint4 w = p[i];
-            uint8_t* c = reinterpret_cast<uint8_t*>(&w);
+            const uint4 w = p[i];
+            const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+            uint32_t n[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) c[e] = F::code(__fmul_rn(F::value(c[e]), ratio));
-            p[i] = w;
+            for (int e = 0; e < 4; ++e) {
+                float y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __fmul_rn(F::value(static_cast<uint8_t>(c[e] >> (8 * k))), ratio);
+                n[e] = F::code4(y);
+            }
+            p[i] = make_uint4(n[0], n[1], n[2], n[3]);
         }
     }
 #pragma unroll
@@ -213,14 +219,18 @@ kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
         if (i < n_units) {
             const int u = i % U, row = r0 + i / U;
             const Unit w = unit_at<D>(u, is_v ? 0 : a.rope_dim, a.rope_style);
-            uint8_t c[16];
+            uint32_t c[4] = {0, 0, 0, 0};
+            if (scale > 0.0f) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) c[e] = scale > 0.0f ? F::code(x[it][e] / scale) : 0;
-            uint2 lo, hi;
-            memcpy(&lo, c, 8);
-            memcpy(&hi, c + 8, 8);
-            *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * D + w.c0) = lo;
-            *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * D + w.c1) = hi;
+                for (int e = 0; e < 4; ++e) {
+                    float y[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = x[it][4 * e + k] / scale;
+                    c[e] = F::code4(y);
+                }
+            }
+            *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * D + w.c0) = make_uint2(c[0], c[1]);
+            *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * D + w.c1) = make_uint2(c[2], c[3]);
         }
     }
     if (tid == 0) *scale_at = scale;
@@ -238,7 +248,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvReadArgs 
     const int tok = static_cast<int>(w / parts);
     if (tok >= a.b.n_tokens) return;
     const int first = static_cast<int>(w % parts) * 32 * kReadVectors + (threadIdx.x & 31);
-    const int seq = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
+    const int seq = a.b.uniform_q ? tok / a.b.uniform_q : warp_seq_of_token(a.b.cu, a.b.n_seq, tok);
     const long long pos = static_cast<long long>(a.b.kv_lens[seq]) + (tok - a.b.cu[seq]);
     const long long lp = pos < 0 ? -1 : pos / a.page_size;
     const int page = lp >= 0 && lp < a.b.pages_per_seq
