@@ -4,11 +4,16 @@
 // kv_append: one thread block per (page the call writes to, kv head, K or V)
 // finds the block's largest |new value|, settles the block's scale and writes
 // the codes, so the scale needs no atomics and every result is independent of
-// order; further thread blocks of the same launch rotate q.  A thread holds
-// its (rotated) values in registers between the maximum and the rounding, so
-// the new rows are read once.  Products and sums of the rotation are rounded
-// one by one (no fused multiply-add) and the division is the exact one: the
-// stored codes do not depend on how a compiler contracts an expression.
+// order.  A thread holds its (rotated) values in registers between the maximum
+// and the rounding, so the new rows are read once.  Products and sums of the
+// rotation are rounded one by one (no fused multiply-add) and the division is
+// the exact one: the stored codes do not depend on how a compiler contracts an
+// expression.  q is rotated by further thread blocks: of the same launch for a
+// few tokens, where the chain of look-ups (lengths, page, scale) bounds the time
+// and a second launch would add to it; of a kernel beside it for prompts, where
+// registers bound how many warps cover that chain (8,688 tokens, 32 + 2 x 8 heads
+// of 128: 79 us in one kernel, 52 us in two; the bytes alone take 30 us).
+// kv_read: bytes bound it, 90% of the measured HBM rate at 16,000 tokens.
 #include <algorithm>
 
 #include "gdn_internal.h"
@@ -86,55 +91,74 @@ __device__ __forceinline__ const float* rope_row(const KvAppendArgs& a, int tok,
 
 constexpr int kQUnits = 2;  // units of q a lane has in flight
 
-// UNITS: units of new rows a thread holds in registers (4: whole pages; 1: a few
-// rows a page, where small thread blocks keep many pages in flight).
+// q: a warp takes 32 kQUnits units of one token, which has one position and one
+// table row.  `block`: thread blocks of q before this one.
+template <typename T, int D>
+__device__ __forceinline__ void rotate_q(const KvAppendArgs& a, unsigned block) {
+    constexpr int U = D / 16;  // units of a row
+    const int units = a.n_q_heads * U, parts = (units + 32 * kQUnits - 1) / (32 * kQUnits);
+    const long long w = static_cast<long long>(block) * (blockDim.x / 32) + (threadIdx.x >> 5);
+    const int tok = static_cast<int>(w / parts);
+    if (tok >= a.b.n_tokens) return;
+    const int first = static_cast<int>(w % parts) * 32 * kQUnits + (threadIdx.x & 31);
+    const T* src = static_cast<const T*>(a.q.data) + tok * a.q.token_stride;
+    T* dst = static_cast<T*>(a.q_out) + static_cast<size_t>(tok) * a.n_q_heads * D;
+    float x[kQUnits][16];
+#pragma unroll
+    for (int k = 0; k < kQUnits; ++k) {
+        const int i = first + 32 * k;
+        if (i < units) {
+            const Unit r = unit_at<D>(i % U, a.rope_dim, a.rope_style);
+            const T* row = src + i / U * a.q.head_stride;
+            load8(row + r.c0, x[k]);
+            load8(row + r.c1, x[k] + 8);
+        }
+    }
+    const float* row = nullptr;
+    if (a.rope_dim > 0) {
+        int pos = 0;
+        if (!a.positions) {
+            const int s = a.b.uniform_q ? tok / a.b.uniform_q : warp_seq_of_token(a.b.cu, a.b.n_seq, tok);
+            pos = a.b.kv_lens[s] - (a.b.cu[s + 1] - tok);
+        }
+        row = rope_row(a, tok, pos);
+    }
+#pragma unroll
+    for (int k = 0; k < kQUnits; ++k) {
+        const int i = first + 32 * k;
+        if (i < units) {
+            const int u = i % U;
+            const Unit r = unit_at<D>(u, a.rope_dim, a.rope_style);
+            if (row) rotate_unit(x[k], row, u, r, a.rope_dim, a.rope_style);
+            store8(dst + i / U * D + r.c0, x[k]);
+            store8(dst + i / U * D + r.c1, x[k] + 8);
+        }
+    }
+}
+
+constexpr int kQThreads = 256;
+
+// Prompts: q by a kernel of its own, which its few registers let fill the SMs,
+// beside the storing kernel (a programmatic dependent that depends on nothing of
+// it).  Its first thread block waits for that kernel, so that whatever follows
+// in the stream follows both.
+template <typename T, int D>
+__global__ void __launch_bounds__(kQThreads) kv_rotate_q_kernel(const KvAppendArgs a) {
+    rotate_q<T, D>(a, blockIdx.x);
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// UNITS: units of new rows a thread holds in registers (2: whole pages, q apart;
+// 1: a few rows a page, small thread blocks, q by further ones of the launch).
 template <typename T, typename F, int D, int UNITS>
-__global__ void __launch_bounds__(UNITS == 1 ? 256 : 512)
+__global__ void __launch_bounds__(UNITS == 1 ? 256 : 1024)
 kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
     constexpr int U = D / 16;  // units of a row
     const int tid = threadIdx.x, nt = blockDim.x;
     const int B = a.page_size;
-
-    if (static_cast<int>(blockIdx.x) >= n_store_blocks) {
-        // q: a warp takes 32 kQUnits units of one token, which has one position and one table row
-        const int units = a.n_q_heads * U, parts = (units + 32 * kQUnits - 1) / (32 * kQUnits);
-        const long long w = static_cast<long long>(blockIdx.x - n_store_blocks) * (nt / 32) + (tid >> 5);
-        const int tok = static_cast<int>(w / parts);
-        if (tok >= a.b.n_tokens) return;
-        const int first = static_cast<int>(w % parts) * 32 * kQUnits + (tid & 31);
-        const T* src = static_cast<const T*>(a.q.data) + tok * a.q.token_stride;
-        T* dst = static_cast<T*>(a.q_out) + static_cast<size_t>(tok) * a.n_q_heads * D;
-        float x[kQUnits][16];
-#pragma unroll
-        for (int k = 0; k < kQUnits; ++k) {
-            const int i = first + 32 * k;
-            if (i < units) {
-                const Unit r = unit_at<D>(i % U, a.rope_dim, a.rope_style);
-                const T* row = src + i / U * a.q.head_stride;
-                load8(row + r.c0, x[k]);
-                load8(row + r.c1, x[k] + 8);
-            }
-        }
-        const float* row = nullptr;
-        if (a.rope_dim > 0) {
-            int pos = 0;
-            if (!a.positions) {
-                const int s = a.b.uniform_q ? tok / a.b.uniform_q : warp_seq_of_token(a.b.cu, a.b.n_seq, tok);
-                pos = a.b.kv_lens[s] - (a.b.cu[s + 1] - tok);
-            }
-            row = rope_row(a, tok, pos);
-        }
-#pragma unroll
-        for (int k = 0; k < kQUnits; ++k) {
-            const int i = first + 32 * k;
-            if (i < units) {
-                const int u = i % U;
-                const Unit r = unit_at<D>(u, a.rope_dim, a.rope_style);
-                if (row) rotate_unit(x[k], row, u, r, a.rope_dim, a.rope_style);
-                store8(dst + i / U * D + r.c0, x[k]);
-                store8(dst + i / U * D + r.c1, x[k] + 8);
-            }
-        }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (UNITS == 1 && static_cast<int>(blockIdx.x) >= n_store_blocks) {
+        rotate_q<T, D>(a, blockIdx.x - n_store_blocks);
         return;
     }
 
@@ -187,7 +211,7 @@ kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
     const size_t block = static_cast<size_t>(page) * a.n_kv_heads + h;
     float* scale_at = (is_v ? a.c.v_scale : a.c.k_scale) + block;
     const float old = kept > 0 ? *scale_at : 0.0f;
-    __shared__ float part[16];
+    __shared__ float part[32];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
     if ((tid & 31) == 0) part[tid >> 5] = most;
@@ -301,18 +325,31 @@ cudaError_t append_units(const KvAppendArgs& a, int nt, cudaStream_t st) {
                                           : static_cast<long long>(a.b.n_tokens) / B + 2LL * a.b.n_seq;
     const long long store = slots * a.n_kv_heads * 2;
     const long long parts = (a.n_q_heads * (D / 16) + 32 * kQUnits - 1) / (32 * kQUnits);
-    const long long q_blocks = a.q.data ? (a.b.n_tokens * parts + nt / 32 - 1) / (nt / 32) : 0;
+    const int q_warps = (UNITS == 1 ? nt : kQThreads) / 32;
+    const long long q_blocks = a.q.data ? (a.b.n_tokens * parts + q_warps - 1) / q_warps : 0;
     if (store + q_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kv_append_kernel<T, F, D, UNITS><<<static_cast<unsigned>(store + q_blocks), nt, 0, st>>>(a, static_cast<int>(store));
-    return cudaGetLastError();
+    const long long blocks = store + (UNITS == 1 ? q_blocks : 0);
+    kv_append_kernel<T, F, D, UNITS><<<static_cast<unsigned>(blocks), nt, 0, st>>>(a, static_cast<int>(store));
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || UNITS == 1 || q_blocks == 0) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(q_blocks));
+    cfg.blockDim = dim3(kQThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_rotate_q_kernel<T, D>, a);
 }
 
 template <typename T, typename F, int D>
 cudaError_t append_t(const KvAppendArgs& a, cudaStream_t st) {
-    // units of new rows in a page: up to 128 are a small thread block's one each, whole pages four a thread
+    // units of new rows in a page: up to 128 are a small thread block's one each, whole pages two a thread
     const int units = std::min(a.b.max_q, a.page_size) * (D / 16);
     return units <= 128 ? append_units<T, F, D, 1>(a, std::max(64, (units + 31) / 32 * 32), st)
-                        : append_units<T, F, D, 4>(a, std::max(64, (units + 127) / 128 * 32), st);
+                        : append_units<T, F, D, 2>(a, std::max(64, (units + 63) / 64 * 32), st);
 }
 
 template <typename T, typename F, int D>
