@@ -10,22 +10,30 @@
 // largest, weights (times 2^kBias) with 11 bits; weights below 2^-31 of the
 // reference are dropped.
 //
-// One thread block takes 128 rows (token, head of the group) of a sequence and
-// kv head and walks its keys in tiles of 64.  Roles:
-//   4 softmax warps    a thread a row: score row from tensor memory, weights to
-//                      shared memory as f16, rescaling of the output in tensor
-//                      memory when the reference moves, and the epilogue
-//   converter warps    codes from global memory (prefetched two tiles ahead in
-//                      registers) to f16 operand tiles in shared memory, K and
-//                      V in turn, two buffers each; V needs no transpose, its
-//                      operand is MN-major
-//   1 look-up warp     pages' scales to the block constants of the tiles ahead
-//   1 issuing thread   S_i+1 = Q K_i+1^T ahead of O += P_i V_i, so that the
-//                      softmax of one tile runs under the products of others
-// The operand tiles are written by ordinary stores and read by the tensor core:
-// the issuing thread, which has waited for the writers, fences the one against
-// the other.  (A writer's fence would also wait for the loads that it has in
-// flight: 275 us instead of @@ for a prompt of 4096 tokens.)
+// One thread block takes one 128-row tile (head_dim 256), or two, of the rows
+// (token, head of the group) of a sequence and kv head, and walks its keys in
+// tiles of 64.  Roles:
+//   8 softmax warps      a thread a row, two groups of four warps: a row tile
+//                        each, or (head_dim 256) 32 of the tile's keys each,
+//                        agreeing on the reference; scores from tensor memory,
+//                        weights back over them as f16, rescaling of the output
+//                        when the reference moves, the epilogue
+//   4 + 4 converter      codes of K, of V, from global memory (prefetched two
+//     warps              tiles ahead in registers) to f16 operand tiles in
+//                        shared memory, three buffers each; V needs no
+//                        transpose, its operand is MN-major
+//   1 look-up warp       pages' scales to the block constants of the tiles ahead
+//   1 issuing thread     S_i+1 = Q K_i+1^T ahead of O += P_i V_i, so that the
+//                        softmax of one tile runs under the products of others
+// Tensor memory (512 columns): two score tiles of 64 columns a row tile, whose
+// weights take their place; the output; at head_dim 256 the queries too.  The
+// operands that stay (P, and Q of head_dim 256) are there because shared memory
+// bounds this kernel: at head_dim 256 a tile moves 64 KB of converted codes in
+// and 64 KB out, 1024 cycles at 128 bytes, as long as its products take; with Q
+// and P in shared memory it was 224 KB.
+// The converted tiles are written by ordinary stores and read by the tensor
+// core: the issuing thread, which has waited for the writers, fences the one
+// against the other (a writer's fence would also wait for its loads in flight).
 // Every wait is bounded (2 s); a wait that gives up records a code (42..48) in
 // this file's device error word and its role stops.
 #include <algorithm>
@@ -46,18 +54,22 @@ __device__ __forceinline__ void prompt_fail(int code) { atomicCAS(&g_kv_prompt_e
 constexpr int kM = 128, kKeys = 64;
 constexpr int kGroups = kKeys / 16;  // 16-key groups of a tile: one page each
 constexpr int kConst = 4;            // tiles whose block constants are kept
+constexpr int kStages = 3;           // buffers of K tiles, and of V tiles
+constexpr int kSoftWarps = 8, kConvWarps = 4;  // softmax; K's converters, and V's
+constexpr int kThreads = 32 * (kSoftWarps + 2 * kConvWarps + 2);
 constexpr float kLazy = 8.0f;
 constexpr float kBias = 7.0f;        // weights are 2^7 times theirs: at most 2^15
 
 template <int D> struct PCfg {
-    static constexpr int kConvWarps = D == 256 ? 8 : 4;
-    static constexpr int kThreads = 32 * (4 + kConvWarps + 2);
-    static constexpr int kPBufs = D == 256 ? 2 : 1;
-    static constexpr uint32_t kQ = kM * D * 2, kTile = kKeys * D * 2, kP = kM * kKeys * 2;
-    // the operand tiles, then Shared; at head_dim 128 two thread blocks fill an SM's 228 KB to the byte
-    static constexpr uint32_t kData = kQ + 4 * kTile + kPBufs * kP, kSmem = kData + 1024;
-    static constexpr uint32_t kCols = D == 256 ? 512 : 256;  // tensor memory: two score tiles, then the output
-    static constexpr int kBlocks = D == 256 ? 1 : 2;
+    static constexpr int kTiles = D == 256 ? 1 : 2;       // row tiles of a thread block
+    static constexpr int kHalves = 3 - kTiles;            // softmax threads a row
+    static constexpr int kCols = kKeys / kHalves;         // keys of a softmax thread
+    static constexpr bool kQInTmem = D == 256;
+    static constexpr uint32_t kQ = kM * D * 2, kTile = kKeys * D * 2;  // bytes: a row tile's queries, a K or V tile
+    // K tiles, V tiles, then queries; those of tensor memory only pass through K's buffers
+    static constexpr uint32_t kData = 2 * kStages * kTile + (kQInTmem ? 0 : kTiles * kQ), kSmem = kData + 4096;
+    // tensor memory columns: scores (two tiles a row tile), output, queries
+    static constexpr uint32_t kOut = kTiles * 2 * kKeys, kQCol = kOut + kTiles * D;
 };
 
 // Instruction descriptor, kind::f16: f16 A and B, fp32 accumulator.
@@ -66,17 +78,44 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// 32 lanes x 32 columns of 32-bit, registers to tensor memory.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+// 32 lanes x N columns of 32-bit, registers to tensor memory.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]),
-        "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
-        "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
-        "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(taddr)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    tmem_st16(taddr, v);
+    tmem_st16(taddr + 16, v + 16);
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, f16, issued by one thread.  A: lane = row,
+// a column holds two consecutive K elements.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// OR of a predicate over `count` threads at named barrier `id`.
+__device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(count), "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0;
 }
 
 // Block constants of one 16-key group: factor of the scores, their offset
@@ -86,26 +125,73 @@ struct GroupConst {
 };
 
 struct Shared {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2],
-        c_full[kConst], c_empty[kConst], o_full;
+    uint64_t q_full, q_staged, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [row tile][score buffer]
+    uint64_t c_full[kConst], c_empty[kConst], o_full;
     GroupConst consts[kConst][kGroups];
-    float q_scale[kM];
+    float q_scale[2 * kM];
+    float swap[2][kM];  // a row's two threads: maxima, sums
     uint32_t tmem_slot;
 };
-static_assert(sizeof(Shared) <= 1024, "part of kSmem");
+static_assert(sizeof(Shared) <= 4096, "part of kSmem");
+
+// Queries of 16 or 32 rows by one warp, eight at a time: rounded to f16 under a
+// power of two of the row, into a K-major swizzled tile of kM rows at `tile`.
+template <int D>
+__device__ __forceinline__ void stage_queries(const KvAttnArgs& a, uint8_t* tile, float* q_scale, int row0, int n_rows,
+                                              int first, int count, int q0, int h, int G, int lane) {
+    constexpr int E = D / 32;  // channels of a lane
+    for (int r8 = first; r8 < first + count; r8 += 8) {
+        uint32_t raw[8][E / 2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r8 + i, row = row0 + r;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) raw[i][e] = 0;
+            if (r < n_rows) {
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.data) +
+                                           (q0 + row / G) * a.q.token_stride + (h * G + row % G) * a.q.head_stride;
+                memcpy(raw[i], __builtin_assume_aligned(src + E * lane, E * 2), E * 2);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r8 + i;
+            float most = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+                most = fmaxf(most, fmaxf(fabsf(__uint_as_float(raw[i][e] << 16)),
+                                         fabsf(__uint_as_float(raw[i][e] & 0xFFFF0000u))));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+            const int ex = most > 0.0f && most <= 3.402823466e38f
+                               ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126) : 0;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            if (lane == 0) q_scale[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+            uint32_t w[E / 2];
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+                w[e] = pack_f16(__uint_as_float(raw[i][e] << 16) * down, __uint_as_float(raw[i][e] & 0xFFFF0000u) * down);
+            // channel E lane of column block (E lane) / 64
+            const uint32_t byte = (E * lane % 64) * 2;
+            uint8_t* dst = tile + (E * lane / 64) * (kM * 128) + sw128_offset(r, byte >> 4) + (byte & 15);
+            memcpy(__builtin_assume_aligned(dst, E * 2), w, E * 2);
+        }
+    }
+}
 
 template <typename F, int D>
-__global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt_kernel(const KvAttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs a) {
     using C = PCfg<D>;
-    constexpr int CW = C::kConvWarps, PB = C::kPBufs;
+    constexpr int NT = C::kTiles, NC = C::kCols;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles start on 1024-byte boundaries
     Shared& sh = *reinterpret_cast<Shared*>(smem + C::kData);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int seq = blockIdx.y, h = blockIdx.x, G = a.n_q_heads / a.n_kv_heads;
     const int q0 = a.b.cu[seq], qn = a.b.cu[seq + 1] - q0;
-    const int row0 = (static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z)) * kM;  // most keys first
-    const int n_rows = min(kM, qn * G - row0);
+    const int row0 = (static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z)) * (NT * kM);  // most keys first
+    const int n_rows = min(NT * kM, qn * G - row0);
     if (n_rows <= 0) return;
     int len = a.b.kv_lens[seq];
     const int start = len - qn;  // position of the call's first query
@@ -118,282 +204,290 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
     const int first = a.window ? max(0, lo_pos - a.window + 1) / kKeys * kKeys : 0;
     const int end = min(hi_pos + 1, len);
     const int n_tiles = end > first ? (end - first + kKeys - 1) / kKeys : 0;
+    const int active = n_rows > kM ? NT : 1;  // row tiles with rows
 
     if (smem_u32(smem) & 1023u) {
         if (tid == 0) prompt_fail(48);
         return;
     }
-    uint8_t* sq = smem;
-    uint8_t* sk = sq + C::kQ;
-    uint8_t* sv = sk + 2 * C::kTile;
-    uint8_t* sp = sv + 2 * C::kTile;
+    uint8_t* sk = smem;
+    uint8_t* sv = sk + kStages * C::kTile;
+    uint8_t* sq = C::kQInTmem ? nullptr : sv + kStages * C::kTile;
 
+    const int soft = C::kHalves == 2 ? kSoftWarps : 4 * active;  // softmax warps at work
     if (tid == 0) {
-        mbar_init(&sh.q_full, 4);
+        mbar_init(&sh.q_full, soft);
+        mbar_init(&sh.q_staged, soft);
         mbar_init(&sh.o_full, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.k_full[i], CW);
-            mbar_init(&sh.v_full[i], CW);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.k_full[i], kConvWarps);
+            mbar_init(&sh.v_full[i], kConvWarps);
             mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_empty[i], 1);
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_empty[i], 4);
         }
-        for (int i = 0; i < PB; ++i) {
-            mbar_init(&sh.p_full[i], 4);
-            mbar_init(&sh.p_empty[i], 1);
-        }
+        for (int t = 0; t < 2; ++t)
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sh.s_full[t][i], 1);
+                mbar_init(&sh.p_full[t][i], C::kHalves == 2 ? kSoftWarps : 4);
+                mbar_init(&sh.pv_done[t][i], 1);
+            }
         for (int i = 0; i < kConst; ++i) {
             mbar_init(&sh.c_full[i], 1);
-            mbar_init(&sh.c_empty[i], 4);
+            mbar_init(&sh.c_empty[i], soft);
         }
         fence_barrier_init();
     }
-    if (warp == 5 + CW) tmem_alloc(&sh.tmem_slot, C::kCols);
+    constexpr int kLookWarp = kSoftWarps + 2 * kConvWarps, kIssueWarp = kLookWarp + 1;
+    if (warp == kIssueWarp) tmem_alloc(&sh.tmem_slot, 512);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = sh.tmem_slot, t_out = tmem + 2 * kKeys;
-
+    const uint32_t tmem = sh.tmem_slot;
     auto page_of = [&](int key) {  // negative: past the end, or not mapped
         if (key >= end) return -1;
         const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + key / a.page_size];
         return page < a.c.n_pages ? page : -1;
     };
 
-    if (warp < 4) {
-        // ---- queries: 32 rows a warp, rounded to f16 under a power of two of the row
-        constexpr int E = D / 32;  // channels of a lane
-        for (int r8 = 0; r8 < 32; r8 += 8) {
-            uint32_t raw[8][E / 2];
+    if (warp < kSoftWarps) {
+        const int grp = warp >> 2, t = C::kHalves == 2 ? 0 : grp;  // group of four warps; its row tile
+        const int r = tid & (kM - 1);                              // row of the tile
+        const uint32_t t_lane = (32u * (warp & 3)) << 16;
+        const int tile_row0 = row0 + t * kM;
+        if (t < active) {
+            // ---- queries
+            if (C::kQInTmem) {
+                // through the first K buffers: 16 rows a warp, then each thread half of its row
+                static_assert(!C::kQInTmem || 2 * C::kTile >= C::kQ, "two K buffers hold the queries");
+                stage_queries<D>(a, sk, sh.q_scale, row0, n_rows, 32 * (warp & 3) + 16 * grp, 16, q0, h, G, lane);
+                group_sync(1, 32 * kSoftWarps);
+                const uint8_t* src = sk + 2 * grp * (kM * 128);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 32 * warp + r8 + i, row = row0 + r;
+                for (int blk = 0; blk < 2; ++blk) {
+                    uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e) raw[i][e] = 0;
-                if (r < n_rows) {
-                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.data) +
-                                               (q0 + row / G) * a.q.token_stride + (h * G + row % G) * a.q.head_stride;
-                    memcpy(raw[i], __builtin_assume_aligned(src + E * lane, E * 2), E * 2);
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(src + blk * (kM * 128) + sw128_offset(r, c));
+                        w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+                    }
+                    tmem_st32(tmem + t_lane + C::kQCol + 64 * grp + 32 * blk, w);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 32 * warp + r8 + i;
-                float most = 0.0f;
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e)
-                    most = fmaxf(most, fmaxf(fabsf(__uint_as_float(raw[i][e] << 16)),
-                                             fabsf(__uint_as_float(raw[i][e] & 0xFFFF0000u))));
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-                const int ex = most > 0.0f && most <= 3.402823466e38f
-                                   ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126) : 0;
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-                if (lane == 0)
-                    sh.q_scale[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-                uint32_t w[E / 2];
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e)
-                    w[e] = pack_f16(__uint_as_float(raw[i][e] << 16) * down, __uint_as_float(raw[i][e] & 0xFFFF0000u) * down);
-                // channel E lane of column block (E lane) / 64
-                const uint32_t byte = (E * lane % 64) * 2;
-                uint8_t* dst = sq + (E * lane / 64) * (kM * 128) + sw128_offset(r, byte >> 4) + (byte & 15);
-                memcpy(__builtin_assume_aligned(dst, E * 2), w, E * 2);
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full);
-
-        // ---- softmax: thread = row
-        const int r = tid, pos = start + (row0 + r) / G;
-        const float qs = sh.q_scale[r];
-        const int max_lo = a.window ? hi_pos - a.window + 1 : 0;
-        const uint32_t t_lane = (32u * warp) << 16;
-        float m = -INFINITY, l = 0.0f;
-        bool ok = true;
-        for (int i = 0; i < n_tiles; ++i) {
-            const int key = first + i * kKeys, sb = i & 1, pb = i % PB;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_full[sb], (i >> 1) & 1) &&
-                                                   mbar_wait_brief(&sh.c_full[i % kConst], (i / kConst) & 1)))) {
-                if (lane == 0) prompt_fail(42);
-                break;
-            }
-            tc_fence_after_sync();
-            float s[kKeys];
-            tmem_ld64(tmem + t_lane + sb * kKeys, s);
-            GroupConst gc[kGroups];
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) gc[g] = sh.consts[i % kConst][g];
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.s_empty[sb]);
-                mbar_arrive(&sh.c_empty[i % kConst]);
-            }
-            const bool whole = key + kKeys - 1 <= lo_pos && key >= max_lo && key + kKeys <= end;
-#pragma unroll
-            for (int j = 0; j < kKeys; ++j) s[j] = fmaf(s[j], qs * gc[j / 16].ks, gc[j / 16].lv);
-            if (!whole) {
-                const int hi = min(pos, end - 1) - key, lo = a.window ? pos - a.window + 1 - key : 0;
-#pragma unroll
-                for (int j = 0; j < kKeys; ++j) s[j] = j > hi || j < lo ? -INFINITY : s[j];
-            }
-            float tops[4] = {s[0], s[1], s[2], s[3]};  // four chains
-#pragma unroll
-            for (int j = 4; j < kKeys; ++j) tops[j & 3] = fmaxf(tops[j & 3], s[j]);
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            const bool lift = __any_sync(0xffffffffu, top > m + kLazy);
-            float f = 1.0f;
-            if (lift) {
-                const float mn = fmaxf(m, top);
-                f = m == -INFINITY ? 0.0f : exp2_ftz(m - mn);
-                m = mn;
-                l *= f;
-            }
-            const float ref = m == -INFINITY ? 0.0f : m - kBias;
-            uint32_t p[kKeys / 2];
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                float sum = 0.0f;
-                const bool dead = gc[g].inv < 0.0f;  // values of a scale of 0: counted, not added
-#pragma unroll
-                for (int j = 16 * g; j < 16 * g + 16; j += 2) {
-                    const float w0 = exp2_ftz(s[j] - ref), w1 = exp2_ftz(s[j + 1] - ref);
-                    sum += w0 + w1;
-                    p[j / 2] = dead ? 0u : pack_f16(w0, w1);
-                }
-                l = fmaf(sum, fabsf(gc[g].inv), l);
-            }
-            // the buffer's earlier weights were used; with one buffer, that is the last tile's product
-            if (i >= PB && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.p_empty[pb], (i / PB - 1) & 1)))) {
-                if (lane == 0) prompt_fail(43);
-                break;
-            }
-            uint8_t* prow = sp + pb * C::kP;
-#pragma unroll
-            for (int c = 0; c < kKeys / 8; ++c)
-                *reinterpret_cast<uint4*>(prow + sw128_offset(r, c)) =
-                    make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
-            if (lift && i > 0) {  // the output so far, once the products before this tile's are done
-                const int last = i - 1;
-                if (PB > 1 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.p_empty[last % PB], (last / PB) & 1)))) {
-                    if (lane == 0) prompt_fail(43);
-                    break;
-                }
-                tc_fence_after_sync();
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float v[32];
-                    tmem_ld32(t_out + t_lane + c, v);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] *= f;
-                    tmem_st32(t_out + t_lane + c, v);
-                }
+                tmem_wait_st();
                 tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.q_staged);
+                    mbar_arrive(&sh.q_full);
+                }
+            } else {
+                stage_queries<D>(a, sq + t * C::kQ, sh.q_scale + t * kM, tile_row0, n_rows - t * kM, 32 * (warp & 3), 32, q0, h,
+                                 G, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_full);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[pb]);
-        }
-        // ---- epilogue
-        if (ok && n_tiles > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.o_full, 0))) && lane == 0) prompt_fail(44);
-        if (ok) {
-            tc_fence_after_sync();
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            const int row = row0 + r;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                 (static_cast<size_t>(q0 + row / G) * a.n_q_heads + h * G + row % G) * D;
+
+            // ---- softmax: a thread's row, all keys of a tile or 32 of them
+            const int pos = start + (tile_row0 + r) / G;
+            const float qs = sh.q_scale[t * kM + r];
+            const int my_lo = start + tile_row0 / G;  // the row tile's first position
+            const int max_lo = a.window ? hi_pos - a.window + 1 : 0;
+            const uint32_t t_score = tmem + t_lane + t * 2 * kKeys + (C::kHalves == 2 ? grp * NC : 0);
+            const uint32_t t_out = tmem + t_lane + C::kOut + t * D;
+            float m = -INFINITY, l = 0.0f;
+            bool ok = true;
+            for (int i = 0; i < n_tiles; ++i) {
+                const int key = first + i * kKeys + (C::kHalves == 2 ? grp * NC : 0), sb = i & 1;
+                // A wait that gave up is not waited for again, but the warp goes on through the tiles
+                // (with results that are invalid): the barriers between the warps stay complete.
+                if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_full[t][sb], (i >> 1) & 1) &&
+                                                             mbar_wait_brief(&sh.c_full[i % kConst], (i / kConst) & 1))) &&
+                    lane == 0)
+                    prompt_fail(42);
+                tc_fence_after_sync();
+                float s[NC];
+                if (NC == 64) tmem_ld64(t_score + sb * kKeys, s);
+                else tmem_ld32(t_score + sb * kKeys, s);
+                GroupConst gc[NC / 16];
+#pragma unroll
+                for (int g = 0; g < NC / 16; ++g) gc[g] = sh.consts[i % kConst][(C::kHalves == 2 ? grp * (NC / 16) : 0) + g];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.c_empty[i % kConst]);
+#pragma unroll
+                for (int j = 0; j < NC; ++j) s[j] = fmaf(s[j], qs * gc[j / 16].ks, gc[j / 16].lv);
+                if (!(key + NC - 1 <= my_lo && key >= max_lo && key + NC <= end)) {
+                    const int hi = min(pos, end - 1) - key, lo = a.window ? pos - a.window + 1 - key : 0;
+#pragma unroll
+                    for (int j = 0; j < NC; ++j) s[j] = j > hi || j < lo ? -INFINITY : s[j];
+                }
+                float tops[4] = {s[0], s[1], s[2], s[3]};  // four chains
+#pragma unroll
+                for (int j = 4; j < NC; ++j) tops[j & 3] = fmaxf(tops[j & 3], s[j]);
+                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                // whether the reference of any row moves: of the warp, or of both threads of any row
+                const bool lift = C::kHalves == 2 ? group_any(1, 32 * kSoftWarps, top > m + kLazy)
+                                                  : __any_sync(0xffffffffu, top > m + kLazy);
+                float f = 1.0f;
+                if (lift) {
+                    if (C::kHalves == 2) {
+                        sh.swap[grp][r] = top;
+                        group_sync(2, 32 * kSoftWarps);
+                        top = fmaxf(top, sh.swap[grp ^ 1][r]);
+                    }
+                    const float mn = fmaxf(m, top);
+                    f = m == -INFINITY ? 0.0f : exp2_ftz(m - mn);
+                    m = mn;
+                    l *= f;
+                }
+                const float ref = m == -INFINITY ? 0.0f : m - kBias;
+                uint32_t p[NC / 2];
+#pragma unroll
+                for (int g = 0; g < NC / 16; ++g) {
+                    float sum[2] = {0.0f, 0.0f};
+                    const bool dead = gc[g].inv < 0.0f;  // values of a scale of 0: counted, not added
+#pragma unroll
+                    for (int j = 16 * g; j < 16 * g + 16; j += 2) {
+                        const float w0 = exp2_ftz(s[j] - ref), w1 = exp2_ftz(s[j + 1] - ref);
+                        sum[0] += w0;
+                        sum[1] += w1;
+                        p[j / 2] = dead ? 0u : pack_f16(w0, w1);
+                    }
+                    l = fmaf(sum[0] + sum[1], fabsf(gc[g].inv), l);
+                }
+                // over this thread's own scores
+                if (NC == 64) tmem_st32(t_score + sb * kKeys, p);
+                else tmem_st16(t_score + sb * kKeys, p);
+                if (lift && i > 0) {  // the output so far, once the products before this tile's are done
+                    if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pv_done[t][sb ^ 1], ((i - 1) >> 1) & 1))) &&
+                        lane == 0)
+                        prompt_fail(43);
+                    tc_fence_after_sync();
+                    constexpr int W = D / C::kHalves;  // this thread's share of the row
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float v[32];
-                if (n_tiles > 0) tmem_ld32(t_out + t_lane + c, v);
-                if (r < n_rows) {
+                    for (int c = 0; c < W; c += 32) {
+                        float v[32];
+                        uint32_t u[32];
+                        const uint32_t at = t_out + (C::kHalves == 2 ? grp * W : 0) + c;
+                        tmem_ld32(at, v);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float x[8];
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
+                        tmem_st32(at, u);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[t][sb]);
+            }
+            // ---- epilogue
+            if (ok && n_tiles > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.o_full, 0))) && lane == 0)
+                prompt_fail(44);
+            if (C::kHalves == 2) {  // the row's sum
+                group_sync(1, 32 * kSoftWarps);
+                sh.swap[grp][r] = l;
+                group_sync(2, 32 * kSoftWarps);
+                l += sh.swap[grp ^ 1][r];
+            }
+            if (ok) {
+                tc_fence_after_sync();
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const int row = tile_row0 + r;
+                constexpr int W = D / C::kHalves;
+                const int c0 = C::kHalves == 2 ? grp * W : 0;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                     (static_cast<size_t>(q0 + row / G) * a.n_q_heads + h * G + row % G) * D + c0;
+#pragma unroll 1
+                for (int c = 0; c < W; c += 32) {
+                    float v[32];
+                    if (n_tiles > 0) tmem_ld32(t_out + c0 + c, v);
+                    if (t * kM + r < n_rows) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = n_tiles > 0 ? v[e + k] * inv : 0.0f;
-                        Vec16<__nv_bfloat16>::store(out + c + e, x);
+                        for (int e = 0; e < 32; e += 8) {
+                            float x[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) x[k] = n_tiles > 0 ? v[e + k] * inv : 0.0f;
+                            Vec16<__nv_bfloat16>::store(out + c + e, x);
+                        }
                     }
                 }
             }
         }
-    } else if (warp < 4 + CW) {
-        // ---- converters: a thread takes 16-byte chunks c0, c0 + 4, .. of RT rows of a tile
-        constexpr int RT = kKeys / (8 * CW), N = D / 64;
-        const int cw = warp - 4, c0 = lane >> 3;
+    } else if (warp < kLookWarp) {
+        // ---- converters: a thread takes 16-byte chunks c0, c0 + 4, .. of RT rows of K's or V's tiles
+        constexpr int RT = kKeys / (8 * kConvWarps), N = D / 64;
+        const bool is_v = warp >= kSoftWarps + kConvWarps;
+        const int cw = warp & (kConvWarps - 1), c0 = lane >> 3;
+        uint64_t* full = is_v ? sh.v_full : sh.k_full;
+        uint64_t* empty = is_v ? sh.v_empty : sh.k_empty;
+        uint8_t* tiles = is_v ? sv : sk;
+        const uint8_t* codes = (is_v ? a.c.v : a.c.k) + 16 * c0;
         int row[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) row[i] = 8 * (cw + CW * i) + (lane & 7);
-        const uint8_t* codes[2] = {a.c.k, a.c.v};
+        for (int i = 0; i < RT; ++i) row[i] = 8 * (cw + kConvWarps * i) + (lane & 7);
         // Two tiles of codes are in flight in registers: a tile's registers take the codes two tiles
-        // on as soon as they are converted; pages are looked up one tile before that.
-        uint4 raw[2][2][RT][N];
+        // on as soon as they are converted; pages are looked up two tiles before that.
+        uint4 raw[2][RT][N];
         int page[2][RT];
-        auto load = [&](int b, int kv, int i) {  // rows past the end, and of unmapped pages, are zeros
+        auto load = [&](int b, int i) {  // rows past the end, and of unmapped pages, are zeros
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
                 const int key = first + i * kKeys + row[t], pg = page[b][t];
                 const bool take = pg >= 0;
-                const size_t at = take ? ((static_cast<size_t>(pg) * a.n_kv_heads + h) * a.page_size + key % a.page_size) * D
-                                       : 0;
+                const uint8_t* at = codes;
+                if (take) at += ((static_cast<size_t>(pg) * a.n_kv_heads + h) * a.page_size + key % a.page_size) * D;
 #pragma unroll
                 for (int n = 0; n < N; ++n)
-                    raw[b][kv][t][n] = take ? *reinterpret_cast<const uint4*>(codes[kv] + at + 16 * (c0 + 4 * n))
-                                            : make_uint4(0, 0, 0, 0);
+                    raw[b][t][n] = take ? *reinterpret_cast<const uint4*>(at + 64 * n) : make_uint4(0, 0, 0, 0);
             }
         };
         bool ok = true;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + b * kKeys + row[t]);
-        }
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            load(b, 0, b);
-            load(b, 1, b);
-        }
+        for (int b = 0; b < 2; ++b) load(b, b);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + (b + 2) * kKeys + row[t]);
+        if (C::kQInTmem && !is_v) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_staged, 0));  // read out of them
+        int stage = 0, round = 0;
         for (int i0 = 0; ok && i0 < n_tiles; i0 += 2) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int i = i0 + b;
                 if (i >= n_tiles || !ok) break;
+                if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait_brief(&empty[stage], (round - 1) & 1));
+                if (!ok) break;
+                uint8_t* tile = tiles + stage * C::kTile;
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (i >= 2 && ok)
-                        ok = __all_sync(0xffffffffu, mbar_wait_brief(kv ? &sh.v_empty[b] : &sh.k_empty[b], ((i >> 1) - 1) & 1));
-                    if (!ok) break;
-                    uint8_t* tile = (kv ? sv : sk) + b * C::kTile;
+                for (int t = 0; t < RT; ++t)
 #pragma unroll
-                    for (int t = 0; t < RT; ++t)
-#pragma unroll
-                        for (int n = 0; n < N; ++n) {
-                            // 16 codes are two 16-byte chunks of column block n: row of 64 channels, swizzled
-                            const uint4 x = raw[b][kv][t][n];
-                            uint4 lo, hi;
-                            widen_f16<F>(x.x, lo.x, lo.y);
-                            widen_f16<F>(x.y, lo.z, lo.w);
-                            widen_f16<F>(x.z, hi.x, hi.y);
-                            widen_f16<F>(x.w, hi.z, hi.w);
-                            uint8_t* dst = tile + n * (kKeys * 128);
-                            *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0)) = lo;
-                            *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0 + 1)) = hi;
-                        }
-                    load(b, kv, i + 2);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(kv ? &sh.v_full[b] : &sh.k_full[b]);
-                }
+                    for (int n = 0; n < N; ++n) {
+                        // 16 codes are two 16-byte chunks of column block n: row of 64 channels, swizzled
+                        const uint4 x = raw[b][t][n];
+                        uint4 lo, hi;
+                        widen_f16<F>(x.x, lo.x, lo.y);
+                        widen_f16<F>(x.y, lo.z, lo.w);
+                        widen_f16<F>(x.z, hi.x, hi.y);
+                        widen_f16<F>(x.w, hi.z, hi.w);
+                        uint8_t* dst = tile + n * (kKeys * 128);
+                        *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0)) = lo;
+                        *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0 + 1)) = hi;
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[stage]);
+                load(b, i + 2);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + (i + 4) * kKeys + row[t]);
+                if (++stage == kStages) {
+                    stage = 0;
+                    ++round;
+                }
             }
         }
         if (!ok && lane == 0) prompt_fail(45);
-    } else if (warp == 4 + CW) {
+    } else if (warp == kLookWarp) {
         // ---- block constants, kConst tiles of groups at a time
         float vs_low = INFINITY;
         bool ok = true;
@@ -432,45 +526,69 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
     } else if (lane == 0) {
         // ---- issue
         constexpr uint32_t id_s = idesc_f16_f32(kM, kKeys, false), id_o = idesc_f16_f32(kM, D, true);
-        const uint32_t aq = smem_u32(sq), ak = smem_u32(sk), av = smem_u32(sv), ap = smem_u32(sp);
+        const uint32_t ak = smem_u32(sk), av = smem_u32(sv), aq = C::kQInTmem ? 0 : smem_u32(sq);
         bool ok = n_tiles == 0 || mbar_wait_brief(&sh.q_full, 0);
         uint64_t* last = nullptr;
         uint32_t last_par = 0;
+        int ks = 0, kr = 0, vs = 0, vr = 0;  // buffer and round of the next K and V tile
         for (int i = 0; ok && i <= n_tiles; ++i) {
             if (i < n_tiles) {
                 const int b = i & 1;
-                if (!(ok = mbar_wait_brief(&sh.k_full[b], (i >> 1) & 1))) break;
-                if (i >= 2 && !(ok = mbar_wait_brief(&sh.s_empty[b], ((i >> 1) - 1) & 1))) break;
-                tc_fence_after_sync();
+                if (!(ok = mbar_wait_brief(&sh.k_full[ks], kr & 1))) break;
                 fence_proxy_async_smem();
+                for (int t = 0; t < active; ++t) {
+                    // the buffer's last weights were used
+                    if (i >= 2 && !(ok = mbar_wait_brief(&sh.pv_done[t][b], ((i >> 1) - 1) & 1))) break;
+                    tc_fence_after_sync();
+                    const uint32_t d = tmem + (t * 2 + b) * kKeys;
 #pragma unroll
-                for (int n = 0; n < D / 64; ++n) {
-                    const uint64_t da = desc_kmajor_sw128(aq + n * (kM * 128));
-                    const uint64_t db = desc_kmajor_sw128(ak + b * C::kTile + n * (kKeys * 128));
+                    for (int n = 0; n < D / 64; ++n) {
+                        const uint64_t db = desc_kmajor_sw128(ak + ks * C::kTile + n * (kKeys * 128));
+                        const uint64_t da = C::kQInTmem ? 0 : desc_kmajor_sw128(aq + t * C::kQ + n * (kM * 128));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + b * kKeys, da + 2 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
+                        for (int k = 0; k < 4; ++k) {
+                            if (C::kQInTmem)
+                                mma_f16_ta(d, tmem + C::kQCol + 32 * n + 8 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
+                            else
+                                mma_bf16(d, da + 2 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
+                        }
+                    }
+                    mma_commit(&sh.s_full[t][b]);
+                    last = &sh.s_full[t][b];
+                    last_par = (i >> 1) & 1;
                 }
-                mma_commit(&sh.k_empty[b]);
-                mma_commit(&sh.s_full[b]);
-                last = &sh.s_full[b];
-                last_par = (i >> 1) & 1;
+                if (!ok) break;
+                mma_commit(&sh.k_empty[ks]);
+                if (++ks == kStages) {
+                    ks = 0;
+                    ++kr;
+                }
             }
             if (i > 0) {
-                const int j = i - 1, b = j & 1, pb = j % PB;
-                if (!(ok = mbar_wait_brief(&sh.v_full[b], (j >> 1) & 1))) break;
-                if (!(ok = mbar_wait_brief(&sh.p_full[pb], (j / PB) & 1))) break;
-                tc_fence_after_sync();
+                const int j = i - 1, b = j & 1;
+                if (!(ok = mbar_wait_brief(&sh.v_full[vs], vr & 1))) break;
                 fence_proxy_async_smem();
-                const uint64_t da = desc_kmajor_sw128(ap + pb * C::kP);
+                for (int t = 0; t < active; ++t) {
+                    if (!(ok = mbar_wait_brief(&sh.p_full[t][b], (j >> 1) & 1))) break;
+                    tc_fence_after_sync();
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    mma_bf16(t_out, da + 2 * k, desc_mnmajor_sw128(av + b * C::kTile + k * 2048, kKeys * 128), id_o,
-                             (j > 0 || k > 0) ? 1u : 0u);
-                mma_commit(&sh.v_empty[b]);
-                mma_commit(&sh.p_empty[pb]);
-                last = &sh.p_empty[pb];
-                last_par = (j / PB) & 1;
+                    for (int k = 0; k < kKeys / 16; ++k) {
+                        // 16 keys of weights are 8 columns; a softmax thread's keys start at its own scores
+                        const uint32_t pcol = C::kHalves == 2 ? (k >> 1) * NC + (k & 1) * 8 : 8 * k;
+                        mma_f16_ta(tmem + C::kOut + t * D, tmem + (t * 2 + b) * kKeys + pcol,
+                                   desc_mnmajor_sw128(av + vs * C::kTile + k * 2048, kKeys * 128), id_o,
+                                   (j > 0 || k > 0) ? 1u : 0u);
+                    }
+                    mma_commit(&sh.pv_done[t][b]);
+                    last = &sh.pv_done[t][b];
+                    last_par = (j >> 1) & 1;
+                }
+                if (!ok) break;
+                mma_commit(&sh.v_empty[vs]);
+                if (++vs == kStages) {
+                    vs = 0;
+                    ++vr;
+                }
                 if (i == n_tiles) {
                     mma_commit(&sh.o_full);
                     last = &sh.o_full;
@@ -486,7 +604,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, PCfg<D>::kBlocks) kv_prompt
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 5 + CW) tmem_dealloc(tmem, C::kCols);
+    if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
 }
 
 template <typename F, int D>
@@ -495,9 +613,9 @@ cudaError_t prompt_t(const KvAttnArgs& a, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     cudaError_t e = allow_smem(kv_prompt_kernel<F, D>, C::kSmem, ready);
     if (e != cudaSuccess) return e;
-    const long long tiles = (static_cast<long long>(a.b.max_q) * (a.n_q_heads / a.n_kv_heads) + kM - 1) / kM;
+    const long long tiles = (static_cast<long long>(a.b.max_q) * (a.n_q_heads / a.n_kv_heads) + C::kTiles * kM - 1) / (C::kTiles * kM);
     return timed_launch("kv_prompt", st, [&] {
-        kv_prompt_kernel<F, D><<<dim3(a.n_kv_heads, a.b.n_seq, static_cast<unsigned>(tiles)), C::kThreads, C::kSmem, st>>>(a);
+        kv_prompt_kernel<F, D><<<dim3(a.n_kv_heads, a.b.n_seq, static_cast<unsigned>(tiles)), kThreads, C::kSmem, st>>>(a);
         return cudaGetLastError();
     });
 }
