@@ -22,7 +22,8 @@
 //     warps              tiles ahead in registers) to f16 operand tiles in
 //                        shared memory, three buffers each; V needs no
 //                        transpose, its operand is MN-major
-//   1 look-up warp       pages' scales to the block constants of the tiles ahead
+//   2 look-up warps      pages to where the tiles ahead lie, for the converters,
+//                        and pages' scales to block constants, for the softmax
 //   1 issuing thread     S_i+1 = Q K_i+1^T ahead of O += P_i V_i, so that the
 //                        softmax of one tile runs under the products of others
 // Tensor memory (512 columns): two score tiles of 64 columns a row tile, whose
@@ -53,10 +54,10 @@ __device__ __forceinline__ void prompt_fail(int code) { atomicCAS(&g_kv_prompt_e
 
 constexpr int kM = 128, kKeys = 64;
 constexpr int kGroups = kKeys / 16;  // 16-key groups of a tile: one page each
-constexpr int kConst = 4;            // tiles whose block constants are kept
+constexpr int kPass = 32 / kGroups;  // tiles that a look-up warp looks up at a time
 constexpr int kStages = 3;           // buffers of K tiles, and of V tiles
 constexpr int kSoftWarps = 8, kConvWarps = 4;  // softmax; K's converters, and V's
-constexpr int kThreads = 32 * (kSoftWarps + 2 * kConvWarps + 2);
+constexpr int kThreads = 32 * (kSoftWarps + 2 * kConvWarps + 3);
 constexpr float kLazy = 8.0f;
 constexpr float kBias = 7.0f;        // weights are 2^7 times theirs: at most 2^15
 
@@ -127,8 +128,11 @@ struct GroupConst {
 struct Shared {
     uint64_t q_full, q_staged, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [row tile][score buffer]
-    uint64_t c_full[kConst], c_empty[kConst], o_full;
-    GroupConst consts[kConst][kGroups];
+    uint64_t c_full[2], c_empty[2];  // halves of consts
+    uint64_t l_full[2], l_empty[2];  // halves of place
+    uint64_t o_full;
+    GroupConst consts[2 * kPass][kGroups];
+    long long place[2 * kPass][kGroups];  // a group's first code in the cache, or -1
     float q_scale[2 * kM];
     float swap[2][kM];  // a row's two threads: maxima, sums
     uint32_t tmem_slot;
@@ -231,13 +235,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 mbar_init(&sh.p_full[t][i], C::kHalves == 2 ? kSoftWarps : 4);
                 mbar_init(&sh.pv_done[t][i], 1);
             }
-        for (int i = 0; i < kConst; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.c_full[i], 1);
             mbar_init(&sh.c_empty[i], soft);
+            mbar_init(&sh.l_full[i], 1);
+            mbar_init(&sh.l_empty[i], 2 * kConvWarps);
         }
         fence_barrier_init();
     }
-    constexpr int kLookWarp = kSoftWarps + 2 * kConvWarps, kIssueWarp = kLookWarp + 1;
+    constexpr int kPlaceWarp = kSoftWarps + 2 * kConvWarps, kIssueWarp = kPlaceWarp + 2;  // one between: constants
     if (warp == kIssueWarp) tmem_alloc(&sh.tmem_slot, 512);
     tc_fence_before_sync();
     __syncthreads();
@@ -299,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 const int key = first + i * kKeys + (C::kHalves == 2 ? grp * NC : 0), sb = i & 1;
                 // A wait that gave up is not waited for again, but the warp goes on through the tiles
                 // (with results that are invalid): the barriers between the warps stay complete.
-                if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_full[t][sb], (i >> 1) & 1) &&
-                                                             mbar_wait_brief(&sh.c_full[i % kConst], (i / kConst) & 1))) &&
+                if (ok && !(ok = __all_sync(0xffffffffu, (i % kPass || mbar_wait_brief(&sh.c_full[i / kPass & 1], (i / (2 * kPass)) & 1)) &&
+                                                             mbar_wait_brief(&sh.s_full[t][sb], (i >> 1) & 1))) &&
                     lane == 0)
                     prompt_fail(42);
                 tc_fence_after_sync();
@@ -309,9 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 else tmem_ld32(t_score + sb * kKeys, s);
                 GroupConst gc[NC / 16];
 #pragma unroll
-                for (int g = 0; g < NC / 16; ++g) gc[g] = sh.consts[i % kConst][(C::kHalves == 2 ? grp * (NC / 16) : 0) + g];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.c_empty[i % kConst]);
+                for (int g = 0; g < NC / 16; ++g) gc[g] = sh.consts[i % (2 * kPass)][(C::kHalves == 2 ? grp * (NC / 16) : 0) + g];
 #pragma unroll
                 for (int j = 0; j < NC; ++j) s[j] = fmaf(s[j], qs * gc[j / 16].ks, gc[j / 16].lv);
                 if (!(key + NC - 1 <= my_lo && key >= max_lo && key + NC <= end)) {
@@ -376,7 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 tmem_wait_st();
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[t][sb]);
+                if (lane == 0) {
+                    mbar_arrive(&sh.p_full[t][sb]);
+                    if (i % kPass == kPass - 1) mbar_arrive(&sh.c_empty[i / kPass & 1]);
+                }
             }
             // ---- epilogue
             if (ok && n_tiles > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.o_full, 0))) && lane == 0)
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 }
             }
         }
-    } else if (warp < kLookWarp) {
+    } else if (warp < kPlaceWarp) {
         // ---- converters: a thread takes 16-byte chunks c0, c0 + 4, .. of RT rows of K's or V's tiles
         constexpr int RT = kKeys / (8 * kConvWarps), N = D / 64;
         const bool is_v = warp >= kSoftWarps + kConvWarps;
@@ -424,32 +431,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
 #pragma unroll
         for (int i = 0; i < RT; ++i) row[i] = 8 * (cw + kConvWarps * i) + (lane & 7);
         // Two tiles of codes are in flight in registers: a tile's registers take the codes two tiles
-        // on as soon as they are converted; pages are looked up two tiles before that.
+        // on as soon as they are converted.
         uint4 raw[2][RT][N];
-        int page[2][RT];
+        bool ok = true;
         auto load = [&](int b, int i) {  // rows past the end, and of unmapped pages, are zeros
+            if (i >= n_tiles) return;
+            const int hb = i / kPass & 1;
+            if (i % kPass == 0 && ok)
+                ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.l_full[hb], (i / (2 * kPass)) & 1));
+            long long at[RT];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const int key = first + i * kKeys + row[t], pg = page[b][t];
-                const bool take = pg >= 0;
-                const uint8_t* at = codes;
-                if (take) at += ((static_cast<size_t>(pg) * a.n_kv_heads + h) * a.page_size + key % a.page_size) * D;
+                at[t] = sh.place[i % (2 * kPass)][row[t] >> 4];
+                at[t] = at[t] >= 0 && first + i * kKeys + row[t] < end ? at[t] + (row[t] & 15) * D : -1;
+            }
+            if (i % kPass == kPass - 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.l_empty[hb]);
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
 #pragma unroll
                 for (int n = 0; n < N; ++n)
-                    raw[b][t][n] = take ? *reinterpret_cast<const uint4*>(at + 64 * n) : make_uint4(0, 0, 0, 0);
-            }
+                    raw[b][t][n] = at[t] >= 0 ? *reinterpret_cast<const uint4*>(codes + at[t] + 64 * n) : make_uint4(0, 0, 0, 0);
         };
-        bool ok = true;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + b * kKeys + row[t]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) load(b, b);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + (b + 2) * kKeys + row[t]);
         if (C::kQInTmem && !is_v) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_staged, 0));  // read out of them
         int stage = 0, round = 0;
         for (int i0 = 0; ok && i0 < n_tiles; i0 += 2) {
@@ -478,8 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[stage]);
                 load(b, i + 2);
-#pragma unroll
-                for (int t = 0; t < RT; ++t) page[b][t] = page_of(first + (i + 4) * kKeys + row[t]);
                 if (++stage == kStages) {
                     stage = 0;
                     ++round;
@@ -487,18 +492,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             }
         }
         if (!ok && lane == 0) prompt_fail(45);
-    } else if (warp == kLookWarp) {
-        // ---- block constants, kConst tiles of groups at a time
+    } else if (warp < kIssueWarp) {
+        // ---- look-ups, kPass tiles of groups at a time, two passes ahead of their readers
+        const bool place = warp == kPlaceWarp;
+        uint64_t *full = place ? sh.l_full : sh.c_full, *empty = place ? sh.l_empty : sh.c_empty;
         float vs_low = INFINITY;
         bool ok = true;
-        for (int i0 = 0; ok && i0 < n_tiles; i0 += kConst) {
-            const int key = first + i0 * kKeys + 16 * lane;
+        for (int i0 = 0, pass = 0; ok && i0 < n_tiles; i0 += kPass, ++pass) {
+            const int key = first + i0 * kKeys + 16 * lane, pg = page_of(key), hb = pass & 1;
+            const size_t block = static_cast<size_t>(max(pg, 0)) * a.n_kv_heads + h;
             GroupConst g{0.0f, -INFINITY, 1.0f};
-            float vs = 1.0f;
-            if (lane < kConst * kGroups) {
-                const int pg = page_of(key);
+            if (!place) {
+                float vs = 1.0f;
                 if (pg >= 0) {
-                    const size_t block = static_cast<size_t>(pg) * a.n_kv_heads + h;
                     g.ks = a.c.k_scale[block];
                     vs = a.c.v_scale[block];
                     g.lv = 0.0f;
@@ -506,22 +512,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 } else if (key < end && (!a.window || key + 15 > lo_pos - a.window)) {
                     prompt_fail(kKvErrTable);
                 }
-            }
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
-            const bool zero = vs == 0.0f;  // such a group is given the smallest scale in sight, and a mark
-            if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
-            g.lv += log2f(vs);
-            g.inv = (zero ? -1.0f : 1.0f) / vs;
-            for (int q = 0; q < kConst && i0 + q < n_tiles; ++q) {
-                if (i0 > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.c_empty[q], (i0 / kConst - 1) & 1)))) {
-                    if (lane == 0) prompt_fail(45);
-                    break;
-                }
-                if (lane / kGroups == q) sh.consts[q][lane % kGroups] = g;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.c_full[q]);
+                for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
+                const bool zero = vs == 0.0f;  // such a group is given the smallest scale in sight, and a mark
+                if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
+                g.lv += log2f(vs);
+                g.inv = (zero ? -1.0f : 1.0f) / vs;
             }
+            if (pass >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&empty[hb], ((pass >> 1) - 1) & 1)))) {
+                if (lane == 0) prompt_fail(45);
+                break;
+            }
+            const int slot = hb * kPass + lane / kGroups;
+            if (place)
+                sh.place[slot][lane % kGroups] =
+                    pg >= 0 ? static_cast<long long>((block * a.page_size + key % a.page_size) * D) : -1;
+            else
+                sh.consts[slot][lane % kGroups] = g;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[hb]);
         }
     } else if (lane == 0) {
         // ---- issue
