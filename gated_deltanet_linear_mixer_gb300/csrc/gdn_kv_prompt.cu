@@ -24,8 +24,8 @@
 //                        transpose, its operand is MN-major
 //   2 look-up warps      pages to where the tiles ahead lie, for the converters,
 //                        and pages' scales to block constants, for the softmax
-//   1 issuing thread     S_i+1 = Q K_i+1^T ahead of O += P_i V_i, so that the
-//                        softmax of one tile runs under the products of others
+//   2 issuing threads    S = Q K^T, a tile ahead, and O += P V: one of them
+//                        waits and fences while the other's products run
 // Tensor memory (512 columns): two score tiles of 64 columns a row tile, whose
 // weights take their place; the output; at head_dim 256 the queries too.  The
 // operands that stay (P, and Q of head_dim 256) are there because shared memory
@@ -33,7 +33,7 @@
 // and 64 KB out, 1024 cycles at 128 bytes, as long as its products take; with Q
 // and P in shared memory it was 224 KB.
 // The converted tiles are written by ordinary stores and read by the tensor
-// core: the issuing thread, which has waited for the writers, fences the one
+// core: an issuing thread, which has waited for the writers, fences the one
 // against the other (a writer's fence would also wait for its loads in flight).
 // Every wait is bounded (2 s); a wait that gives up records a code (42..48) in
 // this file's device error word and its role stops.
@@ -57,7 +57,7 @@ constexpr int kGroups = kKeys / 16;  // 16-key groups of a tile: one page each
 constexpr int kPass = 32 / kGroups;  // tiles that a look-up warp looks up at a time
 constexpr int kStages = 3;           // buffers of K tiles, and of V tiles
 constexpr int kSoftWarps = 8, kConvWarps = 4;  // softmax; K's converters, and V's
-constexpr int kThreads = 32 * (kSoftWarps + 2 * kConvWarps + 3);
+constexpr int kThreads = 32 * (kSoftWarps + 2 * kConvWarps + 4);
 constexpr float kLazy = 8.0f;
 constexpr float kBias = 7.0f;        // weights are 2^7 times theirs: at most 2^15
 
@@ -533,26 +533,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             if (lane == 0) mbar_arrive(&full[hb]);
         }
     } else if (lane == 0) {
-        // ---- issue
+        // ---- issue: scores by one warp's thread, outputs by the next one's
+        const bool scores = warp == kIssueWarp;
         constexpr uint32_t id_s = idesc_f16_f32(kM, kKeys, false), id_o = idesc_f16_f32(kM, D, true);
         const uint32_t ak = smem_u32(sk), av = smem_u32(sv), aq = C::kQInTmem ? 0 : smem_u32(sq);
-        bool ok = n_tiles == 0 || mbar_wait_brief(&sh.q_full, 0);
+        bool ok = n_tiles == 0 || !scores || mbar_wait_brief(&sh.q_full, 0);
         uint64_t* last = nullptr;
         uint32_t last_par = 0;
-        int ks = 0, kr = 0, vs = 0, vr = 0;  // buffer and round of the next K and V tile
-        for (int i = 0; ok && i <= n_tiles; ++i) {
-            if (i < n_tiles) {
-                const int b = i & 1;
-                if (!(ok = mbar_wait_brief(&sh.k_full[ks], kr & 1))) break;
-                fence_proxy_async_smem();
-                for (int t = 0; t < active; ++t) {
-                    // the buffer's last weights were used
-                    if (i >= 2 && !(ok = mbar_wait_brief(&sh.pv_done[t][b], ((i >> 1) - 1) & 1))) break;
-                    tc_fence_after_sync();
-                    const uint32_t d = tmem + (t * 2 + b) * kKeys;
+        int stage = 0, round = 0;  // buffer and round of the tile
+        for (int i = 0; ok && i < n_tiles; ++i) {
+            const int b = i & 1;
+            if (!(ok = mbar_wait_brief(scores ? &sh.k_full[stage] : &sh.v_full[stage], round & 1))) break;
+            fence_proxy_async_smem();
+            for (int t = 0; t < active; ++t) {
+                // scores: the score tile's last weights were used; outputs: its weights are there
+                if (scores ? i >= 2 && !(ok = mbar_wait_brief(&sh.pv_done[t][b], ((i >> 1) - 1) & 1))
+                           : !(ok = mbar_wait_brief(&sh.p_full[t][b], (i >> 1) & 1)))
+                    break;
+                tc_fence_after_sync();
+                const uint32_t d = tmem + (t * 2 + b) * kKeys;
+                if (scores) {
 #pragma unroll
                     for (int n = 0; n < D / 64; ++n) {
-                        const uint64_t db = desc_kmajor_sw128(ak + ks * C::kTile + n * (kKeys * 128));
+                        const uint64_t db = desc_kmajor_sw128(ak + stage * C::kTile + n * (kKeys * 128));
                         const uint64_t da = C::kQInTmem ? 0 : desc_kmajor_sw128(aq + t * C::kQ + n * (kM * 128));
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -564,49 +567,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                     }
                     mma_commit(&sh.s_full[t][b]);
                     last = &sh.s_full[t][b];
-                    last_par = (i >> 1) & 1;
-                }
-                if (!ok) break;
-                mma_commit(&sh.k_empty[ks]);
-                if (++ks == kStages) {
-                    ks = 0;
-                    ++kr;
-                }
-            }
-            if (i > 0) {
-                const int j = i - 1, b = j & 1;
-                if (!(ok = mbar_wait_brief(&sh.v_full[vs], vr & 1))) break;
-                fence_proxy_async_smem();
-                for (int t = 0; t < active; ++t) {
-                    if (!(ok = mbar_wait_brief(&sh.p_full[t][b], (j >> 1) & 1))) break;
-                    tc_fence_after_sync();
+                } else {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k) {
                         // 16 keys of weights are 8 columns; a softmax thread's keys start at its own scores
                         const uint32_t pcol = C::kHalves == 2 ? (k >> 1) * NC + (k & 1) * 8 : 8 * k;
-                        mma_f16_ta(tmem + C::kOut + t * D, tmem + (t * 2 + b) * kKeys + pcol,
-                                   desc_mnmajor_sw128(av + vs * C::kTile + k * 2048, kKeys * 128), id_o,
-                                   (j > 0 || k > 0) ? 1u : 0u);
+                        mma_f16_ta(tmem + C::kOut + t * D, d + pcol,
+                                   desc_mnmajor_sw128(av + stage * C::kTile + k * 2048, kKeys * 128), id_o,
+                                   (i > 0 || k > 0) ? 1u : 0u);
                     }
                     mma_commit(&sh.pv_done[t][b]);
                     last = &sh.pv_done[t][b];
-                    last_par = (j >> 1) & 1;
                 }
-                if (!ok) break;
-                mma_commit(&sh.v_empty[vs]);
-                if (++vs == kStages) {
-                    vs = 0;
-                    ++vr;
-                }
-                if (i == n_tiles) {
-                    mma_commit(&sh.o_full);
-                    last = &sh.o_full;
-                    last_par = 0;
-                }
+                last_par = (i >> 1) & 1;
+            }
+            if (!ok) break;
+            mma_commit(scores ? &sh.k_empty[stage] : &sh.v_empty[stage]);
+            if (!scores && i == n_tiles - 1) {
+                mma_commit(&sh.o_full);
+                last = &sh.o_full;
+                last_par = 0;
+            }
+            if (++stage == kStages) {
+                stage = 0;
+                ++round;
             }
         }
         if (!ok) prompt_fail(46);
-        // nothing of this thread block is in flight when its tensor memory is freed
+        // nothing of this thread is in flight when the tensor memory is freed
         if (last && !mbar_wait_brief(last, last_par)) prompt_fail(47);
     }
     __syncwarp();
