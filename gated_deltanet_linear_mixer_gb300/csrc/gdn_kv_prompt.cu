@@ -16,7 +16,7 @@
 //   8 softmax warps      a thread a row, two groups of four warps: a row tile
 //                        each, or (head_dim 256) 32 of the tile's keys each,
 //                        agreeing on the reference; scores from tensor memory,
-//                        weights back over them as f16, rescaling of the output
+//                        weights back to it as f16, rescaling of the output
 //                        when the reference moves, the epilogue
 //   4 + 4 converter      codes of K, of V, from global memory (prefetched two
 //     warps              tiles ahead in registers) to f16 operand tiles in
@@ -26,12 +26,13 @@
 //                        and pages' scales to block constants, for the softmax
 //   2 issuing threads    S = Q K^T, a tile ahead, and O += P V: one of them
 //                        waits and fences while the other's products run
-// Tensor memory (512 columns): two score tiles of 64 columns a row tile, whose
-// weights take their place; the output; at head_dim 256 the queries too.  The
-// operands that stay (P, and Q of head_dim 256) are there because shared memory
-// bounds this kernel: at head_dim 256 a tile moves 64 KB of converted codes in
-// and 64 KB out, 1024 cycles at 128 bytes, as long as its products take; with Q
-// and P in shared memory it was 224 KB.
+// Tensor memory (512 columns): a score tile of 64 columns a row tile, read into
+// registers at once so that the next one can follow; two tiles of weights, f16,
+// 32 columns each; the output; at head_dim 256 the queries too.  The operands
+// that stay (P, and Q of head_dim 256) are there to spare shared memory, which
+// at head_dim 256 moves 64 KB of converted codes in and 64 KB out a tile, 1024
+// cycles at 128 bytes, as long as the tile's products take; with Q and P in
+// shared memory it was 224 KB.
 // The converted tiles are written by ordinary stores and read by the tensor
 // core: an issuing thread, which has waited for the writers, fences the one
 // against the other (a writer's fence would also wait for its loads in flight).
@@ -69,8 +70,8 @@ template <int D> struct PCfg {
     static constexpr uint32_t kQ = kM * D * 2, kTile = kKeys * D * 2;  // bytes: a row tile's queries, a K or V tile
     // K tiles, V tiles, then queries; those of tensor memory only pass through K's buffers
     static constexpr uint32_t kData = 2 * kStages * kTile + (kQInTmem ? 0 : kTiles * kQ), kSmem = kData + 4096;
-    // tensor memory columns: scores (two tiles a row tile), output, queries
-    static constexpr uint32_t kOut = kTiles * 2 * kKeys, kQCol = kOut + kTiles * D;
+    // tensor memory columns: scores, weights (two tiles a row tile), output, queries
+    static constexpr uint32_t kWeights = kTiles * kKeys, kOut = 2 * kWeights, kQCol = kOut + kTiles * D;
 };
 
 // Instruction descriptor, kind::f16: f16 A and B, fp32 accumulator.
@@ -127,7 +128,7 @@ struct GroupConst {
 
 struct Shared {
     uint64_t q_full, q_staged, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [row tile][score buffer]
+    uint64_t s_full[2], s_empty[2], p_full[2][2], pv_done[2][2];  // of a row tile (and a buffer of weights)
     uint64_t c_full[2], c_empty[2];  // halves of consts
     uint64_t l_full[2], l_empty[2];  // halves of place
     uint64_t o_full;
@@ -229,12 +230,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_empty[i], 1);
         }
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.s_empty[t], C::kHalves == 2 ? kSoftWarps : 4);
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&sh.s_full[t][i], 1);
                 mbar_init(&sh.p_full[t][i], C::kHalves == 2 ? kSoftWarps : 4);
                 mbar_init(&sh.pv_done[t][i], 1);
             }
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.c_full[i], 1);
             mbar_init(&sh.c_empty[i], soft);
@@ -297,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             const float qs = sh.q_scale[t * kM + r];
             const int my_lo = start + tile_row0 / G;  // the row tile's first position
             const int max_lo = a.window ? hi_pos - a.window + 1 : 0;
-            const uint32_t t_score = tmem + t_lane + t * 2 * kKeys + (C::kHalves == 2 ? grp * NC : 0);
+            const uint32_t t_score = tmem + t_lane + t * kKeys + (C::kHalves == 2 ? grp * NC : 0);
+            const uint32_t t_weight = tmem + t_lane + C::kWeights + t * kKeys + (C::kHalves == 2 ? grp * NC / 2 : 0);
             const uint32_t t_out = tmem + t_lane + C::kOut + t * D;
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
@@ -306,13 +310,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 // A wait that gave up is not waited for again, but the warp goes on through the tiles
                 // (with results that are invalid): the barriers between the warps stay complete.
                 if (ok && !(ok = __all_sync(0xffffffffu, (i % kPass || mbar_wait_brief(&sh.c_full[i / kPass & 1], (i / (2 * kPass)) & 1)) &&
-                                                             mbar_wait_brief(&sh.s_full[t][sb], (i >> 1) & 1))) &&
+                                                             mbar_wait_brief(&sh.s_full[t], i & 1))) &&
                     lane == 0)
                     prompt_fail(42);
                 tc_fence_after_sync();
                 float s[NC];
-                if (NC == 64) tmem_ld64(t_score + sb * kKeys, s);
-                else tmem_ld32(t_score + sb * kKeys, s);
+                if (NC == 64) tmem_ld64(t_score, s);
+                else tmem_ld32(t_score, s);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_empty[t]);  // the next tile's scores may come
                 GroupConst gc[NC / 16];
 #pragma unroll
                 for (int g = 0; g < NC / 16; ++g) gc[g] = sh.consts[i % (2 * kPass)][(C::kHalves == 2 ? grp * (NC / 16) : 0) + g];
@@ -357,9 +364,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                     }
                     l = fmaf(sum[0] + sum[1], fabsf(gc[g].inv), l);
                 }
-                // over this thread's own scores
-                if (NC == 64) tmem_st32(t_score + sb * kKeys, p);
-                else tmem_st16(t_score + sb * kKeys, p);
+                // the buffer's last weights were used
+                if (ok && i >= 2 &&
+                    !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pv_done[t][sb], ((i >> 1) - 1) & 1))) && lane == 0)
+                    prompt_fail(43);
+                tc_fence_after_sync();
+                if (NC == 64) tmem_st32(t_weight + sb * (kKeys / 2), p);
+                else tmem_st16(t_weight + sb * (kKeys / 2), p);
                 if (lift && i > 0) {  // the output so far, once the products before this tile's are done
                     if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pv_done[t][sb ^ 1], ((i - 1) >> 1) & 1))) &&
                         lane == 0)
@@ -546,12 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             if (!(ok = mbar_wait_brief(scores ? &sh.k_full[stage] : &sh.v_full[stage], round & 1))) break;
             fence_proxy_async_smem();
             for (int t = 0; t < active; ++t) {
-                // scores: the score tile's last weights were used; outputs: its weights are there
-                if (scores ? i >= 2 && !(ok = mbar_wait_brief(&sh.pv_done[t][b], ((i >> 1) - 1) & 1))
+                // scores: the last ones were read; outputs: the weights are there
+                if (scores ? i >= 1 && !(ok = mbar_wait_brief(&sh.s_empty[t], (i - 1) & 1))
                            : !(ok = mbar_wait_brief(&sh.p_full[t][b], (i >> 1) & 1)))
                     break;
                 tc_fence_after_sync();
-                const uint32_t d = tmem + (t * 2 + b) * kKeys;
                 if (scores) {
 #pragma unroll
                     for (int n = 0; n < D / 64; ++n) {
@@ -560,26 +570,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             if (C::kQInTmem)
-                                mma_f16_ta(d, tmem + C::kQCol + 32 * n + 8 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
+                                mma_f16_ta(tmem + t * kKeys, tmem + C::kQCol + 32 * n + 8 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
                             else
-                                mma_bf16(d, da + 2 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
+                                mma_bf16(tmem + t * kKeys, da + 2 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
                         }
                     }
-                    mma_commit(&sh.s_full[t][b]);
-                    last = &sh.s_full[t][b];
+                    mma_commit(&sh.s_full[t]);
+                    last = &sh.s_full[t];
+                    last_par = i & 1;
                 } else {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k) {
-                        // 16 keys of weights are 8 columns; a softmax thread's keys start at its own scores
-                        const uint32_t pcol = C::kHalves == 2 ? (k >> 1) * NC + (k & 1) * 8 : 8 * k;
-                        mma_f16_ta(tmem + C::kOut + t * D, d + pcol,
+                    for (int k = 0; k < kKeys / 16; ++k)  // 16 keys of weights are 8 columns
+                        mma_f16_ta(tmem + C::kOut + t * D, tmem + C::kWeights + t * kKeys + b * (kKeys / 2) + 8 * k,
                                    desc_mnmajor_sw128(av + stage * C::kTile + k * 2048, kKeys * 128), id_o,
                                    (i > 0 || k > 0) ? 1u : 0u);
-                    }
                     mma_commit(&sh.pv_done[t][b]);
                     last = &sh.pv_done[t][b];
+                    last_par = (i >> 1) & 1;
                 }
-                last_par = (i >> 1) & 1;
             }
             if (!ok) break;
             mma_commit(scores ? &sh.k_empty[stage] : &sh.v_empty[stage]);
