@@ -430,41 +430,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             }
         }
     } else if (warp < kPlaceWarp) {
-        // ---- converters: a thread takes 16-byte chunks c0, c0 + 4, .. of RT rows of K's or V's tiles
-        constexpr int RT = kKeys / (8 * kConvWarps), N = D / 64;
+        // ---- converters: a warp takes 16 rows of K's or V's tiles, one 16-key group.  A load covers
+        // whole 128-byte lines (4 rows of 128 bytes: a load of 8 half lines took eight times the
+        // cycles of the load pipe), 8 neighbouring lanes two rows of one block of 64 channels, whose
+        // swizzled chunks lie in different banks.
+        constexpr int RS = D == 64 ? 8 : 4, RJ = 16 / RS, P = D == 256 ? 2 : 1;  // rows a load, loads of 16 rows
         const bool is_v = warp >= kSoftWarps + kConvWarps;
-        const int cw = warp & (kConvWarps - 1), c0 = lane >> 3;
+        const int cw = warp & (kConvWarps - 1);
+        const int r_in = D == 64 ? lane >> 2 : ((lane >> 2) & 1) | (lane >> 4) << 1;
+        const int ch = D == 64 ? lane & 3 : (lane & 3) | ((lane >> 3) & 1) << 2;  // 16-byte chunk of a row
         uint64_t* full = is_v ? sh.v_full : sh.k_full;
         uint64_t* empty = is_v ? sh.v_empty : sh.k_empty;
         uint8_t* tiles = is_v ? sv : sk;
-        const uint8_t* codes = (is_v ? a.c.v : a.c.k) + 16 * c0;
-        int row[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) row[i] = 8 * (cw + kConvWarps * i) + (lane & 7);
+        const uint8_t* codes = (is_v ? a.c.v : a.c.k) + r_in * D + 16 * ch;
         // Two tiles of codes are in flight in registers: a tile's registers take the codes two tiles
         // on as soon as they are converted.
-        uint4 raw[2][RT][N];
+        uint4 raw[2][RJ][P];
         bool ok = true;
         auto load = [&](int b, int i) {  // rows past the end, and of unmapped pages, are zeros
             if (i >= n_tiles) return;
             const int hb = i / kPass & 1;
             if (i % kPass == 0 && ok)
                 ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.l_full[hb], (i / (2 * kPass)) & 1));
-            long long at[RT];
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                at[t] = sh.place[i % (2 * kPass)][row[t] >> 4];
-                at[t] = at[t] >= 0 && first + i * kKeys + row[t] < end ? at[t] + (row[t] & 15) * D : -1;
-            }
+            const long long at = sh.place[i % (2 * kPass)][cw];
+            const int left = at >= 0 ? end - (first + i * kKeys + 16 * cw + r_in) : 0;  // keys from this lane's first row on
             if (i % kPass == kPass - 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.l_empty[hb]);
             }
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
+            for (int j = 0; j < RJ; ++j)
 #pragma unroll
-                for (int n = 0; n < N; ++n)
-                    raw[b][t][n] = at[t] >= 0 ? *reinterpret_cast<const uint4*>(codes + at[t] + 64 * n) : make_uint4(0, 0, 0, 0);
+                for (int q = 0; q < P; ++q)
+                    raw[b][j][q] = RS * j < left ? *reinterpret_cast<const uint4*>(codes + at + RS * j * D + 128 * q)
+                                                 : make_uint4(0, 0, 0, 0);
         };
 #pragma unroll
         for (int b = 0; b < 2; ++b) load(b, b);
@@ -479,19 +478,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 if (!ok) break;
                 uint8_t* tile = tiles + stage * C::kTile;
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
+                for (int j = 0; j < RJ; ++j)
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        // 16 codes are two 16-byte chunks of column block n: row of 64 channels, swizzled
-                        const uint4 x = raw[b][t][n];
+                    for (int q = 0; q < P; ++q) {
+                        // 16 codes are two 16-byte chunks of a row of 64 channels, swizzled
+                        const uint4 x = raw[b][j][q];
                         uint4 lo, hi;
                         widen_f16<F>(x.x, lo.x, lo.y);
                         widen_f16<F>(x.y, lo.z, lo.w);
                         widen_f16<F>(x.z, hi.x, hi.y);
                         widen_f16<F>(x.w, hi.z, hi.w);
-                        uint8_t* dst = tile + n * (kKeys * 128);
-                        *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0)) = lo;
-                        *reinterpret_cast<uint4*>(dst + sw128_offset(row[t], 2 * c0 + 1)) = hi;
+                        const int row = 16 * cw + RS * j + r_in;
+                        uint8_t* dst = tile + (2 * q + (ch >> 2)) * (kKeys * 128);
+                        *reinterpret_cast<uint4*>(dst + sw128_offset(row, 2 * (ch & 3))) = lo;
+                        *reinterpret_cast<uint4*>(dst + sw128_offset(row, 2 * (ch & 3) + 1)) = hi;
                     }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[stage]);
