@@ -24,7 +24,7 @@
 //                        transpose, its operand is MN-major
 //   2 look-up warps      pages to where the tiles ahead lie, for the converters,
 //                        and pages' scales to block constants, for the softmax
-//   2 issuing threads    S = Q K^T, a tile ahead, and O += P V: one of them
+//   2 issuing warps      S = Q K^T, a tile ahead, and O += P V: one of them
 //                        waits and fences while the other's products run
 // Tensor memory (512 columns): a score tile of 64 columns a row tile, read into
 // registers at once so that the next one can follow; two tiles of weights, f16,
@@ -106,6 +106,17 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // OR of a predicate over `count` threads at named barrier `id`.
 __device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool x) {
     uint32_t r;
@@ -140,48 +151,49 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 4096, "part of kSmem");
 
-// Queries of 16 or 32 rows by one warp, eight at a time: rounded to f16 under a
-// power of two of the row, into a K-major swizzled tile of kM rows at `tile`.
-template <int D>
+// Queries of ROWS rows by one warp, all loads in flight at once: rounded to f16
+// under a power of two of the row, into a K-major swizzled tile of kM rows.
+template <int D, int ROWS>
 __device__ __forceinline__ void stage_queries(const KvAttnArgs& a, uint8_t* tile, float* q_scale, int row0, int n_rows,
-                                              int first, int count, int q0, int h, int G, int lane) {
+                                              int first, int q0, int h, int G, int lane) {
     constexpr int E = D / 32;  // channels of a lane
-    for (int r8 = first; r8 < first + count; r8 += 8) {
-        uint32_t raw[8][E / 2];
+    uint32_t raw[ROWS][E / 2];
+    int tok = (row0 + first) / G, g = (row0 + first) % G;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = r8 + i, row = row0 + r;
+    for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e) raw[i][e] = 0;
-            if (r < n_rows) {
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.data) +
-                                           (q0 + row / G) * a.q.token_stride + (h * G + row % G) * a.q.head_stride;
-                memcpy(raw[i], __builtin_assume_aligned(src + E * lane, E * 2), E * 2);
-            }
+        for (int e = 0; e < E / 2; ++e) raw[i][e] = 0;
+        if (first + i < n_rows) {
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.data) + (q0 + tok) * a.q.token_stride +
+                                       (h * G + g) * a.q.head_stride;
+            memcpy(raw[i], __builtin_assume_aligned(src + E * lane, E * 2), E * 2);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = r8 + i;
-            float most = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-                most = fmaxf(most, fmaxf(fabsf(__uint_as_float(raw[i][e] << 16)),
-                                         fabsf(__uint_as_float(raw[i][e] & 0xFFFF0000u))));
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-            const int ex = most > 0.0f && most <= 3.402823466e38f
-                               ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126) : 0;
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-            if (lane == 0) q_scale[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-            uint32_t w[E / 2];
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-                w[e] = pack_f16(__uint_as_float(raw[i][e] << 16) * down, __uint_as_float(raw[i][e] & 0xFFFF0000u) * down);
-            // channel E lane of column block (E lane) / 64
-            const uint32_t byte = (E * lane % 64) * 2;
-            uint8_t* dst = tile + (E * lane / 64) * (kM * 128) + sw128_offset(r, byte >> 4) + (byte & 15);
-            memcpy(__builtin_assume_aligned(dst, E * 2), w, E * 2);
+        if (++g == G) {
+            g = 0;
+            ++tok;
         }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = first + i;
+        float most = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(raw[i][e] << 16)), fabsf(__uint_as_float(raw[i][e] & 0xFFFF0000u))));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+        const int ex = most > 0.0f && most <= 3.402823466e38f
+                           ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126) : 0;
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        if (lane == 0) q_scale[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        uint32_t w[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+            w[e] = pack_f16(__uint_as_float(raw[i][e] << 16) * down, __uint_as_float(raw[i][e] & 0xFFFF0000u) * down);
+        // channel E lane of column block (E lane) / 64
+        const uint32_t byte = (E * lane % 64) * 2;
+        uint8_t* dst = tile + (E * lane / 64) * (kM * 128) + sw128_offset(r, byte >> 4) + (byte & 15);
+        memcpy(__builtin_assume_aligned(dst, E * 2), w, E * 2);
     }
 }
 
@@ -268,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             if (C::kQInTmem) {
                 // through the first K buffers: 16 rows a warp, then each thread half of its row
                 static_assert(!C::kQInTmem || 2 * C::kTile >= C::kQ, "two K buffers hold the queries");
-                stage_queries<D>(a, sk, sh.q_scale, row0, n_rows, 32 * (warp & 3) + 16 * grp, 16, q0, h, G, lane);
+                stage_queries<D, 16>(a, sk, sh.q_scale, row0, n_rows, 32 * (warp & 3) + 16 * grp, q0, h, G, lane);
                 group_sync(1, 32 * kSoftWarps);
                 const uint8_t* src = sk + 2 * grp * (kM * 128);
 #pragma unroll
@@ -289,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                     mbar_arrive(&sh.q_full);
                 }
             } else {
-                stage_queries<D>(a, sq + t * C::kQ, sh.q_scale + t * kM, tile_row0, n_rows - t * kM, 32 * (warp & 3), 32, q0, h,
-                                 G, lane);
+                stage_queries<D, 32>(a, sq + t * C::kQ, sh.q_scale + t * kM, tile_row0, n_rows - t * kM, 32 * (warp & 3), q0, h,
+                                     G, lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.q_full);
             }
@@ -543,67 +555,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[hb]);
         }
-    } else if (lane == 0) {
-        // ---- issue: scores by one warp's thread, outputs by the next one's
-        const bool scores = warp == kIssueWarp;
+    } else {
+        // ---- issue: scores by one warp, outputs by the next.  The whole warp runs the loop, so that
+        // addresses and descriptors stay warp-uniform; one lane issues.
+        const bool scores = warp == kIssueWarp, leader = elect_one();
         constexpr uint32_t id_s = idesc_f16_f32(kM, kKeys, false), id_o = idesc_f16_f32(kM, D, true);
-        const uint32_t ak = smem_u32(sk), av = smem_u32(sv), aq = C::kQInTmem ? 0 : smem_u32(sq);
-        bool ok = n_tiles == 0 || !scores || mbar_wait_brief(&sh.q_full, 0);
+        const uint64_t da0 = C::kQInTmem ? 0 : desc_kmajor_sw128(smem_u32(sq));
+        const uint64_t db0 = scores ? desc_kmajor_sw128(smem_u32(sk)) : desc_mnmajor_sw128(smem_u32(sv), kKeys * 128);
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_brief(bar, parity)) != 0; };
+        bool ok = n_tiles == 0 || !scores || wait(&sh.q_full, 0);
         uint64_t* last = nullptr;
         uint32_t last_par = 0;
         int stage = 0, round = 0;  // buffer and round of the tile
         for (int i = 0; ok && i < n_tiles; ++i) {
             const int b = i & 1;
-            if (!(ok = mbar_wait_brief(scores ? &sh.k_full[stage] : &sh.v_full[stage], round & 1))) break;
+            if (!(ok = wait(scores ? &sh.k_full[stage] : &sh.v_full[stage], round & 1))) break;
             fence_proxy_async_smem();
+            const uint64_t db = db0 + static_cast<uint64_t>(stage) * (C::kTile >> 4);
             for (int t = 0; t < active; ++t) {
                 // scores: the last ones were read; outputs: the weights are there
-                if (scores ? i >= 1 && !(ok = mbar_wait_brief(&sh.s_empty[t], (i - 1) & 1))
-                           : !(ok = mbar_wait_brief(&sh.p_full[t][b], (i >> 1) & 1)))
+                if (scores ? i >= 1 && !(ok = wait(&sh.s_empty[t], (i - 1) & 1))
+                           : !(ok = wait(&sh.p_full[t][b], (i >> 1) & 1)))
                     break;
                 tc_fence_after_sync();
                 if (scores) {
+                    const uint64_t da = da0 + static_cast<uint64_t>(t) * (C::kQ >> 4);
+                    const uint32_t d = tmem + t * kKeys;
+                    if (leader) {
 #pragma unroll
-                    for (int n = 0; n < D / 64; ++n) {
-                        const uint64_t db = desc_kmajor_sw128(ak + stage * C::kTile + n * (kKeys * 128));
-                        const uint64_t da = C::kQInTmem ? 0 : desc_kmajor_sw128(aq + t * C::kQ + n * (kM * 128));
+                        for (int n = 0; n < D / 64; ++n)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (C::kQInTmem)
-                                mma_f16_ta(tmem + t * kKeys, tmem + C::kQCol + 32 * n + 8 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
-                            else
-                                mma_bf16(tmem + t * kKeys, da + 2 * k, db + 2 * k, id_s, (n > 0 || k > 0) ? 1u : 0u);
-                        }
+                            for (int k = 0; k < 4; ++k) {
+                                const uint64_t dbk = db + (n * (kKeys * 128) >> 4) + 2 * k;
+                                if (C::kQInTmem)
+                                    mma_f16_ta(d, tmem + C::kQCol + 32 * n + 8 * k, dbk, id_s, (n > 0 || k > 0) ? 1u : 0u);
+                                else
+                                    mma_bf16(d, da + (n * (kM * 128) >> 4) + 2 * k, dbk, id_s, (n > 0 || k > 0) ? 1u : 0u);
+                            }
+                        mma_commit(&sh.s_full[t]);
                     }
-                    mma_commit(&sh.s_full[t]);
                     last = &sh.s_full[t];
                     last_par = i & 1;
                 } else {
+                    const uint32_t d = tmem + C::kOut + t * D, p = tmem + C::kWeights + t * kKeys + b * (kKeys / 2);
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)  // 16 keys of weights are 8 columns
-                        mma_f16_ta(tmem + C::kOut + t * D, tmem + C::kWeights + t * kKeys + b * (kKeys / 2) + 8 * k,
-                                   desc_mnmajor_sw128(av + stage * C::kTile + k * 2048, kKeys * 128), id_o,
-                                   (i > 0 || k > 0) ? 1u : 0u);
-                    mma_commit(&sh.pv_done[t][b]);
+                        for (int k = 0; k < kKeys / 16; ++k)  // 16 keys of weights are 8 columns
+                            mma_f16_ta(d, p + 8 * k, db + k * (2048 >> 4), id_o, (i > 0 || k > 0) ? 1u : 0u);
+                        mma_commit(&sh.pv_done[t][b]);
+                    }
                     last = &sh.pv_done[t][b];
                     last_par = (i >> 1) & 1;
                 }
+                __syncwarp();
             }
             if (!ok) break;
-            mma_commit(scores ? &sh.k_empty[stage] : &sh.v_empty[stage]);
+            if (leader) mma_commit(scores ? &sh.k_empty[stage] : &sh.v_empty[stage]);
             if (!scores && i == n_tiles - 1) {
-                mma_commit(&sh.o_full);
+                if (leader) mma_commit(&sh.o_full);
                 last = &sh.o_full;
                 last_par = 0;
             }
+            __syncwarp();
             if (++stage == kStages) {
                 stage = 0;
                 ++round;
             }
         }
-        if (!ok) prompt_fail(46);
-        // nothing of this thread is in flight when the tensor memory is freed
-        if (last && !mbar_wait_brief(last, last_par)) prompt_fail(47);
+        if (!ok && leader) prompt_fail(46);
+        // nothing of this warp is in flight when the tensor memory is freed
+        if (last && !wait(last, last_par) && leader) prompt_fail(47);
     }
     __syncwarp();
     tc_fence_before_sync();
