@@ -106,6 +106,12 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+// Bulk copy shared -> global of `bytes` (a multiple of 16, both ends aligned),
+// tracked by the issuing thread's bulk group.
+__device__ __forceinline__ void bulk_store_1d(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -145,56 +151,48 @@ struct Shared {
     uint64_t o_full;
     GroupConst consts[2 * kPass][kGroups];
     long long place[2 * kPass][kGroups];  // a group's first code in the cache, or -1
-    float q_scale[2 * kM];
     float swap[2][kM];  // a row's two threads: maxima, sums
     uint32_t tmem_slot;
 };
 static_assert(sizeof(Shared) <= 4096, "part of kSmem");
 
-// Queries of ROWS rows by one warp, all loads in flight at once: rounded to f16
-// under a power of two of the row, into a K-major swizzled tile of kM rows.
-template <int D, int ROWS>
-__device__ __forceinline__ void stage_queries(const KvAttnArgs& a, uint8_t* tile, float* q_scale, int row0, int n_rows,
-                                              int first, int q0, int h, int G, int lane) {
-    constexpr int E = D / 32;  // channels of a lane
-    uint32_t raw[ROWS][E / 2];
-    int tok = (row0 + first) / G, g = (row0 + first) % G;
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) raw[i][e] = 0;
-        if (first + i < n_rows) {
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.data) + (q0 + tok) * a.q.token_stride +
-                                       (h * G + g) * a.q.head_stride;
-            memcpy(raw[i], __builtin_assume_aligned(src + E * lane, E * 2), E * 2);
-        }
-        if (++g == G) {
-            g = 0;
-            ++tok;
-        }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+    const int n = take ? 16 : 0;  // 0: the 16 bytes become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// A row tile's queries as they are (bf16; zeros past the last row) by THREADS
+// threads into a swizzled tile of kM rows in blocks of 64 channels.
+template <int D, int THREADS>
+__device__ __forceinline__ void fetch_queries(const KvAttnArgs& a, uint8_t* tile, int row0, int n_rows, int q0, int h, int G,
+                                              int tid) {
+    constexpr int V = D / 8, STEP = THREADS / V;  // 16-byte vectors of a row; rows at a time
+    const int c = tid % V;
+    const uint32_t base = smem_u32(tile) + (c / 8) * (kM * 128);
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) + 8 * c;
+#pragma unroll 4
+    for (int r = tid / V; r < kM; r += STEP) {
+        const int row = row0 + r;
+        const bool take = r < n_rows;
+        const __nv_bfloat16* src = q + (q0 + row / G) * a.q.token_stride + (h * G + row % G) * a.q.head_stride;
+        cp_async16(base + sw128_offset(r, c % 8), take ? src : q, take);
     }
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+// The exponent under which a row whose largest magnitude is `most` is rounded to f16.
+__device__ __forceinline__ int row_exponent(float most) {
+    return most > 0.0f && most <= 3.402823466e38f ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126) : 0;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+__device__ __forceinline__ float most_of(uint4 v, float most) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int r = first + i;
-        float most = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e)
-            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(raw[i][e] << 16)), fabsf(__uint_as_float(raw[i][e] & 0xFFFF0000u))));
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-        const int ex = most > 0.0f && most <= 3.402823466e38f
-                           ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126) : 0;
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        if (lane == 0) q_scale[r] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-        uint32_t w[E / 2];
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e)
-            w[e] = pack_f16(__uint_as_float(raw[i][e] << 16) * down, __uint_as_float(raw[i][e] & 0xFFFF0000u) * down);
-        // channel E lane of column block (E lane) / 64
-        const uint32_t byte = (E * lane % 64) * 2;
-        uint8_t* dst = tile + (E * lane / 64) * (kM * 128) + sw128_offset(r, byte >> 4) + (byte & 15);
-        memcpy(__builtin_assume_aligned(dst, E * 2), w, E * 2);
-    }
+    for (int i = 0; i < 4; ++i)
+        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+    return most;
+}
+__device__ __forceinline__ uint32_t scaled_f16(uint32_t bf16_pair, float f) {
+    return pack_f16(__uint_as_float(bf16_pair << 16) * f, __uint_as_float(bf16_pair & 0xFFFF0000u) * f);
 }
 
 template <typename F, int D>
@@ -277,19 +275,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
         const int tile_row0 = row0 + t * kM;
         if (t < active) {
             // ---- queries
-            if (C::kQInTmem) {
-                // through the first K buffers: 16 rows a warp, then each thread half of its row
+            // A thread finds its row's (with a row's two threads: its half's) largest magnitude and rounds
+            // the row to f16 under a power of two.
+            float qs;
+            if (C::kQInTmem) {  // through the first K buffers
                 static_assert(!C::kQInTmem || 2 * C::kTile >= C::kQ, "two K buffers hold the queries");
-                stage_queries<D, 16>(a, sk, sh.q_scale, row0, n_rows, 32 * (warp & 3) + 16 * grp, q0, h, G, lane);
+                fetch_queries<D, 32 * kSoftWarps>(a, sk, row0, n_rows, q0, h, G, tid);
                 group_sync(1, 32 * kSoftWarps);
                 const uint8_t* src = sk + 2 * grp * (kM * 128);
+                float most = 0.0f;
 #pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    most = most_of(*reinterpret_cast<const uint4*>(src + (c >> 3) * (kM * 128) + sw128_offset(r, c & 7)), most);
+                sh.swap[grp][r] = most;
+                group_sync(2, 32 * kSoftWarps);
+                const int ex = row_exponent(fmaxf(most, sh.swap[grp ^ 1][r]));
+                const float down = pow2(-ex);
+                qs = a.scale * kLog2e * pow2(ex);
+#pragma unroll 1
                 for (int blk = 0; blk < 2; ++blk) {
                     uint32_t w[32];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const uint4 v = *reinterpret_cast<const uint4*>(src + blk * (kM * 128) + sw128_offset(r, c));
-                        w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+                        w[4 * c] = scaled_f16(v.x, down);
+                        w[4 * c + 1] = scaled_f16(v.y, down);
+                        w[4 * c + 2] = scaled_f16(v.z, down);
+                        w[4 * c + 3] = scaled_f16(v.w, down);
                     }
                     tmem_st32(tmem + t_lane + C::kQCol + 64 * grp + 32 * blk, w);
                 }
@@ -301,15 +313,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                     mbar_arrive(&sh.q_full);
                 }
             } else {
-                stage_queries<D, 32>(a, sq + t * C::kQ, sh.q_scale + t * kM, tile_row0, n_rows - t * kM, 32 * (warp & 3), q0, h,
-                                     G, lane);
+                uint8_t* tile = sq + t * C::kQ;
+                fetch_queries<D, kM>(a, tile, tile_row0, n_rows - t * kM, q0, h, G, r);
+                group_sync(1 + t, kM);
+                float most = 0.0f;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    most = most_of(*reinterpret_cast<const uint4*>(tile + (c >> 3) * (kM * 128) + sw128_offset(r, c & 7)), most);
+                const int ex = row_exponent(most);
+                const float down = pow2(-ex);
+                qs = a.scale * kLog2e * pow2(ex);
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * (kM * 128) + sw128_offset(r, c & 7));
+                    const uint4 v = *at;
+                    *at = make_uint4(scaled_f16(v.x, down), scaled_f16(v.y, down), scaled_f16(v.z, down), scaled_f16(v.w, down));
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.q_full);
             }
 
             // ---- softmax: a thread's row, all keys of a tile or 32 of them
             const int pos = start + (tile_row0 + r) / G;
-            const float qs = sh.q_scale[t * kM + r];
             const int my_lo = start + tile_row0 / G;  // the row tile's first position
             const int max_lo = a.window ? hi_pos - a.window + 1 : 0;
             const uint32_t t_score = tmem + t_lane + t * kKeys + (C::kHalves == 2 ? grp * NC : 0);
@@ -419,25 +444,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             }
             if (ok) {
                 tc_fence_after_sync();
+                // through the K and V buffers, whose products are done, so that a row leaves as one piece
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 const int row = tile_row0 + r;
-                constexpr int W = D / C::kHalves;
+                constexpr int W = D / C::kHalves, PITCH = 2 * D + 16;  // 16 bytes more: rows in different banks
+                static_assert(C::kTiles * kM * PITCH <= 2 * kStages * C::kTile, "the buffers hold the output");
                 const int c0 = C::kHalves == 2 ? grp * W : 0;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                     (static_cast<size_t>(q0 + row / G) * a.n_q_heads + h * G + row % G) * D + c0;
+                uint8_t* mine = smem + (t * kM + r) * PITCH + 2 * c0;
 #pragma unroll 1
                 for (int c = 0; c < W; c += 32) {
                     float v[32];
                     if (n_tiles > 0) tmem_ld32(t_out + c0 + c, v);
-                    if (t * kM + r < n_rows) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            float x[8];
+                    for (int e = 0; e < 32; e += 8) {
+                        float x[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) x[k] = n_tiles > 0 ? v[e + k] * inv : 0.0f;
-                            Vec16<__nv_bfloat16>::store(out + c + e, x);
-                        }
+                        for (int k = 0; k < 8; ++k) x[k] = n_tiles > 0 ? v[e + k] * inv : 0.0f;
+                        Vec16<__nv_bfloat16>::store(reinterpret_cast<__nv_bfloat16*>(mine) + c + e, x);
                     }
+                }
+                fence_proxy_async_smem();
+                if (t * kM + r < n_rows) {
+                    bulk_store_1d(static_cast<__nv_bfloat16*>(a.out) +
+                                      (static_cast<size_t>(q0 + row / G) * a.n_q_heads + h * G + row % G) * D + c0,
+                                  mine, 2 * W);
+                    bulk_commit();
+                    bulk_wait_read();
                 }
             }
         }
