@@ -106,6 +106,24 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Bulk copy shared -> global of `bytes` (a multiple of 16, both ends aligned),
 // tracked by the issuing thread's bulk group.
 __device__ __forceinline__ void bulk_store_1d(void* dst, const void* src, uint32_t bytes) {
@@ -361,7 +379,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
 #pragma unroll
                 for (int g = 0; g < NC / 16; ++g) gc[g] = sh.consts[i % (2 * kPass)][(C::kHalves == 2 ? grp * (NC / 16) : 0) + g];
 #pragma unroll
-                for (int j = 0; j < NC; ++j) s[j] = fmaf(s[j], qs * gc[j / 16].ks, gc[j / 16].lv);
+                for (int g = 0; g < NC / 16; ++g) {
+                    const float f = qs * gc[g].ks, o = gc[g].lv;
+                    const uint64_t f2 = pair(f, f), o2 = pair(o, o);
+#pragma unroll
+                    for (int j = 16 * g; j < 16 * g + 16; j += 2) unpair(fma2(pair(s[j], s[j + 1]), f2, o2), s[j], s[j + 1]);
+                }
                 if (!(key + NC - 1 <= my_lo && key >= max_lo && key + NC <= end)) {
                     const int hi = min(pos, end - 1) - key, lo = a.window ? pos - a.window + 1 - key : 0;
 #pragma unroll
@@ -388,18 +411,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 }
                 const float ref = m == -INFINITY ? 0.0f : m - kBias;
                 uint32_t p[NC / 2];
+                const uint64_t ref2 = pair(-ref, -ref);
 #pragma unroll
                 for (int g = 0; g < NC / 16; ++g) {
-                    float sum[2] = {0.0f, 0.0f};
-                    const bool dead = gc[g].inv < 0.0f;  // values of a scale of 0: counted, not added
+                    uint64_t sums = 0;  // 0.0f twice
 #pragma unroll
                     for (int j = 16 * g; j < 16 * g + 16; j += 2) {
-                        const float w0 = exp2_ftz(s[j] - ref), w1 = exp2_ftz(s[j + 1] - ref);
-                        sum[0] += w0;
-                        sum[1] += w1;
-                        p[j / 2] = dead ? 0u : pack_f16(w0, w1);
+                        float w0, w1;
+                        unpair(add2(pair(s[j], s[j + 1]), ref2), w0, w1);
+                        w0 = exp2_ftz(w0);
+                        w1 = exp2_ftz(w1);
+                        sums = add2(sums, pair(w0, w1));
+                        p[j / 2] = pack_f16(w0, w1);
                     }
-                    l = fmaf(sum[0] + sum[1], fabsf(gc[g].inv), l);
+                    float s0, s1;
+                    unpair(sums, s0, s1);
+                    l = fmaf(s0 + s1, fabsf(gc[g].inv), l);
+                    if (gc[g].inv < 0.0f) {  // values of a scale of 0: counted, not added
+#pragma unroll
+                        for (int j = 8 * g; j < 8 * g + 8; ++j) p[j] = 0;
+                    }
                 }
                 // the buffer's last weights were used
                 if (ok && i >= 2 &&
