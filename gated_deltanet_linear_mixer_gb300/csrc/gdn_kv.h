@@ -82,7 +82,7 @@ cudaError_t launch_kv_read(const KvReadArgs& a, int head_dim, bool bf16, bool e4
 size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window,
                               bool bf16, int max_kv_len);
 // The kernel for many rows (gdn_kv_prompt.cu): whether it takes a call, and its launch.
-bool kv_prompt_serves(int n_seq, int max_q, int n_q_heads, int n_kv_heads, bool bf16);
+bool kv_prompt_serves(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, bool bf16);
 cudaError_t launch_kv_prompt(const KvAttnArgs& a, int head_dim, bool e4m3, cudaStream_t stream);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3,
                                 cudaStream_t stream);

@@ -752,7 +752,7 @@ cudaError_t attn_t(const KvAttnArgs& a, cudaStream_t st) {
 
 size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window, bool bf16,
                               int max_kv_len) {
-    if (max_q == 0 || kv_prompt_serves(n_seq, max_q, n_q_heads, n_kv_heads, bf16)) return 0;
+    if (max_q == 0 || kv_prompt_serves(n_seq, max_q, n_q_heads, n_kv_heads, head_dim, bf16)) return 0;
     const long long all = static_cast<long long>(max_q) * (n_q_heads / n_kv_heads);
     const int rows = 8 * tiles_of_8(head_dim, all);
     const Split sp = split_of(rows, n_seq, max_q, n_q_heads, n_kv_heads, window, max_kv_len);
@@ -763,7 +763,7 @@ size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_head
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
-    if (kv_prompt_serves(a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, bf16))
+    if (kv_prompt_serves(a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, head_dim, bf16))
         return launch_kv_prompt(a, head_dim, e4m3, stream);
     return GDN_KV_PICK(attn_t);
 }

@@ -718,11 +718,18 @@ cudaError_t prompt_d(const KvAttnArgs& a, int head_dim, cudaStream_t st) {
 
 // Whole tiles of 128 rows pay once there are enough of them to occupy a fair
 // part of the SMs (their keys are not split): below that the kernel for few
-// rows spreads the keys.  The grid's third dimension bounds the tiles.
-bool kv_prompt_serves(int n_seq, int max_q, int n_q_heads, int n_kv_heads, bool bf16) {
+// rows spreads the keys.  Wider heads pay earlier, since that kernel takes
+// them in narrower tiles.  Tiles (of all heads and sequences): microseconds
+// here against there, over calls of 0 to 8000 keys of context,
+//   head_dim  64:  8: 132 / 54, 32: 60 / 45, 38: 12.8 / 15.1 to 42.5 / 38.9, 80: 76 / 99;
+//   head_dim 128:  8: 67 / 79 to 165 / 91, 16: 167 / 97, 32: 69 / 73, 38: 53 / 71, 80: 93 / 168;
+//   head_dim 256:  8: 68 / 65 to 127 / 87, 16: 128 / 142, 32: 69 / 95, 38: 73 / 177, 80: 73 / 277.
+// The grid's third dimension bounds the tiles.
+bool kv_prompt_serves(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, bool bf16) {
     const long long rows = static_cast<long long>(max_q) * (n_q_heads / n_kv_heads);
     const long long tiles = (rows + kM - 1) / kM;
-    return bf16 && rows > 32 && tiles <= 65535 && tiles * n_kv_heads * n_seq >= 40;
+    const int least = head_dim == 64 ? 40 : head_dim == 128 ? 32 : 16;
+    return bf16 && rows > 32 && tiles <= 65535 && tiles * n_kv_heads * n_seq >= least;
 }
 
 cudaError_t launch_kv_prompt(const KvAttnArgs& a, int head_dim, bool e4m3, cudaStream_t stream) {
