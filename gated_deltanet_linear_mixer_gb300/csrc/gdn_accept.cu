@@ -11,8 +11,9 @@
 // A cluster of thread blocks takes a sequence, each block a slice of the
 // vocabulary; sums and winners are exchanged through distributed shared memory,
 // so a sequence needs one launch and no workspace.  What bounds it: HBM for
-// large vocabularies and many sequences, else the chain of memory round trips:
-// lengths, rows, exchange, row again, exchange.  Of logits, the rows of `step`
+// large vocabularies and many sequences (64 x 4 drafts of 131,072 probabilities:
+// 20 us, 5.0 TB/s), else the chain of memory round trips: lengths, rows,
+// exchange, row again, exchange (48 x 3 drafts of 32,003 bf16 logits: 14.5 us).  Of logits, the rows of `step`
 // drafts are summed at a time, different warps on different rows: all of them
 // where a block's slice is short, one draft after the other where bytes count
 // and a fallen draft spares the rows behind it.
@@ -284,9 +285,14 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptArgs a, co
 template <typename T, bool LOGITS>
 cudaError_t accept_t(const AcceptArgs& a, cudaStream_t st) {
     // Blocks of a sequence: enough to occupy the SMs (four blocks fit on one), no slice below 1024.
+    // Microseconds with 1 / 2 / 4 / 8 blocks: 1 sequence of 131,072 probabilities 41 / 22 / 13 / 8.4 (8 taken),
+    // of 4000 4.7 / 4.1 / 4.6 / 4.6 (2), 256 of 32,000 25 / 20 / 22 / 28 (2); 48 of 32,003 logits
+    // 51 / 32 / 20 / 15 (8), 256 of them 89 / 81 / 95 / 114 (2).
     int C = kMaxCluster;
     while (C > 1 && (static_cast<long long>(a.n_seq) * C > 152 * 4 || a.vocab / C < 1024)) C /= 2;
-    // Drafts summed at a time: all of them while a lane's share of a row stays below 64 logits.
+    // Drafts summed at a time: one where bytes count, all where the round trips do.  Microseconds at
+    // 1 / 4 / 16: 64 x 8 drafts of 8000 logits 26 / 14.2 / 13.0 (16 taken), 48 x 3 of 32,003 20 / 14.7 / 14.9 (4),
+    // 256 x 4 of them, whose slices are longer, 80 / 108 / 108 (1), 64 x 4 of 131,072 84 / 107 / 107 (1).
     const int share = a.vocab / C / kThreads;
     const int step = share * (a.T + 1) <= 128 ? kMaxDrafts : share <= 32 ? 4 : 1;
     cudaLaunchConfig_t cfg{};

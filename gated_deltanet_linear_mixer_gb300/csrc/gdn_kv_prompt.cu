@@ -36,6 +36,13 @@
 // The converted tiles are written by ordinary stores and read by the tensor
 // core: an issuing thread, which has waited for the writers, fences the one
 // against the other (a writer's fence would also wait for its loads in flight).
+// What bounds it: no unit is saturated, the chain of waits between the roles is.
+// A prompt of 4096 tokens (16 heads of 256) takes 135 us, 1.02 PFLOP/s over the
+// visible pairs: 1.23 us a tile and SM, of which the products need 1024 cycles
+// (tensor pipe 42% busy, issue slots 56%).  16 ragged prompts with a window (32
+// heads of 128) take 315 us, 0.67 PFLOP/s (30%, 47%); each thread block there
+// also walks fewer keys per start.  Tiles of 128 keys were slower when tried, on
+// an earlier form of this kernel: 226 and 609 us, against 222 and 507.
 // Every wait is bounded (2 s); a wait that gives up records a code (42..48) in
 // this file's device error word and its role stops.
 #include <algorithm>

@@ -414,9 +414,12 @@ gdn_status gdn_kv_read(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
  *   attended to in full).
  *   workspace: at least gdn_kv_attention_workspace_size() bytes, 256-byte
  *   aligned (NULL when that is 0).
- * bf16 activations: tensor cores, codes and probabilities as f16 operands,
- * fp32 accumulation and softmax.  fp32 activations: the same with queries and
- * probabilities as f16 (hi, lo) pairs.
+ * Tensor cores, codes as f16 or bf16 operands (exact), fp32 accumulation and
+ * softmax.  bf16 activations: weights are f16 (11 bits) or, where some are too
+ * small for that, two bf16 terms (16 bits); calls of many rows (prompts) keep to
+ * f16 and drop weights below 2^-31 of a row's reference, which lies within 2^8
+ * of its largest.  fp32 activations: queries are f16 (hi, lo) pairs, weights
+ * three bf16 terms.
  */
 gdn_status gdn_kv_attention_workspace_size(const gdn_kv_dims* dims, int32_t n_seq,
                                            const int32_t* cu_seqlens_host, int32_t max_kv_len,
@@ -481,7 +484,8 @@ size_t gdn_timing_report(char* buf, size_t buf_len);
  * launch's wait for a chunk's prep rows; 13 and 14 its per-channel decay prep's
  * waits for its tiles, and for its v tile, products and the next item's tiles;
  * 20..23 the projection GEMM's; 30 the
- * token-recurrent kernel's wait for a state copy) and exit cleanly; their
+ * token-recurrent kernel's wait for a state copy; 42..48 the cache attention's
+ * tensor-core kernel's waits between its roles) and exit cleanly; their
  * outputs are then invalid.  Codes 40 and 41 are not waits: a cache operator
  * met device data out of range (see the cache above) and stayed in bounds.  Waits for the device (cudaMemcpyFromSymbol), writes the code to
  * *code (0 = no error) and clears it when reset != 0.
