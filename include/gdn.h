@@ -453,7 +453,7 @@ typedef enum gdn_dist_form { GDN_DIST_PROBS = 0, GDN_DIST_LOGITS = 1 } gdn_dist_
  *   T + 1, or T, rows); noise [n_seq, vocab] fp32 with its row stride;
  *   temperature [n_seq] fp32 >= 0 (logits; NULL: 1).  0 <= T <= 16.
  *   accepted [n_seq] int32: how many drafts stand (gdn_decode_commit's
- *   `accepted`).  tokens [n_seq, T + 1] int32: those drafts, the drawn token,
+ *   `accepted`, plus one where its x begins with the last kept token).  tokens [n_seq, T + 1] int32: those drafts, the drawn token,
  *   then -1.
  */
 gdn_status gdn_accept_drafts(int32_t n_seq, int32_t T, int32_t vocab, int32_t form, int32_t dtype,
