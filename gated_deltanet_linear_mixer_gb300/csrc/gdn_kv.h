@@ -81,9 +81,23 @@ cudaError_t launch_kv_read(const KvReadArgs& a, int head_dim, bool bf16, bool e4
                            cudaStream_t stream);
 size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window,
                               bool bf16, int max_kv_len);
-// The kernel for many rows (gdn_kv_prompt.cu): whether it takes a call, and its launch.
-bool kv_prompt_serves(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, bool bf16);
-cudaError_t launch_kv_prompt(const KvAttnArgs& a, int head_dim, bool e4m3, cudaStream_t stream);
+// Keys split into n ranges of `chunk`; the last takes what is left.
+struct KvSplit {
+    int n, chunk;
+};
+// How the kernel for many rows (gdn_kv_prompt.cu) takes a call: thread blocks
+// of `rows` rows, tiles of a sequence and head (0: it does not take the call).
+struct KvPrompt {
+    int tiles, rows;
+    KvSplit split;
+};
+KvPrompt kv_prompt_plan(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window, bool bf16,
+                        long long max_kv_len);
+cudaError_t launch_kv_prompt(const KvAttnArgs& a, const KvPrompt& c, int head_dim, bool e4m3, cudaStream_t stream);
+// Joins partial results [seq][kv head][tile][split] of rows x D outputs, then
+// rows references and rows sums (bf16 activations).
+cudaError_t launch_kv_join(const KvAttnArgs& a, const KvSplit& split, int rows, int tiles, int head_dim,
+                           cudaStream_t stream);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3,
                                 cudaStream_t stream);
 // form: gdn_dist_form; logits and probabilities in bf16 or f32.

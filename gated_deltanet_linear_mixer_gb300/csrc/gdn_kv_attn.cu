@@ -187,9 +187,7 @@ __device__ __forceinline__ bool tile_of(const KvAttnArgs& a, int rows, int tile,
     return true;
 }
 
-struct Split {
-    int n, chunk;  // ranges of `chunk` keys; the last takes what is left
-};
+using Split = KvSplit;
 
 // Four channels of a row of the output.
 template <typename T, int D>
@@ -694,6 +692,15 @@ cudaError_t join_t(const KvAttnArgs& a, const Split sp, int rows, int n_tiles, c
     return cudaLaunchKernelEx(&cfg, kv_attn_join<T, D, GROUPS>, a, sp, rows, n_tiles);
 }
 
+template <typename T, int D>
+cudaError_t join_d(const KvAttnArgs& a, const Split& sp, int rows, int n_tiles, cudaStream_t st) {
+    return timed_launch("kv_attn_join", st, [&] {
+        return sp.n <= kJoinEach       ? join_t<T, D, 1>(a, sp, rows, n_tiles, st)
+               : sp.n <= 4 * kJoinEach ? join_t<T, D, 4>(a, sp, rows, n_tiles, st)
+                                       : join_t<T, D, 32>(a, sp, rows, n_tiles, st);
+    });
+}
+
 // Rows of a thread block: the fewest tiles of 8 that hold a sequence's rows,
 // as far as the output's registers (D / 16 x 4 x NQ a lane, at most 128) allow.
 int tiles_of_8(int head_dim, long long rows) {
@@ -741,11 +748,7 @@ cudaError_t attn_nq(const KvAttnArgs& a, cudaStream_t st) {
         return cudaGetLastError();
     });
     if (e != cudaSuccess || sp.n == 1) return e;
-    return timed_launch("kv_attn_join", st, [&] {
-        return sp.n <= kJoinEach       ? join_t<T, D, 1>(a, sp, C::kRows, nt, st)
-               : sp.n <= 4 * kJoinEach ? join_t<T, D, 4>(a, sp, C::kRows, nt, st)
-                                       : join_t<T, D, 32>(a, sp, C::kRows, nt, st);
-    });
+    return join_d<T, D>(a, sp, C::kRows, nt, st);
 }
 
 template <typename T, typename F, int D>
@@ -761,19 +764,29 @@ cudaError_t attn_t(const KvAttnArgs& a, cudaStream_t st) {
 
 size_t kv_attention_workspace(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window, bool bf16,
                               int max_kv_len) {
-    if (max_q == 0 || kv_prompt_serves(n_seq, max_q, n_q_heads, n_kv_heads, head_dim, bf16)) return 0;
+    if (max_q == 0) return 0;
+    const KvPrompt p = kv_prompt_plan(n_seq, max_q, n_q_heads, n_kv_heads, head_dim, window, bf16, max_kv_len);
+    const auto bytes_of = [&](size_t tiles, int n, size_t rows) {
+        const size_t bytes = n == 1 ? 0 : tiles * n_kv_heads * n_seq * n * rows * (head_dim + 2) * sizeof(float);
+        return (bytes + 255) & ~static_cast<size_t>(255);
+    };
+    if (p.tiles > 0) return bytes_of(p.tiles, p.split.n, p.rows);
     const long long all = static_cast<long long>(max_q) * (n_q_heads / n_kv_heads);
     const int rows = 8 * tiles_of_8(head_dim, all);
     const Split sp = split_of(rows, n_seq, max_q, n_q_heads, n_kv_heads, window, max_kv_len);
-    if (sp.n == 1) return 0;
-    const size_t tiles = (all + rows - 1) / rows;
-    const size_t bytes = tiles * n_kv_heads * n_seq * sp.n * rows * (head_dim + 2) * sizeof(float);
-    return (bytes + 255) & ~static_cast<size_t>(255);
+    return bytes_of((all + rows - 1) / rows, sp.n, rows);
+}
+
+cudaError_t launch_kv_join(const KvAttnArgs& a, const KvSplit& split, int rows, int tiles, int head_dim,
+                           cudaStream_t stream) {
+    return head_dim == 64    ? join_d<__nv_bfloat16, 64>(a, split, rows, tiles, stream)
+           : head_dim == 128 ? join_d<__nv_bfloat16, 128>(a, split, rows, tiles, stream)
+                             : join_d<__nv_bfloat16, 256>(a, split, rows, tiles, stream);
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
-    if (kv_prompt_serves(a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, head_dim, bf16))
-        return launch_kv_prompt(a, head_dim, e4m3, stream);
+    const KvPrompt p = kv_prompt_plan(a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, head_dim, a.window, bf16, a.max_kv_len);
+    if (p.tiles > 0) return launch_kv_prompt(a, p, head_dim, e4m3, stream);
     return GDN_KV_PICK(attn_t);
 }
 

@@ -37,10 +37,10 @@
 // core: an issuing thread, which has waited for the writers, fences the one
 // against the other (a writer's fence would also wait for its loads in flight).
 // What bounds it: no unit is saturated, the chain of waits between the roles is.
-// A prompt of 4096 tokens (16 heads of 256) takes 135 us, 1.02 PFLOP/s over the
-// visible pairs: 1.23 us a tile and SM, of which the products need 1024 cycles
+// A prompt of 4096 tokens (16 heads of 256) takes 131 us, 1.05 PFLOP/s over the
+// visible pairs: 1.2 us a tile and SM, of which the products need 1024 cycles
 // (tensor pipe 42% busy, issue slots 56%).  16 ragged prompts with a window (32
-// heads of 128) take 315 us, 0.67 PFLOP/s (30%, 47%); each thread block there
+// heads of 128) take 314 us, 0.67 PFLOP/s (30%, 47%); each thread block there
 // also walks fewer keys per start.  Tiles of 128 keys were slower when tried, on
 // an earlier form of this kernel: 226 and 609 us, against 222 and 507.
 // Every wait is bounded (2 s); a wait that gives up records a code (42..48) in
@@ -220,8 +220,10 @@ __device__ __forceinline__ uint32_t scaled_f16(uint32_t bf16_pair, float f) {
     return pack_f16(__uint_as_float(bf16_pair << 16) * f, __uint_as_float(bf16_pair & 0xFFFF0000u) * f);
 }
 
-template <typename F, int D>
-__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs a) {
+// SPLIT: the keys are split, and results are partial ones for the join.  A kernel
+// of its own: with both in one the 4096-token prompt takes 134 us instead of 131.
+template <typename F, int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs a, const KvSplit sp) {
     using C = PCfg<D>;
     constexpr int NT = C::kTiles, NC = C::kCols;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles start on 1024-byte boundaries
@@ -230,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int seq = blockIdx.y, h = blockIdx.x, G = a.n_q_heads / a.n_kv_heads;
     const int q0 = a.b.cu[seq], qn = a.b.cu[seq + 1] - q0;
-    const int row0 = (static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z)) * (NT * kM);  // most keys first
+    const int block_tile = (static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z)) / (SPLIT ? sp.n : 1);  // most keys first
+    const int split = SPLIT ? static_cast<int>(blockIdx.z) % sp.n : 0, row0 = block_tile * (NT * kM);
     const int n_rows = min(NT * kM, qn * G - row0);
     if (n_rows <= 0) return;
     int len = a.b.kv_lens[seq];
@@ -241,8 +244,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
         len = static_cast<int>(cap);
     }
     const int lo_pos = start + row0 / G, hi_pos = start + (row0 + n_rows - 1) / G;
-    const int first = a.window ? max(0, lo_pos - a.window + 1) / kKeys * kKeys : 0;
-    const int end = min(hi_pos + 1, len);
+    // this thread block's range of the keys; the join does not read an empty one past the first
+    const int all_first = a.window ? max(0, lo_pos - a.window + 1) / kKeys * kKeys : 0;
+    const int span = max(0, min(hi_pos + 1, len) - all_first), from = SPLIT ? split * sp.chunk : 0;
+    if (SPLIT && split > 0 && from >= span) return;
+    const int first = all_first + from, end = all_first + (!SPLIT || split == sp.n - 1 ? span : min(span, from + sp.chunk));
     const int n_tiles = end > first ? (end - first + kKeys - 1) / kKeys : 0;
     const int active = n_rows > kM ? NT : 1;  // row tiles with rows
 
@@ -482,32 +488,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             }
             if (ok) {
                 tc_fence_after_sync();
-                // through the K and V buffers, whose products are done, so that a row leaves as one piece
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                const int row = tile_row0 + r;
-                constexpr int W = D / C::kHalves, PITCH = 2 * D + 16;  // 16 bytes more: rows in different banks
-                static_assert(C::kTiles * kM * PITCH <= 2 * kStages * C::kTile, "the buffers hold the output");
-                const int c0 = C::kHalves == 2 ? grp * W : 0;
-                uint8_t* mine = smem + (t * kM + r) * PITCH + 2 * c0;
+                constexpr int W = D / C::kHalves;  // this thread's share of the row
+                const int c0 = C::kHalves == 2 ? grp * W : 0, row = tile_row0 + r;
+                if constexpr (SPLIT) {  // a partial result: unscaled outputs, reference and sum
+                    constexpr int R = C::kTiles * kM;
+                    float* part = a.partial + (((static_cast<size_t>(seq) * a.n_kv_heads + h) * (gridDim.z / sp.n) + block_tile) *
+                                                   sp.n + split) * (static_cast<size_t>(R) * (D + 2));
+                    const int rr = t * kM + r;
 #pragma unroll 1
-                for (int c = 0; c < W; c += 32) {
-                    float v[32];
-                    if (n_tiles > 0) tmem_ld32(t_out + c0 + c, v);
+                    for (int c = 0; c < W; c += 32) {
+                        float v[32];
+                        if (n_tiles > 0) tmem_ld32(t_out + c0 + c, v);
+                        if (rr < n_rows) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float x[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = n_tiles > 0 ? v[e + k] * inv : 0.0f;
-                        Vec16<__nv_bfloat16>::store(reinterpret_cast<__nv_bfloat16*>(mine) + c + e, x);
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4*>(part + static_cast<size_t>(rr) * D + c0 + c + e) =
+                                    n_tiles > 0 ? make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_float4(0, 0, 0, 0);
+                        }
                     }
-                }
-                fence_proxy_async_smem();
-                if (t * kM + r < n_rows) {
-                    bulk_store_1d(static_cast<__nv_bfloat16*>(a.out) +
-                                      (static_cast<size_t>(q0 + row / G) * a.n_q_heads + h * G + row % G) * D + c0,
-                                  mine, 2 * W);
-                    bulk_commit();
-                    bulk_wait_read();
+                    if (rr < n_rows && c0 == 0) {
+                        part[static_cast<size_t>(R) * D + rr] = m;
+                        part[static_cast<size_t>(R) * D + R + rr] = l;
+                    }
+                } else {
+                    // through the K and V buffers, whose products are done, so that a row leaves as one piece
+                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                    constexpr int PITCH = 2 * D + 16;  // 16 bytes more: rows in different banks
+                    static_assert(C::kTiles * kM * PITCH <= 2 * kStages * C::kTile, "the buffers hold the output");
+                    uint8_t* mine = smem + (t * kM + r) * PITCH + 2 * c0;
+#pragma unroll 1
+                    for (int c = 0; c < W; c += 32) {
+                        float v[32];
+                        if (n_tiles > 0) tmem_ld32(t_out + c0 + c, v);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            float x[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) x[k] = n_tiles > 0 ? v[e + k] * inv : 0.0f;
+                            Vec16<__nv_bfloat16>::store(reinterpret_cast<__nv_bfloat16*>(mine) + c + e, x);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    if (t * kM + r < n_rows) {
+                        bulk_store_1d(static_cast<__nv_bfloat16*>(a.out) +
+                                          (static_cast<size_t>(q0 + row / G) * a.n_q_heads + h * G + row % G) * D + c0,
+                                      mine, 2 * W);
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
                 }
             }
         }
@@ -703,44 +731,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
     if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
 }
 
-template <typename F, int D>
-cudaError_t prompt_t(const KvAttnArgs& a, cudaStream_t st) {
+template <typename F, int D, bool SPLIT>
+cudaError_t prompt_s(const KvAttnArgs& a, const KvPrompt& c, cudaStream_t st) {
     using C = PCfg<D>;
     static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = allow_smem(kv_prompt_kernel<F, D>, C::kSmem, ready);
+    const cudaError_t e = allow_smem(kv_prompt_kernel<F, D, SPLIT>, C::kSmem, ready);
     if (e != cudaSuccess) return e;
-    const long long tiles = (static_cast<long long>(a.b.max_q) * (a.n_q_heads / a.n_kv_heads) + C::kTiles * kM - 1) / (C::kTiles * kM);
     return timed_launch("kv_prompt", st, [&] {
-        kv_prompt_kernel<F, D><<<dim3(a.n_kv_heads, a.b.n_seq, static_cast<unsigned>(tiles)), kThreads, C::kSmem, st>>>(a);
+        kv_prompt_kernel<F, D, SPLIT>
+            <<<dim3(a.n_kv_heads, a.b.n_seq, c.tiles * c.split.n), kThreads, C::kSmem, st>>>(a, c.split);
         return cudaGetLastError();
     });
 }
 
+template <typename F, int D>
+cudaError_t prompt_t(const KvAttnArgs& a, const KvPrompt& c, cudaStream_t st) {
+    if (c.split.n == 1) return prompt_s<F, D, false>(a, c, st);
+    const cudaError_t e = prompt_s<F, D, true>(a, c, st);
+    return e != cudaSuccess ? e : launch_kv_join(a, c.split, c.rows, c.tiles, D, st);
+}
+
 template <typename F>
-cudaError_t prompt_d(const KvAttnArgs& a, int head_dim, cudaStream_t st) {
-    return head_dim == 64 ? prompt_t<F, 64>(a, st) : head_dim == 128 ? prompt_t<F, 128>(a, st) : prompt_t<F, 256>(a, st);
+cudaError_t prompt_d(const KvAttnArgs& a, const KvPrompt& c, int head_dim, cudaStream_t st) {
+    return head_dim == 64    ? prompt_t<F, 64>(a, c, st)
+           : head_dim == 128 ? prompt_t<F, 128>(a, c, st)
+                             : prompt_t<F, 256>(a, c, st);
 }
 
 }  // namespace
 
-// Whole tiles of 128 rows pay once there are enough of them to occupy a fair
-// part of the SMs (their keys are not split): below that the kernel for few
-// rows spreads the keys.  Wider heads pay earlier, since that kernel takes
-// them in narrower tiles.  Tiles (of all heads and sequences): microseconds
-// here against there, over calls of 0 to 8000 keys of context,
-//   head_dim  64:  8: 132 / 54, 32: 60 / 45, 38: 12.8 / 15.1 to 42.5 / 38.9, 80: 76 / 99;
-//   head_dim 128:  8: 67 / 79 to 165 / 91, 16: 167 / 97, 32: 69 / 73, 38: 53 / 71, 80: 93 / 168;
-//   head_dim 256:  8: 68 / 65 to 127 / 87, 16: 128 / 142, 32: 69 / 95, 38: 73 / 177, 80: 73 / 277.
-// The grid's third dimension bounds the tiles.
-bool kv_prompt_serves(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, bool bf16) {
-    const long long rows = static_cast<long long>(max_q) * (n_q_heads / n_kv_heads);
-    const long long tiles = (rows + kM - 1) / kM;
-    const int least = head_dim == 64 ? 40 : head_dim == 128 ? 32 : 16;
-    return bf16 && rows > 32 && tiles <= 65535 && tiles * n_kv_heads * n_seq >= least;
+// Which calls this kernel takes, and how it splits their keys.
+//
+// Below 17 rows (33 at head_dim 64) the kernel for few rows reads each code once
+// in one tile, and wins where there are many: 64 sequences of 8 kv heads with 32
+// rows and 4000 keys take it 150 us at head_dim 64, this one 240 us; at head_dim
+// 128 263 and 266 us, at 256, where it has two tiles of 16 rows, 440 and 304 us.
+// Above that this one wins once there is enough work for its longer start: 2^19
+// row and key pairs (head_dim 128, here against there: 16.4 / 12.3 us at 0.25 M
+// pairs, 14.0 / 14.5 at 0.5 M, 14.9 / 22.5 at 1 M, 27 / 70 us at 4 M), or 16 tiles
+// of 128 rows (16 sequences of 128 rows and 116 keys, 0.24 M pairs: 10.3 / 13.0).
+//
+// A call with fewer thread blocks than SMs splits its keys into as many ranges as
+// fill them once (38 blocks, 8000 keys, head_dim 256: 130 / 80 / 61 / 52 us in 1 to
+// 4 ranges, 72 us in 6), of two steps of 64 keys at least, if that takes 12 steps
+// off each block: partial results and the join cost about as much (32 blocks of 18
+// steps, head_dim 128: 33 us, 26 us in 4 ranges; 64 blocks: 33 us, 34 us in 2).
+// More than 32 ranges need the join's widest form (2 blocks of 8000 keys, head_dim
+// 256: 16.5 us in 32, 23 us in 48), which pays for a single block with a long axis
+// (30,000 keys, head_dim 64 / 128 / 256: 22 / 24 / 26 us in 32, 13 / 19 / 21 us in 152).
+KvPrompt kv_prompt_plan(int n_seq, int max_q, int n_q_heads, int n_kv_heads, int head_dim, int window, bool bf16,
+                        long long max_kv_len) {
+    KvPrompt p{};
+    const long long G = n_q_heads / n_kv_heads, rows = max_q * G, heads = static_cast<long long>(n_kv_heads) * n_seq;
+    if (!bf16 || rows <= (head_dim == 64 ? 32 : 16)) return p;
+    p.rows = kM * (head_dim == 256 ? PCfg<256>::kTiles : PCfg<128>::kTiles);
+    long long keys = std::max(1LL, max_kv_len);  // that a thread block walks
+    if (window) keys = std::min(keys, window + p.rows / G + 1LL + kKeys);
+    const bool many = rows > 32 && (rows + kM - 1) / kM * heads >= 16;
+    if (!many && static_cast<double>(rows) * heads * keys < 1 << 19) return p;
+    const long long tiles = (rows + p.rows - 1) / p.rows, blocks = tiles * heads, steps = (keys + kKeys - 1) / kKeys;
+    const long long most = blocks == 1 && steps > 8 * 32 ? 152 : 32;
+    const long long n = std::max(1LL, std::min({152 / blocks, steps / 2, most}));
+    long long each = (steps + n - 1) / n;
+    if (steps - each < 12) each = steps;
+    p.split = KvSplit{static_cast<int>((steps + each - 1) / each), static_cast<int>(std::min(each * kKeys, 0x7fffffffLL / kKeys * kKeys))};
+    if (tiles * p.split.n <= 65535) p.tiles = static_cast<int>(tiles);  // the grid's third dimension
+    return p;
 }
 
-cudaError_t launch_kv_prompt(const KvAttnArgs& a, int head_dim, bool e4m3, cudaStream_t stream) {
-    return e4m3 ? prompt_d<KvE4m3>(a, head_dim, stream) : prompt_d<KvInt8>(a, head_dim, stream);
+cudaError_t launch_kv_prompt(const KvAttnArgs& a, const KvPrompt& c, int head_dim, bool e4m3, cudaStream_t stream) {
+    return e4m3 ? prompt_d<KvE4m3>(a, c, head_dim, stream) : prompt_d<KvInt8>(a, c, head_dim, stream);
 }
 
 cudaError_t read_kv_prompt_error(int* code, bool reset) {
