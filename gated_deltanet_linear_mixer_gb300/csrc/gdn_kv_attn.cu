@@ -711,11 +711,10 @@ int tiles_of_8(int head_dim, long long rows) {
 // How many ranges the keys are split into.  Several rounds of thread blocks over
 // the SMs' 456 places even out ragged lengths, but a range's fixed cost (its
 // queries, its partial result) counts from about 16 thread blocks an SM on: 256
-// sequences of 127..8191 keys, head_dim 256, take 224 / 196 / 193 / 195 us at
-// 1024 / 2048 / 3072 / 4096 blocks, 64 x 4 drafts of head_dim 128 118 / 107 / 114
-// / 118 us.  One sequence is split down to one step a warp (1000 keys: 7.3 us;
-// 9.3 us at 128 keys a range), 131,000 keys into half a round (31 us; 36 us at 76
-// ranges).
+// sequences of 127..8191 keys, head_dim 256, take 224 / 196 / 195 us at 1024 /
+// 2048 / 4096 blocks, 64 x 4 drafts of head_dim 128 118 / 107 / 118 us.  One
+// sequence is split down to one step a warp (1000 keys: 7.3 us; 9.3 us at 128 keys
+// a range), 131,000 keys into half a round (31 us; 36 us at 76 ranges).
 constexpr int kMinChunk = kStepKeys;
 constexpr long long kTargetBlocks = 152 * 16, kMostSplits = 228;
 static_assert(kMostSplits <= 32 * kJoinEach, "the join holds this many splits");
