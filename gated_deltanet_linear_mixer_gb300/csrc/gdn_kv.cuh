@@ -51,6 +51,22 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     return y;
 }
 
+// Values of a block whose scale is 0 add nothing to the output, but their weights
+// count in the softmax's sum, as 2^(score - reference).  They move the reference
+// only as if their scale were 2^-kZeroLog: values of a larger one lift it as soon
+// as they come, and keep their weights' bits.  (A weight of the sum is then at
+// most 2^(15 + kZeroLog), and 2^21 of them are an fp32 number.)
+constexpr float kZeroLog = 90.0f;
+
+// 2^x, x <= 0, in two factors, neither of which is flushed to 0 before 2^-200: the
+// sums above span more than fp32's normal numbers reach to one side.
+struct Pow2Pair {
+    float a, b;
+};
+__device__ __forceinline__ Pow2Pair exp2_pair(float x) {
+    return Pow2Pair{exp2_ftz(fmaxf(x, -100.0f)), exp2_ftz(fminf(x + 100.0f, 0.0f))};
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);

@@ -251,7 +251,6 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     const int n_steps = begin < end ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
     const int min_pos = t.start + t.row0 / G;
     int steps = 0, key0 = 0;
-    float vs_low = INFINITY;
     auto fetch = [&](int i) {
         if (i < steps) {
             const int key = key0 + i * kStepKeys, page = look_page[i];
@@ -304,17 +303,11 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             const size_t block = static_cast<size_t>(page) * a.n_kv_heads + t.h;
             ks = a.c.k_scale[block];
             vs = a.c.v_scale[block];
-            if (vs > 0.0f) vs_low = fminf(vs_low, vs);
         }
-        // Values of a scale of 0 add nothing to the output but count in the sum: such a group
-        // is given the smallest scale in sight, so that it does not lift m, and a mark.
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
-        const bool zero = vs == 0.0f;
-        if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
+        const bool zero = vs == 0.0f;  // marked by a negative reciprocal
         look_k[lane] = ks;
-        look_lv[lane] = log2f(vs);
-        look_inv[lane] = (zero ? -1.0f : 1.0f) / vs;
+        look_lv[lane] = zero ? 0.0f : log2f(vs);
+        look_inv[lane] = zero ? -1.0f : 1.0f / vs;
         __syncwarp();
     };
     if (n_steps > 0) open_span(0);
@@ -436,6 +429,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             }
             const float ks = look_k[i], lv = look_lv[i], mark = look_inv[i], inv = fabsf(mark);
             const bool whole = key + kGroup - 1 <= min_pos && key >= max_lo && key + kGroup <= end;
+            const float drop = mark < 0.0f ? kZeroLog : 0.0f;
             bool lift = false;
             float top[NQ][2];
 #pragma unroll
@@ -455,7 +449,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                         }
                         s[0][n][2 * k + c] = v[k];
                     }
-                    top[n][c] = fmaxf(v[0], v[1]);
+                    top[n][c] = fmaxf(v[0], v[1]) - drop;
                     lift |= top[n][c] > m[n][c] + kLazy;
                 }
             if (__any_sync(0xffffffffu, lift)) {
@@ -467,10 +461,11 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
                         mn = fmaxf(m[n][c], mn);
-                        const float f = m[n][c] == -INFINITY ? 0.0f : exp2_ftz(m[n][c] - mn);
+                        const Pow2Pair f2 = m[n][c] == -INFINITY ? Pow2Pair{0.0f, 0.0f} : exp2_pair(m[n][c] - mn);
+                        const float f = f2.a * f2.b;
                         m[n][c] = mn;
                         if (fresh) continue;
-                        l[n][c] *= f;
+                        l[n][c] = l[n][c] * f2.a * f2.b;
 #pragma unroll
                         for (int i2 = 0; i2 < MT; ++i2) {
                             o[i2][n][c] *= f;
@@ -591,7 +586,8 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float mw = part_m[w * R + row];
-            sum += mw == -INFINITY ? 0.0f : part_l[w * R + row] * exp2_ftz(mw - top);
+            const Pow2Pair f = exp2_pair(mw - top);
+            sum += mw == -INFINITY ? 0.0f : part_l[w * R + row] * f.a * f.b;
         }
         if (sp.n > 1) {
             *reinterpret_cast<float4*>(part + row * D + d) = x;
@@ -648,8 +644,9 @@ kv_attn_join(const KvAttnArgs a, const Split sp, const int rows, const int n_til
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < kJoinEach; ++k) {
-        const float c = ms[k] == -INFINITY ? 0.0f : exp2_ftz(ms[k] - top);
-        sum += ls[k] * c;
+        const Pow2Pair f = ms[k] == -INFINITY ? Pow2Pair{0.0f, 0.0f} : exp2_pair(ms[k] - top);
+        const float c = f.a * f.b;
+        sum += ls[k] * f.a * f.b;
         x.x += vs[k].x * c; x.y += vs[k].y * c; x.z += vs[k].z * c; x.w += vs[k].w * c;
     }
     if (GROUPS > 1) {
@@ -668,9 +665,10 @@ kv_attn_join(const KvAttnArgs a, const Split sp, const int rows, const int n_til
         x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
         for (int w = 0; w < GROUPS; ++w) {
-            const float c = sm[here][w] == -INFINITY ? 0.0f : exp2_ftz(sm[here][w] - top);
+            const Pow2Pair f = sm[here][w] == -INFINITY ? Pow2Pair{0.0f, 0.0f} : exp2_pair(sm[here][w] - top);
+            const float c = f.a * f.b;
             const float4 v = sx[here][w][lane];
-            sum += sl[here][w] * c;
+            sum += sl[here][w] * f.a * f.b;
             x.x += v.x * c; x.y += v.y * c; x.z += v.z * c; x.w += v.w * c;
         }
     }

@@ -418,15 +418,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                         top = fmaxf(top, sh.swap[grp ^ 1][r]);
                     }
                     const float mn = fmaxf(m, top);
-                    f = m == -INFINITY ? 0.0f : exp2_ftz(m - mn);
+                    const Pow2Pair f2 = m == -INFINITY ? Pow2Pair{0.0f, 0.0f} : exp2_pair(m - mn);
+                    f = f2.a * f2.b;
                     m = mn;
-                    l *= f;
+                    l = l * f2.a * f2.b;
                 }
                 const float ref = m == -INFINITY ? 0.0f : m - kBias;
                 uint32_t p[NC / 2];
-                const uint64_t ref2 = pair(-ref, -ref);
 #pragma unroll
                 for (int g = 0; g < NC / 16; ++g) {
+                    const float up = gc[g].inv < 0.0f ? kZeroLog - ref : -ref;
+                    const uint64_t ref2 = pair(up, up);
                     uint64_t sums = 0;  // 0.0f twice
 #pragma unroll
                     for (int j = 16 * g; j < 16 * g + 16; j += 2) {
@@ -617,28 +619,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
         // ---- look-ups, kPass tiles of groups at a time, two passes ahead of their readers
         const bool place = warp == kPlaceWarp;
         uint64_t *full = place ? sh.l_full : sh.c_full, *empty = place ? sh.l_empty : sh.c_empty;
-        float vs_low = INFINITY;
         bool ok = true;
         for (int i0 = 0, pass = 0; ok && i0 < n_tiles; i0 += kPass, ++pass) {
             const int key = first + i0 * kKeys + 16 * lane, pg = page_of(key), hb = pass & 1;
             const size_t block = static_cast<size_t>(max(pg, 0)) * a.n_kv_heads + h;
             GroupConst g{0.0f, -INFINITY, 1.0f};
             if (!place) {
-                float vs = 1.0f;
                 if (pg >= 0) {
                     g.ks = a.c.k_scale[block];
-                    vs = a.c.v_scale[block];
-                    g.lv = 0.0f;
-                    if (vs > 0.0f) vs_low = fminf(vs_low, vs);
+                    const float vs = a.c.v_scale[block];
+                    g.lv = vs == 0.0f ? -kZeroLog : log2f(vs);
+                    g.inv = vs == 0.0f ? -1.0f : 1.0f / vs;
                 } else if (key < end && (!a.window || key + 15 > lo_pos - a.window)) {
                     prompt_fail(kKvErrTable);
                 }
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) vs_low = fminf(vs_low, __shfl_xor_sync(0xffffffffu, vs_low, off));
-                const bool zero = vs == 0.0f;  // such a group is given the smallest scale in sight, and a mark
-                if (zero) vs = vs_low < INFINITY ? vs_low : 1.0f;
-                g.lv += log2f(vs);
-                g.inv = (zero ? -1.0f : 1.0f) / vs;
             }
             if (pass >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&empty[hb], ((pass >> 1) - 1) & 1)))) {
                 if (lane == 0) prompt_fail(45);

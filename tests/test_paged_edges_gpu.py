@@ -1,0 +1,78 @@
+"""Edges of the paged-cache operators on the GPU: value scales of zero, subnormal and far apart,
+pages that a window has left behind, windows near 2^31.
+
+References and bounds are those of paged_cases.py; calls of many rows add the weights that f16
+drops, 2^-31 of the reference a key (2^-20 of the largest |value| for up to 2^11 keys)."""
+import pytest
+import torch
+
+import gated_deltanet_linear_mixer_gb300 as gdn
+from paged_cases import attention_excess, attention_ref, cu_of, gen, make_cache
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_deltanet_linear_mixer_gb300 import _build
+    _build.build()
+    gdn.load()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    gdn.device_error(reset=True)
+    yield
+    assert gdn.device_error(reset=True) == 0
+
+
+FORMS = {
+    # name: (Hq, Hkv, D, dtype, queries, kernels of a call that ends at position 1600)
+    "few": (16, 2, 128, BF, [1], {"kv_attn", "kv_attn_join"}),
+    "few_f32": (16, 2, 256, F32, [3], {"kv_attn", "kv_attn_join"}),
+    "prompt": (32, 8, 128, BF, [600], {"kv_prompt"}),
+    "prompt_d256": (32, 8, 256, BF, [300], {"kv_prompt"}),
+    "split": (16, 2, 128, BF, [40], {"kv_prompt", "kv_attn_join"}),
+    "split_d256": (16, 2, 256, BF, [40], {"kv_prompt", "kv_attn_join"}),
+}
+
+
+def _call(d, cache, table, counts, kv, q, kernels):
+    lens = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    gdn.timing_enable(True)
+    out = gdn.kv_attention(d, cache, cu_of(counts), lens, table, q)
+    report = gdn.timing_report()
+    gdn.timing_enable(False)
+    assert set(report) == kernels, report
+    return out
+
+
+def _excess(d, cache, table, counts, kv, q, out):
+    ref, size, s = attention_ref(d, cache, table, counts, kv, q)
+    if d.dtype == F32:
+        return attention_excess(d, out, ref, size, s)
+    got = out.double()
+    assert torch.isfinite(got).all()
+    values = torch.stack([cache.v[p].float().abs().amax((1, 2)) * cache.v_scale[p] for p in table[0].tolist() if p >= 0])
+    tol = 2.0 ** -9 * size + 2.0 ** -8 * got.abs() + 2.0 ** -20 * float(values.max())
+    return float(((got - ref).abs() / tol.clamp(min=1e-36)).max())
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("power", [-20, -40, -80, 0, 60])
+def test_values_after_many_keys_of_zeros(form, power):
+    """1280 keys whose values are all zero, then values of scale 2^power: the zeros count in the
+    softmax's sum and leave the others' weights their precision."""
+    hq, hkv, dim, dtype, counts, kernels = FORMS[form]
+    d = gdn.KVDims(hq, hkv, dim, page_size=64, dtype=dtype)
+    kv = [1600]
+    cache, table = make_cache(d, kv, 81)
+    pages = table[0].long()
+    cache.v_scale[pages[:20]] = 0.0
+    cache.v_scale[pages[20:]] *= 2.0 ** power
+    q = (torch.randn(sum(counts), hq, dim, generator=gen(82), device="cuda") * 0.3).to(dtype)
+    out = _call(d, cache, table, counts, kv, q, kernels)
+    assert out.any()
+    assert _excess(d, cache, table, counts, kv, q, out) <= 1.0
