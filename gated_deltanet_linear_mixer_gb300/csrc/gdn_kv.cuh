@@ -57,6 +57,10 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 // as they come, and keep their weights' bits.  (A weight of the sum is then at
 // most 2^(15 + kZeroLog), and 2^21 of them are an fp32 number.)
 constexpr float kZeroLog = 90.0f;
+// Scales below 2^-kZeroLog count as 0: a reciprocal of up to 2^kZeroLog leaves a
+// sum of 2^21 weights an fp32 number (that of a subnormal scale is infinite).  What
+// is lost is below 2^-81 in magnitude.
+__device__ __forceinline__ bool zero_scale(float s) { return s >= 0.0f && s < 8.07793567e-28f; }
 
 // 2^x, x <= 0, in two factors, neither of which is flushed to 0 before 2^-200: the
 // sums above span more than fp32's normal numbers reach to one side.

@@ -304,7 +304,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             ks = a.c.k_scale[block];
             vs = a.c.v_scale[block];
         }
-        const bool zero = vs == 0.0f;  // marked by a negative reciprocal
+        const bool zero = zero_scale(vs);  // marked by a negative reciprocal
         look_k[lane] = ks;
         look_lv[lane] = zero ? 0.0f : log2f(vs);
         look_inv[lane] = zero ? -1.0f : 1.0f / vs;

@@ -628,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 if (pg >= 0) {
                     g.ks = a.c.k_scale[block];
                     const float vs = a.c.v_scale[block];
-                    g.lv = vs == 0.0f ? -kZeroLog : log2f(vs);
-                    g.inv = vs == 0.0f ? -1.0f : 1.0f / vs;
+                    g.lv = zero_scale(vs) ? -kZeroLog : log2f(vs);
+                    g.inv = zero_scale(vs) ? -1.0f : 1.0f / vs;
                 } else if (key < end && (!a.window || key + 15 > lo_pos - a.window)) {
                     prompt_fail(kKvErrTable);
                 }

@@ -419,7 +419,7 @@ gdn_status gdn_kv_read(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
  * small for that, two bf16 terms (16 bits); calls of many rows (prompts) keep to
  * f16 and drop weights below 2^-31 of a row's reference, which lies within 2^8
  * of its largest.  fp32 activations: queries are f16 (hi, lo) pairs, weights
- * three bf16 terms.
+ * three bf16 terms.  Values whose block has a scale below 2^-90 count as 0.
  */
 gdn_status gdn_kv_attention_workspace_size(const gdn_kv_dims* dims, int32_t n_seq,
                                            const int32_t* cu_seqlens_host, int32_t max_kv_len,

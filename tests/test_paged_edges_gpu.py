@@ -76,3 +76,23 @@ def test_values_after_many_keys_of_zeros(form, power):
     out = _call(d, cache, table, counts, kv, q, kernels)
     assert out.any()
     assert _excess(d, cache, table, counts, kv, q, out) <= 1.0
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("tiny", [1e-39, 1e-45, 2.0 ** -100])
+def test_pages_of_tiny_values_beside_ordinary_ones(form, tiny):
+    """Value scales whose reciprocal is no fp32 number, as appended values near the smallest normal
+    numbers have them, among scales of ordinary size and of zero."""
+    hq, hkv, dim, dtype, counts, kernels = FORMS[form]
+    d = gdn.KVDims(hq, hkv, dim, page_size=64, dtype=dtype)
+    kv = [1600]
+    for zeros in (False, True):
+        cache, table = make_cache(d, kv, 83)
+        pages = table[0].long()
+        cache.v_scale[pages[3]] = tiny
+        cache.v_scale[pages[22]] = tiny
+        if zeros:
+            cache.v_scale[pages[4]] = 0.0
+        q = (torch.randn(sum(counts), hq, dim, generator=gen(84), device="cuda") * 0.3).to(dtype)
+        out = _call(d, cache, table, counts, kv, q, kernels)
+        assert _excess(d, cache, table, counts, kv, q, out) <= 1.0
