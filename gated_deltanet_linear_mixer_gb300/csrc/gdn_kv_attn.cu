@@ -250,6 +250,9 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * 2 * C::kTile;
     const int n_steps = begin < end ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
     const int min_pos = t.start + t.row0 / G;
+    // Groups that end here or before are behind every row's window: their entries are not followed,
+    // since what they point to may be another sequence's by now, or no numbers.
+    const int behind = a.window ? max(min_pos, -1) - a.window : -1;
     int steps = 0, key0 = 0;
     auto fetch = [&](int i) {
         if (i < steps) {
@@ -282,11 +285,10 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
         key0 = begin + span * kStepKeys + warp * kGroup;
         const int key = key0 + lane * kStepKeys;
         int page = -1;
-        if (lane < steps && key < end) {
+        if (lane < steps && key < end && key + kGroup - 1 > behind) {
             page = a.b.table[static_cast<size_t>(t.seq) * a.b.pages_per_seq + key / a.page_size];
             if (page < 0 || page >= a.c.n_pages) {
-                // needed unless every row's window has left it behind
-                if (!a.window || key + kGroup - 1 > min_pos - a.window) atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
+                atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
                 page = -1;
             }
         }

@@ -293,8 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem_slot;
-    auto page_of = [&](int key) {  // negative: past the end, or not mapped
-        if (key >= end) return -1;
+    // groups of keys that end here or before are behind every row's window: their entries are not followed
+    const int behind = a.window ? max(lo_pos, -1) - a.window : -1;
+    auto page_of = [&](int key) {  // negative: past the end, behind, or not mapped
+        if (key >= end || key + 15 <= behind) return -1;
         const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + key / a.page_size];
         return page < a.c.n_pages ? page : -1;
     };
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                     const float vs = a.c.v_scale[block];
                     g.lv = zero_scale(vs) ? -kZeroLog : log2f(vs);
                     g.inv = zero_scale(vs) ? -1.0f : 1.0f / vs;
-                } else if (key < end && (!a.window || key + 15 > lo_pos - a.window)) {
+                } else if (key < end && key + 15 > behind) {
                     prompt_fail(kKvErrTable);
                 }
             }

@@ -407,7 +407,9 @@ gdn_status gdn_kv_read(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
  *   o_t = sum_j p_tj v_j,  p_t = softmax_j(scale q_t . k_j)
  * over max(0, P - window + 1) <= j <= P, P the query's position (window 0: all
  * j <= P).  A query that sees no key (its position is negative, or every page
- * it would see is unmapped) gives zeros.
+ * it would see is unmapped) gives zeros.  Block table entries of pages that lie
+ * before every query's window are not followed: such pages may have been given
+ * to other sequences.
  *   q [T, n_q_heads, head_dim] rows (rotated already), out [T, n_q_heads,
  *   head_dim] contiguous.  max_kv_len: at least every kv_lens[i]; it sets how
  *   the keys are split among thread blocks (a longer sequence is still

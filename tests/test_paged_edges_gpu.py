@@ -96,3 +96,28 @@ def test_pages_of_tiny_values_beside_ordinary_ones(form, tiny):
         q = (torch.randn(sum(counts), hq, dim, generator=gen(84), device="cuda") * 0.3).to(dtype)
         out = _call(d, cache, table, counts, kv, q, kernels)
         assert _excess(d, cache, table, counts, kv, q, out) <= 1.0
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("fmt,page", [("e4m3", 16), ("int8", 32)])
+def test_pages_left_behind_by_the_window_may_hold_anything(form, fmt, page):
+    """Pages before every query's window may have been given to other sequences: what their entries
+    point to (unwritten pages with scales and codes that are no numbers) does not reach a result."""
+    hq, hkv, dim, dtype, counts, _ = FORMS[form]
+    kv = [1600]
+    for window in (600, 601, 657):
+        d = gdn.KVDims(hq, hkv, dim, page_size=page, dtype=dtype, cache=fmt, window=window)
+        cache, table = make_cache(d, kv, 85)
+        q = torch.randn(sum(counts), hq, dim, generator=gen(86), device="cuda").to(dtype)
+        lens = torch.tensor(kv, dtype=torch.int32, device="cuda")
+        hints = (None, 64)  # 64: the keys in one range, as in a call of many sequences
+        clean = [gdn.kv_attention(d, cache, cu_of(counts), lens, table, q, max_kv_len=n) for n in hints]
+        assert all(_excess(d, cache, table, counts, kv, q, x) <= 1.0 for x in clean)
+        gone = max(0, kv[0] - counts[0] - window + 1) // page
+        old = table[0, :gone].long()
+        for x in (cache.k, cache.v):
+            x.view(torch.int8)[old] = 0x7F
+        for x in (cache.k_scale, cache.v_scale):
+            x[old] = float("nan")
+        for n, x in zip(hints, clean):
+            assert torch.equal(gdn.kv_attention(d, cache, cu_of(counts), lens, table, q, max_kv_len=n), x)
