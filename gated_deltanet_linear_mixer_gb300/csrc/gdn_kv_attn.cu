@@ -153,6 +153,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
+// Queries before position 0 see nothing.  They are all taken to be at -1, so that
+// no position less a window leaves 32 bits.
+__device__ __forceinline__ int position(int p) { return max(p, -1); }
+
 // The keys [first, last] that a thread block's rows may see, from their
 // positions; first is rounded down to a step.
 struct Range {
@@ -183,7 +187,7 @@ __device__ __forceinline__ bool tile_of(const KvAttnArgs& a, int rows, int tile,
     t.start = t.len - qn;
     const long long cap = static_cast<long long>(a.b.pages_per_seq) * a.page_size;
     if (t.len > cap) t.len = static_cast<int>(cap);
-    t.keys = key_range(t.start + t.row0 / G, t.start + (t.row0 + t.n_rows - 1) / G, t.len, a.window);
+    t.keys = key_range(position(t.start + t.row0 / G), position(t.start + (t.row0 + t.n_rows - 1) / G), t.len, a.window);
     return true;
 }
 
@@ -249,10 +253,10 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     // that the codes of the first groups are on their way before anything else is waited for.
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * 2 * C::kTile;
     const int n_steps = begin < end ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
-    const int min_pos = t.start + t.row0 / G;
+    const int min_pos = position(t.start + t.row0 / G);
     // Groups that end here or before are behind every row's window: their entries are not followed,
     // since what they point to may be another sequence's by now, or no numbers.
-    const int behind = a.window ? max(min_pos, -1) - a.window : -1;
+    const int behind = a.window ? min_pos - a.window : -1;
     int steps = 0, key0 = 0;
     auto fetch = [&](int i) {
         if (i < steps) {
@@ -367,7 +371,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             for (int n = 0; n < NQ; ++n) qf[C::kPair ? 0 : s][n] = load_q(s, 0, n);
 
     const int kr = 4 * (g >> 1) + (g & 1);  // this lane's keys of a group: kr, and kr + 2
-    const int max_lo = a.window ? t.start + (t.row0 + t.n_rows - 1) / G - a.window + 1 : 0;
+    const int max_lo = a.window ? position(t.start + (t.row0 + t.n_rows - 1) / G) - a.window + 1 : 0;
     float o[MT][NQ][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -446,7 +450,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                         if (CH > 1) x += s[CH - 1][n][2 * k + c];
                         v[k] = fmaf(x, f, lv);
                         if (!whole) {
-                            const int j = key + kr + 2 * k, pos = t.start + (t.row0 + 8 * n + 2 * t4 + c) / G;
+                            const int j = key + kr + 2 * k, pos = position(t.start + (t.row0 + 8 * n + 2 * t4 + c) / G);
                             if (j > pos || j >= end || (a.window && j <= pos - a.window)) v[k] = -INFINITY;
                         }
                         s[0][n][2 * k + c] = v[k];

@@ -243,7 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
         if (tid == 0) prompt_fail(kKvErrTable);
         len = static_cast<int>(cap);
     }
-    const int lo_pos = start + row0 / G, hi_pos = start + (row0 + n_rows - 1) / G;
+    // positions; queries before 0, which see nothing, are all taken to be at -1, so that no position less
+    // a window leaves 32 bits
+    const int lo_pos = max(start + row0 / G, -1), hi_pos = max(start + (row0 + n_rows - 1) / G, -1);
     // this thread block's range of the keys; the join does not read an empty one past the first
     const int all_first = a.window ? max(0, lo_pos - a.window + 1) / kKeys * kKeys : 0;
     const int span = max(0, min(hi_pos + 1, len) - all_first), from = SPLIT ? split * sp.chunk : 0;
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem_slot;
     // groups of keys that end here or before are behind every row's window: their entries are not followed
-    const int behind = a.window ? max(lo_pos, -1) - a.window : -1;
+    const int behind = a.window ? lo_pos - a.window : -1;
     auto page_of = [&](int key) {  // negative: past the end, behind, or not mapped
         if (key >= end || key + 15 <= behind) return -1;
         const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + key / a.page_size];
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             }
 
             // ---- softmax: a thread's row, all keys of a tile or 32 of them
-            const int pos = start + (tile_row0 + r) / G;
+            const int pos = max(start + (tile_row0 + r) / G, -1);
             const int my_lo = start + tile_row0 / G;  // the row tile's first position
             const int max_lo = a.window ? hi_pos - a.window + 1 : 0;
             const uint32_t t_score = tmem + t_lane + t * kKeys + (C::kHalves == 2 ? grp * NC : 0);

@@ -121,3 +121,18 @@ def test_pages_left_behind_by_the_window_may_hold_anything(form, fmt, page):
             x[old] = float("nan")
         for n, x in zip(hints, clean):
             assert torch.equal(gdn.kv_attention(d, cache, cu_of(counts), lens, table, q, max_kv_len=n), x)
+
+
+@pytest.mark.parametrize("counts", [[5], [300]])
+@pytest.mark.parametrize("dim", [128, 256])
+def test_the_widest_window_is_none(dim, counts):
+    """A window of 2^31 - 1 leaves nothing out, of sequences with more queries than positions either."""
+    kv = [counts[0] - 2]
+    d = gdn.KVDims(16, 8, dim, page_size=64)
+    wide = gdn.KVDims(16, 8, dim, page_size=64, window=2 ** 31 - 1)
+    cache, table = make_cache(d, kv, 87)
+    q = torch.randn(sum(counts), 16, dim, generator=gen(88), device="cuda").to(BF)
+    lens = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    a = gdn.kv_attention(d, cache, cu_of(counts), lens, table, q)
+    b = gdn.kv_attention(wide, cache, cu_of(counts), lens, table, q)
+    assert a[2:].any() and torch.equal(a, b)
