@@ -62,13 +62,10 @@ constexpr float kZeroLog = 90.0f;
 // is lost is below 2^-81 in magnitude.
 __device__ __forceinline__ bool zero_scale(float s) { return s >= 0.0f && s < 8.07793567e-28f; }
 
-// 2^x, x <= 0, in two factors, neither of which is flushed to 0 before 2^-200: the
-// sums above span more than fp32's normal numbers reach to one side.
-struct Pow2Pair {
-    float a, b;
-};
-__device__ __forceinline__ Pow2Pair exp2_pair(float x) {
-    return Pow2Pair{exp2_ftz(fmaxf(x, -100.0f)), exp2_ftz(fminf(x + 100.0f, 0.0f))};
+// l 2^x, x <= 0, given f = 2^x: the sums above span more than fp32's normal
+// numbers reach to one side, so that f may be flushed to 0 where the product is not.
+__device__ __forceinline__ float times_pow2(float l, float x, float f) {
+    return x >= -100.0f ? l * f : l * 7.88860905e-31f * exp2_ftz(x + 100.0f);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

@@ -254,9 +254,6 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * 2 * C::kTile;
     const int n_steps = begin < end ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
     const int min_pos = position(t.start + t.row0 / G);
-    // Groups that end here or before are behind every row's window: their entries are not followed,
-    // since what they point to may be another sequence's by now, or no numbers.
-    const int behind = a.window ? min_pos - a.window : -1;
     int steps = 0, key0 = 0;
     auto fetch = [&](int i) {
         if (i < steps) {
@@ -289,9 +286,13 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
         key0 = begin + span * kStepKeys + warp * kGroup;
         const int key = key0 + lane * kStepKeys;
         int page = -1;
-        if (lane < steps && key < end && key + kGroup - 1 > behind) {
+        if (lane < steps && key < end) {
             page = a.b.table[static_cast<size_t>(t.seq) * a.b.pages_per_seq + key / a.page_size];
-            if (page < 0 || page >= a.c.n_pages) {
+            if (a.window && key + kGroup - 1 <= min_pos - a.window) {
+                // behind every row's window: what the entry points to may be another sequence's by
+                // now, or no numbers
+                page = -1;
+            } else if (page < 0 || page >= a.c.n_pages) {
                 atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
                 page = -1;
             }
@@ -311,9 +312,10 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             vs = a.c.v_scale[block];
         }
         const bool zero = zero_scale(vs);  // marked by a negative reciprocal
+        if (zero) vs = 1.0f;
         look_k[lane] = ks;
-        look_lv[lane] = zero ? 0.0f : log2f(vs);
-        look_inv[lane] = zero ? -1.0f : 1.0f / vs;
+        look_lv[lane] = log2f(vs);
+        look_inv[lane] = (zero ? -1.0f : 1.0f) / vs;
         __syncwarp();
     };
     if (n_steps > 0) open_span(0);
@@ -435,7 +437,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             }
             const float ks = look_k[i], lv = look_lv[i], mark = look_inv[i], inv = fabsf(mark);
             const bool whole = key + kGroup - 1 <= min_pos && key >= max_lo && key + kGroup <= end;
-            const float drop = mark < 0.0f ? kZeroLog : 0.0f;
+            const float lazy = mark < 0.0f ? kLazy + kZeroLog : kLazy;
             bool lift = false;
             float top[NQ][2];
 #pragma unroll
@@ -455,8 +457,8 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                         }
                         s[0][n][2 * k + c] = v[k];
                     }
-                    top[n][c] = fmaxf(v[0], v[1]) - drop;
-                    lift |= top[n][c] > m[n][c] + kLazy;
+                    top[n][c] = fmaxf(v[0], v[1]);
+                    lift |= top[n][c] > m[n][c] + lazy;
                 }
             if (__any_sync(0xffffffffu, lift)) {
 #pragma unroll
@@ -466,12 +468,12 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                         float mn = top[n][c];
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-                        mn = fmaxf(m[n][c], mn);
-                        const Pow2Pair f2 = m[n][c] == -INFINITY ? Pow2Pair{0.0f, 0.0f} : exp2_pair(m[n][c] - mn);
-                        const float f = f2.a * f2.b;
+                        mn = fmaxf(m[n][c], mn - (lazy - kLazy));
+                        const float by = m[n][c] == -INFINITY ? 0.0f : m[n][c] - mn;  // l and o are 0 with -inf
+                        const float f = exp2_ftz(by);
                         m[n][c] = mn;
                         if (fresh) continue;
-                        l[n][c] = l[n][c] * f2.a * f2.b;
+                        l[n][c] = times_pow2(l[n][c], by, f);
 #pragma unroll
                         for (int i2 = 0; i2 < MT; ++i2) {
                             o[i2][n][c] *= f;
@@ -558,6 +560,18 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             }
         }
     __syncthreads();
+    float* row_l = q_scale;  // the rows' sums
+    if (tid < R) {
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * R + tid]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = part_m[w * R + tid], by = mw == -INFINITY ? 0.0f : mw - top;
+            sum += times_pow2(part_l[w * R + tid], by, exp2_ftz(by));
+        }
+        row_l[tid] = sum;
+    }
     float* all = reinterpret_cast<float*>(smem);  // [warp][row][kJoinPitch]
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -586,18 +600,13 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
             const float4 v = *reinterpret_cast<const float4*>(all + (w * R + row) * C::kJoinPitch + d);
             x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
         }
-        float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * R + row]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float mw = part_m[w * R + row];
-            const Pow2Pair f = exp2_pair(mw - top);
-            sum += mw == -INFINITY ? 0.0f : part_l[w * R + row] * f.a * f.b;
-        }
+        const float sum = row_l[row];
         if (sp.n > 1) {
             *reinterpret_cast<float4*>(part + row * D + d) = x;
             if (d == 0) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * R + row]);
                 part[R * D + row] = top;
                 part[R * D + R + row] = sum;
             }
@@ -646,14 +655,23 @@ kv_attn_join(const KvAttnArgs a, const Split sp, const int rows, const int n_til
     }
 #pragma unroll
     for (int k = 0; k < kJoinEach; ++k) top = fmaxf(top, ms[k]);
-    float sum = 0.0f;
+    float sum = 0.0f, low = 0.0f;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < kJoinEach; ++k) {
-        const Pow2Pair f = ms[k] == -INFINITY ? Pow2Pair{0.0f, 0.0f} : exp2_pair(ms[k] - top);
-        const float c = f.a * f.b;
-        sum += ls[k] * f.a * f.b;
+        const float by = ms[k] == -INFINITY ? 0.0f : ms[k] - top;  // its outputs and sum are 0 with -inf
+        const float c = exp2_ftz(by);
+        low = fminf(low, by);
+        sum += ls[k] * c;
         x.x += vs[k].x * c; x.y += vs[k].y * c; x.z += vs[k].z * c; x.w += vs[k].w * c;
+    }
+    if (low < -100.0f) {  // factors that are flushed where their products need not be
+        sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kJoinEach; ++k) {
+            const float by = ms[k] == -INFINITY ? 0.0f : ms[k] - top;
+            sum += times_pow2(ls[k], by, exp2_ftz(by));
+        }
     }
     if (GROUPS > 1) {
         __shared__ float sm[kUnits][GROUPS], sl[kUnits][GROUPS];
@@ -671,11 +689,18 @@ kv_attn_join(const KvAttnArgs a, const Split sp, const int rows, const int n_til
         x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
         for (int w = 0; w < GROUPS; ++w) {
-            const Pow2Pair f = sm[here][w] == -INFINITY ? Pow2Pair{0.0f, 0.0f} : exp2_pair(sm[here][w] - top);
-            const float c = f.a * f.b;
+            const float by = sm[here][w] == -INFINITY ? 0.0f : sm[here][w] - top, c = exp2_ftz(by);
             const float4 v = sx[here][w][lane];
-            sum += sl[here][w] * f.a * f.b;
+            low = fminf(low, by);
+            sum += sl[here][w] * c;
             x.x += v.x * c; x.y += v.y * c; x.z += v.z * c; x.w += v.w * c;
+        }
+        if (low < -100.0f) {
+            sum = 0.0f;
+            for (int w = 0; w < GROUPS; ++w) {
+                const float by = sm[here][w] == -INFINITY ? 0.0f : sm[here][w] - top;
+                sum += times_pow2(sl[here][w], by, exp2_ftz(by));
+            }
         }
     }
     if (mine) store_row<T, D>(a, t, t.row0 + row, d, x, sum > 0.0f ? 1.0f / sum : 0.0f);

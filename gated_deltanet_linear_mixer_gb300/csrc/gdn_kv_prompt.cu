@@ -422,10 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                         top = fmaxf(top, sh.swap[grp ^ 1][r]);
                     }
                     const float mn = fmaxf(m, top);
-                    const Pow2Pair f2 = m == -INFINITY ? Pow2Pair{0.0f, 0.0f} : exp2_pair(m - mn);
-                    f = f2.a * f2.b;
+                    const float by = m == -INFINITY ? 0.0f : m - mn;  // l and the output are 0 with -inf
+                    const float half = exp2_ftz(0.5f * by);  // the sum's factor may lie below fp32's normal numbers
+                    f = half * half;
                     m = mn;
-                    l = l * f2.a * f2.b;
+                    l = l * half * half;
                 }
                 const float ref = m == -INFINITY ? 0.0f : m - kBias;
                 uint32_t p[NC / 2];
