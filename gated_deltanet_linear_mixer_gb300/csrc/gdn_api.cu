@@ -201,6 +201,7 @@ void drain_pending_locked() {
 namespace gdn {
 
 gdn_status inject_fault(const char* site, const char* fn) { return injected(site, fn); }
+bool fault_site(const char* site) { return fault_listed(site); }
 
 gdn_status set_error(gdn_status st, const char* fn, const char* fmt, ...) {
     int n = std::snprintf(g_err, sizeof(g_err), "%s: ", fn);

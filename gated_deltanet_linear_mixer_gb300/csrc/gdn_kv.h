@@ -63,6 +63,7 @@ struct KvAttnArgs {
     void* out;
     float* partial;   // split partials (workspace), see gdn_kv_attn.cu
     int max_kv_len;
+    int stall;        // test hook: the kernel for many rows waits for look-ups that never come
 };
 
 struct AcceptArgs {

@@ -13,6 +13,7 @@ gdn_status set_error(gdn_status st, const char* fn, const char* fmt, ...);
 void clear_error();
 // GDN_ERR_INJECTED when the environment variable GDN_FAULT lists `site`.
 gdn_status inject_fault(const char* site, const char* fn);
+bool fault_site(const char* site);  // whether it does
 }  // namespace gdn
 
 using gdn::set_error;
@@ -231,6 +232,7 @@ gdn_status gdn_kv_attention(const gdn_kv_dims* dims, const gdn_kv_cache* cache, 
     a.n_q_heads = dims->n_q_heads; a.n_kv_heads = dims->n_kv_heads; a.page_size = dims->page_size;
     a.window = dims->window; a.scale = dims->scale; a.out = out; a.partial = static_cast<float*>(workspace);
     a.max_kv_len = max_kv_len;
+    a.stall = gdn::fault_site("stall_attention") ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(gdn::launch_kv_attention(a, dims->head_dim, dims->dtype == GDN_DTYPE_BF16,
                                                 dims->format == GDN_KV_E4M3, s), fn, "attention launch");

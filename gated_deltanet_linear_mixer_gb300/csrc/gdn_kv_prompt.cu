@@ -569,8 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
             const int hb = i / kPass & 1;
             if (i % kPass == 0 && ok)
                 ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.l_full[hb], (i / (2 * kPass)) & 1));
+            // keys from this lane's first row on; none once a wait gave up, after which the places may be anything
             const long long at = sh.place[i % (2 * kPass)][cw];
-            const int left = at >= 0 ? end - (first + i * kKeys + 16 * cw + r_in) : 0;  // keys from this lane's first row on
+            const int left = at >= 0 && ok ? end - (first + i * kKeys + 16 * cw + r_in) : 0;
             if (i % kPass == kPass - 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.l_empty[hb]);
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
         };
 #pragma unroll
         for (int b = 0; b < 2; ++b) load(b, b);
-        if (C::kQInTmem && !is_v) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_staged, 0));  // read out of them
+        if (C::kQInTmem && !is_v && ok) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_staged, 0));  // read out of them
         int stage = 0, round = 0;
         for (int i0 = 0; ok && i0 < n_tiles; i0 += 2) {
 #pragma unroll
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
         // ---- look-ups, kPass tiles of groups at a time, two passes ahead of their readers
         const bool place = warp == kPlaceWarp;
         uint64_t *full = place ? sh.l_full : sh.c_full, *empty = place ? sh.l_empty : sh.c_empty;
-        bool ok = true;
+        bool ok = !(place && a.stall);  // the test hook: no place is ever published
         for (int i0 = 0, pass = 0; ok && i0 < n_tiles; i0 += kPass, ++pass) {
             const int key = first + i0 * kKeys + 16 * lane, pg = page_of(key), hb = pass & 1;
             const size_t block = static_cast<size_t>(max(pg, 0)) * a.n_kv_heads + h;

@@ -44,11 +44,13 @@
  *   commit, layer, kv_append, kv_read, kv_attention, accept, or all.  A call
  *   whose site is listed validates its arguments, then returns
  *   GDN_ERR_INJECTED without enqueuing anything, so every caller buffer is
- *   left as it was.  The site stall_scan is a device
- *   test hook: a bf16 prefill that takes the fused tensor-core launch makes
- *   its scan wait (for at most 1 ms) on a chunk flag that nothing sets, so
- *   that the bounded wait runs out; the call returns GDN_OK and the next
- *   gdn_sync_status reports GDN_ERR_TIMEOUT.  GDN_FAULT is read on every call.
+ *   left as it was.  Two sites are device test hooks, under which a bounded
+ *   wait runs out, the call returns GDN_OK and the next gdn_sync_status
+ *   reports GDN_ERR_TIMEOUT: stall_scan (a bf16 prefill that takes the fused
+ *   tensor-core launch makes its scan wait, for at most 1 ms, on a chunk flag
+ *   that nothing sets) and stall_attention (a gdn_kv_attention call that takes
+ *   the kernel for many rows waits, for 2 s, for page look-ups that are never
+ *   published).  GDN_FAULT is read on every call.
  */
 #ifndef GDN_H
 #define GDN_H

@@ -1,0 +1,66 @@
+"""Failure detection of the cache operators on the GPU, made without faulting the GPU: a bounded
+wait of the kernel for many rows runs out (GDN_FAULT=stall_attention: its look-up warp publishes
+nothing, for which the others wait 2 s).  Every role gives up without using what did not come, the
+kernel ends, gdn_sync_status reports GDN_ERR_TIMEOUT, and the next call computes correct results.
+"""
+import pytest
+import torch
+
+import gated_deltanet_linear_mixer_gb300 as gdn
+from paged_cases import attention_excess, attention_ref, cu_of, gen, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_deltanet_linear_mixer_gb300 import _build
+    _build.build()
+    gdn.load()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    gdn.device_error(reset=True)
+    yield
+    gdn.device_error(reset=True)
+
+
+def _inputs(dim, seed):
+    """Few enough row tiles (32 of 128 rows) to run all at once; rows past the end hold no numbers."""
+    d = gdn.KVDims(16, 4, dim, page_size=64)
+    counts, kv = [256], [700]
+    cache, table = make_cache(d, kv, seed)
+    q = torch.randn(256, 16, dim, generator=gen(seed + 1), device="cuda").bfloat16()
+    return d, cache, table, counts, kv, q
+
+
+def _call(d, cache, table, counts, kv, q):
+    lens = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    gdn.timing_enable(True)
+    out = gdn.kv_attention(d, cache, cu_of(counts), lens, table, q, max_kv_len=kv[0])
+    report = gdn.timing_report()
+    gdn.timing_enable(False)
+    assert "kv_prompt" in report, report
+    return out
+
+
+@pytest.mark.parametrize("dim", [128, 256])
+def test_a_wait_that_runs_out_is_reported(monkeypatch, dim):
+    d, cache, table, counts, kv, q = _inputs(dim, 5)
+    monkeypatch.setenv("GDN_FAULT", "stall_attention")
+    _call(d, cache, table, counts, kv, q)
+    with pytest.raises(gdn.GDNError) as e:
+        gdn.sync_status()
+    assert e.value.status == gdn.GDN_ERR_TIMEOUT
+    gdn.sync_status()  # the word was cleared by the report
+    monkeypatch.delenv("GDN_FAULT")
+    out = _call(d, cache, table, counts, kv, q)
+    gdn.sync_status()
+    assert attention_excess(d, out, *attention_ref(d, cache, table, counts, kv, q)) <= 1.0
+
+
+def test_the_hook_does_not_touch_the_kernel_for_few_rows(monkeypatch):
+    d, cache, table, _, kv, q = _inputs(128, 7)
+    monkeypatch.setenv("GDN_FAULT", "stall_attention")
+    lens = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    out = gdn.kv_attention(d, cache, cu_of([1]), lens, table, q[:1])
+    gdn.sync_status()
+    assert attention_excess(d, out, *attention_ref(d, cache, table, [1], kv, q[:1])) <= 1.0
