@@ -89,16 +89,15 @@ class KVDims:
                           _DTYPES[self.dtype], KV_FORMATS[self.cache][0], self.rope_dim,
                           ROPE_STYLES[self.rope_style], self.window, scale)
             object.__setattr__(self, "_c", got)
-            object.__setattr__(self, "_at", ctypes.addressof(got))
         return got
 
     def address(self) -> int:
-        """Where the C struct of these dimensions lies."""
-        got = self.__dict__.get("_at")
-        if got is None:
-            self.c()
-            got = self.__dict__["_at"]
-        return got
+        """Where the C struct of these dimensions lies, for as long as they do."""
+        return ctypes.addressof(self.c())
+
+    def __getstate__(self):
+        """Copies and pickles hold the fields alone: the C struct belongs to one object."""
+        return {name: getattr(self, name) for name in self.__dataclass_fields__}
 
 
 class KVCache:
