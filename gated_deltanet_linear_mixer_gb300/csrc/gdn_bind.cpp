@@ -78,6 +78,24 @@ template <typename T> const T* struct_at(PyObject* o) {
 at::ScalarType type_of(int32_t dtype) { return dtype == GDN_DTYPE_BF16 ? at::kBFloat16 : at::kFloat; }
 int32_t dtype_of(at::ScalarType t) { return t == at::kBFloat16 ? GDN_DTYPE_BF16 : GDN_DTYPE_F32; }
 
+// The cache's codes k, v and scales k_scale, v_scale, as they are at this call.
+gdn_kv_cache cache_of(const gdn_kv_dims* d, PyObject* const* a) {
+    const at::ScalarType code = d->format == GDN_KV_E4M3 ? at::kFloat8_e4m3fn : at::kChar;
+    const at::Tensor& k = tensor(a[0], "cache.k");
+    const int64_t n = k.dim() > 0 ? k.size(0) : 0;
+    const int64_t codes[4] = {n, d->n_kv_heads, d->page_size, d->head_dim}, scales[2] = {n, d->n_kv_heads};
+    if (k.scalar_type() != code || k.sizes() != at::IntArrayRef(codes, 4))
+        bad(PyExc_ValueError, "the cache was made for other dimensions or codes");
+    if (n > 0x7fffffff) bad(PyExc_ValueError, "a cache has at most 2^31 - 1 pages");
+    gdn_kv_cache c;
+    c.k = plain(a[0], "cache.k", code).data_ptr();
+    c.v = plain(a[1], "cache.v", code, codes).data_ptr();
+    c.k_scale = plain(a[2], "cache.k_scale", at::kFloat, scales).data_ptr<float>();
+    c.v_scale = plain(a[3], "cache.v_scale", at::kFloat, scales).data_ptr<float>();
+    c.n_pages = static_cast<int32_t>(n);
+    return c;
+}
+
 // cu_seqlens as a (device, host) pair of int32 tensors, the lengths and the pages.
 gdn_kv_batch batch_of(PyObject* cu_dev, PyObject* cu_host, PyObject* lens, const char* lens_name, PyObject* table,
                       const int32_t** lens_ptr, int64_t* tokens) {
@@ -152,28 +170,28 @@ int32_t as_int(PyObject* o) {
     return static_cast<int32_t>(v);
 }
 
-// dims, cache, cu_dev, cu_host, kv_lens, block_table, k, v, q, rope, positions, q_out
+// dims, the cache's k, v, k_scale, v_scale, cu_dev, cu_host, kv_lens, block_table, k, v, q, rope, positions, q_out
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 12, [&]() -> PyObject* {
+    return guarded(n, 15, [&]() -> PyObject* {
         const auto* d = struct_at<gdn_kv_dims>(a[0]);
-        const auto* c = struct_at<gdn_kv_cache>(a[1]);
+        const gdn_kv_cache c = cache_of(d, a + 1);
         const int32_t* lens;
         int64_t tokens;
-        const gdn_kv_batch b = batch_of(a[2], a[3], a[4], "kv_lens", a[5], &lens, &tokens);
-        const gdn_rows k = rows_of(a[6], "k", d, tokens, d->n_kv_heads);
-        const gdn_rows v = rows_of(a[7], "v", d, tokens, d->n_kv_heads);
-        const at::Tensor& like = THPVariable_Unpack(a[6]);
+        const gdn_kv_batch b = batch_of(a[5], a[6], a[7], "kv_lens", a[8], &lens, &tokens);
+        const gdn_rows k = rows_of(a[9], "k", d, tokens, d->n_kv_heads);
+        const gdn_rows v = rows_of(a[10], "v", d, tokens, d->n_kv_heads);
+        const at::Tensor& like = THPVariable_Unpack(a[9]);
         gdn_rows q{};
         at::Tensor out;
-        const bool with_q = a[8] != Py_None;
+        const bool with_q = a[11] != Py_None;
         if (with_q) {
-            q = rows_of(a[8], "q", d, tokens, d->n_q_heads);
-            out = output(a[11], "q_out", type_of(d->dtype), {tokens, d->n_q_heads, d->head_dim}, like);
+            q = rows_of(a[11], "q", d, tokens, d->n_q_heads);
+            out = output(a[14], "q_out", type_of(d->dtype), {tokens, d->n_q_heads, d->head_dim}, like);
         }
         const float* rope = nullptr;
         int64_t rope_rows = 0;
-        if (a[9] != Py_None) {
-            const at::Tensor& r = plain(a[9], "rope", at::kFloat);
+        if (a[12] != Py_None) {
+            const at::Tensor& r = plain(a[12], "rope", at::kFloat);
             if (r.dim() != 2 || r.size(1) != d->rope_dim)
                 bad(PyExc_ValueError, "rope must have shape (rows, %d), got %s", d->rope_dim,
                     shape_text(r.sizes()).c_str());
@@ -181,54 +199,54 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             rope_rows = r.size(0);
         }
         const int32_t* positions =
-            a[10] == Py_None ? nullptr : plain(a[10], "positions", at::kInt, {tokens}).data_ptr<int32_t>();
+            a[13] == Py_None ? nullptr : plain(a[13], "positions", at::kInt, {tokens}).data_ptr<int32_t>();
         check("gdn_kv_append",
-              gdn_kv_append(d, c, &b, lens, with_q ? &q : nullptr, &k, &v, rope, static_cast<int32_t>(rope_rows),
+              gdn_kv_append(d, &c, &b, lens, with_q ? &q : nullptr, &k, &v, rope, static_cast<int32_t>(rope_rows),
                             positions, with_q ? out.data_ptr() : nullptr, stream_of(like)));
         if (!with_q) Py_RETURN_NONE;
         return THPVariable_Wrap(out);
     });
 }
 
-// dims, cache, cu_dev, cu_host, starts, block_table, dtype, k_out, v_out
+// dims, the cache's k, v, k_scale, v_scale, cu_dev, cu_host, starts, block_table, dtype, k_out, v_out
 PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 9, [&]() -> PyObject* {
+    return guarded(n, 12, [&]() -> PyObject* {
         const auto* d = struct_at<gdn_kv_dims>(a[0]);
-        const auto* c = struct_at<gdn_kv_cache>(a[1]);
+        const gdn_kv_cache c = cache_of(d, a + 1);
         const int32_t* starts;
         int64_t tokens;
-        const gdn_kv_batch b = batch_of(a[2], a[3], a[4], "starts", a[5], &starts, &tokens);
-        const int32_t dtype = as_int(a[6]);
-        const at::Tensor& like = THPVariable_Unpack(a[5]);
+        const gdn_kv_batch b = batch_of(a[5], a[6], a[7], "starts", a[8], &starts, &tokens);
+        const int32_t dtype = as_int(a[9]);
+        const at::Tensor& like = THPVariable_Unpack(a[8]);
         const int64_t shape[3] = {tokens, d->n_kv_heads, d->head_dim};
-        at::Tensor k = output(a[7], "k_out", type_of(dtype), shape, like);
-        at::Tensor v = output(a[8], "v_out", type_of(dtype), shape, like);
-        check("gdn_kv_read", gdn_kv_read(d, c, &b, starts, dtype, k.data_ptr(), v.data_ptr(), stream_of(like)));
+        at::Tensor k = output(a[10], "k_out", type_of(dtype), shape, like);
+        at::Tensor v = output(a[11], "v_out", type_of(dtype), shape, like);
+        check("gdn_kv_read", gdn_kv_read(d, &c, &b, starts, dtype, k.data_ptr(), v.data_ptr(), stream_of(like)));
         return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
     });
 }
 
-// dims, cache, cu_dev, cu_host, kv_lens, block_table, q, max_kv_len, out, workspace
+// dims, the cache's k, v, k_scale, v_scale, cu_dev, cu_host, kv_lens, block_table, q, max_kv_len, out, workspace
 PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 10, [&]() -> PyObject* {
+    return guarded(n, 13, [&]() -> PyObject* {
         const auto* d = struct_at<gdn_kv_dims>(a[0]);
-        const auto* c = struct_at<gdn_kv_cache>(a[1]);
+        const gdn_kv_cache c = cache_of(d, a + 1);
         const int32_t* lens;
         int64_t tokens;
-        const gdn_kv_batch b = batch_of(a[2], a[3], a[4], "kv_lens", a[5], &lens, &tokens);
-        const gdn_rows q = rows_of(a[6], "q", d, tokens, d->n_q_heads);
-        const at::Tensor& like = THPVariable_Unpack(a[6]);
+        const gdn_kv_batch b = batch_of(a[5], a[6], a[7], "kv_lens", a[8], &lens, &tokens);
+        const gdn_rows q = rows_of(a[9], "q", d, tokens, d->n_q_heads);
+        const at::Tensor& like = THPVariable_Unpack(a[9]);
         int32_t longest;
-        if (a[7] == Py_None) {
+        if (a[10] == Py_None) {
             const int64_t room = static_cast<int64_t>(b.pages_per_seq) * d->page_size;
             longest = room < 0x7fffffff ? static_cast<int32_t>(room) : 0x7fffffff;
         } else {
-            longest = as_int(a[7]);
+            longest = as_int(a[10]);
         }
-        at::Tensor out = output(a[8], "out", type_of(d->dtype), {tokens, d->n_q_heads, d->head_dim}, like);
+        at::Tensor out = output(a[11], "out", type_of(d->dtype), {tokens, d->n_q_heads, d->head_dim}, like);
         at::Tensor ws;
-        if (a[9] != Py_None) {
-            ws = tensor(a[9], "workspace");
+        if (a[12] != Py_None) {
+            ws = tensor(a[12], "workspace");
             if (!ws.is_contiguous()) bad(PyExc_ValueError, "workspace must be contiguous");
             want_cuda(ws, "workspace");
         } else {
@@ -238,7 +256,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (need) ws = at::empty({static_cast<int64_t>(need)}, like.options().dtype(at::kByte));
         }
         check("gdn_kv_attention",
-              gdn_kv_attention(d, c, &b, lens, longest, &q, out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr,
+              gdn_kv_attention(d, &c, &b, lens, longest, &q, out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr,
                                ws.defined() ? ws.nbytes() : 0, stream_of(like)));
         return THPVariable_Wrap(out);
     });

@@ -28,7 +28,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import DTYPE_BF16, DTYPE_F32, _PKG, GDNError, _check, _cu_pair, _KVCache, _KVDims, _t, load
+from . import DTYPE_BF16, DTYPE_F32, _PKG, GDNError, _check, _cu_pair, _KVDims, _t, load
 
 KV_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
 ROPE_STYLES = {"half": 0, "interleaved": 1}
@@ -102,7 +102,8 @@ class KVDims:
 
 class KVCache:
     """The pages of one layer: codes k, v [n_pages, Hkv, page_size, head_dim] and one fp32 scale
-    per page and head, k_scale, v_scale [n_pages, Hkv].  Holds the tensors it is given."""
+    per page and head, k_scale, v_scale [n_pages, Hkv].  Holds the tensors it is given; a call takes
+    those that it holds then, so that they may be replaced (by larger ones, by a copy's own)."""
 
     def __init__(self, d: KVDims, k, v, k_scale, v_scale):
         d.c()
@@ -113,10 +114,11 @@ class KVCache:
         _t(v, "v", code, shape)
         _t(k_scale, "k_scale", torch.float32, shape[:2])
         _t(v_scale, "v_scale", torch.float32, shape[:2])
-        self.k, self.v, self.k_scale, self.v_scale, self.n_pages = k, v, k_scale, v_scale, n
-        self._c = _KVCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n)
-        self._at = ctypes.addressof(self._c)
-        self._of, self._last = (d.n_kv_heads, d.page_size, d.head_dim, d.cache), d
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+
+    @property
+    def n_pages(self) -> int:
+        return int(self.k.shape[0])
 
     @classmethod
     def empty(cls, d: KVDims, n_pages: int, device="cuda") -> "KVCache":
@@ -127,14 +129,6 @@ class KVCache:
         codes = [torch.empty(shape, dtype=KV_FORMATS[d.cache][1], device=device) for _ in "kv"]
         scales = [torch.empty(shape[:2], device=device) for _ in "kv"]
         return cls(d, *codes, *scales)
-
-    def address(self, d: KVDims) -> int:
-        """Where the C struct of this cache lies, for a call with dimensions d."""
-        if d is not self._last:
-            if self._of != (d.n_kv_heads, d.page_size, d.head_dim, d.cache):
-                raise ValueError("the cache was made for other dimensions or codes")
-            self._last = d
-        return self._at
 
 
 def _pair(cu_seqlens, like):
@@ -147,8 +141,8 @@ def kv_append(d: KVDims, cache: KVCache, cu_seqlens, kv_lens, block_table, k, v,
     rope [rows, rope_dim] (cosines | sines) on the way; positions [T] int32 where they are not the
     cache positions.  Returns the rotated q [T, Hq, D] (None without q)."""
     cu_d, cu_h = _pair(cu_seqlens, k)
-    return (_native or _bind()).kv_append(d.address(), cache.address(d), cu_d, cu_h, kv_lens, block_table,
-                                          k, v, q, rope, positions, q_out)
+    return (_native or _bind()).kv_append(d.address(), cache.k, cache.v, cache.k_scale, cache.v_scale, cu_d, cu_h,
+                                          kv_lens, block_table, k, v, q, rope, positions, q_out)
 
 
 def kv_read(d: KVDims, cache: KVCache, cu_seqlens, starts, block_table, *, dtype=None, k_out=None,
@@ -159,8 +153,8 @@ def kv_read(d: KVDims, cache: KVCache, cu_seqlens, starts, block_table, *, dtype
     dtype = d.dtype if dtype is None else dtype
     if dtype not in _DTYPES:
         raise ValueError("dtype must be torch.float32 or torch.bfloat16")
-    return (_native or _bind()).kv_read(d.address(), cache.address(d), cu_d, cu_h, starts, block_table,
-                                        _DTYPES[dtype], k_out, v_out)
+    return (_native or _bind()).kv_read(d.address(), cache.k, cache.v, cache.k_scale, cache.v_scale, cu_d, cu_h,
+                                        starts, block_table, _DTYPES[dtype], k_out, v_out)
 
 
 def kv_attention_workspace_size(d: KVDims, cu_seqlens, max_kv_len: int) -> int:
@@ -184,8 +178,8 @@ def kv_attention(d: KVDims, cache: KVCache, cu_seqlens, kv_lens, block_table, q,
     """gdn_kv_attention: q [T, Hq, D] against the cache.  max_kv_len (None: what block_table can
     hold) bounds kv_lens on the host.  Returns out [T, Hq, D]."""
     cu_d, cu_h = _pair(cu_seqlens, q)
-    return (_native or _bind()).kv_attention(d.address(), cache.address(d), cu_d, cu_h, kv_lens, block_table,
-                                             q, max_kv_len, out, workspace)
+    return (_native or _bind()).kv_attention(d.address(), cache.k, cache.v, cache.k_scale, cache.v_scale, cu_d, cu_h,
+                                             kv_lens, block_table, q, max_kv_len, out, workspace)
 
 
 def accept_drafts(drafts, target, draft, uniforms, noise, *, form="probs", temperature=None,

@@ -3,6 +3,8 @@ pages that a window has left behind, windows near 2^31.
 
 References and bounds are those of paged_cases.py; calls of many rows add the weights that f16
 drops, 2^-31 of the reference a key (2^-20 of the largest |value| for up to 2^11 keys)."""
+import copy
+
 import pytest
 import torch
 
@@ -136,3 +138,34 @@ def test_the_widest_window_is_none(dim, counts):
     a = gdn.kv_attention(d, cache, cu_of(counts), lens, table, q)
     b = gdn.kv_attention(wide, cache, cu_of(counts), lens, table, q)
     assert a[2:].any() and torch.equal(a, b)
+
+
+def test_a_cache_s_tensors_may_be_replaced():
+    """A call takes the tensors that the cache holds then: a cache that grew is written to and read
+    where it is now."""
+    d = gdn.KVDims(4, 2, 64, page_size=16)
+    cache, table = make_cache(d, [16], 89, poison=False)
+    old = (cache.k, cache.v, cache.k_scale, cache.v_scale)
+    before = [x.clone() for x in old]
+    for name, x in zip(("k", "v", "k_scale", "v_scale"), old):
+        setattr(cache, name, torch.cat([x, torch.zeros_like(x)]))
+    new = torch.randn(16, 2, 64, generator=gen(90), device="cuda").to(BF)
+    lens = torch.tensor([16], dtype=torch.int32, device="cuda")
+    entry = torch.full_like(table, cache.k.shape[0] - 1)  # a page that only the grown cache has
+    gdn.kv_append(d, cache, cu_of([16]), lens, entry, new, new)
+    k, _ = gdn.kv_read(d, cache, cu_of([16]), lens * 0, entry, dtype=F32)
+    assert (k - new.float()).abs().max() < 0.03
+    assert all(torch.equal(x, y) for x, y in zip(old, before))
+
+
+def test_a_copied_cache_is_its_own():
+    d = gdn.KVDims(4, 2, 64, page_size=16)
+    cache, table = make_cache(d, [16], 92, poison=False)
+    twin = copy.deepcopy(cache)
+    new = torch.randn(16, 2, 64, generator=gen(93), device="cuda").to(BF)
+    lens = torch.tensor([16], dtype=torch.int32, device="cuda")
+    gdn.kv_append(d, twin, cu_of([16]), lens, table, new, new)
+    k, _ = gdn.kv_read(d, twin, cu_of([16]), lens * 0, table, dtype=F32)
+    assert (k - new.float()).abs().max() < 0.03
+    fresh, _ = make_cache(d, [16], 92, poison=False)
+    assert torch.equal(cache.k, fresh.k) and torch.equal(cache.k_scale, fresh.k_scale)
