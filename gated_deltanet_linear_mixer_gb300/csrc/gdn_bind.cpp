@@ -10,9 +10,12 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cstdarg>
+#include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "gdn.h"
@@ -137,7 +140,33 @@ at::Tensor output(PyObject* o, const char* name, at::ScalarType type, at::IntArr
     return at::empty(shape, like.options().dtype(type));
 }
 
-void* stream_of(const at::Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
+struct Named {
+    int at;
+    const char* name;
+};
+// The device of a call: that of its CUDA tensors, which must agree (arguments that are not CUDA
+// tensors are refused where they are checked).  Looked at before anything else of them.
+std::optional<at::Device> device_of(PyObject* const* a, std::initializer_list<Named> args) {
+    std::optional<at::Device> device;
+    for (const Named& x : args) {
+        if (!THPVariable_Check(a[x.at])) continue;
+        const at::Tensor& t = THPVariable_Unpack(a[x.at]);
+        if (!t.is_cuda()) continue;
+        if (!device) device = t.device();
+        if (t.device() != *device)
+            bad(PyExc_ValueError, "%s is on device %s, the call's other tensors are on %s", x.name, t.device().str().c_str(),
+                device->str().c_str());
+    }
+    return device;
+}
+
+// The current stream of a call's device, which is the current device while this lives: a launch on a
+// device's default stream goes to the current device.
+struct Launch {
+    c10::cuda::CUDAGuard guard;
+    explicit Launch(const std::optional<at::Device>& device) : guard(device.value()) {}
+    void* stream() const { return c10::cuda::getCurrentCUDAStream(guard.current_device().index()).stream(); }
+};
 
 void check(const char* fn, gdn_status st) {
     if (st == GDN_OK) return;
@@ -173,6 +202,9 @@ int32_t as_int(PyObject* o) {
 // dims, the cache's k, v, k_scale, v_scale, cu_dev, cu_host, kv_lens, block_table, k, v, q, rope, positions, q_out
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 15, [&]() -> PyObject* {
+        const auto device = device_of(a, {{1, "cache.k"}, {2, "cache.v"}, {3, "cache.k_scale"}, {4, "cache.v_scale"}, {5, "cu_seqlens"},
+                                          {7, "kv_lens"}, {8, "block_table"}, {9, "k"}, {10, "v"}, {11, "q"}, {12, "rope"},
+                                          {13, "positions"}, {14, "q_out"}});
         const auto* d = struct_at<gdn_kv_dims>(a[0]);
         const gdn_kv_cache c = cache_of(d, a + 1);
         const int32_t* lens;
@@ -202,7 +234,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             a[13] == Py_None ? nullptr : plain(a[13], "positions", at::kInt, {tokens}).data_ptr<int32_t>();
         check("gdn_kv_append",
               gdn_kv_append(d, &c, &b, lens, with_q ? &q : nullptr, &k, &v, rope, static_cast<int32_t>(rope_rows),
-                            positions, with_q ? out.data_ptr() : nullptr, stream_of(like)));
+                            positions, with_q ? out.data_ptr() : nullptr, Launch(device).stream()));
         if (!with_q) Py_RETURN_NONE;
         return THPVariable_Wrap(out);
     });
@@ -211,6 +243,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // dims, the cache's k, v, k_scale, v_scale, cu_dev, cu_host, starts, block_table, dtype, k_out, v_out
 PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 12, [&]() -> PyObject* {
+        const auto device = device_of(a, {{1, "cache.k"}, {2, "cache.v"}, {3, "cache.k_scale"}, {4, "cache.v_scale"}, {5, "cu_seqlens"},
+                                          {7, "starts"}, {8, "block_table"}, {10, "k_out"}, {11, "v_out"}});
         const auto* d = struct_at<gdn_kv_dims>(a[0]);
         const gdn_kv_cache c = cache_of(d, a + 1);
         const int32_t* starts;
@@ -221,7 +255,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t shape[3] = {tokens, d->n_kv_heads, d->head_dim};
         at::Tensor k = output(a[10], "k_out", type_of(dtype), shape, like);
         at::Tensor v = output(a[11], "v_out", type_of(dtype), shape, like);
-        check("gdn_kv_read", gdn_kv_read(d, &c, &b, starts, dtype, k.data_ptr(), v.data_ptr(), stream_of(like)));
+        check("gdn_kv_read", gdn_kv_read(d, &c, &b, starts, dtype, k.data_ptr(), v.data_ptr(), Launch(device).stream()));
         return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
     });
 }
@@ -229,6 +263,8 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // dims, the cache's k, v, k_scale, v_scale, cu_dev, cu_host, kv_lens, block_table, q, max_kv_len, out, workspace
 PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 13, [&]() -> PyObject* {
+        const auto device = device_of(a, {{1, "cache.k"}, {2, "cache.v"}, {3, "cache.k_scale"}, {4, "cache.v_scale"}, {5, "cu_seqlens"},
+                                          {7, "kv_lens"}, {8, "block_table"}, {9, "q"}, {11, "out"}, {12, "workspace"}});
         const auto* d = struct_at<gdn_kv_dims>(a[0]);
         const gdn_kv_cache c = cache_of(d, a + 1);
         const int32_t* lens;
@@ -257,7 +293,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         check("gdn_kv_attention",
               gdn_kv_attention(d, &c, &b, lens, longest, &q, out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr,
-                               ws.defined() ? ws.nbytes() : 0, stream_of(like)));
+                               ws.defined() ? ws.nbytes() : 0, Launch(device).stream()));
         return THPVariable_Wrap(out);
     });
 }
@@ -277,6 +313,8 @@ int64_t dist_stride(const at::Tensor& t, const char* name, at::ScalarType type, 
 // drafts, target, draft, uniforms, noise, form, temperature, accepted, tokens
 PyObject* accept_drafts(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     return guarded(n_args, 9, [&]() -> PyObject* {
+        const auto device = device_of(a, {{0, "drafts"}, {1, "target"}, {2, "draft"}, {3, "uniforms"}, {4, "noise"},
+                                          {6, "temperature"}, {7, "accepted"}, {8, "tokens"}});
         const at::Tensor& target = tensor(a[1], "target");
         const at::ScalarType type = target.scalar_type();
         if (type != at::kFloat && type != at::kBFloat16)
@@ -308,7 +346,7 @@ PyObject* accept_drafts(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
               gdn_accept_drafts(static_cast<int32_t>(n), static_cast<int32_t>(T), static_cast<int32_t>(vocab),
                                 as_int(a[5]), dtype_of(type), x.data_ptr<int32_t>(), target.data_ptr(), ts, draft, ds,
                                 temp, u.data_ptr<float>(), e.data_ptr<float>(), ns, accepted.data_ptr<int32_t>(),
-                                tokens.data_ptr<int32_t>(), stream_of(target)));
+                                tokens.data_ptr<int32_t>(), Launch(device).stream()));
         return Py_BuildValue("NN", THPVariable_Wrap(accepted), THPVariable_Wrap(tokens));
     });
 }

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import gated_deltanet_linear_mixer_gb300 as gdn
+from gated_deltanet_linear_mixer_gb300 import _build
 
 COPIES = {
     "copy": copy.copy,
@@ -38,3 +39,65 @@ def test_copied_dims_have_a_struct_of_their_own(how, used):
     noise = [gdn.KVDims(1, 1, 64, page_size=16) for _ in range(64)]
     assert all(n.address() != e.address() for n in noise)
     assert _fields(gdn._KVDims.from_address(e.address())) == want
+
+
+# --------------------------------------------------- tensors of several devices
+D = gdn.KVDims(4, 2, 64, page_size=16, rope_dim=16)
+
+
+def _calls(fake):
+    """name -> (call, its tensor arguments); tensors without memory on a device of that name."""
+    def t(*shape, dtype=torch.float32):
+        return fake(shape, dtype)
+
+    i32, bf = torch.int32, torch.bfloat16
+    host = torch.tensor([0, 3], dtype=i32)
+    cache = {"cache.k": t(5, 2, 16, 64, dtype=torch.int8), "cache.v": t(5, 2, 16, 64, dtype=torch.int8),
+             "cache.k_scale": t(5, 2), "cache.v_scale": t(5, 2)}
+    batch = {"cu_seqlens": t(2, dtype=i32), "lens": t(1, dtype=i32), "block_table": t(1, 4, dtype=i32)}
+    rows = {"k": t(3, 2, 64, dtype=bf), "v": t(3, 2, 64, dtype=bf), "q": t(3, 4, 64, dtype=bf)}
+
+    def held(a):
+        c = object.__new__(gdn.KVCache)
+        c.k, c.v, c.k_scale, c.v_scale = (a[f"cache.{x}"] for x in ("k", "v", "k_scale", "v_scale"))
+        return c
+
+    append = dict(**cache, **batch, **rows, rope=t(20, 16), positions=t(3, dtype=i32), q_out=t(3, 4, 64, dtype=bf))
+    read = dict(**cache, **batch, k_out=t(3, 2, 64, dtype=bf), v_out=t(3, 2, 64, dtype=bf))
+    attend = dict(**cache, **batch, q=rows["q"], out=t(3, 4, 64, dtype=bf), workspace=t(1 << 20, dtype=torch.uint8))
+    accept = dict(drafts=t(2, 3, dtype=i32), target=t(2, 4, 10), draft=t(2, 3, 10), uniforms=t(2, 3), noise=t(2, 10),
+                  temperature=t(2), accepted=t(2, dtype=i32), tokens=t(2, 4, dtype=i32))
+    return {
+        "append": (lambda a: gdn.kv_append(D, held(a), (a["cu_seqlens"], host), a["lens"], a["block_table"], a["k"],
+                                           a["v"], q=a["q"], rope=a["rope"], positions=a["positions"],
+                                           q_out=a["q_out"]), append),
+        "read": (lambda a: gdn.kv_read(D, held(a), (a["cu_seqlens"], host), a["lens"], a["block_table"],
+                                       k_out=a["k_out"], v_out=a["v_out"]), read),
+        "attention": (lambda a: gdn.kv_attention(D, held(a), (a["cu_seqlens"], host), a["lens"], a["block_table"],
+                                                 a["q"], max_kv_len=10, out=a["out"], workspace=a["workspace"]), attend),
+        "accept": (lambda a: gdn.accept_drafts(a["drafts"], a["target"], a["draft"], a["uniforms"], a["noise"],
+                                               form="logits", temperature=a["temperature"], accepted=a["accepted"],
+                                               tokens=a["tokens"]), accept),
+    }
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="for a machine without a GPU: nothing can be launched")
+@pytest.mark.parametrize("name", ["append", "read", "attention", "accept"])
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_tensors_of_two_devices_are_refused(name):
+    """Each tensor in turn on another device than the rest."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    _build.build()
+    mode = FakeTensorMode(allow_non_fake_inputs=True)
+
+    def on(device):
+        def make(shape, dtype):
+            with mode:
+                return torch.empty(shape, dtype=dtype, device=device)
+        return make
+
+    call, args = _calls(on("cuda:0"))[name]
+    _, others = _calls(on("cuda:1"))[name]
+    for moved in args:
+        with pytest.raises(ValueError, match="device"):
+            call({**args, moved: others[moved]})
