@@ -33,6 +33,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxDrafts = 16, kMaxCluster = 8;
 constexpr int kRowsMost = 2 * kMaxDrafts + 1;
 constexpr int kUnroll = 8;
+static_assert(2 * kUnroll * kThreads <= 0x7fffffff - kMostVocab, "indexes past a row's end fit 32 bits");
 
 // A row's logits over one lane's share: running maximum and sum of exponentials
 // (of base 2, arguments times c = log2 e / tau), or maximum and its lowest index.

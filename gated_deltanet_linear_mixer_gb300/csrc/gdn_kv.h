@@ -66,6 +66,8 @@ struct KvAttnArgs {
     int stall;        // test hook: the kernel for many rows waits for look-ups that never come
 };
 
+// The largest vocabulary: the kernel's strides go past a row's end, in 32 bits.
+constexpr int kMostVocab = 0x7fffffff - 4096;
 struct AcceptArgs {
     int n_seq, T, vocab;
     const int32_t* drafts;

@@ -250,6 +250,8 @@ gdn_status gdn_accept_drafts(int32_t n_seq, int32_t T, int32_t vocab, int32_t fo
                          GDN_MAX_SEQUENCES, n_seq);
     if (T < 0 || T > 16) return set_error(GDN_ERR_INVALID_ARG, fn, "T must be 0..16 (got %d)", T);
     if (vocab < 1) return set_error(GDN_ERR_INVALID_ARG, fn, "vocab must be >= 1 (got %d)", vocab);
+    if (vocab > gdn::kMostVocab)
+        return set_error(GDN_ERR_UNSUPPORTED, fn, "vocab %d is above %d", vocab, gdn::kMostVocab);
     if (form != GDN_DIST_PROBS && form != GDN_DIST_LOGITS)
         return set_error(GDN_ERR_INVALID_ARG, fn, "form %d is not a gdn_dist_form", form);
     if (dtype != GDN_DTYPE_F32 && dtype != GDN_DTYPE_BF16)

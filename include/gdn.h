@@ -455,7 +455,8 @@ typedef enum gdn_dist_form { GDN_DIST_PROBS = 0, GDN_DIST_LOGITS = 1 } gdn_dist_
  *   drafts, uniforms [n_seq, T]; target [n_seq, T + 1, vocab] and draft
  *   [n_seq, T, vocab] with row strides in elements (the sequence stride is
  *   T + 1, or T, rows); noise [n_seq, vocab] fp32 with its row stride;
- *   temperature [n_seq] fp32 >= 0 (logits; NULL: 1).  0 <= T <= 16.
+ *   temperature [n_seq] fp32 >= 0 (logits; NULL: 1).  0 <= T <= 16; vocab at
+ *   most 2^31 - 4097.
  *   accepted [n_seq] int32: how many drafts stand (gdn_decode_commit's
  *   `accepted`, plus one where its x begins with the last kept token).  tokens [n_seq, T + 1] int32: those drafts, the drawn token,
  *   then -1.

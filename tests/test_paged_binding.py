@@ -101,3 +101,17 @@ def test_tensors_of_two_devices_are_refused(name):
     for moved in args:
         with pytest.raises(ValueError, match="device"):
             call({**args, moved: others[moved]})
+
+
+# ------------------------------------------------------------ the C entry points
+@pytest.mark.parametrize("vocab,fits", [(2 ** 31 - 1, False), (2 ** 31 - 4096, False), (2 ** 31 - 4097, True),
+                                        (2 ** 30, True)])
+def test_vocabularies_whose_indexes_leave_32_bits_are_refused(monkeypatch, vocab, fits):
+    """The kernel steps up to 2048 past a row's end in 32 bits.  No call gets past the checks: those
+    that are accepted end in the injected failure."""
+    _build.build()
+    lib, at = gdn.load(), 0x10000
+    monkeypatch.setenv("GDN_FAULT", "accept")
+    got = lib.gdn_accept_drafts(1, 1, vocab, 0, 0, at, at, vocab, at, vocab, None, at, at, vocab, at, at, None)
+    assert got == (gdn.GDN_ERR_INJECTED if fits else 2)
+    assert ("vocab" in lib.gdn_last_error().decode()) == (not fits)
