@@ -58,7 +58,8 @@ using namespace tc;
 namespace {
 
 __device__ int g_kv_prompt_error = 0;
-__device__ __forceinline__ void prompt_fail(int code) { atomicCAS(&g_kv_prompt_error, 0, code); }
+// The largest code stays: a wait that gave up (42..48) outranks data out of range (40).
+__device__ __forceinline__ void prompt_fail(int code) { atomicMax(&g_kv_prompt_error, code); }
 
 constexpr int kM = 128, kKeys = 64;
 constexpr int kGroups = kKeys / 16;  // 16-key groups of a tile: one page each

@@ -64,3 +64,23 @@ def test_the_hook_does_not_touch_the_kernel_for_few_rows(monkeypatch):
     out = gdn.kv_attention(d, cache, cu_of([1]), lens, table, q[:1])
     gdn.sync_status()
     assert attention_excess(d, out, *attention_ref(d, cache, table, [1], kv, q[:1])) <= 1.0
+
+
+@pytest.mark.parametrize("same_call", [True, False])
+def test_a_wait_that_runs_out_outranks_data_out_of_range(monkeypatch, same_call):
+    """An unmapped page, met first in the same call or in the one before, does not hide the timeout."""
+    d, cache, table, counts, kv, q = _inputs(128, 9)
+    holed = table.clone()
+    holed[0, 3] = -1
+    if not same_call:
+        _call(d, cache, holed, counts, kv, q)
+    monkeypatch.setenv("GDN_FAULT", "stall_attention")
+    _call(d, cache, holed if same_call else table, counts, kv, q)
+    with pytest.raises(gdn.GDNError) as e:
+        gdn.sync_status()
+    assert e.value.status == gdn.GDN_ERR_TIMEOUT
+    monkeypatch.delenv("GDN_FAULT")
+    _call(d, cache, holed, counts, kv, q)
+    with pytest.raises(gdn.GDNError, match="code 40"):
+        gdn.sync_status()
+    gdn.sync_status()
