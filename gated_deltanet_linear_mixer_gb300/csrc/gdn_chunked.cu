@@ -48,9 +48,11 @@ using namespace tc;
 
 constexpr int kChunkThreads = 256;
 
-__device__ int g_device_error = 0;
+// The first wait code of this file's kernels; the largest code of the cache
+// operators, which have it by its address (cache_error_word): one copy reads both.
+__device__ int g_device_error[2] = {0, 0};
 
-__device__ __forceinline__ void report_error(int code) { atomicCAS(&g_device_error, 0, code); }
+__device__ __forceinline__ void report_error(int code) { atomicCAS(&g_device_error[0], 0, code); }
 
 // --------------------------------------------------------------- chunk_prep
 // One CTA per (chunk, key head); its R = Hv/Hk value heads are processed in
@@ -1500,23 +1502,36 @@ cudaError_t launch_chunked_prefill(const ChunkLaunch& a, cudaStream_t st) {
 }
 
 cudaError_t read_device_error(int* code, bool reset) {
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_device_error, sizeof(int));
-    if (e == cudaSuccess && reset) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
+    // A word is cleared only where it is set: every copy waits for the device.
+    int own[2] = {0, 0};
+    cudaError_t e = cudaMemcpyFromSymbol(own, g_device_error, sizeof(own));
+    if (e == cudaSuccess && reset && (own[0] || own[1])) {
+        const int zero[2] = {0, 0};
+        e = cudaMemcpyToSymbol(g_device_error, zero, sizeof(zero));
     }
     // the projection GEMM's word (codes 20..23), the recurrent kernel's (30),
-    // the per-channel prep's (13, 14), the cache operators' (40, 41, 42..47)
-    int gemm = 0, rec = 0, kda = 0, kv = 0, attn = 0, prompt = 0;
+    // the per-channel prep's (13, 14); last the cache operators', which may be
+    // data out of range (40, 41) and no wait (42..48)
+    int gemm = 0, rec = 0, kda = 0;
     if (e == cudaSuccess) e = read_gemm_error(&gemm, reset);
     if (e == cudaSuccess) e = read_rec_error(&rec, reset);
     if (e == cudaSuccess) e = read_kda_error(&kda, reset);
-    if (e == cudaSuccess) e = read_kv_error(&kv, reset);
-    if (e == cudaSuccess) e = read_kv_attn_error(&attn, reset);
-    if (e == cudaSuccess) e = read_kv_prompt_error(&prompt, reset);
-    if (e == cudaSuccess && *code == 0)
-        *code = gemm ? gemm : rec ? rec : kda ? kda : prompt ? prompt : attn ? attn : kv;
+    *code = own[0] ? own[0] : gemm ? gemm : rec ? rec : kda ? kda : own[1];
     return e;
+}
+
+cudaError_t cache_error_word(int** word) {
+    static std::atomic<int*> known[64];  // by device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*word = known[dev].load(std::memory_order_relaxed))) return cudaSuccess;
+    void* at = nullptr;
+    e = cudaGetSymbolAddress(&at, g_device_error);
+    if (e != cudaSuccess) return e;
+    *word = static_cast<int*>(at) + 1;
+    if (dev < 64) known[dev].store(*word, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 }  // namespace gdn

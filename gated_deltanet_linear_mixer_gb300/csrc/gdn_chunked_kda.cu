@@ -632,7 +632,7 @@ cudaError_t launch_kda_prep(const CUtensorMap& map_qh, const CUtensorMap& map_ql
 
 cudaError_t read_kda_error(int* code, bool reset) {
     cudaError_t e = cudaMemcpyFromSymbol(code, g_kda_error, sizeof(int));
-    if (e == cudaSuccess && reset) {
+    if (e == cudaSuccess && reset && *code) {
         const int zero = 0;
         e = cudaMemcpyToSymbol(g_kda_error, &zero, sizeof(int));
     }

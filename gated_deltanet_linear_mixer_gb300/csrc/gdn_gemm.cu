@@ -336,7 +336,7 @@ cudaError_t launch_gemm_bf16(const GemmLaunch& l, cudaStream_t st) {
 
 cudaError_t read_gemm_error(int* code, bool reset) {
     cudaError_t e = cudaMemcpyFromSymbol(code, g_gemm_error, sizeof(int));
-    if (e == cudaSuccess && reset) {
+    if (e == cudaSuccess && reset && *code) {
         const int zero = 0;
         e = cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof(int));
     }

@@ -11,6 +11,9 @@ namespace gdn {
 // Device error codes of the cache operators (not waits).
 constexpr int kKvErrTable = 40;  // block table entry or length out of range
 constexpr int kKvErrRope = 41;   // position outside the rotation table
+// The word on the current device where the operators' kernels record codes: the
+// largest stays, so that a wait that gave up (42..48) outranks data out of range.
+cudaError_t cache_error_word(int** word);
 
 struct KvCache {
     uint8_t* k;      // codes [n_pages, Hkv, B, D]
@@ -45,6 +48,7 @@ struct KvAppendArgs {
     int rope_len;
     const int32_t* positions;   // [T] or null
     void* q_out;
+    int* error;                 // cache_error_word
 };
 
 struct KvReadArgs {
@@ -52,6 +56,7 @@ struct KvReadArgs {
     KvBatch b;
     int n_kv_heads, page_size;
     void *k_out, *v_out;
+    int* error;
 };
 
 struct KvAttnArgs {
@@ -63,6 +68,7 @@ struct KvAttnArgs {
     void* out;
     float* partial;   // split partials (workspace), see gdn_kv_attn.cu
     int max_kv_len;
+    int* error;
     int stall;        // test hook: the kernel for many rows waits for look-ups that never come
 };
 
@@ -105,9 +111,5 @@ cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bo
                                 cudaStream_t stream);
 // form: gdn_dist_form; logits and probabilities in bf16 or f32.
 cudaError_t launch_accept_drafts(const AcceptArgs& a, bool logits, bool bf16, cudaStream_t stream);
-
-cudaError_t read_kv_error(int* code, bool reset);       // append, read
-cudaError_t read_kv_attn_error(int* code, bool reset);  // attention, few rows
-cudaError_t read_kv_prompt_error(int* code, bool reset);  // attention, many rows
 
 }  // namespace gdn

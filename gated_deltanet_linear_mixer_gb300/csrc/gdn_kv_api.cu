@@ -154,6 +154,7 @@ gdn_status gdn_kv_append(const gdn_kv_dims* dims, const gdn_kv_cache* cache, con
     if (dims->rope_dim > 0 && (!rope || rope_len < 1 || !aligned16(rope)))
         return set_error(GDN_ERR_INVALID_ARG, fn, "rope must hold at least one row and be 16-byte aligned");
     if ((st = gdn::inject_fault("kv_append", fn)) != GDN_OK) return st;
+    if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.c = cache_of(cache);
     a.n_q_heads = dims->n_q_heads; a.n_kv_heads = dims->n_kv_heads; a.page_size = dims->page_size;
     a.rope_dim = dims->rope_dim; a.rope_style = dims->rope_style; a.rope = rope; a.rope_len = rope_len;
@@ -180,6 +181,7 @@ gdn_status gdn_kv_read(const gdn_kv_dims* dims, const gdn_kv_cache* cache, const
     if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
         return set_error(GDN_ERR_INVALID_ARG, fn, "k_out and v_out must be given and 16-byte aligned");
     if ((st = gdn::inject_fault("kv_read", fn)) != GDN_OK) return st;
+    if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.c = cache_of(cache);
     a.n_kv_heads = dims->n_kv_heads; a.page_size = dims->page_size; a.k_out = k_out; a.v_out = v_out;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -228,6 +230,7 @@ gdn_status gdn_kv_attention(const gdn_kv_dims* dims, const gdn_kv_cache* cache, 
     if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return set_error(GDN_ERR_WORKSPACE, fn, "workspace must be 256-byte aligned");
     if ((st = gdn::inject_fault("kv_attention", fn)) != GDN_OK) return st;
+    if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.c = cache_of(cache);
     a.n_q_heads = dims->n_q_heads; a.n_kv_heads = dims->n_kv_heads; a.page_size = dims->page_size;
     a.window = dims->window; a.scale = dims->scale; a.out = out; a.partial = static_cast<float*>(workspace);

@@ -52,8 +52,6 @@ namespace gdn {
 
 namespace {
 
-__device__ int g_kv_attn_error = 0;
-
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kGroup = 16;        // keys of a warp's step
 constexpr int kStepKeys = kGroup * kWarps;
@@ -235,7 +233,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
     const int G = a.n_q_heads / a.n_kv_heads;
     Tile t;
     if (!tile_of(a, R, tile, blockIdx.y, blockIdx.z, t)) return;
-    if (tid == 0 && t.len < a.b.kv_lens[t.seq]) atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
+    if (tid == 0 && t.len < a.b.kv_lens[t.seq]) atomicMax(a.error, kKvErrTable);
     const int begin = t.keys.first + split * sp.chunk;
     const int end = split == sp.n - 1 ? t.keys.end : min(t.keys.end, begin + sp.chunk);
     if (split > 0 && begin >= end) return;  // the join does not read this one
@@ -293,7 +291,7 @@ kv_attn_kernel(const KvAttnArgs a, const Split sp, const int n_tiles) {
                 // now, or no numbers
                 page = -1;
             } else if (page < 0 || page >= a.c.n_pages) {
-                atomicCAS(&g_kv_attn_error, 0, kKvErrTable);
+                atomicMax(a.error, kKvErrTable);
                 page = -1;
             }
         }
@@ -816,15 +814,6 @@ cudaError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, bool bf16, bo
     const KvPrompt p = kv_prompt_plan(a.b.n_seq, a.b.max_q, a.n_q_heads, a.n_kv_heads, head_dim, a.window, bf16, a.max_kv_len);
     if (p.tiles > 0) return launch_kv_prompt(a, p, head_dim, e4m3, stream);
     return GDN_KV_PICK(attn_t);
-}
-
-cudaError_t read_kv_attn_error(int* code, bool reset) {
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_kv_attn_error, sizeof(int));
-    if (e == cudaSuccess && reset) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbol(g_kv_attn_error, &zero, sizeof(int));
-    }
-    return e;
 }
 
 }  // namespace gdn

@@ -26,8 +26,6 @@ namespace gdn {
 
 namespace {
 
-__device__ int g_kv_error = 0;
-
 // 16 channels of a row, as two 8-channel vectors at c0 and c1, such that
 // neighbouring units' vectors are neighbours in memory: the two members of 8
 // rotation pairs (style half), else vectors that hold whole pairs, or none.
@@ -86,7 +84,7 @@ __device__ __forceinline__ void rotate_unit(float* x, const float* row, int u, c
 __device__ __forceinline__ const float* rope_row(const KvAppendArgs& a, int tok, int pos) {
     int p = a.positions ? a.positions[tok] : pos;
     if (p < 0 || p >= a.rope_len) {
-        atomicCAS(&g_kv_error, 0, kKvErrRope);
+        atomicMax(a.error, kKvErrRope);
         p = p < 0 ? 0 : a.rope_len - 1;
     }
     return a.rope + static_cast<size_t>(p) * a.rope_dim;
@@ -178,13 +176,13 @@ kv_append_kernel(const KvAppendArgs a, const int n_store_blocks) {
     }
     const int q0 = a.b.cu[seq], len = a.b.kv_lens[seq], start = len - (a.b.cu[seq + 1] - q0);
     const long long cap = static_cast<long long>(a.b.pages_per_seq) * B;
-    if ((start < 0 || len > cap) && tid == 0) atomicCAS(&g_kv_error, 0, kKvErrTable);
+    if ((start < 0 || len > cap) && tid == 0) atomicMax(a.error, kKvErrTable);
     const int p0 = max(start, 0), p1 = static_cast<int>(min(static_cast<long long>(len), cap));
     const int lp = p0 / B + local;
     if (p0 >= p1 || lp > (p1 - 1) / B) return;
     const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + lp];
     if (page < 0 || page >= a.c.n_pages) {
-        if (tid == 0) atomicCAS(&g_kv_error, 0, kKvErrTable);
+        if (tid == 0) atomicMax(a.error, kKvErrTable);
         return;
     }
     const int r0 = max(p0 - lp * B, 0), r1 = min(p1 - lp * B, B);  // new rows of the page
@@ -281,7 +279,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvReadArgs 
     const int page = lp >= 0 && lp < a.b.pages_per_seq
                          ? a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + lp] : -1;
     const bool mapped = page >= 0 && page < a.c.n_pages;  // else zeros
-    if (!mapped && (threadIdx.x & 31) == 0) atomicCAS(&g_kv_error, 0, kKvErrTable);
+    if (!mapped && (threadIdx.x & 31) == 0) atomicMax(a.error, kKvErrTable);
     const size_t block0 = static_cast<size_t>(mapped ? page : 0) * a.n_kv_heads;
     const int slot = mapped ? static_cast<int>(pos % a.page_size) : 0;
     uint2 code[kReadVectors][2];
@@ -375,15 +373,6 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, int head_dim, bool bf16, boo
 
 cudaError_t launch_kv_read(const KvReadArgs& a, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
     return GDN_KV_PICK(read_t);
-}
-
-cudaError_t read_kv_error(int* code, bool reset) {
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_kv_error, sizeof(int));
-    if (e == cudaSuccess && reset) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbol(g_kv_error, &zero, sizeof(int));
-    }
-    return e;
 }
 
 }  // namespace gdn

@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(256) commit_state_kernel(CommitArgs p) {
 
 cudaError_t read_rec_error(int* code, bool reset) {
     cudaError_t e = cudaMemcpyFromSymbol(code, g_rec_error, sizeof(int));
-    if (e == cudaSuccess && reset) {
+    if (e == cudaSuccess && reset && *code) {
         const int zero = 0;
         e = cudaMemcpyToSymbol(g_rec_error, &zero, sizeof(int));
     }

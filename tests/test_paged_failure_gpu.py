@@ -3,10 +3,15 @@ wait of the kernel for many rows runs out (GDN_FAULT=stall_attention: its look-u
 nothing, for which the others wait 2 s).  Every role gives up without using what did not come, the
 kernel ends, gdn_sync_status reports GDN_ERR_TIMEOUT, and the next call computes correct results.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import gated_deltanet_linear_mixer_gb300 as gdn
+from conftest import ROOT
 from paged_cases import attention_excess, attention_ref, cu_of, gen, make_cache
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +89,40 @@ def test_a_wait_that_runs_out_outranks_data_out_of_range(monkeypatch, same_call)
     with pytest.raises(gdn.GDNError, match="code 40"):
         gdn.sync_status()
     gdn.sync_status()
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """What a process's first calls look up on the device does not get in a capture's way, and a
+    replay's codes are reported."""
+    code = """
+import torch, gated_deltanet_linear_mixer_gb300 as gdn
+from paged_cases import cu_of
+d = gdn.KVDims(16, 4, 128, page_size=64, rope_dim=64)
+cache = gdn.KVCache(d, *(torch.zeros(20, 4, 64, 128, dtype=torch.int8, device="cuda") for _ in "kv"),
+                    *(torch.ones(20, 4, device="cuda") for _ in "kv"))
+table = torch.arange(20, dtype=torch.int32, device="cuda").view(1, 20)
+lens = torch.tensor([700], dtype=torch.int32, device="cuda")
+new = torch.randn(300, 24, 128, device="cuda").bfloat16()
+rope, cu, one = torch.ones(1280, 64, device="cuda"), cu_of([300]), cu_of([1])
+ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    q = gdn.kv_append(d, cache, cu, lens, table, new[:, 16:20], new[:, 20:], q=new[:, :16], rope=rope)
+    a = gdn.kv_attention(d, cache, cu, lens, table, q, workspace=ws)
+    b = gdn.kv_attention(d, cache, one, lens, table, q[299:], workspace=ws)
+    k, v = gdn.kv_read(d, cache, one, lens - 1, table)
+graph.replay()
+gdn.sync_status()
+assert torch.isfinite(a).all() and (a[299:].float() - b.float()).abs().max() < 0.02, (a[299:] - b).abs().max()
+table.fill_(-1)
+graph.replay()
+try:
+    gdn.sync_status()
+except gdn.GDNError as e:
+    assert "code 40" in str(e)
+    print("reported")
+"""
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, cwd=ROOT)
+    assert run.returncode == 0 and run.stdout.strip() == "reported", run.stdout + run.stderr
