@@ -3,7 +3,7 @@ _gdn_bind.so (the native argument marshalling of paged.py) with g++.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library next to this file.  Rebuilds only when a source or header is newer than
-the libraries.
+the libraries, or the module was built for another PyTorch or Python.
 """
 from __future__ import annotations
 
@@ -22,6 +22,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgdn.so")
 BIND_SRC = os.path.join(CSRC, "gdn_bind.cpp")
 BIND_PATH = os.path.join(PKG, "_gdn_bind.so")
+BIND_STAMP = os.path.join(BUILD_DIR, "bind.txt")  # what _gdn_bind.so was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -47,8 +48,16 @@ def _inputs():
 def up_to_date() -> bool:
     if not os.path.exists(LIB_PATH) or not os.path.exists(BIND_PATH):
         return False
+    if not os.path.exists(BIND_STAMP) or open(BIND_STAMP).read() != _bind_for():
+        return False
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BIND_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _bind_for() -> str:
+    """The PyTorch and the Python that the binding's module is tied to."""
+    import torch
+    return f"{torch.__version__} {os.path.dirname(torch.__file__)} {sysconfig.get_config_var('EXT_SUFFIX')}"
 
 
 def _bind_flags():
@@ -103,6 +112,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     tmp = BIND_PATH + f".tmp{os.getpid()}"
     run("link of _gdn_bind.so", [cxx, bind_obj, "-o", tmp, *bind_link])
     os.replace(tmp, BIND_PATH)
+    with open(BIND_STAMP, "w") as f:
+        f.write(_bind_for())
     return LIB_PATH
 
 

@@ -3,6 +3,7 @@ import copy
 import ctypes
 import dataclasses
 import pickle
+import sysconfig
 
 import pytest
 import torch
@@ -115,3 +116,17 @@ def test_vocabularies_whose_indexes_leave_32_bits_are_refused(monkeypatch, vocab
     got = lib.gdn_accept_drafts(1, 1, vocab, 0, 0, at, at, vocab, at, vocab, None, at, at, vocab, at, at, None)
     assert got == (gdn.GDN_ERR_INJECTED if fits else 2)
     assert ("vocab" in lib.gdn_last_error().decode()) == (not fits)
+
+
+# ------------------------------------------------------------------- the build
+@pytest.mark.parametrize("what", ["torch", "python"])
+def test_a_binding_built_for_another_pytorch_is_rebuilt(monkeypatch, what):
+    """The binding's module is tied to the PyTorch and the Python that it was built with."""
+    _build.build()
+    assert _build.up_to_date()
+    if what == "torch":
+        monkeypatch.setattr(torch, "__version__", "2.9.0+other")
+    else:
+        monkeypatch.setattr(sysconfig, "get_config_var",
+                            lambda name, old=sysconfig.get_config_var: ".other.so" if name == "EXT_SUFFIX" else old(name))
+    assert not _build.up_to_date()
