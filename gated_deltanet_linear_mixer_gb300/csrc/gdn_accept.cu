@@ -292,8 +292,9 @@ cudaError_t accept_t(const AcceptArgs& a, cudaStream_t st) {
     int C = kMaxCluster;
     while (C > 1 && (static_cast<long long>(a.n_seq) * C > 152 * 4 || a.vocab / C < 1024)) C /= 2;
     // Drafts summed at a time: one where bytes count, all where the round trips do.  Microseconds at
-    // 1 / 4 / 16: 64 x 8 drafts of 8000 logits 26 / 14.2 / 13.0 (16 taken), 48 x 3 of 32,003 20 / 14.7 / 14.9 (4),
-    // 256 x 4 of them, whose slices are longer, 80 / 108 / 108 (1), 64 x 4 of 131,072 84 / 107 / 107 (1).
+    // 1 / 4 / 16: 64 x 8 drafts of 8000 logits 26 / 14.2 / 13.0 (16 taken), 48 x 3 of 32,003 20 at 1 and 14.8
+    // otherwise (16, which with three drafts is what 4 is), 256 x 4 of them, whose slices are longer,
+    // 80 / 108 / 108 (1), 64 x 4 of 131,072 84 / 107 / 107 (1).
     const int share = a.vocab / C / kThreads;
     const int step = share * (a.T + 1) <= 128 ? kMaxDrafts : share <= 32 ? 4 : 1;
     cudaLaunchConfig_t cfg{};

@@ -10,8 +10,9 @@
 // The value scale enters the exponent; the denominator takes it out again, once
 // per 16 keys.  m_r is a reference, not the exact maximum: it moves (and o_r is
 // rescaled) only when a score exceeds it by 2^kLazy.
-// Queries become f16 after division by a power of two per row (bf16 has fewer
-// bits than f16, so that is exact down to 2^-24 of the row's largest).  Weights
+// Queries become f16 after division by a power of two per row (bf16's 8 bits are
+// exact from 2^-17 of the row's largest up; below, the error is at most 2^-25 of
+// it).  Weights
 // become f16, 11 bits, in a group of keys whose weights are all normal f16
 // numbers (2^-14 .. 2^15 with kBias, scores within 2^-21 of the reference);
 // else two bf16 terms, 16 bits: f16 would drop weights below 2^-24 of the
@@ -36,12 +37,12 @@
 // over thread blocks and joined by kv_attn_join.
 //
 // What bounds it: the codes' bytes for single tokens in groups of 8 heads (256
-// sequences: 195 us, 1.16 GB, 5.9 TB/s of the 6.8 that a copy reaches; one of
-// 131,000 keys 31 us, 4.4 TB/s, since half a round of thread blocks and the join
+// sequences: 194 us, 1.16 GB, 6.0 TB/s of the 6.8 that a copy reaches; one of
+// 131,000 keys 31 us, 4.3 TB/s, since half a round of thread blocks and the join
 // are latency); latency at three thread blocks an SM (168 registers) for drafts,
 // whose rows need more of the warps' work per code (64 x 4 drafts of 32 heads:
-// 110 us, 4.3 TB/s, issue slots 49% busy, most stalls fixed latencies); the
-// two launches for short contexts (1000 keys: 7.2 us).
+// 110 us, 4.3 TB/s, issue slots 47% busy, most stalls fixed latencies); the
+// two launches for short contexts (1000 keys: 7.5 us).
 #include <algorithm>
 #include <atomic>
 

@@ -6,9 +6,9 @@
 //   y_rj = (q_r . ck_j) scale s_k log2 e + log2 s_v,   w_rj = 2^(y_rj - m_r)
 //   o_r = sum_j w_rj cv_j / sum_blk (sum_j w_rj) / s_v
 // with a reference m_r that lags behind the maximum by at most 2^kLazy.  All
-// operands are f16: codes exactly, queries exactly down to 2^-24 of a row's
-// largest, weights (times 2^kBias) with 11 bits; weights below 2^-31 of the
-// reference are dropped.
+// operands are f16: codes exactly, queries exactly from 2^-17 of a row's largest
+// up (below, to 2^-25 of it), weights (times 2^kBias) with 11 bits; weights below
+// 2^-31 of the reference are dropped.
 //
 // One thread block takes one 128-row tile (head_dim 256), or two, of the rows
 // (token, head of the group) of a sequence and kv head, and walks its keys in
@@ -37,10 +37,10 @@
 // core: an issuing thread, which has waited for the writers, fences the one
 // against the other (a writer's fence would also wait for its loads in flight).
 // What bounds it: no unit is saturated, the chain of waits between the roles is.
-// A prompt of 4096 tokens (16 heads of 256) takes 131 us, 1.05 PFLOP/s over the
+// A prompt of 4096 tokens (16 heads of 256) takes 133 us, 1.03 PFLOP/s over the
 // visible pairs: 1.2 us a tile and SM, of which the products need 1024 cycles
-// (tensor pipe 42% busy, issue slots 56%).  16 ragged prompts with a window (32
-// heads of 128) take 314 us, 0.67 PFLOP/s (30%, 47%); each thread block there
+// (tensor pipe 42% busy, issue slots 58%).  16 ragged prompts with a window (32
+// heads of 128) take 307 us, 0.68 PFLOP/s (30%, 48%); each thread block there
 // also walks fewer keys per start.  Tiles of 128 keys were slower when tried, on
 // an earlier form of this kernel: 226 and 609 us, against 222 and 507.
 // Every wait is bounded (2 s); a wait that gives up records a code (42..48) in
@@ -222,7 +222,7 @@ __device__ __forceinline__ uint32_t scaled_f16(uint32_t bf16_pair, float f) {
 }
 
 // SPLIT: the keys are split, and results are partial ones for the join.  A kernel
-// of its own: with both in one the 4096-token prompt takes 134 us instead of 131.
+// of its own: with both in one the 4096-token prompt took 134 us instead of 131.
 template <typename F, int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs a, const KvSplit sp) {
     using C = PCfg<D>;

@@ -311,9 +311,10 @@ gdn_status gdn_layer_prefill(const gdn_dims* dims, const gdn_params* params,
  *   A block_table entry outside [0, n_pages) is an unmapped page: nothing is
  * written to it and no query sees its keys.  A call that meets one where it
  * needs a page, a kv_len above pages_per_seq * page_size, a negative first
- * position or a position outside the rotation table stays in bounds and
- * records a code in the device error word: gdn_sync_status then returns
- * GDN_ERR_INVALID_ARG (40 block table or length, 41 rotation table).
+ * position (in gdn_kv_append and gdn_kv_read; gdn_kv_attention gives zeros) or a
+ * position outside the rotation table stays in bounds and records a code in the
+ * device error word: gdn_sync_status then returns GDN_ERR_INVALID_ARG (40 block
+ * table or length, 41 rotation table).
  */
 
 /* Codes of the cache: int8 (round to nearest even, symmetric, +-127) or
@@ -419,7 +420,9 @@ gdn_status gdn_kv_read(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
  *   workspace: at least gdn_kv_attention_workspace_size() bytes, 256-byte
  *   aligned (NULL when that is 0).
  * Tensor cores, codes as f16 or bf16 operands (exact), fp32 accumulation and
- * softmax.  bf16 activations: weights are f16 (11 bits) or, where some are too
+ * softmax (the hardware's exponentials, 2 ulp).  bf16 activations: queries are f16
+ * under a power of two of their row (exact from 2^-17 of the largest up, below
+ * that to 2^-25 of it); weights are f16 (11 bits) or, where some are too
  * small for that, two bf16 terms (16 bits); calls of many rows (prompts) keep to
  * f16 and drop weights below 2^-31 of a row's reference, which lies within 2^8
  * of its largest.  fp32 activations: queries are f16 (hi, lo) pairs, weights
@@ -458,8 +461,10 @@ typedef enum gdn_dist_form { GDN_DIST_PROBS = 0, GDN_DIST_LOGITS = 1 } gdn_dist_
  *   temperature [n_seq] fp32 >= 0 (logits; NULL: 1).  0 <= T <= 16; vocab at
  *   most 2^31 - 4097.
  *   accepted [n_seq] int32: how many drafts stand (gdn_decode_commit's
- *   `accepted`, plus one where its x begins with the last kept token).  tokens [n_seq, T + 1] int32: those drafts, the drawn token,
- *   then -1.
+ *   `accepted`, plus one where its x begins with the last kept token).
+ *   tokens [n_seq, T + 1] int32: those drafts, the drawn token, then -1.
+ * Exponentials are the hardware's (2 ulp, results below 2^-126 are 0), sums and
+ * comparisons fp32.
  */
 gdn_status gdn_accept_drafts(int32_t n_seq, int32_t T, int32_t vocab, int32_t form, int32_t dtype,
                              const int32_t* drafts, const void* target, int64_t target_stride,
@@ -492,8 +497,10 @@ size_t gdn_timing_report(char* buf, size_t buf_len);
  * token-recurrent kernel's wait for a state copy; 42..48 the cache attention's
  * tensor-core kernel's waits between its roles) and exit cleanly; their
  * outputs are then invalid.  Codes 40 and 41 are not waits: a cache operator
- * met device data out of range (see the cache above) and stayed in bounds.  Waits for the device (cudaMemcpyFromSymbol), writes the code to
- * *code (0 = no error) and clears it when reset != 0.
+ * met device data out of range (see the cache above) and stayed in bounds; a
+ * wait's code is given before them.  Waits for the device
+ * (cudaMemcpyFromSymbol), writes the code to *code (0 = no error) and clears it
+ * when reset != 0.
  */
 gdn_status gdn_device_error(int32_t* code, int32_t reset);
 
@@ -503,7 +510,8 @@ gdn_status gdn_device_error(int32_t* code, int32_t reset);
  * up since the last check (the outputs and states of the calls since then are
  * invalid and must be recomputed; the CUDA context stays usable),
  * GDN_ERR_INVALID_ARG if a cache operator met device data out of range,
- * GDN_ERR_CUDA if the stream reports a CUDA error, else GDN_OK.  A serving loop calls it
+ * GDN_ERR_CUDA if the stream reports a CUDA error, else GDN_OK.  Four copies of a
+ * few bytes, and one more for a word that is set.  A serving loop calls it
  * where it would synchronize anyway, and fails the affected requests closed.
  */
 gdn_status gdn_sync_status(void* stream);
