@@ -10,7 +10,9 @@ is missing the calls raise.  Build it with ``gated_deltanet_linear_mixer_gb300._
 Entry points (same names as the C ABI, without the ``gdn_`` prefix):
 ``conv``, ``prefill``, ``prefill_workspace_size``, ``decode``, ``decode_commit``; for the
 full-attention layers of a hybrid stack and its speculative loop (``paged.py``):
-``kv_append``, ``kv_attention``, ``kv_read``, ``accept_drafts``.
+``kv_append``, ``kv_attention``, ``kv_read``, ``accept_drafts``; for those whose cache holds
+latents, and for the pages of any cache (``latent.py``): ``latent_append``, ``latent_read``,
+``latent_attention``, ``expanded_attention``, ``copy_pages``.
 """
 from __future__ import annotations
 
@@ -36,7 +38,9 @@ EXPORTS = ("gdn_conv", "gdn_prefill_workspace_size", "gdn_prefill", "gdn_prefill
            "gdn_prefill_noalloc_scratch_bytes", "gdn_decode", "gdn_verify", "gdn_decode_commit",
            "gdn_layer_prefill_workspace_size", "gdn_layer_prefill",
            "gdn_kv_append", "gdn_kv_read", "gdn_kv_attention_workspace_size", "gdn_kv_attention",
-           "gdn_accept_drafts", "gdn_timing_enable", "gdn_timing_report",
+           "gdn_accept_drafts", "gdn_latent_append", "gdn_latent_read",
+           "gdn_latent_attention_workspace_size", "gdn_latent_attention", "gdn_expanded_attention",
+           "gdn_copy_pages", "gdn_timing_enable", "gdn_timing_report",
            "gdn_device_error", "gdn_sync_status", "gdn_last_error", "gdn_version")
 
 
@@ -86,6 +90,17 @@ class _KVBatch(ctypes.Structure):
                 ("block_table", ctypes.c_void_p)]
 
 
+class _LatentDims(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("rope_style", ctypes.c_int32), ("nope_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("norm_eps", ctypes.c_float)]
+
+
+class _LatentCache(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("n_pages", ctypes.c_int32)]
+
+
 class _Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64)]
@@ -126,6 +141,16 @@ def load(path: str | None = None):
     lib.gdn_kv_attention.argtypes = [PK, PC, PB, P, I32, PR, P, P, ctypes.c_size_t, P]
     lib.gdn_accept_drafts.argtypes = [I32, I32, I32, I32, I32, P, P, I64, P, I64, P, P, P, I64, P,
                                       P, P]
+    PL, PA = ctypes.POINTER(_LatentDims), ctypes.POINTER(_LatentCache)
+    lib.gdn_latent_append.argtypes = [PL, PA, PB, P, PR, P, PR, PR, P, I32, P, P, P]
+    lib.gdn_latent_read.argtypes = [PL, PA, PB, P, P, P]
+    lib.gdn_latent_attention_workspace_size.argtypes = [PL, I32, P, ctypes.POINTER(ctypes.c_size_t)]
+    lib.gdn_latent_attention.argtypes = [PL, PA, PB, P, PR, P, P, ctypes.c_size_t, P]
+    lib.gdn_expanded_attention.argtypes = [PL, I32, P, P, P, P, PR, PR, PR, PR, P, P]
+    lib.gdn_copy_pages.argtypes = [I32, P, P, I32, I32, P, P, P]
+    for f in ("gdn_latent_append", "gdn_latent_read", "gdn_latent_attention_workspace_size",
+              "gdn_latent_attention", "gdn_expanded_attention", "gdn_copy_pages"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("gdn_kv_append", "gdn_kv_read", "gdn_kv_attention_workspace_size",
               "gdn_kv_attention", "gdn_accept_drafts"):
         getattr(lib, f).restype = ctypes.c_int
@@ -503,8 +528,12 @@ def decode_commit(d: Dims, accepted, x, inter_states, state, conv_state=None):
 
 from .paged import (KVCache, KVDims, accept_drafts, kv_append, kv_attention,  # noqa: E402
                     kv_attention_workspace_size, kv_read)
+from .latent import (LatentCache, LatentDims, copy_pages, expanded_attention, latent_append,  # noqa: E402
+                     latent_attention, latent_attention_workspace_size, latent_read)
 
-__all__ = ["KVCache", "KVDims", "accept_drafts", "kv_append", "kv_attention",
+__all__ = ["LatentCache", "LatentDims", "copy_pages", "expanded_attention", "latent_append",
+           "latent_attention", "latent_attention_workspace_size", "latent_read",
+           "KVCache", "KVDims", "accept_drafts", "kv_append", "kv_attention",
            "kv_attention_workspace_size", "kv_read", "Dims", "Params", "GDNError", "load", "version", "timing_enable", "timing_report",
            "device_error", "sync_status",
            "conv", "prefill",

@@ -1,5 +1,5 @@
-// Python module _gdn_bind: argument marshalling of the cache operators and of
-// draft verification in native code.
+// Python module _gdn_bind: argument marshalling of the cache operators (8-bit and
+// latent), of expanded attention, page copies and draft verification in native code.
 //
 // These calls take a few microseconds on the GPU; looking at a dozen tensors'
 // types, shapes, strides and devices from Python takes several times that.  So
@@ -13,10 +13,12 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <initializer_list>
 #include <optional>
 #include <string>
+#include <vector>
 
 #include "gdn.h"
 
@@ -351,6 +353,211 @@ PyObject* accept_drafts(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
+// ------------------------------------------------------------ the latent cache
+gdn_latent_cache latent_cache_of(const gdn_latent_dims* d, PyObject* rows) {
+    const at::Tensor& r = tensor(rows, "cache.rows");
+    const int64_t n = r.dim() > 0 ? r.size(0) : 0, shape[3] = {n, d->page_size, d->latent_dim + d->rope_dim};
+    if (r.scalar_type() != at::kBFloat16 || r.sizes() != at::IntArrayRef(shape, 3))
+        bad(PyExc_ValueError, "the cache was made for other dimensions");
+    if (n > 0x7fffffff) bad(PyExc_ValueError, "a cache has at most 2^31 - 1 pages");
+    return gdn_latent_cache{plain(rows, "cache.rows", at::kBFloat16).data_ptr(), static_cast<int32_t>(n)};
+}
+
+// bf16 rows [tokens, heads, width] (heads 0: [tokens, width]) with free strides.  An axis of one
+// element is never stepped along: its stride, which may be anything, is given as the dense one.
+gdn_rows bf16_rows(const at::Tensor& t, const char* name, int64_t tokens, int64_t heads, int64_t width) {
+    want_type(t, name, at::kBFloat16);
+    if (heads > 0) want_shape(t, name, {tokens, heads, width});
+    else want_shape(t, name, {tokens, width});
+    want_cuda(t, name);
+    if (t.numel() > 0 && t.stride(t.dim() - 1) != 1) bad(PyExc_ValueError, "%s: a row's channels must be contiguous", name);
+    const int64_t hs = heads > 1 ? t.stride(1) : width;
+    return gdn_rows{t.data_ptr(), tokens > 1 ? t.stride(0) : (heads > 1 ? heads : 1) * width, hs};
+}
+gdn_rows bf16_rows(PyObject* o, const char* name, int64_t tokens, int64_t heads, int64_t width) {
+    return bf16_rows(tensor(o, name), name, tokens, heads, width);
+}
+
+// dims, cache.rows, cu_dev, cu_host, kv_lens, block_table, c, norm_w, q_rope, q_out, rope, positions, rows_out
+PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject* {
+        const auto device = device_of(a, {{1, "cache.rows"}, {2, "cu_seqlens"}, {4, "kv_lens"}, {5, "block_table"}, {6, "c"},
+                                          {7, "norm_w"}, {8, "q_rope"}, {9, "q_out"}, {10, "rope"}, {11, "positions"},
+                                          {12, "rows_out"}});
+        const auto* d = struct_at<gdn_latent_dims>(a[0]);
+        const gdn_latent_cache c = latent_cache_of(d, a[1]);
+        const int32_t* lens;
+        int64_t tokens;
+        const gdn_kv_batch b = batch_of(a[2], a[3], a[4], "kv_lens", a[5], &lens, &tokens);
+        const int64_t width = d->latent_dim + d->rope_dim;
+        const gdn_rows rows = bf16_rows(a[6], "c", tokens, 0, width);
+        const at::Tensor& like = THPVariable_Unpack(a[6]);
+        const float* norm = a[7] == Py_None ? nullptr : plain(a[7], "norm_w", at::kFloat, {d->latent_dim}).data_ptr<float>();
+        gdn_rows q{}, q_out{};
+        at::Tensor out;
+        const bool with_q = a[8] != Py_None;
+        if (with_q) {
+            q = bf16_rows(a[8], "q_rope", tokens, d->n_heads, d->rope_dim);
+            out = a[9] != Py_None ? tensor(a[9], "q_out")
+                                  : at::empty({tokens, d->n_heads, d->rope_dim}, like.options().dtype(at::kBFloat16));
+            q_out = bf16_rows(out, "q_out", tokens, d->n_heads, d->rope_dim);
+        }
+        const float* rope = nullptr;
+        int64_t rope_rows = 0;
+        if (a[10] != Py_None) {
+            const at::Tensor& r = plain(a[10], "rope", at::kFloat);
+            if (r.dim() != 2 || r.size(1) != d->rope_dim)
+                bad(PyExc_ValueError, "rope must have shape (rows, %d), got %s", d->rope_dim, shape_text(r.sizes()).c_str());
+            rope = r.data_ptr<float>();
+            rope_rows = r.size(0);
+            if (rope_rows < 1) bad(PyExc_ValueError, "rope must hold at least one row");
+            if (rope_rows > 0x7fffffff) bad(PyExc_ValueError, "rope has at most 2^31 - 1 rows");
+        }
+        const int32_t* positions =
+            a[11] == Py_None ? nullptr : plain(a[11], "positions", at::kInt, {tokens}).data_ptr<int32_t>();
+        void* packed = a[12] == Py_None ? nullptr : plain(a[12], "rows_out", at::kBFloat16, {tokens, width}).data_ptr();
+        check("gdn_latent_append",
+              gdn_latent_append(d, &c, &b, lens, &rows, norm, with_q ? &q : nullptr, with_q ? &q_out : nullptr, rope,
+                                static_cast<int32_t>(rope_rows), positions, packed, Launch(device).stream()));
+        if (!with_q) Py_RETURN_NONE;
+        return THPVariable_Wrap(out);
+    });
+}
+
+// dims, cache.rows, cu_dev, cu_host, starts, block_table, out
+PyObject* latent_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject* {
+        const auto device = device_of(a, {{1, "cache.rows"}, {2, "cu_seqlens"}, {4, "starts"}, {5, "block_table"}, {6, "out"}});
+        const auto* d = struct_at<gdn_latent_dims>(a[0]);
+        const gdn_latent_cache c = latent_cache_of(d, a[1]);
+        const int32_t* starts;
+        int64_t tokens;
+        const gdn_kv_batch b = batch_of(a[2], a[3], a[4], "starts", a[5], &starts, &tokens);
+        at::Tensor out = output(a[6], "out", at::kBFloat16, {tokens, d->latent_dim + d->rope_dim}, THPVariable_Unpack(a[5]));
+        check("gdn_latent_read", gdn_latent_read(d, &c, &b, starts, out.data_ptr(), Launch(device).stream()));
+        return THPVariable_Wrap(out);
+    });
+}
+
+// dims, cache.rows, cu_dev, cu_host, kv_lens, block_table, q, out, workspace
+PyObject* latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        const auto device = device_of(a, {{1, "cache.rows"}, {2, "cu_seqlens"}, {4, "kv_lens"}, {5, "block_table"}, {6, "q"},
+                                          {7, "out"}, {8, "workspace"}});
+        const auto* d = struct_at<gdn_latent_dims>(a[0]);
+        const gdn_latent_cache c = latent_cache_of(d, a[1]);
+        const int32_t* lens;
+        int64_t tokens;
+        const gdn_kv_batch b = batch_of(a[2], a[3], a[4], "kv_lens", a[5], &lens, &tokens);
+        const gdn_rows q = bf16_rows(a[6], "q", tokens, d->n_heads, d->latent_dim + d->rope_dim);
+        const at::Tensor& like = THPVariable_Unpack(a[6]);
+        at::Tensor out = output(a[7], "out", at::kBFloat16, {tokens, d->n_heads, d->latent_dim}, like);
+        at::Tensor ws;
+        if (a[8] != Py_None) {
+            ws = tensor(a[8], "workspace");
+            if (!ws.is_contiguous()) bad(PyExc_ValueError, "workspace must be contiguous");
+            want_cuda(ws, "workspace");
+        } else {
+            size_t need = 0;
+            check("gdn_latent_attention_workspace_size",
+                  gdn_latent_attention_workspace_size(d, b.n_seq, b.cu_seqlens_host, &need));
+            if (need) ws = at::empty({static_cast<int64_t>(need)}, like.options().dtype(at::kByte));
+        }
+        check("gdn_latent_attention",
+              gdn_latent_attention(d, &c, &b, lens, &q, out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr,
+                                   ws.defined() ? ws.nbytes() : 0, Launch(device).stream()));
+        return THPVariable_Wrap(out);
+    });
+}
+
+// A (device, host) pair of int32 cu_seqlens: entries and pointers.
+struct Cu {
+    const int32_t *dev, *host;
+    int64_t n, total;
+};
+Cu cu_of(PyObject* cu_dev, PyObject* cu_host, const char* name) {
+    const at::Tensor& dev = plain(cu_dev, name, at::kInt);
+    const at::Tensor& host = tensor(cu_host, name);
+    want_type(host, name, at::kInt);
+    if (host.is_cuda() || !host.is_contiguous() || host.numel() != dev.numel() || host.numel() < 1)
+        bad(PyExc_ValueError, "%s pair must be (device tensor, host tensor) of equal size", name);
+    Cu c{dev.data_ptr<int32_t>(), host.data_ptr<int32_t>(), host.numel() - 1, 0};
+    if (c.n > 0) c.total = c.host[c.n];
+    return c;
+}
+
+// dims, cu_q dev, host, cu_kv dev, host, q, k, k_rope, v, out
+PyObject* expanded_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject* {
+        const auto device = device_of(a, {{1, "cu_q"}, {3, "cu_kv"}, {5, "q"}, {6, "k"}, {7, "k_rope"}, {8, "v"}, {9, "out"}});
+        const auto* d = struct_at<gdn_latent_dims>(a[0]);
+        const Cu cq = cu_of(a[1], a[2], "cu_q"), ck = cu_of(a[3], a[4], "cu_kv");
+        if (cq.n != ck.n) bad(PyExc_ValueError, "cu_q and cu_kv must name as many sequences");
+        const gdn_rows q = bf16_rows(a[5], "q", cq.total, d->n_heads, d->nope_dim + d->rope_dim);
+        const gdn_rows k = bf16_rows(a[6], "k", ck.total, d->n_heads, d->nope_dim);
+        const gdn_rows r = bf16_rows(a[7], "k_rope", ck.total, 0, d->rope_dim);
+        const gdn_rows v = bf16_rows(a[8], "v", ck.total, d->n_heads, d->v_dim);
+        at::Tensor out = output(a[9], "out", at::kBFloat16, {cq.total, d->n_heads, d->v_dim}, THPVariable_Unpack(a[5]));
+        check("gdn_expanded_attention",
+              gdn_expanded_attention(d, static_cast<int32_t>(cq.n), cq.dev, cq.host, ck.dev, ck.host, &q, &k, &r, &v,
+                                     out.data_ptr(), Launch(device).stream()));
+        return THPVariable_Wrap(out);
+    });
+}
+
+// Page numbers: a list or tuple of ints, or a 1-d int32 tensor on the host.
+std::vector<int32_t> pages_of(PyObject* o, const char* name) {
+    std::vector<int32_t> v;
+    if (THPVariable_Check(o)) {
+        const at::Tensor& t = THPVariable_Unpack(o);
+        want_type(t, name, at::kInt);
+        if (t.is_cuda() || t.dim() != 1 || !t.is_contiguous())
+            bad(PyExc_ValueError, "%s must be a list of page numbers or a 1-d host tensor", name);
+        v.assign(t.data_ptr<int32_t>(), t.data_ptr<int32_t>() + t.numel());
+        return v;
+    }
+    if (!PyList_Check(o) && !PyTuple_Check(o))
+        bad(PyExc_TypeError, "%s must be a list of page numbers or a 1-d host tensor", name);
+    PyObject** items = PySequence_Fast_ITEMS(o);
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    v.reserve(n);
+    for (Py_ssize_t i = 0; i < n; ++i) v.push_back(as_int(items[i]));
+    return v;
+}
+
+// the caches' tensors (a tuple, first axis: pages), src, dst
+PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        if (!PyTuple_Check(a[0])) bad(PyExc_TypeError, "caches must be a tuple of tensors");
+        const Py_ssize_t n_buffers = PyTuple_GET_SIZE(a[0]);
+        std::vector<void*> bases;
+        std::vector<size_t> bytes;
+        int64_t pages = 0x7fffffff;
+        std::optional<at::Device> device;
+        for (Py_ssize_t i = 0; i < n_buffers; ++i) {
+            const at::Tensor& t = tensor(PyTuple_GET_ITEM(a[0], i), "a cache's tensor");
+            want_cuda(t, "a cache's tensor");
+            if (!t.is_contiguous() || t.dim() < 2) bad(PyExc_ValueError, "a cache's tensor must be contiguous");
+            if (!device) device = t.device();
+            if (t.device() != *device)
+                bad(PyExc_ValueError, "the caches are on devices %s and %s", device->str().c_str(), t.device().str().c_str());
+            pages = std::min(pages, t.size(0));
+            if (t.size(0) == 0) continue;
+            bases.push_back(t.data_ptr());
+            bytes.push_back(t.nbytes() / t.size(0));
+        }
+        const std::vector<int32_t> src = pages_of(a[1], "src"), dst = pages_of(a[2], "dst");
+        if (src.size() != dst.size()) bad(PyExc_ValueError, "src and dst must have as many pages (%zu, %zu)", src.size(), dst.size());
+        if (src.size() > 0x7fffffff) bad(PyExc_ValueError, "more than 2^31 - 1 pairs");
+        if (bases.empty() && (n_buffers == 0 || src.empty())) Py_RETURN_NONE;
+        if (bases.empty()) bad(PyExc_ValueError, "the caches have no pages");
+        check("gdn_copy_pages",
+              gdn_copy_pages(static_cast<int32_t>(bases.size()), bases.data(), bytes.data(), static_cast<int32_t>(pages),
+                             static_cast<int32_t>(src.size()), src.data(), dst.data(), Launch(device).stream()));
+        Py_RETURN_NONE;
+    });
+}
+
 PyObject* on_failure(PyObject*, PyObject* f) {
     Py_XDECREF(g_fail);
     Py_INCREF(f);
@@ -363,6 +570,11 @@ PyMethodDef methods[] = {
     {"kv_read", reinterpret_cast<PyCFunction>(kv_read), METH_FASTCALL, nullptr},
     {"kv_attention", reinterpret_cast<PyCFunction>(kv_attention), METH_FASTCALL, nullptr},
     {"accept_drafts", reinterpret_cast<PyCFunction>(accept_drafts), METH_FASTCALL, nullptr},
+    {"latent_append", reinterpret_cast<PyCFunction>(latent_append), METH_FASTCALL, nullptr},
+    {"latent_read", reinterpret_cast<PyCFunction>(latent_read), METH_FASTCALL, nullptr},
+    {"latent_attention", reinterpret_cast<PyCFunction>(latent_attention), METH_FASTCALL, nullptr},
+    {"expanded_attention", reinterpret_cast<PyCFunction>(expanded_attention), METH_FASTCALL, nullptr},
+    {"copy_pages", reinterpret_cast<PyCFunction>(copy_pages), METH_FASTCALL, nullptr},
     {"on_failure", on_failure, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -1,0 +1,287 @@
+// The latent cache's rows: appending (norm, position rotation, store), reading
+// back; and copying pages of any cache.
+//
+// latent_append: a warp per token and part: its row (latent and position key), or
+// 64 units of 16 channels of its q.  The row stays in registers between the
+// norm's sum and the store.  Products and sums of the rotation are rounded one by
+// one (no fused multiply-add), as the 8-bit cache's are.
+// latent_read: a warp takes kReadTokens consecutive rows, whose places its first
+// lanes look up side by side.
+// copy_pages: the pairs travel as kernel arguments, so that nothing is copied to
+// the device and a captured call keeps its pairs.
+#include <algorithm>
+#include <utility>
+#include <vector>
+
+#include "gdn_internal.h"
+#include "gdn_kv.cuh"
+#include "gdn_latent.h"
+
+namespace gdn {
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float ra = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    const float rb = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    a = ra;
+    b = rb;
+}
+
+// Unit u (0..3) of a position part: 8 rotation pairs as two 8-channel vectors.
+__device__ __forceinline__ int unit_first(int u, int style) { return style == 0 ? 8 * u : 16 * u; }
+__device__ __forceinline__ int unit_second(int u, int style) { return style == 0 ? 8 * u + kRopeDim / 2 : 16 * u + 8; }
+
+// x: the two vectors of unit u; row: cosines and sines of the token.
+__device__ __forceinline__ void turn_unit(float* x, const float* row, int u, int style) {
+    float c[8], s[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        Vec16<float>::load(row + 8 * u + i, c + i);
+        Vec16<float>::load(row + kRopeDim / 2 + 8 * u + i, s + i);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (style == 0) turn(x[i], x[8 + i], c[i], s[i]);
+        else turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
+    }
+}
+
+// Eight values rounded to bf16, finite: NaN becomes 0, infinities the largest number.
+__device__ __forceinline__ uint4 finite_bf16(const float* x) {
+    constexpr float kTop = 3.3895313892515355e38f;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -kTop), kTop) : 0.0f;
+    return make_uint4(pack_bf16_pair(y[0], y[1]), pack_bf16_pair(y[2], y[3]), pack_bf16_pair(y[4], y[5]),
+                      pack_bf16_pair(y[6], y[7]));
+}
+
+constexpr int kAppendThreads = 128;
+constexpr int kUnits = 4;                // of a position part
+constexpr int kQUnits = 2;               // units of q a lane has in flight
+
+template <int C>
+__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const LatentAppendArgs a, const int parts) {
+    constexpr int N = C / 256;           // 8-channel vectors of the latent a lane holds
+    const int lane = threadIdx.x & 31;
+    const long long w = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const int tok = static_cast<int>(w / parts), part = static_cast<int>(w % parts);  // part 0: the row
+    if (tok >= a.b.n_tokens) return;
+
+    // loads first: they depend on nothing
+    float x[2][16];
+    const bf16* src = static_cast<const bf16*>(a.rows.data) + tok * a.rows.token_stride;
+    const bf16* qs = static_cast<const bf16*>(a.q.data) + tok * a.q.token_stride;
+    const int u0 = (part - 1) * 32 * kQUnits + lane, n_units = a.n_heads * kUnits;
+    if (part == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) Vec16<bf16>::load(src + 8 * lane + 256 * i, x[0] + 8 * i);
+        if (lane < kUnits) {
+            Vec16<bf16>::load(src + C + unit_first(lane, a.rope_style), x[1]);
+            Vec16<bf16>::load(src + C + unit_second(lane, a.rope_style), x[1] + 8);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kQUnits; ++k) {
+            const int u = u0 + 32 * k;
+            if (u >= n_units) break;
+            const bf16* head = qs + u / kUnits * a.q.head_stride;
+            Vec16<bf16>::load(head + unit_first(u % kUnits, a.rope_style), x[k]);
+            Vec16<bf16>::load(head + unit_second(u % kUnits, a.rope_style), x[k] + 8);
+        }
+    }
+
+    const int seq = a.b.uniform_q ? tok / a.b.uniform_q : warp_seq_of_token(a.b.cu, a.b.n_seq, tok);
+    const long long pos = static_cast<long long>(a.b.kv_lens[seq]) - (a.b.cu[seq + 1] - tok);
+    const float* table = nullptr;
+    if (a.rope) {
+        long long p = a.positions ? a.positions[tok] : pos;
+        if (p < 0 || p >= a.rope_len) {
+            if (lane == 0) atomicMax(a.error, kKvErrRope);
+            p = p < 0 ? 0 : a.rope_len - 1;
+        }
+        table = a.rope + static_cast<size_t>(p) * kRopeDim;
+    }
+
+    if (part > 0) {
+        bf16* qd = static_cast<bf16*>(const_cast<void*>(a.q_out.data)) + tok * a.q_out.token_stride;
+#pragma unroll
+        for (int k = 0; k < kQUnits; ++k) {
+            const int u = u0 + 32 * k;
+            if (u >= n_units) break;
+            if (table) turn_unit(x[k], table, u % kUnits, a.rope_style);
+            bf16* head = qd + u / kUnits * a.q_out.head_stride;
+            Vec16<bf16>::store(head + unit_first(u % kUnits, a.rope_style), x[k]);
+            Vec16<bf16>::store(head + unit_second(u % kUnits, a.rope_style), x[k] + 8);
+        }
+        return;
+    }
+
+    const long long lp = pos < 0 ? -1 : pos / a.page_size;
+    const int page = lp >= 0 && lp < a.b.pages_per_seq ? a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + lp] : -1;
+    const bool mapped = page >= 0 && page < a.c.n_pages;
+    if (!mapped && lane == 0) atomicMax(a.error, kKvErrTable);
+    if (a.norm_w) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8 * N; ++i) sum = fmaf(x[0][i], x[0][i], sum);
+        const float r = rsqrtf(group_sum<32>(sum) * (1.0f / C) + a.eps);
+#pragma unroll
+        for (int i = 0; i < 8 * N; i += 4) {
+            float g[4];
+            Vec16<float>::load(a.norm_w + 8 * lane + 256 * (i / 8) + i % 8, g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[0][i + e] = x[0][i + e] * r * g[e];
+        }
+    }
+    uint4 v[N], k0 = make_uint4(0, 0, 0, 0), k1 = k0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = finite_bf16(x[0] + 8 * i);
+    if (lane < kUnits) {
+        if (table) turn_unit(x[1], table, lane, a.rope_style);
+        k0 = finite_bf16(x[1]);
+        k1 = finite_bf16(x[1] + 8);
+    }
+    auto store = [&](bf16* row) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(row + 8 * lane + 256 * i) = v[i];
+        if (lane < kUnits) {
+            *reinterpret_cast<uint4*>(row + C + unit_first(lane, a.rope_style)) = k0;
+            *reinterpret_cast<uint4*>(row + C + unit_second(lane, a.rope_style)) = k1;
+        }
+    };
+    constexpr int W = C + kRopeDim;
+    if (mapped)
+        store(static_cast<bf16*>(a.c.rows) + (static_cast<size_t>(page) * a.page_size + static_cast<int>(pos % a.page_size)) * W);
+    if (a.rows_out) store(static_cast<bf16*>(a.rows_out) + static_cast<size_t>(tok) * W);
+}
+
+constexpr int kReadThreads = 256, kReadTokens = 4;
+
+template <int C>
+__global__ void __launch_bounds__(kReadThreads) latent_read_kernel(const LatentReadArgs a) {
+    constexpr int V = (C + kRopeDim) / 8, K = (kReadTokens * V + 31) / 32;  // vectors of a row, of a lane
+    const int lane = threadIdx.x & 31;
+    const long long w = static_cast<long long>(blockIdx.x) * (kReadThreads / 32) + (threadIdx.x >> 5);
+    if (w * kReadTokens >= a.b.n_tokens) return;
+    const int tok0 = static_cast<int>(w) * kReadTokens, n = min(kReadTokens, a.b.n_tokens - tok0);
+    long long at = -1;  // row in the cache of token tok0 + lane
+    if (lane < n) {
+        const int tok = tok0 + lane, seq = a.b.uniform_q ? tok / a.b.uniform_q : seq_of_token(a.b.cu, a.b.n_seq, tok);
+        const long long pos = static_cast<long long>(a.b.kv_lens[seq]) + (tok - a.b.cu[seq]);
+        const long long lp = pos < 0 ? -1 : pos / a.page_size;
+        const int page = lp >= 0 && lp < a.b.pages_per_seq ? a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + lp] : -1;
+        if (page >= 0 && page < a.c.n_pages) at = static_cast<long long>(page) * a.page_size + pos % a.page_size;
+        else atomicMax(a.error, kKvErrTable);
+    }
+    const uint4* src = static_cast<const uint4*>(a.c.rows);
+    uint4* dst = static_cast<uint4*>(a.out) + static_cast<size_t>(tok0) * V;
+    uint4 v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = lane + 32 * k, t = i / V;
+        const long long row = __shfl_sync(0xffffffffu, at, t & 31);
+        v[k] = t < n && row >= 0 ? src[row * V + i % V] : make_uint4(0, 0, 0, 0);  // zeros of unmapped pages
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = lane + 32 * k;
+        if (i < n * V) dst[i] = v[k];
+    }
+}
+
+// ---------------------------------------------------------------- page copies
+template <int PAIRS, int BUFFERS> struct CopyArgs {
+    uint8_t* base[BUFFERS];
+    unsigned bytes[BUFFERS];
+    int n_buffers;
+    int2 pair[PAIRS];  // source, destination
+};
+constexpr int kCopyThreads = 256, kCopyVectors = 4;
+
+// W: what is moved at a time, uint4 or uint32_t.
+template <typename W, typename A>
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ A a) {
+    const int2 p = a.pair[blockIdx.y];
+    for (int b = blockIdx.z; b < a.n_buffers; b += gridDim.z) {
+        const unsigned n = a.bytes[b] / sizeof(W);
+        const W* src = reinterpret_cast<const W*>(a.base[b] + static_cast<size_t>(p.x) * a.bytes[b]);
+        W* dst = reinterpret_cast<W*>(a.base[b] + static_cast<size_t>(p.y) * a.bytes[b]);
+        for (unsigned i0 = blockIdx.x * kCopyThreads * kCopyVectors + threadIdx.x; i0 < n;
+             i0 += gridDim.x * kCopyThreads * kCopyVectors) {
+            W v[kCopyVectors];
+#pragma unroll
+            for (int k = 0; k < kCopyVectors; ++k)
+                if (i0 + k * kCopyThreads < n) v[k] = src[i0 + k * kCopyThreads];
+#pragma unroll
+            for (int k = 0; k < kCopyVectors; ++k)
+                if (i0 + k * kCopyThreads < n) dst[i0 + k * kCopyThreads] = v[k];
+        }
+    }
+}
+
+template <typename W, int PAIRS, int BUFFERS>
+cudaError_t copy_some(const std::pair<uint8_t*, unsigned>* buffers, int n_buffers, const int32_t* src, const int32_t* dst,
+                      int n_pairs, cudaStream_t st) {
+    using A = CopyArgs<PAIRS, BUFFERS>;
+    A a;
+    for (int b0 = 0; b0 < n_buffers; b0 += BUFFERS) {
+        a.n_buffers = std::min(BUFFERS, n_buffers - b0);
+        unsigned most = 0;
+        for (int b = 0; b < a.n_buffers; ++b) {
+            a.base[b] = buffers[b0 + b].first;
+            a.bytes[b] = buffers[b0 + b].second;
+            most = std::max(most, a.bytes[b]);
+        }
+        const unsigned step = kCopyThreads * kCopyVectors * sizeof(W);
+        for (int p0 = 0; p0 < n_pairs; p0 += PAIRS) {
+            const int n = std::min(PAIRS, n_pairs - p0);
+            for (int i = 0; i < n; ++i) a.pair[i] = make_int2(src[p0 + i], dst[p0 + i]);
+            copy_pages_kernel<W, A><<<dim3((most + step - 1) / step, n, a.n_buffers), kCopyThreads, 0, st>>>(a);
+            const cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const LatentAppendArgs& a, int latent_dim, cudaStream_t st) {
+    const int parts = 1 + (a.q.data ? (a.n_heads * kUnits + 32 * kQUnits - 1) / (32 * kQUnits) : 0);
+    const long long warps = static_cast<long long>(a.b.n_tokens) * parts;
+    const long long blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (latent_dim == 512) latent_append_kernel<512><<<static_cast<unsigned>(blocks), kAppendThreads, 0, st>>>(a, parts);
+    else latent_append_kernel<256><<<static_cast<unsigned>(blocks), kAppendThreads, 0, st>>>(a, parts);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_latent_read(const LatentReadArgs& a, int latent_dim, cudaStream_t st) {
+    const long long warps = (static_cast<long long>(a.b.n_tokens) + kReadTokens - 1) / kReadTokens;
+    const unsigned blocks = static_cast<unsigned>((warps + kReadThreads / 32 - 1) / (kReadThreads / 32));
+    if (latent_dim == 512) latent_read_kernel<512><<<blocks, kReadThreads, 0, st>>>(a);
+    else latent_read_kernel<256><<<blocks, kReadThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_copy_pages(void* const* bases, const size_t* page_bytes, int n_buffers, const int32_t* src,
+                              const int32_t* dst, int n_pairs, cudaStream_t st) {
+    // arrays whose pages all lie on 16 bytes, and the others
+    std::vector<std::pair<uint8_t*, unsigned>> wide, narrow;
+    for (int b = 0; b < n_buffers; ++b) {
+        const bool w = page_bytes[b] % 16 == 0 && (reinterpret_cast<uintptr_t>(bases[b]) & 15u) == 0;
+        (w ? wide : narrow).emplace_back(static_cast<uint8_t*>(bases[b]), static_cast<unsigned>(page_bytes[b]));
+    }
+    cudaError_t e = cudaSuccess;
+    if (!wide.empty())
+        e = copy_some<uint4, 400, 32>(wide.data(), static_cast<int>(wide.size()), src, dst, n_pairs, st);
+    if (e == cudaSuccess && !narrow.empty())
+        e = copy_some<uint32_t, 400, 32>(narrow.data(), static_cast<int>(narrow.size()), src, dst, n_pairs, st);
+    return e;
+}
+
+}  // namespace gdn

@@ -41,7 +41,8 @@
  * - Failure injection (testing a caller's failure path, as cortiq-engine
  *   0.8.76 pipeline.rs does with its test-only nll_test_fail_at): the environment variable GDN_FAULT
  *   is a comma-separated list of sites -- conv, prefill, decode, verify,
- *   commit, layer, kv_append, kv_read, kv_attention, accept, or all.  A call
+ *   commit, layer, kv_append, kv_read, kv_attention, accept, latent_append,
+ *   latent_read, latent_attention, expanded_attention, copy_pages, or all.  A call
  *   whose site is listed validates its arguments, then returns
  *   GDN_ERR_INJECTED without enqueuing anything, so every caller buffer is
  *   left as it was.  Two sites are device test hooks, under which a bounded
@@ -435,6 +436,133 @@ gdn_status gdn_kv_attention(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
                             const gdn_kv_batch* batch, const int32_t* kv_lens,
                             int32_t max_kv_len, const gdn_rows* q, void* out, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Latent attention: the full-attention layer whose cache holds one vector a
+ * token, a normalised latent of latent_dim channels that keys and values of all
+ * heads are projections of, and a position key of rope_dim channels that all
+ * heads share (the hybrid stacks of the per-channel decayed mixer interleave
+ * it).  Two forms of the same attention: absorbed (queries are taken into the
+ * latent space, the cached rows are keys and values: single tokens, drafts,
+ * short pieces behind a long context) and expanded (keys and values of each
+ * head are projected out of the latents first: prompts; a cached prefix comes
+ * back through gdn_latent_read).  Activations and cache are bf16.
+ *
+ * The cache.  Page p holds page_size consecutive tokens of one sequence:
+ *   rows [n_pages, page_size, latent_dim + rope_dim] bf16
+ * Sequences, lengths, block table entries out of range and what they record in
+ * the device error word are as above (kv_lens counts the call's own tokens; a
+ * gdn_kv_batch names the sequences).
+ */
+
+/* Geometry.  latent_dim 256 or 512; rope_dim 64; page_size 16, 32, 64 or 128;
+ * nope_dim and v_dim 64 or 128: a head's channels in the expanded form (its
+ * keys have nope_dim + rope_dim).  1 <= n_heads <= 1024.  scale > 0 multiplies
+ * q.k in both forms. */
+typedef struct gdn_latent_dims {
+    int32_t n_heads;
+    int32_t latent_dim;
+    int32_t rope_dim;
+    int32_t page_size;
+    int32_t rope_style; /* gdn_rope_style */
+    int32_t nope_dim;
+    int32_t v_dim;
+    float scale;
+    float norm_eps;     /* gdn_latent_append's norm, >= 0 */
+} gdn_latent_dims;
+
+typedef struct gdn_latent_cache {
+    void* rows;
+    int32_t n_pages;
+} gdn_latent_cache;
+
+/*
+ * gdn_latent_append -- norm, rotate and append.  Of c's rows [T, latent_dim +
+ * rope_dim] (the down projection's output; head_stride is not used) the latent
+ * part becomes
+ *   c (mean(c^2) + norm_eps)^-1/2 norm_w     where norm_w [latent_dim] fp32 is
+ *                                            given, c where it is NULL
+ * and the position part, like q_rope where given, is rotated as in
+ * gdn_kv_append where rope is given, and kept where it is NULL.  fp32, rounded
+ * once; what is stored is finite (NaN becomes 0, infinities the largest number).
+ *   rope [rope_len, rope_dim] fp32 (cosines | sines), positions [T] int32 or
+ *   NULL: as in gdn_kv_append.
+ *   q_rope [T, n_heads, rope_dim] rows or NULL, q_out the same (its memory is
+ *   written; may be q_rope itself): rows of a wider query buffer, its last
+ *   rope_dim channels, for one.  q_out's rows must not overlap one another.
+ *   rows_out [T, latent_dim + rope_dim] contiguous or NULL: the rows as stored,
+ *   packed, of every token of the call (those of unmapped pages too).
+ */
+gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache* cache,
+                             const gdn_kv_batch* batch, const int32_t* kv_lens, const gdn_rows* c,
+                             const float* norm_w, const gdn_rows* q_rope, const gdn_rows* q_out,
+                             const float* rope, int32_t rope_len, const int32_t* positions,
+                             void* rows_out, void* stream);
+
+/*
+ * gdn_latent_read -- cached rows back out of the pages: of sequence i the
+ * cu_seqlens[i+1] - cu_seqlens[i] tokens from position starts[i] on, packed,
+ * into out [R, latent_dim + rope_dim] bf16.  Tokens of unmapped pages read as 0.
+ */
+gdn_status gdn_latent_read(const gdn_latent_dims* dims, const gdn_latent_cache* cache,
+                           const gdn_kv_batch* batch, const int32_t* starts, void* out,
+                           void* stream);
+
+/*
+ * gdn_latent_attention -- the absorbed form over the cache:
+ *   o_th = sum_j p_j row_j[:latent_dim],  p = softmax_j(scale q_th . row_j)
+ * over the positions j up to the query's own.  A query that sees no key gives
+ * zeros.
+ *   q [T, n_heads, latent_dim + rope_dim] rows (rotated already), out [T,
+ *   n_heads, latent_dim] contiguous.
+ *   workspace: at least gdn_latent_attention_workspace_size() bytes, 256-byte
+ *   aligned.  Calls that may run at the same time need one each.
+ * Rows that some query of a sequence sees have to be finite, as appended ones
+ * are; whatever lies behind a sequence's end does not matter.  fp32
+ * accumulation and softmax (the hardware's exponentials, 2 ulp), weights bf16
+ * (8 bits); the sum takes the rounded weights.
+ */
+gdn_status gdn_latent_attention_workspace_size(const gdn_latent_dims* dims, int32_t n_seq,
+                                               const int32_t* cu_seqlens_host, size_t* bytes);
+gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_cache* cache,
+                                const gdn_kv_batch* batch, const int32_t* kv_lens, const gdn_rows* q,
+                                void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_expanded_attention -- the expanded form, over packed keys and values:
+ *   o_th = sum_j p_j v_jh,
+ *   p = softmax_j(scale (q_th[:nope_dim] . k_jh + q_th[nope_dim:] . k_rope_j))
+ * Sequence i has cu_q[i+1] - cu_q[i] queries, the last ones of its
+ * cu_kv[i+1] - cu_kv[i] positions; a query sees the positions up to its own
+ * (none, and gives zeros, where a sequence has fewer keys than queries and it is
+ * one of the first).
+ *   q [Tq, n_heads, nope_dim + rope_dim], k [Tk, n_heads, nope_dim] and v [Tk,
+ *   n_heads, v_dim] rows (one projection's output may hold k and v side by
+ *   side), k_rope [Tk, rope_dim] rows (head_stride is not used); token strides
+ *   > 0, a head stride of 0 shares one head.  out [Tq, n_heads, v_dim]
+ *   contiguous.
+ * Values that some query of a sequence sees have to be finite.  Accuracy as
+ * gdn_latent_attention.
+ */
+gdn_status gdn_expanded_attention(const gdn_latent_dims* dims, int32_t n_seq, const int32_t* cu_q,
+                                  const int32_t* cu_q_host, const int32_t* cu_kv,
+                                  const int32_t* cu_kv_host, const gdn_rows* q, const gdn_rows* k,
+                                  const gdn_rows* k_rope, const gdn_rows* v, void* out,
+                                  void* stream);
+
+/*
+ * gdn_copy_pages -- page src[i] to page dst[i], for i < n_pairs, in each of
+ * n_buffers arrays of n_pages pages (page_bytes[b] bytes each, a multiple of 4):
+ * a forked sequence's partly filled page, a compacted pool, in the caches of all
+ * layers at once; a cache's codes and scales are arrays of their own.  All four
+ * lists are on the host and are read before the call returns.  Refused: a page
+ * that is written twice, or both read and written.  Pages not named stay as
+ * they are.  bases 4-byte aligned (16 bytes, with page_bytes a multiple of 16,
+ * is the fast form).
+ */
+gdn_status gdn_copy_pages(int32_t n_buffers, void* const* bases, const size_t* page_bytes,
+                          int32_t n_pages, int32_t n_pairs, const int32_t* src, const int32_t* dst,
+                          void* stream);
 
 /* What target and draft rows hold: probabilities (fp32), or logits (fp32 or
  * bf16) of which the distribution is softmax(logits / temperature). */
