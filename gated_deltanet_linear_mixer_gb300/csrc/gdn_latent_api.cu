@@ -50,10 +50,12 @@ gdn_status check_dims(const gdn_latent_dims* d, const char* fn) {
     return GDN_OK;
 }
 
-gdn_status check_cache(const gdn_latent_cache* c, const char* fn) {
+gdn_status check_cache(const gdn_latent_cache* c, const gdn_latent_dims* d, const char* fn) {
     if (!c) return set_error(GDN_ERR_INVALID_ARG, fn, "cache is NULL");
     if (c->n_pages < 0) return set_error(GDN_ERR_INVALID_ARG, fn, "n_pages must be >= 0 (got %d)", c->n_pages);
     if (c->n_pages > 0 && !c->rows) return set_error(GDN_ERR_INVALID_ARG, fn, "the cache's pointer is NULL");
+    if (static_cast<long long>(c->n_pages) * d->page_size > 0x7fffffff)
+        return set_error(GDN_ERR_UNSUPPORTED, fn, "%d pages of %d rows are more than 2^31 - 1", c->n_pages, d->page_size);
     if (!aligned16(c->rows)) return set_error(GDN_ERR_INVALID_ARG, fn, "the cache's rows must be 16-byte aligned");
     return GDN_OK;
 }
@@ -126,7 +128,7 @@ gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache
     gdn_status st;
     gdn::LatentAppendArgs a{};
     if ((st = check_dims(dims, fn)) != GDN_OK) return st;
-    if ((st = check_cache(cache, fn)) != GDN_OK) return st;
+    if ((st = check_cache(cache, dims, fn)) != GDN_OK) return st;
     if ((st = check_batch(batch, kv_lens, &a.b, fn)) != GDN_OK) return st;
     gdn::clear_error();
     if (a.b.n_tokens == 0) return GDN_OK;
@@ -159,7 +161,7 @@ gdn_status gdn_latent_read(const gdn_latent_dims* dims, const gdn_latent_cache* 
     gdn_status st;
     gdn::LatentReadArgs a{};
     if ((st = check_dims(dims, fn)) != GDN_OK) return st;
-    if ((st = check_cache(cache, fn)) != GDN_OK) return st;
+    if ((st = check_cache(cache, dims, fn)) != GDN_OK) return st;
     if ((st = check_batch(batch, starts, &a.b, fn)) != GDN_OK) return st;
     gdn::clear_error();
     if (a.b.n_tokens == 0) return GDN_OK;
@@ -194,7 +196,7 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
     gdn_status st;
     gdn::LatentAttnArgs a{};
     if ((st = check_dims(dims, fn)) != GDN_OK) return st;
-    if ((st = check_cache(cache, fn)) != GDN_OK) return st;
+    if ((st = check_cache(cache, dims, fn)) != GDN_OK) return st;
     if ((st = check_batch(batch, kv_lens, &a.b, fn)) != GDN_OK) return st;
     gdn::clear_error();
     if (a.b.n_tokens == 0) return GDN_OK;

@@ -1,71 +1,864 @@
-// Attention over the latent cache, absorbed form: one row (token, head) a warp.
+// Attention over the latent cache, absorbed form, on the 5th-generation tensor
+// cores.
+//
+// The mathematics, in powers of two (y = scale log2 e q . row):
+//   w_rj = 2^(y_rj - m_r),   o_r = sum_j w_rj row_j[:C] / sum_j w_rj
+// over the rows r = (token, head) of a sequence, which all read the same keys: one
+// pass over the cached rows serves up to 64 of them.  The reference m_r lags
+// behind the row's maximum by at most 2^kLazy, so that the output is rescaled
+// only where the maximum rises by more than that.  Weights are rounded to bf16
+// (the values' type, as the tensor core asks), and the sum takes the rounded ones.
+//
+// A thread block walks tiles of 64 keys.  S = Q K^T has the rows as its M = 64 and
+// the keys as its N, so that a row's scores lie in four lanes of one warp.
+// O^T = V^T P^T has the latent channels as its M (C / 128 products of 128) and the
+// rows as its N: a tile of cached rows is the K-major operand of the first product
+// and the MN-major one of the second as it lies in shared memory, and the output
+// of 64 rows takes half of the tensor memory, where rows as M would take all of
+// it.  Per tile of 64 rows the products need 1152 + 768 cycles of shared memory
+// bandwidth, the tile's bytes (72 KB) 3100 cycles of an SM's share of DRAM.
+//
+// Work.  (sequence, group of row tiles, key tile) in that order is one axis, cut
+// into equal spans, one a thread block (G row tiles of one group: G thread blocks
+// side by side, whose second reads come from L2).  So ragged lengths fill every SM
+// alike, whatever they are; lengths are only known on the device, where every
+// thread block finds its span by a scan over the sequences.  What a span holds of a
+// sequence that it does not hold whole is a partial result (at most two a span);
+// a second launch joins them.
+//
+// Roles: 4 softmax warps (also: rescaling, epilogue), a warp for the rows' TMA
+// loads (with the page look-ups), one issuing S, one issuing O^T, one loading
+// queries.  Cached rows are in a ring of 16 KB slots (64 keys x 128 channels) and
+// one of 8 KB slots (position keys).  Every wait is bounded (2 s); a wait that gives
+// up records a code (50..58) in the cache operators' device error word.
+#include <algorithm>
+
 #include "gdn_internal.h"
 #include "gdn_kv.cuh"
 #include "gdn_latent.h"
+#include "gdn_tc.cuh"
+#include "gdn_tma_host.h"
 
 namespace gdn {
+
+using namespace tc;
 
 namespace {
 
 using bf16 = __nv_bfloat16;
 
+constexpr int kSms = 152;
+constexpr int kKeys = 64;
+constexpr int kThreads = 256;
+constexpr float kLazy = 8.0f;
+constexpr int kMinSpan = 1;      // key tiles of a span at least
+constexpr int kPieces = 16;      // pieces of a span that are laid out at a time
+constexpr int kMasks = 8;
+constexpr int kMaxSlots = 12;
+constexpr uint32_t kSmemMax = 232448, kSharedBytes = 3072;
+
+template <int C, int NR> struct LCfg {
+    static constexpr int W = C + kRopeDim, kBlocks = W / 64, kPairs = C / 128;
+    static constexpr uint32_t kSlot = 16384, kRope = 8192;
+    static constexpr uint32_t kQBlock = NR * 128;                                // 64 channels of the row tile
+    static constexpr uint32_t kQ = kBlocks * kQBlock + (64 - NR) * 128;          // M = 64 reads past the last block
+    static constexpr uint32_t kP = NR * 128;
+    static constexpr int kFit = (kSmemMax - kSharedBytes - kQ - kP - 2 * kRope) / kSlot;
+    static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+    static constexpr uint32_t kRopeAt = kSlots * kSlot, kQAt = kRopeAt + 2 * kRope, kPAt = kQAt + kQ, kSharedAt = kPAt + kP;
+    static constexpr uint32_t kSmem = kSharedAt + kSharedBytes;
+    static constexpr int kActive = NR / 16;                                      // softmax warps with rows
+    static constexpr uint32_t kOut = 128;                                        // tensor memory: S twice, then O^T
+    static_assert(kSlots >= 2 * kPairs, "two tiles fit");
+    static_assert(kOut + kPairs * NR <= 512, "the output fits");
+    static constexpr size_t kPart = static_cast<size_t>(NR) * (C + 2);           // floats of a partial result
+};
+
+struct Piece {
+    int q0;             // the sequence's first token
+    int seq;
+    int row0, n_rows;   // rows (token, head) of the sequence
+    int start, n_keys;  // position of the sequence's first query; keys that some row sees
+    int a, b;           // key tiles
+    int slot;           // partial result, or -1: the sequence's keys are all here
+};
+
+struct Join {  // a sequence's row tile whose pieces start in this span and end in another
+    int n_pieces;  // 0: none
+    int out_row, n_rows, slot;
+};
+
+struct Shared {
+    uint64_t pair_full[kMaxSlots], pair_empty[kMaxSlots], rope_full[2], rope_empty[2];
+    uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, m_full[kMasks], drained[2];
+    long long scan[2][16];
+    long long first_item, last_item;
+    int mask[kMasks];
+    float factor[64], stat[64];
+    Piece piece[kPieces];
+    int dead;
+    uint32_t tmem_slot;
+};
+static_assert(sizeof(Shared) <= kSharedBytes, "part of kSmem");
+
+__device__ __noinline__ void record(int* error, int code) { atomicMax(error, code); }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(count), "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+    const int n = take ? 16 : 0;  // 0: the 16 bytes become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// 16 lanes x 64 columns of 32-bit: v[4 i + 2 h + e] is row lane / 4 + 8 h, column
+// 8 i + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 lanes x 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"f"(v[0]),
+        "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// What a sequence needs: groups of G row tiles, and key tiles of each (at least one,
+// so that rows without keys are somebody's).
+struct Need {
+    int q0, qn, len, groups, tiles;
+};
+template <int NR>
+__device__ __forceinline__ Need need_of(const LatentAttnArgs& a, int seq, int G) {
+    Need n;
+    n.q0 = a.b.cu[seq];
+    n.qn = a.b.cu[seq + 1] - n.q0;
+    n.len = a.b.kv_lens[seq];
+    const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
+    const int len = static_cast<int>(min(static_cast<long long>(max(n.len, 0)), cap));
+    n.groups = static_cast<int>((static_cast<long long>(n.qn) * a.n_heads + NR * G - 1) / (NR * G));
+    n.tiles = max(1, (len - 1) / kKeys + 1);
+    return n;
+}
+
+template <int C, int NR>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensorMap map, const int G, float* parts, Join* joins) {
+    using L = LCfg<C, NR>;
+    constexpr int NP = L::kPairs, NS = L::kSlots;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem + L::kSharedAt);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g_own = static_cast<int>(blockIdx.x) % G, span = static_cast<int>(blockIdx.x) / G;
+    const int n_spans = static_cast<int>(gridDim.x) / G;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- this thread block's span of the (sequence, group, key tile) axis
+    const int each = (a.b.n_seq + kThreads - 1) / kThreads;
+    const int s0 = min(tid * each, a.b.n_seq), s1 = min(s0 + each, a.b.n_seq);
+    long long units = 0, items = 0;
+    for (int s = s0; s < s1; ++s) {
+        const Need n = need_of<NR>(a, s, G);
+        units += static_cast<long long>(n.groups) * n.tiles;
+        items += n.groups;
+    }
+    long long u_in = units, i_in = items;  // inclusive
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, u_in, off), i = __shfl_up_sync(0xffffffffu, i_in, off);
+        if (lane >= off) {
+            u_in += u;
+            i_in += i;
+        }
+    }
+    if (lane == 31) {
+        sh.scan[0][warp] = u_in;
+        sh.scan[1][warp] = i_in;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&sh.pair_full[i], 1);
+            mbar_init(&sh.pair_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.rope_full[i], 1);
+            mbar_init(&sh.rope_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_empty[i], L::kActive);
+        }
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.p_full, 4);
+        mbar_init(&sh.pv_done, 1);
+        for (int i = 0; i < kMasks; ++i) mbar_init(&sh.m_full[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sh.drained[i], 1);
+        sh.dead = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    long long u_base = u_in - units, i_base = i_in - items, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) {
+            u_base += sh.scan[0][w];
+            i_base += sh.scan[1][w];
+        }
+        total += sh.scan[0][w];
+    }
+    const long long per = max((total + n_spans - 1) / n_spans, static_cast<long long>(kMinSpan));
+    const long long u0 = span * per, u1 = min(u0 + per, total);
+    if (u0 >= u1 || (smem_u32(smem) & 1023u)) {
+        if (tid == 0) {
+            joins[blockIdx.x].n_pieces = 0;
+            if (u0 < u1) record(a.error, 58);
+        }
+        return;
+    }
+    if (warp == 5) tmem_alloc(&sh.tmem_slot, 512);
+    {
+        long long u = u_base, i = i_base;
+        for (int s = s0; s < s1; ++s) {
+            const Need n = need_of<NR>(a, s, G);
+            const long long all = static_cast<long long>(n.groups) * n.tiles;
+            if (u <= u0 && u0 < u + all) sh.first_item = i + (u0 - u) / n.tiles;
+            if (u < u1 && u1 <= u + all) {  // holds the span's last tile
+                const int k = static_cast<int>((u1 - 1 - u) / n.tiles);
+                const long long head = u + static_cast<long long>(k) * n.tiles;
+                const long long rest = head + n.tiles - u1;  // tiles in the spans that follow
+                sh.last_item = i + k;
+                const long long row0 = (static_cast<long long>(k) * G + g_own) * NR;
+                const long long rows = min(static_cast<long long>(NR), static_cast<long long>(n.qn) * a.n_heads - row0);
+                Join j{0, 0, 0, 0};
+                if (head >= u0 && rest > 0 && rows > 0) {
+                    j.n_pieces = 1 + static_cast<int>((rest + per - 1) / per);
+                    j.out_row = static_cast<int>(static_cast<long long>(n.q0) * a.n_heads + row0);
+                    j.n_rows = static_cast<int>(rows);
+                    j.slot = 2 * span + (head > u0 ? 1 : 0);
+                }
+                joins[blockIdx.x] = j;
+            }
+            u += all;
+            i += n.groups;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = sh.tmem_slot;
+    const int n_pieces = static_cast<int>(sh.last_item - sh.first_item) + 1;
+
+    // counts that the roles carry from round to round
+    uint32_t g = 0;   // key tiles
+    uint32_t qc = 0;  // pieces with tiles
+    bool ok = true;
+    uint32_t ropes = 0, pairs = 0;  // loads started
+
+    for (int p0 = 0; p0 < n_pieces; p0 += kPieces) {
+        {   // the pieces of this round
+            long long u = u_base, i = i_base;
+            const long long i0 = sh.first_item + p0, i1 = min(sh.last_item + 1, i0 + kPieces);
+            for (int s = s0; s < s1 && i < i1; ++s) {
+                const Need n = need_of<NR>(a, s, G);
+                if (i + n.groups > i0) {
+                    const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
+                    if (n.len > cap) record(a.error, kKvErrTable);
+                    const int len = static_cast<int>(min(static_cast<long long>(max(n.len, 0)), cap));
+                    for (long long k = max(i0 - i, 0ll); k < n.groups && i + k < i1; ++k) {
+                        const long long head = u + k * n.tiles, row0 = (k * G + g_own) * NR;
+                        const long long rows = min(static_cast<long long>(NR), static_cast<long long>(n.qn) * a.n_heads - row0);
+                        Piece p;
+                        p.q0 = n.q0;
+                        p.seq = s;
+                        p.row0 = static_cast<int>(row0);
+                        p.n_rows = rows > 0 ? static_cast<int>(rows) : 0;
+                        p.start = max(n.len, 0) - n.qn;  // queries before 0 see nothing
+                        p.n_keys = rows > 0 ? max(0, min(p.start + static_cast<int>((row0 + rows - 1) / a.n_heads) + 1, len)) : 0;
+                        p.a = static_cast<int>(max(u0 - head, 0ll));
+                        const int b = static_cast<int>(min(u1 - head, static_cast<long long>(n.tiles)));
+                        p.b = max(p.a, min(b, (p.n_keys + kKeys - 1) / kKeys));
+                        p.slot = p.a == 0 && b == n.tiles ? -1 : 2 * span + (head + p.a > u0 ? 1 : 0);
+                        sh.piece[i + k - i0] = p;
+                    }
+                }
+                u += static_cast<long long>(n.groups) * n.tiles;
+                i += n.groups;
+            }
+        }
+        __syncthreads();
+        const int n_round = min(kPieces, n_pieces - p0);
+        const bool dead = sh.dead != 0;
+
+        if (dead) {
+            // a wait gave up in an earlier round: nothing more is started
+        } else if (warp < 4) {
+            // ---- softmax
+            const bool active = warp < L::kActive;
+            const float scale2 = a.scale * kLog2e;
+            const uint32_t t_lane = (32u * warp) << 16;
+            for (int i = 0; i < n_round; ++i) {
+                const Piece p = sh.piece[i];
+                if (p.n_rows == 0) continue;
+                const int rA = 16 * warp + (lane >> 2), rB = rA + 8;
+                int limA = 0, limB = 0;  // keys that this lane's rows see
+                if (rA < p.n_rows) limA = min(p.start + (p.row0 + rA) / a.n_heads + 1, p.n_keys);
+                if (rB < p.n_rows) limB = min(p.start + (p.row0 + rB) / a.n_heads + 1, p.n_keys);
+                const int lim = min(limA, limB);
+                float mA = -INFINITY, mB = -INFINITY, lA = 0.0f, lB = 0.0f;
+                for (int t = p.a; t < p.b; ++t, ++g) {
+                    const int key0 = t * kKeys, valid = p.n_keys - key0;  // keys of the tile that exist
+                    const uint32_t sb = g & 1;
+                    float s[32];
+                    bool lift = false;
+                    float topA = -INFINITY, topB = -INFINITY;
+                    if ((active || valid < kKeys) && ok &&
+                        !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_full[sb], (g >> 1) & 1) &&
+                                                           mbar_wait_brief(&sh.m_full[g % kMasks], (g / kMasks) & 1))) &&
+                        lane == 0)
+                        record(a.error, 50);
+                    if (active) {
+                        tc_fence_after_sync();
+                        tmem_ld_rows16(tmem + t_lane + 64 * sb, s);
+                        const int mask = sh.mask[g % kMasks];
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j] *= scale2;
+                        if (key0 + kKeys > lim || mask != 15) {
+                            const int c = key0 + 2 * (lane & 3);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const int key = c + 8 * (j >> 2) + (j & 1);
+                                if (key >= (j & 2 ? limB : limA) || !(mask >> (j >> 3) & 1)) s[j] = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            topA = fmaxf(topA, fmaxf(s[j], s[j + 1]));
+                            topB = fmaxf(topB, fmaxf(s[j + 2], s[j + 3]));
+                        }
+#pragma unroll
+                        for (int off = 1; off < 4; off <<= 1) {
+                            topA = fmaxf(topA, __shfl_xor_sync(0xffffffffu, topA, off));
+                            topB = fmaxf(topB, __shfl_xor_sync(0xffffffffu, topB, off));
+                        }
+                        lift = topA > mA + kLazy || topB > mB + kLazy;
+                    }
+                    lift = group_any(1, 128, lift);
+                    if (lift) {
+                        if (active) {
+                            const float nA = fmaxf(mA, topA), nB = fmaxf(mB, topB);
+                            const float fA = mA == -INFINITY ? 0.0f : exp2_ftz(mA - nA), fB = mB == -INFINITY ? 0.0f : exp2_ftz(mB - nB);
+                            lA *= fA;
+                            lB *= fB;
+                            mA = nA;
+                            mB = nB;
+                            if ((lane & 3) == 0) {
+                                sh.factor[rA] = fA;
+                                sh.factor[rB] = fB;
+                            }
+                        }
+                        if (t > p.a) {  // the output so far
+                            group_sync(1, 128);
+                            if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pv_done, (g - 1) & 1))) && lane == 0)
+                                record(a.error, 51);
+                            tc_fence_after_sync();
+#pragma unroll 1
+                            for (int c = 0; c < NP * NR; c += 16) {
+                                float v[16];
+                                tmem_ld16(tmem + t_lane + L::kOut + c, v);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) v[e] *= sh.factor[c % NR + e];
+                                tmem_st16(tmem + t_lane + L::kOut + c, v);
+                            }
+                            tmem_wait_st();
+                            tc_fence_before_sync();
+                        }
+                    }
+                    if (active) {
+                        const float refA = mA == -INFINITY ? 0.0f : mA, refB = mB == -INFINITY ? 0.0f : mB;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float ref = j & 2 ? refB : refA;
+                            w[j / 2] = pack_bf16x2(exp2_ftz(s[j] - ref), exp2_ftz(s[j + 1] - ref));
+                            const float sum = __uint_as_float(w[j / 2] << 16) + __uint_as_float(w[j / 2] & 0xFFFF0000u);
+                            if (j & 2) lB += sum;
+                            else lA += sum;
+                        }
+                        // the weights before these were used
+                        if (g > 0 && ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pv_done, (g - 1) & 1))) && lane == 0)
+                            record(a.error, 52);
+                        uint8_t* tile = smem + L::kPAt;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            *reinterpret_cast<uint32_t*>(tile + sw128_offset(rA, c) + 4 * (lane & 3)) = w[2 * c];
+                            *reinterpret_cast<uint32_t*>(tile + sw128_offset(rB, c) + 4 * (lane & 3)) = w[2 * c + 1];
+                        }
+                    }
+                    if (valid < kKeys) {  // rows behind the last key may be anything: weights of 0 do not undo a NaN
+                        for (int q = 0; q < NP; ++q) {
+                            const uint32_t n = g * NP + q, slot = n % NS;
+                            if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_full[slot], (n / NS) & 1))) && lane == 0)
+                                record(a.error, 53);
+                            uint4* row = reinterpret_cast<uint4*>(smem + slot * L::kSlot);
+                            for (int x = tid; x < 2 * (kKeys - valid) * 8; x += 128) {
+                                const int half = x & 1, r = valid + x / 16, c = x / 2 % 8;
+                                row[half * 512 + r * 8 + c] = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_full);
+                }
+                // ---- epilogue
+                const bool any = p.b > p.a;
+                if (any && ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pv_done, (g - 1) & 1))) && lane == 0)
+                    record(a.error, 54);
+                if (active) {
+#pragma unroll
+                    for (int off = 1; off < 4; off <<= 1) {
+                        lA += __shfl_xor_sync(0xffffffffu, lA, off);
+                        lB += __shfl_xor_sync(0xffffffffu, lB, off);
+                    }
+                    if ((lane & 3) == 0) {
+                        if (p.slot < 0) {  // a sum that is no number stays one
+                            sh.stat[rA] = lA == 0.0f ? 0.0f : 1.0f / lA;
+                            sh.stat[rB] = lB == 0.0f ? 0.0f : 1.0f / lB;
+                        } else {
+                            float* st = parts + (static_cast<size_t>(p.slot) * G + g_own) * L::kPart + NR * C;
+                            st[rA] = mA;
+                            st[rB] = mB;
+                            st[NR + rA] = lA;
+                            st[NR + rB] = lB;
+                        }
+                    }
+                }
+                group_sync(1, 128);
+                tc_fence_after_sync();
+                if (p.slot < 0) {
+                    bf16* out = static_cast<bf16*>(a.out) + (static_cast<size_t>(p.q0) * a.n_heads + p.row0) * C + 32 * warp + lane;
+#pragma unroll 1
+                    for (int c = 0; c < NP * NR; c += 16) {
+                        float v[16];
+                        if (any) tmem_ld16(tmem + t_lane + L::kOut + c, v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int r = c % NR + e;
+                            if (r < p.n_rows) out[static_cast<size_t>(r) * C + c / NR * 128] = __float2bfloat16_rn(any ? v[e] * sh.stat[r] : 0.0f);
+                        }
+                    }
+                } else if (any) {
+                    float* out = parts + (static_cast<size_t>(p.slot) * G + g_own) * L::kPart + 32 * warp + lane;
+#pragma unroll 1
+                    for (int c = 0; c < NP * NR; c += 16) {
+                        float v[16];
+                        tmem_ld16(tmem + t_lane + L::kOut + c, v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int r = c % NR + e;
+                            if (r < p.n_rows) out[static_cast<size_t>(r) * C + c / NR * 128] = v[e];
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                group_sync(1, 128);  // stat, and the output in tensor memory, may be written again
+            }
+        } else if (warp == 4) {
+            // ---- cached rows: page look-ups by the warp, loads by one lane
+            const int R = min(a.page_size, kKeys), per_tile = kKeys / R;
+            const bool leader = elect_one();
+            const int nowhere = a.c.n_pages * a.page_size;  // past the last row: the load gives zeros
+            for (int i = 0; ok && i < n_round; ++i) {
+                const Piece p = sh.piece[i];
+                int row = 0;
+                const int first = p.a * per_tile, n = (p.b - p.a) * per_tile;
+                auto look_up = [&](int x) {  // where chunk x of the piece lies; negative: not mapped
+                    const int key = (first + x) * R;
+                    if (x >= n || key >= p.n_keys) return nowhere;
+                    const int page = a.b.table[static_cast<size_t>(p.seq) * a.b.pages_per_seq + key / a.page_size];
+                    return page >= 0 && page < a.c.n_pages ? page * a.page_size + key % a.page_size : -1;
+                };
+                int ahead = n > 0 ? look_up(lane) : 0;
+                for (int t = p.a; ok && t < p.b; ++t, ++g) {
+                    const int x = (t - p.a) * per_tile;
+                    if (x % 32 == 0) {
+                        row = ahead;
+                        ahead = look_up(x + 32 + lane);
+                    }
+                    int at[4];
+                    int mask = 15;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c >= per_tile) break;
+                        at[c] = __shfl_sync(0xffffffffu, row, (x + c) & 31);
+                        if (at[c] < 0) {
+                            if (leader) record(a.error, kKvErrTable);
+                            mask &= ~(((1 << (R / 16)) - 1) << (c * (R / 16)));
+                            at[c] = nowhere;
+                        }
+                    }
+                    if (leader) {
+                        sh.mask[g % kMasks] = mask;
+                        mbar_arrive(&sh.m_full[g % kMasks]);
+                    }
+                    const uint32_t rb = g & 1;
+                    if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.rope_empty[rb], ((g >> 1) - 1) & 1));
+                    if (!ok) break;
+                    ++ropes;
+                    if (leader) {
+                        mbar_arrive_expect_tx(&sh.rope_full[rb], L::kRope);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (c < per_tile)
+                                tma_load_2d(smem + L::kRopeAt + rb * L::kRope + c * R * 128, &map, &sh.rope_full[rb], C, at[c]);
+                    }
+                    for (int q = 0; q < NP; ++q) {
+                        const uint32_t fill = g * NP + q, slot = fill % NS;
+                        if (fill >= NS) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_empty[slot], (fill / NS - 1) & 1));
+                        if (!ok) break;
+                        ++pairs;
+                        if (leader) {
+                            mbar_arrive_expect_tx(&sh.pair_full[slot], L::kSlot);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (c < per_tile) {
+                                    uint8_t* dst = smem + slot * L::kSlot + c * R * 128;
+                                    tma_load_2d(dst, &map, &sh.pair_full[slot], 128 * q, at[c]);
+                                    tma_load_2d(dst + 8192, &map, &sh.pair_full[slot], 128 * q + 64, at[c]);
+                                }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (!ok && lane == 0) record(a.error, 55);
+            __syncwarp();
+            if (!ok) sh.dead = 1;
+        } else if (warp == 5) {
+            // ---- S = Q K^T
+            const bool leader = elect_one();
+            constexpr uint32_t id = idesc_bf16_f32(64, kKeys);
+            const uint64_t dq = desc_kmajor_sw128(smem_u32(smem + L::kQAt)), dr = desc_kmajor_sw128(smem_u32(smem + L::kRopeAt)),
+                           dk = desc_kmajor_sw128(smem_u32(smem));
+            for (int i = 0; ok && i < n_round; ++i) {
+                const int a0 = sh.piece[i].a, b0 = sh.piece[i].b;
+                if (sh.piece[i].n_rows == 0 || a0 >= b0) continue;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_full, qc & 1)))) break;
+                ++qc;
+                for (int t = a0; ok && t < b0; ++t, ++g) {
+                    const uint32_t sb = g & 1;
+                    if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_empty[sb], ((g >> 1) - 1) & 1));
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_brief(&sh.rope_full[sb], (g >> 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(tmem + 64 * sb, dq + ((C / 64) * L::kQBlock >> 4) + 2 * k, dr + (sb * L::kRope >> 4) + 2 * k, id,
+                                     k > 0 ? 1u : 0u);
+                        mma_commit(&sh.rope_empty[sb]);
+                    }
+                    for (int q = 0; q < NP; ++q) {
+                        const uint32_t fill = g * NP + q, slot = fill % NS;
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_full[slot], (fill / NS) & 1)))) break;
+                        tc_fence_after_sync();
+                        if (leader) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_bf16(tmem + 64 * sb, dq + ((2 * q + h) * L::kQBlock >> 4) + 2 * k,
+                                             dk + ((slot * L::kSlot + h * 8192) >> 4) + 2 * k, id, 1u);
+                        }
+                        __syncwarp();
+                    }
+                    if (leader) mma_commit(&sh.s_full[sb]);
+                    __syncwarp();
+                }
+                if (leader) mma_commit(&sh.q_empty);
+                __syncwarp();
+            }
+            if (!ok && lane == 0) record(a.error, 56);
+            if (!ok) sh.dead = 1;
+        } else if (warp == 6) {
+            // ---- O^T += V^T P^T
+            const bool leader = elect_one();
+            constexpr uint32_t id = idesc_bf16_f32(128, NR, true, false);
+            const uint64_t dv = desc_mnmajor_sw128(smem_u32(smem), 8192), dp = desc_kmajor_sw128(smem_u32(smem + L::kPAt));
+            for (int i = 0; ok && i < n_round; ++i) {
+                const int a0 = sh.piece[i].a, b0 = sh.piece[i].b;
+                if (sh.piece[i].n_rows == 0) continue;
+                for (int t = a0; ok && t < b0; ++t, ++g) {
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.p_full, g & 1)))) break;
+                    for (int q = 0; q < NP; ++q) {
+                        const uint32_t fill = g * NP + q, slot = fill % NS;
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_full[slot], (fill / NS) & 1)))) break;
+                        tc_fence_after_sync();
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16(tmem + L::kOut + q * NR, dv + ((slot * L::kSlot + k * 2048) >> 4), dp + 2 * k, id,
+                                         (t > a0 || k > 0) ? 1u : 0u);
+                            mma_commit(&sh.pair_empty[slot]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (leader) mma_commit(&sh.pv_done);
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) record(a.error, 56);
+            if (!ok) sh.dead = 1;
+        } else {
+            // ---- queries
+            for (int i = 0; ok && i < n_round; ++i) {
+                const Piece p = sh.piece[i];
+                if (p.n_rows == 0 || p.a >= p.b) continue;
+                if (qc > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty, (qc - 1) & 1)))) break;
+                ++qc;
+                constexpr int V = L::W / 8;
+                const uint32_t base = smem_u32(smem + L::kQAt);
+                const bf16* q = static_cast<const bf16*>(a.q.data);
+                for (int x = lane; x < NR * V; x += 32) {
+                    const int r = x / V, c = x % V, row = p.row0 + r;
+                    const bool take = r < p.n_rows;
+                    const bf16* src = q + (p.q0 + row / a.n_heads) * a.q.token_stride + row % a.n_heads * a.q.head_stride + 8 * c;
+                    cp_async16(base + (c / 8) * L::kQBlock + sw128_offset(r, c % 8), take ? src : q, take);
+                }
+                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_full);
+            }
+            if (!ok && lane == 0) record(a.error, 57);
+            if (!ok) sh.dead = 1;
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    // nothing of this thread block is in flight when its memory is given back
+    if (warp == 4) {
+        for (uint32_t s = 0; s < 2; ++s)
+            if (ropes > s) mbar_wait_brief(&sh.rope_full[s], ((ropes - 1 - s) / 2) & 1);
+        for (uint32_t s = 0; s < NS; ++s)
+            if (pairs > s) mbar_wait_brief(&sh.pair_full[s], ((pairs - 1 - s) / NS) & 1);
+    } else if (warp == 5 || warp == 6) {
+        if (elect_one()) mma_commit(&sh.drained[warp - 5]);
+        if (!mbar_wait_brief(&sh.drained[warp - 5], 0) && lane == 0) record(a.error, 57);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 5) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of row tiles that were split: tasks of one row and 128 channels,
+// by a warp each where pieces are few, else by a thread block.
+constexpr int kJoinThreads = 256;
+template <int C, int NR>
+__global__ void __launch_bounds__(kJoinThreads)
+latent_join_kernel(const LatentAttnArgs a, const float* parts, const Join* joins, const int n_joins, const int G) {
+    using L = LCfg<C, NR>;
+    constexpr int kWarps = kJoinThreads / 32, kCols = C / 128;
+    __shared__ Join list[kSms];
+    __shared__ int begin[kSms + 1], most;
+    __shared__ float4 sum[kWarps][32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) {  // tasks of each
+        int at = 0, top = 0;
+        for (int j0 = 0; j0 < n_joins; j0 += 32) {
+            Join j{0, 0, 0, 0};
+            if (j0 + lane < n_joins) j = joins[j0 + lane];
+            const int n = j.n_pieces > 0 ? j.n_rows : 0;
+            int in = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, in, off);
+                if (lane >= off) in += x;
+            }
+            if (j0 + lane < n_joins) {
+                list[j0 + lane] = j;
+                begin[j0 + lane] = at + in - n;
+            }
+            at += __shfl_sync(0xffffffffu, in, 31);
+            top = max(top, j.n_pieces);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+        if (lane == 0) {
+            begin[n_joins] = at;
+            most = top;
+        }
+    }
+    __syncthreads();
+    const int tasks = begin[n_joins] * kCols;
+    const bool alone = most <= 4;  // a warp a task
+    const int step = alone ? gridDim.x * kWarps : gridDim.x, first = alone ? blockIdx.x * kWarps + warp : blockIdx.x;
+    for (int task = first; task < tasks; task += step) {
+        const int r_all = task / kCols, col = task % kCols * 128 + 4 * lane;
+        int lo = 0, hi = n_joins - 1;  // the last join that begins at or before the row
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (begin[mid] <= r_all) lo = mid;
+            else hi = mid - 1;
+        }
+        const Join j = list[lo];
+        const int row = r_all - begin[lo], g = lo % G;
+        auto part = [&](int p) {  // the first piece's slot, then the following spans' first ones
+            const int slot = p == 0 ? j.slot : 2 * (j.slot / 2 + p);
+            return parts + (static_cast<size_t>(slot) * G + g) * L::kPart;
+        };
+        float top = -INFINITY;
+        for (int p = lane; p < j.n_pieces; p += 32) top = fmaxf(top, part(p)[NR * C + row]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float total = 0.0f;
+        for (int p = lane; p < j.n_pieces; p += 32) {
+            const float l = part(p)[NR * C + NR + row];
+            if (l != 0.0f) total += l * exp2_ftz(part(p)[NR * C + row] - ref);
+        }
+        total = group_sum<32>(total);
+        float4 x = make_float4(0, 0, 0, 0);
+        const int from = alone ? 0 : warp, by = alone ? 1 : kWarps;
+#pragma unroll 4
+        for (int p = from; p < j.n_pieces; p += by) {
+            const float l = part(p)[NR * C + NR + row], w = exp2_ftz(part(p)[NR * C + row] - ref);
+            if (l == 0.0f) continue;  // saw no key: its outputs were not written
+            const float4 v = *reinterpret_cast<const float4*>(part(p) + static_cast<size_t>(row) * C + col);
+            x.x = fmaf(v.x, w, x.x);
+            x.y = fmaf(v.y, w, x.y);
+            x.z = fmaf(v.z, w, x.z);
+            x.w = fmaf(v.w, w, x.w);
+        }
+        if (!alone) {
+            sum[warp][lane] = x;
+            __syncthreads();
+            if (warp == 0)
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 v = sum[w][lane];
+                    x.x += v.x;
+                    x.y += v.y;
+                    x.z += v.z;
+                    x.w += v.w;
+                }
+        }
+        if (alone || warp == 0) {
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (static_cast<size_t>(j.out_row) + row) * C + col) =
+                make_uint2(pack_bf16_pair(x.x * inv, x.y * inv), pack_bf16_pair(x.z * inv, x.w * inv));
+        }
+        if (!alone) __syncthreads();
+    }
+}
+
+int rows_of_tile(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+template <int C, int NR>
+cudaError_t launch_t(const LatentAttnArgs& a, int G, cudaStream_t st) {
+    using L = LCfg<C, NR>;
+    static std::atomic<unsigned long long> ready{0};
+    cudaError_t e = allow_smem(latent_attention_kernel<C, NR>, L::kSmem, ready);
+    if (e != cudaSuccess) return e;
+    CUtensorMap map{};
+    if (a.c.n_pages > 0 && !make_tma_map_bf16_2d(&map, a.c.rows, static_cast<uint64_t>(a.c.n_pages) * a.page_size, L::W, L::W,
+                                                 std::min(a.page_size, kKeys), 64))
+        return cudaErrorInvalidValue;
+    if (static_cast<long long>(a.b.n_tokens) * a.n_heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int n = kSms / G * G;
+    Join* joins = static_cast<Join*>(a.workspace);
+    float* parts = reinterpret_cast<float*>(joins + kSms);
+    e = timed_launch("latent_attention", st, [&] {
+        latent_attention_kernel<C, NR><<<n, kThreads, L::kSmem, st>>>(a, map, G, parts, joins);
+        return cudaGetLastError();
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(4 * kSms);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return timed_launch("latent_join", st, [&] {
+        return cudaLaunchKernelEx(&cfg, latent_join_kernel<C, NR>, a, static_cast<const float*>(parts), static_cast<const Join*>(joins), n, G);
+    });
+}
+
 template <int C>
-__global__ void __launch_bounds__(128) latent_attention_kernel(const LatentAttnArgs a) {
-    constexpr int W = C + kRopeDim, K = W / 32;
-    const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= static_cast<long long>(a.b.n_tokens) * a.n_heads) return;
-    const int tok = static_cast<int>(row / a.n_heads), h = static_cast<int>(row % a.n_heads);
-    const int seq = seq_of_token(a.b.cu, a.b.n_seq, tok);
-    const long long cap = static_cast<long long>(a.b.pages_per_seq) * a.page_size;
-    long long end = static_cast<long long>(a.b.kv_lens[seq]) - (a.b.cu[seq + 1] - tok) + 1;
-    if (a.b.kv_lens[seq] > cap) {
-        if (lane == 0) atomicMax(a.error, kKvErrTable);
-        end = min(end, cap);
+cudaError_t launch_c(const LatentAttnArgs& a, cudaStream_t st) {
+    const long long rows = static_cast<long long>(a.b.max_q) * a.n_heads;
+    const int G = rows > 64 ? 2 : 1;
+    switch (rows_of_tile(rows)) {
+        case 16: return launch_t<C, 16>(a, G, st);
+        case 32: return launch_t<C, 32>(a, G, st);
+        default: return launch_t<C, 64>(a, G, st);
     }
-    const bf16* q = static_cast<const bf16*>(a.q.data) + tok * a.q.token_stride + h * a.q.head_stride;
-    float x[K], o[C / 32];
-#pragma unroll
-    for (int i = 0; i < K; ++i) x[i] = to_f32(q[lane + 32 * i]);
-#pragma unroll
-    for (int i = 0; i < C / 32; ++i) o[i] = 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    for (long long j = 0; j < end; ++j) {
-        const int page = a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + j / a.page_size];
-        if (page < 0 || page >= a.c.n_pages) {
-            if (lane == 0) atomicMax(a.error, kKvErrTable);
-            continue;
-        }
-        const bf16* r = static_cast<const bf16*>(a.c.rows) + (static_cast<size_t>(page) * a.page_size + j % a.page_size) * W;
-        float v[K], s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            v[i] = to_f32(r[lane + 32 * i]);
-            s = fmaf(x[i], v[i], s);
-        }
-        s = group_sum<32>(s) * a.scale;
-        const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.0f : expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < C / 32; ++i) o[i] = o[i] * f + p * v[i];
-    }
-    const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-    bf16* out = static_cast<bf16*>(a.out) + row * C;
-#pragma unroll
-    for (int i = 0; i < C / 32; ++i) out[lane + 32 * i] = from_f32<bf16>(o[i] * inv);
 }
 
 }  // namespace
 
-size_t latent_attention_workspace(int, int, int, int) { return 0; }
+size_t latent_attention_workspace(int n_heads, int latent_dim, int n_seq, int max_q) {
+    if (n_seq == 0 || max_q == 0) return 0;
+    const size_t nr = rows_of_tile(static_cast<long long>(max_q) * n_heads);
+    return kSms * sizeof(Join) + 2 * kSms * nr * (latent_dim + 2) * sizeof(float);
+}
 
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, int latent_dim, cudaStream_t st) {
-    const long long blocks = (static_cast<long long>(a.b.n_tokens) * a.n_heads + 3) / 4;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (latent_dim == 512) latent_attention_kernel<512><<<static_cast<unsigned>(blocks), 128, 0, st>>>(a);
-    else latent_attention_kernel<256><<<static_cast<unsigned>(blocks), 128, 0, st>>>(a);
-    return cudaGetLastError();
+    return latent_dim == 512 ? launch_c<512>(a, st) : launch_c<256>(a, st);
 }
 
 }  // namespace gdn
