@@ -175,6 +175,13 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 struct Need {
     int q0, qn, len, groups, tiles;
 };
+template <int N> constexpr int kLog2 = 1 + kLog2<N / 2>;
+template <> constexpr int kLog2<1> = 0;
+// x / y, in 32 bits where they fit: a 64-bit division takes several hundred cycles.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
 template <int NR>
 __device__ __forceinline__ Need need_of(const LatentAttnArgs& a, int seq, int G) {
     Need n;
@@ -183,14 +190,15 @@ __device__ __forceinline__ Need need_of(const LatentAttnArgs& a, int seq, int G)
     n.len = a.b.kv_lens[seq];
     const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
     const int len = static_cast<int>(min(static_cast<long long>(max(n.len, 0)), cap));
-    n.groups = static_cast<int>((static_cast<long long>(n.qn) * a.n_heads + NR * G - 1) / (NR * G));
+    n.groups = (n.qn * a.n_heads + NR * G - 1) >> (G == 2 ? kLog2<2 * NR> : kLog2<NR>);
     n.tiles = max(1, (len - 1) / kKeys + 1);
     return n;
 }
 
 template <int C, int NR>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensorMap map, const int G, float* parts, Join* joins) {
+latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
+                        const int dense_q, const int G, float* parts, Join* joins) {
     using L = LCfg<C, NR>;
     constexpr int NP = L::kPairs, NS = L::kSlots;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -204,8 +212,10 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
     const int each = (a.b.n_seq + kThreads - 1) / kThreads;
     const int s0 = min(tid * each, a.b.n_seq), s1 = min(s0 + each, a.b.n_seq);
     long long units = 0, items = 0;
+    Need first{};  // of s0: all that this thread has where there are no more sequences than threads
     for (int s = s0; s < s1; ++s) {
         const Need n = need_of<NR>(a, s, G);
+        if (s == s0) first = n;
         units += static_cast<long long>(n.groups) * n.tiles;
         items += n.groups;
     }
@@ -251,7 +261,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
         }
         total += sh.scan[0][w];
     }
-    const long long per = max((total + n_spans - 1) / n_spans, static_cast<long long>(kMinSpan));
+    const long long per = max(quotient(total + n_spans - 1, n_spans), static_cast<long long>(kMinSpan));
     const long long u0 = span * per, u1 = min(u0 + per, total);
     if (u0 >= u1 || (smem_u32(smem) & 1023u)) {
         if (tid == 0) {
@@ -264,11 +274,11 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
     {
         long long u = u_base, i = i_base;
         for (int s = s0; s < s1; ++s) {
-            const Need n = need_of<NR>(a, s, G);
+            const Need n = s == s0 ? first : need_of<NR>(a, s, G);
             const long long all = static_cast<long long>(n.groups) * n.tiles;
-            if (u <= u0 && u0 < u + all) sh.first_item = i + (u0 - u) / n.tiles;
+            if (u <= u0 && u0 < u + all) sh.first_item = i + quotient(u0 - u, n.tiles);
             if (u < u1 && u1 <= u + all) {  // holds the span's last tile
-                const int k = static_cast<int>((u1 - 1 - u) / n.tiles);
+                const int k = static_cast<int>(quotient(u1 - 1 - u, n.tiles));
                 const long long head = u + static_cast<long long>(k) * n.tiles;
                 const long long rest = head + n.tiles - u1;  // tiles in the spans that follow
                 sh.last_item = i + k;
@@ -276,7 +286,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                 const long long rows = min(static_cast<long long>(NR), static_cast<long long>(n.qn) * a.n_heads - row0);
                 Join j{0, 0, 0, 0};
                 if (head >= u0 && rest > 0 && rows > 0) {
-                    j.n_pieces = 1 + static_cast<int>((rest + per - 1) / per);
+                    j.n_pieces = 1 + static_cast<int>(quotient(rest + per - 1, per));
                     j.out_row = static_cast<int>(static_cast<long long>(n.q0) * a.n_heads + row0);
                     j.n_rows = static_cast<int>(rows);
                     j.slot = 2 * span + (head > u0 ? 1 : 0);
@@ -304,7 +314,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
             long long u = u_base, i = i_base;
             const long long i0 = sh.first_item + p0, i1 = min(sh.last_item + 1, i0 + kPieces);
             for (int s = s0; s < s1 && i < i1; ++s) {
-                const Need n = need_of<NR>(a, s, G);
+                const Need n = s == s0 ? first : need_of<NR>(a, s, G);
                 if (i + n.groups > i0) {
                     const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
                     if (n.len > cap) record(a.error, kKvErrTable);
@@ -533,18 +543,17 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                         row = ahead;
                         ahead = look_up(x + 32 + lane);
                     }
-                    int at[4];
+                    // where chunk lane (of the tile's per_tile) lies, and chunk lane / 2
+                    int mine = __shfl_sync(0xffffffffu, row, (x + lane % per_tile) & 31);
+                    const uint32_t gone = __ballot_sync(0xffffffffu, mine < 0);  // the tile's lowest bits, over and over
                     int mask = 15;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c >= per_tile) break;
-                        at[c] = __shfl_sync(0xffffffffu, row, (x + c) & 31);
-                        if (at[c] < 0) {
-                            if (leader) record(a.error, kKvErrTable);
-                            mask &= ~(((1 << (R / 16)) - 1) << (c * (R / 16)));
-                            at[c] = nowhere;
-                        }
+                    if (gone) {
+                        if (leader) record(a.error, kKvErrTable);
+                        for (int c = 0; c < per_tile; ++c)
+                            if (gone >> c & 1) mask &= ~(((1 << (R / 16)) - 1) << (c * (R / 16)));
+                        if (mine < 0) mine = nowhere;
                     }
+                    const int mine2 = __shfl_sync(0xffffffffu, mine, lane >> 1);
                     if (leader) {
                         sh.mask[g % kMasks] = mask;
                         mbar_arrive(&sh.m_full[g % kMasks]);
@@ -553,27 +562,20 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                     if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.rope_empty[rb], ((g >> 1) - 1) & 1));
                     if (!ok) break;
                     ++ropes;
-                    if (leader) {
-                        mbar_arrive_expect_tx(&sh.rope_full[rb], L::kRope);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (c < per_tile)
-                                tma_load_2d(smem + L::kRopeAt + rb * L::kRope + c * R * 128, &map, &sh.rope_full[rb], C, at[c]);
-                    }
+                    if (leader) mbar_arrive_expect_tx(&sh.rope_full[rb], L::kRope);
+                    __syncwarp();
+                    if (lane < per_tile)
+                        tma_load_2d(smem + L::kRopeAt + rb * L::kRope + lane * R * 128, &map, &sh.rope_full[rb], C, mine);
                     for (int q = 0; q < NP; ++q) {
                         const uint32_t fill = g * NP + q, slot = fill % NS;
                         if (fill >= NS) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_empty[slot], (fill / NS - 1) & 1));
                         if (!ok) break;
                         ++pairs;
-                        if (leader) {
-                            mbar_arrive_expect_tx(&sh.pair_full[slot], L::kSlot);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                if (c < per_tile) {
-                                    uint8_t* dst = smem + slot * L::kSlot + c * R * 128;
-                                    tma_load_2d(dst, &map, &sh.pair_full[slot], 128 * q, at[c]);
-                                    tma_load_2d(dst + 8192, &map, &sh.pair_full[slot], 128 * q + 64, at[c]);
-                                }
+                        if (leader) mbar_arrive_expect_tx(&sh.pair_full[slot], L::kSlot);
+                        __syncwarp();
+                        if (lane < 2 * per_tile) {  // a lane a box: chunk lane / 2, half lane % 2
+                            uint8_t* dst = smem + slot * L::kSlot + (lane & 1) * 8192 + (lane >> 1) * R * 128;
+                            tma_load_2d(dst, &map, &sh.pair_full[slot], 128 * q + 64 * (lane & 1), mine2);
                         }
                         __syncwarp();
                     }
@@ -665,14 +667,27 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                 if (p.n_rows == 0 || p.a >= p.b) continue;
                 if (qc > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty, (qc - 1) & 1)))) break;
                 ++qc;
+                uint8_t* tile = smem + L::kQAt;
+                if (dense_q) {  // evenly spaced rows: those behind the sequence's last are another's, or zeros, and not used
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sh.q_full, L::kBlocks * L::kQBlock);
+                        for (int b = 0; b < L::kBlocks; ++b)
+                            tma_load_2d(tile + b * L::kQBlock, &map_q, &sh.q_full, 64 * b, p.q0 * a.n_heads + p.row0);
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 constexpr int V = L::W / 8;
-                const uint32_t base = smem_u32(smem + L::kQAt);
                 const bf16* q = static_cast<const bf16*>(a.q.data);
-                for (int x = lane; x < NR * V; x += 32) {
-                    const int r = x / V, c = x % V, row = p.row0 + r;
-                    const bool take = r < p.n_rows;
-                    const bf16* src = q + (p.q0 + row / a.n_heads) * a.q.token_stride + row % a.n_heads * a.q.head_stride + 8 * c;
-                    cp_async16(base + (c / 8) * L::kQBlock + sw128_offset(r, c % 8), take ? src : q, take);
+                for (int r0 = 0; r0 < NR; r0 += 32) {
+                    const int row = p.row0 + r0 + lane;  // whose place this lane works out
+                    const bf16* at = q + (p.q0 + row / a.n_heads) * a.q.token_stride + row % a.n_heads * a.q.head_stride;
+                    for (int r = r0; r < min(r0 + 32, NR); ++r) {
+                        const bool take = r < p.n_rows;
+                        const bf16* src = reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(at), r - r0));
+                        for (int c = lane; c < V; c += 32)
+                            cp_async16(smem_u32(tile) + (c / 8) * L::kQBlock + sw128_offset(r, c % 8), take ? src + 8 * c : q, take);
+                    }
                 }
                 asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
@@ -691,6 +706,8 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
             if (ropes > s) mbar_wait_brief(&sh.rope_full[s], ((ropes - 1 - s) / 2) & 1);
         for (uint32_t s = 0; s < NS; ++s)
             if (pairs > s) mbar_wait_brief(&sh.pair_full[s], ((pairs - 1 - s) / NS) & 1);
+    } else if (warp == 7) {
+        if (dense_q && qc > 0) mbar_wait_brief(&sh.q_full, (qc - 1) & 1);
     } else if (warp == 5 || warp == 6) {
         if (elect_one()) mma_commit(&sh.drained[warp - 5]);
         if (!mbar_wait_brief(&sh.drained[warp - 5], 0) && lane == 0) record(a.error, 57);
@@ -703,48 +720,43 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
 }
 
 // Joins the pieces of row tiles that were split: tasks of one row and 128 channels,
-// by a warp each where pieces are few, else by a thread block.
-constexpr int kJoinThreads = 256;
+// by a warp each where pieces are few, else by a thread block whose warps take
+// every eighth piece.
+constexpr int kJoinThreads = 256, kJoinBlocks = 6 * kSms, kChunk = 8;
 template <int C, int NR>
 __global__ void __launch_bounds__(kJoinThreads)
 latent_join_kernel(const LatentAttnArgs a, const float* parts, const Join* joins, const int n_joins, const int G) {
     using L = LCfg<C, NR>;
     constexpr int kWarps = kJoinThreads / 32, kCols = C / 128;
+    static_assert(kSms <= kJoinThreads, "a thread a join");
     __shared__ Join list[kSms];
-    __shared__ int begin[kSms + 1], most;
+    __shared__ int begin[kJoinThreads + 1], warps[kWarps];
     __shared__ float4 sum[kWarps][32];
+    __shared__ float2 stat[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 0) {  // tasks of each
-        int at = 0, top = 0;
-        for (int j0 = 0; j0 < n_joins; j0 += 32) {
-            Join j{0, 0, 0, 0};
-            if (j0 + lane < n_joins) j = joins[j0 + lane];
-            const int n = j.n_pieces > 0 ? j.n_rows : 0;
-            int in = n;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, in, off);
-                if (lane >= off) in += x;
-            }
-            if (j0 + lane < n_joins) {
-                list[j0 + lane] = j;
-                begin[j0 + lane] = at + in - n;
-            }
-            at += __shfl_sync(0xffffffffu, in, 31);
-            top = max(top, j.n_pieces);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-        if (lane == 0) {
-            begin[n_joins] = at;
-            most = top;
-        }
+    int n = 0, in;
+    bool many = false;
+    if (tid < n_joins) {  // rows of each, and of those before it
+        const Join j = joins[tid];
+        list[tid] = j;
+        n = j.n_pieces > 0 ? j.n_rows : 0;
+        many = j.n_pieces > kChunk;
     }
+    in = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, in, off);
+        if (lane >= off) in += x;
+    }
+    if (lane == 31) warps[warp] = in;
+    const bool alone = !__syncthreads_or(many);  // a warp a task
+    for (int w = 0; w < warp; ++w) in += warps[w];
+    begin[tid + 1] = in;
+    if (tid == 0) begin[0] = 0;
     __syncthreads();
-    const int tasks = begin[n_joins] * kCols;
-    const bool alone = most <= 4;  // a warp a task
-    const int step = alone ? gridDim.x * kWarps : gridDim.x, first = alone ? blockIdx.x * kWarps + warp : blockIdx.x;
+    const int tasks = begin[kJoinThreads] * kCols;
+    const int step = alone ? gridDim.x * kWarps : gridDim.x, first = alone ? warp * gridDim.x + blockIdx.x : blockIdx.x;
     for (int task = first; task < tasks; task += step) {
         const int r_all = task / kCols, col = task % kCols * 128 + 4 * lane;
         int lo = 0, hi = n_joins - 1;  // the last join that begins at or before the row
@@ -759,47 +771,67 @@ latent_join_kernel(const LatentAttnArgs a, const float* parts, const Join* joins
             const int slot = p == 0 ? j.slot : 2 * (j.slot / 2 + p);
             return parts + (static_cast<size_t>(slot) * G + g) * L::kPart;
         };
-        float top = -INFINITY;
-        for (int p = lane; p < j.n_pieces; p += 32) top = fmaxf(top, part(p)[NR * C + row]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float total = 0.0f;
-        for (int p = lane; p < j.n_pieces; p += 32) {
-            const float l = part(p)[NR * C + NR + row];
-            if (l != 0.0f) total += l * exp2_ftz(part(p)[NR * C + row] - ref);
-        }
-        total = group_sum<32>(total);
+        const int by = alone ? 1 : kWarps;
+        float m = -INFINITY, l = 0.0f;
         float4 x = make_float4(0, 0, 0, 0);
-        const int from = alone ? 0 : warp, by = alone ? 1 : kWarps;
-#pragma unroll 4
-        for (int p = from; p < j.n_pieces; p += by) {
-            const float l = part(p)[NR * C + NR + row], w = exp2_ftz(part(p)[NR * C + row] - ref);
-            if (l == 0.0f) continue;  // saw no key: its outputs were not written
-            const float4 v = *reinterpret_cast<const float4*>(part(p) + static_cast<size_t>(row) * C + col);
-            x.x = fmaf(v.x, w, x.x);
-            x.y = fmaf(v.y, w, x.y);
-            x.z = fmaf(v.z, w, x.z);
-            x.w = fmaf(v.w, w, x.w);
+        for (int p0 = alone ? 0 : warp; p0 < j.n_pieces; p0 += kChunk * by) {
+            float4 v[kChunk];  // all loads of a chunk at once
+            const int mine = p0 + lane * by;
+            float pm = -INFINITY, pl = 0.0f;
+            if (lane < kChunk && mine < j.n_pieces) {
+                pm = part(mine)[NR * C + row];
+                pl = part(mine)[NR * C + NR + row];
+            }
+#pragma unroll
+            for (int k = 0; k < kChunk; ++k)
+                if (p0 + k * by < j.n_pieces) v[k] = *reinterpret_cast<const float4*>(part(p0 + k * by) + static_cast<size_t>(row) * C + col);
+            float top = fmaxf(m, pm);
+#pragma unroll
+            for (int off = kChunk / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            top = __shfl_sync(0xffffffffu, top, 0);
+            const float ref = top == -INFINITY ? 0.0f : top, f = m == -INFINITY ? 0.0f : exp2_ftz(m - ref);
+            const float w = exp2_ftz(pm - ref);
+            l *= f;
+            x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+            m = top;
+#pragma unroll
+            for (int k = 0; k < kChunk; ++k) {
+                const float lk = __shfl_sync(0xffffffffu, pl, k), wk = __shfl_sync(0xffffffffu, w, k);
+                if (lk != 0.0f) {  // else it saw no key, and its outputs were not written
+                    l = fmaf(lk, wk, l);
+                    x.x = fmaf(v[k].x, wk, x.x);
+                    x.y = fmaf(v[k].y, wk, x.y);
+                    x.z = fmaf(v[k].z, wk, x.z);
+                    x.w = fmaf(v[k].w, wk, x.w);
+                }
+            }
         }
         if (!alone) {
             sum[warp][lane] = x;
+            if (lane == 0) stat[warp] = make_float2(m, l);
             __syncthreads();
-            if (warp == 0)
-                for (int w = 1; w < kWarps; ++w) {
-                    const float4 v = sum[w][lane];
-                    x.x += v.x;
-                    x.y += v.y;
-                    x.z += v.z;
-                    x.w += v.w;
-                }
+            float top = -INFINITY;
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w].x);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            l = 0.0f;
+            x = make_float4(0, 0, 0, 0);
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = exp2_ftz(stat[w].x - ref);
+                if (stat[w].y == 0.0f) continue;
+                const float4 v = sum[w][lane];
+                l = fmaf(stat[w].y, f, l);
+                x.x = fmaf(v.x, f, x.x);
+                x.y = fmaf(v.y, f, x.y);
+                x.z = fmaf(v.z, f, x.z);
+                x.w = fmaf(v.w, f, x.w);
+            }
+            __syncthreads();
         }
         if (alone || warp == 0) {
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (static_cast<size_t>(j.out_row) + row) * C + col) =
                 make_uint2(pack_bf16_pair(x.x * inv, x.y * inv), pack_bf16_pair(x.z * inv, x.w * inv));
         }
-        if (!alone) __syncthreads();
     }
 }
 
@@ -815,17 +847,24 @@ cudaError_t launch_t(const LatentAttnArgs& a, int G, cudaStream_t st) {
     if (a.c.n_pages > 0 && !make_tma_map_bf16_2d(&map, a.c.rows, static_cast<uint64_t>(a.c.n_pages) * a.page_size, L::W, L::W,
                                                  std::min(a.page_size, kKeys), 64))
         return cudaErrorInvalidValue;
-    if (static_cast<long long>(a.b.n_tokens) * a.n_heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (static_cast<long long>(a.b.n_tokens) * a.n_heads > 0x7fffffffLL - 2 * NR) return cudaErrorInvalidConfiguration;
+    // queries whose rows (token, head) are evenly spaced are loaded as one matrix
+    const long long pitch = a.n_heads == 1 ? a.q.token_stride : a.q.head_stride;
+    const bool dense_q = pitch >= L::W && pitch < 1ll << 36 &&
+                         (a.n_heads == 1 || a.b.n_tokens == 1 || a.q.token_stride == a.n_heads * a.q.head_stride);
+    CUtensorMap map_q{};
+    if (dense_q && !make_tma_map_bf16_2d(&map_q, a.q.data, static_cast<uint64_t>(a.b.n_tokens) * a.n_heads, L::W, pitch, NR, 64))
+        return cudaErrorInvalidValue;
     const int n = kSms / G * G;
     Join* joins = static_cast<Join*>(a.workspace);
     float* parts = reinterpret_cast<float*>(joins + kSms);
     e = timed_launch("latent_attention", st, [&] {
-        latent_attention_kernel<C, NR><<<n, kThreads, L::kSmem, st>>>(a, map, G, parts, joins);
+        latent_attention_kernel<C, NR><<<n, kThreads, L::kSmem, st>>>(a, map, map_q, dense_q, G, parts, joins);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(4 * kSms);
+    cfg.gridDim = dim3(kJoinBlocks);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};
