@@ -73,13 +73,6 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(r));
     return r != 0;
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void bulk_store_1d(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
@@ -387,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
 // A map of rows [tokens, heads, width] in boxes of 128 tokens x 64 channels of a head.
 bool map_rows(CUtensorMap* map, const KvRows& r, int tokens, int heads, int width) {
     return make_tma_map_bf16_3d(map, r.data, width, tokens, r.head_stride ? heads : 1, r.token_stride,
-                                r.head_stride ? r.head_stride : r.token_stride, 64, 128);
+                                r.head_stride ? r.head_stride : r.token_stride, 64, 128, 1);
 }
 
 template <int NOPE, int V>

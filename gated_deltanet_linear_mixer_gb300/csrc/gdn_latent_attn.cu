@@ -26,9 +26,8 @@
 // sequence that it does not hold whole is a partial result (at most two a span);
 // a second launch joins them.
 //
-// Roles: 4 softmax warps (also: rescaling, epilogue), a warp for the rows' TMA
-// loads (with the page look-ups), one issuing S, one issuing O^T, one loading
-// queries.  Cached rows are in a ring of 16 KB slots (64 keys x 128 channels) and
+// Roles: 4 softmax warps (also: rescaling, epilogue), two for the rows' TMA loads
+// (with the page look-ups), one loading queries and issuing S, one issuing O^T.  Cached rows are in a ring of 16 KB slots (64 keys x 128 channels) and
 // one of 8 KB slots (position keys).  Every wait is bounded (2 s); a wait that gives
 // up records a code (50..58) in the cache operators' device error word.
 #include <algorithm>
@@ -48,7 +47,8 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kSms = 152;
-constexpr int kKeys = 64;
+constexpr int kKeys = 64;        // of a tile
+constexpr int kRopes = 2;        // slots of position keys
 constexpr int kThreads = 256;
 constexpr float kLazy = 8.0f;
 constexpr int kMinSpan = 1;      // key tiles of a span at least
@@ -59,13 +59,13 @@ constexpr uint32_t kSmemMax = 232448, kSharedBytes = 3072;
 
 template <int C, int NR> struct LCfg {
     static constexpr int W = C + kRopeDim, kBlocks = W / 64, kPairs = C / 128;
-    static constexpr uint32_t kSlot = 16384, kRope = 8192;
+    static constexpr uint32_t kRope = kKeys * 128, kSlot = 2 * kRope;            // 64 channels of a tile, and 128
     static constexpr uint32_t kQBlock = NR * 128;                                // 64 channels of the row tile
     static constexpr uint32_t kQ = kBlocks * kQBlock + (64 - NR) * 128;          // M = 64 reads past the last block
     static constexpr uint32_t kP = NR * 128;
-    static constexpr int kFit = (kSmemMax - kSharedBytes - kQ - kP - 2 * kRope) / kSlot;
+    static constexpr int kFit = (kSmemMax - kSharedBytes - kQ - kP - kRopes * kRope) / kSlot;
     static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
-    static constexpr uint32_t kRopeAt = kSlots * kSlot, kQAt = kRopeAt + 2 * kRope, kPAt = kQAt + kQ, kSharedAt = kPAt + kP;
+    static constexpr uint32_t kRopeAt = kSlots * kSlot, kQAt = kRopeAt + kRopes * kRope, kPAt = kQAt + kQ, kSharedAt = kPAt + kP;
     static constexpr uint32_t kSmem = kSharedAt + kSharedBytes;
     static constexpr int kActive = NR / 16;                                      // softmax warps with rows
     static constexpr uint32_t kOut = 128;                                        // tensor memory: S twice, then O^T
@@ -78,7 +78,7 @@ struct Piece {
     int q0;             // the sequence's first token
     int seq;
     int row0, n_rows;   // rows (token, head) of the sequence
-    int start, n_keys;  // position of the sequence's first query; keys that some row sees
+    int start, n_keys;  // position of the sequence's first query; keys that some row of the group sees
     int a, b;           // key tiles
     int slot;           // partial result, or -1: the sequence's keys are all here
 };
@@ -89,10 +89,10 @@ struct Join {  // a sequence's row tile whose pieces start in this span and end 
 };
 
 struct Shared {
-    uint64_t pair_full[kMaxSlots], pair_empty[kMaxSlots], rope_full[2], rope_empty[2];
+    uint64_t pair_full[kMaxSlots], pair_empty[kMaxSlots], rope_full[kRopes], rope_empty[kRopes];
     uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, m_full[kMasks], drained[2];
-    long long scan[2][16];
-    long long first_item, last_item;
+    long long scan[kThreads / 32];
+    int n_round, more;
     int mask[kMasks];
     float factor[64], stat[64];
     Piece piece[kPieces];
@@ -175,32 +175,36 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 struct Need {
     int q0, qn, len, groups, tiles;
 };
-template <int N> constexpr int kLog2 = 1 + kLog2<N / 2>;
-template <> constexpr int kLog2<1> = 0;
 // x / y, in 32 bits where they fit: a 64-bit division takes several hundred cycles.
 __device__ __forceinline__ long long quotient(long long x, long long y) {
     if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
     return x / y;
 }
-template <int NR>
-__device__ __forceinline__ Need need_of(const LatentAttnArgs& a, int seq, int G) {
+template <int ROWS>
+__device__ __forceinline__ Need need_of(const LatentAttnArgs& a, int seq) {
     Need n;
     n.q0 = a.b.cu[seq];
     n.qn = a.b.cu[seq + 1] - n.q0;
     n.len = a.b.kv_lens[seq];
     const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
     const int len = static_cast<int>(min(static_cast<long long>(max(n.len, 0)), cap));
-    n.groups = (n.qn * a.n_heads + NR * G - 1) >> (G == 2 ? kLog2<2 * NR> : kLog2<NR>);
-    n.tiles = max(1, (len - 1) / kKeys + 1);
+    n.groups = (n.qn * a.n_heads + ROWS - 1) / ROWS;
+    n.tiles = max(1, (len + kKeys - 1) / kKeys);
     return n;
 }
 
-template <int C, int NR>
+struct Maps {
+    CUtensorMap rows;   // boxes of a page's (at most a tile's) rows x 64 channels
+    CUtensorMap pairs;  // of a tile's rows x 128 channels, in two halves
+    CUtensorMap q;      // of a row tile x 64 channels
+};
+
+template <int C, int NR, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
-                        const int dense_q, const int G, float* parts, Join* joins) {
+latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps maps, const int dense_q, float* parts, Join* joins) {
     using L = LCfg<C, NR>;
-    constexpr int NP = L::kPairs, NS = L::kSlots;
+    constexpr int NP = L::kPairs, NS = L::kSlots, G = PAIR ? 2 : 1;
+    constexpr int kScores = kKeys / 2;  // of a lane: two rows of a quarter of the keys
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem + L::kSharedAt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -211,35 +215,30 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
     // ---- this thread block's span of the (sequence, group, key tile) axis
     const int each = (a.b.n_seq + kThreads - 1) / kThreads;
     const int s0 = min(tid * each, a.b.n_seq), s1 = min(s0 + each, a.b.n_seq);
-    long long units = 0, items = 0;
+    long long units = 0;
     Need first{};  // of s0: all that this thread has where there are no more sequences than threads
     for (int s = s0; s < s1; ++s) {
-        const Need n = need_of<NR>(a, s, G);
+        const Need n = need_of<NR * G>(a, s);
         if (s == s0) first = n;
         units += static_cast<long long>(n.groups) * n.tiles;
-        items += n.groups;
     }
-    long long u_in = units, i_in = items;  // inclusive
+    long long u_in = units;  // inclusive
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, u_in, off), i = __shfl_up_sync(0xffffffffu, i_in, off);
-        if (lane >= off) {
-            u_in += u;
-            i_in += i;
-        }
+        const long long u = __shfl_up_sync(0xffffffffu, u_in, off);
+        if (lane >= off) u_in += u;
     }
-    if (lane == 31) {
-        sh.scan[0][warp] = u_in;
-        sh.scan[1][warp] = i_in;
-    }
+    if (lane == 31) sh.scan[warp] = u_in;
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sh.pair_full[i], 1);
-            mbar_init(&sh.pair_empty[i], 1);
+            mbar_init(&sh.pair_empty[i], G);
+        }
+        for (int i = 0; i < kRopes; ++i) {
+            mbar_init(&sh.rope_full[i], 1);
+            mbar_init(&sh.rope_empty[i], G);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.rope_full[i], 1);
-            mbar_init(&sh.rope_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.s_empty[i], L::kActive);
         }
@@ -253,13 +252,11 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
         fence_barrier_init();
     }
     __syncthreads();
-    long long u_base = u_in - units, i_base = i_in - items, total = 0;
+    long long u_base = u_in - units, total = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) {
-            u_base += sh.scan[0][w];
-            i_base += sh.scan[1][w];
-        }
-        total += sh.scan[0][w];
+        if (w < warp) u_base += sh.scan[w];
+        total += sh.scan[w];
     }
     const long long per = max(quotient(total + n_spans - 1, n_spans), static_cast<long long>(kMinSpan));
     const long long u0 = span * per, u1 = min(u0 + per, total);
@@ -271,79 +268,105 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
         return;
     }
     if (warp == 5) tmem_alloc(&sh.tmem_slot, 512);
-    {
-        long long u = u_base, i = i_base;
-        for (int s = s0; s < s1; ++s) {
-            const Need n = s == s0 ? first : need_of<NR>(a, s, G);
-            const long long all = static_cast<long long>(n.groups) * n.tiles;
-            if (u <= u0 && u0 < u + all) sh.first_item = i + quotient(u0 - u, n.tiles);
-            if (u < u1 && u1 <= u + all) {  // holds the span's last tile
-                const int k = static_cast<int>(quotient(u1 - 1 - u, n.tiles));
-                const long long head = u + static_cast<long long>(k) * n.tiles;
-                const long long rest = head + n.tiles - u1;  // tiles in the spans that follow
-                sh.last_item = i + k;
-                const long long row0 = (static_cast<long long>(k) * G + g_own) * NR;
-                const long long rows = min(static_cast<long long>(NR), static_cast<long long>(n.qn) * a.n_heads - row0);
+    // The thread whose sequences hold the span's first tile lays out the pieces, kPieces at a time.
+    long long u_at = u_base;  // where sequence s_at begins
+    int s_at = s0, k_at = 0;
+    Need n_at = first;
+    const bool walker = u_base <= u0 && u0 < u_base + units;
+    if (walker) {
+        for (long long all = static_cast<long long>(n_at.groups) * n_at.tiles; u_at + all <= u0;
+             all = static_cast<long long>(n_at.groups) * n_at.tiles) {
+            u_at += all;
+            n_at = need_of<NR * G>(a, ++s_at);
+        }
+        k_at = static_cast<int>(quotient(u0 - u_at, n_at.tiles));
+    }
+    auto lay_out = [&] {
+        const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
+        int i = 0;
+        bool more = true;
+        while (i < kPieces) {
+            const long long all = static_cast<long long>(n_at.groups) * n_at.tiles;
+            const long long head = u_at + static_cast<long long>(k_at) * n_at.tiles;  // the item's first tile
+            if (k_at == n_at.groups) {  // on to the next sequence
+                u_at += all;
+                k_at = 0;
+                if (u_at >= u1) {
+                    more = false;
+                    break;
+                }
+                n_at = need_of<NR * G>(a, ++s_at);
+                continue;
+            }
+            if (head >= u1) {
+                more = false;
+                break;
+            }
+            if (n_at.len > cap) record(a.error, kKvErrTable);
+            const int len = static_cast<int>(min(static_cast<long long>(max(n_at.len, 0)), cap));
+            const int all_rows = n_at.qn * a.n_heads, row0 = (k_at * G + g_own) * NR, rows = min(NR, all_rows - row0);
+            const int last_row = min((k_at + 1) * G * NR, all_rows) - 1;  // of the group
+            Piece p;
+            p.q0 = n_at.q0;
+            p.seq = s_at;
+            p.row0 = row0;
+            p.n_rows = max(rows, 0);
+            p.start = max(n_at.len, 0) - n_at.qn;  // queries before 0 see nothing
+            p.n_keys = max(0, min(p.start + last_row / a.n_heads + 1, len));
+            p.a = static_cast<int>(max(u0 - head, 0ll));
+            const int b = static_cast<int>(min(u1 - head, static_cast<long long>(n_at.tiles)));
+            p.b = max(p.a, min(b, (p.n_keys + kKeys - 1) / kKeys));
+            p.slot = p.a == 0 && b == n_at.tiles ? -1 : 2 * span + (head + p.a > u0 ? 1 : 0);
+            sh.piece[i++] = p;
+            if (head + n_at.tiles >= u1) {  // the span's last one
                 Join j{0, 0, 0, 0};
+                const long long rest = head + n_at.tiles - u1;  // tiles in the spans that follow
                 if (head >= u0 && rest > 0 && rows > 0) {
                     j.n_pieces = 1 + static_cast<int>(quotient(rest + per - 1, per));
-                    j.out_row = static_cast<int>(static_cast<long long>(n.q0) * a.n_heads + row0);
-                    j.n_rows = static_cast<int>(rows);
-                    j.slot = 2 * span + (head > u0 ? 1 : 0);
+                    j.out_row = n_at.q0 * a.n_heads + row0;
+                    j.n_rows = rows;
+                    j.slot = p.slot;
                 }
                 joins[blockIdx.x] = j;
+                more = false;
+                break;
             }
-            u += all;
-            i += n.groups;
+            ++k_at;
         }
+        sh.n_round = i;
+        sh.more = more;
+    };
+    if (walker) {
+        // the loading warps' first look-up, on its way meanwhile
+        const long long key = (u0 - u_at - static_cast<long long>(k_at) * n_at.tiles) * kKeys;
+        if (key / a.page_size < a.b.pages_per_seq)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.b.table + static_cast<size_t>(s_at) * a.b.pages_per_seq + key / a.page_size));
+        lay_out();
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if (PAIR) {  // the other's barriers are initialised
+        cluster_arrive();
+        cluster_wait();
+    }
     const uint32_t tmem = sh.tmem_slot;
-    const int n_pieces = static_cast<int>(sh.last_item - sh.first_item) + 1;
 
+    // a slot is free once the products of both thread blocks of a pair are done
+    auto give = [&](uint64_t* bar) {
+        if (PAIR) mma_commit_multicast(bar, 3);
+        else mma_commit(bar);
+    };
     // counts that the roles carry from round to round
     uint32_t g = 0;   // key tiles
     uint32_t qc = 0;  // pieces with tiles
     bool ok = true;
     uint32_t ropes = 0, pairs = 0;  // loads started
 
-    for (int p0 = 0; p0 < n_pieces; p0 += kPieces) {
-        {   // the pieces of this round
-            long long u = u_base, i = i_base;
-            const long long i0 = sh.first_item + p0, i1 = min(sh.last_item + 1, i0 + kPieces);
-            for (int s = s0; s < s1 && i < i1; ++s) {
-                const Need n = s == s0 ? first : need_of<NR>(a, s, G);
-                if (i + n.groups > i0) {
-                    const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
-                    if (n.len > cap) record(a.error, kKvErrTable);
-                    const int len = static_cast<int>(min(static_cast<long long>(max(n.len, 0)), cap));
-                    for (long long k = max(i0 - i, 0ll); k < n.groups && i + k < i1; ++k) {
-                        const long long head = u + k * n.tiles, row0 = (k * G + g_own) * NR;
-                        const long long rows = min(static_cast<long long>(NR), static_cast<long long>(n.qn) * a.n_heads - row0);
-                        Piece p;
-                        p.q0 = n.q0;
-                        p.seq = s;
-                        p.row0 = static_cast<int>(row0);
-                        p.n_rows = rows > 0 ? static_cast<int>(rows) : 0;
-                        p.start = max(n.len, 0) - n.qn;  // queries before 0 see nothing
-                        p.n_keys = rows > 0 ? max(0, min(p.start + static_cast<int>((row0 + rows - 1) / a.n_heads) + 1, len)) : 0;
-                        p.a = static_cast<int>(max(u0 - head, 0ll));
-                        const int b = static_cast<int>(min(u1 - head, static_cast<long long>(n.tiles)));
-                        p.b = max(p.a, min(b, (p.n_keys + kKeys - 1) / kKeys));
-                        p.slot = p.a == 0 && b == n.tiles ? -1 : 2 * span + (head + p.a > u0 ? 1 : 0);
-                        sh.piece[i + k - i0] = p;
-                    }
-                }
-                u += static_cast<long long>(n.groups) * n.tiles;
-                i += n.groups;
-            }
-        }
-        __syncthreads();
-        const int n_round = min(kPieces, n_pieces - p0);
+    for (;;) {
+        const int n_round = sh.n_round;
         const bool dead = sh.dead != 0;
-
+        const bool more = sh.more;
         if (dead) {
             // a wait gave up in an earlier round: nothing more is started
         } else if (warp < 4) {
@@ -353,7 +376,6 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
             const uint32_t t_lane = (32u * warp) << 16;
             for (int i = 0; i < n_round; ++i) {
                 const Piece p = sh.piece[i];
-                if (p.n_rows == 0) continue;
                 const int rA = 16 * warp + (lane >> 2), rB = rA + 8;
                 int limA = 0, limB = 0;  // keys that this lane's rows see
                 if (rA < p.n_rows) limA = min(p.start + (p.row0 + rA) / a.n_heads + 1, p.n_keys);
@@ -363,7 +385,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                 for (int t = p.a; t < p.b; ++t, ++g) {
                     const int key0 = t * kKeys, valid = p.n_keys - key0;  // keys of the tile that exist
                     const uint32_t sb = g & 1;
-                    float s[32];
+                    float s[kScores];
                     bool lift = false;
                     float topA = -INFINITY, topB = -INFINITY;
                     if ((active || valid < kKeys) && ok &&
@@ -373,23 +395,23 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                         record(a.error, 50);
                     if (active) {
                         tc_fence_after_sync();
-                        tmem_ld_rows16(tmem + t_lane + 64 * sb, s);
+                        tmem_ld_rows16(tmem + t_lane + kKeys * sb, s);
                         const int mask = sh.mask[g % kMasks];
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) s[j] *= scale2;
-                        if (key0 + kKeys > lim || mask != 15) {
+                        for (int j = 0; j < kScores; ++j) s[j] *= scale2;
+                        if (key0 + kKeys > lim || mask != (1 << (kKeys / 16)) - 1) {
                             const int c = key0 + 2 * (lane & 3);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
+                            for (int j = 0; j < kScores; ++j) {
                                 const int key = c + 8 * (j >> 2) + (j & 1);
                                 if (key >= (j & 2 ? limB : limA) || !(mask >> (j >> 3) & 1)) s[j] = -INFINITY;
                             }
                         }
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
+                        for (int j = 0; j < kScores; j += 4) {
                             topA = fmaxf(topA, fmaxf(s[j], s[j + 1]));
                             topB = fmaxf(topB, fmaxf(s[j + 2], s[j + 3]));
                         }
@@ -433,9 +455,9 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                     }
                     if (active) {
                         const float refA = mA == -INFINITY ? 0.0f : mA, refB = mB == -INFINITY ? 0.0f : mB;
-                        uint32_t w[16];
+                        uint32_t w[kScores / 2];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
+                        for (int j = 0; j < kScores; j += 2) {
                             const float ref = j & 2 ? refB : refA;
                             w[j / 2] = pack_bf16x2(exp2_ftz(s[j] - ref), exp2_ftz(s[j + 1] - ref));
                             const float sum = __uint_as_float(w[j / 2] << 16) + __uint_as_float(w[j / 2] & 0xFFFF0000u);
@@ -447,7 +469,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                             record(a.error, 52);
                         uint8_t* tile = smem + L::kPAt;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
+                        for (int c = 0; c < kKeys / 8; ++c) {
                             *reinterpret_cast<uint32_t*>(tile + sw128_offset(rA, c) + 4 * (lane & 3)) = w[2 * c];
                             *reinterpret_cast<uint32_t*>(tile + sw128_offset(rB, c) + 4 * (lane & 3)) = w[2 * c + 1];
                         }
@@ -460,7 +482,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                             uint4* row = reinterpret_cast<uint4*>(smem + slot * L::kSlot);
                             for (int x = tid; x < 2 * (kKeys - valid) * 8; x += 128) {
                                 const int half = x & 1, r = valid + x / 16, c = x / 2 % 8;
-                                row[half * 512 + r * 8 + c] = make_uint4(0, 0, 0, 0);
+                                row[half * (L::kRope / 16) + r * 8 + c] = make_uint4(0, 0, 0, 0);
                             }
                         }
                     }
@@ -493,45 +515,55 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                 }
                 group_sync(1, 128);
                 tc_fence_after_sync();
+                constexpr int kStep = NR < 32 ? 16 : 32;
+                auto load_out = [&](int c, float* v) {
+                    if (kStep == 32) tmem_ld32(tmem + t_lane + L::kOut + c, v);
+                    else tmem_ld16(tmem + t_lane + L::kOut + c, v);
+                };
                 if (p.slot < 0) {
                     bf16* out = static_cast<bf16*>(a.out) + (static_cast<size_t>(p.q0) * a.n_heads + p.row0) * C + 32 * warp + lane;
 #pragma unroll 1
-                    for (int c = 0; c < NP * NR; c += 16) {
-                        float v[16];
-                        if (any) tmem_ld16(tmem + t_lane + L::kOut + c, v);
+                    for (int c = 0; c < NP * NR; c += kStep) {
+                        float v[kStep];
+                        if (any) load_out(c, v);
+                        bf16* at = out + static_cast<size_t>(c % NR) * C + c / NR * 128;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int r = c % NR + e;
-                            if (r < p.n_rows) out[static_cast<size_t>(r) * C + c / NR * 128] = __float2bfloat16_rn(any ? v[e] * sh.stat[r] : 0.0f);
-                        }
+                        for (int e = 0; e < kStep; ++e)
+                            if (c % NR + e < p.n_rows) at[e * C] = __float2bfloat16_rn(any ? v[e] * sh.stat[c % NR + e] : 0.0f);
                     }
                 } else if (any) {
                     float* out = parts + (static_cast<size_t>(p.slot) * G + g_own) * L::kPart + 32 * warp + lane;
 #pragma unroll 1
-                    for (int c = 0; c < NP * NR; c += 16) {
-                        float v[16];
-                        tmem_ld16(tmem + t_lane + L::kOut + c, v);
+                    for (int c = 0; c < NP * NR; c += kStep) {
+                        float v[kStep];
+                        load_out(c, v);
+                        float* at = out + static_cast<size_t>(c % NR) * C + c / NR * 128;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int r = c % NR + e;
-                            if (r < p.n_rows) out[static_cast<size_t>(r) * C + c / NR * 128] = v[e];
-                        }
+                        for (int e = 0; e < kStep; ++e)
+                            if (c % NR + e < p.n_rows) at[e * C] = v[e];
                     }
                 }
                 tc_fence_before_sync();
                 group_sync(1, 128);  // stat, and the output in tensor memory, may be written again
             }
-        } else if (warp == 4) {
-            // ---- cached rows: page look-ups by the warp, loads by one lane
+        } else if (warp == 4 || warp == 7) {
+            // ---- cached rows: page look-ups by the warp, loads by one lane.  A load takes about 55 cycles to
+            // issue, and pages of 16 rows need 36 a tile: two warps share them, the first the position keys
+            // and two slots, the second the others.  Of a pair each thread block loads half of what both
+            // need into both.
             const int R = min(a.page_size, kKeys), per_tile = kKeys / R;
-            const bool leader = elect_one();
+            const bool leader = elect_one(), lead_warp = warp == 4;
             const int nowhere = a.c.n_pages * a.page_size;  // past the last row: the load gives zeros
+            auto load = [&](uint8_t* dst, uint64_t* bar, int col, int row) {
+                if (PAIR) tma_load_2d_multicast(dst, &maps.rows, bar, col, row, 3);
+                else tma_load_2d(dst, &maps.rows, bar, col, row);
+            };
             for (int i = 0; ok && i < n_round; ++i) {
                 const Piece p = sh.piece[i];
                 int row = 0;
-                const int first = p.a * per_tile, n = (p.b - p.a) * per_tile;
+                const int first_chunk = p.a * per_tile, n = (p.b - p.a) * per_tile;
                 auto look_up = [&](int x) {  // where chunk x of the piece lies; negative: not mapped
-                    const int key = (first + x) * R;
+                    const int key = (first_chunk + x) * R;
                     if (x >= n || key >= p.n_keys) return nowhere;
                     const int page = a.b.table[static_cast<size_t>(p.seq) * a.b.pages_per_seq + key / a.page_size];
                     return page >= 0 && page < a.c.n_pages ? page * a.page_size + key % a.page_size : -1;
@@ -543,39 +575,61 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                         row = ahead;
                         ahead = look_up(x + 32 + lane);
                     }
-                    // where chunk lane (of the tile's per_tile) lies, and chunk lane / 2
-                    int mine = __shfl_sync(0xffffffffu, row, (x + lane % per_tile) & 31);
-                    const uint32_t gone = __ballot_sync(0xffffffffu, mine < 0);  // the tile's lowest bits, over and over
-                    int mask = 15;
-                    if (gone) {
-                        if (leader) record(a.error, kKvErrTable);
-                        for (int c = 0; c < per_tile; ++c)
-                            if (gone >> c & 1) mask &= ~(((1 << (R / 16)) - 1) << (c * (R / 16)));
-                        if (mine < 0) mine = nowhere;
+                    int at[4];
+                    int mask = (1 << (kKeys / 16)) - 1;
+#pragma unroll
+                    for (int c = 0; c < kKeys / 16; ++c) {
+                        at[c] = __shfl_sync(0xffffffffu, row, (x + c) & 31);
+                        if (c < per_tile && at[c] < 0) {
+                            if (leader && lead_warp) record(a.error, kKvErrTable);
+                            mask &= ~(((1 << (R / 16)) - 1) << (c * (R / 16)));
+                            at[c] = nowhere;
+                        }
                     }
-                    const int mine2 = __shfl_sync(0xffffffffu, mine, lane >> 1);
-                    if (leader) {
-                        sh.mask[g % kMasks] = mask;
-                        mbar_arrive(&sh.m_full[g % kMasks]);
+                    if (lead_warp) {
+                        if (leader) {
+                            sh.mask[g % kMasks] = mask;
+                            mbar_arrive(&sh.m_full[g % kMasks]);
+                        }
+                        const uint32_t rb = g % kRopes;
+                        if (g >= kRopes) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.rope_empty[rb], (g / kRopes - 1) & 1));
+                        if (!ok) break;
+                        ++ropes;
+                        if (leader) {
+                            mbar_arrive_expect_tx(&sh.rope_full[rb], L::kRope);
+                            if (!PAIR || static_cast<int>(g & 1) == g_own)
+#pragma unroll
+                                for (int c = 0; c < kKeys / 16; ++c)
+                                    if (c < per_tile)
+                                        load(smem + L::kRopeAt + rb * L::kRope + c * R * 128, &sh.rope_full[rb], C, at[c]);
+                        }
+                        __syncwarp();
                     }
-                    const uint32_t rb = g & 1;
-                    if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.rope_empty[rb], ((g >> 1) - 1) & 1));
-                    if (!ok) break;
-                    ++ropes;
-                    if (leader) mbar_arrive_expect_tx(&sh.rope_full[rb], L::kRope);
-                    __syncwarp();
-                    if (lane < per_tile)
-                        tma_load_2d(smem + L::kRopeAt + rb * L::kRope + lane * R * 128, &map, &sh.rope_full[rb], C, mine);
-                    for (int q = 0; q < NP; ++q) {
+                    const int q0 = lead_warp ? 0 : 2;
+#pragma unroll
+                    for (int qq = 0; qq < 2; ++qq) {
+                        const int q = q0 + qq;
+                        if (q >= NP) break;
                         const uint32_t fill = g * NP + q, slot = fill % NS;
                         if (fill >= NS) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_empty[slot], (fill / NS - 1) & 1));
                         if (!ok) break;
-                        ++pairs;
-                        if (leader) mbar_arrive_expect_tx(&sh.pair_full[slot], L::kSlot);
-                        __syncwarp();
-                        if (lane < 2 * per_tile) {  // a lane a box: chunk lane / 2, half lane % 2
-                            uint8_t* dst = smem + slot * L::kSlot + (lane & 1) * 8192 + (lane >> 1) * R * 128;
-                            tma_load_2d(dst, &map, &sh.pair_full[slot], 128 * q + 64 * (lane & 1), mine2);
+                        pairs = fill + 1;
+                        if (leader) {
+                            uint8_t* dst = smem + slot * L::kSlot;
+                            mbar_arrive_expect_tx(&sh.pair_full[slot], L::kSlot);
+                            if (PAIR && (q & 1) != g_own) {
+                                // the other's to load
+                            } else if (per_tile == 1) {
+                                if (PAIR) tma_load_3d_multicast(dst, &maps.pairs, &sh.pair_full[slot], 0, at[0], 2 * q, 3);
+                                else tma_load_3d(dst, &maps.pairs, &sh.pair_full[slot], 0, at[0], 2 * q);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < kKeys / 16; ++c)
+                                    if (c < per_tile) {
+                                        load(dst + c * R * 128, &sh.pair_full[slot], 128 * q, at[c]);
+                                        load(dst + L::kRope + c * R * 128, &sh.pair_full[slot], 128 * q + 64, at[c]);
+                                    }
+                            }
                         }
                         __syncwarp();
                     }
@@ -590,92 +644,16 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
             constexpr uint32_t id = idesc_bf16_f32(64, kKeys);
             const uint64_t dq = desc_kmajor_sw128(smem_u32(smem + L::kQAt)), dr = desc_kmajor_sw128(smem_u32(smem + L::kRopeAt)),
                            dk = desc_kmajor_sw128(smem_u32(smem));
-            for (int i = 0; ok && i < n_round; ++i) {
-                const int a0 = sh.piece[i].a, b0 = sh.piece[i].b;
-                if (sh.piece[i].n_rows == 0 || a0 >= b0) continue;
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_full, qc & 1)))) break;
-                ++qc;
-                for (int t = a0; ok && t < b0; ++t, ++g) {
-                    const uint32_t sb = g & 1;
-                    if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_empty[sb], ((g >> 1) - 1) & 1));
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait_brief(&sh.rope_full[sb], (g >> 1) & 1));
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + 64 * sb, dq + ((C / 64) * L::kQBlock >> 4) + 2 * k, dr + (sb * L::kRope >> 4) + 2 * k, id,
-                                     k > 0 ? 1u : 0u);
-                        mma_commit(&sh.rope_empty[sb]);
-                    }
-                    for (int q = 0; q < NP; ++q) {
-                        const uint32_t fill = g * NP + q, slot = fill % NS;
-                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_full[slot], (fill / NS) & 1)))) break;
-                        tc_fence_after_sync();
-                        if (leader) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_bf16(tmem + 64 * sb, dq + ((2 * q + h) * L::kQBlock >> 4) + 2 * k,
-                                             dk + ((slot * L::kSlot + h * 8192) >> 4) + 2 * k, id, 1u);
-                        }
-                        __syncwarp();
-                    }
-                    if (leader) mma_commit(&sh.s_full[sb]);
-                    __syncwarp();
-                }
-                if (leader) mma_commit(&sh.q_empty);
-                __syncwarp();
-            }
-            if (!ok && lane == 0) record(a.error, 56);
-            if (!ok) sh.dead = 1;
-        } else if (warp == 6) {
-            // ---- O^T += V^T P^T
-            const bool leader = elect_one();
-            constexpr uint32_t id = idesc_bf16_f32(128, NR, true, false);
-            const uint64_t dv = desc_mnmajor_sw128(smem_u32(smem), 8192), dp = desc_kmajor_sw128(smem_u32(smem + L::kPAt));
-            for (int i = 0; ok && i < n_round; ++i) {
-                const int a0 = sh.piece[i].a, b0 = sh.piece[i].b;
-                if (sh.piece[i].n_rows == 0) continue;
-                for (int t = a0; ok && t < b0; ++t, ++g) {
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.p_full, g & 1)))) break;
-                    for (int q = 0; q < NP; ++q) {
-                        const uint32_t fill = g * NP + q, slot = fill % NS;
-                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_full[slot], (fill / NS) & 1)))) break;
-                        tc_fence_after_sync();
-                        if (leader) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16(tmem + L::kOut + q * NR, dv + ((slot * L::kSlot + k * 2048) >> 4), dp + 2 * k, id,
-                                         (t > a0 || k > 0) ? 1u : 0u);
-                            mma_commit(&sh.pair_empty[slot]);
-                        }
-                        __syncwarp();
-                    }
-                    if (!ok) break;
-                    if (leader) mma_commit(&sh.pv_done);
-                    __syncwarp();
-                }
-            }
-            if (!ok && lane == 0) record(a.error, 56);
-            if (!ok) sh.dead = 1;
-        } else {
-            // ---- queries
-            for (int i = 0; ok && i < n_round; ++i) {
-                const Piece p = sh.piece[i];
-                if (p.n_rows == 0 || p.a >= p.b) continue;
-                if (qc > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty, (qc - 1) & 1)))) break;
-                ++qc;
+            auto load_queries = [&](const Piece& p) {
                 uint8_t* tile = smem + L::kQAt;
                 if (dense_q) {  // evenly spaced rows: those behind the sequence's last are another's, or zeros, and not used
-                    if (lane == 0) {
+                    if (leader) {
                         mbar_arrive_expect_tx(&sh.q_full, L::kBlocks * L::kQBlock);
                         for (int b = 0; b < L::kBlocks; ++b)
-                            tma_load_2d(tile + b * L::kQBlock, &map_q, &sh.q_full, 64 * b, p.q0 * a.n_heads + p.row0);
+                            tma_load_2d(tile + b * L::kQBlock, &maps.q, &sh.q_full, 64 * b, p.q0 * a.n_heads + p.row0);
                     }
                     __syncwarp();
-                    continue;
+                    return;
                 }
                 constexpr int V = L::W / 8;
                 const bf16* q = static_cast<const bf16*>(a.q.data);
@@ -692,23 +670,97 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
                 asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.q_full);
+                if (leader) mbar_arrive(&sh.q_full);
+            };
+            for (int i = 0; ok && i < n_round; ++i) {
+                const int a0 = sh.piece[i].a, b0 = sh.piece[i].b;
+                if (a0 >= b0) continue;
+                // queries, once the products with the last ones are done
+                if (qc > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty, (qc - 1) & 1)))) break;
+                load_queries(sh.piece[i]);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_full, qc & 1)))) break;
+                ++qc;
+                for (int t = a0; ok && t < b0; ++t, ++g) {
+                    const uint32_t sb = g & 1;
+                    if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_empty[sb], ((g >> 1) - 1) & 1));
+                    const uint32_t rb = g % kRopes;
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_brief(&sh.rope_full[rb], (g / kRopes) & 1));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(tmem + kKeys * sb, dq + ((C / 64) * L::kQBlock >> 4) + 2 * k, dr + (rb * L::kRope >> 4) + 2 * k, id,
+                                     k > 0 ? 1u : 0u);
+                        give(&sh.rope_empty[rb]);
+                    }
+                    for (int q = 0; q < NP; ++q) {
+                        const uint32_t fill = g * NP + q, slot = fill % NS;
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_full[slot], (fill / NS) & 1)))) break;
+                        tc_fence_after_sync();
+                        if (leader) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_bf16(tmem + kKeys * sb, dq + ((2 * q + h) * L::kQBlock >> 4) + 2 * k,
+                                             dk + ((slot * L::kSlot + h * L::kRope) >> 4) + 2 * k, id, 1u);
+                        }
+                        __syncwarp();
+                    }
+                    if (leader) mma_commit(&sh.s_full[sb]);
+                    __syncwarp();
+                }
+                if (leader) mma_commit(&sh.q_empty);
+                __syncwarp();
             }
-            if (!ok && lane == 0) record(a.error, 57);
+            if (!ok && lane == 0) record(a.error, 56);
+            if (!ok) sh.dead = 1;
+        } else if (warp == 6) {
+            // ---- O^T += V^T P^T
+            const bool leader = elect_one();
+            constexpr uint32_t id = idesc_bf16_f32(128, NR, true, false);
+            const uint64_t dv = desc_mnmajor_sw128(smem_u32(smem), L::kRope), dp = desc_kmajor_sw128(smem_u32(smem + L::kPAt));
+            for (int i = 0; ok && i < n_round; ++i) {
+                const int a0 = sh.piece[i].a, b0 = sh.piece[i].b;
+                for (int t = a0; ok && t < b0; ++t, ++g) {
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.p_full, g & 1)))) break;
+                    for (int q = 0; q < NP; ++q) {
+                        const uint32_t fill = g * NP + q, slot = fill % NS;
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pair_full[slot], (fill / NS) & 1)))) break;
+                        tc_fence_after_sync();
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                mma_bf16(tmem + L::kOut + q * NR, dv + ((slot * L::kSlot + k * 2048) >> 4), dp + 2 * k, id,
+                                         (t > a0 || k > 0) ? 1u : 0u);
+                            give(&sh.pair_empty[slot]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (leader) mma_commit(&sh.pv_done);
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) record(a.error, 56);
             if (!ok) sh.dead = 1;
         }
         __syncwarp();
         __syncthreads();
+        if (!more) break;
+        if (walker) lay_out();
+        __syncthreads();
     }
     // nothing of this thread block is in flight when its memory is given back
-    if (warp == 4) {
-        for (uint32_t s = 0; s < 2; ++s)
-            if (ropes > s) mbar_wait_brief(&sh.rope_full[s], ((ropes - 1 - s) / 2) & 1);
-        for (uint32_t s = 0; s < NS; ++s)
-            if (pairs > s) mbar_wait_brief(&sh.pair_full[s], ((pairs - 1 - s) / NS) & 1);
-    } else if (warp == 7) {
-        if (dense_q && qc > 0) mbar_wait_brief(&sh.q_full, (qc - 1) & 1);
+    if ((warp == 4 || warp == 7) && sh.dead) {  // else all of it was used
+        for (uint32_t s = 0; s < kRopes; ++s)
+            if (ropes > s) mbar_wait_brief(&sh.rope_full[s], ((ropes - 1 - s) / kRopes) & 1);
+        // this warp's last fill of each slot
+        for (uint32_t fill = pairs > NS ? pairs - NS : 0; fill < pairs; ++fill)
+            if ((fill % NP >= 2) == (warp == 7)) mbar_wait_brief(&sh.pair_full[fill % NS], (fill / NS) & 1);
     } else if (warp == 5 || warp == 6) {
+        if (warp == 5 && !ok && dense_q) mbar_wait_brief(&sh.q_full, qc & 1);  // queries on their way
         if (elect_one()) mma_commit(&sh.drained[warp - 5]);
         if (!mbar_wait_brief(&sh.drained[warp - 5], 0) && lane == 0) record(a.error, 57);
     }
@@ -717,6 +769,10 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensor
     __syncthreads();
     tc_fence_after_sync();
     if (warp == 5) tmem_dealloc(tmem, 512);
+    if (PAIR) {  // nothing of the other is on its way here any more
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // Joins the pieces of row tiles that were split: tasks of one row and 128 channels,
@@ -837,30 +893,41 @@ latent_join_kernel(const LatentAttnArgs a, const float* parts, const Join* joins
 
 int rows_of_tile(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-template <int C, int NR>
-cudaError_t launch_t(const LatentAttnArgs& a, int G, cudaStream_t st) {
+template <int C, int NR, bool PAIR>
+cudaError_t launch_t(const LatentAttnArgs& a, cudaStream_t st) {
+    constexpr int G = PAIR ? 2 : 1;
     using L = LCfg<C, NR>;
     static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = allow_smem(latent_attention_kernel<C, NR>, L::kSmem, ready);
+    cudaError_t e = allow_smem(latent_attention_kernel<C, NR, PAIR>, L::kSmem, ready);
     if (e != cudaSuccess) return e;
-    CUtensorMap map{};
-    if (a.c.n_pages > 0 && !make_tma_map_bf16_2d(&map, a.c.rows, static_cast<uint64_t>(a.c.n_pages) * a.page_size, L::W, L::W,
-                                                 std::min(a.page_size, kKeys), 64))
+    Maps maps{};
+    const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) * a.page_size;
+    if (rows > 0 && !(make_tma_map_bf16_2d(&maps.rows, a.c.rows, rows, L::W, L::W, std::min(a.page_size, kKeys), 64) &&
+                      make_tma_map_bf16_3d(&maps.pairs, a.c.rows, 64, rows, L::W / 64, L::W, 64, 64, kKeys, 2)))
         return cudaErrorInvalidValue;
     if (static_cast<long long>(a.b.n_tokens) * a.n_heads > 0x7fffffffLL - 2 * NR) return cudaErrorInvalidConfiguration;
     // queries whose rows (token, head) are evenly spaced are loaded as one matrix
     const long long pitch = a.n_heads == 1 ? a.q.token_stride : a.q.head_stride;
     const bool dense_q = pitch >= L::W && pitch < 1ll << 36 &&
                          (a.n_heads == 1 || a.b.n_tokens == 1 || a.q.token_stride == a.n_heads * a.q.head_stride);
-    CUtensorMap map_q{};
-    if (dense_q && !make_tma_map_bf16_2d(&map_q, a.q.data, static_cast<uint64_t>(a.b.n_tokens) * a.n_heads, L::W, pitch, NR, 64))
+    if (dense_q && !make_tma_map_bf16_2d(&maps.q, a.q.data, static_cast<uint64_t>(a.b.n_tokens) * a.n_heads, L::W, pitch, NR, 64))
         return cudaErrorInvalidValue;
     const int n = kSms / G * G;
     Join* joins = static_cast<Join*>(a.workspace);
     float* parts = reinterpret_cast<float*>(joins + kSms);
+    cudaLaunchConfig_t main{};
+    main.gridDim = dim3(n);
+    main.blockDim = dim3(kThreads);
+    main.dynamicSmemBytes = L::kSmem;
+    main.stream = st;
+    cudaLaunchAttribute pair{};
+    pair.id = cudaLaunchAttributeClusterDimension;
+    pair.val.clusterDim.x = 2;
+    pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+    main.attrs = &pair;
+    main.numAttrs = PAIR ? 1 : 0;
     e = timed_launch("latent_attention", st, [&] {
-        latent_attention_kernel<C, NR><<<n, kThreads, L::kSmem, st>>>(a, map, map_q, dense_q, G, parts, joins);
-        return cudaGetLastError();
+        return cudaLaunchKernelEx(&main, latent_attention_kernel<C, NR, PAIR>, a, maps, static_cast<int>(dense_q), parts, joins);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -880,11 +947,10 @@ cudaError_t launch_t(const LatentAttnArgs& a, int G, cudaStream_t st) {
 template <int C>
 cudaError_t launch_c(const LatentAttnArgs& a, cudaStream_t st) {
     const long long rows = static_cast<long long>(a.b.max_q) * a.n_heads;
-    const int G = rows > 64 ? 2 : 1;
     switch (rows_of_tile(rows)) {
-        case 16: return launch_t<C, 16>(a, G, st);
-        case 32: return launch_t<C, 32>(a, G, st);
-        default: return launch_t<C, 64>(a, G, st);
+        case 16: return launch_t<C, 16, false>(a, st);
+        case 32: return launch_t<C, 32, false>(a, st);
+        default: return rows > 64 ? launch_t<C, 64, true>(a, st) : launch_t<C, 64, false>(a, st);
     }
 }
 

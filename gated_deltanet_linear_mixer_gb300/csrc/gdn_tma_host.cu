@@ -57,12 +57,13 @@ bool make_tma_map_f32_2d(CUtensorMap* map, const void* base, uint64_t rows, uint
 }
 
 bool make_tma_map_bf16_3d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t planes,
-                          uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols, uint32_t box_rows) {
+                          uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols, uint32_t box_rows,
+                          uint32_t box_planes) {
     auto fn = encode_fn();
     if (!fn || cols == 0 || rows == 0 || planes == 0) return false;
     cuuint64_t dims[3] = {cols, rows, planes};
     cuuint64_t strides[2] = {2 * row_pitch, 2 * plane_pitch};
-    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t box[3] = {box_cols, box_rows, box_planes};
     cuuint32_t elem_strides[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem_strides,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,

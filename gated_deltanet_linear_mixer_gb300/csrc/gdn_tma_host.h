@@ -18,8 +18,9 @@ bool make_tma_map_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uin
 bool make_tma_map_f32_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                          uint64_t pitch_elems, uint32_t box_rows, uint32_t box_cols);
 // A 3-D bf16 array [planes, rows, cols], cols contiguous, with row and plane pitches in elements
-// (in any order of size), read in boxes of one plane's box_rows x box_cols with the 128-byte swizzle.
+// (in any order of size), read in boxes of box_planes x box_rows x box_cols with the 128-byte swizzle.
 bool make_tma_map_bf16_3d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t planes,
-                          uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols, uint32_t box_rows);
+                          uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols, uint32_t box_rows,
+                          uint32_t box_planes);
 
 }  // namespace gdn
