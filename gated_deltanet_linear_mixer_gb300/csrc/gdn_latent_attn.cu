@@ -775,10 +775,10 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     }
 }
 
-// Joins the pieces of row tiles that were split: tasks of one row and 128 channels,
-// by a warp each where pieces are few, else by a thread block whose warps take
-// every eighth piece.
-constexpr int kJoinThreads = 256, kJoinBlocks = 6 * kSms, kChunk = 8;
+// Joins the pieces of row tiles that were split.  Where every row has at most
+// kFew pieces, a warp joins a row; else a thread block joins 128 channels of a
+// row, each of its warps every eighth piece.
+constexpr int kJoinThreads = 256, kJoinBlocks = 6 * kSms, kFew = 8;
 template <int C, int NR>
 __global__ void __launch_bounds__(kJoinThreads)
 latent_join_kernel(const LatentAttnArgs a, const float* parts, const Join* joins, const int n_joins, const int G) {
@@ -791,59 +791,117 @@ latent_join_kernel(const LatentAttnArgs a, const float* parts, const Join* joins
     __shared__ float2 stat[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int n = 0, in;
+    int n = 0;
     bool many = false;
     if (tid < n_joins) {  // rows of each, and of those before it
         const Join j = joins[tid];
         list[tid] = j;
         n = j.n_pieces > 0 ? j.n_rows : 0;
-        many = j.n_pieces > kChunk;
+        many = j.n_pieces > kFew;
     }
-    in = n;
+    int in = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, in, off);
         if (lane >= off) in += x;
     }
     if (lane == 31) warps[warp] = in;
-    const bool alone = !__syncthreads_or(many);  // a warp a task
+    const bool few = !__syncthreads_or(many);
     for (int w = 0; w < warp; ++w) in += warps[w];
     begin[tid + 1] = in;
     if (tid == 0) begin[0] = 0;
     __syncthreads();
-    const int tasks = begin[kJoinThreads] * kCols;
-    const int step = alone ? gridDim.x * kWarps : gridDim.x, first = alone ? warp * gridDim.x + blockIdx.x : blockIdx.x;
-    for (int task = first; task < tasks; task += step) {
-        const int r_all = task / kCols, col = task % kCols * 128 + 4 * lane;
-        int lo = 0, hi = n_joins - 1;  // the last join that begins at or before the row
-        while (lo < hi) {
+    const int rows = begin[kJoinThreads];
+
+    Join j{0, 0, 0, 0};
+    const float* base = nullptr;  // the first piece's results
+    size_t gap = 0;               // from the first following piece's to the next one's
+    const float* next = nullptr;  // the first following piece's: the next span's first slot
+    auto find = [&](int r) {      // row r of all joins; its number within its own
+        int lo = 0, hi = n_joins - 1;
+        while (lo < hi) {         // the last join that begins at or before it
             const int mid = (lo + hi + 1) >> 1;
-            if (begin[mid] <= r_all) lo = mid;
+            if (begin[mid] <= r) lo = mid;
             else hi = mid - 1;
         }
-        const Join j = list[lo];
-        const int row = r_all - begin[lo], g = lo % G;
-        auto part = [&](int p) {  // the first piece's slot, then the following spans' first ones
-            const int slot = p == 0 ? j.slot : 2 * (j.slot / 2 + p);
-            return parts + (static_cast<size_t>(slot) * G + g) * L::kPart;
-        };
-        const int by = alone ? 1 : kWarps;
+        j = list[lo];
+        const int g = lo % G;
+        base = parts + (static_cast<size_t>(j.slot) * G + g) * L::kPart;
+        next = parts + (static_cast<size_t>(2 * (j.slot / 2 + 1)) * G + g) * L::kPart;
+        gap = 2 * static_cast<size_t>(G) * L::kPart;
+        return r - begin[lo];
+    };
+    auto part = [&](int p) { return p == 0 ? base : next + (p - 1) * gap; };
+    auto store = [&](int row, int col, float4 x, float inv) {
+        *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (static_cast<size_t>(j.out_row) + row) * C + col) =
+            make_uint2(pack_bf16_pair(x.x * inv, x.y * inv), pack_bf16_pair(x.z * inv, x.w * inv));
+    };
+    auto add = [](float4& x, float4 v, float w) {
+        x.x = fmaf(v.x, w, x.x);
+        x.y = fmaf(v.y, w, x.y);
+        x.z = fmaf(v.z, w, x.z);
+        x.w = fmaf(v.w, w, x.w);
+    };
+
+    if (few) {
+        for (int r = warp * gridDim.x + blockIdx.x; r < rows; r += gridDim.x * kWarps) {
+            const int row = find(r);
+            float m = -INFINITY, l = 0.0f;
+            if (lane < j.n_pieces) {
+                m = part(lane)[NR * C + row];
+                l = part(lane)[NR * C + NR + row];
+            }
+            float4 first[kCols], x[kCols];
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) first[c] = reinterpret_cast<const float4*>(base + static_cast<size_t>(row) * C)[32 * c + lane];
+            float top = m;
+#pragma unroll
+            for (int off = kFew / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            // a piece that saw no key has a sum of 0, and its outputs were not written
+            const float w = l == 0.0f ? 0.0f : exp2_ftz(m - (top == -INFINITY ? 0.0f : top));
+            float total = l == 0.0f ? 0.0f : l * w;
+#pragma unroll
+            for (int off = kFew / 2; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+            total = __shfl_sync(0xffffffffu, total, 0);
+            const unsigned seen = __ballot_sync(0xffffffffu, l != 0.0f);
+            const float w0 = __shfl_sync(0xffffffffu, w, 0);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                x[c] = make_float4(0, 0, 0, 0);
+                if (seen & 1u) add(x[c], first[c], w0);
+            }
+#pragma unroll 2
+            for (int p = 1; p < j.n_pieces; ++p) {
+                const float wp = __shfl_sync(0xffffffffu, w, p);
+                if (!(seen >> p & 1u)) continue;
+                const float4* v = reinterpret_cast<const float4*>(part(p) + static_cast<size_t>(row) * C);
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) add(x[c], v[32 * c + lane], wp);
+            }
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) store(row, 128 * c + 4 * lane, x[c], inv);
+        }
+        return;
+    }
+    for (int task = blockIdx.x; task < rows * kCols; task += gridDim.x) {
+        const int row = find(task / kCols), col = task % kCols * 128 + 4 * lane;
         float m = -INFINITY, l = 0.0f;
         float4 x = make_float4(0, 0, 0, 0);
-        for (int p0 = alone ? 0 : warp; p0 < j.n_pieces; p0 += kChunk * by) {
-            float4 v[kChunk];  // all loads of a chunk at once
-            const int mine = p0 + lane * by;
+        for (int p0 = warp; p0 < j.n_pieces; p0 += kFew * kWarps) {
+            float4 v[kFew];  // all loads of a chunk at once
+            const int mine = p0 + lane * kWarps;
             float pm = -INFINITY, pl = 0.0f;
-            if (lane < kChunk && mine < j.n_pieces) {
+            if (lane < kFew && mine < j.n_pieces) {
                 pm = part(mine)[NR * C + row];
                 pl = part(mine)[NR * C + NR + row];
             }
 #pragma unroll
-            for (int k = 0; k < kChunk; ++k)
-                if (p0 + k * by < j.n_pieces) v[k] = *reinterpret_cast<const float4*>(part(p0 + k * by) + static_cast<size_t>(row) * C + col);
+            for (int k = 0; k < kFew; ++k)
+                if (p0 + k * kWarps < j.n_pieces) v[k] = *reinterpret_cast<const float4*>(part(p0 + k * kWarps) + static_cast<size_t>(row) * C + col);
             float top = fmaxf(m, pm);
 #pragma unroll
-            for (int off = kChunk / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            for (int off = kFew / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             top = __shfl_sync(0xffffffffu, top, 0);
             const float ref = top == -INFINITY ? 0.0f : top, f = m == -INFINITY ? 0.0f : exp2_ftz(m - ref);
             const float w = exp2_ftz(pm - ref);
@@ -851,43 +909,32 @@ latent_join_kernel(const LatentAttnArgs a, const float* parts, const Join* joins
             x.x *= f; x.y *= f; x.z *= f; x.w *= f;
             m = top;
 #pragma unroll
-            for (int k = 0; k < kChunk; ++k) {
+            for (int k = 0; k < kFew; ++k) {
                 const float lk = __shfl_sync(0xffffffffu, pl, k), wk = __shfl_sync(0xffffffffu, w, k);
-                if (lk != 0.0f) {  // else it saw no key, and its outputs were not written
+                if (lk != 0.0f) {
                     l = fmaf(lk, wk, l);
-                    x.x = fmaf(v[k].x, wk, x.x);
-                    x.y = fmaf(v[k].y, wk, x.y);
-                    x.z = fmaf(v[k].z, wk, x.z);
-                    x.w = fmaf(v[k].w, wk, x.w);
+                    add(x, v[k], wk);
                 }
             }
         }
-        if (!alone) {
-            sum[warp][lane] = x;
-            if (lane == 0) stat[warp] = make_float2(m, l);
-            __syncthreads();
+        sum[warp][lane] = x;
+        if (lane == 0) stat[warp] = make_float2(m, l);
+        __syncthreads();
+        if (warp == 0) {
             float top = -INFINITY;
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w].x);
             const float ref = top == -INFINITY ? 0.0f : top;
             l = 0.0f;
             x = make_float4(0, 0, 0, 0);
             for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2_ftz(stat[w].x - ref);
                 if (stat[w].y == 0.0f) continue;
-                const float4 v = sum[w][lane];
+                const float f = exp2_ftz(stat[w].x - ref);
                 l = fmaf(stat[w].y, f, l);
-                x.x = fmaf(v.x, f, x.x);
-                x.y = fmaf(v.y, f, x.y);
-                x.z = fmaf(v.z, f, x.z);
-                x.w = fmaf(v.w, f, x.w);
+                add(x, sum[w][lane], f);
             }
-            __syncthreads();
+            store(row, col, x, l == 0.0f ? 0.0f : 1.0f / l);
         }
-        if (alone || warp == 0) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (static_cast<size_t>(j.out_row) + row) * C + col) =
-                make_uint2(pack_bf16_pair(x.x * inv, x.y * inv), pack_bf16_pair(x.z * inv, x.w * inv));
-        }
+        __syncthreads();
     }
 }
 
