@@ -43,20 +43,27 @@ constexpr uint32_t kBlock = 16384;  // 128 rows x 64 channels
 constexpr uint32_t kSmemMax = 232448, kSharedBytes = 3072;
 constexpr int kMaxSlots = 12;
 
-template <int NOPE, int V> struct ECfg {
-    static constexpr int kQBlocks = NOPE / 64 + 1, kVBlocks = V / 64, kPer = kQBlocks + kVBlocks;  // blocks of a key tile
-    static constexpr uint32_t kQ = kQBlocks * kBlock;  // a query tile
-    static constexpr int kPitch = 2 * V + 16;          // of a staged output row: neighbours in different banks
+// PAIR: a thread block of a pair holds half of a key tile's keys (as keys) and half of its values' channels.
+template <int NOPE, int V, bool PAIR> struct ECfg {
+    static constexpr int kQBlocks = NOPE / 64 + 1;                     // of 64 channels
+    static constexpr uint32_t kQ = kQBlocks * kBlock;                  // a query tile
+    static constexpr uint32_t kKBlock = PAIR ? kBlock / 2 : kBlock;    // a key tile's 64 channels
+    static constexpr uint32_t kVTile = kKeys * V * 2 / (PAIR ? 2 : 1);
+    static constexpr int kPitch = 2 * V + 16;                          // of a staged output row: neighbours in different banks
     static constexpr uint32_t kStaged = (kM * kPitch + 1023) / 1024 * 1024, kPlace = kQ > kStaged ? kQ : kStaged;
-    static constexpr int kFit = (kSmemMax - kSharedBytes - kTiles * kPlace) / kBlock;
-    static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
-    static constexpr uint32_t kQAt = kSlots * kBlock, kSharedAt = kQAt + kTiles * kPlace, kSmem = kSharedAt + kSharedBytes;
-    static constexpr uint32_t kOut = kTiles * kKeys;   // tensor memory: scores (weights) of both tiles, outputs
-    static_assert(kSlots >= kPer + kQBlocks, "a tile and the next tile's keys fit");
+    static constexpr uint32_t kRoom = kSmemMax - kSharedBytes - kTiles * kPlace;
+    static constexpr int kFit = kRoom / (kQBlocks * kKBlock + kVTile), NV = kFit < 2 ? 2 : kFit;  // slots of value tiles
+    static constexpr int kFitK = (kRoom - NV * kVTile) / kKBlock, NK = kFitK < kMaxSlots ? kFitK : kMaxSlots;  // of key blocks
+    static constexpr uint32_t kVAt = NK * kKBlock, kQAt = kVAt + NV * kVTile, kSharedAt = kQAt + kTiles * kPlace;
+    static constexpr uint32_t kSmem = kSharedAt + kSharedBytes;
+    static constexpr uint32_t kOut = kTiles * kKeys;                   // tensor memory: scores (weights) of both tiles, outputs
+    static constexpr int kRows = PAIR ? 2 * kM : kM;                   // of a product
+    static_assert(NK > kQBlocks, "a tile's keys and the next one's first fit");
+    static_assert(NV <= kMaxSlots && (!PAIR || V == 128), "a half of the channels is a 128-byte row");
 };
 
 struct Shared {
-    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
     uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles], pv_done[kTiles], drained;
     uint32_t tmem_slot;
 };
@@ -118,28 +125,48 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// The same by a pair of thread blocks: 128 rows of A and half of B's N from each.
+__device__ __forceinline__ void mma_bf16_ta_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// mbar_wait_brief that acquires at cluster scope.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const long long c0 = clock64();
+    for (uint32_t n = 1; !mbar_try_wait_cluster(bar, parity); ++n)
+        if ((n & 255u) == 0 && clock64() - c0 > (1ll << 32)) return false;
+    return true;
+}
+
 struct Maps {
     CUtensorMap q, k, r, v;
 };
 
-template <int NOPE, int V>
+template <int NOPE, int V, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArgs a, const __grid_constant__ Maps maps) {
-    using L = ECfg<NOPE, V>;
-    constexpr int NS = L::kSlots, QB = L::kQBlocks, VB = L::kVBlocks;
+    using L = ECfg<NOPE, V, PAIR>;
+    constexpr int NK = L::NK, NV = L::NV, QB = L::kQBlocks;
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem + L::kSharedAt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x, seq = blockIdx.y;
+    const int rank = PAIR ? static_cast<int>(blockIdx.x & 1) : 0;
+    const int h = PAIR ? blockIdx.x >> 1 : blockIdx.x, seq = blockIdx.y;
     const int q0 = a.cu_q[seq], qn = a.cu_q[seq + 1] - q0, k0 = a.cu_kv[seq], kv = a.cu_kv[seq + 1] - k0;
-    const int row0 = (static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z)) * (kTiles * kM);  // most keys first
+    // most keys first; tile t of a thread block: rows row0 + t kRows + rank kM onwards
+    const int row0 = (static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z)) * (kTiles * L::kRows);
     if (row0 >= qn) return;
     const int start = kv - qn;  // position of the sequence's first query
-    int n[kTiles];              // key tiles of each query tile
+    int n[kTiles];              // key tiles of each query tile (of a pair's both)
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-        const int rows = min(kM, qn - row0 - t * kM);
-        n[t] = rows > 0 ? max(0, (start + row0 + t * kM + rows - 1) / kKeys + 1) : 0;
-        if (start + row0 + t * kM + rows - 1 < 0) n[t] = 0;
+        const int last = min(row0 + (t + 1) * L::kRows, qn) - 1;  // the tile's last query
+        n[t] = last >= row0 + t * L::kRows && start + last >= 0 ? (start + last) / kKeys + 1 : 0;
     }
     const int n_tiles = max(n[0], n[1]);
     if (smem_u32(smem) & 1023u) {
@@ -147,38 +174,52 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(&sh.k_full[i], 1);
+            mbar_init(&sh.k_empty[i], 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&sh.v_full[i], 1);
+            mbar_init(&sh.v_empty[i], 1);
         }
         for (int t = 0; t < kTiles; ++t) {
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_full[t], 4);
+            mbar_init(&sh.p_full[t], PAIR ? 8 : 4);
             mbar_init(&sh.pv_done[t], 1);
         }
         mbar_init(&sh.drained, 1);
         fence_barrier_init();
     }
-    if (warp == 9) tmem_alloc(&sh.tmem_slot, 512);
+    if (warp == 9) {
+        if (PAIR) tmem_alloc_pair(&sh.tmem_slot, 512);
+        else tmem_alloc(&sh.tmem_slot, 512);
+    }
     tc_fence_before_sync();
     __syncthreads();
+    if (PAIR) {  // the other's barriers are initialised
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem_slot;
 
     if (warp < 8) {
         // ---- softmax: a thread's row
-        const int t = warp >> 2, r = tid & (kM - 1), row = row0 + t * kM + r;
+        const int t = warp >> 2, r = tid & (kM - 1), row = row0 + t * L::kRows + rank * kM + r;
         const bool mine = row < qn;
         const int lim = mine ? max(0, min(start + row + 1, kv)) : 0;  // keys that the row sees
         const int low = __reduce_min_sync(0xffffffffu, lim);
         const uint32_t t_lane = (32u * (warp & 3)) << 16;
         const uint32_t t_score = tmem + t_lane + t * kKeys, t_out = tmem + t_lane + L::kOut + t * V;
+        const uint32_t p_full = PAIR ? map_to_rank(smem_u32(&sh.p_full[t]), 0) : 0;
         const float scale2 = a.scale * kLog2e;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int i = 0; i < n[t]; ++i) {
             const int key0 = i * kKeys;
+            // A wait that gave up is not waited for again, but the warp goes on through the tiles (with
+            // results that are invalid): the barriers between the warps stay complete.
             if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_full[t], i & 1))) && lane == 0) record(a.error, 60);
             tc_fence_after_sync();
             float s[kKeys];
@@ -236,12 +277,13 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             }
             // rows behind the sequence's last key may be anything: weights of 0 do not undo a NaN.  By the
             // first of the tiles that use them.
-            if (key0 + kKeys > kv && (t == 0 || i >= n[0])) {
-                for (int b = 0; b < VB; ++b) {
-                    const uint32_t fill = i * L::kPer + QB + b, slot = fill % NS;
-                    if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.full[slot], (fill / NS) & 1))) && lane == 0)
-                        record(a.error, 62);
-                    uint4* rows = reinterpret_cast<uint4*>(smem + slot * kBlock);
+            const bool cleared = key0 + kKeys > kv && (t == 0 || i >= n[0]);
+            if (cleared) {
+                const int slot = i % NV;
+                if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.v_full[slot], rank ? 0 : (i / NV) & 1))) && lane == 0)
+                    record(a.error, 62);  // (the second block's only ones on its own barrier)
+                for (uint32_t b = 0; b < L::kVTile; b += kBlock) {
+                    uint4* rows = reinterpret_cast<uint4*>(smem + L::kVAt + slot * L::kVTile + b);
                     for (int x = 8 * (kv - key0) + r; x < 8 * kKeys; x += kM) rows[x] = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
@@ -249,7 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[t]);
+            if (lane == 0) {
+                // Weights are in tensor memory by now; only zeroed rows, in shared memory, are to be released (a
+                // releasing arrival on the other thread block's barrier takes some 1500 cycles).
+                if (!PAIR) mbar_arrive(&sh.p_full[t]);
+                else if (cleared) mbar_arrive_remote(p_full);
+                else mbar_arrive_remote_relaxed(p_full, l);
+            }
         }
         // ---- epilogue: through the query tile's place, whose products are done, so that a row leaves as one piece
         if (n[t] > 0 && ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pv_done[t], (n[t] - 1) & 1))) && lane == 0)
@@ -276,138 +324,197 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             bulk_wait_read();
         }
     } else if (warp == 8) {
-        // ---- loads
+        // ---- loads: of a pair the first thread block's keys are the tile's first half, its values the first channels
         const bool leader = elect_one();
         const int hq = a.q.head_stride ? h : 0, hk = a.k.head_stride ? h : 0, hv = a.v.head_stride ? h : 0;
+        // The products' issuer, in a pair's first thread block, waits for both blocks' bytes on a barrier of its
+        // own.  But the second block's values behind a sequence's end wait for its softmax, which clears them.
+        const uint32_t both = PAIR ? 2 : 1;
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, bool here) {
+            if (!PAIR || here) tma_load_3d(dst, map, bar, x, y, z);
+            else tma_load_3d_pair(dst, map, map_to_rank(smem_u32(bar), 0), x, y, z);
+        };
         bool ok = true;
-        uint32_t fills = 0;
+        uint32_t fills = 0;  // of key blocks
+        int i = 0;
         if (leader && n_tiles > 0) {
             for (int t = 0; t < kTiles; ++t) {
                 if (n[t] == 0) continue;
-                mbar_arrive_expect_tx(&sh.q_full[t], L::kQ);
+                if (rank == 0) mbar_arrive_expect_tx(&sh.q_full[t], both * L::kQ);
                 for (int b = 0; b < QB; ++b)
-                    tma_load_3d(smem + L::kQAt + t * L::kPlace + b * kBlock, &maps.q, &sh.q_full[t], 64 * b, q0 + row0 + t * kM, hq);
+                    load(smem + L::kQAt + t * L::kPlace + b * kBlock, &maps.q, &sh.q_full[t], 64 * b,
+                         q0 + row0 + t * L::kRows + rank * kM, hq, false);
             }
         }
         __syncwarp();
-        for (int i = 0; ok && i < n_tiles; ++i) {
-            const int key = k0 + i * kKeys;
-            for (int b = 0; b < L::kPer; ++b, ++fills) {
-                const uint32_t slot = fills % NS;
-                if (fills >= NS && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.empty[slot], (fills / NS - 1) & 1)))) break;
+        for (; i < n_tiles; ++i) {
+            const int key = k0 + i * kKeys, slot_v = i % NV;
+            for (int b = 0; ok && b < QB; ++b) {
+                const uint32_t slot = fills % NK;
+                if (fills >= NK && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.k_empty[slot], (fills / NK - 1) & 1)))) break;
+                ++fills;
                 if (leader) {
-                    uint8_t* dst = smem + slot * kBlock;
-                    mbar_arrive_expect_tx(&sh.full[slot], kBlock);
-                    if (b < QB - 1) tma_load_3d(dst, &maps.k, &sh.full[slot], 64 * b, key, hk);
-                    else if (b == QB - 1) tma_load_2d(dst, &maps.r, &sh.full[slot], 0, key);
-                    else tma_load_3d(dst, &maps.v, &sh.full[slot], 64 * (b - QB), key, hv);
+                    uint8_t* dst = smem + slot * L::kKBlock;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.k_full[slot], both * L::kKBlock);
+                    if (b < QB - 1) load(dst, &maps.k, &sh.k_full[slot], 64 * b, key + rank * (kKeys / 2), hk, false);
+                    else load(dst, &maps.r, &sh.k_full[slot], 0, key + rank * (kKeys / 2), 0, false);
                 }
                 __syncwarp();
             }
+            if (ok && i >= NV) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.v_empty[slot_v], (i / NV - 1) & 1));
+            if (!ok) break;
+            if (leader) {
+                uint8_t* dst = smem + L::kVAt + slot_v * L::kVTile;
+                const bool own = PAIR && (i + 1) * kKeys > kv;  // each block waits for its own
+                if (rank == 0 || own) mbar_arrive_expect_tx(&sh.v_full[slot_v], (own ? 1 : both) * L::kVTile);
+                for (uint32_t b = 0; b < L::kVTile / kBlock; ++b)
+                    load(dst + b * kBlock, &maps.v, &sh.v_full[slot_v], 64 * (b + rank), key, hv, own);
+            }
+            __syncwarp();
         }
-        if (!ok && lane == 0) record(a.error, 64);
         // nothing is in flight when the memory is given back
-        for (int t = 0; t < kTiles; ++t)
-            if (n[t] > 0) mbar_wait_brief(&sh.q_full[t], 0);
-        for (uint32_t s = 0; s < NS; ++s)
-            if (fills > s) mbar_wait_brief(&sh.full[s], ((fills - 1 - s) / NS) & 1);
-    } else if (warp == 9) {
-        // ---- products
+        if (!ok) {
+            if (lane == 0) record(a.error, 64);
+            if (rank == 0) {
+                for (uint32_t f = fills > NK ? fills - NK : 0; f < fills; ++f) mbar_wait_brief(&sh.k_full[f % NK], (f / NK) & 1);
+                for (int f = max(0, i - NV); f < i; ++f) mbar_wait_brief(&sh.v_full[f % NV], (f / NV) & 1);
+            } else {  // its bytes are counted in the other block: a millisecond will do
+                const uint64_t t0 = globaltimer_ns();
+                const long long c0 = clock64();
+                while (globaltimer_ns() - t0 < 1000000 && clock64() - c0 < (1ll << 24)) {}
+            }
+        }
+        if (rank == 0)
+            for (int t = 0; t < kTiles; ++t)
+                if (n[t] > 0) mbar_wait_brief(&sh.q_full[t], 0);
+    } else if (warp == 9 && rank == 0) {
+        // ---- products (of a pair by its first thread block)
         const bool leader = elect_one();
-        constexpr uint32_t id_s = idesc_bf16_f32(kM, kKeys), id_o = idesc_bf16_f32(kM, 64, false, true);
+        constexpr uint32_t id_s = idesc_bf16_f32(L::kRows, kKeys), id_o = idesc_bf16_f32(L::kRows, V, false, true);
         const uint64_t dq = desc_kmajor_sw128(smem_u32(smem + L::kQAt)), dk = desc_kmajor_sw128(smem_u32(smem)),
-                       dv = desc_mnmajor_sw128(smem_u32(smem), kBlock);
-        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_brief(bar, parity)) != 0; };
+                       dv = desc_mnmajor_sw128(smem_u32(smem + L::kVAt), kBlock);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, PAIR ? wait_cluster(bar, parity) : mbar_wait_brief(bar, parity)) != 0;
+        };
+        auto commit = [&](uint64_t* bar) {
+            if (PAIR) mma_commit_pair(bar, 3);
+            else mma_commit(bar);
+        };
         bool ok = true;
         // scores of tile t and key tile i; the last tile that uses a block gives it back
         auto scores = [&](int t, int i, bool give) {
-            for (int b = 0; ok && b < QB; ++b) {
-                const uint32_t fill = i * L::kPer + b, slot = fill % NS;
-                if (!(ok = wait(&sh.full[slot], (fill / NS) & 1))) return;
+            for (int b = 0; b < QB; ++b) {
+                const uint32_t fill = i * QB + b, slot = fill % NK;
+                if (!(ok = wait(&sh.k_full[slot], (fill / NK) & 1))) return;
                 tc_fence_after_sync();
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + t * kKeys, dq + ((t * L::kPlace + b * kBlock) >> 4) + 2 * k, dk + (slot * kBlock >> 4) + 2 * k,
-                                 id_s, (b > 0 || k > 0) ? 1u : 0u);
-                    if (give) mma_commit(&sh.empty[slot]);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t da = dq + ((t * L::kPlace + b * kBlock) >> 4) + 2 * k, db = dk + (slot * L::kKBlock >> 4) + 2 * k;
+                        if (PAIR) mma_bf16_pair(tmem + t * kKeys, da, db, id_s, (b > 0 || k > 0) ? 1u : 0u);
+                        else mma_bf16(tmem + t * kKeys, da, db, id_s, (b > 0 || k > 0) ? 1u : 0u);
+                    }
+                    if (give) commit(&sh.k_empty[slot]);
                 }
                 __syncwarp();
             }
-            if (leader) mma_commit(&sh.s_full[t]);
+            if (leader) commit(&sh.s_full[t]);
             __syncwarp();
         };
         for (int t = 0; ok && t < kTiles; ++t)
             if (n[t] > 0) {
                 if (!(ok = wait(&sh.q_full[t], 0))) break;
-                scores(t, 0, t == kTiles - 1 || n[t + 1 < kTiles ? t + 1 : t] == 0);
+                scores(t, 0, t == 1 || n[1] == 0);
             }
         for (int i = 0; ok && i < n_tiles; ++i) {
             for (int t = 0; ok && t < kTiles; ++t) {
                 if (i < n[t]) {
+                    const int slot = i % NV;
                     if (!(ok = wait(&sh.p_full[t], i & 1))) break;
-                    const bool give = t == 1 || i >= n[1];
-                    for (int b = 0; ok && b < VB; ++b) {
-                        const uint32_t fill = i * L::kPer + QB + b, slot = fill % NS;
-                        if (!(ok = wait(&sh.full[slot], (fill / NS) & 1))) break;
-                        tc_fence_after_sync();
-                        if (leader) {
+                    if (!(ok = wait(&sh.v_full[slot], (i / NV) & 1))) break;
+                    tc_fence_after_sync();
+                    if (leader) {
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)  // 16 keys of weights are 8 columns
-                                mma_bf16_ta(tmem + L::kOut + t * V + 64 * b, tmem + t * kKeys + 8 * k,
-                                            dv + ((slot * kBlock + k * 2048) >> 4), id_o, (i > 0 || k > 0) ? 1u : 0u);
-                            if (give) mma_commit(&sh.empty[slot]);
+                        for (int k = 0; k < kKeys / 16; ++k) {  // 16 keys of weights are 8 columns
+                            const uint32_t d = tmem + L::kOut + t * V, p = tmem + t * kKeys + 8 * k;
+                            const uint64_t db = dv + ((slot * L::kVTile + k * 2048) >> 4);
+                            if (PAIR) mma_bf16_ta_pair(d, p, db, id_o, (i > 0 || k > 0) ? 1u : 0u);
+                            else mma_bf16_ta(d, p, db, id_o, (i > 0 || k > 0) ? 1u : 0u);
                         }
-                        __syncwarp();
+                        if (t == 1 || i >= n[1]) commit(&sh.v_empty[slot]);
+                        commit(&sh.pv_done[t]);
                     }
-                    if (leader) mma_commit(&sh.pv_done[t]);
                     __syncwarp();
                 }
                 if (ok && i + 1 < n[t]) scores(t, i + 1, t == 1 || i + 1 >= n[1]);
             }
         }
         if (!ok && lane == 0) record(a.error, 65);
-        if (leader) mma_commit(&sh.drained);
+        if (leader) {
+            if (PAIR) mma_commit_pair(&sh.drained, 1);
+            else mma_commit(&sh.drained);
+        }
         mbar_wait_brief(&sh.drained, 0);
     }
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
+    if (PAIR) {  // nothing of the other is on its way here any more, and both are done with tensor memory
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after_sync();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 9) {
+        if (PAIR) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
+    }
 }
 
-// A map of rows [tokens, heads, width] in boxes of 128 tokens x 64 channels of a head.
-bool map_rows(CUtensorMap* map, const KvRows& r, int tokens, int heads, int width) {
+// A map of rows [tokens, heads, width] in boxes of `box` tokens x 64 channels of a head.
+bool map_rows(CUtensorMap* map, const KvRows& r, int tokens, int heads, int width, int box) {
     return make_tma_map_bf16_3d(map, r.data, width, tokens, r.head_stride ? heads : 1, r.token_stride,
-                                r.head_stride ? r.head_stride : r.token_stride, 64, 128, 1);
+                                r.head_stride ? r.head_stride : r.token_stride, 64, box, 1);
 }
 
-template <int NOPE, int V>
+template <int NOPE, int V, bool PAIR>
 cudaError_t expanded_t(const ExpandedArgs& a, cudaStream_t st) {
-    using L = ECfg<NOPE, V>;
+    using L = ECfg<NOPE, V, PAIR>;
     static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = allow_smem(expanded_kernel<NOPE, V>, L::kSmem, ready);
+    cudaError_t e = allow_smem(expanded_kernel<NOPE, V, PAIR>, L::kSmem, ready);
     if (e != cudaSuccess) return e;
     Maps maps{};
+    const int keys = PAIR ? kKeys / 2 : kKeys;
     if (a.n_kv > 0 &&
-        !(map_rows(&maps.q, a.q, a.n_q, a.n_heads, NOPE + kRopeDim) && map_rows(&maps.k, a.k, a.n_kv, a.n_heads, NOPE) &&
-          make_tma_map_bf16_2d(&maps.r, a.k_rope.data, a.n_kv, kRopeDim, a.k_rope.token_stride, 128, 64) &&
-          map_rows(&maps.v, a.v, a.n_kv, a.n_heads, V)))
+        !(map_rows(&maps.q, a.q, a.n_q, a.n_heads, NOPE + kRopeDim, kM) && map_rows(&maps.k, a.k, a.n_kv, a.n_heads, NOPE, keys) &&
+          map_rows(&maps.r, KvRows{a.k_rope.data, a.k_rope.token_stride, 0}, a.n_kv, 1, kRopeDim, keys) &&
+          map_rows(&maps.v, a.v, a.n_kv, a.n_heads, V, kKeys)))
         return cudaErrorInvalidValue;
-    const int tiles = (a.max_q + kTiles * kM - 1) / (kTiles * kM);
+    const int tiles = (a.max_q - 1) / (kTiles * L::kRows) + 1;
     if (tiles > 65535) return cudaErrorInvalidConfiguration;
-    return timed_launch("expanded_attention", st, [&] {
-        expanded_kernel<NOPE, V><<<dim3(a.n_heads, a.n_seq, tiles), kThreads, L::kSmem, st>>>(a, maps);
-        return cudaGetLastError();
-    });
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.n_heads * (PAIR ? 2 : 1), a.n_seq, tiles);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute two{};
+    two.id = cudaLaunchAttributeClusterDimension;
+    two.val.clusterDim.x = 2;
+    two.val.clusterDim.y = two.val.clusterDim.z = 1;
+    cfg.attrs = &two;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return timed_launch("expanded_attention", st, [&] { return cudaLaunchKernelEx(&cfg, expanded_kernel<NOPE, V, PAIR>, a, maps); });
+}
+
+template <int NOPE>
+cudaError_t expanded_n(const ExpandedArgs& a, int v_dim, cudaStream_t st) {
+    if (v_dim == 64) return expanded_t<NOPE, 64, false>(a, st);
+    return a.max_q > kTiles * kM ? expanded_t<NOPE, 128, true>(a, st) : expanded_t<NOPE, 128, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_expanded_attention(const ExpandedArgs& a, int nope_dim, int v_dim, cudaStream_t st) {
-    if (nope_dim == 128) return v_dim == 128 ? expanded_t<128, 128>(a, st) : expanded_t<128, 64>(a, st);
-    return v_dim == 128 ? expanded_t<64, 128>(a, st) : expanded_t<64, 64>(a, st);
+    return nope_dim == 128 ? expanded_n<128>(a, v_dim, st) : expanded_n<64>(a, v_dim, st);
 }
 
 }  // namespace gdn

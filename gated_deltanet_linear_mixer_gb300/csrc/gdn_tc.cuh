@@ -139,6 +139,14 @@ __device__ __forceinline__ void tma_load_3d_multicast(void* smem_dst, const CUte
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"(cta_mask)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar_addr,
+                                                 int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar_addr)
+        : "memory");
+}
 // 2-D tiled bulk tensor store shared -> global of one box, tracked by the
 // issuing thread's bulk-async group (commit with bulk_commit, then wait).
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src,

@@ -359,6 +359,9 @@ def _kv(counts_kv, heads, nope, vd, seed, fused, shared=False):
     (20, 128, 128, True, [33], [1000]),
     (2, 128, 128, False, [600], [600]),
     (2, 128, 128, True, [257, 300], [513, 300]),
+    (3, 64, 128, True, [300, 0, 513, 70], [300, 5, 700, 1000]),
+    (1, 128, 128, False, [1030], [1030]),
+    (2, 128, 128, True, [512, 256, 1], [640, 320, 64]),
     (16, 128, 128, True, [1] * 12, [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 700]),
 ])
 def test_expanded_attention(heads, nope, vd, fused, counts, lens):
@@ -378,10 +381,11 @@ def test_expanded_attention_of_one_shared_head():
     check(got, *expanded(d, [100], [150], q, k, r, v))
 
 
-def test_expanded_queries_that_see_nothing_and_sequences_side_by_side():
+@pytest.mark.parametrize("more", [0, 400])
+def test_expanded_queries_that_see_nothing_and_sequences_side_by_side(more):
     """More queries than keys; a neighbour's values that are no numbers do not come over."""
     d = gdn.LatentDims(4)
-    counts, lens = [10, 140, 3, 5], [4, 130, 0, 200]
+    counts, lens = [10, 140, 3, 5 + more], [4, 130, 0, 200 + more]
     k, r, v = _kv(lens, 4, 128, 128, 131, True)
     q = _queries(sum(counts), 4, 192, 132)
     want, tol = expanded(d, counts, lens, q, k, r, v)
