@@ -50,7 +50,7 @@ struct LatentAttnArgs {
 struct ExpandedArgs {
     int n_seq, n_heads;
     float scale;
-    const int32_t *cu_q, *cu_kv;
+    const int32_t *cu_q, *cu_kv, *cu_q_host, *cu_kv_host;
     int n_q, n_kv;  // cu_q[n_seq], cu_kv[n_seq]
     int max_q;      // longest sequence in queries
     KvRows q, k, k_rope, v;

@@ -248,6 +248,7 @@ gdn_status gdn_expanded_attention(const gdn_latent_dims* dims, int32_t n_seq, co
     if ((st = gdn::inject_fault("expanded_attention", fn)) != GDN_OK) return st;
     if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.n_heads = dims->n_heads; a.scale = dims->scale; a.cu_q = cu_q; a.cu_kv = cu_kv; a.out = out;
+    a.cu_q_host = cu_q_host; a.cu_kv_host = cu_kv_host;
     return cuda_status(gdn::launch_expanded_attention(a, dims->nope_dim, dims->v_dim, static_cast<cudaStream_t>(stream)), fn,
                        "attention launch");
 }

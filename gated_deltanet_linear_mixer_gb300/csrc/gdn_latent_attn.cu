@@ -211,6 +211,11 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     const int g_own = static_cast<int>(blockIdx.x) % G, span = static_cast<int>(blockIdx.x) / G;
     const int n_spans = static_cast<int>(gridDim.x) / G;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 7) {
+        tma_prefetch_desc(&maps.rows);
+        tma_prefetch_desc(&maps.pairs);
+        tma_prefetch_desc(&maps.q);
+    }
 
     // ---- this thread block's span of the (sequence, group, key tile) axis
     const int each = (a.b.n_seq + kThreads - 1) / kThreads;

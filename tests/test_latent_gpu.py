@@ -361,6 +361,10 @@ def _kv(counts_kv, heads, nope, vd, seed, fused, shared=False):
     (2, 128, 128, True, [257, 300], [513, 300]),
     (3, 64, 128, True, [300, 0, 513, 70], [300, 5, 700, 1000]),
     (1, 128, 128, False, [1030], [1030]),
+    (40, 128, 128, True, [3, 300, 1, 17, 128, 5] * 4, [3, 301, 77, 400, 128, 64] * 4),   # many items a thread block
+    (33, 64, 64, True, [9, 130, 1] * 9, [9, 131, 129] * 9),
+    (1, 128, 64, True, [1] * 1100, [(i * 37) % 200 for i in range(1100)]),               # more blocks than are listed
+    (1, 128, 128, True, [1] * 1100 + [300], [(i * 37) % 200 for i in range(1100)] + [310]),
     (2, 128, 128, True, [512, 256, 1], [640, 320, 64]),
     (16, 128, 128, True, [1] * 12, [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 700]),
 ])
