@@ -337,11 +337,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         for (int round = 0; ok && round < rounds; ++round) {
             Item x;
             if (!item_of(round, x)) continue;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {  // queries, once the products with the last ones are done
-                if (x.n[t] == 0) continue;
-                if (queries[t] > 0 && !(ok = ok && __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty[t], (queries[t] - 1) & 1)))) break;
-                ++queries[t];
+            auto load_queries = [&](int t) {  // once the products with the tile's last ones are done
+                if ((t ? x.n[1] : x.n[0]) == 0) return;
+                uint32_t& before = t ? queries[1] : queries[0];
+                if (before > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty[t], (before - 1) & 1)))) return;
+                ++before;
                 if (leader) {
                     mbar_arrive_expect_tx(&sh.q_full[t], L::kQ);
                     for (int b = 0; b < QB; ++b)
@@ -349,8 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                                     a.q.head_stride ? x.h : 0);
                 }
                 __syncwarp();
-            }
+            };
+            load_queries(0);
             for (int i = 0; ok && i < x.n_tiles; ++i) {
+                if (i == 1) load_queries(1);  // behind the first tile's first keys and values
+                if (!ok) break;
                 const int key = x.k0 + i * kKeys;
                 for (int b = 0; ok && b < QB; ++b) {
                     const uint32_t slot = keys % NK;
@@ -376,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                 }
                 __syncwarp();
             }
+            if (ok && x.n_tiles == 1) load_queries(1);
         }
         if (!ok) {  // nothing is in flight when the memory is given back
             if (lane == 0) record(a.error, 64);
