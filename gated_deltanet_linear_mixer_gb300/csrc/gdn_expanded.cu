@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         mbar_init(&sh.drained, 1);
         fence_barrier_init();
     }
-    if (warp == 8) {
+    if (warp == 8 && a.n_kv > 0) {
         tma_prefetch_desc(&plan.q);
         tma_prefetch_desc(&plan.k);
         tma_prefetch_desc(&plan.r);

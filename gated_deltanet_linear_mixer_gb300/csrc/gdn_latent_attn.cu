@@ -51,7 +51,6 @@ constexpr int kKeys = 64;        // of a tile
 constexpr int kRopes = 2;        // slots of position keys
 constexpr int kThreads = 256;
 constexpr float kLazy = 8.0f;
-constexpr int kMinSpan = 1;      // key tiles of a span at least
 constexpr int kPieces = 16;      // pieces of a span that are laid out at a time
 constexpr int kMasks = 8;
 constexpr int kMaxSlots = 12;
@@ -212,9 +211,11 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     const int n_spans = static_cast<int>(gridDim.x) / G;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 7) {
-        tma_prefetch_desc(&maps.rows);
-        tma_prefetch_desc(&maps.pairs);
-        tma_prefetch_desc(&maps.q);
+        if (a.c.n_pages > 0) {
+            tma_prefetch_desc(&maps.rows);
+            tma_prefetch_desc(&maps.pairs);
+        }
+        if (dense_q) tma_prefetch_desc(&maps.q);
     }
 
     // ---- this thread block's span of the (sequence, group, key tile) axis
@@ -234,7 +235,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
         if (lane >= off) u_in += u;
     }
     if (lane == 31) sh.scan[warp] = u_in;
-    if (tid == 0) {
+    if (tid == 32 * 6) {  // beside the warp that most of the sequences are in
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sh.pair_full[i], 1);
             mbar_init(&sh.pair_empty[i], G);
@@ -263,7 +264,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
         if (w < warp) u_base += sh.scan[w];
         total += sh.scan[w];
     }
-    const long long per = max(quotient(total + n_spans - 1, n_spans), static_cast<long long>(kMinSpan));
+    const long long per = quotient(total + n_spans - 1, n_spans);  // (0 without any)
     const long long u0 = span * per, u1 = min(u0 + per, total);
     if (u0 >= u1 || (smem_u32(smem) & 1023u)) {
         if (tid == 0) {

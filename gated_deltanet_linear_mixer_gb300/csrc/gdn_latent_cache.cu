@@ -10,8 +10,6 @@
 // copy_pages: the pairs travel as kernel arguments, so that nothing is copied to
 // the device and a captured call keeps its pairs.
 #include <algorithm>
-#include <utility>
-#include <vector>
 
 #include "gdn_internal.h"
 #include "gdn_kv.cuh"
@@ -34,18 +32,23 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 __device__ __forceinline__ int unit_first(int u, int style) { return style == 0 ? 8 * u : 16 * u; }
 __device__ __forceinline__ int unit_second(int u, int style) { return style == 0 ? 8 * u + kRopeDim / 2 : 16 * u + 8; }
 
-// x: the two vectors of unit u; row: cosines and sines of the token.
-__device__ __forceinline__ void turn_unit(float* x, const float* row, int u, int style) {
+// Cosines and sines of unit u's pairs.
+struct Angles {
     float c[8], s[8];
+    __device__ __forceinline__ void load(const float* row, int u) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-        Vec16<float>::load(row + 8 * u + i, c + i);
-        Vec16<float>::load(row + kRopeDim / 2 + 8 * u + i, s + i);
+        for (int i = 0; i < 8; i += 4) {
+            Vec16<float>::load(row + 8 * u + i, c + i);
+            Vec16<float>::load(row + kRopeDim / 2 + 8 * u + i, s + i);
+        }
     }
+};
+// x: the two vectors of a unit.
+__device__ __forceinline__ void turn_unit(float* x, const Angles& a, int style) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (style == 0) turn(x[i], x[8 + i], c[i], s[i]);
-        else turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
+        if (style == 0) turn(x[i], x[8 + i], a.c[i], a.s[i]);
+        else turn(x[2 * i], x[2 * i + 1], a.c[i], a.s[i]);
     }
 }
 
@@ -60,62 +63,63 @@ __device__ __forceinline__ uint4 finite_bf16(const float* x) {
 }
 
 constexpr int kAppendThreads = 128;
-constexpr int kUnits = 4;                // of a position part
-constexpr int kQUnits = 2;               // units of q a lane has in flight
+constexpr int kUnits = 4;   // of a position part
+constexpr int kQUnits = 4;  // units of q a lane has in flight: 32 heads a warp
 
 template <int C>
 __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const LatentAppendArgs a, const int parts) {
-    constexpr int N = C / 256;           // 8-channel vectors of the latent a lane holds
+    constexpr int N = C / 256, W = C + kRopeDim;  // 8-channel vectors of the latent a lane holds; channels of a row
     const int lane = threadIdx.x & 31;
     const long long w = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int tok = static_cast<int>(w / parts), part = static_cast<int>(w % parts);  // part 0: the row
     if (tok >= a.b.n_tokens) return;
 
-    // loads first: they depend on nothing
-    float x[2][16];
-    const bf16* src = static_cast<const bf16*>(a.rows.data) + tok * a.rows.token_stride;
-    const bf16* qs = static_cast<const bf16*>(a.q.data) + tok * a.q.token_stride;
-    const int u0 = (part - 1) * 32 * kQUnits + lane, n_units = a.n_heads * kUnits;
-    if (part == 0) {
+    // a unit's place does not depend on its head: this lane's are all unit lane % 4, heads apart
+    const int u = lane % kUnits, head0 = (part - 1) * 8 * kQUnits + lane / kUnits;
+    const int c0 = unit_first(u, a.rope_style), c1 = unit_second(u, a.rope_style);
+    uint4 raw[2 * kQUnits];
+    if (part == 0) {  // loads first: they depend on nothing
+        const bf16* src = static_cast<const bf16*>(a.rows.data) + tok * a.rows.token_stride;
 #pragma unroll
-        for (int i = 0; i < N; ++i) Vec16<bf16>::load(src + 8 * lane + 256 * i, x[0] + 8 * i);
+        for (int i = 0; i < N; ++i) raw[i] = Vec16<bf16>::load_raw(src + 8 * lane + 256 * i);
         if (lane < kUnits) {
-            Vec16<bf16>::load(src + C + unit_first(lane, a.rope_style), x[1]);
-            Vec16<bf16>::load(src + C + unit_second(lane, a.rope_style), x[1] + 8);
+            raw[N] = Vec16<bf16>::load_raw(src + C + c0);
+            raw[N + 1] = Vec16<bf16>::load_raw(src + C + c1);
         }
     } else {
+        const bf16* src = static_cast<const bf16*>(a.q.data) + tok * a.q.token_stride;
 #pragma unroll
-        for (int k = 0; k < kQUnits; ++k) {
-            const int u = u0 + 32 * k;
-            if (u >= n_units) break;
-            const bf16* head = qs + u / kUnits * a.q.head_stride;
-            Vec16<bf16>::load(head + unit_first(u % kUnits, a.rope_style), x[k]);
-            Vec16<bf16>::load(head + unit_second(u % kUnits, a.rope_style), x[k] + 8);
-        }
+        for (int k = 0; k < kQUnits; ++k)
+            if (head0 + 8 * k < a.n_heads) {
+                const bf16* head = src + (head0 + 8 * k) * a.q.head_stride;
+                raw[2 * k] = Vec16<bf16>::load_raw(head + c0);
+                raw[2 * k + 1] = Vec16<bf16>::load_raw(head + c1);
+            }
     }
 
     const int seq = a.b.uniform_q ? tok / a.b.uniform_q : warp_seq_of_token(a.b.cu, a.b.n_seq, tok);
     const long long pos = static_cast<long long>(a.b.kv_lens[seq]) - (a.b.cu[seq + 1] - tok);
-    const float* table = nullptr;
+    Angles angles;
     if (a.rope) {
         long long p = a.positions ? a.positions[tok] : pos;
         if (p < 0 || p >= a.rope_len) {
             if (lane == 0) atomicMax(a.error, kKvErrRope);
             p = p < 0 ? 0 : a.rope_len - 1;
         }
-        table = a.rope + static_cast<size_t>(p) * kRopeDim;
+        if (part > 0 || lane < kUnits) angles.load(a.rope + p * kRopeDim, u);
     }
-
     if (part > 0) {
-        bf16* qd = static_cast<bf16*>(const_cast<void*>(a.q_out.data)) + tok * a.q_out.token_stride;
+        bf16* dst = static_cast<bf16*>(const_cast<void*>(a.q_out.data)) + tok * a.q_out.token_stride;
 #pragma unroll
-        for (int k = 0; k < kQUnits; ++k) {
-            const int u = u0 + 32 * k;
-            if (u >= n_units) break;
-            if (table) turn_unit(x[k], table, u % kUnits, a.rope_style);
-            bf16* head = qd + u / kUnits * a.q_out.head_stride;
-            Vec16<bf16>::store(head + unit_first(u % kUnits, a.rope_style), x[k]);
-            Vec16<bf16>::store(head + unit_second(u % kUnits, a.rope_style), x[k] + 8);
+        for (int i = 0; i < kQUnits; ++i) {
+            if (head0 + 8 * i >= a.n_heads) break;
+            float x[16];
+            Vec16<bf16>::unpack(raw[2 * i], x);
+            Vec16<bf16>::unpack(raw[2 * i + 1], x + 8);
+            if (a.rope) turn_unit(x, angles, a.rope_style);
+            bf16* head = dst + (head0 + 8 * i) * a.q_out.head_stride;
+            Vec16<bf16>::store(head + c0, x);
+            Vec16<bf16>::store(head + c1, x + 8);
         }
         return;
     }
@@ -124,39 +128,53 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
     const int page = lp >= 0 && lp < a.b.pages_per_seq ? a.b.table[static_cast<size_t>(seq) * a.b.pages_per_seq + lp] : -1;
     const bool mapped = page >= 0 && page < a.c.n_pages;
     if (!mapped && lane == 0) atomicMax(a.error, kKvErrTable);
+    float x[8 * N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) Vec16<bf16>::unpack(raw[i], x + 8 * i);
     if (a.norm_w) {
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8 * N; ++i) sum = fmaf(x[0][i], x[0][i], sum);
+        for (int i = 0; i < 8 * N; ++i) sum = fmaf(x[i], x[i], sum);
         const float r = rsqrtf(group_sum<32>(sum) * (1.0f / C) + a.eps);
 #pragma unroll
         for (int i = 0; i < 8 * N; i += 4) {
             float g[4];
             Vec16<float>::load(a.norm_w + 8 * lane + 256 * (i / 8) + i % 8, g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[0][i + e] = x[0][i + e] * r * g[e];
+            for (int e = 0; e < 4; ++e) x[i + e] = x[i + e] * r * g[e];
         }
     }
     uint4 v[N], k0 = make_uint4(0, 0, 0, 0), k1 = k0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = finite_bf16(x[0] + 8 * i);
+    for (int i = 0; i < N; ++i) v[i] = finite_bf16(x + 8 * i);
     if (lane < kUnits) {
-        if (table) turn_unit(x[1], table, lane, a.rope_style);
-        k0 = finite_bf16(x[1]);
-        k1 = finite_bf16(x[1] + 8);
+        float y[16];
+        Vec16<bf16>::unpack(raw[N], y);
+        Vec16<bf16>::unpack(raw[N + 1], y + 8);
+        if (a.rope) turn_unit(y, angles, a.rope_style);
+        k0 = finite_bf16(y);
+        k1 = finite_bf16(y + 8);
     }
-    auto store = [&](bf16* row) {
+    auto store = [&](bf16* to) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(row + 8 * lane + 256 * i) = v[i];
+        for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(to + 8 * lane + 256 * i) = v[i];
         if (lane < kUnits) {
-            *reinterpret_cast<uint4*>(row + C + unit_first(lane, a.rope_style)) = k0;
-            *reinterpret_cast<uint4*>(row + C + unit_second(lane, a.rope_style)) = k1;
+            *reinterpret_cast<uint4*>(to + C + c0) = k0;
+            *reinterpret_cast<uint4*>(to + C + c1) = k1;
         }
     };
-    constexpr int W = C + kRopeDim;
     if (mapped)
         store(static_cast<bf16*>(a.c.rows) + (static_cast<size_t>(page) * a.page_size + static_cast<int>(pos % a.page_size)) * W);
     if (a.rows_out) store(static_cast<bf16*>(a.rows_out) + static_cast<size_t>(tok) * W);
+}
+
+template <int C>
+cudaError_t append_t(const LatentAppendArgs& a, cudaStream_t st) {
+    const int parts = 1 + (a.q.data ? (a.n_heads + 8 * kQUnits - 1) / (8 * kQUnits) : 0);
+    const long long blocks = (static_cast<long long>(a.b.n_tokens) * parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    latent_append_kernel<C><<<static_cast<unsigned>(blocks), kAppendThreads, 0, st>>>(a, parts);
+    return cudaGetLastError();
 }
 
 constexpr int kReadThreads = 256, kReadTokens = 4;
@@ -194,9 +212,10 @@ __global__ void __launch_bounds__(kReadThreads) latent_read_kernel(const LatentR
 }
 
 // ---------------------------------------------------------------- page copies
-template <int PAIRS, int BUFFERS> struct CopyArgs {
-    uint8_t* base[BUFFERS];
-    unsigned bytes[BUFFERS];
+constexpr int kBuffers = 32, kFewPairs = 256, kManyPairs = 2048;  // of a launch, whose arguments they are
+template <int PAIRS> struct CopyArgs {
+    uint8_t* base[kBuffers];
+    unsigned bytes[kBuffers];
     int n_buffers;
     int2 pair[PAIRS];  // source, destination
 };
@@ -206,36 +225,37 @@ constexpr int kCopyThreads = 256, kCopyVectors = 4;
 template <typename W, typename A>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ A a) {
     const int2 p = a.pair[blockIdx.y];
-    for (int b = blockIdx.z; b < a.n_buffers; b += gridDim.z) {
-        const unsigned n = a.bytes[b] / sizeof(W);
-        const W* src = reinterpret_cast<const W*>(a.base[b] + static_cast<size_t>(p.x) * a.bytes[b]);
-        W* dst = reinterpret_cast<W*>(a.base[b] + static_cast<size_t>(p.y) * a.bytes[b]);
-        for (unsigned i0 = blockIdx.x * kCopyThreads * kCopyVectors + threadIdx.x; i0 < n;
-             i0 += gridDim.x * kCopyThreads * kCopyVectors) {
-            W v[kCopyVectors];
+    const int b = blockIdx.z;
+    const unsigned n = a.bytes[b] / sizeof(W);
+    const W* src = reinterpret_cast<const W*>(a.base[b] + static_cast<size_t>(p.x) * a.bytes[b]);
+    W* dst = reinterpret_cast<W*>(a.base[b] + static_cast<size_t>(p.y) * a.bytes[b]);
+    const unsigned i0 = blockIdx.x * (kCopyThreads * kCopyVectors) + threadIdx.x;
+    W v[kCopyVectors];
 #pragma unroll
-            for (int k = 0; k < kCopyVectors; ++k)
-                if (i0 + k * kCopyThreads < n) v[k] = src[i0 + k * kCopyThreads];
+    for (int k = 0; k < kCopyVectors; ++k)
+        if (i0 + k * kCopyThreads < n) v[k] = src[i0 + k * kCopyThreads];
 #pragma unroll
-            for (int k = 0; k < kCopyVectors; ++k)
-                if (i0 + k * kCopyThreads < n) dst[i0 + k * kCopyThreads] = v[k];
-        }
-    }
+    for (int k = 0; k < kCopyVectors; ++k)
+        if (i0 + k * kCopyThreads < n) dst[i0 + k * kCopyThreads] = v[k];
 }
 
-template <typename W, int PAIRS, int BUFFERS>
-cudaError_t copy_some(const std::pair<uint8_t*, unsigned>* buffers, int n_buffers, const int32_t* src, const int32_t* dst,
+// The arrays whose pages all lie on 16 bytes, or (W 32 bits) the others.
+template <typename W, int PAIRS>
+cudaError_t copy_some(void* const* bases, const size_t* page_bytes, int n_buffers, const int32_t* src, const int32_t* dst,
                       int n_pairs, cudaStream_t st) {
-    using A = CopyArgs<PAIRS, BUFFERS>;
+    using A = CopyArgs<PAIRS>;
     A a;
-    for (int b0 = 0; b0 < n_buffers; b0 += BUFFERS) {
-        a.n_buffers = std::min(BUFFERS, n_buffers - b0);
+    for (int b = 0; b < n_buffers;) {
+        a.n_buffers = 0;
         unsigned most = 0;
-        for (int b = 0; b < a.n_buffers; ++b) {
-            a.base[b] = buffers[b0 + b].first;
-            a.bytes[b] = buffers[b0 + b].second;
-            most = std::max(most, a.bytes[b]);
+        for (; b < n_buffers && a.n_buffers < kBuffers; ++b) {
+            const bool wide = page_bytes[b] % 16 == 0 && (reinterpret_cast<uintptr_t>(bases[b]) & 15u) == 0;
+            if (wide != (sizeof(W) == 16)) continue;
+            a.base[a.n_buffers] = static_cast<uint8_t*>(bases[b]);
+            a.bytes[a.n_buffers++] = static_cast<unsigned>(page_bytes[b]);
+            most = std::max(most, static_cast<unsigned>(page_bytes[b]));
         }
+        if (a.n_buffers == 0) break;
         const unsigned step = kCopyThreads * kCopyVectors * sizeof(W);
         for (int p0 = 0; p0 < n_pairs; p0 += PAIRS) {
             const int n = std::min(PAIRS, n_pairs - p0);
@@ -251,13 +271,7 @@ cudaError_t copy_some(const std::pair<uint8_t*, unsigned>* buffers, int n_buffer
 }  // namespace
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int latent_dim, cudaStream_t st) {
-    const int parts = 1 + (a.q.data ? (a.n_heads * kUnits + 32 * kQUnits - 1) / (32 * kQUnits) : 0);
-    const long long warps = static_cast<long long>(a.b.n_tokens) * parts;
-    const long long blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (latent_dim == 512) latent_append_kernel<512><<<static_cast<unsigned>(blocks), kAppendThreads, 0, st>>>(a, parts);
-    else latent_append_kernel<256><<<static_cast<unsigned>(blocks), kAppendThreads, 0, st>>>(a, parts);
-    return cudaGetLastError();
+    return latent_dim == 512 ? append_t<512>(a, st) : append_t<256>(a, st);
 }
 
 cudaError_t launch_latent_read(const LatentReadArgs& a, int latent_dim, cudaStream_t st) {
@@ -270,18 +284,13 @@ cudaError_t launch_latent_read(const LatentReadArgs& a, int latent_dim, cudaStre
 
 cudaError_t launch_copy_pages(void* const* bases, const size_t* page_bytes, int n_buffers, const int32_t* src,
                               const int32_t* dst, int n_pairs, cudaStream_t st) {
-    // arrays whose pages all lie on 16 bytes, and the others
-    std::vector<std::pair<uint8_t*, unsigned>> wide, narrow;
-    for (int b = 0; b < n_buffers; ++b) {
-        const bool w = page_bytes[b] % 16 == 0 && (reinterpret_cast<uintptr_t>(bases[b]) & 15u) == 0;
-        (w ? wide : narrow).emplace_back(static_cast<uint8_t*>(bases[b]), static_cast<unsigned>(page_bytes[b]));
-    }
-    cudaError_t e = cudaSuccess;
-    if (!wide.empty())
-        e = copy_some<uint4, 400, 32>(wide.data(), static_cast<int>(wide.size()), src, dst, n_pairs, st);
-    if (e == cudaSuccess && !narrow.empty())
-        e = copy_some<uint32_t, 400, 32>(narrow.data(), static_cast<int>(narrow.size()), src, dst, n_pairs, st);
-    return e;
+    auto copy = [&](auto word) {
+        using W = decltype(word);
+        return n_pairs <= kFewPairs ? copy_some<W, kFewPairs>(bases, page_bytes, n_buffers, src, dst, n_pairs, st)
+                                    : copy_some<W, kManyPairs>(bases, page_bytes, n_buffers, src, dst, n_pairs, st);
+    };
+    const cudaError_t e = copy(uint4{});
+    return e != cudaSuccess ? e : copy(uint32_t{});
 }
 
 }  // namespace gdn
