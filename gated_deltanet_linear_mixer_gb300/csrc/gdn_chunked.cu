@@ -1511,7 +1511,7 @@ cudaError_t read_device_error(int* code, bool reset) {
     }
     // the projection GEMM's word (codes 20..23), the recurrent kernel's (30),
     // the per-channel prep's (13, 14); last the cache operators', which may be
-    // data out of range (40, 41) and no wait (42..48)
+    // data out of range (40, 41) and no wait (42..66)
     int gemm = 0, rec = 0, kda = 0;
     if (e == cudaSuccess) e = read_gemm_error(&gemm, reset);
     if (e == cudaSuccess) e = read_rec_error(&rec, reset);

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
     if (warp == 8) {
         // ---- loads
         const bool leader = elect_one();
-        bool ok = true;
+        bool ok = !a.stall;  // the test hook
         uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0};  // fills so far
         for (int round = 0; ok && round < rounds; ++round) {
             Item x;

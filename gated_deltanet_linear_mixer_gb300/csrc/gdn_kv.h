@@ -12,7 +12,7 @@ namespace gdn {
 constexpr int kKvErrTable = 40;  // block table entry or length out of range
 constexpr int kKvErrRope = 41;   // position outside the rotation table
 // The word on the current device where the operators' kernels record codes: the
-// largest stays, so that a wait that gave up (42..48) outranks data out of range.
+// largest stays, so that a wait that gave up (42..66) outranks data out of range.
 cudaError_t cache_error_word(int** word);
 
 struct KvCache {

@@ -45,6 +45,7 @@ struct LatentAttnArgs {
     void* out;
     void* workspace;
     int* error;
+    int stall;  // test hook: no cached row is ever loaded
 };
 
 struct ExpandedArgs {
@@ -56,6 +57,7 @@ struct ExpandedArgs {
     KvRows q, k, k_rope, v;
     void* out;
     int* error;
+    int stall;  // test hook: nothing is ever loaded
 };
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int latent_dim, cudaStream_t stream);

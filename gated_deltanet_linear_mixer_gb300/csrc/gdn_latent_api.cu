@@ -15,6 +15,7 @@ gdn_status set_error(gdn_status st, const char* fn, const char* fmt, ...);
 void clear_error();
 // GDN_ERR_INJECTED when the environment variable GDN_FAULT lists `site`.
 gdn_status inject_fault(const char* site, const char* fn);
+bool fault_site(const char* site);  // whether it does
 }  // namespace gdn
 
 using gdn::set_error;
@@ -212,6 +213,7 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
     if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.c = gdn::LatentCache{cache->rows, cache->n_pages};
     a.n_heads = dims->n_heads; a.page_size = dims->page_size; a.scale = dims->scale; a.out = out; a.workspace = workspace;
+    a.stall = gdn::fault_site("stall_latent") ? 1 : 0;
     return cuda_status(gdn::launch_latent_attention(a, dims->latent_dim, static_cast<cudaStream_t>(stream)), fn,
                        "attention launch");
 }
@@ -249,6 +251,7 @@ gdn_status gdn_expanded_attention(const gdn_latent_dims* dims, int32_t n_seq, co
     if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.n_heads = dims->n_heads; a.scale = dims->scale; a.cu_q = cu_q; a.cu_kv = cu_kv; a.out = out;
     a.cu_q_host = cu_q_host; a.cu_kv_host = cu_kv_host;
+    a.stall = gdn::fault_site("stall_expanded") ? 1 : 0;
     return cuda_status(gdn::launch_expanded_attention(a, dims->nope_dim, dims->v_dim, static_cast<cudaStream_t>(stream)), fn,
                        "attention launch");
 }

@@ -365,7 +365,8 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     };
     // counts that the roles carry from round to round
     uint32_t g = 0;   // key tiles
-    uint32_t qc = 0;  // pieces with tiles
+    uint32_t qc = 0;  // pieces with tiles whose queries came
+    uint32_t asked = 0;  // whose queries were asked for
     bool ok = true;
     uint32_t ropes = 0, pairs = 0;  // loads started
 
@@ -559,6 +560,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
             // need into both.
             const int R = min(a.page_size, kKeys), per_tile = kKeys / R;
             const bool leader = elect_one(), lead_warp = warp == 4;
+            if (a.stall) ok = false;  // the test hook
             const int nowhere = a.c.n_pages * a.page_size;  // past the last row: the load gives zeros
             auto load = [&](uint8_t* dst, uint64_t* bar, int col, int row) {
                 if (PAIR) tma_load_2d_multicast(dst, &maps.rows, bar, col, row, 3);
@@ -684,6 +686,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                 // queries, once the products with the last ones are done
                 if (qc > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty, (qc - 1) & 1)))) break;
                 load_queries(sh.piece[i]);
+                ++asked;
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_full, qc & 1)))) break;
                 ++qc;
                 for (int t = a0; ok && t < b0; ++t, ++g) {
@@ -766,7 +769,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
         for (uint32_t fill = pairs > NS ? pairs - NS : 0; fill < pairs; ++fill)
             if ((fill % NP >= 2) == (warp == 7)) mbar_wait_brief(&sh.pair_full[fill % NS], (fill / NS) & 1);
     } else if (warp == 5 || warp == 6) {
-        if (warp == 5 && !ok && dense_q) mbar_wait_brief(&sh.q_full, qc & 1);  // queries on their way
+        if (warp == 5 && asked > qc) mbar_wait_brief(&sh.q_full, qc & 1);  // queries on their way
         if (elect_one()) mma_commit(&sh.drained[warp - 5]);
         if (!mbar_wait_brief(&sh.drained[warp - 5], 0) && lane == 0) record(a.error, 57);
     }

@@ -45,13 +45,14 @@
  *   latent_read, latent_attention, expanded_attention, copy_pages, or all.  A call
  *   whose site is listed validates its arguments, then returns
  *   GDN_ERR_INJECTED without enqueuing anything, so every caller buffer is
- *   left as it was.  Two sites are device test hooks, under which a bounded
+ *   left as it was.  Four sites are device test hooks, under which a bounded
  *   wait runs out, the call returns GDN_OK and the next gdn_sync_status
  *   reports GDN_ERR_TIMEOUT: stall_scan (a bf16 prefill that takes the fused
  *   tensor-core launch makes its scan wait, for at most 1 ms, on a chunk flag
- *   that nothing sets) and stall_attention (a gdn_kv_attention call that takes
+ *   that nothing sets), stall_attention (a gdn_kv_attention call that takes
  *   the kernel for many rows waits, for 2 s, for page look-ups that are never
- *   published).  GDN_FAULT is read on every call.
+ *   published), stall_latent and stall_expanded (gdn_latent_attention and
+ *   gdn_expanded_attention wait, for 2 s, for loads that are never started).  GDN_FAULT is read on every call.
  */
 #ifndef GDN_H
 #define GDN_H
@@ -623,7 +624,8 @@ size_t gdn_timing_report(char* buf, size_t buf_len);
  * waits for its tiles, and for its v tile, products and the next item's tiles;
  * 20..23 the projection GEMM's; 30 the
  * token-recurrent kernel's wait for a state copy; 42..48 the cache attention's
- * tensor-core kernel's waits between its roles) and exit cleanly; their
+ * tensor-core kernel's waits between its roles, 50..57 latent attention's, 60..65
+ * expanded attention's; 48, 58 and 66 shared memory that is not where it has to be) and exit cleanly; their
  * outputs are then invalid.  Codes 40 and 41 are not waits: a cache operator
  * met device data out of range (see the cache above) and stayed in bounds; a
  * wait's code is given before them.  Waits for the device

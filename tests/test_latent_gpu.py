@@ -580,3 +580,40 @@ def test_prompt_then_drafts_of_a_forked_sequence():
         close(o[part], ref)
         close(e[part], ref)
     _status_ok()
+
+
+# ------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("heads,counts,lens,strided", [(16, [1, 1], [700, 80], False), (32, [1], [3000], True), (32, [4], [500], False)])
+def test_latent_attention_reports_a_wait_that_runs_out(monkeypatch, heads, counts, lens, strided):
+    """Loads that are never started (GDN_FAULT=stall_latent): every role gives up after 2 s, the status
+    says so, and the next call is right.  By one thread block a span, and by pairs."""
+    d = gdn.LatentDims(heads, 512)
+    cache, table = make_cache(d, lens, 161)
+    q = _queries(sum(counts), heads, 576, 162, strided=strided)
+    monkeypatch.setenv("GDN_FAULT", "stall_latent")
+    gdn.latent_attention(d, cache, cu_of(counts), ints(lens), table, q)
+    with pytest.raises(gdn.GDNError) as e:
+        gdn.sync_status()
+    assert e.value.status == gdn.GDN_ERR_TIMEOUT
+    _status_ok()
+    monkeypatch.delenv("GDN_FAULT")
+    got = gdn.latent_attention(d, cache, cu_of(counts), ints(lens), table, q)
+    _status_ok()
+    check(got, *absorbed(d, cache, counts, lens, table, q))
+
+
+def test_expanded_attention_reports_a_wait_that_runs_out(monkeypatch):
+    d = gdn.LatentDims(4)
+    counts, lens = [300, 5], [300, 400]
+    k, r, v = _kv(lens, 4, 128, 128, 171, True)
+    q = _queries(305, 4, 192, 172)
+    monkeypatch.setenv("GDN_FAULT", "stall_expanded")
+    gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v)
+    with pytest.raises(gdn.GDNError) as e:
+        gdn.sync_status()
+    assert e.value.status == gdn.GDN_ERR_TIMEOUT
+    _status_ok()
+    monkeypatch.delenv("GDN_FAULT")
+    got = gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v)
+    _status_ok()
+    check(got, *expanded(d, counts, lens, q, k, r, v))
