@@ -39,7 +39,7 @@ struct LatentReadArgs {
 struct LatentAttnArgs {
     LatentCache c;
     KvBatch b;
-    int n_heads, page_size;
+    int n_heads, page_shift;  // a page has 1 << page_shift tokens
     float scale;
     KvRows q;  // [T, n_heads, C + kRopeDim]
     void* out;

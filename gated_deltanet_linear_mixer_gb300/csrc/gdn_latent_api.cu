@@ -212,7 +212,8 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
     if ((st = gdn::inject_fault("latent_attention", fn)) != GDN_OK) return st;
     if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.c = gdn::LatentCache{cache->rows, cache->n_pages};
-    a.n_heads = dims->n_heads; a.page_size = dims->page_size; a.scale = dims->scale; a.out = out; a.workspace = workspace;
+    a.n_heads = dims->n_heads; a.scale = dims->scale; a.out = out; a.workspace = workspace;
+    while (1 << a.page_shift < dims->page_size) ++a.page_shift;
     a.stall = gdn::fault_site("stall_latent") ? 1 : 0;
     return cuda_status(gdn::launch_latent_attention(a, dims->latent_dim, static_cast<cudaStream_t>(stream)), fn,
                        "attention launch");

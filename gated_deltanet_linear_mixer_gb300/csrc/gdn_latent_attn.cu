@@ -128,6 +128,48 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+// How long rows stay in L2: those of sequences that a single group of row tiles
+// reads leave before the partial results, which are read again (256 single tokens of
+// 32 heads: 224 us, 222 us so; 131,000 keys: 39.3, 37.9), those that other groups
+// read after this one do not (256 tokens of 32 heads after 1744: 119 us if they did, 108 us).
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+    uint64_t p;
+    if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+// Loads into this thread block, or both of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, uint64_t policy) {
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+            " [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+            : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_halves(void* dst, const CUtensorMap* map, uint64_t* bar, int y, int z, uint64_t policy) {
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+            : "memory");
+}
+
 // 16 lanes x 64 columns of 32-bit: v[4 i + 2 h + e] is row lane / 4 + 8 h, column
 // 8 i + 2 (lane % 4) + e.
 __device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float* v) {
@@ -185,7 +227,7 @@ __device__ __forceinline__ Need need_of(const LatentAttnArgs& a, int seq) {
     n.q0 = a.b.cu[seq];
     n.qn = a.b.cu[seq + 1] - n.q0;
     n.len = a.b.kv_lens[seq];
-    const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
+    const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) << a.page_shift : 0;
     const int len = static_cast<int>(min(static_cast<long long>(max(n.len, 0)), cap));
     n.groups = (n.qn * a.n_heads + ROWS - 1) / ROWS;
     n.tiles = max(1, (len + kKeys - 1) / kKeys);
@@ -288,7 +330,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
         k_at = static_cast<int>(quotient(u0 - u_at, n_at.tiles));
     }
     auto lay_out = [&] {
-        const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) * a.page_size : 0;
+        const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) << a.page_shift : 0;
         int i = 0;
         bool more = true;
         while (i < kPieces) {
@@ -345,8 +387,8 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     if (walker) {
         // the loading warps' first look-up, on its way meanwhile
         const long long key = (u0 - u_at - static_cast<long long>(k_at) * n_at.tiles) * kKeys;
-        if (key / a.page_size < a.b.pages_per_seq)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.b.table + static_cast<size_t>(s_at) * a.b.pages_per_seq + key / a.page_size));
+        if (key >> a.page_shift < a.b.pages_per_seq)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.b.table + static_cast<size_t>(s_at) * a.b.pages_per_seq + (key >> a.page_shift)));
         lay_out();
     }
     tc_fence_before_sync();
@@ -558,14 +600,12 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
             // issue, and pages of 16 rows need 36 a tile: two warps share them, the first the position keys
             // and two slots, the second the others.  Of a pair each thread block loads half of what both
             // need into both.
-            const int R = min(a.page_size, kKeys), per_tile = kKeys / R;
+            const int page_size = 1 << a.page_shift, R = min(page_size, kKeys), per_tile = kKeys >> min(a.page_shift, 6);
             const bool leader = elect_one(), lead_warp = warp == 4;
             if (a.stall) ok = false;  // the test hook
-            const int nowhere = a.c.n_pages * a.page_size;  // past the last row: the load gives zeros
-            auto load = [&](uint8_t* dst, uint64_t* bar, int col, int row) {
-                if (PAIR) tma_load_2d_multicast(dst, &maps.rows, bar, col, row, 3);
-                else tma_load_2d(dst, &maps.rows, bar, col, row);
-            };
+            const int nowhere = a.c.n_pages << a.page_shift;  // past the last row: the load gives zeros
+            const uint64_t policy = l2_policy(static_cast<long long>(a.b.max_q) * a.n_heads <= NR * G);
+            auto load = [&](uint8_t* dst, uint64_t* bar, int col, int row) { load_rows<PAIR>(dst, &maps.rows, bar, col, row, policy); };
             for (int i = 0; ok && i < n_round; ++i) {
                 const Piece p = sh.piece[i];
                 int row = 0;
@@ -573,8 +613,8 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                 auto look_up = [&](int x) {  // where chunk x of the piece lies; negative: not mapped
                     const int key = (first_chunk + x) * R;
                     if (x >= n || key >= p.n_keys) return nowhere;
-                    const int page = a.b.table[static_cast<size_t>(p.seq) * a.b.pages_per_seq + key / a.page_size];
-                    return page >= 0 && page < a.c.n_pages ? page * a.page_size + key % a.page_size : -1;
+                    const int page = a.b.table[static_cast<size_t>(p.seq) * a.b.pages_per_seq + (key >> a.page_shift)];
+                    return page >= 0 && page < a.c.n_pages ? (page << a.page_shift) + (key & (page_size - 1)) : -1;
                 };
                 int ahead = n > 0 ? look_up(lane) : 0;
                 for (int t = p.a; ok && t < p.b; ++t, ++g) {
@@ -628,8 +668,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                             if (PAIR && (q & 1) != g_own) {
                                 // the other's to load
                             } else if (per_tile == 1) {
-                                if (PAIR) tma_load_3d_multicast(dst, &maps.pairs, &sh.pair_full[slot], 0, at[0], 2 * q, 3);
-                                else tma_load_3d(dst, &maps.pairs, &sh.pair_full[slot], 0, at[0], 2 * q);
+                                load_halves<PAIR>(dst, &maps.pairs, &sh.pair_full[slot], at[0], 2 * q, policy);
                             } else {
 #pragma unroll
                                 for (int c = 0; c < kKeys / 16; ++c)
@@ -957,8 +996,8 @@ cudaError_t launch_t(const LatentAttnArgs& a, cudaStream_t st) {
     cudaError_t e = allow_smem(latent_attention_kernel<C, NR, PAIR>, L::kSmem, ready);
     if (e != cudaSuccess) return e;
     Maps maps{};
-    const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) * a.page_size;
-    if (rows > 0 && !(make_tma_map_bf16_2d(&maps.rows, a.c.rows, rows, L::W, L::W, std::min(a.page_size, kKeys), 64) &&
+    const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) << a.page_shift;
+    if (rows > 0 && !(make_tma_map_bf16_2d(&maps.rows, a.c.rows, rows, L::W, L::W, std::min(1 << a.page_shift, kKeys), 64) &&
                       make_tma_map_bf16_3d(&maps.pairs, a.c.rows, 64, rows, L::W / 64, L::W, 64, 64, kKeys, 2)))
         return cudaErrorInvalidValue;
     if (static_cast<long long>(a.b.n_tokens) * a.n_heads > 0x7fffffffLL - 2 * NR) return cudaErrorInvalidConfiguration;
