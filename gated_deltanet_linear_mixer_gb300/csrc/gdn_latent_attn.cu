@@ -14,22 +14,34 @@
 // O^T = V^T P^T has the latent channels as its M (C / 128 products of 128) and the
 // rows as its N: a tile of cached rows is the K-major operand of the first product
 // and the MN-major one of the second as it lies in shared memory, and the output
-// of 64 rows takes half of the tensor memory, where rows as M would take all of
-// it.  Per tile of 64 rows the products need 1152 + 768 cycles of shared memory
-// bandwidth, the tile's bytes (72 KB) 3100 cycles of an SM's share of DRAM.
+// of 64 rows takes half of the tensor memory, where rows as M would take all of it.
 //
 // Work.  (sequence, group of row tiles, key tile) in that order is one axis, cut
-// into equal spans, one a thread block (G row tiles of one group: G thread blocks
-// side by side, whose second reads come from L2).  So ragged lengths fill every SM
-// alike, whatever they are; lengths are only known on the device, where every
-// thread block finds its span by a scan over the sequences.  What a span holds of a
+// into equal spans, one a thread block.  So ragged lengths fill every SM alike,
+// whatever they are; lengths are only known on the device, where every thread
+// block finds its span by a scan over the sequences.  What a span holds of a
 // sequence that it does not hold whole is a partial result (at most two a span);
-// a second launch joins them.
+// a second launch joins them.  Above 64 rows a group is two row tiles, of a pair of
+// thread blocks that walk the same span and load each half of the rows into both.
 //
 // Roles: 4 softmax warps (also: rescaling, epilogue), two for the rows' TMA loads
-// (with the page look-ups), one loading queries and issuing S, one issuing O^T.  Cached rows are in a ring of 16 KB slots (64 keys x 128 channels) and
-// one of 8 KB slots (position keys).  Every wait is bounded (2 s); a wait that gives
-// up records a code (50..58) in the cache operators' device error word.
+// (with the page look-ups), one loading queries and issuing S, one issuing O^T.
+// Cached rows are in a ring of 16 KB slots (64 keys x 128 channels) and one of 8 KB
+// slots (position keys).  Every wait is bounded (2 s); a wait that gives up records
+// a code (50..57) in the cache operators' device error word.
+//
+// What bounds it.  Up to 32 rows a sequence the rows' bytes: a tile's 72 KB are
+// 3100 cycles of an SM's share of DRAM, its products 2160 (16 rows) or 2290 (32).
+// 256 single tokens of 32 heads after 127..8191 keys take 222 us, 88% of the
+// measured copy rate, 16 heads 205 us (92%).  With 64 rows the products: 36 of S at 37
+// cycles (64 x 64 x 16) and 16 of O^T at 76 (128 x 64 x 16 with the first operand
+// MN-major; 53 were it K-major) make 2540 cycles a tile, of which the ring's two tiles
+// let it reach 2900: 64 x 4 drafts of 32 heads after 500..6000 keys take 110 us, of
+// which the partial results of 152 thread blocks and their join are 20.  Tiles of
+// 32 keys, four in the ring, were slower (145 us, then 119), and so was fetching
+// tiles into L2 ahead of their loads (256 x 1: 229 us without, 246 three tiles
+// ahead).  One token after 1000 keys takes 13 us, all of it latency: the plan 2 us,
+// the look-up 1.5, a load 1, products and softmax 2.5, the partial result 1, the join 4.
 #include <algorithm>
 
 #include "gdn_internal.h"

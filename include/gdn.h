@@ -542,8 +542,9 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
  *   side), k_rope [Tk, rope_dim] rows (head_stride is not used); token strides
  *   > 0, a head stride of 0 shares one head.  out [Tq, n_heads, v_dim]
  *   contiguous.
- * Values that some query of a sequence sees have to be finite.  Accuracy as
- * gdn_latent_attention.
+ * Values that some query of a sequence sees have to be finite.  fp32 accumulation
+ * and softmax (the hardware's exponentials, 2 ulp), weights bf16 (8 bits); the sum
+ * takes them as they are.
  */
 gdn_status gdn_expanded_attention(const gdn_latent_dims* dims, int32_t n_seq, const int32_t* cu_q,
                                   const int32_t* cu_q_host, const int32_t* cu_kv,
