@@ -4,8 +4,9 @@
 //   w_rj = 2^(y_rj - m_r),   o_r = sum_j w_rj v_j / sum_j w_rj
 // with a reference m_r that lags behind the row's maximum by at most 2^kLazy, so
 // that the output is rescaled only where the maximum rises by more than that.
-// Weights are rounded to bf16 (the values' type, as the tensor core asks), and the
-// sum takes the rounded ones.
+// Weights are rounded to bf16 (the values' type, as the tensor core asks); the sum
+// takes them unrounded, which costs 0.0002 of the output's error and 5% less time
+// than the sum of the rounded ones.
 //
 // A thread block takes two tiles of 128 queries of a head and walks the keys in
 // tiles of 128 up to the last query's position.  While one tile's softmax runs, the
@@ -22,6 +23,24 @@
 // O0 += P0 V, S0 = Q0 K', O1 += P1 V, S1 = Q1 K'.  Every wait is bounded (2 s); a
 // wait that gives up records a code (60..66) in the cache operators' device error
 // word.
+//
+// What bounds it (128 channels, 128 wide values): for 128 keys and both tiles the
+// tensor core takes 24 instructions of S (128 x 128 x 16, 71 cycles each, measured
+// alone) and 16 of O (74, their A operand in tensor memory): 2890 cycles.  The keys
+// and values that come in meanwhile, 80 KB, take 640 cycles of the shared memory's
+// bandwidth, which those products use in full.  About 3700 cycles are reached: what
+// remains are the queries' loads at an item's start and keys that wait for room (the
+// queries leave room for 1.6 tiles of keys).  The exponentials (32 a cycle and SM: 1024
+// cycles) do not bound it.  4096 tokens, 32 heads: 137 us, 1.26 PFLOP/s; 16
+// prompts of 1 to 4096 tokens: 172 us, 0.94 PFLOP/s, where short items and the
+// last thread blocks' tails weigh more.
+//
+// Tried and slower (us, the two cases above): pairs of thread blocks that share keys
+// (134 and 215 where a block of the same form took 141 and 179); two threads a
+// row (165 against 140); weights handed over by halves (144); an issuing warp per
+// tile (146 and 180); one ring for keys and values (148 and 190); a thread that
+// polls both tiles' barriers and issues what is ready (149); scores read by one
+// load of 128 columns (140 and 178).
 #include <algorithm>
 
 #include "gdn_internal.h"
@@ -328,135 +347,135 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             tc_fence_before_sync();
         }
     } else {
-    regs_dec<88>();
-    if (warp == 8) {
-        // ---- loads
-        const bool leader = elect_one();
-        bool ok = !a.stall;  // the test hook
-        uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0};  // fills so far
-        for (int round = 0; ok && round < rounds; ++round) {
-            Item x;
-            if (!item_of(round, x)) continue;
-            auto load_queries = [&](int t) {  // once the products with the tile's last ones are done
-                if ((t ? x.n[1] : x.n[0]) == 0) return;
-                uint32_t& before = t ? queries[1] : queries[0];
-                if (before > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty[t], (before - 1) & 1)))) return;
-                ++before;
-                if (leader) {
-                    mbar_arrive_expect_tx(&sh.q_full[t], L::kQ);
-                    for (int b = 0; b < QB; ++b)
-                        tma_load_3d(smem + L::kQAt + t * L::kQ + b * kBlock, &plan.q, &sh.q_full[t], 64 * b, x.q0 + x.row0 + t * kM,
-                                    a.q.head_stride ? x.h : 0);
-                }
-                __syncwarp();
-            };
-            load_queries(0);
-            for (int i = 0; ok && i < x.n_tiles; ++i) {
-                if (i == 1) load_queries(1);  // behind the first tile's first keys and values
-                if (!ok) break;
-                const int key = x.k0 + i * kKeys;
-                for (int b = 0; ok && b < QB; ++b) {
-                    const uint32_t slot = keys % NK;
-                    if (keys >= NK && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.k_empty[slot], (keys / NK - 1) & 1)))) break;
-                    ++keys;
+        regs_dec<88>();
+        if (warp == 8) {
+            // ---- loads
+            const bool leader = elect_one();
+            bool ok = !a.stall;  // the test hook
+            uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0};  // fills so far
+            for (int round = 0; ok && round < rounds; ++round) {
+                Item x;
+                if (!item_of(round, x)) continue;
+                auto load_queries = [&](int t) {  // once the products with the tile's last ones are done
+                    if ((t ? x.n[1] : x.n[0]) == 0) return;
+                    uint32_t& before = t ? queries[1] : queries[0];
+                    if (before > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty[t], (before - 1) & 1)))) return;
+                    ++before;
                     if (leader) {
-                        uint8_t* dst = smem + slot * kBlock;
-                        mbar_arrive_expect_tx(&sh.k_full[slot], kBlock);
-                        if (b < QB - 1) tma_load_3d(dst, &plan.k, &sh.k_full[slot], 64 * b, key, a.k.head_stride ? x.h : 0);
-                        else tma_load_2d(dst, &plan.r, &sh.k_full[slot], 0, key);
+                        mbar_arrive_expect_tx(&sh.q_full[t], L::kQ);
+                        for (int b = 0; b < QB; ++b)
+                            tma_load_3d(smem + L::kQAt + t * L::kQ + b * kBlock, &plan.q, &sh.q_full[t], 64 * b, x.q0 + x.row0 + t * kM,
+                                        a.q.head_stride ? x.h : 0);
+                    }
+                    __syncwarp();
+                };
+                load_queries(0);
+                for (int i = 0; ok && i < x.n_tiles; ++i) {
+                    if (i == 1) load_queries(1);  // behind the first tile's first keys and values
+                    if (!ok) break;
+                    const int key = x.k0 + i * kKeys;
+                    for (int b = 0; ok && b < QB; ++b) {
+                        const uint32_t slot = keys % NK;
+                        if (keys >= NK && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.k_empty[slot], (keys / NK - 1) & 1)))) break;
+                        ++keys;
+                        if (leader) {
+                            uint8_t* dst = smem + slot * kBlock;
+                            mbar_arrive_expect_tx(&sh.k_full[slot], kBlock);
+                            if (b < QB - 1) tma_load_3d(dst, &plan.k, &sh.k_full[slot], 64 * b, key, a.k.head_stride ? x.h : 0);
+                            else tma_load_2d(dst, &plan.r, &sh.k_full[slot], 0, key);
+                        }
+                        __syncwarp();
+                    }
+                    const uint32_t slot = values % NV;
+                    if (ok && values >= NV) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.v_empty[slot], (values / NV - 1) & 1));
+                    if (!ok) break;
+                    ++values;
+                    if (leader) {
+                        uint8_t* dst = smem + L::kVAt + slot * L::kVTile;
+                        mbar_arrive_expect_tx(&sh.v_full[slot], L::kVTile);
+                        for (uint32_t b = 0; b < L::kVTile / kBlock; ++b)
+                            tma_load_3d(dst + b * kBlock, &plan.v, &sh.v_full[slot], 64 * b, key, a.v.head_stride ? x.h : 0);
                     }
                     __syncwarp();
                 }
-                const uint32_t slot = values % NV;
-                if (ok && values >= NV) ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.v_empty[slot], (values / NV - 1) & 1));
-                if (!ok) break;
-                ++values;
-                if (leader) {
-                    uint8_t* dst = smem + L::kVAt + slot * L::kVTile;
-                    mbar_arrive_expect_tx(&sh.v_full[slot], L::kVTile);
-                    for (uint32_t b = 0; b < L::kVTile / kBlock; ++b)
-                        tma_load_3d(dst + b * kBlock, &plan.v, &sh.v_full[slot], 64 * b, key, a.v.head_stride ? x.h : 0);
-                }
-                __syncwarp();
+                if (ok && x.n_tiles == 1) load_queries(1);
             }
-            if (ok && x.n_tiles == 1) load_queries(1);
-        }
-        if (!ok) {  // nothing is in flight when the memory is given back
-            if (lane == 0) record(a.error, 64);
-            for (uint32_t f = keys > NK ? keys - NK : 0; f < keys; ++f) mbar_wait_brief(&sh.k_full[f % NK], (f / NK) & 1);
-            for (uint32_t f = values > NV ? values - NV : 0; f < values; ++f) mbar_wait_brief(&sh.v_full[f % NV], (f / NV) & 1);
-            for (int t = 0; t < kTiles; ++t)
-                if (queries[t] > 0) mbar_wait_brief(&sh.q_full[t], (queries[t] - 1) & 1);
-        }
-    } else if (warp == 9) {
-        // ---- products
-        const bool leader = elect_one();
-        constexpr uint32_t id_s = idesc_bf16_f32(kM, kKeys), id_o = idesc_bf16_f32(kM, V, false, true);
-        const uint64_t dq = desc_kmajor_sw128(smem_u32(smem + L::kQAt)), dk = desc_kmajor_sw128(smem_u32(smem)),
-                       dv = desc_mnmajor_sw128(smem_u32(smem + L::kVAt), kBlock);
-        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_brief(bar, parity)) != 0; };
-        bool ok = true;
-        uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0}, steps[kTiles] = {0, 0};  // of the items before this one
-        for (int round = 0; ok && round < rounds; ++round) {
-            Item x;
-            if (!item_of(round, x)) continue;
-            // scores of tile t and key tile i; the last tile that uses a block gives it back
-            auto scores = [&](int t, int i) {
-                const bool give = t == 1 || i >= x.n[1];
-                for (int b = 0; b < QB; ++b) {
-                    const uint32_t fill = keys + i * QB + b, slot = fill % NK;
-                    if (!(ok = wait(&sh.k_full[slot], (fill / NK) & 1))) return;
-                    tc_fence_after_sync();
-                    if (leader) {
+            if (!ok) {  // nothing is in flight when the memory is given back
+                if (lane == 0) record(a.error, 64);
+                for (uint32_t f = keys > NK ? keys - NK : 0; f < keys; ++f) mbar_wait_brief(&sh.k_full[f % NK], (f / NK) & 1);
+                for (uint32_t f = values > NV ? values - NV : 0; f < values; ++f) mbar_wait_brief(&sh.v_full[f % NV], (f / NV) & 1);
+                for (int t = 0; t < kTiles; ++t)
+                    if (queries[t] > 0) mbar_wait_brief(&sh.q_full[t], (queries[t] - 1) & 1);
+            }
+        } else if (warp == 9) {
+            // ---- products
+            const bool leader = elect_one();
+            constexpr uint32_t id_s = idesc_bf16_f32(kM, kKeys), id_o = idesc_bf16_f32(kM, V, false, true);
+            const uint64_t dq = desc_kmajor_sw128(smem_u32(smem + L::kQAt)), dk = desc_kmajor_sw128(smem_u32(smem)),
+                           dv = desc_mnmajor_sw128(smem_u32(smem + L::kVAt), kBlock);
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_brief(bar, parity)) != 0; };
+            bool ok = true;
+            uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0}, steps[kTiles] = {0, 0};  // of the items before this one
+            for (int round = 0; ok && round < rounds; ++round) {
+                Item x;
+                if (!item_of(round, x)) continue;
+                // scores of tile t and key tile i; the last tile that uses a block gives it back
+                auto scores = [&](int t, int i) {
+                    const bool give = t == 1 || i >= x.n[1];
+                    for (int b = 0; b < QB; ++b) {
+                        const uint32_t fill = keys + i * QB + b, slot = fill % NK;
+                        if (!(ok = wait(&sh.k_full[slot], (fill / NK) & 1))) return;
+                        tc_fence_after_sync();
+                        if (leader) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + t * kKeys, dq + ((t * L::kQ + b * kBlock) >> 4) + 2 * k, dk + (slot * kBlock >> 4) + 2 * k,
-                                     id_s, (b > 0 || k > 0) ? 1u : 0u);
-                        if (give) mma_commit(&sh.k_empty[slot]);
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16(tmem + t * kKeys, dq + ((t * L::kQ + b * kBlock) >> 4) + 2 * k, dk + (slot * kBlock >> 4) + 2 * k,
+                                         id_s, (b > 0 || k > 0) ? 1u : 0u);
+                            if (give) mma_commit(&sh.k_empty[slot]);
+                        }
+                        __syncwarp();
+                    }
+                    if (leader) {
+                        mma_commit(&sh.s_full[t]);
+                        if (i == x.n[t] - 1) mma_commit(&sh.q_empty[t]);
                     }
                     __syncwarp();
-                }
-                if (leader) {
-                    mma_commit(&sh.s_full[t]);
-                    if (i == x.n[t] - 1) mma_commit(&sh.q_empty[t]);
-                }
-                __syncwarp();
-            };
-            for (int t = 0; ok && t < kTiles; ++t)
-                if (x.n[t] > 0) {
-                    if (!(ok = wait(&sh.q_full[t], queries[t] & 1))) break;
-                    scores(t, 0);
-                }
-            for (int i = 0; ok && i < x.n_tiles; ++i) {
-                for (int t = 0; ok && t < kTiles; ++t) {
-                    if (i >= x.n[t]) continue;
-                    const uint32_t fill = values + i, slot = fill % NV;
-                    if (!(ok = wait(&sh.v_full[slot], (fill / NV) & 1) && wait(&sh.p_full[t], (steps[t] + i) & 1))) break;
-                    tc_fence_after_sync();
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)  // 16 keys of weights are 8 columns
-                            mma_bf16_ta(tmem + L::kOut + t * V, tmem + t * kKeys + 8 * k, dv + ((slot * L::kVTile + k * 2048) >> 4), id_o,
-                                        (i > 0 || k > 0) ? 1u : 0u);
-                        if (t == 1 || i >= x.n[1]) mma_commit(&sh.v_empty[slot]);
-                        mma_commit(&sh.pv_done[t]);
+                };
+                for (int t = 0; ok && t < kTiles; ++t)
+                    if (x.n[t] > 0) {
+                        if (!(ok = wait(&sh.q_full[t], queries[t] & 1))) break;
+                        scores(t, 0);
                     }
-                    __syncwarp();
-                    if (i + 1 < x.n[t]) scores(t, i + 1);
+                for (int i = 0; ok && i < x.n_tiles; ++i) {
+                    for (int t = 0; ok && t < kTiles; ++t) {
+                        if (i >= x.n[t]) continue;
+                        const uint32_t fill = values + i, slot = fill % NV;
+                        if (!(ok = wait(&sh.v_full[slot], (fill / NV) & 1) && wait(&sh.p_full[t], (steps[t] + i) & 1))) break;
+                        tc_fence_after_sync();
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)  // 16 keys of weights are 8 columns
+                                mma_bf16_ta(tmem + L::kOut + t * V, tmem + t * kKeys + 8 * k, dv + ((slot * L::kVTile + k * 2048) >> 4), id_o,
+                                            (i > 0 || k > 0) ? 1u : 0u);
+                            if (t == 1 || i >= x.n[1]) mma_commit(&sh.v_empty[slot]);
+                            mma_commit(&sh.pv_done[t]);
+                        }
+                        __syncwarp();
+                        if (i + 1 < x.n[t]) scores(t, i + 1);
+                    }
+                }
+                keys += x.n_tiles * QB;
+                values += x.n_tiles;
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    steps[t] += x.n[t];
+                    queries[t] += x.n[t] > 0;
                 }
             }
-            keys += x.n_tiles * QB;
-            values += x.n_tiles;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                steps[t] += x.n[t];
-                queries[t] += x.n[t] > 0;
-            }
+            if (!ok && lane == 0) record(a.error, 65);
+            if (leader) mma_commit(&sh.drained);
+            mbar_wait_brief(&sh.drained, 0);
         }
-        if (!ok && lane == 0) record(a.error, 65);
-        if (leader) mma_commit(&sh.drained);
-        mbar_wait_brief(&sh.drained, 0);
-    }
     }
     __syncwarp();
     tc_fence_before_sync();

@@ -3,9 +3,10 @@ implementations written from the formulas (per sequence, no paging).
 
 Tolerances (derived, not fitted), both forms of the attention.  With u = 2^-8,
 bf16's largest relative rounding error:
-- Weights enter the second product rounded to bf16 and the sum takes the rounded
-  ones: sum_j p_j (1 + e_j) v_j / sum_j p_j (1 + e_j) with |e_j| <= u is off by
-  at most u (sum_j p_j |v_j| + |o|) / (1 - u).
+- Weights enter the second product rounded to bf16.  Where the sum takes the
+  rounded ones, sum_j p_j (1 + e_j) v_j / sum_j p_j (1 + e_j) with |e_j| <= u is
+  off by at most u (sum_j p_j |v_j| + |o|) / (1 - u); where it takes the
+  unrounded ones, by u sum_j p_j |v_j|, which is less.
 - The result's own rounding: u |o| (of the computed one: times 1 + 2 u).
 - Scores: at most 53 additions of exact products one after another in fp32 (36
   steps of the tensor core and 16 products within one, each possibly truncated:
