@@ -1,6 +1,8 @@
 // C-ABI entry points of the latent cache, of both forms of its attention and of
 // page copies (declared in include/gdn.h): host-side validation, error
 // reporting and dispatch on the caller's stream.
+#include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdlib>
 #include <memory>
@@ -117,6 +119,15 @@ gdn_status check_rows(const gdn_rows* r, const char* name, gdn::KvRows* out, con
     return GDN_OK;
 }
 
+// Whether rows that are written may overlap: false where one axis' rows lie apart and
+// the other one steps over all of them.
+bool rows_overlap(const gdn::KvRows& r, long long tokens, long long heads, long long width) {
+    const long long ts = tokens > 1 ? r.token_stride : LLONG_MAX, hs = heads > 1 ? r.head_stride : LLONG_MAX;
+    if (ts < width || hs < width) return true;
+    if (tokens == 1 || heads == 1) return false;
+    return (ts - width) / (heads - 1) < hs && (hs - width) / (tokens - 1) < ts;
+}
+
 }  // namespace
 
 extern "C" {
@@ -140,8 +151,8 @@ gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache
     if (q_rope) {
         if ((st = check_rows(q_rope, "q_rope", &a.q, fn)) != GDN_OK) return st;
         if ((st = check_rows(q_out, "q_out", &a.q_out, fn)) != GDN_OK) return st;
-        if ((a.b.n_tokens > 1 && q_out->token_stride < dims->rope_dim) || (dims->n_heads > 1 && q_out->head_stride < dims->rope_dim))
-            return set_error(GDN_ERR_INVALID_ARG, fn, "q_out's rows overlap (a stride below %d)", dims->rope_dim);
+        if (rows_overlap(a.q_out, a.b.n_tokens, dims->n_heads, dims->rope_dim))
+            return set_error(GDN_ERR_INVALID_ARG, fn, "q_out's rows overlap, or its tokens and heads interleave");
     }
     if (rope && (rope_len < 1 || !aligned16(rope)))
         return set_error(GDN_ERR_INVALID_ARG, fn, "rope must hold at least one row and be 16-byte aligned");
@@ -271,8 +282,20 @@ gdn_status gdn_copy_pages(int32_t n_buffers, void* const* bases, const size_t* p
             return set_error(GDN_ERR_INVALID_ARG, fn, "array %d: NULL, or its base or page_bytes is no multiple of 4", b);
         if (page_bytes[b] > 1u << 30) return set_error(GDN_ERR_UNSUPPORTED, fn, "array %d: pages above 2^30 bytes", b);
     }
+    struct Free { void operator()(void* p) const { std::free(p); } };
+    // arrays side by side: a page of one that is written is no page of another
+    struct Range { uintptr_t begin, end; };
+    std::unique_ptr<Range, Free> ranges(static_cast<Range*>(std::malloc(n_buffers * sizeof(Range))));
+    if (!ranges) return set_error(GDN_ERR_WORKSPACE, fn, "no host memory for %d arrays", n_buffers);
+    Range* const r = ranges.get();
+    for (int b = 0; b < n_buffers; ++b) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(bases[b]);
+        r[b] = Range{at, at + static_cast<size_t>(n_pages) * page_bytes[b]};
+    }
+    std::sort(r, r + n_buffers, [](const Range& x, const Range& y) { return x.begin < y.begin; });
+    for (int b = 1; b < n_buffers; ++b)
+        if (r[b].begin < r[b - 1].end) return set_error(GDN_ERR_INVALID_ARG, fn, "two arrays overlap");
     // one bit a page: the pages that are written (zeroed memory is taken as it is touched)
-    struct Free { void operator()(uint32_t* p) const { std::free(p); } };
     std::unique_ptr<uint32_t, Free> written(static_cast<uint32_t*>(std::calloc(static_cast<size_t>(n_pages) / 32 + 1, 4)));
     if (!written) return set_error(GDN_ERR_WORKSPACE, fn, "no host memory for %d pages", n_pages);
     for (int i = 0; i < n_pairs; ++i) {

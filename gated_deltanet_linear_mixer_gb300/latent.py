@@ -152,7 +152,8 @@ def expanded_attention(d: LatentDims, cu_q, cu_kv, q, k, k_rope, v, *, out=None)
 def copy_pages(caches, src, dst) -> None:
     """gdn_copy_pages: page src[i] to page dst[i] in a cache (KVCache or LatentCache), or in each of a
     list of them (the layers of a stack, which share a block table).  src, dst: lists of ints, or
-    1-d int32 tensors on the host; no page may be written twice, or both read and written."""
+    1-d int32 tensors on the host; no page may be written twice, or both read and written, and no
+    cache given twice."""
     tensors = []
     for c in caches if isinstance(caches, (list, tuple)) else (caches,):
         if isinstance(c, KVCache):

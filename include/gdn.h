@@ -490,9 +490,12 @@ typedef struct gdn_latent_cache {
  *   NULL: as in gdn_kv_append.
  *   q_rope [T, n_heads, rope_dim] rows or NULL, q_out the same (its memory is
  *   written; may be q_rope itself): rows of a wider query buffer, its last
- *   rope_dim channels, for one.  q_out's rows must not overlap one another.
+ *   rope_dim channels, for one.  q_out's rows must not overlap one another: a
+ *   token's heads lie before the next token's, or a head's tokens before the next
+ *   head's (else refused).
  *   rows_out [T, latent_dim + rope_dim] contiguous or NULL: the rows as stored,
- *   packed, of every token of the call (those of unmapped pages too).
+ *   packed, of every token of the call (those of unmapped pages too); may be c
+ *   itself where that is contiguous.
  */
 gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache* cache,
                              const gdn_kv_batch* batch, const int32_t* kv_lens, const gdn_rows* c,
@@ -542,6 +545,7 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
  *   side), k_rope [Tk, rope_dim] rows (head_stride is not used); token strides
  *   > 0, a head stride of 0 shares one head.  out [Tq, n_heads, v_dim]
  *   contiguous.
+ * The work is laid out by the host copies: a captured call keeps its sequences.
  * Values that some query of a sequence sees have to be finite.  fp32 accumulation
  * and softmax (the hardware's exponentials, 2 ulp), weights bf16 (8 bits); the sum
  * takes them as they are.
@@ -557,9 +561,9 @@ gdn_status gdn_expanded_attention(const gdn_latent_dims* dims, int32_t n_seq, co
  * n_buffers arrays of n_pages pages (page_bytes[b] bytes each, a multiple of 4):
  * a forked sequence's partly filled page, a compacted pool, in the caches of all
  * layers at once; a cache's codes and scales are arrays of their own.  All four
- * lists are on the host and are read before the call returns.  Refused: a page
- * that is written twice, or both read and written.  Pages not named stay as
- * they are.  bases 4-byte aligned (16 bytes, with page_bytes a multiple of 16,
+ * lists are on the host and are read before the call returns (a captured call
+ * keeps its pairs).  Refused: a page that is written twice, or both read and
+ * written, and arrays that overlap.  Pages not named stay as they are.  bases 4-byte aligned (16 bytes, with page_bytes a multiple of 16,
  * is the fast form).
  */
 gdn_status gdn_copy_pages(int32_t n_buffers, void* const* bases, const size_t* page_bytes,

@@ -213,3 +213,85 @@ def test_copied_dims_have_a_struct_of_their_own():
     for e in (copy.deepcopy(d), pickle.loads(pickle.dumps(d)), copy.copy(d)):
         assert e == d and e.address() == ctypes.addressof(e.c())
     assert copy.deepcopy(d).address() != d.address()
+
+
+@pytest.mark.parametrize("heads,token,head,overlap", [
+    (8, 512, 64, False), (8, 504, 64, True), (8, 64, 256, False), (8, 64, 248, True), (8, 64, 64, True),
+    (8, 128, 128, True), (8, 0, 64, True), (8, 512, 0, True), (1, 64, 0, False), (1, 56, 512, True),
+])
+def test_outputs_whose_rows_overlap_are_refused(lib, monkeypatch, heads, token, head, overlap):
+    """4 tokens of 64 channels a head; accepted calls end in the injected failure."""
+    monkeypatch.setenv("GDN_FAULT", "latent_append")
+    got = _append(lib, d=_dims(n_heads=heads), q_out=_r(token=token, head=head))
+    assert got == (1 if overlap else gdn.GDN_ERR_INJECTED)
+    assert ("overlap" in _message(lib)) == overlap
+
+
+@pytest.mark.parametrize("bases,sizes,overlap", [
+    ((P, P + 640), (64, 64), False), ((P, P + 636), (64, 64), True), ((P, P), (64, 64), True),
+    ((P + 640, P), (64, 64), False), ((P + 640, P, P + 320), (64, 32, 32), False), ((P + 640, P, P + 316), (64, 32, 32), True),
+])
+def test_arrays_that_overlap_are_refused(lib, monkeypatch, bases, sizes, overlap):
+    monkeypatch.setenv("GDN_FAULT", "copy_pages")
+    assert _copy(lib, [0], [1], bases=bases, sizes=sizes) == (1 if overlap else gdn.GDN_ERR_INJECTED)
+    assert ("overlap" in _message(lib)) == overlap
+
+
+def _calls(make):
+    """The latent cache's calls as functions of their tensors."""
+    d = gdn.LatentDims(2, 256, page_size=16)
+    b, i, f = torch.bfloat16, torch.int32, torch.float32
+    batch = {"cu": make((2,), i), "lens": make((1,), i), "table": make((1, 2), i)}
+    rows = {"rows": make((3, 16, 320), b)}
+    host = torch.tensor([0, 4], dtype=i)
+
+    def cache(t):
+        return gdn.LatentCache(d, t["rows"])
+
+    def append(t):
+        gdn.latent_append(d, cache(t), (t["cu"], host), t["lens"], t["table"], t["c"], norm_w=t["norm_w"], q_rope=t["q_rope"],
+                          q_out=t["q_out"], rope=t["rope"], positions=t["positions"], rows_out=t["rows_out"])
+
+    def read(t):
+        gdn.latent_read(d, cache(t), (t["cu"], host), t["lens"], t["table"], out=t["out"])
+
+    def attend(t):
+        gdn.latent_attention(d, cache(t), (t["cu"], host), t["lens"], t["table"], t["q"], out=t["out"], workspace=t["ws"])
+
+    def expand(t):
+        gdn.expanded_attention(d, (t["cu"], host), (t["ck"], host), t["q"], t["k"], t["k_rope"], t["v"], out=t["out"])
+
+    def copy(t):
+        gdn.copy_pages([cache(t), gdn.LatentCache(d, t["more"])], [0], [1])
+
+    return {
+        "append": (append, {**batch, **rows, "c": make((4, 320), b), "norm_w": make((256,), f), "q_rope": make((4, 2, 64), b),
+                            "q_out": make((4, 2, 64), b), "rope": make((9, 64), f), "positions": make((4,), i),
+                            "rows_out": make((4, 320), b)}),
+        "read": (read, {**batch, **rows, "out": make((4, 320), b)}),
+        "attend": (attend, {**batch, **rows, "q": make((4, 2, 320), b), "out": make((4, 2, 256), b),
+                            "ws": make((1 << 20,), torch.uint8)}),
+        "expand": (expand, {"cu": make((2,), i), "ck": make((2,), i), "q": make((4, 2, 192), b), "k": make((4, 2, 128), b),
+                            "k_rope": make((4, 64), b), "v": make((4, 2, 128), b), "out": make((4, 2, 128), b)}),
+        "copy": (copy, {**rows, "more": make((3, 16, 320), b)}),
+    }
+
+
+@pytest.mark.parametrize("name", ["append", "read", "attend", "expand", "copy"])
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_tensors_of_two_devices_are_refused(name):
+    """Each tensor in turn on another device than the rest."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    mode = FakeTensorMode(allow_non_fake_inputs=True)
+
+    def on(device):
+        def make(shape, dtype):
+            with mode:
+                return torch.empty(shape, dtype=dtype, device=device)
+        return make
+
+    call, args = _calls(on("cuda:0"))[name]
+    _, others = _calls(on("cuda:1"))[name]
+    for moved in args:
+        with pytest.raises(ValueError, match="device"):
+            call({**args, moved: others[moved]})
