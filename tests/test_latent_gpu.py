@@ -617,3 +617,126 @@ def test_expanded_attention_reports_a_wait_that_runs_out(monkeypatch):
     got = gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v)
     _status_ok()
     check(got, *expanded(d, counts, lens, q, k, r, v))
+
+
+# ------------------------------------------------- strides, streams, graphs
+@pytest.mark.parametrize("heads,counts,lens", [(16, [1, 1, 1], [70, 300, 1]), (8, [9, 40], [500, 41])])
+@pytest.mark.parametrize("form", ["head_stride_0", "token_stride_0", "heads_first", "wide"])
+def test_absorbed_queries_with_any_strides(heads, counts, lens, form):
+    d = gdn.LatentDims(heads, 256, page_size=32)
+    t, g = sum(counts), gen(161)
+    cache, table = make_cache(d, lens, 162)
+    if form == "head_stride_0":
+        q = torch.randn(t, 1, 320, generator=g, device="cuda").bfloat16().expand(t, heads, 320)
+    elif form == "token_stride_0":
+        q = torch.randn(1, heads, 320, generator=g, device="cuda").bfloat16().expand(t, heads, 320)
+    elif form == "heads_first":
+        q = torch.randn(heads, t, 320, generator=g, device="cuda").bfloat16().transpose(0, 1)
+    else:
+        q = torch.randn(t, heads + 1, 384, generator=g, device="cuda").bfloat16()[:, 1:, 40:360]
+    got = gdn.latent_attention(d, cache, cu_of(counts), ints(lens), table, q)
+    check(got, *absorbed(d, cache, counts, lens, table, q))
+    _status_ok()
+
+
+@pytest.mark.parametrize("form", ["heads_first", "head_stride_0"])
+def test_expanded_rows_with_any_strides(form):
+    d = gdn.LatentDims(5, nope_dim=64, v_dim=128)
+    g = gen(163)
+
+    def make(t, width):
+        if form == "heads_first":
+            return torch.randn(5, t, width, generator=g, device="cuda").bfloat16().transpose(0, 1)
+        return torch.randn(t, 1, width, generator=g, device="cuda").bfloat16().expand(t, 5, width)
+
+    counts, lens = [3, 150], [200, 150]
+    q, k, v = make(153, 128), make(350, 64), make(350, 128)
+    r = torch.randn(350, 192, generator=g, device="cuda").bfloat16()[:, 64:128]
+    check(gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v), *expanded(d, counts, lens, q, k, r, v))
+    _status_ok()
+
+
+def test_rows_are_packed_into_the_appended_ones():
+    """rows_out may be c itself."""
+    d = gdn.LatentDims(2, 512, page_size=16, rope_style="interleaved")
+    g = gen(164)
+    cache, table = make_cache(d, [300], 165)
+    c = torch.randn(300, 576, generator=g, device="cuda").bfloat16()
+    w, tab = torch.rand(512, generator=g, device="cuda") + 0.5, rope_table(300)
+    packed = torch.empty_like(c)
+    gdn.latent_append(d, cache, [0, 300], ints([300]), table, c, norm_w=w, rope=tab, rows_out=packed)
+    gdn.latent_append(d, cache, [0, 300], ints([300]), table, c, norm_w=w, rope=tab, rows_out=c)
+    assert torch.equal(c, packed)
+    assert torch.equal(gdn.latent_read(d, cache, [0, 300], ints([0]), table), packed)
+    _status_ok()
+
+
+def test_calls_on_two_streams_and_graphs_at_once():
+    """Two captured calls with a workspace each, replayed on streams of their own."""
+    d = gdn.LatentDims(32, 512)
+    runs = []
+    for i, (counts, lens) in enumerate([([1, 1, 1], [5000, 3, 900]), ([4], [3000])]):
+        cache, table = make_cache(d, lens, 170 + i)
+        q = _queries(sum(counts), 32, 576, 172 + i)
+        cu, n, ws = cu_of(counts), ints(lens), None
+        ws = torch.empty(gdn.latent_attention_workspace_size(d, cu), dtype=torch.uint8, device="cuda")
+        out = torch.empty(sum(counts), 32, 512, dtype=torch.bfloat16, device="cuda")
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            gdn.latent_attention(d, cache, cu, n, table, q, out=out, workspace=ws)
+        runs.append((graph, stream, out, absorbed(d, cache, counts, lens, table, q), (cache, table, q, cu, n, ws)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, out, want, _ in runs:
+        check(out, *want)
+    _status_ok()
+
+
+def test_copies_of_thousands_of_pairs():
+    cache = _filled(gdn.LatentDims(1, 256, page_size=16), 9001, 3)
+    order = torch.randperm(9001, generator=torch.Generator().manual_seed(5)).to(torch.int32)
+    src, dst = order[:4500].contiguous(), order[4500:9000].contiguous()
+    want = cache.rows.clone()
+    want[dst.long().cuda()] = want[src.long().cuda()]
+    gdn.copy_pages(cache, src.tolist(), dst)
+    assert torch.equal(cache.rows.view(torch.int16), want.view(torch.int16))
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing is set up by an eager call that a captured one needs."""
+    import subprocess
+    import sys
+    code = """
+import torch, gated_deltanet_linear_mixer_gb300 as gdn
+d = gdn.LatentDims(4, 256, page_size=16)
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+rows = torch.ones(4, 16, 320, device="cuda").bfloat16()
+cache, table, lens, starts = gdn.LatentCache(d, rows), i([[2, 0]]), i([20]), i([0])
+cu = (i([0, 20]), torch.tensor([0, 20], dtype=torch.int32))
+c = torch.full((20, 320), 2.0, device="cuda").bfloat16()
+q, qe = torch.ones(20, 4, 320, device="cuda").bfloat16(), torch.ones(20, 4, 192, device="cuda").bfloat16()
+k, v = torch.ones(20, 4, 128, device="cuda").bfloat16(), torch.full((20, 4, 128), 3.0, device="cuda").bfloat16()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    gdn.latent_append(d, cache, cu, lens, table, c)
+    o = gdn.latent_attention(d, cache, cu, lens, table, q)
+    e = gdn.expanded_attention(d, cu, cu, qe, k, c[:, 256:], v)
+    gdn.copy_pages(cache, [2], [3])
+    r = gdn.latent_read(d, cache, cu, starts, table)
+assert bool((rows == 1).all())
+g.replay()
+torch.cuda.synchronize()
+gdn.sync_status()
+assert bool((o == 2).all()) and bool((e == 3).all()) and bool((r == 2).all()) and bool((rows[3] == 2).all())
+assert bool((rows[0, :4] == 2).all()) and bool((rows[0, 4:] == 1).all())
+"""
+    import pathlib
+    got = subprocess.run([sys.executable, "-c", code], cwd=pathlib.Path(__file__).parents[1], capture_output=True, text=True,
+                         timeout=300)
+    assert got.returncode == 0, got.stderr[-2000:]
