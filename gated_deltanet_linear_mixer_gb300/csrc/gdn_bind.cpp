@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <initializer_list>
+#include <memory>
 #include <optional>
 #include <string>
 #include <vector>
@@ -518,10 +519,13 @@ std::vector<int32_t> pages_of(PyObject* o, const char* name) {
     }
     if (!PyList_Check(o) && !PyTuple_Check(o))
         bad(PyExc_TypeError, "%s must be a list of page numbers or a 1-d host tensor", name);
-    PyObject** items = PySequence_Fast_ITEMS(o);
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
-    v.reserve(n);
-    for (Py_ssize_t i = 0; i < n; ++i) v.push_back(as_int(items[i]));
+    v.reserve(PySequence_Fast_GET_SIZE(o));
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(o); ++i) {  // an item's __index__ may change the list
+        PyObject* item = PySequence_Fast_GET_ITEM(o, i);
+        Py_INCREF(item);
+        const std::unique_ptr<PyObject, void (*)(PyObject*)> held(item, Py_DecRef);
+        v.push_back(as_int(item));
+    }
     return v;
 }
 

@@ -295,3 +295,17 @@ def test_tensors_of_two_devices_are_refused(name):
     for moved in args:
         with pytest.raises(ValueError, match="device"):
             call({**args, moved: others[moved]})
+
+
+def test_page_lists_may_change_while_they_are_read():
+    """A list whose items' __index__ shortens it is read to its end as it is then."""
+    src = []
+
+    class Page:
+        def __index__(self):
+            del src[1:]
+            return 3
+
+    src += [Page(), Page(), Page()]
+    with pytest.raises(ValueError, match=r"\(1, 3\)"):
+        gdn.copy_pages([], src, [0, 1, 2])
