@@ -14,9 +14,11 @@
 // O as many; the weights overwrite their scores' columns and are the second
 // product's A operand where they lie.  Keys stream through a ring of
 // 16 KB blocks (128 keys x 64 channels), values through one of whole tiles; the
-// position keys come from their own array, which all heads share.  Thread blocks
-// stay: each takes its share of (sequence, queries, head) items, the longest first,
-// and loads the next item while it finishes one.
+// position keys come from their own array, which all heads share.  There is a thread
+// block an item (sequence, queries, head), the longest first, and one that is done
+// takes on the item of a block that has not started (try_cancel), whose loads begin
+// while it finishes its own: 137 and 172 us where every 152nd item was a block's from
+// the start, 131 and 163 us so (the two cases below).
 //
 // Roles: 8 softmax warps (a thread a row; a rescaling concerns one warp's rows
 // alone), a warp for the loads, one issuing the products, in the order
@@ -31,12 +33,12 @@
 // bandwidth, which those products use in full.  About 3700 cycles are reached: what
 // remains are the queries' loads at an item's start and keys that wait for room (the
 // queries leave room for 1.6 tiles of keys).  The exponentials (32 a cycle and SM: 1024
-// cycles) do not bound it.  4096 tokens, 32 heads: 137 us, 1.26 PFLOP/s; 16
-// prompts of 1 to 4096 tokens: 172 us, 0.94 PFLOP/s, where short items and the
-// last thread blocks' tails weigh more.
+// cycles) do not bound it.  4096 tokens, 32 heads: 131 us, 1.31 PFLOP/s; 16
+// ragged prompts of up to 1100 tokens behind up to 3000: 163 us, 0.99 PFLOP/s, where
+// short items and tiles that are partly masked weigh more.
 //
-// Tried and slower (us, the two cases above): pairs of thread blocks that share keys
-// (134 and 215 where a block of the same form took 141 and 179); two threads a
+// Tried and slower (us, the two cases above, with fixed shares): pairs of thread blocks
+// that share keys (134 and 215 where a block of the same form took 141 and 179); two threads a
 // row (165 against 140); weights handed over by halves (144); an issuing warp per
 // tile (146 and 180); one ring for keys and values (148 and 190); a thread that
 // polls both tiles' barriers and issues what is ready (149); scores read by one
@@ -77,7 +79,17 @@ template <int NOPE, int V> struct ECfg {
     static_assert(NK > kQBlocks && NK <= kMaxSlots && NV <= kMaxSlots, "a tile's keys and some of the next one's fit");
 };
 
+// One block of queries of a head.
+struct Item {
+    int h, q0, qn, k0, kv, row0, start;  // h < 0: there is none
+    int n[kTiles], n_tiles;              // key tiles of each query tile
+};
+constexpr int kItems = 2;  // that the loading warp tells the others of
+
 struct Shared {
+    uint4 next;  // the answer to a request for another thread block's item
+    uint64_t next_full, item_full[kItems], item_empty[kItems];
+    Item item[kItems];
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
     uint64_t q_full[kTiles], q_empty[kTiles], s_full[kTiles], p_full[kTiles], pv_done[kTiles], drained;
     uint32_t tmem_slot;
@@ -145,11 +157,30 @@ struct Plan {
     uint32_t pair[kPairs];     // sequence << 16 | block
 };
 
-// One block of queries of a head.
-struct Item {
-    int h, q0, qn, k0, kv, row0, start;
-    int n[kTiles], n_tiles;  // key tiles of each query tile
-};
+// Asks for a thread block of this grid that has not started, which then never does: its
+// number comes into the 16 bytes at `to`, and completes as many on `bar`.
+__device__ __forceinline__ void ask_for_block(uint4* to, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(to)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The answer: a block, or -1 where none was left (no more may be asked for then).
+__device__ __forceinline__ int block_answered(const uint4* at) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        ".reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(at))
+        : "memory");
+    return got ? static_cast<int>(x) : -1;
+}
 
 template <int NOPE, int V>
 __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArgs a, const __grid_constant__ Plan plan) {
@@ -159,12 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem + L::kSharedAt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // This thread block's items: every gridDim.x-th, the order turning round after each.
-    const int team = blockIdx.x, n_teams = gridDim.x;
     const long long items = (plan.n_pairs < 0 ? static_cast<long long>(plan.blocks) * a.n_seq : plan.n_pairs) * a.n_heads;
-    const int rounds = static_cast<int>((items + n_teams - 1) / n_teams);
-    auto item_of = [&](int round, Item& x) {  // whether there is one
-        const long long at = static_cast<long long>(round) * n_teams + (round & 1 ? n_teams - 1 - team : team);
+    auto item_of = [&](long long at, Item& x) {  // whether there is one
         if (at >= items) return false;
         const int p = static_cast<int>(at / a.n_heads);
         int seq, block;
@@ -191,6 +218,15 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         x.n_tiles = max(x.n[0], x.n[1]);
         return true;
     };
+    // The k-th item as the loading warp tells it; false where the wait for it gave up.
+    auto take = [&](uint32_t k, Item& x) {
+        const uint32_t s = k % kItems;
+        if (!__all_sync(0xffffffffu, mbar_wait_brief(&sh.item_full[s], (k / kItems) & 1))) return false;
+        x = sh.item[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[s]);
+        return true;
+    };
     if (smem_u32(smem) & 1023u) {
         if (tid == 0) record(a.error, 66);
         return;
@@ -211,6 +247,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             mbar_init(&sh.p_full[t], 4);
             mbar_init(&sh.pv_done[t], 1);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], 9);
+        }
+        mbar_init(&sh.next_full, 1);
         mbar_init(&sh.drained, 1);
         fence_barrier_init();
     }
@@ -238,9 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         const float scale2 = a.scale * kLog2e;
         bool ok = true;
         uint32_t steps = 0, values = 0;  // key tiles of this query tile so far, of the items before
-        for (int round = 0; round < rounds; ++round) {
+        for (uint32_t item = 0; ok; ++item) {
             Item x;
-            if (!item_of(round, x)) continue;
+            if (!(ok = take(item, x)) && lane == 0) record(a.error, 60);
+            if (!ok || x.h < 0) break;
             const int row = x.row0 + t * kM + r, n = t ? x.n[1] : x.n[0];
             const bool mine = row < x.qn;
             const int lim = mine ? max(0, min(x.start + row + 1, x.kv)) : 0;  // keys that the row sees
@@ -351,11 +393,53 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         if (warp == 8) {
             // ---- loads
             const bool leader = elect_one();
-            bool ok = !a.stall;  // the test hook
+            bool ok = true;
             uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0};  // fills so far
-            for (int round = 0; ok && round < rounds; ++round) {
+            const bool others = plan.n_pairs >= 0;  // a block an item: this one's, then those of blocks that never start
+            uint32_t asked = 0;
+            auto ask = [&] {
+                __syncwarp();
+                if (leader) {
+                    fence_proxy_async_smem();  // the last answer was read
+                    mbar_arrive_expect_tx(&sh.next_full, sizeof(sh.next));
+                    ask_for_block(&sh.next, &sh.next_full);
+                }
+                ++asked;
+            };
+            auto answer = [&] {  // of the last one asked for
+                if (!__all_sync(0xffffffffu, mbar_wait_brief(&sh.next_full, (asked - 1) & 1))) {
+                    ok = false;
+                    return -1;
+                }
+                return block_answered(&sh.next);
+            };
+            int at = blockIdx.x, round = 0;
+            bool waiting = false;  // for an answer
+            for (uint32_t item = 0; ok; ++item) {
                 Item x;
-                if (!item_of(round, x)) continue;
+                bool some = false;
+                if (others) {
+                    some = at >= 0 && item_of(at, x);
+                } else {  // every gridDim.x-th, the order turning round after each
+                    const long long n = gridDim.x;
+                    while (!some && round * n < items) {
+                        some = item_of(round * n + (round & 1 ? n - 1 - at : at), x);
+                        ++round;
+                    }
+                }
+                if (!some) x.h = -1;
+                const uint32_t place = item % kItems;
+                if (item >= kItems && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.item_empty[place], (item / kItems - 1) & 1)))) break;
+                if (leader) {
+                    sh.item[place] = x;
+                    mbar_arrive(&sh.item_full[place]);
+                }
+                __syncwarp();
+                if (!some) break;
+                if (a.stall) {  // the test hook
+                    ok = false;
+                    break;
+                }
                 auto load_queries = [&](int t) {  // once the products with the tile's last ones are done
                     if ((t ? x.n[1] : x.n[0]) == 0) return;
                     uint32_t& before = t ? queries[1] : queries[0];
@@ -370,7 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                     __syncwarp();
                 };
                 load_queries(0);
+                const int early = max(0, x.n_tiles - 2);  // an answer takes less than two tiles
+                if (others && x.n_tiles == 0) ask(), waiting = true;
                 for (int i = 0; ok && i < x.n_tiles; ++i) {
+                    if (others && i == early) ask(), waiting = true;
                     if (i == 1) load_queries(1);  // behind the first tile's first keys and values
                     if (!ok) break;
                     const int key = x.k0 + i * kKeys;
@@ -399,9 +486,18 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                     __syncwarp();
                 }
                 if (ok && x.n_tiles == 1) load_queries(1);
+                if (ok && others) {
+                    at = answer();
+                    waiting = !ok;
+                }
             }
-            if (!ok) {  // nothing is in flight when the memory is given back
+            if (!ok) {  // nothing is in flight when the memory is given back, and no block starts to wait like this one
                 if (lane == 0) record(a.error, 64);
+                if (others && at >= 0) {
+                    ok = true;
+                    if (!waiting) ask();
+                    while (ok && answer() >= 0) ask();
+                }
                 for (uint32_t f = keys > NK ? keys - NK : 0; f < keys; ++f) mbar_wait_brief(&sh.k_full[f % NK], (f / NK) & 1);
                 for (uint32_t f = values > NV ? values - NV : 0; f < values; ++f) mbar_wait_brief(&sh.v_full[f % NV], (f / NV) & 1);
                 for (int t = 0; t < kTiles; ++t)
@@ -416,9 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_brief(bar, parity)) != 0; };
             bool ok = true;
             uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0}, steps[kTiles] = {0, 0};  // of the items before this one
-            for (int round = 0; ok && round < rounds; ++round) {
+            for (uint32_t item = 0; ok; ++item) {
                 Item x;
-                if (!item_of(round, x)) continue;
+                if (!(ok = take(item, x)) || x.h < 0) break;
                 // scores of tile t and key tile i; the last tile that uses a block gives it back
                 auto scores = [&](int t, int i) {
                     const bool give = t == 1 || i >= x.n[1];
@@ -490,7 +586,7 @@ bool map_rows(CUtensorMap* map, const KvRows& r, int tokens, int heads, int widt
                                 r.head_stride ? r.head_stride : r.token_stride, 64, 128, 1);
 }
 
-// Key tiles that the block of queries from row0 on walks (0 where it has no queries).
+// Key tiles that the tile of queries from row0 on walks (0 where it has no queries).
 int key_tiles(int q, int kv, int row0, int rows) {
     if (row0 >= q) return 0;
     return std::max(0, kv - q + std::min(row0 + rows, q) - 1 + kKeys) / kKeys;
@@ -517,7 +613,8 @@ cudaError_t expanded_t(const ExpandedArgs& a, cudaStream_t st) {
         for (int i = 0; i < a.n_seq; ++i) {
             const int q = a.cu_q_host[i + 1] - a.cu_q_host[i], kv = a.cu_kv_host[i + 1] - a.cu_kv_host[i];
             for (int b = 0; b * static_cast<long long>(rows) < q; ++b) {
-                cost[plan.n_pairs] = key_tiles(q, kv, b * rows, rows);
+                const int n0 = key_tiles(q, kv, b * rows, kM), n1 = key_tiles(q, kv, b * rows + kM, kM);
+                cost[plan.n_pairs] = 3 * std::min(n0, n1) + 7 * std::max(n0, n1);  // two steps side by side: 10, one alone: 7
                 plan.pair[plan.n_pairs++] = static_cast<uint32_t>(i) << 16 | b;
             }
         }
@@ -532,7 +629,7 @@ cudaError_t expanded_t(const ExpandedArgs& a, cudaStream_t st) {
         plan.n_pairs = -1;
     }
     if (n * a.n_heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = static_cast<unsigned>(std::min(n * a.n_heads, static_cast<long long>(kSms)));
+    const unsigned grid = static_cast<unsigned>(plan.n_pairs < 0 ? std::min(n * a.n_heads, static_cast<long long>(kSms)) : n * a.n_heads);
     return timed_launch("expanded_attention", st, [&] {
         expanded_kernel<NOPE, V><<<grid, kThreads, L::kSmem, st>>>(a, plan);
         return cudaGetLastError();
