@@ -82,7 +82,8 @@ template <int NOPE, int V> struct ECfg {
 // One block of queries of a head.
 struct Item {
     int h, q0, qn, k0, kv, row0, start;  // h < 0: there is none
-    int n[kTiles], n_tiles;              // key tiles of each query tile
+    int n0, n1, n_tiles;                 // key tiles of each query tile; that are loaded
+    int step;                            // 2: both are the first one, which walk every other key tile each
 };
 constexpr int kItems = 2;  // that the loading warp tells the others of
 
@@ -92,6 +93,8 @@ struct Shared {
     Item item[kItems];
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
     uint64_t q_full[kTiles], q_empty[kTiles], s_full[kTiles], p_full[kTiles], pv_done[kTiles], drained;
+    uint64_t stat_full[kTiles], merged[kTiles];  // of query tiles that were walked by halves
+    float2 stat[kTiles][kM];                     // their references and sums
     uint32_t tmem_slot;
 };
 static_assert(sizeof(Shared) <= kSharedBytes, "part of kSmem");
@@ -223,12 +226,19 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         x.row0 = block * kRows;  // tile t: rows row0 + t kM onwards
         if (x.row0 >= x.qn) return false;
         x.start = x.kv - x.qn;  // position of the sequence's first query
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
+        auto tiles = [&](int t) {
             const int last = min(x.row0 + (t + 1) * kM, x.qn) - 1;  // the tile's last query
-            x.n[t] = last >= x.row0 + t * kM && x.start + last >= 0 ? (x.start + last) / kKeys + 1 : 0;
+            return last >= x.row0 + t * kM && x.start + last >= 0 ? (x.start + last) / kKeys + 1 : 0;
+        };
+        x.n0 = tiles(0);
+        x.n1 = tiles(1);
+        x.n_tiles = max(x.n0, x.n1);
+        x.step = 1;
+        if (x.row0 + kM >= x.qn && x.n_tiles > 1) {
+            x.step = 2;
+            x.n1 = x.n_tiles / 2;
+            x.n0 -= x.n1;
         }
-        x.n_tiles = max(x.n[0], x.n[1]);
         return true;
     };
     // The k-th item as the loading warp tells it; false where the wait for it gave up.
@@ -259,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             mbar_init(&sh.s_full[t], 1);
             mbar_init(&sh.p_full[t], 4);
             mbar_init(&sh.pv_done[t], 1);
+            mbar_init(&sh.stat_full[t], 4);
+            mbar_init(&sh.merged[t], 4);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
@@ -282,9 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem_slot;
 
-    // the softmax holds a row's scores in registers: 2 x 208 + 88 of the 3 x 168 that a thread block has
+    // the softmax holds a row's scores in registers: 2 x 192 + 120 of the 3 x 168 that a thread block has (with 208 and 88
+    // the issuing warp spills: 136 and 159 us where the two cases take 125 and 145)
     if (warp < 8) {
-        regs_inc<208>();
+        regs_inc<192>();
         // ---- softmax: a thread's row
         const int t = warp >> 2, r = tid & (kM - 1);
         const uint32_t t_lane = (32u * (warp & 3)) << 16;
@@ -292,18 +305,19 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         const float scale2 = a.scale * kLog2e;
         const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         bool ok = true;
-        uint32_t steps = 0, values = 0;  // key tiles of this query tile so far, of the items before
+        uint32_t steps = 0, values = 0, merges = 0;  // key tiles of this query tile so far, of the items before
         for (uint32_t item = 0; ok; ++item) {
             Item x;
             if (!(ok = take(item, x)) && lane == 0) record(a.error, 60);
             if (!ok || x.h < 0) break;
-            const int row = x.row0 + t * kM + r, n = t ? x.n[1] : x.n[0];
+            const int row = x.row0 + (x.step == 2 ? 0 : t * kM) + r, n = t ? x.n1 : x.n0;
             const bool mine = row < x.qn;
             const int lim = mine ? max(0, min(x.start + row + 1, x.kv)) : 0;  // keys that the row sees
             const int low = __reduce_min_sync(0xffffffffu, lim);
             float m = -INFINITY, l = 0.0f;
-            for (int i = 0; i < n; ++i, ++steps) {
-                const int key0 = i * kKeys;
+            int kt = x.step == 2 ? t : 0;  // the key tile
+            for (int i = 0; i < n; ++i, ++steps, kt += x.step) {
+                const int key0 = kt * kKeys;
                 // A wait that gave up is not waited for again, but the warp goes on through the tiles (with
                 // results that are invalid): the barriers between the warps stay complete.
                 if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_full[t], steps & 1))) && lane == 0) record(a.error, 60);
@@ -364,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                 }
                 // rows behind the sequence's last key may be anything: weights of 0 do not undo a NaN.  By the
                 // first of the tiles that use them.
-                if (key0 + kKeys > x.kv && (t == 0 || i >= x.n[0])) {
-                    const uint32_t slot = (values + i) % NV;
-                    if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.v_full[slot], ((values + i) / NV) & 1))) && lane == 0)
+                if (key0 + kKeys > x.kv && (t == 0 || i >= x.n0 || x.step == 2)) {
+                    const uint32_t slot = (values + kt) % NV;
+                    if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.v_full[slot], ((values + kt) / NV) & 1))) && lane == 0)
                         record(a.error, 62);
                     for (uint32_t b = 0; b < L::kVTile; b += kBlock) {
                         uint4* rows = reinterpret_cast<uint4*>(smem + L::kVAt + slot * L::kVTile + b);
@@ -384,8 +398,45 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             if (n > 0 && ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.pv_done[t], (steps - 1) & 1))) && lane == 0)
                 record(a.error, 63);
             tc_fence_after_sync();
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a sum that is no number stays one
             bf16* out = static_cast<bf16*>(a.out) + (static_cast<size_t>(x.q0 + row) * a.n_heads + x.h) * V;
+            if (x.step == 2) {  // both halves' results, half of the channels by the warps of each
+                auto meet = [&](uint64_t* bars) {  // the other half's warps
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[t]);
+                    if (ok && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&bars[1 - t], merges & 1))) && lane == 0) record(a.error, 63);
+                    tc_fence_after_sync();
+                };
+                sh.stat[t][r] = make_float2(m, l);
+                meet(sh.stat_full);
+                const float2 s0 = sh.stat[0][r], s1 = sh.stat[1][r];
+                const float top = fmaxf(s0.x, s1.x);
+                float f0 = s0.y == 0.0f ? 0.0f : exp2_ftz(s0.x - top), f1 = s1.y == 0.0f ? 0.0f : exp2_ftz(s1.x - top);
+                const float sum = s0.y * f0 + s1.y * f1, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                f0 *= inv;
+                f1 *= inv;
+                const uint32_t t_both = tmem + t_lane + L::kOut;
+#pragma unroll 1
+                for (int c = t * (V / 2); c < (t + 1) * (V / 2); c += 32) {
+                    float v0[32], v1[32];
+                    tmem_ld32(t_both + c, v0);
+                    tmem_ld32(t_both + V + c, v1);
+                    if (mine && ok) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                y[k] = pack_bf16x2(v0[e + 2 * k] * f0 + v1[e + 2 * k] * f1, v0[e + 2 * k + 1] * f0 + v1[e + 2 * k + 1] * f1);
+                            store32(out + c + e, y, wide);
+                        }
+                    }
+                }
+                meet(sh.merged);  // nothing of the other's is read any more
+                ++merges;
+                continue;
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a sum that is no number stays one
 #pragma unroll 1
             for (int c = 0; c < V; c += 32) {
                 float v[32];
@@ -403,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             tc_fence_before_sync();
         }
     } else {
-        regs_dec<88>();
+        regs_dec<120>();
         if (warp == 8) {
             // ---- loads
             const bool leader = elect_one();
@@ -455,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                     break;
                 }
                 auto load_queries = [&](int t) {  // once the products with the tile's last ones are done
-                    if ((t ? x.n[1] : x.n[0]) == 0) return;
+                    if ((t ? x.n1 : x.n0) == 0 || (t == 1 && x.step == 2)) return;
                     uint32_t& before = t ? queries[1] : queries[0];
                     if (before > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.q_empty[t], (before - 1) & 1)))) return;
                     ++before;
@@ -529,57 +580,66 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             for (uint32_t item = 0; ok; ++item) {
                 Item x;
                 if (!(ok = take(item, x)) || x.h < 0) break;
-                // scores of tile t and key tile i; the last tile that uses a block gives it back
-                auto scores = [&](int t, int i) {
-                    const bool give = t == 1 || i >= x.n[1];
-                    for (int b = 0; b < QB; ++b) {
-                        const uint32_t fill = keys + i * QB + b, slot = fill % NK;
-                        if (!(ok = wait(&sh.k_full[slot], (fill / NK) & 1))) return;
-                        tc_fence_after_sync();
-                        if (leader) {
+                auto walk = [&](auto by_halves) {
+                    constexpr bool kHalves = decltype(by_halves)::value;
+                    auto tile = [](int t, int i) { return kHalves ? 2 * i + t : i; };
+                    // scores of tile t and its i-th key tile; the last tile that uses a block gives it back
+                    auto scores = [&](int t, int i) {
+                        const bool give = kHalves || t == 1 || i >= x.n1;
+                        const int kt = tile(t, i), tq = kHalves ? 0 : t;
+                        for (int b = 0; b < QB; ++b) {
+                            const uint32_t fill = keys + kt * QB + b, slot = fill % NK;
+                            if (!(ok = wait(&sh.k_full[slot], (fill / NK) & 1))) return;
+                            tc_fence_after_sync();
+                            if (leader) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16(tmem + t * kKeys, dq + ((t * L::kQ + b * kBlock) >> 4) + 2 * k, dk + (slot * kBlock >> 4) + 2 * k,
-                                         id_s, (b > 0 || k > 0) ? 1u : 0u);
-                            if (give) mma_commit(&sh.k_empty[slot]);
+                                for (int k = 0; k < 4; ++k)
+                                    mma_bf16(tmem + t * kKeys, dq + ((tq * L::kQ + b * kBlock) >> 4) + 2 * k, dk + (slot * kBlock >> 4) + 2 * k,
+                                             id_s, (b > 0 || k > 0) ? 1u : 0u);
+                                if (give) mma_commit(&sh.k_empty[slot]);
+                            }
+                            __syncwarp();
+                        }
+                        if (leader) {
+                            mma_commit(&sh.s_full[t]);
+                            if (kHalves ? kt == x.n_tiles - 1 : i == (t ? x.n1 : x.n0) - 1) mma_commit(&sh.q_empty[tq]);
                         }
                         __syncwarp();
+                    };
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t)
+                        if (ok && (t ? x.n1 : x.n0) > 0) {
+                            if (!(ok = wait(&sh.q_full[kHalves ? 0 : t], queries[kHalves ? 0 : t] & 1))) break;
+                            scores(t, 0);
+                        }
+                    for (int i = 0; ok && i < x.n_tiles; ++i) {
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t) {
+                            if (!ok || i >= (t ? x.n1 : x.n0)) continue;
+                            const uint32_t fill = values + tile(t, i), slot = fill % NV;
+                            if (!(ok = wait(&sh.v_full[slot], (fill / NV) & 1) && wait(&sh.p_full[t], (steps[t] + i) & 1))) break;
+                            tc_fence_after_sync();
+                            if (leader) {
+#pragma unroll
+                                for (int k = 0; k < kKeys / 16; ++k)  // 16 keys of weights are 8 columns
+                                    mma_bf16_ta(tmem + L::kOut + t * V, tmem + t * kKeys + 8 * k, dv + ((slot * L::kVTile + k * 2048) >> 4), id_o,
+                                                (i > 0 || k > 0) ? 1u : 0u);
+                                if (kHalves || t == 1 || i >= x.n1) mma_commit(&sh.v_empty[slot]);
+                                mma_commit(&sh.pv_done[t]);
+                            }
+                            __syncwarp();
+                            if (i + 1 < (t ? x.n1 : x.n0)) scores(t, i + 1);
+                        }
                     }
-                    if (leader) {
-                        mma_commit(&sh.s_full[t]);
-                        if (i == x.n[t] - 1) mma_commit(&sh.q_empty[t]);
-                    }
-                    __syncwarp();
                 };
-                for (int t = 0; ok && t < kTiles; ++t)
-                    if (x.n[t] > 0) {
-                        if (!(ok = wait(&sh.q_full[t], queries[t] & 1))) break;
-                        scores(t, 0);
-                    }
-                for (int i = 0; ok && i < x.n_tiles; ++i) {
-                    for (int t = 0; ok && t < kTiles; ++t) {
-                        if (i >= x.n[t]) continue;
-                        const uint32_t fill = values + i, slot = fill % NV;
-                        if (!(ok = wait(&sh.v_full[slot], (fill / NV) & 1) && wait(&sh.p_full[t], (steps[t] + i) & 1))) break;
-                        tc_fence_after_sync();
-                        if (leader) {
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)  // 16 keys of weights are 8 columns
-                                mma_bf16_ta(tmem + L::kOut + t * V, tmem + t * kKeys + 8 * k, dv + ((slot * L::kVTile + k * 2048) >> 4), id_o,
-                                            (i > 0 || k > 0) ? 1u : 0u);
-                            if (t == 1 || i >= x.n[1]) mma_commit(&sh.v_empty[slot]);
-                            mma_commit(&sh.pv_done[t]);
-                        }
-                        __syncwarp();
-                        if (i + 1 < x.n[t]) scores(t, i + 1);
-                    }
-                }
+                if (x.step == 2) walk(std::true_type{});
+                else walk(std::false_type{});
                 keys += x.n_tiles * QB;
                 values += x.n_tiles;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    steps[t] += x.n[t];
-                    queries[t] += x.n[t] > 0;
+                    steps[t] += (t ? x.n1 : x.n0);
+                    queries[t] += (t ? x.n1 : x.n0) > 0 && (t == 0 || x.step == 1);
                 }
             }
             if (!ok && lane == 0) record(a.error, 65);
@@ -628,7 +688,8 @@ cudaError_t expanded_t(const ExpandedArgs& a, cudaStream_t st) {
             const int q = a.cu_q_host[i + 1] - a.cu_q_host[i], kv = a.cu_kv_host[i + 1] - a.cu_kv_host[i];
             for (int b = 0; b * static_cast<long long>(rows) < q; ++b) {
                 const int n0 = key_tiles(q, kv, b * rows, kM), n1 = key_tiles(q, kv, b * rows + kM, kM);
-                cost[plan.n_pairs] = 3 * std::min(n0, n1) + 7 * std::max(n0, n1);  // two steps side by side: 10, one alone: 7
+                // two steps side by side: 10; one alone: 7; those of one query tile, by halves: 5
+                cost[plan.n_pairs] = n1 == 0 ? 5 * n0 : 3 * std::min(n0, n1) + 7 * std::max(n0, n1);
                 plan.pair[plan.n_pairs++] = static_cast<uint32_t>(i) << 16 | b;
             }
         }

@@ -436,6 +436,24 @@ def test_expanded_attention_in_a_graph_on_another_stream():
     _status_ok()
 
 
+@pytest.mark.parametrize("nope,vd", [(128, 128), (64, 64), (128, 64), (64, 128)])
+@pytest.mark.parametrize("rise", [False, True])
+def test_expanded_pieces_of_one_query_tile(nope, vd, rise):
+    """Up to 128 queries, also at the end of longer pieces, behind contexts of one to many key tiles; with
+    scores that rise along the keys, or fall."""
+    d = gdn.LatentDims(7, nope_dim=nope, v_dim=vd)
+    counts = [1, 128, 100, 1, 1, 257, 384, 5, 60, 127]
+    lens = [1000, 128, 129, 128, 129, 257, 1500, 4, 385, 2600]
+    k, r, v = _kv(lens, 7, nope, vd, 181, True)
+    if rise:
+        grow = torch.cat([torch.linspace(0.1, 4.0, n, device="cuda") for n in lens])[:, None, None]
+        grow = torch.cat([grow.expand(-1, 4, 1), grow.flip(0).expand(-1, 3, 1)], 1)
+        k, r = (k * grow).bfloat16(), r * 0.25
+    q = _queries(sum(counts), 7, nope + 64, 182)
+    check(gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v), *expanded(d, counts, lens, q, k, r, v))
+    _status_ok()
+
+
 # ------------------------------------------------------------------ copies
 def _filled(d, n, seed):
     c = gdn.KVCache.empty(d, n) if isinstance(d, gdn.KVDims) else gdn.LatentCache.empty(d, n)
