@@ -18,7 +18,10 @@
 // block an item (sequence, queries, head), the longest first, and one that is done
 // takes on the item of a block that has not started (try_cancel), whose loads begin
 // while it finishes its own: 137 and 172 us where every 152nd item was a block's from
-// the start, 131 and 163 us so (the two cases below).
+// the start, 131 and 163 us so (the two cases below, at that stage).  Where an item
+// has one tile of queries, both halves of the thread block take it, for every other
+// key tile each, and join their results: a key tile alone takes 1.5 us, 1.0 us so
+// (pairs of tiles: 1.9), 16 ragged prompts 145 where 159.
 //
 // Roles: 8 softmax warps (a thread a row; a rescaling concerns one warp's rows
 // alone), a warp for the loads, one issuing the products, in the order
@@ -30,14 +33,12 @@
 // tensor core takes 24 instructions of S (128 x 128 x 16, 71 cycles each, measured
 // alone) and 16 of O (74, their A operand in tensor memory): 2890 cycles.  The keys
 // and values that come in meanwhile, 80 KB, take 640 cycles of the shared memory's
-// bandwidth, which those products use in full.  About 3700 cycles are reached: what
-// remains are the queries' loads at an item's start and keys that wait for room (the
-// queries leave room for 1.6 tiles of keys).  The exponentials (32 a cycle and SM: 1024
-// cycles) do not bound it.  4096 tokens, 32 heads: 131 us, 1.31 PFLOP/s; 16
-// ragged prompts of up to 1100 tokens behind up to 3000: 163 us, 0.99 PFLOP/s, where
-// short items and tiles that are partly masked weigh more.
+// bandwidth, which those products use in full: 3530.  About 3570 are reached.  The
+// exponentials (32 a cycle and SM: 1024 cycles) do not bound it.  4096 tokens, 32
+// heads: 125 us, 1.38 PFLOP/s; 16 ragged prompts of up to 1100 tokens behind up to
+// 3000: 145 us, 1.11 PFLOP/s, where tiles that are partly masked or empty weigh more.
 //
-// Tried and slower (us, the two cases above, with fixed shares): pairs of thread blocks
+// Tried and slower (us, the two cases above, with fixed shares and 208 and 88 registers): pairs of thread blocks
 // that share keys (134 and 215 where a block of the same form took 141 and 179); two threads a
 // row (165 against 140); weights handed over by halves (144); an issuing warp per
 // tile (146 and 180); one ring for keys and values (148 and 190); a thread that
