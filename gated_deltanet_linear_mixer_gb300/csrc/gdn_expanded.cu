@@ -165,12 +165,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// What a call walks: (sequence, block of queries) pairs, most keys first, of every head; or, where
-// they are more than kPairs, all blocks of all sequences, the last ones first.
+// What a launch walks: (sequence, block of queries) pairs, most keys first, of every head.
 constexpr int kPairs = 1024;
 struct Plan {
     CUtensorMap q, k, r, v;
-    int n_pairs, blocks;       // blocks: of the longest sequence, where the pairs are not listed (n_pairs < 0)
+    int n_pairs;
     uint32_t pair[kPairs];     // sequence << 16 | block
 };
 
@@ -207,19 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem + L::kSharedAt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long items = (plan.n_pairs < 0 ? static_cast<long long>(plan.blocks) * a.n_seq : plan.n_pairs) * a.n_heads;
-    auto item_of = [&](long long at, Item& x) {  // whether there is one
-        if (at >= items) return false;
-        const int p = static_cast<int>(at / a.n_heads);
-        int seq, block;
-        if (plan.n_pairs < 0) {
-            seq = p % a.n_seq;
-            block = plan.blocks - 1 - p / a.n_seq;
-        } else {
-            seq = plan.pair[p] >> 16;
-            block = plan.pair[p] & 0xFFFF;
-        }
-        x.h = static_cast<int>(at - static_cast<long long>(p) * a.n_heads);
+    auto item_of = [&](int at, Item& x) {  // whether there is one
+        const int p = at / a.n_heads, seq = plan.pair[p] >> 16, block = plan.pair[p] & 0xFFFF;
+        x.h = at - p * a.n_heads;
         x.q0 = a.cu_q[seq];
         x.qn = a.cu_q[seq + 1] - x.q0;
         x.k0 = a.cu_kv[seq];
@@ -461,7 +450,6 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             const bool leader = elect_one();
             bool ok = true;
             uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0};  // fills so far
-            const bool others = plan.n_pairs >= 0;  // a block an item: this one's, then those of blocks that never start
             uint32_t asked = 0;
             auto ask = [&] {
                 __syncwarp();
@@ -479,20 +467,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                 }
                 return block_answered(&sh.next);
             };
-            int at = blockIdx.x, round = 0;
+            int at = blockIdx.x;   // a block an item: this one's, then those of blocks that never start
             bool waiting = false;  // for an answer
             for (uint32_t item = 0; ok; ++item) {
                 Item x;
-                bool some = false;
-                if (others) {
-                    some = at >= 0 && item_of(at, x);
-                } else {  // every gridDim.x-th, the order turning round after each
-                    const long long n = gridDim.x;
-                    while (!some && round * n < items) {
-                        some = item_of(round * n + (round & 1 ? n - 1 - at : at), x);
-                        ++round;
-                    }
-                }
+                const bool some = at >= 0 && item_of(at, x);
                 if (!some) x.h = -1;
                 const uint32_t place = item % kItems;
                 if (item >= kItems && !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.item_empty[place], (item / kItems - 1) & 1)))) break;
@@ -521,9 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                 };
                 load_queries(0);
                 const int early = max(0, x.n_tiles - 2);  // an answer takes less than two tiles
-                if (others && x.n_tiles == 0) ask(), waiting = true;
+                if (x.n_tiles == 0) ask(), waiting = true;
                 for (int i = 0; ok && i < x.n_tiles; ++i) {
-                    if (others && i == early) ask(), waiting = true;
+                    if (i == early) ask(), waiting = true;
                     if (i == 1) load_queries(1);  // behind the first tile's first keys and values
                     if (!ok) break;
                     const int key = x.k0 + i * kKeys;
@@ -552,14 +531,14 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                     __syncwarp();
                 }
                 if (ok && x.n_tiles == 1) load_queries(1);
-                if (ok && others) {
+                if (ok) {
                     at = answer();
                     waiting = !ok;
                 }
             }
             if (!ok) {  // nothing is in flight when the memory is given back, and no block starts to wait like this one
                 if (lane == 0) record(a.error, 64);
-                if (others && at >= 0) {
+                if (at >= 0) {
                     ok = true;
                     if (!waiting) ask();
                     while (ok && answer() >= 0) ask();
@@ -674,42 +653,38 @@ cudaError_t expanded_t(const ExpandedArgs& a, cudaStream_t st) {
     cudaError_t e = allow_smem(expanded_kernel<NOPE, V>, L::kSmem, ready);
     if (e != cudaSuccess) return e;
     Plan plan{};
-    constexpr int rows = kTiles * kM;
     if (a.n_kv > 0 &&
         !(map_rows(&plan.q, a.q, a.n_q, a.n_heads, NOPE + kRopeDim) && map_rows(&plan.k, a.k, a.n_kv, a.n_heads, NOPE) &&
           make_tma_map_bf16_2d(&plan.r, a.k_rope.data, a.n_kv, kRopeDim, a.k_rope.token_stride, kKeys, 64) &&
           map_rows(&plan.v, a.v, a.n_kv, a.n_heads, V)))
         return cudaErrorInvalidValue;
-    plan.blocks = (a.max_q - 1) / rows + 1;
-    long long n = 0;
-    for (int i = 0; i < a.n_seq; ++i) n += (a.cu_q_host[i + 1] - a.cu_q_host[i] + rows - 1) / rows;
-    if (n <= kPairs && plan.blocks <= 65536) {
-        int cost[kPairs];
-        for (int i = 0; i < a.n_seq; ++i) {
-            const int q = a.cu_q_host[i + 1] - a.cu_q_host[i], kv = a.cu_kv_host[i + 1] - a.cu_kv_host[i];
-            for (int b = 0; b * static_cast<long long>(rows) < q; ++b) {
-                const int n0 = key_tiles(q, kv, b * rows, kM), n1 = key_tiles(q, kv, b * rows + kM, kM);
-                // two steps side by side: 10; one alone: 7; those of one query tile, by halves: 5
-                cost[plan.n_pairs] = n1 == 0 ? 5 * n0 : 3 * std::min(n0, n1) + 7 * std::max(n0, n1);
-                plan.pair[plan.n_pairs++] = static_cast<uint32_t>(i) << 16 | b;
-            }
+    constexpr int rows = kTiles * kM;
+    int cost[kPairs], order[kPairs];
+    uint32_t pair[kPairs];
+    int n = 0;
+    auto launch = [&] {  // the pairs so far
+        for (int i = 0; i < n; ++i) order[i] = i;
+        std::sort(order, order + n, [&](int x, int y) { return cost[x] != cost[y] ? cost[x] > cost[y] : x < y; });
+        for (int i = 0; i < n; ++i) plan.pair[i] = pair[order[i]];
+        plan.n_pairs = n;
+        const unsigned grid = static_cast<unsigned>(n) * a.n_heads;
+        n = 0;
+        return timed_launch("expanded_attention", st, [&] {
+            expanded_kernel<NOPE, V><<<grid, kThreads, L::kSmem, st>>>(a, plan);
+            return cudaGetLastError();
+        });
+    };
+    for (int i = 0; i < a.n_seq; ++i) {
+        const int q = a.cu_q_host[i + 1] - a.cu_q_host[i], kv = a.cu_kv_host[i + 1] - a.cu_kv_host[i];
+        for (int b = 0; b * rows < q; ++b) {  // (below 2^24 queries: checked by the caller)
+            const int n0 = key_tiles(q, kv, b * rows, kM), n1 = key_tiles(q, kv, b * rows + kM, kM);
+            // two steps side by side: 10; one alone: 7; those of one query tile, by halves: 5
+            cost[n] = n1 == 0 ? 5 * n0 : 3 * std::min(n0, n1) + 7 * std::max(n0, n1);
+            pair[n++] = static_cast<uint32_t>(i) << 16 | b;
+            if (n == kPairs && (e = launch()) != cudaSuccess) return e;
         }
-        int order[kPairs];
-        uint32_t sorted[kPairs];
-        for (int i = 0; i < plan.n_pairs; ++i) order[i] = i;
-        std::sort(order, order + plan.n_pairs, [&](int x, int y) { return cost[x] != cost[y] ? cost[x] > cost[y] : x < y; });
-        for (int i = 0; i < plan.n_pairs; ++i) sorted[i] = plan.pair[order[i]];
-        std::copy(sorted, sorted + plan.n_pairs, plan.pair);
-    } else {
-        n = static_cast<long long>(plan.blocks) * a.n_seq;
-        plan.n_pairs = -1;
     }
-    if (n * a.n_heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = static_cast<unsigned>(plan.n_pairs < 0 ? std::min(n * a.n_heads, static_cast<long long>(kSms)) : n * a.n_heads);
-    return timed_launch("expanded_attention", st, [&] {
-        expanded_kernel<NOPE, V><<<grid, kThreads, L::kSmem, st>>>(a, plan);
-        return cudaGetLastError();
-    });
+    return n > 0 ? launch() : cudaSuccess;
 }
 
 }  // namespace

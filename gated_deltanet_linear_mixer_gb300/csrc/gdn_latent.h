@@ -53,7 +53,6 @@ struct ExpandedArgs {
     float scale;
     const int32_t *cu_q, *cu_kv, *cu_q_host, *cu_kv_host;
     int n_q, n_kv;  // cu_q[n_seq], cu_kv[n_seq]
-    int max_q;      // longest sequence in queries
     KvRows q, k, k_rope, v;
     void* out;
     int* error;

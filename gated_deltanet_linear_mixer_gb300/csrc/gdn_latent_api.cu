@@ -242,8 +242,10 @@ gdn_status gdn_expanded_attention(const gdn_latent_dims* dims, int32_t n_seq, co
     gdn::clear_error();
     if (n_seq == 0 || cu_q_host[n_seq] == 0) return GDN_OK;
     a.n_seq = n_seq; a.n_q = cu_q_host[n_seq]; a.n_kv = cu_kv_host[n_seq];
-    int uniform;
-    spread(cu_q_host, n_seq, &a.max_q, &uniform);
+    int longest, uniform;
+    spread(cu_q_host, n_seq, &longest, &uniform);
+    if (longest > 1 << 24) return set_error(GDN_ERR_UNSUPPORTED, fn, "a sequence has %d queries, more than 2^24", longest);
+    if (a.n_kv > 1 << 30) return set_error(GDN_ERR_UNSUPPORTED, fn, "%d keys are more than 2^30", a.n_kv);
     if (!cu_q || !cu_kv) return set_error(GDN_ERR_INVALID_ARG, fn, "cu_q or cu_kv is NULL");
     if ((st = check_rows(q, "q", &a.q, fn)) != GDN_OK) return st;
     if (a.n_kv > 0) {  // without keys nothing of them is looked at

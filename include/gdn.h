@@ -545,7 +545,8 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
  *   side), k_rope [Tk, rope_dim] rows (head_stride is not used); token strides
  *   > 0, a head stride of 0 shares one head.  out [Tq, n_heads, v_dim]
  *   contiguous.
- * The work is laid out by the host copies: a captured call keeps its sequences.
+ * The work is laid out by the host copies: a captured call keeps its sequences.  A
+ * sequence has at most 2^24 queries, a call 2^30 keys.
  * Values that some query of a sequence sees have to be finite.  fp32 accumulation
  * and softmax (the hardware's exponentials, 2 ulp), weights bf16 (8 bits); the sum
  * takes them as they are.

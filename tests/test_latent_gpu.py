@@ -454,6 +454,35 @@ def test_expanded_pieces_of_one_query_tile(nope, vd, rise):
     _status_ok()
 
 
+@pytest.mark.parametrize("n", [129, 200, 257, 300, 500, 640])
+def test_expanded_pieces_keep_a_neighbours_values_out(n):
+    """Tiles that end within the next sequence's rows, by either half of the thread block."""
+    d = gdn.LatentDims(3)
+    counts, lens = [7, 3], [n, 400]
+    k, r, v = _kv(lens, 3, 128, 128, 191, False)
+    q = _queries(10, 3, 192, 192)
+    want, tol = expanded(d, counts, lens, q, k, r, v)
+    k[n:], v[n:] = math.nan, math.nan
+    got = gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v)
+    check(got[:7], want[:7], tol[:7])
+    assert bool(got[7:].isnan().all())
+    _status_ok()
+
+
+def test_expanded_results_repeat():
+    """Which thread block takes an item does not matter."""
+    d = gdn.LatentDims(16)
+    counts = [300, 1, 77, 600, 130, 256, 40, 511] * 2
+    lens = [c + 137 * i for i, c in enumerate(counts)]
+    k, r, v = _kv(lens, 16, 128, 128, 193, True)
+    q, cu, ck = _queries(sum(counts), 16, 192, 194), cu_of(counts), cu_of(lens)
+    first = gdn.expanded_attention(d, cu, ck, q, k, r, v)
+    for _ in range(20):
+        assert torch.equal(gdn.expanded_attention(d, cu, ck, q, k, r, v), first)
+    check(first, *expanded(d, counts, lens, q, k, r, v))
+    _status_ok()
+
+
 # ------------------------------------------------------------------ copies
 def _filled(d, n, seed):
     c = gdn.KVCache.empty(d, n) if isinstance(d, gdn.KVDims) else gdn.LatentCache.empty(d, n)

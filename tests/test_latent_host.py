@@ -309,3 +309,11 @@ def test_page_lists_may_change_while_they_are_read():
     src += [Page(), Page(), Page()]
     with pytest.raises(ValueError, match=r"\(1, 3\)"):
         gdn.copy_pages([], src, [0, 1, 2])
+
+
+def test_pieces_of_too_many_queries_are_refused(lib, monkeypatch):
+    monkeypatch.setenv("GDN_FAULT", "expanded_attention")
+    assert _expand(lib, cu=(0, 1 << 24), ck=(0, 1 << 24)) == gdn.GDN_ERR_INJECTED
+    assert _expand(lib, cu=(0, 3, (1 << 24) + 4), ck=(0, 3, 9)) == 2 and "2^24" in _message(lib)
+    assert _expand(lib, cu=(0, 3), ck=(0, 1 << 30)) == gdn.GDN_ERR_INJECTED
+    assert _expand(lib, cu=(0, 3), ck=(0, (1 << 30) + 1)) == 2 and "2^30" in _message(lib)
