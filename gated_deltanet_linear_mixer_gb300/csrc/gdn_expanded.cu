@@ -15,13 +15,13 @@
 // product's A operand where they lie.  Keys stream through a ring of
 // 16 KB blocks (128 keys x 64 channels), values through one of whole tiles; the
 // position keys come from their own array, which all heads share.  There is a thread
-// block an item (sequence, queries, head), the longest first, and one that is done
+// block an item (sequence, queries, head), the longest sequences' first, and one that is done
 // takes on the item of a block that has not started (try_cancel), whose loads begin
 // while it finishes its own: 137 and 172 us where every 152nd item was a block's from
 // the start, 131 and 163 us so (the two cases below, at that stage).  Where an item
 // has one tile of queries, both halves of the thread block take it, for every other
 // key tile each, and join their results: a key tile alone takes 1.5 us, 1.0 us so
-// (pairs of tiles: 1.9), 16 ragged prompts 145 where 159.
+// (pairs of tiles: 1.9), and 16 ragged prompts take 145 us instead of 159.
 //
 // Roles: 8 softmax warps (a thread a row; a rescaling concerns one warp's rows
 // alone), a warp for the loads, one issuing the products, in the order
@@ -36,7 +36,7 @@
 // bandwidth, which those products use in full: 3530.  About 3570 are reached.  The
 // exponentials (32 a cycle and SM: 1024 cycles) do not bound it.  4096 tokens, 32
 // heads: 125 us, 1.38 PFLOP/s; 16 ragged prompts of up to 1100 tokens behind up to
-// 3000: 145 us, 1.11 PFLOP/s, where tiles that are partly masked or empty weigh more.
+// 3000: 142 us, 1.14 PFLOP/s, where tiles that are partly masked or empty weigh more.
 //
 // Tried and slower (us, the two cases above, with fixed shares and 208 and 88 registers): pairs of thread blocks
 // that share keys (134 and 215 where a block of the same form took 141 and 179); two threads a
@@ -165,7 +165,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// What a launch walks: (sequence, block of queries) pairs, most keys first, of every head.
+// What a launch walks: (sequence, block of queries) pairs, of every head.
 constexpr int kPairs = 1024;
 struct Plan {
     CUtensorMap q, k, r, v;
@@ -659,12 +659,23 @@ cudaError_t expanded_t(const ExpandedArgs& a, cudaStream_t st) {
           map_rows(&plan.v, a.v, a.n_kv, a.n_heads, V)))
         return cudaErrorInvalidValue;
     constexpr int rows = kTiles * kM;
-    int cost[kPairs], order[kPairs];
+    int cost[kPairs], order[kPairs], most[kPairs];  // most: of the sequence's
     uint32_t pair[kPairs];
     int n = 0;
     auto launch = [&] {  // the pairs so far
         for (int i = 0; i < n; ++i) order[i] = i;
-        std::sort(order, order + n, [&](int x, int y) { return cost[x] != cost[y] ? cost[x] > cost[y] : x < y; });
+        for (int i = 0, j; i < n; i = j) {
+            int top = 0;
+            for (j = i; j < n && pair[j] >> 16 == pair[i] >> 16; ++j) top = std::max(top, cost[j]);
+            for (int k = i; k < j; ++k) most[k] = top;
+        }
+        // The sequence with the longest item first, so that short items end the launch; a sequence's side by side, so
+        // that they read its keys from L2 (16 ragged prompts: 142 us, by items alone 145).
+        std::sort(order, order + n, [&](int x, int y) {
+            if (most[x] != most[y]) return most[x] > most[y];
+            if (pair[x] >> 16 != pair[y] >> 16 || cost[x] == cost[y]) return x < y;
+            return cost[x] > cost[y];
+        });
         for (int i = 0; i < n; ++i) plan.pair[i] = pair[order[i]];
         plan.n_pairs = n;
         const unsigned grid = static_cast<unsigned>(n) * a.n_heads;
