@@ -787,3 +787,24 @@ assert bool((rows[0, :4] == 2).all()) and bool((rows[0, 4:] == 1).all())
     got = subprocess.run([sys.executable, "-c", code], cwd=pathlib.Path(__file__).parents[1], capture_output=True, text=True,
                          timeout=300)
     assert got.returncode == 0, got.stderr[-2000:]
+
+
+def test_expanded_calls_on_two_streams_at_once():
+    """Thread blocks take over items of their own call only; calls of several launches too."""
+    runs = []
+    for i, (heads, counts, lens) in enumerate([(16, [700, 90, 300], [900, 500, 301]), (8, [600, 1, 64], [600, 700, 64]),
+                                               (1, [1] * 1030 + [300], [9] * 1030 + [310])]):
+        d = gdn.LatentDims(heads)
+        q, (k, r, v) = _queries(sum(counts), heads, 192, 200 + i), _kv(lens, heads, 128, 128, 210 + i, True)
+        out = torch.empty(sum(counts), heads, 128, dtype=torch.bfloat16, device="cuda")
+        args = (d, cu_of(counts), cu_of(lens), q, k, r, v)
+        runs.append((args, out, torch.cuda.Stream(), expanded(d, counts, lens, q, k, r, v)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, out, stream, _ in runs:
+            with torch.cuda.stream(stream):
+                gdn.expanded_attention(*args, out=out)
+    torch.cuda.synchronize()
+    for _, out, _, want in runs:
+        check(out, *want)
+    _status_ok()
