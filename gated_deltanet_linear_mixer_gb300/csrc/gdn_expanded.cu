@@ -5,8 +5,9 @@
 // with a reference m_r that lags behind the row's maximum by at most 2^kLazy, so
 // that the output is rescaled only where the maximum rises by more than that.
 // Weights are rounded to bf16 (the values' type, as the tensor core asks); the sum
-// takes them unrounded, which costs 0.0002 of the output's error and 5% less time
-// than the sum of the rounded ones.
+// takes them unrounded, which takes 3% less time than the sum of the rounded ones
+// and costs at most 0.0001 of the output's relative error (0.0021 and 0.0023 of the
+// two cases below).
 //
 // A thread block takes two tiles of 128 queries of a head and walks the keys in
 // tiles of 128 up to the last query's position.  While one tile's softmax runs, the
