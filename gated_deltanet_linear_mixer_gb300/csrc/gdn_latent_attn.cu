@@ -32,8 +32,8 @@
 //
 // What bounds it.  Up to 32 rows a sequence the rows' bytes: a tile's 72 KB are
 // 3100 cycles of an SM's share of DRAM, its products 2160 (16 rows) or 2290 (32).
-// 256 single tokens of 32 heads after 127..8191 keys take 222 us, 88% of the
-// measured copy rate, 16 heads 205 us (92%).  With 64 rows the products: 36 of S at 37
+// 256 single tokens of 32 heads after 127..8191 keys take 222 to 227 us, 87% of the
+// measured copy rate, 16 heads 205 to 210 us (90%).  With 64 rows the products: 36 of S at 37
 // cycles (64 x 64 x 16) and 16 of O^T at 76 (128 x 64 x 16 with the first operand
 // MN-major; 53 were it K-major) make 2540 cycles a tile, of which the ring's two tiles
 // let it reach 2900: 64 x 4 drafts of 32 heads after 500..6000 keys take 110 us, of
