@@ -66,7 +66,7 @@ constexpr int kM = 128, kKeys = 128, kTiles = 2;
 constexpr int kThreads = 384;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kBlock = 16384;  // 128 rows x 64 channels
-constexpr uint32_t kSmemMax = 232448, kSharedBytes = 3072;
+constexpr uint32_t kSmemMax = 232448, kSharedBytes = 2944;
 constexpr int kMaxSlots = 12;
 
 template <int NOPE, int V> struct ECfg {

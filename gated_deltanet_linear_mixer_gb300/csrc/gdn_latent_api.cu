@@ -149,6 +149,8 @@ gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache
     if ((st = check_rows(&r, "c", &a.rows, fn)) != GDN_OK) return st;
     if (norm_w && !aligned16(norm_w)) return set_error(GDN_ERR_INVALID_ARG, fn, "norm_w must be 16-byte aligned");
     if (q_rope) {
+        if (static_cast<long long>(a.b.n_tokens) * dims->n_heads > 0x7fffff00)
+            return set_error(GDN_ERR_UNSUPPORTED, fn, "%d tokens of %d heads are more than 2^31 - 256 rows", a.b.n_tokens, dims->n_heads);
         if ((st = check_rows(q_rope, "q_rope", &a.q, fn)) != GDN_OK) return st;
         if ((st = check_rows(q_out, "q_out", &a.q_out, fn)) != GDN_OK) return st;
         if (rows_overlap(a.q_out, a.b.n_tokens, dims->n_heads, dims->rope_dim))
@@ -212,6 +214,8 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
     if ((st = check_batch(batch, kv_lens, &a.b, fn)) != GDN_OK) return st;
     gdn::clear_error();
     if (a.b.n_tokens == 0) return GDN_OK;
+    if (static_cast<long long>(a.b.n_tokens) * dims->n_heads > 0x7fffff00)
+        return set_error(GDN_ERR_UNSUPPORTED, fn, "%d tokens of %d heads are more than 2^31 - 256 rows", a.b.n_tokens, dims->n_heads);
     if ((st = check_rows(q, "q", &a.q, fn)) != GDN_OK) return st;
     if (!out || !aligned16(out)) return set_error(GDN_ERR_INVALID_ARG, fn, "out must be given and 16-byte aligned");
     const size_t need = gdn::latent_attention_workspace(dims->n_heads, dims->latent_dim, a.b.n_seq, a.b.max_q);

@@ -66,7 +66,7 @@ constexpr float kLazy = 8.0f;
 constexpr int kPieces = 16;      // pieces of a span that are laid out at a time
 constexpr int kMasks = 8;
 constexpr int kMaxSlots = 12;
-constexpr uint32_t kSmemMax = 232448, kSharedBytes = 3072;
+constexpr uint32_t kSmemMax = 232448, kSharedBytes = 2944;
 
 template <int C, int NR> struct LCfg {
     static constexpr int W = C + kRopeDim, kBlocks = W / 64, kPairs = C / 128;
@@ -1012,7 +1012,6 @@ cudaError_t launch_t(const LatentAttnArgs& a, cudaStream_t st) {
     if (rows > 0 && !(make_tma_map_bf16_2d(&maps.rows, a.c.rows, rows, L::W, L::W, std::min(1 << a.page_shift, kKeys), 64) &&
                       make_tma_map_bf16_3d(&maps.pairs, a.c.rows, 64, rows, L::W / 64, L::W, 64, 64, kKeys, 2)))
         return cudaErrorInvalidValue;
-    if (static_cast<long long>(a.b.n_tokens) * a.n_heads > 0x7fffffffLL - 2 * NR) return cudaErrorInvalidConfiguration;
     // queries whose rows (token, head) are evenly spaced are loaded as one matrix
     const long long pitch = a.n_heads == 1 ? a.q.token_stride : a.q.head_stride;
     const bool dense_q = pitch >= L::W && pitch < 1ll << 36 &&

@@ -76,7 +76,7 @@ template <int C>
 __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const LatentAppendArgs a, const uint32_t parts) {
     constexpr int N = C / 256, W = C + kRopeDim;  // 8-channel vectors of the latent a lane holds; channels of a row
     const int lane = threadIdx.x & 31;
-    const uint32_t w = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);  // below 2^32: checked at the launch
+    const uint32_t w = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);  // below 2^32: the caller checked tokens x heads
     const uint32_t w_tok = w / parts;
     if (w_tok >= static_cast<uint32_t>(a.b.n_tokens)) return;
     const int tok = static_cast<int>(w_tok), part = static_cast<int>(w - w_tok * parts);  // part 0: the row
@@ -178,8 +178,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
 template <int C>
 cudaError_t append_t(const LatentAppendArgs& a, cudaStream_t st) {
     const int parts = 1 + (a.q.data ? (a.n_heads + 8 * kQUnits - 1) / (8 * kQUnits) : 0);
-    const long long blocks = (static_cast<long long>(a.b.n_tokens) * parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-    if (blocks > 0x3fffffffLL) return cudaErrorInvalidConfiguration;  // warps are counted in 32 bits
+    const unsigned long long blocks = (static_cast<unsigned long long>(a.b.n_tokens) * parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     latent_append_kernel<C><<<static_cast<unsigned>(blocks), kAppendThreads, 0, st>>>(a, parts);
     return cudaGetLastError();
 }

@@ -521,6 +521,7 @@ gdn_status gdn_latent_read(const gdn_latent_dims* dims, const gdn_latent_cache* 
  *   n_heads, latent_dim] contiguous.
  *   workspace: at least gdn_latent_attention_workspace_size() bytes, 256-byte
  *   aligned.  Calls that may run at the same time need one each.
+ *   T x n_heads at most 2^31 - 256 (gdn_latent_append with q_rope: the same).
  * Rows that some query of a sequence sees have to be finite, as appended ones
  * are; whatever lies behind a sequence's end does not matter.  fp32
  * accumulation and softmax (the hardware's exponentials, 2 ulp), weights bf16

@@ -317,3 +317,12 @@ def test_pieces_of_too_many_queries_are_refused(lib, monkeypatch):
     assert _expand(lib, cu=(0, 3, (1 << 24) + 4), ck=(0, 3, 9)) == 2 and "2^24" in _message(lib)
     assert _expand(lib, cu=(0, 3), ck=(0, 1 << 30)) == gdn.GDN_ERR_INJECTED
     assert _expand(lib, cu=(0, 3), ck=(0, (1 << 30) + 1)) == 2 and "2^30" in _message(lib)
+
+
+def test_more_rows_than_32_bits_are_refused(lib, monkeypatch):
+    monkeypatch.setenv("GDN_FAULT", "latent_attention,latent_append")
+    d = _dims(n_heads=1024)
+    for call in (_attend, _append):
+        assert call(lib, d=d, b=_batch((0, (1 << 21) - 1)), **({"q_out": _r(token=1 << 16, head=64)} if call is _append else {})) == \
+            gdn.GDN_ERR_INJECTED
+        assert call(lib, d=d, b=_batch((0, 1 << 21))) == 2 and "rows" in _message(lib)
