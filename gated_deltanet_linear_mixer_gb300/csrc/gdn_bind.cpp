@@ -385,6 +385,7 @@ PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const auto device = device_of(a, {{1, "cache.rows"}, {2, "cu_seqlens"}, {4, "kv_lens"}, {5, "block_table"}, {6, "c"},
                                           {7, "norm_w"}, {8, "q_rope"}, {9, "q_out"}, {10, "rope"}, {11, "positions"},
                                           {12, "rows_out"}});
+        if (a[8] == Py_None && a[9] != Py_None) bad(PyExc_ValueError, "q_out without q_rope");
         const auto* d = struct_at<gdn_latent_dims>(a[0]);
         const gdn_latent_cache c = latent_cache_of(d, a[1]);
         const int32_t* lens;

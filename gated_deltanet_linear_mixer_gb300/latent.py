@@ -119,8 +119,8 @@ def latent_attention_workspace_size(d: LatentDims, cu_seqlens) -> int:
     """Bytes of workspace latent_attention needs for these sequences."""
     lib = load()
     if isinstance(cu_seqlens, tuple):
-        host = cu_seqlens[1]
-    elif isinstance(cu_seqlens, torch.Tensor):
+        cu_seqlens = cu_seqlens[1]
+    if isinstance(cu_seqlens, torch.Tensor):
         host = cu_seqlens.detach().to("cpu", torch.int32).contiguous()
     else:
         host = torch.tensor(list(cu_seqlens), dtype=torch.int32)

@@ -326,3 +326,25 @@ def test_more_rows_than_32_bits_are_refused(lib, monkeypatch):
         assert call(lib, d=d, b=_batch((0, (1 << 21) - 1)), **({"q_out": _r(token=1 << 16, head=64)} if call is _append else {})) == \
             gdn.GDN_ERR_INJECTED
         assert call(lib, d=d, b=_batch((0, 1 << 21))) == 2 and "rows" in _message(lib)
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_an_output_without_its_input_is_refused():
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    mode = FakeTensorMode(allow_non_fake_inputs=True)
+
+    def make(shape, dtype):
+        with mode:
+            return torch.empty(shape, dtype=dtype, device="cuda:0")
+
+    call, args = _calls(make)["append"]
+    with pytest.raises(ValueError, match="q_out without q_rope"):
+        call({**args, "q_rope": None})
+
+
+def test_workspace_sizes_of_any_form_of_lengths(lib):
+    d = gdn.LatentDims(32, 512)
+    want = gdn.latent_attention_workspace_size(d, [0, 1, 5])
+    assert want > 0 and want == gdn.latent_attention_workspace_size(d, torch.tensor([0, 1, 5]))
+    assert want == gdn.latent_attention_workspace_size(d, (None, torch.tensor([0, 1, 5], dtype=torch.int64)))
+    assert gdn.latent_attention_workspace_size(d, [0]) == 0 and gdn.latent_attention_workspace_size(d, [0, 0, 0]) == 0
