@@ -808,3 +808,33 @@ def test_expanded_calls_on_two_streams_at_once():
     for _, out, _, want in runs:
         check(out, *want)
     _status_ok()
+
+
+def test_rows_beyond_32_bit_offsets_are_appended_and_read():
+    d = gdn.LatentDims(2, 512)
+    first = 2 ** 32 // (64 * 576) + 1  # its first element's index passes 32 bits
+    rows = torch.empty(first + 4, 64, 576, dtype=torch.bfloat16, device="cuda")
+    cache, table = gdn.LatentCache(d, rows), ints([[first + 2, first]])
+    c = torch.randn(100, 576, generator=gen(220), device="cuda").bfloat16()
+    gdn.latent_append(d, cache, [0, 100], ints([100]), table, c)
+    assert torch.equal(rows[first + 2], c[:64]) and torch.equal(rows[first, :36], c[64:])
+    assert torch.equal(gdn.latent_read(d, cache, [0, 90], ints([10]), table), c[10:])
+    _status_ok()
+
+
+@pytest.mark.parametrize("far", ["keys", "results"])
+def test_expanded_attention_beyond_32_bit_offsets(far):
+    """A short sequence behind one of 600,000 keys without queries, or as many queries without keys."""
+    d, n = gdn.LatentDims(32), 600_000
+    counts, lens = ([0, 5], [n, 300]) if far == "keys" else ([n, 5], [0, 300])
+    g = gen(221)
+    k = torch.zeros(sum(lens), 32, 256, dtype=torch.bfloat16, device="cuda")
+    k[-300:] = torch.randn(300, 32, 256, generator=g, device="cuda").bfloat16()
+    r = torch.zeros(sum(lens), 64, dtype=torch.bfloat16, device="cuda")
+    r[-300:] = torch.randn(300, 64, generator=g, device="cuda").bfloat16()
+    q = torch.zeros(sum(counts), 32, 192, dtype=torch.bfloat16, device="cuda")
+    q[-5:] = _queries(5, 32, 192, 222)
+    got = gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k[..., :128], r, k[..., 128:])
+    _status_ok()
+    check(got[-5:], *expanded(d, [5], [300], q[-5:], k[-300:, :, :128], r[-300:], k[-300:, :, 128:]))
+    assert not got[:-5].any()
