@@ -43,8 +43,9 @@
 // that share keys (134 and 215 where a block of the same form took 141 and 179); two threads a
 // row (165 against 140); weights handed over by halves (144); an issuing warp per
 // tile (146 and 180); one ring for keys and values (148 and 190); a thread that
-// polls both tiles' barriers and issues what is ready (149); scores read by one
-// load of 128 columns (140 and 178).
+// polls both tiles' barriers and issues what is ready (149).  No faster: scores read by
+// one load of 128 columns, three-operand maxima, the first item looked up before the
+// thread block's barriers are there.
 #include <algorithm>
 
 #include "gdn_internal.h"
