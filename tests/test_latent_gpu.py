@@ -838,3 +838,25 @@ def test_expanded_attention_beyond_32_bit_offsets(far):
     _status_ok()
     check(got[-5:], *expanded(d, [5], [300], q[-5:], k[-300:, :, :128], r[-300:], k[-300:, :, 128:]))
     assert not got[:-5].any()
+
+
+def test_expanded_attention_that_waits_in_vain_takes_no_other_blocks_time(monkeypatch):
+    """Many more thread blocks than run at once: those that gave up keep the others from starting to
+    wait as long, and the next call takes all of its blocks."""
+    import time
+    d = gdn.LatentDims(40)
+    counts, lens = [300, 5, 130, 256] * 6, [300, 400, 131, 700] * 6
+    k, r, v = _kv(lens, 40, 128, 128, 231, True)
+    q = _queries(sum(counts), 40, 192, 232)
+    monkeypatch.setenv("GDN_FAULT", "stall_expanded")
+    torch.cuda.synchronize()
+    start = time.monotonic()
+    gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v)
+    with pytest.raises(gdn.GDNError) as e:
+        gdn.sync_status()
+    assert e.value.status == gdn.GDN_ERR_TIMEOUT
+    assert time.monotonic() - start < 9.0  # waits of 2 s: of one wave of blocks, not of eight
+    monkeypatch.delenv("GDN_FAULT")
+    got = gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v)
+    _status_ok()
+    check(got, *expanded(d, counts, lens, q, k, r, v))
