@@ -107,7 +107,8 @@ struct Shared {
     int mask[kMasks];
     float factor[64], stat[64];
     Piece piece[kPieces];
-    int dead;
+    int dead;      // a loading or issuing warp gave up
+    int dead_was;  // whether one had when the round began: written between the thread block's barriers, so that all warps read the same
     uint32_t tmem_slot;
 };
 static_assert(sizeof(Shared) <= kSharedBytes, "part of kSmem");
@@ -308,7 +309,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
         mbar_init(&sh.pv_done, 1);
         for (int i = 0; i < kMasks; ++i) mbar_init(&sh.m_full[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&sh.drained[i], 1);
-        sh.dead = 0;
+        sh.dead = sh.dead_was = 0;
         fence_barrier_init();
     }
     __syncthreads();
@@ -426,10 +427,11 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
 
     for (;;) {
         const int n_round = sh.n_round;
-        const bool dead = sh.dead != 0;
+        const bool dead = sh.dead_was != 0;
         const bool more = sh.more;
         if (dead) {
-            // a wait gave up in an earlier round: nothing more is started
+            // a wait gave up in an earlier round: nothing more is started.  (The softmax warps meet at a barrier of
+            // theirs, which has no time limit: either all of them run a round or none does.)
         } else if (warp < 4) {
             // ---- softmax
             const bool active = warp < L::kActive;
@@ -810,6 +812,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
         __syncthreads();
         if (!more) break;
         if (walker) lay_out();
+        if (tid == 0) sh.dead_was = sh.dead;
         __syncthreads();
     }
     // nothing of this thread block is in flight when its memory is given back

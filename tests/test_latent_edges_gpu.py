@@ -1,0 +1,46 @@
+"""Latent attention on the GPU at its edges: waits that give up, few rows and short rings, very large
+scores and lengths, memory shared between arguments."""
+import time
+
+import pytest
+import torch
+
+import gated_deltanet_linear_mixer_gb300 as gdn
+from latent_cases import absorbed, check, cu_of, gen, ints, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+def _queries(t, heads, width, seed):
+    return torch.randn(t, heads, width, generator=gen(seed), device="cuda").bfloat16()
+
+
+def _timeout():
+    with pytest.raises(gdn.GDNError) as e:
+        gdn.sync_status()
+    assert e.value.status == gdn.GDN_ERR_TIMEOUT
+    gdn.sync_status()  # read and cleared
+
+
+@pytest.mark.parametrize("heads,dc", [(16, 512), (32, 512), (64, 256), (128, 256)])
+def test_waits_that_give_up_in_the_first_of_many_rounds(monkeypatch, heads, dc):
+    """Spans of many sequences, laid out a few at a time: a wait that gives up while the first ones are
+    walked ends the call, by all warps alike, in the time of those; the next call is right."""
+    d = gdn.LatentDims(heads, dc, page_size=16)
+    n = 7600  # 50 a span
+    counts, lens = [1] * n, [1 + i % 70 for i in range(n)]
+    cache, table = make_cache(d, [70], 301)
+    table = table.expand(n, -1).contiguous()  # all read the same pages
+    q = _queries(n, heads, dc + 64, 302)
+    cu = cu_of(counts)
+    monkeypatch.setenv("GDN_FAULT", "stall_latent")
+    torch.cuda.synchronize()
+    start = time.monotonic()
+    gdn.latent_attention(d, cache, cu, ints(lens), table, q)
+    _timeout()
+    assert time.monotonic() - start < 20.0  # waits of about 2 s one after the other, in one round of four
+    monkeypatch.delenv("GDN_FAULT")
+    got = gdn.latent_attention(d, cache, cu, ints(lens), table, q)
+    gdn.sync_status()
+    some = list(range(0, n, 97)) + [n - 1]
+    check(got[some], *absorbed(d, cache, [1] * len(some), [lens[i] for i in some], table[some], q[some]))
