@@ -451,7 +451,9 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                     float s[kScores];
                     bool lift = false;
                     float topA = -INFINITY, topB = -INFINITY;
-                    if ((active || valid < kKeys) && ok &&
+                    // (Warps without rows do not: they count in no barrier that S waits for, so that they might look
+                    // two tiles late.  What they write, rows behind the last key, they write after the lift's barrier.)
+                    if (active && ok &&
                         !(ok = __all_sync(0xffffffffu, mbar_wait_brief(&sh.s_full[sb], (g >> 1) & 1) &&
                                                            mbar_wait_brief(&sh.m_full[g % kMasks], (g / kMasks) & 1))) &&
                         lane == 0)

@@ -44,3 +44,20 @@ def test_waits_that_give_up_in_the_first_of_many_rounds(monkeypatch, heads, dc):
     gdn.sync_status()
     some = list(range(0, n, 97)) + [n - 1]
     check(got[some], *absorbed(d, cache, [1] * len(some), [lens[i] for i in some], table[some], q[some]))
+
+
+@pytest.mark.parametrize("heads", [1, 2, 16, 20, 32])
+@pytest.mark.parametrize("dc", [256, 512])
+def test_few_rows_and_many_short_ragged_sequences(heads, dc):
+    """Up to 32 rows a sequence, so that some softmax warps have none, over tiles that end early, one
+    after the other: several calls, all alike and right."""
+    d = gdn.LatentDims(heads, dc, page_size=64)
+    n = 2000
+    counts, lens = [1] * n, [1 + (i * 37) % 200 for i in range(n)]
+    cache, table = make_cache(d, lens, 311)
+    q, cu = _queries(n, heads, dc + 64, 312), cu_of(counts)
+    want = absorbed(d, cache, counts, lens, table, q)
+    outs = [gdn.latent_attention(d, cache, cu, ints(lens), table, q) for _ in range(5)]
+    gdn.sync_status()
+    check(outs[0], *want)
+    assert all(torch.equal(outs[0], o) for o in outs)
