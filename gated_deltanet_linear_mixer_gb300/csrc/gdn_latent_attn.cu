@@ -21,8 +21,10 @@
 // whatever they are; lengths are only known on the device, where every thread
 // block finds its span by a scan over the sequences.  What a span holds of a
 // sequence that it does not hold whole is a partial result (at most two a span);
-// a second launch joins them.  Above 64 rows a group is two row tiles, of a pair of
-// thread blocks that walk the same span and load each half of the rows into both.
+// a second launch joins them.  Above 64 rows a group is two row tiles, of two
+// neighbouring thread blocks that walk the same span, each with loads of its own: the
+// later one's rows come from L2 (64 x 4 drafts as below: 106 us; 118 us where
+// every row tile was a group, 110 where a cluster shared its loads).
 //
 // Roles: 4 softmax warps (also: rescaling, epilogue), two for the rows' TMA loads
 // (with the page look-ups), one loading queries and issuing S, one issuing O^T.
@@ -36,7 +38,7 @@
 // measured copy rate, 16 heads 205 to 210 us (90%).  With 64 rows the products: 36 of S at 37
 // cycles (64 x 64 x 16) and 16 of O^T at 76 (128 x 64 x 16 with the first operand
 // MN-major; 53 were it K-major) make 2540 cycles a tile, of which the ring's two tiles
-// let it reach 2900: 64 x 4 drafts of 32 heads after 500..6000 keys take 110 us, of
+// let it reach 2900: 64 x 4 drafts of 32 heads after 500..6000 keys take 106 us, of
 // which the partial results of 152 thread blocks and their join are 20.  Tiles of
 // 32 keys, four in the ring, were slower (145 us, then 119), and so was fetching
 // tiles into L2 ahead of their loads (256 x 1: 229 us without, 246 three tiles
@@ -151,36 +153,19 @@ __device__ __forceinline__ uint64_t l2_policy(bool once) {
     else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
-// Loads into this thread block, or both of a pair.
-template <bool PAIR>
 __device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, uint64_t policy) {
-    if (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-            " [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "l"(policy)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-            " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
 }
-template <bool PAIR>
 __device__ __forceinline__ void load_halves(void* dst, const CUtensorMap* map, uint64_t* bar, int y, int z, uint64_t policy) {
-    if (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "l"(policy)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
 }
 
 // 16 lanes x 64 columns of 32-bit: v[4 i + 2 h + e] is row lane / 4 + 8 h, column
@@ -253,11 +238,12 @@ struct Maps {
     CUtensorMap q;      // of a row tile x 64 channels
 };
 
-template <int C, int NR, bool PAIR>
+// G: row tiles of a group, of as many thread blocks.
+template <int C, int NR, int G>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps maps, const int dense_q, float* parts, Join* joins) {
     using L = LCfg<C, NR>;
-    constexpr int NP = L::kPairs, NS = L::kSlots, G = PAIR ? 2 : 1;
+    constexpr int NP = L::kPairs, NS = L::kSlots;
     constexpr int kScores = kKeys / 2;  // of a lane: two rows of a quarter of the keys
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem + L::kSharedAt);
@@ -293,11 +279,11 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     if (tid == 32 * 6) {  // beside the warp that most of the sequences are in
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sh.pair_full[i], 1);
-            mbar_init(&sh.pair_empty[i], G);
+            mbar_init(&sh.pair_empty[i], 1);
         }
         for (int i = 0; i < kRopes; ++i) {
             mbar_init(&sh.rope_full[i], 1);
-            mbar_init(&sh.rope_empty[i], G);
+            mbar_init(&sh.rope_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -407,17 +393,8 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (PAIR) {  // the other's barriers are initialised
-        cluster_arrive();
-        cluster_wait();
-    }
     const uint32_t tmem = sh.tmem_slot;
 
-    // a slot is free once the products of both thread blocks of a pair are done
-    auto give = [&](uint64_t* bar) {
-        if (PAIR) mma_commit_multicast(bar, 3);
-        else mma_commit(bar);
-    };
     // counts that the roles carry from round to round
     uint32_t g = 0;   // key tiles
     uint32_t qc = 0;  // pieces with tiles whose queries came
@@ -614,14 +591,13 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
         } else if (warp == 4 || warp == 7) {
             // ---- cached rows: page look-ups by the warp, loads by one lane.  A load takes about 55 cycles to
             // issue, and pages of 16 rows need 36 a tile: two warps share them, the first the position keys
-            // and two slots, the second the others.  Of a pair each thread block loads half of what both
-            // need into both.
+            // and two slots, the second the others.
             const int page_size = 1 << a.page_shift, R = min(page_size, kKeys), per_tile = kKeys >> min(a.page_shift, 6);
             const bool leader = elect_one(), lead_warp = warp == 4;
             if (a.stall) ok = false;  // the test hook
             const int nowhere = a.c.n_pages << a.page_shift;  // past the last row: the load gives zeros
             const uint64_t policy = l2_policy(static_cast<long long>(a.b.max_q) * a.n_heads <= NR * G);
-            auto load = [&](uint8_t* dst, uint64_t* bar, int col, int row) { load_rows<PAIR>(dst, &maps.rows, bar, col, row, policy); };
+            auto load = [&](uint8_t* dst, uint64_t* bar, int col, int row) { load_rows(dst, &maps.rows, bar, col, row, policy); };
             for (int i = 0; ok && i < n_round; ++i) {
                 const Piece p = sh.piece[i];
                 int row = 0;
@@ -661,11 +637,9 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                         ++ropes;
                         if (leader) {
                             mbar_arrive_expect_tx(&sh.rope_full[rb], L::kRope);
-                            if (!PAIR || static_cast<int>(g & 1) == g_own)
 #pragma unroll
-                                for (int c = 0; c < kKeys / 16; ++c)
-                                    if (c < per_tile)
-                                        load(smem + L::kRopeAt + rb * L::kRope + c * R * 128, &sh.rope_full[rb], C, at[c]);
+                            for (int c = 0; c < kKeys / 16; ++c)
+                                if (c < per_tile) load(smem + L::kRopeAt + rb * L::kRope + c * R * 128, &sh.rope_full[rb], C, at[c]);
                         }
                         __syncwarp();
                     }
@@ -681,10 +655,8 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                         if (leader) {
                             uint8_t* dst = smem + slot * L::kSlot;
                             mbar_arrive_expect_tx(&sh.pair_full[slot], L::kSlot);
-                            if (PAIR && (q & 1) != g_own) {
-                                // the other's to load
-                            } else if (per_tile == 1) {
-                                load_halves<PAIR>(dst, &maps.pairs, &sh.pair_full[slot], at[0], 2 * q, policy);
+                            if (per_tile == 1) {
+                                load_halves(dst, &maps.pairs, &sh.pair_full[slot], at[0], 2 * q, policy);
                             } else {
 #pragma unroll
                                 for (int c = 0; c < kKeys / 16; ++c)
@@ -756,7 +728,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                         for (int k = 0; k < 4; ++k)
                             mma_bf16(tmem + kKeys * sb, dq + ((C / 64) * L::kQBlock >> 4) + 2 * k, dr + (rb * L::kRope >> 4) + 2 * k, id,
                                      k > 0 ? 1u : 0u);
-                        give(&sh.rope_empty[rb]);
+                        mma_commit(&sh.rope_empty[rb]);
                     }
                     for (int q = 0; q < NP; ++q) {
                         const uint32_t fill = g * NP + q, slot = fill % NS;
@@ -798,7 +770,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                             for (int k = 0; k < kKeys / 16; ++k)
                                 mma_bf16(tmem + L::kOut + q * NR, dv + ((slot * L::kSlot + k * 2048) >> 4), dp + 2 * k, id,
                                          (t > a0 || k > 0) ? 1u : 0u);
-                            give(&sh.pair_empty[slot]);
+                            mma_commit(&sh.pair_empty[slot]);
                         }
                         __syncwarp();
                     }
@@ -834,10 +806,6 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     __syncthreads();
     tc_fence_after_sync();
     if (warp == 5) tmem_dealloc(tmem, 512);
-    if (PAIR) {  // nothing of the other is on its way here any more
-        cluster_arrive();
-        cluster_wait();
-    }
 }
 
 // Joins the pieces of row tiles that were split.  Where every row has at most
@@ -1005,12 +973,11 @@ latent_join_kernel(const LatentAttnArgs a, const float* parts, const Join* joins
 
 int rows_of_tile(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-template <int C, int NR, bool PAIR>
+template <int C, int NR, int G>
 cudaError_t launch_t(const LatentAttnArgs& a, cudaStream_t st) {
-    constexpr int G = PAIR ? 2 : 1;
     using L = LCfg<C, NR>;
     static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = allow_smem(latent_attention_kernel<C, NR, PAIR>, L::kSmem, ready);
+    cudaError_t e = allow_smem(latent_attention_kernel<C, NR, G>, L::kSmem, ready);
     if (e != cudaSuccess) return e;
     Maps maps{};
     const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) << a.page_shift;
@@ -1026,19 +993,9 @@ cudaError_t launch_t(const LatentAttnArgs& a, cudaStream_t st) {
     const int n = kSms / G * G;
     Join* joins = static_cast<Join*>(a.workspace);
     float* parts = reinterpret_cast<float*>(joins + kSms);
-    cudaLaunchConfig_t main{};
-    main.gridDim = dim3(n);
-    main.blockDim = dim3(kThreads);
-    main.dynamicSmemBytes = L::kSmem;
-    main.stream = st;
-    cudaLaunchAttribute pair{};
-    pair.id = cudaLaunchAttributeClusterDimension;
-    pair.val.clusterDim.x = 2;
-    pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
-    main.attrs = &pair;
-    main.numAttrs = PAIR ? 1 : 0;
     e = timed_launch("latent_attention", st, [&] {
-        return cudaLaunchKernelEx(&main, latent_attention_kernel<C, NR, PAIR>, a, maps, static_cast<int>(dense_q), parts, joins);
+        latent_attention_kernel<C, NR, G><<<n, kThreads, L::kSmem, st>>>(a, maps, static_cast<int>(dense_q), parts, joins);
+        return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -1059,9 +1016,9 @@ template <int C>
 cudaError_t launch_c(const LatentAttnArgs& a, cudaStream_t st) {
     const long long rows = static_cast<long long>(a.b.max_q) * a.n_heads;
     switch (rows_of_tile(rows)) {
-        case 16: return launch_t<C, 16, false>(a, st);
-        case 32: return launch_t<C, 32, false>(a, st);
-        default: return rows > 64 ? launch_t<C, 64, true>(a, st) : launch_t<C, 64, false>(a, st);
+        case 16: return launch_t<C, 16, 1>(a, st);
+        case 32: return launch_t<C, 32, 1>(a, st);
+        default: return rows > 64 ? launch_t<C, 64, 2>(a, st) : launch_t<C, 64, 1>(a, st);
     }
 }
 
