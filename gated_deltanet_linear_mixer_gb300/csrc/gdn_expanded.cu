@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                 }
                 __syncwarp();
                 if (!some) break;
-                if (a.stall) {  // the test hook
+                if (a.stall == 1) {  // a test hook: no loads
                     ok = false;
                     break;
                 }
@@ -545,10 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                     if (!waiting) ask();
                     while (ok && answer() >= 0) ask();
                 }
-                for (uint32_t f = keys > NK ? keys - NK : 0; f < keys; ++f) mbar_wait_brief(&sh.k_full[f % NK], (f / NK) & 1);
-                for (uint32_t f = values > NV ? values - NV : 0; f < values; ++f) mbar_wait_brief(&sh.v_full[f % NV], (f / NV) & 1);
+                Drain drain;
+                for (uint32_t f = keys > NK ? keys - NK : 0; f < keys; ++f) drain.wait(&sh.k_full[f % NK], (f / NK) & 1);
+                for (uint32_t f = values > NV ? values - NV : 0; f < values; ++f) drain.wait(&sh.v_full[f % NV], (f / NV) & 1);
                 for (int t = 0; t < kTiles; ++t)
-                    if (queries[t] > 0) mbar_wait_brief(&sh.q_full[t], (queries[t] - 1) & 1);
+                    if (queries[t] > 0) drain.wait(&sh.q_full[t], (queries[t] - 1) & 1);
             }
         } else if (warp == 9) {
             // ---- products
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             const uint64_t dq = desc_kmajor_sw128(smem_u32(smem + L::kQAt)), dk = desc_kmajor_sw128(smem_u32(smem)),
                            dv = desc_mnmajor_sw128(smem_u32(smem + L::kVAt), kBlock);
             auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_brief(bar, parity)) != 0; };
-            bool ok = true;
+            bool ok = a.stall != 2;  // a test hook: no products
             uint32_t keys = 0, values = 0, queries[kTiles] = {0, 0}, steps[kTiles] = {0, 0};  // of the items before this one
             for (uint32_t item = 0; ok; ++item) {
                 Item x;

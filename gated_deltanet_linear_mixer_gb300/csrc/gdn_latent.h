@@ -45,7 +45,7 @@ struct LatentAttnArgs {
     void* out;
     void* workspace;
     int* error;
-    int stall;  // test hook: no cached row is ever loaded
+    int stall;  // test hooks: 1 no cached row is ever loaded, 2 no scores are computed
 };
 
 struct ExpandedArgs {
@@ -56,7 +56,7 @@ struct ExpandedArgs {
     KvRows q, k, k_rope, v;
     void* out;
     int* error;
-    int stall;  // test hook: nothing is ever loaded
+    int stall;  // test hooks: 1 nothing is ever loaded, 2 no products are issued
 };
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int latent_dim, cudaStream_t stream);

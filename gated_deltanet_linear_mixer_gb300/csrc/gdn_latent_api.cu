@@ -119,6 +119,8 @@ gdn_status check_rows(const gdn_rows* r, const char* name, gdn::KvRows* out, con
     return GDN_OK;
 }
 
+int stall(const char* loads, const char* products) { return gdn::fault_site(loads) ? 1 : gdn::fault_site(products) ? 2 : 0; }
+
 // Whether rows that are written may overlap: false where one axis' rows lie apart and
 // the other one steps over all of them.
 bool rows_overlap(const gdn::KvRows& r, long long tokens, long long heads, long long width) {
@@ -229,7 +231,7 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
     a.c = gdn::LatentCache{cache->rows, cache->n_pages};
     a.n_heads = dims->n_heads; a.scale = dims->scale; a.out = out; a.workspace = workspace;
     while (1 << a.page_shift < dims->page_size) ++a.page_shift;
-    a.stall = gdn::fault_site("stall_latent") ? 1 : 0;
+    a.stall = stall("stall_latent", "stall_latent_products");
     return cuda_status(gdn::launch_latent_attention(a, dims->latent_dim, static_cast<cudaStream_t>(stream)), fn,
                        "attention launch");
 }
@@ -269,7 +271,7 @@ gdn_status gdn_expanded_attention(const gdn_latent_dims* dims, int32_t n_seq, co
     if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.n_heads = dims->n_heads; a.scale = dims->scale; a.cu_q = cu_q; a.cu_kv = cu_kv; a.out = out;
     a.cu_q_host = cu_q_host; a.cu_kv_host = cu_kv_host;
-    a.stall = gdn::fault_site("stall_expanded") ? 1 : 0;
+    a.stall = stall("stall_expanded", "stall_expanded_products");
     return cuda_status(gdn::launch_expanded_attention(a, dims->nope_dim, dims->v_dim, static_cast<cudaStream_t>(stream)), fn,
                        "attention launch");
 }

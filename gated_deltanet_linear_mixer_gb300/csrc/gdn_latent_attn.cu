@@ -30,7 +30,9 @@
 // (with the page look-ups), one loading queries and issuing S, one issuing O^T.
 // Cached rows are in a ring of 16 KB slots (64 keys x 128 channels) and one of 8 KB
 // slots (position keys).  Every wait is bounded (2 s); a wait that gives up records
-// a code (50..57) in the cache operators' device error word.
+// a code (50..57) in the cache operators' device error word, and its role waits for
+// nothing more but, once for all of them, what it has in flight: a thread block ends
+// within a few such waits.
 //
 // What bounds it.  Up to 32 rows a sequence the rows' bytes: a tile's 72 KB are
 // 3100 cycles of an SM's share of DRAM, its products 2160 (16 rows) or 2290 (32).
@@ -594,7 +596,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
             // and two slots, the second the others.
             const int page_size = 1 << a.page_shift, R = min(page_size, kKeys), per_tile = kKeys >> min(a.page_shift, 6);
             const bool leader = elect_one(), lead_warp = warp == 4;
-            if (a.stall) ok = false;  // the test hook
+            if (a.stall == 1) ok = false;  // a test hook: no loads
             const int nowhere = a.c.n_pages << a.page_shift;  // past the last row: the load gives zeros
             const uint64_t policy = l2_policy(static_cast<long long>(a.b.max_q) * a.n_heads <= NR * G);
             auto load = [&](uint8_t* dst, uint64_t* bar, int col, int row) { load_rows(dst, &maps.rows, bar, col, row, policy); };
@@ -676,6 +678,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
         } else if (warp == 5) {
             // ---- S = Q K^T
             const bool leader = elect_one();
+            if (a.stall == 2) ok = false;  // a test hook: no scores
             constexpr uint32_t id = idesc_bf16_f32(64, kKeys);
             const uint64_t dq = desc_kmajor_sw128(smem_u32(smem + L::kQAt)), dr = desc_kmajor_sw128(smem_u32(smem + L::kRopeAt)),
                            dk = desc_kmajor_sw128(smem_u32(smem));
@@ -791,11 +794,12 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
     }
     // nothing of this thread block is in flight when its memory is given back
     if ((warp == 4 || warp == 7) && sh.dead) {  // else all of it was used
+        Drain drain;
         for (uint32_t s = 0; s < kRopes; ++s)
-            if (ropes > s) mbar_wait_brief(&sh.rope_full[s], ((ropes - 1 - s) / kRopes) & 1);
+            if (ropes > s) drain.wait(&sh.rope_full[s], ((ropes - 1 - s) / kRopes) & 1);
         // this warp's last fill of each slot
         for (uint32_t fill = pairs > NS ? pairs - NS : 0; fill < pairs; ++fill)
-            if ((fill % NP >= 2) == (warp == 7)) mbar_wait_brief(&sh.pair_full[fill % NS], (fill / NS) & 1);
+            if ((fill % NP >= 2) == (warp == 7)) drain.wait(&sh.pair_full[fill % NS], (fill / NS) & 1);
     } else if (warp == 5 || warp == 6) {
         if (warp == 5 && asked > qc) mbar_wait_brief(&sh.q_full, qc & 1);  // queries on their way
         if (elect_one()) mma_commit(&sh.drained[warp - 5]);

@@ -91,6 +91,16 @@ __device__ __forceinline__ bool mbar_wait_brief(uint64_t* bar, uint32_t parity) 
     return true;
 }
 
+// Waits for what is in flight after a wait has given up, one after the other: where one of them
+// takes the whole time, those after it have had as long, and are looked at once.
+struct Drain {
+    bool late = false;
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+        if (late) mbar_try_wait(bar, parity);
+        else late = !mbar_wait_brief(bar, parity);
+    }
+};
+
 // --------------------------------------------------------------------- TMA
 // 2-D tiled bulk tensor load global -> shared, completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,

@@ -45,14 +45,16 @@
  *   latent_read, latent_attention, expanded_attention, copy_pages, or all.  A call
  *   whose site is listed validates its arguments, then returns
  *   GDN_ERR_INJECTED without enqueuing anything, so every caller buffer is
- *   left as it was.  Four sites are device test hooks, under which a bounded
+ *   left as it was.  Six sites are device test hooks, under which a bounded
  *   wait runs out, the call returns GDN_OK and the next gdn_sync_status
  *   reports GDN_ERR_TIMEOUT: stall_scan (a bf16 prefill that takes the fused
  *   tensor-core launch makes its scan wait, for at most 1 ms, on a chunk flag
  *   that nothing sets), stall_attention (a gdn_kv_attention call that takes
  *   the kernel for many rows waits, for 2 s, for page look-ups that are never
  *   published), stall_latent and stall_expanded (gdn_latent_attention and
- *   gdn_expanded_attention wait, for 2 s, for loads that are never started).  GDN_FAULT is read on every call.
+ *   gdn_expanded_attention wait, for 2 s, for loads that are never started),
+ *   stall_latent_products and stall_expanded_products (the same for products, with
+ *   loads in flight).  GDN_FAULT is read on every call.
  */
 #ifndef GDN_H
 #define GDN_H

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gated_deltanet_linear_mixer_gb300 as gdn
-from latent_cases import absorbed, check, cu_of, gen, ints, make_cache
+from latent_cases import absorbed, check, cu_of, expanded, gen, ints, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,43 @@ def test_few_rows_and_many_short_ragged_sequences(heads, dc):
     gdn.sync_status()
     check(outs[0], *want)
     assert all(torch.equal(outs[0], o) for o in outs)
+
+
+@pytest.mark.parametrize("heads,dc,counts,lens", [(16, 512, [1, 1], [5000, 900]), (32, 256, [1] * 400, [400] * 400),
+                                                  (32, 512, [4, 1], [3000, 200]), (128, 256, [2] * 90, [700] * 90)])
+def test_latent_attention_gives_up_with_loads_in_flight(monkeypatch, heads, dc, counts, lens):
+    """Products that are never issued: full rings, whose loads are waited for at the end."""
+    d = gdn.LatentDims(heads, dc, page_size=32)
+    cache, table = make_cache(d, lens, 321)
+    q, cu = _queries(sum(counts), heads, dc + 64, 322), cu_of(counts)
+    monkeypatch.setenv("GDN_FAULT", "stall_latent_products")
+    torch.cuda.synchronize()
+    start = time.monotonic()
+    gdn.latent_attention(d, cache, cu, ints(lens), table, q)
+    _timeout()
+    assert time.monotonic() - start < 20.0
+    monkeypatch.delenv("GDN_FAULT")
+    got = gdn.latent_attention(d, cache, cu, ints(lens), table, q)
+    gdn.sync_status()
+    check(got, *absorbed(d, cache, counts, lens, table, q))
+
+
+@pytest.mark.parametrize("nope,vd", [(128, 128), (64, 64)])
+def test_expanded_attention_gives_up_with_loads_in_flight(monkeypatch, nope, vd):
+    d = gdn.LatentDims(24, nope_dim=nope, v_dim=vd)
+    counts, lens = [300, 5, 130, 256] * 3, [2300, 400, 131, 700] * 3
+    g = gen(331)
+    kv = torch.randn(sum(lens), 24, nope + vd, generator=g, device="cuda").bfloat16()
+    r = torch.randn(sum(lens), 64, generator=g, device="cuda").bfloat16()
+    q = _queries(sum(counts), 24, nope + 64, 332)
+    args = (d, cu_of(counts), cu_of(lens), q, kv[..., :nope], r, kv[..., nope:])
+    monkeypatch.setenv("GDN_FAULT", "stall_expanded_products")
+    torch.cuda.synchronize()
+    start = time.monotonic()
+    gdn.expanded_attention(*args)
+    _timeout()
+    assert time.monotonic() - start < 20.0
+    monkeypatch.delenv("GDN_FAULT")
+    got = gdn.expanded_attention(*args)
+    gdn.sync_status()
+    check(got, *expanded(d, counts, lens, *args[3:]))
