@@ -66,6 +66,12 @@ constexpr int kSms = 152;
 constexpr int kM = 128, kKeys = 128, kTiles = 2;
 constexpr int kThreads = 384;
 constexpr float kLazy = 8.0f;
+// The reference is rounded (m = fl(scale log2 e top)) and a weight 2^fma(scale log2 e, score, -m), so that
+// a row's largest weight is 2^e, e the rounding's error: up to half a unit of m's last place, which from 2^31 on
+// leaves fp32's exponents (all weights 0, or infinite).  Beyond kFar, where e is 2^-15, differences are taken
+// before the scale: two operations a pair of scores instead of one (always so: 134 and 153 us where the two cases above
+// take 127 and 143; by this rule as long as before).
+constexpr float kFar = 1024.0f;
 constexpr uint32_t kBlock = 16384;  // 128 rows x 64 channels
 constexpr uint32_t kSmemMax = 232448, kSharedBytes = 2944;
 constexpr int kMaxSlots = 12;
@@ -306,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             const bool mine = row < x.qn;
             const int lim = mine ? max(0, min(x.start + row + 1, x.kv)) : 0;  // keys that the row sees
             const int low = __reduce_min_sync(0xffffffffu, lim);
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f;  // the reference (a score before the scale), the sum
+            bool far = false;               // whether one of the warp's rows has a reference beyond kFar
             int kt = x.step == 2 ? t : 0;  // the key tile
             for (int i = 0; i < n; ++i, ++steps, kt += x.step) {
                 const int key0 = kt * kKeys;
@@ -325,16 +332,23 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                 float tops[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int j = 4; j < kKeys; ++j) tops[j & 3] = fmaxf(tops[j & 3], s[j]);
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale2;
-                const bool lift = __any_sync(0xffffffffu, top > m + kLazy);
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                const bool lift = __any_sync(0xffffffffu, (top - m) * scale2 > kLazy);
                 float f = 1.0f;
                 if (lift) {
                     const float mn = fmaxf(m, top);
-                    f = m == -INFINITY ? 0.0f : exp2_ftz(m - mn);
+                    f = m == -INFINITY ? 0.0f : exp2_ftz((m - mn) * scale2);
                     m = mn;
                     l *= f;
+                    far = far || __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * scale2) > kFar);
                 }
-                const float ref = m == -INFINITY ? 0.0f : -m;
+                float ref = m == -INFINITY ? 0.0f : -m * scale2;
+                if (far) {
+                    const float less = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                    for (int j = 0; j < kKeys; ++j) s[j] -= less;
+                    ref = 0.0f;
+                }
                 const uint64_t scale22 = pair(scale2, scale2), ref2 = pair(ref, ref);
                 uint64_t sums[2] = {0, 0};
 #pragma unroll
@@ -403,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
                 meet(sh.stat_full);
                 const float2 s0 = sh.stat[0][r], s1 = sh.stat[1][r];
                 const float top = fmaxf(s0.x, s1.x);
-                float f0 = s0.y == 0.0f ? 0.0f : exp2_ftz(s0.x - top), f1 = s1.y == 0.0f ? 0.0f : exp2_ftz(s1.x - top);
+                float f0 = s0.y == 0.0f ? 0.0f : exp2_ftz((s0.x - top) * scale2), f1 = s1.y == 0.0f ? 0.0f : exp2_ftz((s1.x - top) * scale2);
                 const float sum = s0.y * f0 + s1.y * f1, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 f0 *= inv;
                 f1 *= inv;

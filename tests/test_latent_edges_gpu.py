@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gated_deltanet_linear_mixer_gb300 as gdn
-from latent_cases import absorbed, check, cu_of, expanded, gen, ints, make_cache
+from latent_cases import U, absorbed, check, cu_of, expanded, gen, ints, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +101,34 @@ def test_expanded_attention_gives_up_with_loads_in_flight(monkeypatch, nope, vd)
     got = gdn.expanded_attention(*args)
     gdn.sync_status()
     check(got, *expanded(d, counts, lens, *args[3:]))
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("exponent", [16, 31, 40, 90])
+def test_very_large_scores_pick_one_key(sign, exponent):
+    """Scores n 2^exponent, n a whole number of its own for each key: exact in fp32, and far enough apart
+    (192^-1/2 2^16 = 4730) that all weights but the largest are 0: the result is that key's value, to the
+    rounding of its weight (at most U; the sum takes it unrounded) and of the result (at most U more)."""
+    d = gdn.LatentDims(2)
+    counts, lens = [300, 5, 130], [300, 700, 1000]
+    g = gen(341)
+    q = torch.zeros(sum(counts), 2, 192, dtype=torch.bfloat16, device="cuda")
+    q[..., 5:7] = sign * 2.0 ** (exponent // 2)
+    k = torch.zeros(sum(lens), 2, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.randn(sum(lens), 2, 128, generator=g, device="cuda").bfloat16()
+    r = torch.zeros(sum(lens), 64, dtype=torch.bfloat16, device="cuda")
+    want, b = [], 0
+    for c, n in zip(counts, lens):
+        picks = []
+        for h in range(2):
+            rank = torch.randperm(n, generator=g, device="cuda") + 1
+            k[b:b + n, h, 5] = (rank // 32 * 32 * 2.0 ** (exponent - exponent // 2)).bfloat16()
+            k[b:b + n, h, 6] = (rank % 32 * 2.0 ** (exponent - exponent // 2)).bfloat16()
+            best = (sign * rank).cummax(0).indices[n - c:]  # of the keys up to each query's position
+            picks.append(v[b + best, h])
+        want.append(torch.stack(picks, 1))
+        b += n
+    got = gdn.expanded_attention(d, cu_of(counts), cu_of(lens), q, k, r, v)
+    gdn.sync_status()
+    want = torch.cat(want).double()
+    check(got, want, want.abs() * (2 * U + U * U))
