@@ -10,6 +10,7 @@
 #include "gdn.h"
 #include "gdn_internal.h"
 #include "gdn_latent.h"
+#include "gdn_memory.h"
 
 namespace gdn {
 // Records the thread's error message (defined with the other entry points).
@@ -20,6 +21,7 @@ gdn_status inject_fault(const char* site, const char* fn);
 bool fault_site(const char* site);  // whether it does
 }  // namespace gdn
 
+using gdn::Memory;
 using gdn::set_error;
 using gdn::timed_launch;
 
@@ -130,6 +132,10 @@ bool rows_overlap(const gdn::KvRows& r, long long tokens, long long heads, long 
     return (ts - width) / (heads - 1) < hs && (hs - width) / (tokens - 1) < ts;
 }
 
+Memory memory(const gdn::KvRows& r, long long tokens, long long heads, long long channels) {
+    return Memory::rows(r.data, tokens, heads, r.token_stride, r.head_stride, channels, 2);
+}
+
 }  // namespace
 
 extern "C" {
@@ -150,6 +156,7 @@ gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache
     if (c) r = gdn_rows{c->data, c->token_stride, 0};
     if ((st = check_rows(&r, "c", &a.rows, fn)) != GDN_OK) return st;
     if (norm_w && !aligned16(norm_w)) return set_error(GDN_ERR_INVALID_ARG, fn, "norm_w must be 16-byte aligned");
+    if (q_out && !q_rope) return set_error(GDN_ERR_INVALID_ARG, fn, "q_out is given without q_rope");
     if (q_rope) {
         if (static_cast<long long>(a.b.n_tokens) * dims->n_heads > 0x7fffff00)
             return set_error(GDN_ERR_UNSUPPORTED, fn, "%d tokens of %d heads are more than 2^31 - 256 rows", a.b.n_tokens, dims->n_heads);
@@ -161,6 +168,20 @@ gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache
     if (rope && (rope_len < 1 || !aligned16(rope)))
         return set_error(GDN_ERR_INVALID_ARG, fn, "rope must hold at least one row and be 16-byte aligned");
     if (rows_out && !aligned16(rows_out)) return set_error(GDN_ERR_INVALID_ARG, fn, "rows_out must be 16-byte aligned");
+    // what is written while other warps still read: the same rows, or memory of its own
+    const long long tokens = a.b.n_tokens, width = dims->latent_dim + dims->rope_dim;
+    const Memory in_q = memory(a.q, tokens, dims->n_heads, dims->rope_dim), to_q = memory(a.q_out, tokens, dims->n_heads, dims->rope_dim);
+    if (q_rope && !gdn::same(in_q, to_q) && gdn::meet(in_q, to_q))
+        return set_error(GDN_ERR_INVALID_ARG, fn, "q_out shares memory with q_rope and is not the same rows");
+    if (rows_out) {
+        const Memory packed = Memory::array(rows_out, 2 * tokens * width);
+        const bool in_place = rows_out == a.rows.data && (tokens == 1 || a.rows.token_stride == width);
+        if (!in_place && gdn::meet(packed, memory(a.rows, tokens, 1, width)))
+            return set_error(GDN_ERR_INVALID_ARG, fn, "rows_out shares memory with c and is not the same rows");
+        if (gdn::meet(packed, Memory::array(cache->rows, 2ll * cache->n_pages * dims->page_size * width)) ||
+            (q_rope && (gdn::meet(packed, in_q) || gdn::meet(packed, to_q))))
+            return set_error(GDN_ERR_INVALID_ARG, fn, "rows_out shares memory with the cache, q_rope or q_out");
+    }
     if ((st = gdn::inject_fault("latent_append", fn)) != GDN_OK) return st;
     if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.c = gdn::LatentCache{cache->rows, cache->n_pages};

@@ -491,13 +491,16 @@ typedef struct gdn_latent_cache {
  *   rope [rope_len, rope_dim] fp32 (cosines | sines), positions [T] int32 or
  *   NULL: as in gdn_kv_append.
  *   q_rope [T, n_heads, rope_dim] rows or NULL, q_out the same (its memory is
- *   written; may be q_rope itself): rows of a wider query buffer, its last
- *   rope_dim channels, for one.  q_out's rows must not overlap one another: a
- *   token's heads lie before the next token's, or a head's tokens before the next
- *   head's (else refused).
+ *   written; may be q_rope itself, with its strides): rows of a wider query
+ *   buffer, its last rope_dim channels, for one.  q_out's rows must not overlap one
+ *   another: a token's heads lie before the next token's, or a head's tokens before
+ *   the next head's (else refused).  q_out without q_rope is refused.
  *   rows_out [T, latent_dim + rope_dim] contiguous or NULL: the rows as stored,
  *   packed, of every token of the call (those of unmapped pages too); may be c
  *   itself where that is contiguous.
+ * But for these two in-place forms, q_out and rows_out share no memory with one
+ * another, the inputs or the cache.  (Refused: q_out with q_rope, where the token
+ * strides are the same or the two do not interleave; rows_out with any.)
  */
 gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache* cache,
                              const gdn_kv_batch* batch, const int32_t* kv_lens, const gdn_rows* c,
