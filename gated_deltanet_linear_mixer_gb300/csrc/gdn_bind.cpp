@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "gdn.h"
+#include "gdn_memory.h"
 
 namespace {
 
@@ -379,6 +380,16 @@ gdn_rows bf16_rows(PyObject* o, const char* name, int64_t tokens, int64_t heads,
     return bf16_rows(tensor(o, name), name, tokens, heads, width);
 }
 
+// What is written (`name`) is no memory that other thread blocks still read.
+using gdn::Memory;
+Memory memory(const gdn_rows& r, int64_t tokens, int64_t heads, int64_t width) {
+    return Memory::rows(r.data, tokens, heads, r.token_stride, r.head_stride, width, 2);
+}
+Memory memory(const at::Tensor& t) { return Memory::array(t.data_ptr(), static_cast<long long>(t.nbytes())); }
+void want_apart(const char* name, const Memory& m, const char* other, const Memory& o) {
+    if (gdn::meet(m.joined(), o.joined())) bad(PyExc_ValueError, "%s shares memory with %s", name, other);
+}
+
 // dims, cache.rows, cu_dev, cu_host, kv_lens, block_table, c, norm_w, q_rope, q_out, rope, positions, rows_out
 PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 13, [&]() -> PyObject* {
@@ -403,6 +414,11 @@ PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             out = a[9] != Py_None ? tensor(a[9], "q_out")
                                   : at::empty({tokens, d->n_heads, d->rope_dim}, like.options().dtype(at::kBFloat16));
             q_out = bf16_rows(out, "q_out", tokens, d->n_heads, d->rope_dim);
+            const Memory written = memory(q_out, tokens, d->n_heads, d->rope_dim);
+            const Memory read = memory(q, tokens, d->n_heads, d->rope_dim);
+            if (!gdn::same(written, read)) want_apart("q_out", written, "q_rope", read);
+            want_apart("q_out", written, "c", memory(rows, tokens, 1, width));
+            want_apart("q_out", written, "cache.rows", memory(tensor(a[1], "cache.rows")));
         }
         const float* rope = nullptr;
         int64_t rope_rows = 0;
@@ -436,6 +452,7 @@ PyObject* latent_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int64_t tokens;
         const gdn_kv_batch b = batch_of(a[2], a[3], a[4], "starts", a[5], &starts, &tokens);
         at::Tensor out = output(a[6], "out", at::kBFloat16, {tokens, d->latent_dim + d->rope_dim}, THPVariable_Unpack(a[5]));
+        want_apart("out", memory(out), "cache.rows", memory(tensor(a[1], "cache.rows")));
         check("gdn_latent_read", gdn_latent_read(d, &c, &b, starts, out.data_ptr(), Launch(device).stream()));
         return THPVariable_Wrap(out);
     });
@@ -464,6 +481,14 @@ PyObject* latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
             check("gdn_latent_attention_workspace_size",
                   gdn_latent_attention_workspace_size(d, b.n_seq, b.cu_seqlens_host, &need));
             if (need) ws = at::empty({static_cast<int64_t>(need)}, like.options().dtype(at::kByte));
+        }
+        const Memory in_q = memory(q, tokens, d->n_heads, d->latent_dim + d->rope_dim), in_c = memory(tensor(a[1], "cache.rows"));
+        want_apart("out", memory(out), "q", in_q);
+        want_apart("out", memory(out), "cache.rows", in_c);
+        if (a[8] != Py_None) {
+            want_apart("workspace", memory(ws), "q", in_q);
+            want_apart("workspace", memory(ws), "cache.rows", in_c);
+            want_apart("workspace", memory(ws), "out", memory(out));
         }
         check("gdn_latent_attention",
               gdn_latent_attention(d, &c, &b, lens, &q, out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr,
@@ -500,6 +525,11 @@ PyObject* expanded_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const gdn_rows r = bf16_rows(a[7], "k_rope", ck.total, 0, d->rope_dim);
         const gdn_rows v = bf16_rows(a[8], "v", ck.total, d->n_heads, d->v_dim);
         at::Tensor out = output(a[9], "out", at::kBFloat16, {cq.total, d->n_heads, d->v_dim}, THPVariable_Unpack(a[5]));
+        const Memory written = memory(out);
+        want_apart("out", written, "q", memory(q, cq.total, d->n_heads, d->nope_dim + d->rope_dim));
+        want_apart("out", written, "k", memory(k, ck.total, d->n_heads, d->nope_dim));
+        want_apart("out", written, "k_rope", memory(r, ck.total, 1, d->rope_dim));
+        want_apart("out", written, "v", memory(v, ck.total, d->n_heads, d->v_dim));
         check("gdn_expanded_attention",
               gdn_expanded_attention(d, static_cast<int32_t>(cq.n), cq.dev, cq.host, ck.dev, ck.host, &q, &k, &r, &v,
                                      out.data_ptr(), Launch(device).stream()));

@@ -12,12 +12,22 @@ struct Memory {
                        long long bytes) {
         Memory m{static_cast<long long>(reinterpret_cast<uintptr_t>(p)), tokens > 1 ? token_stride : 0,
                  heads > 1 ? head_stride : 0, tokens, heads, bytes * channels};
-        if (m.token_stride >= 1ll << 56 || m.head_stride >= 1ll << 56) m.width = 0;  // no memory is as large
+        // no rows, or strides that no memory is large enough for
+        if (tokens < 1 || heads < 1 || m.token_stride >= 1ll << 56 || m.head_stride >= 1ll << 56) m.width = 0;
         m.token_stride *= m.width ? bytes : 0;
         m.head_stride *= m.width ? bytes : 0;
         return m;
     }
     static Memory array(const void* p, long long bytes) { return rows(p, 1, 1, 0, 0, bytes, 1); }
+    // The same bytes as fewer and longer rows, where rows lie side by side.
+    Memory joined() const {
+        Memory m = *this;
+        for (int i = 0; i < 2; ++i) {
+            if (m.heads > 1 && m.head_stride == m.width) m.width *= m.heads, m.heads = 1, m.head_stride = 0;
+            if (m.tokens > 1 && m.token_stride == m.width) m.width *= m.tokens, m.tokens = 1, m.token_stride = 0;
+        }
+        return m;
+    }
     bool end(long long* at) const {  // false where that is no address
         long long t, h;
         return !__builtin_mul_overflow(tokens - 1, token_stride, &t) && !__builtin_mul_overflow(heads - 1, head_stride, &h) &&

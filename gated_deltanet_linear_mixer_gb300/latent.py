@@ -4,7 +4,8 @@ A layer of this kind keeps one vector a token: a normalised latent that the keys
 and values of all heads are projections of, and a position key that all heads
 share.  Like the rest of the binding this only marshals arguments
 (``csrc/gdn_bind.cpp`` checks them); ``include/gdn.h`` states layouts, formulas
-and errors.
+and errors.  Outputs share no memory with inputs, but for latent_append's two in-place forms
+(``q_out`` is ``q_rope``, ``rows_out`` is a contiguous ``c``): else ``ValueError`` or ``GDNError``.
 
 A step of single tokens or drafts, in the absorbed form (``w_uk`` [H, nope,
 latent] and ``w_uv`` [H, latent, v] are the halves of the up projection)::

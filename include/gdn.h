@@ -499,8 +499,8 @@ typedef struct gdn_latent_cache {
  *   packed, of every token of the call (those of unmapped pages too); may be c
  *   itself where that is contiguous.
  * But for these two in-place forms, q_out and rows_out share no memory with one
- * another, the inputs or the cache.  (Refused: q_out with q_rope, where the token
- * strides are the same or the two do not interleave; rows_out with any.)
+ * another, the inputs or the cache.  (Refused here: q_out in q_rope's memory at the
+ * same token stride, rows_out in any.  The Python binding refuses what it can tell.)
  */
 gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache* cache,
                              const gdn_kv_batch* batch, const int32_t* kv_lens, const gdn_rows* c,
@@ -511,7 +511,8 @@ gdn_status gdn_latent_append(const gdn_latent_dims* dims, const gdn_latent_cache
 /*
  * gdn_latent_read -- cached rows back out of the pages: of sequence i the
  * cu_seqlens[i+1] - cu_seqlens[i] tokens from position starts[i] on, packed,
- * into out [R, latent_dim + rope_dim] bf16.  Tokens of unmapped pages read as 0.
+ * into out [R, latent_dim + rope_dim] bf16, which shares no memory with the cache.
+ * Tokens of unmapped pages read as 0.
  */
 gdn_status gdn_latent_read(const gdn_latent_dims* dims, const gdn_latent_cache* cache,
                            const gdn_kv_batch* batch, const int32_t* starts, void* out,
@@ -523,7 +524,7 @@ gdn_status gdn_latent_read(const gdn_latent_dims* dims, const gdn_latent_cache* 
  * over the positions j up to the query's own.  A query that sees no key gives
  * zeros.
  *   q [T, n_heads, latent_dim + rope_dim] rows (rotated already), out [T,
- *   n_heads, latent_dim] contiguous.
+ *   n_heads, latent_dim] contiguous, which shares no memory with q or the cache.
  *   workspace: at least gdn_latent_attention_workspace_size() bytes, 256-byte
  *   aligned.  Calls that may run at the same time need one each.
  *   T x n_heads at most 2^31 - 256 (gdn_latent_append with q_rope: the same).
@@ -550,7 +551,7 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
  *   n_heads, v_dim] rows (one projection's output may hold k and v side by
  *   side), k_rope [Tk, rope_dim] rows (head_stride is not used); token strides
  *   > 0, a head stride of 0 shares one head.  out [Tq, n_heads, v_dim]
- *   contiguous.
+ *   contiguous, which shares no memory with the inputs.
  * The work is laid out by the host copies: a captured call keeps its sequences.  A
  * sequence has at most 2^24 queries, a call 2^30 keys.
  * Values that some query of a sequence sees have to be finite.  fp32 accumulation

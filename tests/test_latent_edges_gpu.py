@@ -132,3 +132,68 @@ def test_very_large_scores_pick_one_key(sign, exponent):
     gdn.sync_status()
     want = torch.cat(want).double()
     check(got, want, want.abs() * (2 * U + U * U))
+
+
+def test_outputs_in_the_inputs_memory_are_refused():
+    """Every output in every input's memory in turn; next to it is right."""
+    d = gdn.LatentDims(2, 256, page_size=16, nope_dim=64, v_dim=64)
+    cache, table = make_cache(d, [40], 351)
+    cu, lens = cu_of([4]), ints([40])
+    big = torch.randn(1 << 16, generator=gen(352), device="cuda").bfloat16()
+
+    def rows(at, *shape):
+        n = 1
+        for x in shape:
+            n *= x
+        return big[at:at + n].view(shape)
+
+    q, k, v, r, qe = rows(0, 4, 2, 320), rows(8192, 9, 2, 64), rows(16384, 9, 2, 64), rows(24576, 9, 64), rows(32768, 4, 2, 128)
+    want = gdn.latent_attention(d, cache, cu, lens, table, q)
+    for at, bad in ((0, True), (2560 - 8, True), (2560, False)):
+        out = rows(at, 4, 2, 256)
+        if bad:
+            with pytest.raises(ValueError, match="out shares memory with q"):
+                gdn.latent_attention(d, cache, cu, lens, table, q, out=out)
+        else:
+            assert torch.equal(gdn.latent_attention(d, cache, cu, lens, table, q, out=out), want)
+    flat = cache.rows.view(-1)
+    with pytest.raises(ValueError, match="out shares memory with cache.rows"):
+        gdn.latent_attention(d, cache, cu, lens, table, q, out=flat[320:320 + 2048].view(4, 2, 256))
+    size = gdn.latent_attention_workspace_size(d, cu)
+    space = torch.empty(size + 4096, dtype=torch.uint8, device="cuda")
+    out = space[size:size + 4096].view(torch.bfloat16).view(4, 2, 256)
+    assert torch.equal(gdn.latent_attention(d, cache, cu, lens, table, q, out=out, workspace=space[:size]), want)
+    with pytest.raises(ValueError, match="workspace shares memory with out"):
+        gdn.latent_attention(d, cache, cu, lens, table, q, out=out, workspace=space)
+    with pytest.raises(ValueError, match="out shares memory with cache.rows"):
+        gdn.latent_read(d, cache, cu, ints([0]), table, out=flat[-1280:].view(4, 320))
+    ck = cu_of([9])
+    want = gdn.expanded_attention(d, cu, ck, qe, k, r, v)
+    for x, name in ((qe, "q"), (k, "k"), (r, "k_rope"), (v, "v")):
+        at = (x.data_ptr() - big.data_ptr()) // 2 + x.numel()
+        with pytest.raises(ValueError, match=f"out shares memory with {name}$"):
+            gdn.expanded_attention(d, cu, ck, qe, k, r, v, out=rows(at - 8, 4, 2, 64))
+        assert torch.equal(gdn.expanded_attention(d, cu, ck, qe, k, r, v, out=rows(at, 4, 2, 64)), want)
+    c, q_rope = rows(40960, 4, 320), rows(49152, 4, 2, 64)
+    for q_out, other in ((c.view(-1)[:512], "c"), (flat[:512], "cache.rows")):
+        with pytest.raises(ValueError, match=f"q_out shares memory with {other}"):
+            gdn.latent_append(d, cache, cu, lens, table, c, q_rope=q_rope, q_out=q_out.view(4, 2, 64))
+    for at, other in ((49152 + 64, 128), (49152 + 256, 256)):  # shifted by a head; at another token stride
+        with pytest.raises(ValueError, match="q_out shares memory with q_rope"):
+            gdn.latent_append(d, cache, cu, lens, table, c, q_rope=q_rope, q_out=rows(at, 4, other // 64, 64)[:, :2])
+    for outs in ({"rows_out": rows(40960 + 8, 4, 320)}, {"rows_out": rows(49152, 4, 320)}):
+        with pytest.raises(gdn.GDNError, match="shares memory"):
+            gdn.latent_append(d, cache, cu, lens, table, c, q_rope=q_rope, **outs)
+    gdn.sync_status()
+    # no tokens share nothing
+    none = cu_of([0])
+    assert gdn.latent_append(d, cache, none, lens, table, c[:0], q_rope=q_rope[:0], q_out=q_rope[:0], rows_out=c[:0]).shape == (0, 2, 64)
+    assert gdn.latent_append(d, cache, none, lens, table, c[:0], q_rope=q_rope[:0]).shape == (0, 2, 64)
+    assert gdn.latent_attention(d, cache, none, lens, table, q[:0], out=q[:0, :, :256]).shape == (0, 2, 256)
+    assert gdn.expanded_attention(d, none, none, qe[:0], k[:0], r[:0], v[:0], out=v[:0]).shape == (0, 2, 64)
+    # a projection's output that holds c and the queries side by side, turned in place
+    side = torch.randn(4, 2 * 128 + 320, generator=gen(353), device="cuda").bfloat16()
+    turned = gdn.latent_append(d, cache, cu, lens, table, side[:, 256:], q_rope=side[:, :256].view(4, 2, 128)[..., 64:],
+                               q_out=side[:, :256].view(4, 2, 128)[..., :64])
+    assert torch.equal(turned, side[:, :256].view(4, 2, 128)[..., 64:])
+    gdn.sync_status()
