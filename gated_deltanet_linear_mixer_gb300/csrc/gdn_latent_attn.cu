@@ -221,6 +221,8 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
     if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
     return x / y;
 }
+// Key tiles of n keys, up to 2^31 - 1.
+__device__ __forceinline__ int tiles_of(int n) { return static_cast<int>((static_cast<uint32_t>(n) + kKeys - 1) / kKeys); }
 template <int ROWS>
 __device__ __forceinline__ Need need_of(const LatentAttnArgs& a, int seq) {
     Need n;
@@ -230,7 +232,7 @@ __device__ __forceinline__ Need need_of(const LatentAttnArgs& a, int seq) {
     const long long cap = a.c.n_pages > 0 ? static_cast<long long>(a.b.pages_per_seq) << a.page_shift : 0;
     const int len = static_cast<int>(min(static_cast<long long>(max(n.len, 0)), cap));
     n.groups = (n.qn * a.n_heads + ROWS - 1) / ROWS;
-    n.tiles = max(1, (len + kKeys - 1) / kKeys);
+    n.tiles = max(1, tiles_of(len));
     return n;
 }
 
@@ -364,7 +366,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
             p.n_keys = max(0, min(p.start + last_row / a.n_heads + 1, len));
             p.a = static_cast<int>(max(u0 - head, 0ll));
             const int b = static_cast<int>(min(u1 - head, static_cast<long long>(n_at.tiles)));
-            p.b = max(p.a, min(b, (p.n_keys + kKeys - 1) / kKeys));
+            p.b = max(p.a, min(b, tiles_of(p.n_keys)));
             p.slot = p.a == 0 && b == n_at.tiles ? -1 : 2 * span + (head + p.a > u0 ? 1 : 0);
             sh.piece[i++] = p;
             if (head + n_at.tiles >= u1) {  // the span's last one
@@ -446,7 +448,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                         if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
 #pragma unroll
                         for (int j = 0; j < kScores; ++j) s[j] *= scale2;
-                        if (key0 + kKeys > lim || mask != (1 << (kKeys / 16)) - 1) {
+                        if (lim - key0 < kKeys || mask != (1 << (kKeys / 16)) - 1) {
                             const int c = key0 + 2 * (lane & 3);
 #pragma unroll
                             for (int j = 0; j < kScores; ++j) {
@@ -605,8 +607,9 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                 int row = 0;
                 const int first_chunk = p.a * per_tile, n = (p.b - p.a) * per_tile;
                 auto look_up = [&](int x) {  // where chunk x of the piece lies; negative: not mapped
+                    if (x >= n) return nowhere;
                     const int key = (first_chunk + x) * R;
-                    if (x >= n || key >= p.n_keys) return nowhere;
+                    if (key >= p.n_keys) return nowhere;
                     const int page = a.b.table[static_cast<size_t>(p.seq) * a.b.pages_per_seq + (key >> a.page_shift)];
                     return page >= 0 && page < a.c.n_pages ? (page << a.page_shift) + (key & (page_size - 1)) : -1;
                 };

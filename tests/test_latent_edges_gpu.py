@@ -197,3 +197,23 @@ def test_outputs_in_the_inputs_memory_are_refused():
                                q_out=side[:, :256].view(4, 2, 128)[..., :64])
     assert torch.equal(turned, side[:, :256].view(4, 2, 128)[..., 64:])
     gdn.sync_status()
+
+
+@pytest.mark.parametrize("short", [1, 64, 65])
+def test_lengths_next_to_the_largest_32_bit_number(short):
+    """One page a sequence over and over, its keys alike, then the last one: its last key, which the last
+    query alone sees, has a score far above the others'.  All sums are whole numbers below 2^24."""
+    d = gdn.LatentDims(16, 256, page_size=128)
+    n = 2 ** 31 - short
+    pages = (n + 127) // 128
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    rows = torch.zeros(2, 128, 320, dtype=torch.bfloat16, device="cuda")
+    rows[..., :256] = 1.0
+    last = (n - 1) % 128
+    rows[1, last, :256], rows[1, last, 256], rows[1, last + 1:] = 3.0, 64.0, float("nan")
+    q = torch.zeros(2, 16, 320, dtype=torch.bfloat16, device="cuda")
+    q[..., 256] = 64.0
+    got = gdn.latent_attention(d, gdn.LatentCache(d, rows), cu_of([2]), ints([n]), table, q)
+    gdn.sync_status()
+    assert bool((got[0] == 1.0).all()) and bool((got[1] == 3.0).all())
