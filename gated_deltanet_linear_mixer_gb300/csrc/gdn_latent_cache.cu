@@ -68,6 +68,11 @@ __device__ __forceinline__ uint4 finite_bf16(const float* x) {
                       pack_bf16_pair(y[6], y[7]));
 }
 
+// The norm's range.  Squares of bf16 numbers from 2^64 on are infinite in fp32, those below 2^-75 are 0; a row whose
+// mean square (with eps) is out of these bounds is scaled first.  (eps is at most 2^-90 where k is 2^100.)
+constexpr float kTopSquare = 1.6615350e35f, kLowSquare = 8.0779357e-28f;  // 2^117, 2^-90
+constexpr float kDown = 8.4703295e-22f, kUp = 1.2676506e30f;              // 2^-70, 2^100
+
 constexpr int kAppendThreads = 128;
 constexpr int kUnits = 4;   // of a position part
 constexpr int kQUnits = 4;  // units of q a lane has in flight: 32 heads a warp
@@ -139,17 +144,26 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
 #pragma unroll
     for (int i = 0; i < N; ++i) Vec16<bf16>::unpack(raw[i], x + 8 * i);
     if (a.norm_w) {
-        float sum = 0.0f;
+        float g[8 * N];
 #pragma unroll
-        for (int i = 0; i < 8 * N; ++i) sum = fmaf(x[i], x[i], sum);
-        const float r = rsqrtf(group_sum<32>(sum) * (1.0f / C) + a.eps);
+        for (int i = 0; i < 8 * N; i += 4) Vec16<float>::load(a.norm_w + 8 * lane + 256 * (i / 8) + i % 8, g + i);
+        auto mean_square = [&] {
+            float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8 * N; i += 4) {
-            float g[4];
-            Vec16<float>::load(a.norm_w + 8 * lane + 256 * (i / 8) + i % 8, g);
+            for (int i = 0; i < 8 * N; ++i) sum = fmaf(x[i], x[i], sum);
+            return group_sum<32>(sum) * (1.0f / C);
+        };
+        float eps = a.eps, mean = mean_square();
+        if (mean > kTopSquare || mean + eps < kLowSquare) {  // squares that leave fp32: those of k x, with k^2 eps
+            const float k = mean > kTopSquare ? kDown : kUp;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[i + e] = x[i + e] * r * g[e];
+            for (int i = 0; i < 8 * N; ++i) x[i] *= k;
+            eps = eps * k * k;
+            mean = mean_square();
         }
+        const float r = rsqrtf(mean + eps);
+#pragma unroll
+        for (int i = 0; i < 8 * N; ++i) x[i] = x[i] * r * g[i];
     }
     uint4 v[N], k0 = make_uint4(0, 0, 0, 0), k1 = k0;
 #pragma unroll

@@ -217,3 +217,31 @@ def test_lengths_next_to_the_largest_32_bit_number(short):
     got = gdn.latent_attention(d, gdn.LatentCache(d, rows), cu_of([2]), ints([n]), table, q)
     gdn.sync_status()
     assert bool((got[0] == 1.0).all()) and bool((got[1] == 3.0).all())
+
+
+@pytest.mark.parametrize("dc", [256, 512])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+def test_rows_of_all_sizes_are_normalised(dc, eps):
+    """From numbers without normal bits to the largest: squares leave fp32 on both sides.  24 additions and 4
+    ulp as for rows of ordinary size (2^-19); half a step of the result, or of the smallest number."""
+    d = gdn.LatentDims(1, dc, page_size=128, norm_eps=eps)
+    exponents = [125, 118, 70, 64, 63, 59, 58, 57, 40, 0, -14, -30, -44, -46, -60, -75, -100, -120, -128, -132]
+    t = len(exponents)
+    c = torch.randn(t, dc + 64, generator=gen(361), device="cuda").clamp(-3, 3)
+    c = (c.double() * torch.tensor(exponents, device="cuda").double().exp2()[:, None]).bfloat16()
+    c[-1, 5] = 2.0 ** -133
+    w = torch.randn(dc, generator=gen(362), device="cuda").mul(0.2).add(1.0)
+    cache, table = make_cache(d, [t], 363)
+    packed = torch.empty_like(c)
+    gdn.latent_append(d, cache, [0, t], ints([t]), table, c, norm_w=w, rows_out=packed)
+    gdn.sync_status()
+    x = c[:, :dc].double()
+    want = x / torch.sqrt(x.square().mean(-1, keepdim=True) + d.c().norm_eps) * w.double()
+    check(packed[:, :dc], want, want.abs() * (2.0 ** -19 + U * (1 + 2.0 ** -19)) + 2.0 ** -134)
+    assert torch.equal(packed[:, dc:], c[:, dc:])
+    # a row of zeros has none but zeros, one with an infinity as well, beside large numbers too
+    c = torch.zeros(3, dc + 64, dtype=torch.bfloat16, device="cuda")
+    c[1, 7], c[1, 9], c[2, 7], c[2, 9] = float("inf"), 2.0 ** 100, float("nan"), 2.0 ** 100
+    gdn.latent_append(d, cache, [0, 3], ints([3]), table, c, norm_w=w, rows_out=packed[:3])
+    gdn.sync_status()
+    assert bool((packed[:3, :dc] == 0).all())
