@@ -564,6 +564,10 @@ std::vector<int32_t> pages_of(PyObject* o, const char* name) {
 PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 3, [&]() -> PyObject* {
         if (!PyTuple_Check(a[0])) bad(PyExc_TypeError, "caches must be a tuple of tensors");
+        // first: an item's __index__ may do anything, also to the caches' tensors
+        const std::vector<int32_t> src = pages_of(a[1], "src"), dst = pages_of(a[2], "dst");
+        if (src.size() != dst.size()) bad(PyExc_ValueError, "src and dst must have as many pages (%zu, %zu)", src.size(), dst.size());
+        if (src.size() > 0x7fffffff) bad(PyExc_ValueError, "more than 2^31 - 1 pairs");
         const Py_ssize_t n_buffers = PyTuple_GET_SIZE(a[0]);
         std::vector<void*> bases;
         std::vector<size_t> bytes;
@@ -581,9 +585,6 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
             bases.push_back(t.data_ptr());
             bytes.push_back(t.nbytes() / t.size(0));
         }
-        const std::vector<int32_t> src = pages_of(a[1], "src"), dst = pages_of(a[2], "dst");
-        if (src.size() != dst.size()) bad(PyExc_ValueError, "src and dst must have as many pages (%zu, %zu)", src.size(), dst.size());
-        if (src.size() > 0x7fffffff) bad(PyExc_ValueError, "more than 2^31 - 1 pairs");
         if (bases.empty() && (n_buffers == 0 || src.empty())) Py_RETURN_NONE;
         if (bases.empty()) bad(PyExc_ValueError, "the caches have no pages");
         check("gdn_copy_pages",

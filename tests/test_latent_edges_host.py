@@ -5,6 +5,7 @@ import random
 import re
 
 import pytest
+import torch
 
 import gated_deltanet_linear_mixer_gb300 as gdn
 from gated_deltanet_linear_mixer_gb300 import _build
@@ -101,3 +102,20 @@ def test_packed_rows_in_the_inputs_memory(lib, monkeypatch):
     for base, end in ((2 * P, 2 * P + 4 * 256), (3 * P, 3 * P + 4 * 256), (1 << 40, (1 << 40) + 3 * 16 * 640)):
         for out, bad in ((base, True), (base - size + 16, True), (end - 16, True), (base - size, False), (end, False)):
             assert _append(lib, 2, 4, c, q, to, packed=out) == (1 if bad else gdn.GDN_ERR_INJECTED)
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_caches_may_change_while_page_lists_are_read():
+    """The caches are looked at as they are once both lists are read."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    d = gdn.LatentDims(1, 256, page_size=16)
+    with FakeTensorMode():
+        cache = gdn.LatentCache(d, torch.empty(4, 16, 320, dtype=torch.bfloat16, device="cuda:0"))
+
+    class Page:
+        def __index__(self):
+            cache.rows.resize_(7)
+            return 3
+
+    with pytest.raises(ValueError, match="contiguous"):
+        gdn.copy_pages(cache, [0], [Page()])
