@@ -48,8 +48,8 @@ gdn_status check_dims(const gdn_latent_dims* d, const char* fn) {
         return set_error(GDN_ERR_INVALID_ARG, fn, "rope_style %d is not a gdn_rope_style", d->rope_style);
     if ((d->nope_dim != 64 && d->nope_dim != 128) || (d->v_dim != 64 && d->v_dim != 128))
         return set_error(GDN_ERR_UNSUPPORTED, fn, "nope_dim and v_dim must be 64 or 128 (got %d, %d)", d->nope_dim, d->v_dim);
-    if (!(d->scale > 0.f) || !std::isfinite(d->scale))
-        return set_error(GDN_ERR_INVALID_ARG, fn, "scale must be finite and > 0");
+    if (!(d->scale > 0.f) || !std::isfinite(d->scale * 1.4426950408889634f))  // the kernels' scale: they take powers of two
+        return set_error(GDN_ERR_INVALID_ARG, fn, "scale must be finite, times log2 e too, and > 0");
     if (!(d->norm_eps >= 0.f) || !std::isfinite(d->norm_eps))
         return set_error(GDN_ERR_INVALID_ARG, fn, "norm_eps must be finite and >= 0");
     return GDN_OK;

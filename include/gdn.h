@@ -460,8 +460,8 @@ gdn_status gdn_kv_attention(const gdn_kv_dims* dims, const gdn_kv_cache* cache,
 
 /* Geometry.  latent_dim 256 or 512; rope_dim 64; page_size 16, 32, 64 or 128;
  * nope_dim and v_dim 64 or 128: a head's channels in the expanded form (its
- * keys have nope_dim + rope_dim).  1 <= n_heads <= 1024.  scale > 0 multiplies
- * q.k in both forms. */
+ * keys have nope_dim + rope_dim).  1 <= n_heads <= 1024.  scale > 0 (below 2^127)
+ * multiplies q.k in both forms. */
 typedef struct gdn_latent_dims {
     int32_t n_heads;
     int32_t latent_dim;

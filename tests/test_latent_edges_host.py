@@ -119,3 +119,10 @@ def test_caches_may_change_while_page_lists_are_read():
 
     with pytest.raises(ValueError, match="contiguous"):
         gdn.copy_pages(cache, [0], [Page()])
+
+
+@pytest.mark.parametrize("scale,ok", [(2.3e38, True), (2.4e38, False), (3.4e38, False), (1e-45, True)])
+def test_scales_that_leave_fp32_in_powers_of_two_are_refused(lib, scale, ok):
+    d, n, host = gdn._LatentDims(2, 256, 64, 16, 0, 128, 128, scale, 1e-6), ctypes.c_size_t(0), (ctypes.c_int32 * 2)(0, 4)
+    got = lib.gdn_latent_attention_workspace_size(ctypes.byref(d), 1, ctypes.cast(host, ctypes.c_void_p), ctypes.byref(n))
+    assert got == (0 if ok else 1) and (ok or b"scale" in lib.gdn_last_error())
