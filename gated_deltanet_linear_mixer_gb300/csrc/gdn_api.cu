@@ -28,14 +28,6 @@ gdn_status fail(gdn_status st, const char* fn, const char* fmt, ...) {
     return st;
 }
 
-gdn_status cuda_status(cudaError_t e, const char* fn, const char* what) {
-    if (e == cudaSuccess) return GDN_OK;
-    return fail(GDN_ERR_CUDA, fn, "%s failed: %s (%s)", what, cudaGetErrorName(e),
-                cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Whether the comma-separated list in the environment variable GDN_FAULT names
 // `site` (or "all").  Read on every call, so a test can set and clear it.
 bool fault_listed(const char* site) {
@@ -213,6 +205,11 @@ gdn_status set_error(gdn_status st, const char* fn, const char* fmt, ...) {
     return st;
 }
 
+gdn_status cuda_status(cudaError_t e, const char* fn, const char* what) {
+    if (e == cudaSuccess) return GDN_OK;
+    return set_error(GDN_ERR_CUDA, fn, "%s failed: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
 void clear_error() { g_err[0] = '\0'; }
 
 void* timing_start(const char* name, cudaStream_t stream) {
@@ -238,6 +235,8 @@ void timing_stop(void* handle, cudaStream_t stream) {
 
 }  // namespace gdn
 
+using gdn::aligned16;
+using gdn::cuda_status;
 using gdn::timed_launch;
 
 extern "C" {

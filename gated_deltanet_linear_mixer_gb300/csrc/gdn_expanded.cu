@@ -62,7 +62,6 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kSms = 152;
 constexpr int kM = 128, kKeys = 128, kTiles = 2;
 constexpr int kThreads = 384;
 constexpr float kLazy = 8.0f;
@@ -108,17 +107,7 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= kSharedBytes, "part of kSmem");
 
-__device__ __noinline__ void record(int* error, int code) { atomicMax(error, code); }
 
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
 // 32 lanes x 32 columns of 32-bit, registers to tensor memory.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
     asm volatile(
@@ -131,7 +120,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
         "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // D[tmem] (+)= A[tmem] * B[smem]^T, bf16.  A: lane = row, a column holds two consecutive K elements.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -155,29 +143,11 @@ __device__ __forceinline__ void store32(bf16* to, const uint32_t* v, bool wide) 
         reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
 }
-// Two fp32 operations an instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // What a launch walks: (sequence, block of queries) pairs, of every head.
 constexpr int kPairs = 1024;
 struct Plan {
     CUtensorMap q, k, r, v;
-    int n_pairs;
     uint32_t pair[kPairs];     // sequence << 16 | block
 };
 
@@ -694,7 +664,6 @@ cudaError_t expanded_t(const ExpandedArgs& a, cudaStream_t st) {
             return cost[x] > cost[y];
         });
         for (int i = 0; i < n; ++i) plan.pair[i] = pair[order[i]];
-        plan.n_pairs = n;
         const unsigned grid = static_cast<unsigned>(n) * a.n_heads;
         n = 0;
         return timed_launch("expanded_attention", st, [&] {

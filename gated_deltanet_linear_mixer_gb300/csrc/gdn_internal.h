@@ -10,6 +10,8 @@
 
 namespace gdn {
 
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // Tokens per chunk of the tensor-core prefill.
 constexpr int kChunkTokens = 64;
 

@@ -43,6 +43,9 @@ struct KvE4m3 {
     }
 };
 
+// Records a code in the cache operators' error word.
+static __device__ __noinline__ void record(int* error, int code) { atomicMax(error, code); }
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_ftz(float x) {

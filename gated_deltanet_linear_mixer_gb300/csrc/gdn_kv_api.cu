@@ -10,23 +10,19 @@
 namespace gdn {
 // Records the thread's error message (defined with the other entry points).
 gdn_status set_error(gdn_status st, const char* fn, const char* fmt, ...);
+gdn_status cuda_status(cudaError_t e, const char* fn, const char* what);  // GDN_OK, or GDN_ERR_CUDA recorded
 void clear_error();
 // GDN_ERR_INJECTED when the environment variable GDN_FAULT lists `site`.
 gdn_status inject_fault(const char* site, const char* fn);
 bool fault_site(const char* site);  // whether it does
 }  // namespace gdn
 
+using gdn::aligned16;
+using gdn::cuda_status;
 using gdn::set_error;
 using gdn::timed_launch;
 
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-gdn_status cuda_status(cudaError_t e, const char* fn, const char* what) {
-    if (e == cudaSuccess) return GDN_OK;
-    return set_error(GDN_ERR_CUDA, fn, "%s failed: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
 
 gdn_status check_kv_dims(const gdn_kv_dims* d, const char* fn) {
     if (!d) return set_error(GDN_ERR_INVALID_ARG, fn, "dims is NULL");

@@ -59,7 +59,6 @@ namespace {
 
 // The largest code stays.  A call of its own: in line the atomics take registers where nothing fails
 // (16 windowed prompts of 32 heads of 128: 317 us in line, 308 us so; a prompt of 4096 tokens 135 us both).
-__device__ __noinline__ void record(int* error, int code) { atomicMax(error, code); }
 
 constexpr int kM = 128, kKeys = 64;
 constexpr int kGroups = kKeys / 16;  // 16-key groups of a tile: one page each
@@ -100,7 +99,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
     tmem_st16(taddr, v);
     tmem_st16(taddr + 16, v + 16);
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, f16, issued by one thread.  A: lane = row,
 // a column holds two consecutive K elements.
@@ -114,23 +112,6 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
-// Two fp32 operations an instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // Bulk copy shared -> global of `bytes` (a multiple of 16, both ends aligned),
 // tracked by the issuing thread's bulk group.
@@ -138,30 +119,7 @@ __device__ __forceinline__ void bulk_store_1d(void* dst, const void* src, uint32
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
 }
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
 
-// OR of a predicate over `count` threads at named barrier `id`.
-__device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %3, 0;\n\t"
-        "barrier.red.or.pred q, %1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(count), "r"(x ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
 
 // Block constants of one 16-key group: factor of the scores, their offset
 // (log2 of the value scale), and its reciprocal (negative: values are zero).
@@ -182,10 +140,6 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 4096, "part of kSmem");
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-    const int n = take ? 16 : 0;  // 0: the 16 bytes become zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 
 // A row tile's queries as they are (bf16; zeros past the last row) by THREADS
 // threads into a swizzled tile of kM rows in blocks of 64 channels.
@@ -413,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnArgs
                 for (int j = 4; j < NC; ++j) tops[j & 3] = fmaxf(tops[j & 3], s[j]);
                 float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 // whether the reference of any row moves: of the warp, or of both threads of any row
-                const bool lift = C::kHalves == 2 ? group_any(1, 32 * kSoftWarps, top > m + kLazy)
+                const bool lift = C::kHalves == 2 ? group_or(1, 32 * kSoftWarps, top > m + kLazy)
                                                   : __any_sync(0xffffffffu, top > m + kLazy);
                 float f = 1.0f;
                 if (lift) {

@@ -117,33 +117,7 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= kSharedBytes, "part of kSmem");
 
-__device__ __noinline__ void record(int* error, int code) { atomicMax(error, code); }
 
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
-__device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %3, 0;\n\t"
-        "barrier.red.or.pred q, %1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(count), "r"(x ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-    const int n = take ? 16 : 0;  // 0: the 16 bytes become zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 
 // How long rows stay in L2: those of sequences that a single group of row tiles
 // reads leave before the partial results, which are read again (256 single tokens of
@@ -209,7 +183,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
         "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // What a sequence needs: groups of G row tiles, and key tiles of each (at least one,
 // so that rows without keys are somebody's).
@@ -468,7 +441,7 @@ latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps map
                         }
                         lift = topA > mA + kLazy || topB > mB + kLazy;
                     }
-                    lift = group_any(1, 128, lift);
+                    lift = group_or(1, 128, lift);
                     if (lift) {
                         if (active) {
                             const float nA = fmaxf(mA, topA), nB = fmaxf(mB, topB);

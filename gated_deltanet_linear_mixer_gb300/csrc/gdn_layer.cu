@@ -17,6 +17,8 @@ gdn_status set_error(gdn_status st, const char* fn, const char* fmt, ...);
 gdn_status inject_fault(const char* site, const char* fn);
 }  // namespace gdn
 
+using gdn::aligned16;
+
 namespace {
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -39,8 +41,6 @@ LayerLayout layer_layout(const gdn_dims* d, size_t T, size_t core_bytes) {
     l.total = off;
     return l;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 
