@@ -34,10 +34,12 @@
 // tensor core takes 24 instructions of S (128 x 128 x 16, 71 cycles each, measured
 // alone) and 16 of O (74, their A operand in tensor memory): 2890 cycles.  The keys
 // and values that come in meanwhile, 80 KB, take 640 cycles of the shared memory's
-// bandwidth, which those products use in full: 3530.  About 3570 are reached.  The
-// exponentials (32 a cycle and SM: 1024 cycles) do not bound it.  4096 tokens, 32
-// heads: 125 us, 1.38 PFLOP/s; 16 ragged prompts of up to 1100 tokens behind up to
-// 3000: 142 us, 1.14 PFLOP/s, where tiles that are partly masked or empty weigh more.
+// bandwidth, which those products use in full: 3530.  3680 are reached: 1.92 us at 1.91
+// GHz, the SM clock by the kernel's own counters.  The exponentials (32 a cycle and SM:
+// 1024 cycles) do not bound it.  4096 tokens, 32 heads: 126 us, 1.37 PFLOP/s, of which 54
+// such steps an SM are 104, the last tiles of 3.4 items, which one query tile walks alone, 5,
+// the items' ends 6 and the call's start and end 7; 16 ragged prompts of up to 1100 tokens
+// behind up to 3000: 142 us, 1.14 PFLOP/s, where tiles that are partly masked or empty weigh more.
 //
 // Tried and slower (us, the two cases above, with fixed shares and 208 and 88 registers): pairs of thread blocks
 // that share keys (134 and 215 where a block of the same form took 141 and 179); two threads a

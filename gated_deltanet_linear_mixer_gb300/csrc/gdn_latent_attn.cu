@@ -34,14 +34,16 @@
 // nothing more but, once for all of them, what it has in flight: a thread block ends
 // within a few such waits.
 //
-// What bounds it.  Up to 32 rows a sequence the rows' bytes: a tile's 72 KB are
-// 3100 cycles of an SM's share of DRAM, its products 2160 (16 rows) or 2290 (32).
+// What bounds it (cycles at 1.95 GHz, the SM clock by the kernel's own counters).  Up to 32
+// rows a sequence the rows' bytes: a tile's 72 KB are 3200 cycles of an SM's share of
+// DRAM (1.65 us; 1.67 are reached), its products 2160 (16 rows) or 2290 (32).
 // 256 single tokens of 32 heads after 127..8191 keys take 222 to 227 us, 87% of the
 // measured copy rate, 16 heads 205 to 210 us (90%).  With 64 rows the products: 36 of S at 37
 // cycles (64 x 64 x 16) and 16 of O^T at 76 (128 x 64 x 16 with the first operand
 // MN-major; 53 were it K-major) make 2540 cycles a tile, of which the ring's two tiles
-// let it reach 2900: 64 x 4 drafts of 32 heads after 500..6000 keys take 106 us, of
-// which the partial results of 152 thread blocks and their join are 20.  Tiles of
+// let it reach 2870 (1.47 us): 64 x 4 drafts of 32 heads after 500..6000 keys take 106 us,
+// of which 48 tiles are 71, the partial results of 152 thread blocks and their join 20,
+// the call's start, its queries and the outputs of whole sequences 13.  Tiles of
 // 32 keys, four in the ring, were slower (145 us, then 119), and so was fetching
 // tiles into L2 ahead of their loads (256 x 1: 229 us without, 246 three tiles
 // ahead).  One token after 1000 keys takes 13 us, all of it latency: the plan 2 us,

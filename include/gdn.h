@@ -531,7 +531,9 @@ gdn_status gdn_latent_read(const gdn_latent_dims* dims, const gdn_latent_cache* 
  * Rows that some query of a sequence sees have to be finite, as appended ones
  * are; whatever lies behind a sequence's end does not matter.  fp32
  * accumulation and softmax (the hardware's exponentials, 2 ulp), weights bf16
- * (8 bits); the sum takes the rounded weights.
+ * (8 bits); the sum takes the rounded weights.  Scores (scaled ones too) have to be
+ * fp32 numbers, and so have sums of values with weights of up to 2^8 (values below
+ * 2^120 over the number of keys are safe): else infinities or NaN.
  */
 gdn_status gdn_latent_attention_workspace_size(const gdn_latent_dims* dims, int32_t n_seq,
                                                const int32_t* cu_seqlens_host, size_t* bytes);
@@ -556,7 +558,8 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
  * sequence has at most 2^24 queries, a call 2^30 keys.
  * Values that some query of a sequence sees have to be finite.  fp32 accumulation
  * and softmax (the hardware's exponentials, 2 ulp), weights bf16 (8 bits); the sum
- * takes them as they are.
+ * takes them as they are.  What has to be fp32 numbers is as in
+ * gdn_latent_attention, but for scaled scores.
  */
 gdn_status gdn_expanded_attention(const gdn_latent_dims* dims, int32_t n_seq, const int32_t* cu_q,
                                   const int32_t* cu_q_host, const int32_t* cu_kv,
