@@ -36,7 +36,7 @@
 // and values that come in meanwhile, 80 KB, take 640 cycles of the shared memory's
 // bandwidth, which those products use in full: 3530.  3680 are reached: 1.92 us at 1.91
 // GHz, the SM clock by the kernel's own counters.  The exponentials (32 a cycle and SM:
-// 1024 cycles) do not bound it.  4096 tokens, 32 heads: 126 us, 1.37 PFLOP/s, of which 54
+// 1024 cycles) do not bound it.  4096 tokens, 32 heads: 126 us, 1.36 PFLOP/s, of which 54
 // such steps an SM are 104, the last tiles of 3.4 items, which one query tile walks alone, 5,
 // the items' ends 6 and the call's start and end 7; 16 ragged prompts of up to 1100 tokens
 // behind up to 3000: 142 us, 1.14 PFLOP/s, where tiles that are partly masked or empty weigh more.
