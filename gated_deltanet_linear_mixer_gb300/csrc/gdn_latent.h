@@ -39,6 +39,7 @@ struct LatentReadArgs {
 struct LatentAttnArgs {
     LatentCache c;
     KvBatch b;
+    const int32_t* cu_host;
     int n_heads, page_shift;  // a page has 1 << page_shift tokens
     float scale;
     KvRows q;  // [T, n_heads, C + kRopeDim]

@@ -246,6 +246,7 @@ gdn_status gdn_latent_attention(const gdn_latent_dims* dims, const gdn_latent_ca
     if ((st = gdn::inject_fault("latent_attention", fn)) != GDN_OK) return st;
     if ((st = cuda_status(gdn::cache_error_word(&a.error), fn, "finding the error word")) != GDN_OK) return st;
     a.c = gdn::LatentCache{cache->rows, cache->n_pages};
+    a.cu_host = batch->cu_seqlens_host;
     a.n_heads = dims->n_heads; a.scale = dims->scale; a.out = out; a.workspace = workspace;
     while (1 << a.page_shift < dims->page_size) ++a.page_shift;
     a.stall = stall("stall_latent", "stall_latent_products");

@@ -21,10 +21,10 @@
 // whatever they are; lengths are only known on the device, where every thread
 // block finds its span by a scan over the sequences.  What a span holds of a
 // sequence that it does not hold whole is a partial result (at most two a span);
-// a second launch joins them.  Above 64 rows a group is two row tiles, of two
-// neighbouring thread blocks that walk the same span, each with loads of its own: the
-// later one's rows come from L2 (64 x 4 drafts as below: 106 us; 118 us where
-// every row tile was a group, 110 where a cluster shared its loads).
+// a second launch joins them.  Where most sequences have an even number of row tiles a
+// group is two of them, of two neighbouring thread blocks that walk the same span, each
+// with loads of its own: the later one's rows come from L2 (64 x 4 drafts as below: 106
+// us; 110 where a cluster shared its loads).  Else it is one (two_tiles).
 //
 // Roles: 4 softmax warps (also: rescaling, epilogue), two for the rows' TMA loads
 // (with the page look-ups), one loading queries and issuing S, one issuing O^T.
@@ -994,13 +994,27 @@ cudaError_t launch_t(const LatentAttnArgs& a, cudaStream_t st) {
     });
 }
 
+// Whether groups of two row tiles are worth it: they take a tenth less time where they are full, but a
+// sequence's odd tile leaves one of its two thread blocks without rows.  By two, by one: 64 x 4 tokens of 32
+// heads 106 and 118 us, 64 x 5 216 and 191, 64 x 1..8 169 and 154, 255 single tokens beside 3 of one sequence
+// 387 and 238.
+bool two_tiles(const LatentAttnArgs& a) {
+    long long tiles = 0, odd = 0;
+    for (int i = 0; i < a.b.n_seq; ++i) {
+        const long long n = (static_cast<long long>(a.cu_host[i + 1] - a.cu_host[i]) * a.n_heads + 63) / 64;
+        tiles += n;
+        odd += n & 1;
+    }
+    return 10 * odd <= tiles;
+}
+
 template <int C>
 cudaError_t launch_c(const LatentAttnArgs& a, cudaStream_t st) {
     const long long rows = static_cast<long long>(a.b.max_q) * a.n_heads;
     switch (rows_of_tile(rows)) {
         case 16: return launch_t<C, 16, 1>(a, st);
         case 32: return launch_t<C, 32, 1>(a, st);
-        default: return rows > 64 ? launch_t<C, 64, 2>(a, st) : launch_t<C, 64, 1>(a, st);
+        default: return rows > 64 && two_tiles(a) ? launch_t<C, 64, 2>(a, st) : launch_t<C, 64, 1>(a, st);
     }
 }
 

@@ -245,3 +245,22 @@ def test_rows_of_all_sizes_are_normalised(dc, eps):
     gdn.latent_append(d, cache, [0, 3], ints([3]), table, c, norm_w=w, rows_out=packed[:3])
     gdn.sync_status()
     assert bool((packed[:3, :dc] == 0).all())
+
+
+@pytest.mark.parametrize("heads,dc,counts,lens", [
+    (32, 512, [5] * 4, [700, 5, 64, 1000]),                    # three row tiles each
+    (32, 256, [1] * 40 + [3], [130] * 40 + [2000]),            # single tokens beside a piece
+    (16, 512, [40] + [1] * 30, [1500] + [77] * 30),
+    (20, 512, [1, 7, 0, 2, 33, 4], [300, 7, 20, 2, 40, 129]),
+    (65, 256, [1, 1, 1], [500, 64, 1]),
+    (192, 512, [1, 3], [3000, 90]),
+])
+def test_more_rows_than_a_tile_beside_odd_numbers_of_tiles(heads, dc, counts, lens):
+    """Row tiles one to a group: several groups a sequence, or one among short ones; twice alike."""
+    d = gdn.LatentDims(heads, dc, page_size=32)
+    cache, table = make_cache(d, lens, 371)
+    q, cu = _queries(sum(counts), heads, dc + 64, 372), cu_of(counts)
+    got = gdn.latent_attention(d, cache, cu, ints(lens), table, q)
+    gdn.sync_status()
+    check(got, *absorbed(d, cache, counts, lens, table, q))
+    assert torch.equal(got, gdn.latent_attention(d, cache, cu, ints(lens), table, q))
